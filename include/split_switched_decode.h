@@ -3,7 +3,9 @@
  * GB300 (sm_103a): the decode projection with a batch-size kernel switch, the MoE
  * front end (router scores + latent projection as one product, then softmax/top-k),
  * the routed-expert grouped GEMV with the shared expert overlapping it (inside the same
- * launch, or on a side stream), and an L2 prefetch kernel.
+ * launch, or on a side stream), an L2 prefetch kernel, and the attention step between the
+ * projections: a page planner, rotary positions with the cache write, and attention over
+ * the paged key-value cache.
  *
  * The method is the one described in "Hyper Optimizing Kimi K3 in vLLM: Moving Fast
  * and Responsibly" (vLLM blog), Part 1, sections 1-4. Each entry point below cites
@@ -398,6 +400,149 @@ DEC_API dec_status moe_layer_packed(const dec_bf16 *X, const dec_bf16 *Wcat, int
                                     float *topk_w, int32_t *route_map_opt, dec_bf16 *Y,
                                     void *ws, size_t ws_bytes, dec_stream_t main_stream,
                                     dec_stream_t side_stream, int side_max_ctas);
+
+/* ------------------------------------------------- attention over a paged cache ---- */
+
+/*
+ * Between the input and the output projection of a decode layer: kv_plan gives every new
+ * token a place in a paged key-value cache, rope_append rotates the projected rows and
+ * writes the new keys and values there, attn_decode attends over the cache. All three are
+ * asynchronous on `s`, read lengths and tables from DEVICE memory (so that one captured
+ * graph serves every step) and check those values in the kernel: what is out of range is
+ * left out as described below, never read or written out of bounds.
+ *
+ * Paged cache. Keys and values live in num_pages pages of page_size tokens (any number
+ * >= 1). Token `off` of page p, kv head h is the D contiguous elements at
+ *
+ *     cache + p * page_stride + h * head_stride + off * token_stride     (in elements)
+ *
+ * the same strides for K and V: [num_pages, Hkv, page_size, D], token-major
+ * [num_pages, page_size, Hkv, D], or the two halves of one array all fit. Elements are
+ * bf16 (DEC_KV_BF16) or 8-bit e4m3 (DEC_KV_E4M3) that stand for value * scale[h], with
+ * k_scale / v_scale fp32 [Hkv] on the device (NULL: 1). A sequence's tokens are numbered
+ * from 0; token j is in page block_table[s, j / page_size] at offset j % page_size, which
+ * as one number is its slot, page * page_size + offset. Cache pointers are 16-byte
+ * aligned, the strides multiples of 16 bytes, D a multiple of 16, 16..256.
+ */
+typedef enum {
+    DEC_KV_BF16 = 0,
+    DEC_KV_E4M3 = 1
+} dec_kv_type;
+
+/*
+ * Block tables and slot maps from request lengths, one launch.
+ *
+ *     a[s]       new tokens of sequence s that fit: min(new_len[s], max_tokens - q_start[s])
+ *     q_start    [S+1] exclusive sums of a: rows q_start[s] .. q_start[s+1]-1 are s's
+ *     seq_len    [S]   kv_len[s] + a[s]
+ *     block_table[s, i] for the pages i that s did not hold, ceil(kv_len/page_size) <= i <
+ *                ceil(seq_len/page_size): free_pages[*free_used + rank], rank counting
+ *                these pages in (s, i) order; -1 once the free list is used up
+ *     positions  [max_tokens] kv_len[s] + t - q_start[s] of row t; 0 for rows of no sequence
+ *     slots      [max_tokens] block_table[s, pos / page_size] * page_size + pos % page_size;
+ *                -1 for rows of no sequence and tokens without a page
+ *     summary    [4] = { rows in use q_start[S], free pages used after this call,
+ *                new tokens that did not fit max_tokens, pages that were wanted and not
+ *                given (free list or table width exhausted) }, each at most 2^31 - 1
+ *
+ * kv_len int32 [S] tokens already cached, new_len int32 [S] or NULL (one each); negative
+ * lengths count as 0 and kv_len + new_len must stay below 2^31. block_table int32
+ * [S, max_pages], read for the pages a sequence holds and written for new ones only.
+ * free_pages int32 [num_free] (NULL allowed when num_free is 0), free_used int32 [1] or
+ * NULL (0 used). seq_len may be the array kv_len, and free_used may point to summary[1]:
+ * a captured graph then carries the state from step to step. No other output may overlap
+ * an input. S in 1..8192 (DEC_ERR_UNSUPPORTED_SHAPE above). No workspace.
+ */
+DEC_API dec_status kv_plan(const int32_t *kv_len, const int32_t *new_len, int S, int page_size,
+                           int32_t *block_table, int max_pages, const int32_t *free_pages,
+                           int num_free, const int32_t *free_used, int32_t *seq_len,
+                           int32_t *q_start, int32_t *positions, int32_t *slots, int max_tokens,
+                           int32_t *summary, dec_stream_t s);
+
+/* Frequency scalings of rope_frequencies. */
+typedef enum {
+    DEC_ROPE_PLAIN = 0,   /* inv_freq[i] = base^(-2i/rot)                                  */
+    DEC_ROPE_LINEAR = 1,  /* the same / factor: positions interpolated                     */
+    DEC_ROPE_BASE = 2,    /* base * factor^(rot/(rot-2)): the slowest pair as in LINEAR,
+                             the fastest as in PLAIN                                       */
+    DEC_ROPE_PARTS = 3    /* "YaRN: Efficient Context Window Extension of Large Language
+                             Models": pairs that turn more than beta_fast times within
+                             orig_len tokens as in PLAIN, less than beta_slow times as in
+                             LINEAR, a linear ramp over the pairs between; the magnitude is
+                             0.1 ln(factor) + 1                                            */
+} dec_rope_scaling;
+
+/*
+ * Inverse frequencies of rope_append, computed on the HOST in double precision into the
+ * host array inv_freq[rot/2] (rounded once to fp32; copy it to the device), and the
+ * magnitude into *magnitude (1 except for DEC_ROPE_PARTS). rot even, 2..256; base > 1;
+ * factor >= 1; DEC_ROPE_BASE needs rot >= 4; orig_len >= 1 and beta_fast > beta_slow > 0
+ * for DEC_ROPE_PARTS (ignored otherwise). DEC_ERR_INVALID_ARG otherwise.
+ */
+DEC_API dec_status rope_frequencies(int rot, double base, int scaling, double factor,
+                                    int orig_len, double beta_fast, double beta_slow,
+                                    float *inv_freq, float *magnitude);
+
+/*
+ * Rotary positions and the write into the cache, one launch. For row t at positions[t],
+ * with angle a[i] = positions[t] * inv_freq[i], c = magnitude * cos a, n = magnitude * sin a:
+ *
+ *     (x0, x1)  ->  (x0 c - x1 n, x1 c + x0 n)
+ *
+ * for pair i of the first `rot` elements of every q and k head: elements (2i, 2i+1) with
+ * interleaved = 1, (i, i + rot/2) with interleaved = 0; elements rot..D-1 unchanged. The
+ * angle is reduced in double precision, so positions up to 2^31 - 1 lose nothing; the
+ * rotation is fp32 and rounds once. Writes q_out, and K (rotated) and V (as they are, or
+ * both divided by their head's scale and saturated to +-448 for DEC_KV_E4M3) to slot
+ * slots[t] of the cache. A slot below 0 or not below num_pages * page_size is not written.
+ * Two rows with the same slot leave one of the two there.
+ *
+ * q [T,Hq,D], k and v [T,Hkv,D], q_out [T,Hq,D] with the given row strides (in elements):
+ * the three parts of one projection's rows fit, and q_out may be q with the same stride (in
+ * place). Heads are contiguous within a row. positions and slots int32 [T]; inv_freq fp32
+ * [rot/2] on the device; rot even, 0..D. Row pointers are 16-byte aligned and strides
+ * multiples of 8. T >= 1 (up to 2^20), Hq and Hkv 1..1024. No workspace.
+ */
+DEC_API dec_status rope_append(const dec_bf16 *q, int64_t q_stride, const dec_bf16 *k,
+                               int64_t k_stride, const dec_bf16 *v, int64_t v_stride,
+                               const int32_t *positions, const int32_t *slots,
+                               const float *inv_freq, float magnitude, int T, int Hq, int Hkv,
+                               int D, int rot, int interleaved, dec_bf16 *q_out,
+                               int64_t q_out_stride, void *k_cache, void *v_cache, int kv_type,
+                               const float *k_scale, const float *v_scale, int num_pages,
+                               int page_size, int64_t page_stride, int64_t head_stride,
+                               int64_t token_stride, dec_stream_t s);
+
+/*
+ * Attention of new tokens over the paged cache, split over the cache's length and joined.
+ * Row i of the n = q_start[s+1] - q_start[s] rows of sequence s stands at position
+ * pos = seq_len[s] - n + i and sees the keys j <= pos, with window > 0 only j > pos - window;
+ * its head hq reads kv head hq / (Hq / Hkv):
+ *
+ *     out = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale * q . k_j - m),
+ *     lse = ln sum_j exp(scale * q . k_j)
+ *
+ * A row that sees no key (or whose scores are all -infinity) gives out = 0 and
+ * lse = -infinity. Keys whose page is not in 0..num_pages-1 are not seen. What stands in
+ * the cache at a place that a row does not see, NaN included, does not reach that row.
+ *
+ * q and out [T,Hq,D] with row strides in elements (multiples of 8, 16-byte aligned; out may
+ * not overlap q); block_table int32 [S, max_pages]; seq_len int32 [S], the new tokens
+ * included, taken as at most max_pages * page_size; q_start int32 [S+1], or NULL for one
+ * row each (then T == S); lse_opt fp32 [T,Hq] or NULL. Rows of no sequence are not written.
+ * S in 1..8192, T in 1..65536, Hq and Hkv 1..1024 with Hq % Hkv == 0. Scores, maxima, sums
+ * and partial results are fp32; the weights p_j round to 16 bits for the product with V.
+ * Deterministic: the split depends on the lengths, not on timing.
+ */
+DEC_API size_t attn_decode_workspace_bytes(int S, int T, int Hq, int Hkv, int D);
+DEC_API dec_status attn_decode(const dec_bf16 *q, int64_t q_stride, const void *k_cache,
+                               const void *v_cache, int kv_type, const float *k_scale,
+                               const float *v_scale, int num_pages, int page_size,
+                               int64_t page_stride, int64_t head_stride, int64_t token_stride,
+                               const int32_t *block_table, int max_pages, const int32_t *seq_len,
+                               const int32_t *q_start, int S, int T, int Hq, int Hkv, int D,
+                               float scale, int window, dec_bf16 *out, int64_t out_stride,
+                               float *lse_opt, void *ws, size_t ws_bytes, dec_stream_t s);
 
 /* ------------------------------------------------------------ read stream ----- */
 

@@ -43,7 +43,16 @@ EXPORTS = [
     "dec_pack_weight", "dec_gemv_packed", "dec_splitk_gemm_packed", "dec_linear_packed",
     "dec_pack_expert_weights", "moe_experts_packed", "moe_layer_packed",
     "dec_read_stream_bytes", "dec_read_stream",
+    "kv_plan", "rope_frequencies", "rope_append", "attn_decode_workspace_bytes", "attn_decode",
 ]
+
+KV_BF16 = 0
+KV_E4M3 = 1
+
+ROPE_PLAIN = 0
+ROPE_LINEAR = 1
+ROPE_BASE = 2
+ROPE_PARTS = 3
 
 _lib = None
 
@@ -71,6 +80,7 @@ def _load():
             f"{LIB_PATH} is missing: build it first (python -m split_switched_decode_gb300.build)")
     lib = ctypes.CDLL(LIB_PATH)
     P, I, S, U64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_uint64
+    L, F, F64 = ctypes.c_int64, ctypes.c_float, ctypes.c_double
     sig = {
         "dec_status_string": (ctypes.c_char_p, [I]),
         "dec_variant_name": (ctypes.c_char_p, [I]),
@@ -106,6 +116,13 @@ def _load():
         "l2_prefetch": (I, [P, S, I, P]),
         "dec_sim_comm_wait": (I, [U64, P]),
         "dec_splitk_gemm_noalloc": (I, [P, P, P, P, I, I, I, I, P]),
+        "kv_plan": (I, [P, P, I, I, P, I, P, I, P, P, P, P, P, I, P, P]),
+        "rope_frequencies": (I, [I, F64, I, F64, I, F64, F64, P, P]),
+        "rope_append": (I, [P, L, P, L, P, L, P, P, P, F, I, I, I, I, I, I, P, L, P, P, I, P, P,
+                            I, I, L, L, L, P]),
+        "attn_decode_workspace_bytes": (S, [I, I, I, I, I]),
+        "attn_decode": (I, [P, L, P, P, I, P, P, I, I, L, L, L, P, I, P, P, I, I, I, I, I, F, I,
+                            P, L, P, P, S, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -374,3 +391,150 @@ def moe_layer(X, Wcat, E, L, topk, Wgu, Wd, Wgu_shared, Wd_shared, latent, topk_
               _ptr(Wd_shared), B, H, I, _ptr(latent), _ptr(topk_idx), _ptr(topk_w),
               _ptr(route_map), _ptr(Y), _ptr(ws), ws.numel() * ws.element_size(), main, side,
               side_max_ctas), "moe_layer")
+
+
+# ----------------------------------------------------------------- attention ----
+
+def _int32(t, name, ndim=1):
+    import torch
+    if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous() or t.dim() != ndim:
+        raise TypeError(f"{name} must be a contiguous int32 CUDA tensor of {ndim} dimension(s)")
+    return t.data_ptr()
+
+
+def _scales(t, name, heads):
+    import torch
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or not t.is_cuda or not t.is_contiguous() or t.numel() != heads:
+        raise TypeError(f"{name} must be a contiguous float32 CUDA tensor of {heads} values")
+    return t.data_ptr()
+
+
+def _rows(t, name, heads=None, dim=None):
+    """A bf16 [T, heads, D] tensor whose rows are contiguous (any row stride)."""
+    import torch
+    shape = t.shape
+    if t.dtype != torch.bfloat16 or not t.is_cuda or len(shape) != 3:
+        raise TypeError(f"{name} must be a bfloat16 CUDA tensor [rows, heads, D]")
+    if (heads is not None and shape[1] != heads) or (dim is not None and shape[2] != dim):
+        raise ValueError(f"{name} has shape {tuple(shape)}")
+    row, head, one = t.stride()
+    if (one != 1 and shape[2] != 1) or (head != shape[2] and shape[1] != 1):
+        raise TypeError(f"{name}: heads must be contiguous within a row")
+    return t.data_ptr(), row
+
+
+def _cache(k, v):
+    """(type, Hkv, D, pages, page size, strides) of the K and V caches, [pages, Hkv,
+    page size, D] tensors of equal type and strides (views of other orders are fine)."""
+    import torch
+    if k.dtype == torch.bfloat16:
+        kind = KV_BF16
+    elif k.dtype == torch.float8_e4m3fn:
+        kind = KV_E4M3
+    else:
+        raise TypeError("the caches must be bfloat16 or float8_e4m3fn tensors")
+    if v.dtype != k.dtype or not k.is_cuda or not v.is_cuda:
+        raise TypeError("k_cache and v_cache must be CUDA tensors of the same type")
+    shape, stride = k.shape, k.stride()
+    if len(shape) != 4 or v.shape != shape or v.stride() != stride:
+        raise ValueError("k_cache and v_cache must be [pages, Hkv, page size, D] with equal "
+                         "strides")
+    if stride[3] != 1:
+        raise TypeError("the last dimension of the caches must be contiguous")
+    return kind, shape[1], shape[3], shape[0], shape[2], stride
+
+
+def kv_plan(kv_len, new_len, block_table, free_pages, free_used, page_size, seq_len, q_start,
+            positions, slots, summary, stream=None):
+    """Places for new tokens in a paged cache: writes the new pages into block_table
+    [S, max_pages] and fills seq_len [S], q_start [S+1], positions and slots [max_tokens] and
+    summary [4] (rows, free pages used, tokens left out, pages lacking). new_len None: one
+    token each; free_used None: none used yet. seq_len may be kv_len and free_used
+    summary[1:2], which carries the state from call to call."""
+    tp = _int32(block_table, "block_table", 2)
+    S, max_pages = block_table.shape
+    max_tokens = positions.numel()
+    if (kv_len.numel() != S or seq_len.numel() != S or q_start.numel() != S + 1
+            or (new_len is not None and new_len.numel() != S) or slots.numel() != max_tokens
+            or summary.numel() != 4):
+        raise ValueError("kv_plan: sizes do not agree")
+    _check(_load().kv_plan(
+        _int32(kv_len, "kv_len"), None if new_len is None else _int32(new_len, "new_len"), S,
+        page_size, tp, max_pages,
+        _int32(free_pages, "free_pages"), free_pages.numel(),
+        None if free_used is None else _int32(free_used, "free_used"), _int32(seq_len, "seq_len"),
+        _int32(q_start, "q_start"), _int32(positions, "positions"), _int32(slots, "slots"),
+        max_tokens, _int32(summary, "summary"), _stream(stream)), "kv_plan")
+
+
+def rope_frequencies(rot, base=10000.0, scaling=ROPE_PLAIN, factor=1.0, orig_len=4096,
+                     beta_fast=32.0, beta_slow=1.0, device=None):
+    """(inv_freq, magnitude) for rope_append: a float32 tensor of rot/2 values (on `device`,
+    the CPU by default) and a float."""
+    import torch
+    inv = torch.empty(rot // 2, dtype=torch.float32)
+    mag = ctypes.c_float()
+    _check(_load().rope_frequencies(rot, base, scaling, factor, orig_len, beta_fast, beta_slow,
+                                    inv.data_ptr(), ctypes.addressof(mag)), "rope_frequencies")
+    return (inv if device is None else inv.to(device)), mag.value
+
+
+def rope_append(q, k, v, positions, slots, inv_freq, q_out, k_cache, v_cache, interleaved=False,
+                magnitude=1.0, k_scale=None, v_scale=None, stream=None):
+    """Rotate q [T,Hq,D] into q_out (which may be q) and k [T,Hkv,D] into the cache, write v
+    beside it; row t at positions[t] goes to slots[t] (-1: not cached). The first
+    2 * len(inv_freq) elements of a head are rotated (inv_freq None: none)."""
+    kind, Hkv, D, pages, page, stride = _cache(k_cache, v_cache)
+    qp, qs = _rows(q, "q", None, D)
+    T, Hq, _ = q.shape
+    kp, ks = _rows(k, "k", Hkv, D)
+    vp, vs = _rows(v, "v", Hkv, D)
+    op, os_ = _rows(q_out, "q_out", Hq, D)
+    if k.shape[0] != T or v.shape[0] != T or q_out.shape[0] != T or positions.numel() != T \
+            or slots.numel() != T:
+        raise ValueError("rope_append: row counts do not agree")
+    fp, rot = (None, 0) if inv_freq is None else \
+        (_scales(inv_freq, "inv_freq", inv_freq.numel()), 2 * inv_freq.numel())
+    _check(_load().rope_append(
+        qp, qs, kp, ks, vp, vs, _int32(positions, "positions"), _int32(slots, "slots"), fp,
+        magnitude, T, Hq, Hkv, D, rot, int(interleaved), op, os_, k_cache.data_ptr(),
+        v_cache.data_ptr(), kind, _scales(k_scale, "k_scale", Hkv),
+        _scales(v_scale, "v_scale", Hkv), pages, page, stride[0], stride[1], stride[2],
+        _stream(stream)), "rope_append")
+
+
+def attn_decode_workspace_bytes(S, T, Hq, Hkv, D) -> int:
+    return int(_load().attn_decode_workspace_bytes(S, T, Hq, Hkv, D))
+
+
+def attn_decode(q, k_cache, v_cache, block_table, seq_len, out, ws, q_start=None, scale=None,
+                window=0, lse=None, k_scale=None, v_scale=None, stream=None):
+    """Attention of the rows q [T,Hq,D] over a paged cache into out (and lse [T,Hq]): rows
+    q_start[s] .. q_start[s+1]-1 are the last tokens of sequence s, which has seq_len[s]
+    tokens in the pages block_table[s] (q_start None: one row each). scale: 1/sqrt(D) by
+    default; window > 0: a row sees that many last tokens, its own included."""
+    import torch
+    kind, Hkv, D, pages, page, stride = _cache(k_cache, v_cache)
+    qp, qs = _rows(q, "q", None, D)
+    T, Hq, _ = q.shape
+    op, os_ = _rows(out, "out", Hq, D)
+    tp = _int32(block_table, "block_table", 2)
+    S, max_pages = block_table.shape
+    if out.shape[0] != T or seq_len.numel() != S or \
+            (q_start is not None and q_start.numel() != S + 1):
+        raise ValueError("attn_decode: sizes do not agree")
+    lp = None
+    if lse is not None:
+        if lse.dtype != torch.float32 or not lse.is_cuda or not lse.is_contiguous() \
+                or tuple(lse.shape) != (T, Hq):
+            raise TypeError("lse must be a contiguous float32 CUDA tensor [T, Hq]")
+        lp = lse.data_ptr()
+    _check(_load().attn_decode(
+        qp, qs, k_cache.data_ptr(), v_cache.data_ptr(), kind, _scales(k_scale, "k_scale", Hkv),
+        _scales(v_scale, "v_scale", Hkv), pages, page, stride[0], stride[1], stride[2],
+        tp, max_pages, _int32(seq_len, "seq_len"),
+        None if q_start is None else _int32(q_start, "q_start"), S, T, Hq, Hkv, D,
+        D ** -0.5 if scale is None else scale, window, op, os_, lp, ws.data_ptr(),
+        ws.numel() * ws.element_size(), _stream(stream)), "attn_decode")

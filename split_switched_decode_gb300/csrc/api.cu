@@ -154,6 +154,18 @@ bool consume_fault() {
 
 dec_status cuda_status(cudaError_t e) { return e == cudaSuccess ? DEC_OK : DEC_ERR_CUDA; }
 
+}  // namespace
+
+namespace ssd {
+bool host_consume_fault() { return consume_fault(); }
+int host_num_sms(cudaError_t *err) {
+  DeviceInfo *d = device_info(err);
+  return d ? d->num_sms : 0;
+}
+}  // namespace ssd
+
+namespace {
+
 // ------------------------------------------------------------ split-K planning --
 
 struct SplitPlan {

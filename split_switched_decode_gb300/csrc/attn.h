@@ -1,0 +1,67 @@
+// attn.h -- launches of the attention step over the paged cache (not installed):
+// kv_plan.cu, rope_append.cu, attn_decode.cu; argument checks are in api_attn.cu.
+#pragma once
+
+#include "internal.h"
+
+namespace ssd {
+
+constexpr int ATTN_MAX_SEQS = 8192;
+constexpr int ATTN_MAX_HEADS = 1024;
+constexpr int ATTN_MAX_D = 256;
+
+// Where the elements of a paged cache are (strides in elements, the same for K and V).
+struct PagedCache {
+  const void *k;
+  const void *v;
+  const float *k_scale;  // [Hkv] or nullptr
+  const float *v_scale;
+  long long page_stride, head_stride, token_stride;
+  int num_pages, page_size;
+};
+
+// ---------------------------------------------------------------- kv_plan.cu --
+struct KvPlanParams {
+  const int32_t *kv_len, *new_len;  // new_len nullptr: one each
+  int S, page_size;
+  int32_t *block_table;
+  int max_pages;
+  const int32_t *free_pages;
+  int num_free;
+  const int32_t *free_used;  // nullptr: 0
+  int32_t *seq_len, *q_start, *positions, *slots;
+  int max_tokens;
+  int32_t *summary;
+};
+cudaError_t launch_kv_plan(const KvPlanParams &p, cudaStream_t s);
+
+// ------------------------------------------------------------ rope_append.cu --
+struct RopeParams {
+  const uint16_t *q, *k, *v;
+  long long q_stride, k_stride, v_stride, out_stride;
+  const int32_t *positions, *slots;
+  const float *inv_freq;
+  float magnitude;
+  int T, Hq, Hkv, D, rot, interleaved;
+  uint16_t *q_out;
+  PagedCache c;  // written
+};
+cudaError_t launch_rope_append(const RopeParams &p, bool e4m3, cudaStream_t s);
+
+// ------------------------------------------------------------ attn_decode.cu --
+struct AttnParams {
+  const uint16_t *q;
+  long long q_stride, out_stride;
+  PagedCache c;
+  const int32_t *block_table, *seq_len, *q_start;  // q_start nullptr: row s for sequence s
+  int max_pages, S, T, Hq, Hkv, D;
+  float scale;
+  int window;
+  uint16_t *out;
+  float *lse;  // or nullptr
+};
+size_t attn_workspace_bytes(int S, int T, int Hq, int Hkv, int D, int num_sms);
+cudaError_t launch_attn_decode(const AttnParams &p, bool e4m3, void *ws, int num_sms,
+                               cudaStream_t s);
+
+}  // namespace ssd

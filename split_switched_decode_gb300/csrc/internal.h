@@ -79,6 +79,13 @@ struct EngineParams {
 // Programmatic dependent launch on or off for this process (DEC_PDL=0 turns it off).
 bool pdl_enabled();
 
+// ------------------------------------------------------------------ api.cu --
+// Host state shared by the entry points of api.cu and api_attn.cu: the fault injection
+// of dec_set_fault_inject (true: report this launch as failed) and the current device's
+// SM count (0 and *err set when no device is usable).
+bool host_consume_fault();
+int host_num_sms(cudaError_t *err);
+
 // cudaLaunchKernelEx with programmatic stream serialisation when enabled, so the kernel
 // may start (and load weights) while the previous kernel of the stream finishes.
 template <typename... KArgs, typename... Args>
