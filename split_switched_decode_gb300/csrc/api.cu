@@ -162,6 +162,12 @@ int host_num_sms(cudaError_t *err) {
   DeviceInfo *d = device_info(err);
   return d ? d->num_sms : 0;
 }
+unsigned *host_wait_status(uint64_t *limit_ns) {
+  cudaError_t e;
+  DeviceInfo *d = device_info(&e);
+  *limit_ns = g_wait_limit_ns.load();
+  return d ? d->status : nullptr;
+}
 }  // namespace ssd
 
 namespace {

@@ -254,7 +254,9 @@ dec_status attn_decode(const dec_bf16 *q, int64_t q_stride, const void *k_cache,
   p.window = window;
   p.out = out;
   p.lse = lse_opt;
-  return status_of(launch_attn_decode(p, kv_type == DEC_KV_E4M3, ws, sms,
+  uint64_t limit = 0;
+  unsigned *status = host_wait_status(&limit);
+  return status_of(launch_attn_decode(p, kv_type == DEC_KV_E4M3, ws, sms, status, limit,
                                       reinterpret_cast<cudaStream_t>(s)));
 }
 

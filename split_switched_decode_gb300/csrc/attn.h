@@ -62,6 +62,6 @@ struct AttnParams {
 };
 size_t attn_workspace_bytes(int S, int T, int Hq, int Hkv, int D, int num_sms);
 cudaError_t launch_attn_decode(const AttnParams &p, bool e4m3, void *ws, int num_sms,
-                               cudaStream_t s);
+                               unsigned *status, uint64_t wait_limit_ns, cudaStream_t s);
 
 }  // namespace ssd

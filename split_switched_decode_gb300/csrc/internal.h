@@ -81,10 +81,12 @@ bool pdl_enabled();
 
 // ------------------------------------------------------------------ api.cu --
 // Host state shared by the entry points of api.cu and api_attn.cu: the fault injection
-// of dec_set_fault_inject (true: report this launch as failed) and the current device's
-// SM count (0 and *err set when no device is usable).
+// of dec_set_fault_inject (true: report this launch as failed), the current device's SM
+// count (0 and *err set when no device is usable), and its status word with the limit of
+// bounded waits.
 bool host_consume_fault();
 int host_num_sms(cudaError_t *err);
+unsigned *host_wait_status(uint64_t *limit_ns);
 
 // cudaLaunchKernelEx with programmatic stream serialisation when enabled, so the kernel
 // may start (and load weights) while the previous kernel of the stream finishes.
