@@ -451,7 +451,8 @@ typedef enum {
  * free_pages int32 [num_free] (NULL allowed when num_free is 0), free_used int32 [1] or
  * NULL (0 used). seq_len may be the array kv_len, and free_used may point to summary[1]:
  * a captured graph then carries the state from step to step. No other output may overlap
- * an input. S in 1..8192 (DEC_ERR_UNSUPPORTED_SHAPE above). No workspace.
+ * an input. S in 1..8192, max_tokens in 1..2^28 (DEC_ERR_UNSUPPORTED_SHAPE above). No
+ * workspace.
  */
 DEC_API dec_status kv_plan(const int32_t *kv_len, const int32_t *new_len, int S, int page_size,
                            int32_t *block_table, int max_pages, const int32_t *free_pages,

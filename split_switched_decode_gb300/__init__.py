@@ -395,27 +395,44 @@ def moe_layer(X, Wcat, E, L, topk, Wgu, Wd, Wgu_shared, Wd_shared, latent, topk_
 
 # ----------------------------------------------------------------- attention ----
 
+# These calls run once per layer and step, so their marshalling is kept short: torch is
+# looked up once, pointers go to ctypes as plain integers.
+_torch = None
+
+
+def _th():
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
+def _raw_stream(stream):
+    if stream is not None:
+        return stream.cuda_stream
+    c = _th()._C
+    return c._cuda_getCurrentRawStream(c._cuda_getDevice())
+
+
 def _int32(t, name, ndim=1):
-    import torch
-    if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous() or t.dim() != ndim:
+    if t.dtype != _th().int32 or not t.is_cuda or not t.is_contiguous() or t.dim() != ndim:
         raise TypeError(f"{name} must be a contiguous int32 CUDA tensor of {ndim} dimension(s)")
     return t.data_ptr()
 
 
 def _scales(t, name, heads):
-    import torch
     if t is None:
         return None
-    if t.dtype != torch.float32 or not t.is_cuda or not t.is_contiguous() or t.numel() != heads:
+    if t.dtype != _th().float32 or not t.is_cuda or not t.is_contiguous() or t.numel() != heads:
         raise TypeError(f"{name} must be a contiguous float32 CUDA tensor of {heads} values")
     return t.data_ptr()
 
 
 def _rows(t, name, heads=None, dim=None):
     """A bf16 [T, heads, D] tensor whose rows are contiguous (any row stride)."""
-    import torch
     shape = t.shape
-    if t.dtype != torch.bfloat16 or not t.is_cuda or len(shape) != 3:
+    if t.dtype != _th().bfloat16 or not t.is_cuda or len(shape) != 3:
         raise TypeError(f"{name} must be a bfloat16 CUDA tensor [rows, heads, D]")
     if (heads is not None and shape[1] != heads) or (dim is not None and shape[2] != dim):
         raise ValueError(f"{name} has shape {tuple(shape)}")
@@ -428,7 +445,7 @@ def _rows(t, name, heads=None, dim=None):
 def _cache(k, v):
     """(type, Hkv, D, pages, page size, strides) of the K and V caches, [pages, Hkv,
     page size, D] tensors of equal type and strides (views of other orders are fine)."""
-    import torch
+    torch = _th()
     if k.dtype == torch.bfloat16:
         kind = KV_BF16
     elif k.dtype == torch.float8_e4m3fn:
@@ -466,7 +483,7 @@ def kv_plan(kv_len, new_len, block_table, free_pages, free_used, page_size, seq_
         _int32(free_pages, "free_pages"), free_pages.numel(),
         None if free_used is None else _int32(free_used, "free_used"), _int32(seq_len, "seq_len"),
         _int32(q_start, "q_start"), _int32(positions, "positions"), _int32(slots, "slots"),
-        max_tokens, _int32(summary, "summary"), _stream(stream)), "kv_plan")
+        max_tokens, _int32(summary, "summary"), _raw_stream(stream)), "kv_plan")
 
 
 def rope_frequencies(rot, base=10000.0, scaling=ROPE_PLAIN, factor=1.0, orig_len=4096,
@@ -502,7 +519,7 @@ def rope_append(q, k, v, positions, slots, inv_freq, q_out, k_cache, v_cache, in
         magnitude, T, Hq, Hkv, D, rot, int(interleaved), op, os_, k_cache.data_ptr(),
         v_cache.data_ptr(), kind, _scales(k_scale, "k_scale", Hkv),
         _scales(v_scale, "v_scale", Hkv), pages, page, stride[0], stride[1], stride[2],
-        _stream(stream)), "rope_append")
+        _raw_stream(stream)), "rope_append")
 
 
 def attn_decode_workspace_bytes(S, T, Hq, Hkv, D) -> int:
@@ -515,7 +532,6 @@ def attn_decode(q, k_cache, v_cache, block_table, seq_len, out, ws, q_start=None
     q_start[s] .. q_start[s+1]-1 are the last tokens of sequence s, which has seq_len[s]
     tokens in the pages block_table[s] (q_start None: one row each). scale: 1/sqrt(D) by
     default; window > 0: a row sees that many last tokens, its own included."""
-    import torch
     kind, Hkv, D, pages, page, stride = _cache(k_cache, v_cache)
     qp, qs = _rows(q, "q", None, D)
     T, Hq, _ = q.shape
@@ -527,7 +543,7 @@ def attn_decode(q, k_cache, v_cache, block_table, seq_len, out, ws, q_start=None
         raise ValueError("attn_decode: sizes do not agree")
     lp = None
     if lse is not None:
-        if lse.dtype != torch.float32 or not lse.is_cuda or not lse.is_contiguous() \
+        if lse.dtype != _th().float32 or not lse.is_cuda or not lse.is_contiguous() \
                 or tuple(lse.shape) != (T, Hq):
             raise TypeError("lse must be a contiguous float32 CUDA tensor [T, Hq]")
         lp = lse.data_ptr()
@@ -537,4 +553,4 @@ def attn_decode(q, k_cache, v_cache, block_table, seq_len, out, ws, q_start=None
         tp, max_pages, _int32(seq_len, "seq_len"),
         None if q_start is None else _int32(q_start, "q_start"), S, T, Hq, Hkv, D,
         D ** -0.5 if scale is None else scale, window, op, os_, lp, ws.data_ptr(),
-        ws.numel() * ws.element_size(), _stream(stream)), "attn_decode")
+        ws.numel() * ws.element_size(), _raw_stream(stream)), "attn_decode")

@@ -66,7 +66,7 @@ dec_status kv_plan(const int32_t *kv_len, const int32_t *new_len, int S, int pag
   if (S < 1 || page_size < 1 || max_pages < 1 || num_free < 0 || max_tokens < 1)
     return DEC_ERR_INVALID_ARG;
   if (num_free > 0 && !free_pages) return DEC_ERR_INVALID_ARG;
-  if (S > ATTN_MAX_SEQS) return DEC_ERR_UNSUPPORTED_SHAPE;
+  if (S > ATTN_MAX_SEQS || max_tokens > (1 << 28)) return DEC_ERR_UNSUPPORTED_SHAPE;
   if (off(kv_len, 4) || off(new_len, 4) || off(block_table, 4) || off(free_pages, 4) ||
       off(free_used, 4) || off(seq_len, 4) || off(q_start, 4) || off(positions, 4) ||
       off(slots, 4) || off(summary, 4))
@@ -170,7 +170,8 @@ dec_status rope_append(const dec_bf16 *q, int64_t q_stride, const dec_bf16 *k, i
     return DEC_ERR_INVALID_ARG;
   }
   cudaError_t ce;
-  if (host_num_sms(&ce) <= 0) return DEC_ERR_CUDA;
+  const int sms = host_num_sms(&ce);
+  if (sms <= 0) return DEC_ERR_CUDA;
   if (host_consume_fault()) return DEC_ERR_CUDA;
   RopeParams p;
   p.q = q;
@@ -193,7 +194,7 @@ dec_status rope_append(const dec_bf16 *q, int64_t q_stride, const dec_bf16 *k, i
   p.q_out = q_out;
   p.c = cache_of(k_cache, v_cache, k_scale, v_scale, num_pages, page_size, page_stride,
                  head_stride, token_stride);
-  return status_of(launch_rope_append(p, kv_type == DEC_KV_E4M3,
+  return status_of(launch_rope_append(p, kv_type == DEC_KV_E4M3, sms,
                                       reinterpret_cast<cudaStream_t>(s)));
 }
 

@@ -46,7 +46,7 @@ struct RopeParams {
   uint16_t *q_out;
   PagedCache c;  // written
 };
-cudaError_t launch_rope_append(const RopeParams &p, bool e4m3, cudaStream_t s);
+cudaError_t launch_rope_append(const RopeParams &p, bool e4m3, int num_sms, cudaStream_t s);
 
 // ------------------------------------------------------------ attn_decode.cu --
 struct AttnParams {

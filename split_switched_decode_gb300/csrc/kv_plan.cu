@@ -6,6 +6,8 @@ namespace ssd {
 namespace {
 
 constexpr int KP_THREADS = 1024;
+constexpr int KP_CLUSTER = 8;
+constexpr int KP_CLUSTER_TOKENS = 4096;  // rows from which a cluster is launched
 
 __device__ __forceinline__ int pages_of(int tokens, int page_size) {
   return tokens / page_size + (tokens % page_size != 0);
@@ -50,9 +52,14 @@ __device__ __forceinline__ int last_at_most(const int *first, int n, int x) {
   return lo;
 }
 
-// One CTA: two sums over the sequences (rows, then new pages) into shared memory, then
-// every new page and every row finds its sequence by bisection. Everything is read before
-// the first output is written, so seq_len may be kv_len and free_used part of summary.
+// Two sums over the sequences (rows, then new pages) into shared memory, then every new page
+// and every row finds its sequence by bisection. What it reads and writes would take 0.1 us
+// for 65 thousand rows: the launch and the dependent steps (lengths, two sums, bisection,
+// page, store) bound it. One CTA does it all, or with many rows a cluster of 8, each with
+// the sums of all sequences and an eighth of the rows. Everything that may be overwritten is
+// read before the (cluster's) barrier and the first output is written after it, so seq_len
+// may be kv_len and free_used part of summary.
+template <bool CLUSTER>
 __global__ void __launch_bounds__(KP_THREADS) kv_plan_kernel(const KvPlanParams p) {
   extern __shared__ int kp_smem[];
   int *row0 = kp_smem;            // [S] first row of the sequence
@@ -64,7 +71,7 @@ __global__ void __launch_bounds__(KP_THREADS) kv_plan_kernel(const KvPlanParams 
   const int tid = threadIdx.x;
   int used = p.free_used ? *p.free_used : 0;
   used = used < 0 ? 0 : (used > p.num_free ? p.num_free : used);
-  long long rows = 0, fresh = 0, wanted = 0, asked = 0;  // sums so far
+  long long rows = 0, fresh = 0, wanted = 0;  // sums so far
   for (int base = 0; base < p.S; base += KP_THREADS) {
     const int s = base + tid;
     int kv = 0, nw = 0;
@@ -78,14 +85,17 @@ __global__ void __launch_bounds__(KP_THREADS) kv_plan_kernel(const KvPlanParams 
     const int r0 = static_cast<int>(first < cap ? first : cap);
     const int r1 = static_cast<int>(first + nw < cap ? first + nw : cap);
     rows += sum;
-    asked += sum;
     const int len = static_cast<int>(min(static_cast<long long>(kv) + (r1 - r0), 0x7fffffffll));
     const int have = pages_of(kv, p.page_size), need = pages_of(len, p.page_size);
     const int have_t = min(have, p.max_pages), need_t = min(need, p.max_pages);
-    const long long f0 = fresh + cta_exclusive_sum(need_t - have_t, &sum);
-    fresh += sum;
-    cta_exclusive_sum(need - have, &sum);
-    wanted += sum;
+    // new pages that the table has room for, and in the upper half those beyond it: both sums
+    // are at most the rows, below 2^31
+    const int beyond = (need - have) - (need_t - have_t);
+    const long long f0 =
+        fresh + (cta_exclusive_sum((static_cast<long long>(beyond) << 32) | (need_t - have_t),
+                                   &sum) & 0xffffffffll);
+    fresh += sum & 0xffffffffll;
+    wanted += (sum & 0xffffffffll) + (sum >> 32);
     if (s < p.S) {
       row0[s] = r0;
       rank0[s] = static_cast<int>(min(f0, 0x7fffffffll));
@@ -93,7 +103,9 @@ __global__ void __launch_bounds__(KP_THREADS) kv_plan_kernel(const KvPlanParams 
       kv0[s] = kv;
     }
   }
-  __syncthreads();
+  if (CLUSTER) cluster_sync_all();
+  else __syncthreads();
+  const int first = blockIdx.x * KP_THREADS + tid, step = gridDim.x * KP_THREADS;
   const int T = static_cast<int>(min(rows, static_cast<long long>(p.max_tokens)));
   const int F = static_cast<int>(min(fresh, 0x7fffffffll));
   auto row_end = [&](int s) { return s + 1 < p.S ? row0[s + 1] : T; };
@@ -101,17 +113,17 @@ __global__ void __launch_bounds__(KP_THREADS) kv_plan_kernel(const KvPlanParams 
   auto page_at = [&](long long r) {
     return used + r < p.num_free ? p.free_pages[used + r] : -1;
   };
-  for (int s = tid; s < p.S; s += KP_THREADS) {
+  for (int s = first; s < p.S; s += step) {
     p.q_start[s] = row0[s];
     p.seq_len[s] = static_cast<int>(
         min(static_cast<long long>(kv0[s]) + (row_end(s) - row0[s]), 0x7fffffffll));
   }
-  for (int f = tid; f < F; f += KP_THREADS) {
+  for (int f = first; f < F; f += step) {
     const int s = last_at_most(rank0, p.S, f);
     p.block_table[static_cast<long long>(s) * p.max_pages + held[s] + (f - rank0[s])] =
         page_at(f);
   }
-  for (int t = tid; t < p.max_tokens; t += KP_THREADS) {
+  for (int t = first; t < p.max_tokens; t += step) {
     int pos = 0, slot = -1;
     if (t < T) {
       const int s = last_at_most(row0, p.S, t);
@@ -128,12 +140,12 @@ __global__ void __launch_bounds__(KP_THREADS) kv_plan_kernel(const KvPlanParams 
     p.positions[t] = pos;
     p.slots[t] = slot;
   }
-  if (tid == 0) {
+  if (first == 0) {
     const long long after = min(used + fresh, static_cast<long long>(p.num_free));
     p.q_start[p.S] = T;
     p.summary[0] = T;
     p.summary[1] = static_cast<int>(after);
-    p.summary[2] = static_cast<int>(min(asked - T, 0x7fffffffll));
+    p.summary[2] = static_cast<int>(min(rows - T, 0x7fffffffll));
     p.summary[3] = static_cast<int>(min(wanted - (after - used), 0x7fffffffll));
   }
 }
@@ -142,12 +154,16 @@ __global__ void __launch_bounds__(KP_THREADS) kv_plan_kernel(const KvPlanParams 
 
 cudaError_t launch_kv_plan(const KvPlanParams &p, cudaStream_t s) {
   const size_t smem = static_cast<size_t>(4) * p.S * sizeof(int);
+  const bool cluster = p.max_tokens > KP_CLUSTER_TOKENS;
+  auto kernel = cluster ? kv_plan_kernel<true> : kv_plan_kernel<false>;
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(
-        kv_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
-  return launch_pdl(kv_plan_kernel, dim3(1), dim3(KP_THREADS), smem, s, p);
+  if (cluster)
+    return launch_pdl_cluster(kernel, dim3(KP_CLUSTER), dim3(KP_THREADS), smem, s, KP_CLUSTER, p);
+  return launch_pdl(kernel, dim3(1), dim3(KP_THREADS), smem, s, p);
 }
 
 }  // namespace ssd

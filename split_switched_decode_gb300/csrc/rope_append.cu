@@ -26,24 +26,173 @@ __device__ __forceinline__ float2 rope_angle(int pos, float freq, float magnitud
   return make_float2(c * magnitude, s * magnitude);
 }
 
-// One CTA per row: the row's angles once into shared memory, then a thread per element.
+// Where a row's key and value go in the cache (elements), or not at all.
+struct RowPlace {
+  bool stored;
+  long long at;
+};
+__device__ __forceinline__ RowPlace row_place(const RopeParams &p, int t) {
+  const int slot = p.slots[t];
+  RowPlace r;
+  // num_pages * page_size fits an int (checked on the host)
+  r.stored = slot >= 0 && slot < p.c.num_pages * p.c.page_size;
+  const int page = slot / p.c.page_size;
+  r.at = r.stored ? page * p.c.page_stride + (slot - page * p.c.page_size) * p.c.token_stride
+                  : 0;
+  return r;
+}
+
+__device__ __forceinline__ void unpack8(uint4 v, float (&x)[8]) {
+  x[0] = bf16lo(v.x), x[1] = bf16hi(v.x), x[2] = bf16lo(v.y), x[3] = bf16hi(v.y);
+  x[4] = bf16lo(v.z), x[5] = bf16hi(v.z), x[6] = bf16lo(v.w), x[7] = bf16hi(v.w);
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+  return make_uint4(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]), bf16x2(x[4], x[5]),
+                    bf16x2(x[6], x[7]));
+}
+// Eight elements of head h's row into the cache.
 template <bool E4M3>
+__device__ __forceinline__ void put8(const void *base, const float *scale, int h, long long at,
+                                     const float (&x)[8]) {
+  if (!E4M3) {
+    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(const_cast<void *>(base)) + at) = pack8(x);
+    return;
+  }
+  const float s = scale ? scale[h] : 1.0f;
+  uint32_t w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    w[i] = 0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float2 y = make_float2(x[4 * i + 2 * k] / s, x[4 * i + 2 * k + 1] / s);
+      w[i] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3))
+              << (16 * k);
+    }
+  }
+  *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(const_cast<void *>(base)) + at) =
+      make_uint2(w[0], w[1]);
+}
+
+// 16 bytes a thread. Read once and written once, 2 to 3 operations an element: the copy rate
+// bounds it, the launch's latency when rows are few. A thread's unit is a chunk of 8
+// elements with its partner half the rotary part away (half pairs), or alone (interleaved
+// pairs, elements that stay, values), so every thread owns what it overwrites and q_out may
+// be q. The row's angles are computed once per CTA into shared memory (FP64 is scarce: 2
+// multiply-adds a clock and SM) while the first unit's elements are on their way. Rows with
+// many CTAs to spare are cut over gridDim.y so that a thread has one unit.
+template <bool E4M3, bool INTER>
 __global__ void __launch_bounds__(RA_THREADS) rope_append_kernel(const RopeParams p) {
   __shared__ float2 cs[ATTN_MAX_D / 2];
   griddep_wait();
   griddep_launch_dependents();
-  const int t = blockIdx.x, D = p.D, half = p.rot / 2;
+  const int t = blockIdx.x, half = p.rot / 2;
+  // units of a q or k head: rotary pairs of chunks (half pairs) or chunks, then the rest
+  const int turning = INTER ? p.rot / 8 : p.rot / 16;
+  const int per_head = turning + (p.D - p.rot) / 8, per_value = p.D / 8;
+  const int qk = (p.Hq + p.Hkv) * per_head, units = qk + p.Hkv * per_value;
+  struct Unit {
+    int h, d0, d1;  // head counted over q, k, v; first element, partner's (or -1)
+    bool turns;
+  };
+  auto unit_of = [&](int u) {
+    Unit x;
+    if (u < qk) {
+      x.h = u / per_head;
+      const int i = u - x.h * per_head;
+      x.turns = i < turning;
+      x.d0 = x.turns || INTER ? 8 * i : p.rot + 8 * (i - turning);
+      x.d1 = x.turns && !INTER ? half + 8 * i : -1;
+    } else {
+      const int i = (u - qk) / per_value;
+      x.h = p.Hq + p.Hkv + i;
+      x.d0 = 8 * (u - qk - i * per_value);
+      x.d1 = -1;
+      x.turns = false;
+    }
+    return x;
+  };
+  auto source = [&](int h) {
+    return h < p.Hq ? p.q + t * p.q_stride + h * p.D
+           : h < p.Hq + p.Hkv ? p.k + t * p.k_stride + (h - p.Hq) * p.D
+                              : p.v + t * p.v_stride + (h - p.Hq - p.Hkv) * p.D;
+  };
+  const int step = gridDim.y * RA_THREADS;
+  int u = blockIdx.y * RA_THREADS + threadIdx.x;
+  Unit x = {};
+  uint4 a = {}, b = {};
+  auto load = [&]() {
+    x = unit_of(u);
+    const uint16_t *src = source(x.h);
+    a = *reinterpret_cast<const uint4 *>(src + x.d0);
+    if (x.d1 >= 0) b = *reinterpret_cast<const uint4 *>(src + x.d1);
+  };
+  if (u < units) load();
+  const RowPlace place = row_place(p, t);
+  if (threadIdx.x < half) {
+    const int pos = p.positions[t];
+    for (int i = threadIdx.x; i < half; i += RA_THREADS)
+      cs[i] = rope_angle(pos, p.inv_freq[i], p.magnitude);
+  }
+  __syncthreads();
+  for (; u < units;) {
+    float y0[8], y1[8];
+    unpack8(a, y0);
+    if (x.turns && INTER) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 w = cs[x.d0 / 2 + i];
+        const float r = y0[2 * i] * w.x - y0[2 * i + 1] * w.y;
+        y0[2 * i + 1] = y0[2 * i + 1] * w.x + y0[2 * i] * w.y;
+        y0[2 * i] = r;
+      }
+    } else if (x.turns) {
+      unpack8(b, y1);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 w = cs[x.d0 + i];
+        const float r = y0[i] * w.x - y1[i] * w.y;
+        y1[i] = y1[i] * w.x + y0[i] * w.y;
+        y0[i] = r;
+      }
+    }
+    if (x.h < p.Hq) {
+      uint16_t *o = p.q_out + t * p.out_stride + x.h * p.D;
+      *reinterpret_cast<uint4 *>(o + x.d0) = pack8(y0);
+      if (x.d1 >= 0) *reinterpret_cast<uint4 *>(o + x.d1) = pack8(y1);
+    } else if (place.stored) {
+      const bool key = x.h < p.Hq + p.Hkv;
+      const int h = key ? x.h - p.Hq : x.h - p.Hq - p.Hkv;
+      const void *base = key ? p.c.k : p.c.v;
+      const float *scale = key ? p.c.k_scale : p.c.v_scale;
+      const long long at = place.at + h * p.c.head_stride;
+      put8<E4M3>(base, scale, h, at + x.d0, y0);
+      if (x.d1 >= 0) put8<E4M3>(base, scale, h, at + x.d1, y1);
+    }
+    u += step;
+    if (u < units) load();
+  }
+}
+
+// Rotary parts that chunks of 8 do not fit (rot % 16 with half pairs, rot % 8 interleaved): a
+// thread per pair of elements.
+template <bool E4M3>
+__global__ void __launch_bounds__(RA_THREADS) rope_append_pairs_kernel(const RopeParams p) {
+  __shared__ float2 cs[ATTN_MAX_D / 2];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int t = blockIdx.x, half = p.rot / 2;
   const int pos = p.positions[t];
   for (int i = threadIdx.x; i < half; i += RA_THREADS)
     cs[i] = rope_angle(pos, p.inv_freq[i], p.magnitude);
   __syncthreads();
-  const long long slot = p.slots[t];
-  const bool stored = slot >= 0 && slot < static_cast<long long>(p.c.num_pages) * p.c.page_size;
-  const long long at = stored ? slot / p.c.page_size * p.c.page_stride +
-                                    slot % p.c.page_size * p.c.token_stride
-                              : 0;
+  const RowPlace place = row_place(p, t);
   auto put = [&](const void *base, const float *scale, int h, int d, float x) {
-    const long long i = at + h * p.c.head_stride + d;
+    const long long i = place.at + h * p.c.head_stride + d;
     if (E4M3) {
       if (scale) x /= scale[h];
       static_cast<uint8_t *>(const_cast<void *>(base))[i] = to_e4m3(x);
@@ -51,28 +200,29 @@ __global__ void __launch_bounds__(RA_THREADS) rope_append_kernel(const RopeParam
       static_cast<uint16_t *>(const_cast<void *>(base))[i] = f32_to_bf16_rn(x);
     }
   };
-  const int units = D / 2;  // a thread handles two elements: a pair, or two that stay
-  for (int u = threadIdx.x; u < (p.Hq + 2 * p.Hkv) * units; u += RA_THREADS) {
+  const int units = p.D / 2;  // two elements: a pair, or two that stay
+  for (int u = blockIdx.y * RA_THREADS + threadIdx.x; u < (p.Hq + 2 * p.Hkv) * units;
+       u += gridDim.y * RA_THREADS) {
     const int h = u / units, i = u - h * units;
     const bool pair = i < half;
     const int d0 = pair && !p.interleaved ? i : 2 * i;
     const int d1 = pair && !p.interleaved ? i + half : 2 * i + 1;
-    const uint16_t *src = h < p.Hq ? p.q + t * p.q_stride + h * D
+    const uint16_t *src = h < p.Hq ? p.q + t * p.q_stride + h * p.D
                           : h < p.Hq + p.Hkv
-                              ? p.k + t * p.k_stride + (h - p.Hq) * D
-                              : p.v + t * p.v_stride + (h - p.Hq - p.Hkv) * D;
+                              ? p.k + t * p.k_stride + (h - p.Hq) * p.D
+                              : p.v + t * p.v_stride + (h - p.Hq - p.Hkv) * p.D;
     float x0 = bf16_to_f32(src[d0]), x1 = bf16_to_f32(src[d1]);
     if (pair && h < p.Hq + p.Hkv) {
-      const float2 a = cs[i];
-      const float y0 = x0 * a.x - x1 * a.y;
-      x1 = x1 * a.x + x0 * a.y;
+      const float2 w = cs[i];
+      const float y0 = x0 * w.x - x1 * w.y;
+      x1 = x1 * w.x + x0 * w.y;
       x0 = y0;
     }
     if (h < p.Hq) {
-      uint16_t *o = p.q_out + t * p.out_stride + h * D;
+      uint16_t *o = p.q_out + t * p.out_stride + h * p.D;
       o[d0] = f32_to_bf16_rn(x0);
       o[d1] = f32_to_bf16_rn(x1);
-    } else if (stored) {
+    } else if (place.stored) {
       const bool key = h < p.Hq + p.Hkv;
       const int hh = key ? h - p.Hq : h - p.Hq - p.Hkv;
       put(key ? p.c.k : p.c.v, key ? p.c.k_scale : p.c.v_scale, hh, d0, x0);
@@ -83,9 +233,25 @@ __global__ void __launch_bounds__(RA_THREADS) rope_append_kernel(const RopeParam
 
 }  // namespace
 
-cudaError_t launch_rope_append(const RopeParams &p, bool e4m3, cudaStream_t s) {
-  return launch_pdl(e4m3 ? rope_append_kernel<true> : rope_append_kernel<false>, dim3(p.T),
-                    dim3(RA_THREADS), 0, s, p);
+cudaError_t launch_rope_append(const RopeParams &p, bool e4m3, int num_sms, cudaStream_t s) {
+  const bool chunks = p.rot % (p.interleaved ? 8 : 16) == 0;
+  const int heads = p.Hq + 2 * p.Hkv;
+  // units of a row, and CTAs for one unit a thread while the row count alone does not give
+  // every SM two CTAs
+  const int units = chunks ? (p.Hq + p.Hkv) *
+                                     ((p.interleaved ? p.rot / 8 : p.rot / 16) + (p.D - p.rot) / 8) +
+                                 p.Hkv * (p.D / 8)
+                           : heads * (p.D / 2);
+  const int cuts = (units + RA_THREADS - 1) / RA_THREADS;
+  const dim3 grid(p.T, p.T < 2 * num_sms ? cuts : 1);
+  void (*kernel)(const RopeParams);
+  if (!chunks)
+    kernel = e4m3 ? rope_append_pairs_kernel<true> : rope_append_pairs_kernel<false>;
+  else if (p.interleaved)
+    kernel = e4m3 ? rope_append_kernel<true, true> : rope_append_kernel<false, true>;
+  else
+    kernel = e4m3 ? rope_append_kernel<true, false> : rope_append_kernel<false, false>;
+  return launch_pdl(kernel, grid, dim3(RA_THREADS), 0, s, p);
 }
 
 }  // namespace ssd

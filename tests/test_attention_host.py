@@ -38,7 +38,7 @@ PLAN_ARGS = [A, A, 4, 16, A, 8, A, 32, A, A, A, A, A, 64, A, None]
     ({7: -1}, "INVALID_ARG"), ({9: N0}, "INVALID_ARG"), ({10: N0}, "INVALID_ARG"),
     ({11: N0}, "INVALID_ARG"), ({12: N0}, "INVALID_ARG"), ({13: 0}, "INVALID_ARG"),
     ({14: N0}, "INVALID_ARG"), ({2: 8193}, "UNSUPPORTED_SHAPE"), ({0: U}, "MISALIGNED"),
-    ({8: U}, "MISALIGNED"), ({14: U}, "MISALIGNED"),
+    ({13: (1 << 28) + 1}, "UNSUPPORTED_SHAPE"), ({8: U}, "MISALIGNED"), ({14: U}, "MISALIGNED"),
 ])
 def test_kv_plan_refusals(ssd, changes, status):
     assert ssd.lib().kv_plan(*_changed(PLAN_ARGS, changes)) == getattr(ssd, "DEC_ERR_" + status)
