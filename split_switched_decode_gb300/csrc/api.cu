@@ -9,6 +9,7 @@
 #include <mutex>
 
 #include "../../include/split_switched_decode.h"
+#include "attn.h"
 #include "common.cuh"
 #include "internal.h"
 
@@ -167,6 +168,23 @@ unsigned *host_wait_status(uint64_t *limit_ns) {
   DeviceInfo *d = device_info(&e);
   *limit_ns = g_wait_limit_ns.load();
   return d ? d->status : nullptr;
+}
+bool host_cache_map(CUtensorMap *m, const PagedCache &c, const void *base, bool e4m3, int D,
+                    int Hkv, int box, int padded) {
+  if (!encoder_ready()) return false;
+  const cuuint64_t es = e4m3 ? 1 : 2;
+  const cuuint32_t row = padded * es >= 128 ? 128 : 64;  // bytes
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(c.page_size),
+                        static_cast<cuuint64_t>(Hkv), static_cast<cuuint64_t>(c.num_pages)};
+  cuuint64_t strides[3] = {c.token_stride * es, c.head_stride * es, c.page_stride * es};
+  cuuint32_t boxes[4] = {static_cast<cuuint32_t>(row / es), static_cast<cuuint32_t>(box), 1, 1};
+  cuuint32_t one[4] = {1, 1, 1, 1};
+  return g_encode(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                  const_cast<void *>(base), dims, strides, boxes, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  row == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 }  // namespace ssd
 

@@ -59,7 +59,27 @@ struct AttnParams {
   int window;
   uint16_t *out;
   float *lse;  // or nullptr
+  int box;     // tokens of a TMA box of the caches (8..64), 0: 16-byte copies
 };
+// What a launch needs besides the parameters.
+struct AttnLaunch {
+  CUtensorMap kmap, vmap;  // of the caches where box > 0
+  int num_sms;
+  unsigned *status;
+  uint64_t wait_limit_ns;
+};
+// One kernel per padded head size (attn_d64.cu, attn_d128.cu, attn_d256.cu); nr groups of 8
+// rows a warp, wr warps sharing the rows.
+cudaError_t launch_attn_d64(const AttnParams &p, bool e4m3, int nr, int wr, void *ws,
+                            const AttnLaunch &a, cudaStream_t s);
+cudaError_t launch_attn_d128(const AttnParams &p, bool e4m3, int nr, int wr, void *ws,
+                             const AttnLaunch &a, cudaStream_t s);
+cudaError_t launch_attn_d256(const AttnParams &p, bool e4m3, int nr, int wr, void *ws,
+                             const AttnLaunch &a, cudaStream_t s);
+// api.cu: a 4-D map (head element, token of the page, kv head, page) of a cache, boxes of
+// 128 bytes (64 where a padded head has 64 bytes) x box tokens, swizzled accordingly.
+bool host_cache_map(CUtensorMap *m, const PagedCache &c, const void *base, bool e4m3, int D,
+                    int Hkv, int box, int padded);
 size_t attn_workspace_bytes(int S, int T, int Hq, int Hkv, int D, int num_sms);
 cudaError_t launch_attn_decode(const AttnParams &p, bool e4m3, void *ws, int num_sms,
                                unsigned *status, uint64_t wait_limit_ns, cudaStream_t s);

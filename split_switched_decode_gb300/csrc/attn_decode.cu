@@ -1,821 +1,64 @@
-// attn_decode.cu -- attention of new tokens over a paged key-value cache.
-//
-// For a kv head and the rows r = (new token i, head g of the group) that read it,
-//
-//     out_r = sum_j p_rj v_j / sum_j p_rj,   p_rj = 2^(z_rj - m_r),   z = scale log2(e) q.k
-//
-// in one pass over the keys with a running maximum m and sum l. The keys and values are
-// read once from HBM and carry 2 G multiply-adds a byte (G rows), so the copy rate bounds
-// it; the work is cut so that every SM streams the same number of tokens:
-//
-//   - An item is one (sequence, kv head, tile of M = 16 WR rows). Its keys are cut into
-//     stages of 64 tokens (128 with 8-bit elements). All stages of all items, in order, with
-//     a fixed charge for every item's start and end, are divided evenly among the CTAs; a CTA
-//     works through its range segment by segment (a segment is its part of one item).
-//   - Two warps fill a ring of stages with 16-byte asynchronous copies, looking up the page
-//     of every token; they run ahead across segments, so the next item's keys stream while
-//     the last one is joined and written.
-//   - Four warps multiply. WR of them share the rows, 4 / WR the tokens of a stage: with up
-//     to 16 rows each warp takes a quarter of the tokens with its own m, l and output
-//     accumulators (no exchange until the segment ends), with 64 rows each takes 16 of them
-//     and all tokens. Both products run on mma.sync m16n8k16 with the rows as M: scores and
-//     weights stay in registers, and the weights' accumulator layout is the next product's
-//     operand layout.
-//   - At the end of a segment the warps' (m, l, out) are joined in the memory of the
-//     segment's last stage. An item that lies in one CTA is finished there; otherwise each
-//     CTA stores its fp32 partial in the workspace, and the last to arrive at the item's
-//     counter adds them in CTA order: the result depends on the lengths only.
-//
-// e4m3 caches are widened to f16 in registers (every e4m3 value is an f16 value); q is
-// scaled by a power of two per row so that its largest element is in [1, 2) and converted
-// to f16: exact but for elements 2^-14 below the row's largest. The key scale joins the
-// score's factor, the value scale the last division.
-//
-// Every wait on an mbarrier is bounded; after a time-out the waits return at once and the
-// control flow, which depends on the lengths alone, runs to its end over stale data.
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
-
+// attn_decode.cu -- host side of the attention kernel (attn_kernel.cuh): the kernel's shape
+// by head size and rows, the workspace, and the tensor maps of the caches.
 #include "attn.h"
-#include "common.cuh"
 
 namespace ssd {
 namespace {
 
-constexpr int AT_CWARPS = 4;  // warps that multiply
-constexpr int AT_PWARPS = 2;  // warps that copy
-constexpr int AT_CTHREADS = 32 * AT_CWARPS;
-constexpr int AT_THREADS = 32 * (AT_CWARPS + AT_PWARPS);
-constexpr int AT_ITEM_COST = 1;  // stages that an item's start and end are charged as
-constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
-
-template <bool E4M3, int DP, int WR>
-struct AttnCfg {
-  static constexpr int ES = E4M3 ? 1 : 2;        // bytes of a cache element
-  static constexpr int M = 16 * WR;              // rows of an item
-  static constexpr int STEP = E4M3 ? 32 : 16;    // tokens of a warp's inner step
-  static constexpr int TOK = AT_CWARPS * STEP;   // tokens of a stage
-  static constexpr int RB = DP * ES;             // bytes of a token's row in a stage
-  static constexpr int CPR = RB / 16;            // 16-byte chunks of a row
-  static constexpr int STAGE = 2 * TOK * RB;     // K then V
-  static constexpr int ST = DP == 64 ? 4 : (DP == 128 && WR == 4 ? 2 : 3);
-  static constexpr int QB = WR == 1 || (DP == 128 && WR == 4) ? 2 : 1;  // buffers of q
-  static constexpr int QBYTES = M * DP * 2;
-  static constexpr size_t SMEM = ST * STAGE + QB * QBYTES;
-  static constexpr int CTAS = DP <= 128 ? 2 : 1;  // per SM
-  // one partial result: M rows of DP outputs, then m and l of the rows
-  static constexpr int SLOT = M * DP + 2 * M;
-  // the join buffer, 64 rows of DP floats, is exactly a stage
-  static_assert(STAGE == AT_CWARPS * 16 * DP * 4, "join buffer");
-};
-
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-template <bool F16>
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
-  if (F16)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// 16 bytes global -> shared; zeros where !valid (nothing is read).
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(valid ? 16 : 0)
-               : "memory");
-}
-// Arrive on `bar` once this thread's copies so far have landed.
-__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
-               : "memory");
-}
-__device__ __forceinline__ void cp_async_wait_all() {
-  asm volatile("cp.async.wait_all;" ::: "memory");
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// two e4m3 (low 16 bits) -> two f16
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t x) {
-  uint32_t y;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t}"
-      : "=r"(y)
-      : "r"(x));
-  return y;
-}
-template <bool F16>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  uint32_t y;
-  if (F16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
-  else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
-  return y;
-}
-// Shared-memory byte offset of 16-byte chunk `ch` of row `row` (rows of RB bytes): eight
-// consecutive rows' equal chunks fall into different 16-byte bank groups.
-template <int RB>
-__device__ __forceinline__ uint32_t swz(int row, int ch) {
-  return row * RB + ((ch ^ (RB >= 128 ? row & 7 : (row >> 1) & 3)) << 4);
-}
-
-// One sequence's rows and keys.
-struct SeqInfo {
-  int q0, n;       // first row, rows
-  int len, begin;  // keys [begin, len) that some row can see
-  int kt;          // stages of keys (at least 1: an empty row still has to be written)
-  int rt;          // row tiles
-  __device__ __forceinline__ long long units(int Hkv) const {
-    return static_cast<long long>(Hkv) * rt * (kt + AT_ITEM_COST);
-  }
-};
-
-template <int TOK, int M>
-__device__ __forceinline__ SeqInfo seq_info(const AttnParams &p, int G, int s) {
-  SeqInfo x;
-  x.q0 = s;
-  x.n = 1;
-  if (p.q_start) {
-    x.q0 = min(max(p.q_start[s], 0), p.T);
-    x.n = max(0, min(max(p.q_start[s + 1], 0), p.T) - x.q0);
-  }
-  // what the table holds, and no token number of a stage's end passes 2^31
-  const long long cap =
-      min(static_cast<long long>(p.max_pages) * p.c.page_size, 0x7fffff00ll);
-  x.len = static_cast<int>(min(static_cast<long long>(max(p.seq_len[s], 0)), cap));
-  const int pos = x.len - x.n;  // the first row's
-  x.begin = p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
-  x.kt = x.len > x.begin ? (x.len - x.begin - 1) / TOK + 1 : 1;
-  x.rt = (x.n * G + M - 1) / M;
-  return x;
-}
-
-struct AttnPlan {
-  int min_units;  // units a worker takes at least
-  float *partials;
-  int *counters;
-  unsigned *status;
-  uint64_t wait_limit_ns;
-};
-
-// All items' units in order (an item: AT_ITEM_COST, then one per stage), and worker c's
-// share of them: share_n, one more for the first share_r workers.
-struct Shares {
-  long long share_n, share_r;
-  __device__ __forceinline__ int worker_of(long long unit) const {
-    const long long longer = share_r * (share_n + 1);
-    return static_cast<int>(unit < longer ? unit / (share_n + 1)
-                                          : share_r + (unit - longer) / share_n);
-  }
-};
-
-// Walks the segments of one CTA's range.
-template <int TOK, int M>
-struct Cursor {
-  long long cur, end, item;  // next unit, end of the range, first unit of the item
-  int s, hk, rt, t0, t1;     // segment: stages [t0, t1) of item (s, hk, rt)
-  SeqInfo x;
-  // The next segment that has a stage; false at the end of the range.
-  __device__ __forceinline__ bool next(const AttnParams &p, int G) {
-    while (cur < end) {
-      const long long stop = item + AT_ITEM_COST + x.kt;
-      if (cur == stop) {  // the next item
-        item = cur;
-        if (++rt == x.rt) {
-          rt = 0;
-          if (++hk == p.Hkv) {
-            hk = 0;
-            do x = seq_info<TOK, M>(p, G, ++s);
-            while (x.rt == 0);
-          }
-        }
-        continue;
-      }
-      const long long from = cur, to = stop < end ? stop : end;
-      cur = to;
-      t0 = static_cast<int>(max(from - item - AT_ITEM_COST, 0ll));
-      t1 = static_cast<int>(to - item - AT_ITEM_COST);
-      if (t1 > t0) return true;
-    }
-    return false;
-  }
-};
-
-template <bool E4M3, int DP, int WR>
-__global__ void __launch_bounds__(AT_THREADS, (AttnCfg<E4M3, DP, WR>::CTAS))
-    attn_decode_kernel(const AttnParams p, const AttnPlan pl) {
-  using C = AttnCfg<E4M3, DP, WR>;
-  constexpr int TOK = C::TOK, STEP = C::STEP, RB = C::RB, NT = STEP / 8, M = C::M, ST = C::ST;
-  extern __shared__ __align__(128) uint8_t at_smem[];
-  __shared__ long long warp_sum[AT_CWARPS + AT_PWARPS];
-  __shared__ long long start_off;
-  __shared__ __align__(8) uint64_t full[ST], empty[ST], qempty[C::QB];
-  __shared__ float join_ml[AT_CWARPS * 16][2];         // m, l of each warp's rows
-  __shared__ uint32_t stage_valid[ST][TOK / 32];       // tokens of the stage that exist
-  __shared__ int start_seq, is_last, abort_flag;
-  uint8_t *q_smem = at_smem + ST * C::STAGE;
-
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) {
-    abort_flag = 0;
-    for (int i = 0; i < ST; ++i) {
-      mbar_init(&full[i], AT_PWARPS * 33);  // every copying thread's copies, and each warp
-      mbar_init(&empty[i], AT_CWARPS);
-    }
-    for (int i = 0; i < C::QB; ++i) mbar_init(&qempty[i], AT_CWARPS);
-    fence_mbar_init();
-  }
-  griddep_wait();
-  griddep_launch_dependents();
-  const int G = p.Hq / p.Hkv;
-
-  // ---- this CTA's share of all units: one pass over the sequences
-  const int per = (p.S + AT_THREADS - 1) / AT_THREADS;
-  const int s_lo = min(tid * per, p.S), s_hi = min(s_lo + per, p.S);
-  long long mine = 0;
-  for (int s = s_lo; s < s_hi; ++s) mine += seq_info<TOK, M>(p, G, s).units(p.Hkv);
-  long long incl = mine;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += y;
-  }
-  if (lane == 31) warp_sum[warp] = incl;
-  __syncthreads();
-  long long total = 0, before = 0;
-#pragma unroll
-  for (int w = 0; w < AT_CWARPS + AT_PWARPS; ++w) {
-    if (w < warp) before += warp_sum[w];
-    total += warp_sum[w];
-  }
-  const long long most = (total + pl.min_units - 1) / pl.min_units;
-  const int workers = static_cast<int>(most < gridDim.x ? most : gridDim.x);
-  const int me = blockIdx.x;
-  if (me >= workers) return;
-  const Shares sh = {total / workers, total % workers};
-  Cursor<TOK, M> c;
-  c.cur = me * sh.share_n + min(static_cast<long long>(me), sh.share_r);
-  c.end = c.cur + sh.share_n + (me < sh.share_r ? 1 : 0);
-  {
-    long long at = before + incl - mine;  // units before this thread's sequences
-    if (at <= c.cur && c.cur < at + mine) {
-      for (int s = s_lo; s < s_hi; ++s) {
-        const long long n = seq_info<TOK, M>(p, G, s).units(p.Hkv);
-        if (c.cur < at + n) {
-          start_seq = s;
-          start_off = c.cur - at;
-          break;
-        }
-        at += n;
-      }
-    }
-  }
-  __syncthreads();
-  c.s = start_seq;
-  c.x = seq_info<TOK, M>(p, G, c.s);
-  {
-    const long long per_item = c.x.kt + AT_ITEM_COST, i = start_off / per_item;
-    c.hk = static_cast<int>(i / c.x.rt);
-    c.rt = static_cast<int>(i - static_cast<long long>(c.hk) * c.x.rt);
-    c.item = c.cur - (start_off - i * per_item);
-  }
-
-  if (warp >= AT_CWARPS) {
-    // ================================================================ copying warps
-    constexpr int NTOK = TOK / (32 * AT_PWARPS);  // tokens of a lane
-    const int pw = warp - AT_CWARPS;
-    const char *kbase = static_cast<const char *>(p.c.k);
-    const char *vbase = static_cast<const char *>(p.c.v);
-    int k = 0, seg = 0;  // stages and segments so far
-    while (c.next(p, G)) {
-      const int32_t *table = p.block_table + static_cast<long long>(c.s) * p.max_pages;
-      auto token_of = [&](int t, int q) {
-        return c.x.begin + t * TOK + (pw * NTOK + q) * 32 + lane;
-      };
-      int page[NTOK];
-      auto look_up = [&](int t) {
-#pragma unroll
-        for (int q = 0; q < NTOK; ++q) {
-          const int j = token_of(t, q);
-          page[q] = t < c.t1 && j < c.x.len ? table[j / p.c.page_size] : -1;
-        }
-      };
-      look_up(c.t0);
-      for (int t = c.t0; t < c.t1; ++t, ++k) {
-        const int st = k % ST;
-        if (k >= ST)
-          mbar_wait_bounded(&empty[st], ((k / ST) - 1) & 1, pl.status, &abort_flag,
-                            pl.wait_limit_ns);
-        const uint32_t dst = smem_u32(at_smem + st * C::STAGE);
-#pragma unroll
-        for (int q = 0; q < NTOK; ++q) {
-          const bool ok = page[q] >= 0 && page[q] < p.c.num_pages;
-          long long off = -1;
-          if (ok)
-            off = (page[q] * p.c.page_stride + c.hk * p.c.head_stride +
-                   token_of(t, q) % p.c.page_size * p.c.token_stride) * C::ES;
-          const uint32_t valid = __ballot_sync(0xffffffffu, ok);
-          if (lane == 0) stage_valid[st][pw * NTOK + q] = valid;
-#pragma unroll
-          for (int i = 0; i < C::CPR; ++i) {
-            const int row = (i * 32 + lane) / C::CPR, ch = (i * 32 + lane) % C::CPR;
-            const long long o = __shfl_sync(0xffffffffu, off, row);
-            const bool in = o >= 0 && ch * 16 < p.D * C::ES;
-            const long long at = in ? o + ch * 16 : 0;
-            const uint32_t d = dst + swz<RB>((pw * NTOK + q) * 32 + row, ch);
-            cp_async16(d, kbase + at, in);
-            cp_async16(d + TOK * RB, vbase + at, in);
-          }
-        }
-        look_up(t + 1);
-        if (t == c.t0) {
-          // the item's rows of q, zeros past them and past D
-          const int qb = seg % C::QB;
-          if (seg >= C::QB)
-            mbar_wait_bounded(&qempty[qb], ((seg / C::QB) - 1) & 1, pl.status, &abort_flag,
-                              pl.wait_limit_ns);
-          const int n_rows = min(M, c.x.n * G - c.rt * M);
-          const uint32_t qd = smem_u32(q_smem + qb * C::QBYTES);
-#pragma unroll 4
-          for (int i = pw * 32 + lane; i < M * DP / 8; i += 32 * AT_PWARPS) {
-            const int r = i / (DP / 8), ch = i % (DP / 8);
-            const bool in = r < n_rows && ch * 8 < p.D;
-            const int rr = c.rt * M + (in ? r : 0), tok = rr / G, g = rr - tok * G;
-            cp_async16(qd + swz<DP * 2>(r, ch),
-                       p.q + (c.x.q0 + tok) * p.q_stride +
-                           static_cast<long long>(c.hk * G + g) * p.D + (in ? ch * 8 : 0),
-                       in);
-          }
-          ++seg;
-        }
-        cp_async_arrive(&full[st]);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&full[st]);
-      }
-    }
-    cp_async_wait_all();
-    return;
-  }
-
-  // ================================================================ multiplying warps
-  const int wr = warp % WR, wt = warp / WR;  // which rows, which tokens of a stage
-  const int ra = lane >> 2;
-  int k = 0, seg = 0;
-  while (c.next(p, G)) {
-    const SeqInfo &x = c.x;
-    const int n_rows = min(M, x.n * G - c.rt * M);        // of the item
-    const int my_rows = min(16, n_rows - wr * 16);        // of this warp, may be <= 0
-    const int row0 = c.rt * M + wr * 16;                  // this warp's first
-
-    // ---- this thread's two rows: what they see, and their score factor
-    float zf[2];
-    int lo[2], hi[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = max(min(ra + 8 * h, my_rows - 1), 0);  // rows past the last: as the last
-      hi[h] = x.len - x.n + (row0 + r) / G;
-      lo[h] = p.window > 0 && hi[h] >= p.window ? hi[h] - p.window + 1 : 0;
-      zf[h] = p.scale * LOG2E * (p.c.k_scale ? p.c.k_scale[c.hk] : 1.0f);
-    }
-    // what every row of this warp sees: [lo_all, hi_all]
-    const int hi_all = x.len - x.n + row0 / G;
-    const int hi_top = x.len - x.n + (row0 + max(my_rows, 1) - 1) / G;
-    const int lo_all = p.window > 0 && hi_top >= p.window ? hi_top - p.window + 1 : 0;
-
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-    float o[DP / 8][4];
-#pragma unroll
-    for (int i = 0; i < DP / 8; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[i][e] = 0.0f;
-    uint32_t qf[DP / 16][4];
-
-    for (int t = c.t0; t < c.t1; ++t, ++k) {
-      const int st = k % ST;
-      mbar_wait_bounded(&full[st], (k / ST) & 1, pl.status, &abort_flag, pl.wait_limit_ns);
-      const uint8_t *stage = at_smem + st * C::STAGE;
-      if (t == c.t0) {
-        const uint8_t *qs = q_smem + (seg % C::QB) * C::QBYTES;
-        if (!E4M3) {
-#pragma unroll
-          for (int kk = 0; kk < DP / 16; ++kk)
-            ldsm4(qf[kk], smem_u32(qs) + swz<DP * 2>(wr * 16 + (lane & 15), 2 * kk + (lane >> 4)));
-        } else {
-          // f16 operands in the order in which the widened keys come out of their
-          // registers: of each 16 elements this thread holds 4c .. 4c + 3 of its two rows
-          float mx[2] = {0.0f, 0.0f};
-          uint2 raw[DP / 16][2];
-#pragma unroll
-          for (int kk = 0; kk < DP / 16; ++kk)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int c4 = lane & 3;
-              raw[kk][h] = *reinterpret_cast<const uint2 *>(
-                  qs + swz<DP * 2>(wr * 16 + ra + 8 * h, 2 * kk + (c4 >> 1)) + (c4 & 1) * 8);
-              mx[h] = fmaxf(mx[h], fmaxf(fmaxf(fabsf(bf16lo(raw[kk][h].x)),
-                                               fabsf(bf16hi(raw[kk][h].x))),
-                                         fmaxf(fabsf(bf16lo(raw[kk][h].y)),
-                                               fabsf(bf16hi(raw[kk][h].y)))));
-            }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
-            mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
-            int e = static_cast<int>(__float_as_uint(mx[h]) >> 23) - 127;
-            if (mx[h] == 0.0f || e > 127) e = 0;  // zeros, infinities: as they are
-            if (e < -126) e = -126;
-            const float f = e == 127 ? 0.5f * __uint_as_float(1u << 23)
-                                     : __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-            zf[h] *= __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-#pragma unroll
-            for (int kk = 0; kk < DP / 16; ++kk) {
-              const uint2 v = raw[kk][h];
-              qf[kk][h] = pack2<true>(bf16lo(v.x) * f, bf16hi(v.x) * f);
-              qf[kk][2 + h] = pack2<true>(bf16lo(v.y) * f, bf16hi(v.y) * f);
-            }
-          }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&qempty[seg % C::QB]);
-      }
-      if (my_rows > 0) {
-#pragma unroll 1
-        for (int sub = 0; sub < WR; ++sub) {
-          const int tok0 = (wt * WR + sub) * STEP;  // of the stage
-          const uint32_t ks = smem_u32(stage) + tok0 * RB, vs = ks + TOK * RB;
-          const uint32_t valid = STEP == 32 ? stage_valid[st][tok0 >> 5]
-                                            : stage_valid[st][tok0 >> 5] >> (tok0 & 31);
-          const int j0 = x.begin + t * TOK + tok0;
-
-          // ---- scores [16 rows, STEP tokens]
-          float z[NT][4];
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) z[n][e] = 0.0f;
-#pragma unroll
-          for (int kk = 0; kk < DP / 16; kk += E4M3 ? 2 : 1) {
-#pragma unroll
-            for (int tb = 0; tb < STEP / 16; ++tb) {
-              uint32_t r[4];
-              if (E4M3) {
-                ldsm4(r, ks + swz<RB>(tb * 16 + (lane & 15), kk + (lane >> 4)));
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {  // token half q & 1, k step q >> 1
-                  const uint32_t b0 = e4m3x2_to_f16x2(r[q]), b1 = e4m3x2_to_f16x2(r[q] >> 16);
-                  mma16816<true>(z[2 * tb + (q & 1)], qf[E4M3 ? kk + (q >> 1) : kk], b0, b1);
-                }
-              } else {
-                ldsm4(r, ks + swz<RB>(tb * 16 + (lane & 7) + ((lane >> 4) << 3),
-                                      2 * kk + ((lane >> 3) & 1)));
-                mma16816<false>(z[2 * tb], qf[kk], r[0], r[1]);
-                mma16816<false>(z[2 * tb + 1], qf[kk], r[2], r[3]);
-              }
-            }
-          }
-          // ---- running maximum
-          const uint32_t every = STEP == 32 ? 0xffffffffu : (1u << (STEP & 31)) - 1;
-          const bool plain =
-              (valid & every) == every && j0 >= lo_all && j0 + STEP - 1 <= hi_all;
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) z[n][e] *= zf[e >> 1];
-          if (!plain) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int b = n * 8 + 2 * (lane & 3) + (e & 1), j = j0 + b;
-                if (j < lo[e >> 1] || j > hi[e >> 1] || !(valid >> b & 1)) z[n][e] = -INFINITY;
-              }
-          }
-          float base[2], fade[2];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float mx = m[h];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) mx = fmaxf(mx, fmaxf(z[n][2 * h], z[n][2 * h + 1]));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            base[h] = mx == -INFINITY ? 0.0f : mx;
-            fade[h] = ex2(m[h] - base[h]);
-            m[h] = mx;
-            l[h] *= fade[h];
-          }
-          if (__any_sync(0xffffffffu, fade[0] != 1.0f || fade[1] != 1.0f)) {
-#pragma unroll
-            for (int d = 0; d < DP / 8; ++d)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) o[d][e] *= fade[e >> 1];
-          }
-          // ---- weights: summed in fp32, rounded to 16 bits for the product with V (relative
-          // error 2^-9 bf16, 2^-12 f16 for each, independent of one another: below the
-          // output's own rounding once summed)
-          uint32_t w[NT][2];
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              z[n][e] = ex2(z[n][e] - base[e >> 1]);
-              l[e >> 1] += z[n][e];
-            }
-            w[n][0] = pack2<E4M3>(z[n][0], z[n][1]);
-            w[n][1] = pack2<E4M3>(z[n][2], z[n][3]);
-          }
-          // ---- a value that is not finite at a token that some rows do not see must not
-          // reach them as 0 * inf: such steps (the last few of an item) take the values'
-          // finite part through the product and add the rest where it is seen. A
-          // sequence's only row sees every token that is loaded.
-          bool unclean = false;
-          const uint8_t *vrow = stage + (TOK + tok0) * RB;
-          if (x.n > 1 && !plain) {
-            bool bad = false;
-            for (int i = lane; i < STEP * C::CPR; i += 32) {
-              const uint4 v = *reinterpret_cast<const uint4 *>(vrow + i * 16);
-              const uint32_t e[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                if (E4M3) bad |= __vcmpeq4(e[q] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
-                else bad |= __vcmpeq2(e[q] & 0x7f807f80u, 0x7f807f80u) != 0;
-              }
-            }
-            unclean = __any_sync(0xffffffffu, bad);
-          }
-          // ---- out += weights . values
-#pragma unroll
-          for (int tb = 0; tb < STEP / 16; ++tb) {
-            const uint32_t a[4] = {w[2 * tb][0], w[2 * tb][1], w[2 * tb + 1][0],
-                                   w[2 * tb + 1][1]};
-#pragma unroll
-            for (int dd = 0; dd < DP / 16; dd += E4M3 ? 2 : 1) {
-              uint32_t r[4];
-              ldsm4_t(r, vs + swz<RB>(tb * 16 + (lane & 15), (E4M3 ? dd : 2 * dd) + (lane >> 4)));
-              if (unclean) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                  r[q] &= E4M3 ? ~__vcmpeq4(r[q] & 0x7f7f7f7fu, 0x7f7f7f7fu)
-                               : ~__vcmpeq2(r[q] & 0x7f807f80u, 0x7f807f80u);
-              }
-              if (E4M3) {
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                  const uint32_t x0 = __byte_perm(r[2 * q], 0, 0x3120);
-                  const uint32_t x1 = __byte_perm(r[2 * q + 1], 0, 0x3120);
-                  mma16816<true>(o[E4M3 ? 2 * (dd + q) : 0], a, e4m3x2_to_f16x2(x0),
-                                 e4m3x2_to_f16x2(x1));
-                  mma16816<true>(o[E4M3 ? 2 * (dd + q) + 1 : 0], a, e4m3x2_to_f16x2(x0 >> 16),
-                                 e4m3x2_to_f16x2(x1 >> 16));
-                }
-              } else {
-                mma16816<false>(o[2 * dd], a, r[0], r[1]);
-                mma16816<false>(o[2 * dd + 1], a, r[2], r[3]);
-              }
-            }
-          }
-          if (unclean) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-#pragma unroll 1
-                for (int q = 0; q < 4; ++q) {
-                  const int from = (lane & ~3) | q, row = tok0 + n * 8 + 2 * q + e;
-                  const float pa = __shfl_sync(0xffffffffu, z[n][e], from);
-                  const float pb = __shfl_sync(0xffffffffu, z[n][2 + e], from);
-#pragma unroll
-                  for (int d = 0; d < DP / 8; ++d)
-#pragma unroll
-                    for (int f = 0; f < 2; ++f) {
-                      const int col = E4M3 ? 16 * (d >> 1) + 4 * (lane & 3) + 2 * f + (d & 1)
-                                           : 8 * d + 2 * (lane & 3) + f;
-                      const uint8_t *at = stage + TOK * RB + swz<RB>(row, col * C::ES >> 4) +
-                                          (col * C::ES & 15);
-                      float val = NAN;
-                      bool bad = E4M3 && (*at & 0x7f) == 0x7f;
-                      if (!E4M3) {
-                        const uint16_t b = *reinterpret_cast<const uint16_t *>(at);
-                        bad = (b & 0x7f80) == 0x7f80;
-                        val = bf16_to_f32(b);
-                      }
-                      if (bad && pa != 0.0f) o[d][f] += pa * val;
-                      if (bad && pb != 0.0f) o[d][2 + f] += pb * val;
-                    }
-                }
-          }
-        }
-      }
-      if (t + 1 < c.t1) {  // the stage is free again; the segment's last one after the join
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[st]);
-      }
-    }
-    ++seg;
-
-    // ---- join the warps in the last stage's memory: row r of warp w at w * 16 + r, its
-    // 16-byte chunks permuted by the row so that a warp's stores spread over the banks
-    const int last_st = (k - 1) % ST;
-    float *join = reinterpret_cast<float *>(at_smem + last_st * C::STAGE);
-    auto join_at = [&](int row, int col) {  // col a multiple of 2; rows of DP floats
-      return join + row * DP + ((col >> 2) ^ ((row & 7) << 1)) * 4 + (col & 3);
-    };
-    named_bar_sync(1, AT_CTHREADS);  // every warp has read the stage
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-      const int r = ra + 8 * h, row = warp * 16 + r;
-      if ((lane & 3) == 0) {
-        join_ml[row][0] = m[h];
-        join_ml[row][1] = l[h];
-      }
-      if (r < my_rows) {
-        if (E4M3) {
-#pragma unroll
-          for (int d = 0; d < DP / 16; ++d)
-            *reinterpret_cast<float4 *>(join_at(row, 16 * d + 4 * (lane & 3))) =
-                make_float4(o[2 * d][2 * h], o[2 * d + 1][2 * h], o[2 * d][2 * h + 1],
-                            o[2 * d + 1][2 * h + 1]);
-        } else {
-#pragma unroll
-          for (int d = 0; d < DP / 8; ++d)
-            *reinterpret_cast<float2 *>(join_at(row, 8 * d + 2 * (lane & 3))) =
-                make_float2(o[d][2 * h], o[d][2 * h + 1]);
-        }
-      }
-    }
-    named_bar_sync(1, AT_CTHREADS);
-
-    const long long first = c.item + AT_ITEM_COST;  // the unit of the item's first stage
-    const int c0 = sh.worker_of(first), c1 = sh.worker_of(first + x.kt - 1);
-    const float v_scale = p.c.v_scale ? p.c.v_scale[c.hk] : 1.0f;
-    auto row_out = [&](int r, int d, float4 v, float mr, float lr) {
-      const int rr = c.rt * M + r, i = rr / G, g = rr - i * G;
-      const float inv = v_scale / lr;
-      if (lr == 0.0f) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // nothing seen
-      else v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-      uint2 u;
-      u.x = pack2<false>(v.x, v.y);
-      u.y = pack2<false>(v.z, v.w);
-      const long long row = x.q0 + i, head = c.hk * G + g;
-      *reinterpret_cast<uint2 *>(p.out + row * p.out_stride + head * p.D + d) = u;
-      if (p.lse && d == 0)
-        p.lse[row * p.Hq + head] = lr == 0.0f ? -INFINITY : (mr + log2f(lr)) * LN2;
-    };
-    const int cols = p.D / 4;
-    float *slot = pl.partials + static_cast<size_t>(2 * me + (me == c0 ? 1 : 0)) * C::SLOT;
-    for (int i = tid; i < n_rows * cols; i += AT_CTHREADS) {
-      const int r = i / cols, d = 4 * (i - r * cols);
-      float mr = -INFINITY;
-#pragma unroll
-      for (int g = 0; g < AT_CWARPS / WR; ++g)
-        mr = fmaxf(mr, join_ml[g * M + r][0]);
-      const float b = mr == -INFINITY ? 0.0f : mr;
-      float lr = 0.0f;
-      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-      for (int g = 0; g < AT_CWARPS / WR; ++g) {
-        const float f = ex2(join_ml[g * M + r][0] - b);
-        const float4 y = *reinterpret_cast<const float4 *>(join_at(g * M + r, d));
-        lr += f * join_ml[g * M + r][1];
-        v.x += f * y.x;
-        v.y += f * y.y;
-        v.z += f * y.z;
-        v.w += f * y.w;
-      }
-      if (c0 == c1) {
-        row_out(r, d, v, mr, lr);
-      } else {
-        *reinterpret_cast<float4 *>(slot + r * DP + d) = v;
-        if (d == 0) {
-          slot[M * DP + 2 * r] = mr;
-          slot[M * DP + 2 * r + 1] = lr;
-        }
-      }
-    }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&empty[last_st]);
-    // ---- join the CTAs of a split item: the last to arrive
-    if (c0 != c1) {
-      named_bar_sync(1, AT_CTHREADS);
-      if (tid == 0) is_last = atom_add_acq_rel_gpu(pl.counters + c0, 1) == c1 - c0;
-      named_bar_sync(1, AT_CTHREADS);
-      if (is_last) {
-        if (tid == 0) pl.counters[c0] = 0;
-        auto part = [&](int i) {
-          return pl.partials + static_cast<size_t>(2 * i + (i == c0 ? 1 : 0)) * C::SLOT;
-        };
-        for (int i = tid; i < n_rows * cols; i += AT_CTHREADS) {
-          const int r = i / cols, d = 4 * (i - r * cols);
-          float mr = -INFINITY;
-#pragma unroll 8
-          for (int q = c0; q <= c1; ++q) mr = fmaxf(mr, __ldcg(part(q) + M * DP + 2 * r));
-          const float b = mr == -INFINITY ? 0.0f : mr;
-          float lr = 0.0f;
-          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-          for (int q = c0; q <= c1; ++q) {
-            const float *y = part(q);
-            const float f = ex2(__ldcg(y + M * DP + 2 * r) - b);
-            const float4 u = __ldcg(reinterpret_cast<const float4 *>(y + r * DP + d));
-            lr += f * __ldcg(y + M * DP + 2 * r + 1);
-            v.x += f * u.x;
-            v.y += f * u.y;
-            v.z += f * u.z;
-            v.w += f * u.w;
-          }
-          row_out(r, d, v, mr, lr);
-        }
-      }
-    }
-  }
-}
-
 int padded_dim(int D) { return D <= 64 ? 64 : (D <= 128 ? 128 : 256); }
 
-// CTAs: two per SM by shared memory, one above D = 128.
-int attn_grid(int D, int num_sms) { return padded_dim(D) <= 128 ? 2 * num_sms : num_sms; }
+struct AttnShape {
+  int nr, wr;  // 8-row groups of a warp, warps sharing the rows
+  int rows() const { return 8 * nr * wr; }
+};
 
-// Rows of an item, from what the host knows: the rows of an average sequence.
-int attn_wr(int S, int T, int Hq, int Hkv) {
+// Rows of an item, from what the host knows: the rows of an average sequence. More rows than
+// an item holds read the keys once more per item (mostly from L2).
+AttnShape attn_shape(int S, int T, int Hq, int Hkv) {
   const long long rows = static_cast<long long>((T + S - 1) / S) * (Hq / Hkv);
-  return rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
+  return rows <= 8 ? AttnShape{1, 1}
+                   : (rows <= 16 ? AttnShape{2, 1}
+                                 : (rows <= 32 ? AttnShape{2, 2} : AttnShape{2, 4}));
 }
 
-size_t counter_bytes(int grid) {
-  return (static_cast<size_t>(grid) * sizeof(int) + 255) / 256 * 256;
-}
-
-template <bool E4M3, int DP, int WR>
-cudaError_t launch(const AttnParams &p, const AttnPlan &pl, int grid, cudaStream_t s) {
-  using C = AttnCfg<E4M3, DP, WR>;
-  auto kernel = attn_decode_kernel<E4M3, DP, WR>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(C::SMEM));
-  if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3(grid), dim3(AT_THREADS), C::SMEM, s, p, pl);
-}
-
-template <bool E4M3, int DP>
-cudaError_t launch_rows(const AttnParams &p, const AttnPlan &pl, int grid, cudaStream_t s) {
-  switch (attn_wr(p.S, p.T, p.Hq, p.Hkv)) {
-    case 1:
-      return launch<E4M3, DP, 1>(p, pl, grid, s);
-    case 2:
-      return launch<E4M3, DP, 2>(p, pl, grid, s);
-    default:
-      return launch<E4M3, DP, 4>(p, pl, grid, s);
-  }
+// Tokens of a TMA box: the largest power of two in the page size, up to what a copying warp
+// brings of a stage; below 8 (a swizzle group) none.
+int box_tokens(int page_size, bool e4m3) {
+  const int most = e4m3 ? 64 : 32;
+  int box = page_size & -page_size;
+  if (box > most) box = most;
+  return box >= 8 ? box : 0;
 }
 
 }  // namespace
 
 // Counters (one per worker, zero between calls), then two partial slots per worker.
 size_t attn_workspace_bytes(int S, int T, int Hq, int Hkv, int D, int num_sms) {
-  const int grid = attn_grid(D, num_sms), M = 16 * attn_wr(S, T, Hq, Hkv);
-  return counter_bytes(grid) +
-         static_cast<size_t>(2) * grid * (M * padded_dim(D) + 2 * M) * sizeof(float);
+  const int dp = padded_dim(D), grid = dp <= 128 ? 2 * num_sms : num_sms;
+  const size_t M = attn_shape(S, T, Hq, Hkv).rows();
+  const size_t counters = (static_cast<size_t>(grid) * sizeof(int) + 255) / 256 * 256;
+  return counters + 2 * grid * (M * dp + 2 * M) * sizeof(float);
 }
 
-cudaError_t launch_attn_decode(const AttnParams &p, bool e4m3, void *ws, int num_sms,
+cudaError_t launch_attn_decode(const AttnParams &params, bool e4m3, void *ws, int num_sms,
                                unsigned *status, uint64_t wait_limit_ns, cudaStream_t s) {
-  const int grid = attn_grid(p.D, num_sms);
-  AttnPlan pl;
-  pl.min_units = 1 + AT_ITEM_COST;
-  pl.counters = static_cast<int *>(ws);
-  pl.partials = reinterpret_cast<float *>(static_cast<char *>(ws) + counter_bytes(grid));
-  pl.status = status;
-  pl.wait_limit_ns = wait_limit_ns;
-  switch (padded_dim(p.D)) {
-    case 64:
-      return e4m3 ? launch_rows<true, 64>(p, pl, grid, s) : launch_rows<false, 64>(p, pl, grid, s);
-    case 128:
-      return e4m3 ? launch_rows<true, 128>(p, pl, grid, s)
-                  : launch_rows<false, 128>(p, pl, grid, s);
-    default:
-      return e4m3 ? launch_rows<true, 256>(p, pl, grid, s)
-                  : launch_rows<false, 256>(p, pl, grid, s);
+  AttnParams p = params;
+  AttnLaunch a = {};
+  a.num_sms = num_sms;
+  a.status = status;
+  a.wait_limit_ns = wait_limit_ns;
+  const int dp = padded_dim(p.D);
+  p.box = box_tokens(p.c.page_size, e4m3);
+  if (p.box > 0) {
+    // strides of zero (a broadcast cache) or an encoder that refuses: plain copies
+    const bool ok = p.c.page_stride > 0 && p.c.head_stride > 0 && p.c.token_stride > 0 &&
+                    host_cache_map(&a.kmap, p.c, p.c.k, e4m3, p.D, p.Hkv, p.box, dp) &&
+                    host_cache_map(&a.vmap, p.c, p.c.v, e4m3, p.D, p.Hkv, p.box, dp);
+    if (!ok) p.box = 0;
   }
+  const AttnShape sh = attn_shape(p.S, p.T, p.Hq, p.Hkv);
+  auto launch = dp == 64 ? launch_attn_d64 : (dp == 128 ? launch_attn_d128 : launch_attn_d256);
+  return launch(p, e4m3, sh.nr, sh.wr, ws, a, s);
 }
 
 }  // namespace ssd

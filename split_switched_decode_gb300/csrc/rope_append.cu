@@ -8,7 +8,7 @@
 namespace ssd {
 namespace {
 
-constexpr int RA_THREADS = 256;
+constexpr int RA_THREADS = 128;
 constexpr float E4M3_MAX = 448.0f;
 
 __device__ __forceinline__ uint8_t to_e4m3(float x) {
@@ -123,13 +123,14 @@ __global__ void __launch_bounds__(RA_THREADS) rope_append_kernel(const RopeParam
   };
   const int step = gridDim.y * RA_THREADS;
   int u = blockIdx.y * RA_THREADS + threadIdx.x;
-  Unit x = {};
-  uint4 a = {}, b = {};
+  // a unit's elements are requested one unit before they are used
+  Unit next = {};
+  uint4 next_a = {}, next_b = {};
   auto load = [&]() {
-    x = unit_of(u);
-    const uint16_t *src = source(x.h);
-    a = *reinterpret_cast<const uint4 *>(src + x.d0);
-    if (x.d1 >= 0) b = *reinterpret_cast<const uint4 *>(src + x.d1);
+    next = unit_of(u);
+    const uint16_t *src = source(next.h);
+    next_a = *reinterpret_cast<const uint4 *>(src + next.d0);
+    if (next.d1 >= 0) next_b = *reinterpret_cast<const uint4 *>(src + next.d1);
   };
   if (u < units) load();
   const RowPlace place = row_place(p, t);
@@ -139,9 +140,13 @@ __global__ void __launch_bounds__(RA_THREADS) rope_append_kernel(const RopeParam
       cs[i] = rope_angle(pos, p.inv_freq[i], p.magnitude);
   }
   __syncthreads();
-  for (; u < units;) {
+  while (u < units) {
+    const Unit x = next;
     float y0[8], y1[8];
-    unpack8(a, y0);
+    unpack8(next_a, y0);
+    unpack8(next_b, y1);
+    u += step;
+    if (u < units) load();
     if (x.turns && INTER) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -151,7 +156,6 @@ __global__ void __launch_bounds__(RA_THREADS) rope_append_kernel(const RopeParam
         y0[2 * i] = r;
       }
     } else if (x.turns) {
-      unpack8(b, y1);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float2 w = cs[x.d0 + i];
@@ -173,8 +177,6 @@ __global__ void __launch_bounds__(RA_THREADS) rope_append_kernel(const RopeParam
       put8<E4M3>(base, scale, h, at + x.d0, y0);
       if (x.d1 >= 0) put8<E4M3>(base, scale, h, at + x.d1, y1);
     }
-    u += step;
-    if (u < units) load();
   }
 }
 
