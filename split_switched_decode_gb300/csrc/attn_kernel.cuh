@@ -247,11 +247,122 @@ struct Cursor {
   }
 };
 
+// Four outputs of one row, divided, rounded and stored; the row's lse with its first four.
+struct ItemOut {
+  int q0, row0, head0, G;  // first row of the sequence; of the item; its first head
+  float v_scale;
+  __device__ __forceinline__ void put(const AttnParams &p, int r, int d, float4 v, float m,
+                                      float l) const {
+    const int rr = row0 + r, i = rr / G, g = rr - i * G;
+    const float inv = v_scale / l;
+    if (l == 0.0f) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // nothing seen
+    else v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+    uint2 u;
+    u.x = pack2<false>(v.x, v.y);
+    u.y = pack2<false>(v.z, v.w);
+    const long long row = q0 + i, head = head0 + g;
+    *reinterpret_cast<uint2 *>(p.out + row * p.out_stride + head * p.D + d) = u;
+    if (p.lse && d == 0)
+      p.lse[row * p.Hq + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * LN2;
+  }
+};
+
+struct PendingJoin {
+  int c0, parts, n_rows;  // first worker, workers, rows
+  ItemOut dst;
+};
+
+// The workers' partial results of one item, added in their order: every (m, l) into shared
+// memory `ml` in one round trip (hundreds of parts of 64 rows do not fit there and are read
+// where they are), then the outputs with 16 loads of a thread on their way (a round trip to
+// the other die's L2 is 0.7 us; one load at a time took 0.25 us a part). Runs after a CTA's
+// last segment, when neither registers nor stages hold anything else.
+template <int M, int DP, int FIT>
+__device__ __forceinline__ void join_parts(const AttnParams &p, const float *partials, float2 *ml,
+                                        int c0, int parts, int n_rows, ItemOut dst) {
+  constexpr int SLOT = M * DP + 2 * M, AHEAD = 8;
+  const int tid = threadIdx.x, cols = p.D / 4;
+  auto part = [&](int q) {
+    return partials + static_cast<size_t>(2 * (c0 + q) + (q == 0 ? 1 : 0)) * SLOT;
+  };
+  auto ml_of = [&](int q, int r) {
+    return __ldcg(reinterpret_cast<const float2 *>(part(q) + M * DP + 2 * r));
+  };
+  auto add = [](float4 &v, float &l, float4 u, float2 y, float base) {
+    const float f = ex2(y.x - base);
+    l += f * y.y;
+    v.x += f * u.x;
+    v.y += f * u.y;
+    v.z += f * u.z;
+    v.w += f * u.w;
+  };
+  const bool fits = parts * n_rows <= FIT;
+  if (fits) {
+#pragma unroll 4
+    for (int i = tid; i < parts * n_rows; i += AT_CTHREADS)
+      ml[i] = ml_of(i / n_rows, i % n_rows);
+    named_bar_sync(1, AT_CTHREADS);
+  }
+  for (int i = tid; i < n_rows * cols; i += 2 * AT_CTHREADS) {
+    // two blocks of four outputs at once
+    const int blocks = i + AT_CTHREADS < n_rows * cols ? 2 : 1;
+    int r[2], d[2];
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, base[2];
+    float4 v[2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int at = i + (b < blocks ? b : 0) * AT_CTHREADS;
+      r[b] = at / cols;
+      d[b] = 4 * (at - r[b] * cols);
+      v[b] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+    if (fits) {
+      for (int q0 = 0; q0 < parts; q0 += AHEAD) {
+        float4 u[2][AHEAD];
+#pragma unroll
+        for (int e = 0; e < AHEAD; ++e)
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+            if (q0 + e < parts)
+              u[b][e] = __ldcg(
+                  reinterpret_cast<const float4 *>(part(q0 + e) + r[b] * DP + d[b]));
+        if (q0 == 0) {
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+#pragma unroll 4
+            for (int q = 0; q < parts; ++q) m[b] = fmaxf(m[b], ml[q * n_rows + r[b]].x);
+            base[b] = m[b] == -INFINITY ? 0.0f : m[b];
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < AHEAD; ++e)
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+            if (q0 + e < parts)
+              add(v[b], l[b], u[b][e], ml[(q0 + e) * n_rows + r[b]], base[b]);
+      }
+    } else {
+#pragma unroll 1
+      for (int b = 0; b < 2; ++b) {
+        for (int q = 0; q < parts; ++q) m[b] = fmaxf(m[b], ml_of(q, r[b]).x);
+        base[b] = m[b] == -INFINITY ? 0.0f : m[b];
+        for (int q = 0; q < parts; ++q)
+          add(v[b], l[b],
+              __ldcg(reinterpret_cast<const float4 *>(part(q) + r[b] * DP + d[b])),
+              ml_of(q, r[b]), base[b]);
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+      if (b < blocks) dst.put(p, r[b], d[b], v[b], m[b], l[b]);
+  }
+}
+
 template <bool E4M3, int DP, int NR, int WR>
 __global__ void __launch_bounds__(AT_THREADS, (AttnCfg<E4M3, DP, NR, WR>::CTAS))
     attn_decode_kernel(const __grid_constant__ CUtensorMap kmap,
-                       const __grid_constant__ CUtensorMap vmap, const AttnParams p,
-                       const AttnPlan pl) {
+                       const __grid_constant__ CUtensorMap vmap,
+                       const __grid_constant__ AttnParams p, const AttnPlan pl) {
   using C = AttnCfg<E4M3, DP, NR, WR>;
   constexpr int TOK = C::TOK, STEP = C::STEP, RB = C::RB, M = C::M, MW = C::MW, ST = C::ST;
   constexpr int MT = STEP / 16;  // 16-token tiles of a step
@@ -261,12 +372,14 @@ __global__ void __launch_bounds__(AT_THREADS, (AttnCfg<E4M3, DP, NR, WR>::CTAS))
   __shared__ __align__(8) uint64_t full[ST], empty[ST], qempty[C::QB];
   __shared__ float join_ml[AT_CWARPS * MW][2];         // m, l of each warp's rows
   __shared__ uint32_t stage_valid[ST][TOK / 32];       // tokens of the stage that exist
-  __shared__ int start_seq, is_last, abort_flag;
+  __shared__ int start_seq, abort_flag, n_pending;
+  __shared__ PendingJoin pending[2];  // a range splits at most its first and last item
   uint8_t *q_smem = at_smem + ST * C::STAGE;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     abort_flag = 0;
+    n_pending = 0;
     for (int i = 0; i < ST; ++i) {
       mbar_init(&full[i], AT_PWARPS * 33);  // every copying thread's copies, and each warp
       mbar_init(&empty[i], AT_CWARPS);
@@ -350,17 +463,18 @@ __global__ void __launch_bounds__(AT_THREADS, (AttnCfg<E4M3, DP, NR, WR>::CTAS))
       const int32_t *table = p.block_table + static_cast<long long>(c.s) * p.max_pages;
       // first token of this warp in stage t, and the page of the token (or box) a lane copies
       auto token0 = [&](int t) { return c.x.begin + t * TOK + pw * HALF; };
-      int page[WORDS];
-      auto look_up = [&](int t) {
+      int page[WORDS], ahead[WORDS];  // of this stage and the next
+      auto look_up = [&](int t, int (&to)[WORDS]) {
 #pragma unroll
         for (int q = 0; q < WORDS; ++q) {
           const int j = token0(t) + (p.box > 0 ? block * box : q * 32 + lane);
-          page[q] = t < c.t1 && j < c.x.len && (p.box == 0 || (has_box && q == 0))
+          to[q] = t < c.t1 && j < c.x.len && (p.box == 0 || (has_box && q == 0))
                         ? table[j / p.c.page_size]
                         : -1;
         }
       };
-      look_up(c.t0);
+      look_up(c.t0, page);
+      look_up(c.t0 + 1, ahead);
       for (int t = c.t0; t < c.t1; ++t, ++k) {
         const int st = k % ST, j0 = token0(t);
         if (k >= ST)
@@ -410,7 +524,9 @@ __global__ void __launch_bounds__(AT_THREADS, (AttnCfg<E4M3, DP, NR, WR>::CTAS))
             }
           }
         }
-        look_up(t + 1);
+#pragma unroll
+        for (int q = 0; q < WORDS; ++q) page[q] = ahead[q];
+        look_up(t + 2, ahead);
         if (t == c.t0) {
           // the item's rows of q, zeros past them and past D
           const int qb = seg % C::QB;
@@ -806,20 +922,8 @@ __global__ void __launch_bounds__(AT_THREADS, (AttnCfg<E4M3, DP, NR, WR>::CTAS))
 
     const long long first = c.item + AT_ITEM_COST;  // the unit of the item's first stage
     const int c0 = sh.worker_of(first), c1 = sh.worker_of(first + x.kt - 1);
-    const float v_scale = p.c.v_scale ? p.c.v_scale[c.hk] : 1.0f;
-    auto row_out = [&](int r, int d, float4 v, float mr, float lr) {
-      const int rr = c.rt * M + r, i = rr / G, g = rr - i * G;
-      const float inv = v_scale / lr;
-      if (lr == 0.0f) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // nothing seen
-      else v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-      uint2 u;
-      u.x = pack2<false>(v.x, v.y);
-      u.y = pack2<false>(v.z, v.w);
-      const long long row = x.q0 + i, head = c.hk * G + g;
-      *reinterpret_cast<uint2 *>(p.out + row * p.out_stride + head * p.D + d) = u;
-      if (p.lse && d == 0)
-        p.lse[row * p.Hq + head] = lr == 0.0f ? -INFINITY : (mr + log2f(lr)) * LN2;
-    };
+    const ItemOut dst = {x.q0, c.rt * M, c.hk * G, G,
+                         p.c.v_scale ? p.c.v_scale[c.hk] : 1.0f};
     const int cols = p.D / 4;
     float *slot = pl.partials + static_cast<size_t>(2 * me + (me == c0 ? 1 : 0)) * C::SLOT;
     for (int i = tid; i < n_rows * cols; i += AT_CTHREADS) {
@@ -842,65 +946,31 @@ __global__ void __launch_bounds__(AT_THREADS, (AttnCfg<E4M3, DP, NR, WR>::CTAS))
         v.w += f * y.w;
       }
       if (c0 == c1) {
-        row_out(r, d, v, mr, lr);
+        dst.put(p, r, d, v, mr, lr);
       } else {
         *reinterpret_cast<float4 *>(slot + r * DP + d) = v;
         if (d == 0)
           *reinterpret_cast<float2 *>(slot + M * DP + 2 * r) = make_float2(mr, lr);
       }
     }
-    // ---- join the CTAs of a split item: the last to arrive
-    if (c0 != c1) {
-      named_bar_sync(1, AT_CTHREADS);
-      if (tid == 0) is_last = atom_add_acq_rel_gpu(pl.counters + c0, 1) == c1 - c0;
-      named_bar_sync(1, AT_CTHREADS);
-      if (is_last) {
-        if (tid == 0) pl.counters[c0] = 0;
-        auto part = [&](int i) {
-          return pl.partials + static_cast<size_t>(2 * i + (i == c0 ? 1 : 0)) * C::SLOT;
-        };
-        // every partial's (m, l) into the stage's memory, a round trip for all of them, then
-        // the outputs with several loads on their way; hundreds of parts of 64 rows do not
-        // fit there and read (m, l) where they are
-        const int parts = c1 - c0 + 1;
-        const bool fits = parts * n_rows <= C::STAGE / 8;
-        float2 *ml = reinterpret_cast<float2 *>(join);
-        auto ml_of = [&](int q, int r) {
-          return __ldcg(reinterpret_cast<const float2 *>(part(c0 + q) + M * DP + 2 * r));
-        };
-        if (fits) {
-          for (int i = tid; i < parts * n_rows; i += AT_CTHREADS)
-            ml[i] = ml_of(i / n_rows, i % n_rows);
-          named_bar_sync(1, AT_CTHREADS);
-        }
-        for (int i = tid; i < n_rows * cols; i += AT_CTHREADS) {
-          const int r = i / cols, d = 4 * (i - r * cols);
-          float mr = -INFINITY;
-#pragma unroll 4
-          for (int q = 0; q < parts; ++q)
-            mr = fmaxf(mr, (fits ? ml[q * n_rows + r] : ml_of(q, r)).x);
-          const float b = mr == -INFINITY ? 0.0f : mr;
-          float lr = 0.0f;
-          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-          for (int q = 0; q < parts; ++q) {
-            const float4 u =
-                __ldcg(reinterpret_cast<const float4 *>(part(c0 + q) + r * DP + d));
-            const float2 y = fits ? ml[q * n_rows + r] : ml_of(q, r);
-            const float f = ex2(y.x - b);
-            lr += f * y.y;
-            v.x += f * u.x;
-            v.y += f * u.y;
-            v.z += f * u.z;
-            v.w += f * u.w;
-          }
-          row_out(r, d, v, mr, lr);
-        }
-      }
-    }
     fence_proxy_async_smem();  // before later boxes overwrite the join's stores
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[last_st]);
+    // ---- a split item: the last CTA to arrive joins it, once its own range is done
+    if (c0 != c1) {
+      named_bar_sync(1, AT_CTHREADS);
+      if (tid == 0 && atom_add_acq_rel_gpu(pl.counters + c0, 1) == c1 - c0) {
+        pl.counters[c0] = 0;
+        pending[n_pending++] = {c0, c1 - c0 + 1, n_rows, dst};
+      }
+    }
+  }
+  named_bar_sync(1, AT_CTHREADS);
+  for (int i = 0; i < n_pending; ++i) {
+    join_parts<M, DP, ST * C::STAGE / 8>(p, pl.partials, reinterpret_cast<float2 *>(at_smem),
+                                         pending[i].c0, pending[i].parts, pending[i].n_rows,
+                                         pending[i].dst);
+    named_bar_sync(1, AT_CTHREADS);
   }
 }
 
