@@ -32,11 +32,12 @@ int box_tokens(int page_size, bool e4m3) {
 
 }  // namespace
 
-// Counters (one per worker, zero between calls), then two partial slots per worker.
+// Counters (one per worker for items, two for groups of workers, zero between calls), then two
+// partial slots per worker.
 size_t attn_workspace_bytes(int S, int T, int Hq, int Hkv, int D, int num_sms) {
   const int dp = padded_dim(D), grid = dp <= 128 ? 2 * num_sms : num_sms;
   const size_t M = attn_shape(S, T, Hq, Hkv).rows();
-  const size_t counters = (static_cast<size_t>(grid) * sizeof(int) + 255) / 256 * 256;
+  const size_t counters = (static_cast<size_t>(3) * grid * sizeof(int) + 255) / 256 * 256;
   return counters + 2 * grid * (M * dp + 2 * M) * sizeof(float);
 }
 

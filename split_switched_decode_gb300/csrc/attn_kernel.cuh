@@ -52,6 +52,8 @@ constexpr int AT_PWARPS = 2;  // warps that copy
 constexpr int AT_CTHREADS = 32 * AT_CWARPS;
 constexpr int AT_THREADS = 32 * (AT_CWARPS + AT_PWARPS);
 constexpr int AT_ITEM_COST = 1;  // stages that an item's start and end are charged as
+constexpr int AT_MIN_UNITS = 2;  // units a worker takes at least
+constexpr int AT_GROUP = 16;     // workers whose parts of a much split item are joined first
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
 template <bool E4M3, int DP, int NR, int WR>
@@ -197,9 +199,8 @@ __device__ __forceinline__ SeqInfo seq_info(const AttnParams &p, int G, int s) {
 }
 
 struct AttnPlan {
-  int min_units;  // units a worker takes at least
   float *partials;
-  int *counters;
+  int *counters, *group_counters;
   unsigned *status;
   uint64_t wait_limit_ns;
 };
@@ -247,6 +248,46 @@ struct Cursor {
   }
 };
 
+// A copying warp's boxes of one stage: HALF tokens of K and V, lane -> (block of `box`
+// tokens, slab of 128 bytes, K or V), at most 32 boxes.
+template <int RB, int TOK, int ES>
+struct BoxLane {
+  static constexpr int HALF = TOK / AT_PWARPS, WORDS = HALF / 32;
+  static constexpr int SLABS = RB == 64 ? 1 : RB / 128, ROW = RB == 64 ? 64 : 128;
+  static constexpr int PER_BLOCK = 2 * SLABS;
+  int box, block, slab;
+  bool has;
+  __device__ __forceinline__ BoxLane(int tokens, int lane)
+      : box(tokens), block(lane / PER_BLOCK), slab((lane >> 1) % SLABS),
+        has(block * tokens < HALF) {}
+  // Into stage memory `dst` (K, then V TOK * RB bytes on); j0: the warp's first token, at
+  // most `len` of the sequence exist; `page` the page of this lane's block, < 0 for none.
+  // Writes the bits of the tokens that exist and arrives on `full` with the bytes to come.
+  __device__ __forceinline__ void issue(const CUtensorMap *kmap, const CUtensorMap *vmap,
+                                        const PagedCache &cache, uint32_t dst, uint64_t *full,
+                                        uint32_t *valid_words, int pw, int lane, int j0, int len,
+                                        int hk, int page) const {
+    const bool ok = page >= 0 && page < cache.num_pages;
+    const uint32_t blocks = __ballot_sync(0xffffffffu, ok);
+#pragma unroll
+    for (int q = 0; q < WORDS; ++q) {
+      const int tok = q * 32 + lane;
+      const uint32_t valid = __ballot_sync(
+          0xffffffffu, (blocks >> (tok / box * PER_BLOCK) & 1) && j0 + tok < len);
+      if (lane == 0) valid_words[pw * WORDS + q] = valid;
+    }
+    if (lane == 0) mbar_arrive_expect_tx(full, __popc(blocks) * box * ROW);
+    __syncwarp();
+    if (ok) {
+      const bool val = lane & 1;
+      tma_load_4d(dst + (val ? TOK * RB : 0) + slab * (TOK * 128) +
+                      (pw * HALF + block * box) * ROW,
+                  val ? vmap : kmap, full, slab * (128 / ES),
+                  (j0 + block * box) % cache.page_size, hk, page);
+    }
+  }
+};
+
 // Four outputs of one row, divided, rounded and stored; the row's lse with its first four.
 struct ItemOut {
   int q0, row0, head0, G;  // first row of the sequence; of the item; its first head
@@ -268,41 +309,32 @@ struct ItemOut {
 };
 
 struct PendingJoin {
-  int c0, parts, n_rows;  // first worker, workers, rows
+  int c0, parts, group, n_rows;  // first worker, workers, group (-1: the whole item), rows
   ItemOut dst;
 };
 
-// The workers' partial results of one item, added in their order: every (m, l) into shared
-// memory `ml` in one round trip (hundreds of parts of 64 rows do not fit there and are read
-// where they are), then the outputs with 16 loads of a thread on their way (a round trip to
-// the other die's L2 is 0.7 us; one load at a time took 0.25 us a part). Runs after a CTA's
-// last segment, when neither registers nor stages hold anything else.
-template <int M, int DP, int FIT>
-__device__ __forceinline__ void join_parts(const AttnParams &p, const float *partials, float2 *ml,
-                                        int c0, int parts, int n_rows, ItemOut dst) {
+// Where workers leave their parts of an item: worker c has slot 2c for the item that began
+// before its range and 2c + 1 for one that begins in it, and so do the counters of the groups.
+__device__ __forceinline__ int part_slot(int c0, int q) { return 2 * (c0 + q) + (q == 0 ? 1 : 0); }
+
+// Parts first, first + every, ... of an item (n of them), added in their order, into dst or
+// (to != nullptr) as one part. Every (m, l) comes into shared memory `ml` in one round trip,
+// then the outputs with 16 loads of a thread on their way (a round trip to the other die's
+// L2 is 0.7 us; one load at a time took 0.25 us a part).
+template <int M, int DP>
+__device__ __forceinline__ void join_parts(const AttnParams &p, float *partials, float2 *ml,
+                                           int c0, int first, int every, int n, int n_rows,
+                                           float *to, const ItemOut &dst) {
   constexpr int SLOT = M * DP + 2 * M, AHEAD = 8;
   const int tid = threadIdx.x, cols = p.D / 4;
-  auto part = [&](int q) {
-    return partials + static_cast<size_t>(2 * (c0 + q) + (q == 0 ? 1 : 0)) * SLOT;
+  auto part = [&](int i) {
+    return partials + static_cast<size_t>(part_slot(c0, first + i * every)) * SLOT;
   };
-  auto ml_of = [&](int q, int r) {
-    return __ldcg(reinterpret_cast<const float2 *>(part(q) + M * DP + 2 * r));
-  };
-  auto add = [](float4 &v, float &l, float4 u, float2 y, float base) {
-    const float f = ex2(y.x - base);
-    l += f * y.y;
-    v.x += f * u.x;
-    v.y += f * u.y;
-    v.z += f * u.z;
-    v.w += f * u.w;
-  };
-  const bool fits = parts * n_rows <= FIT;
-  if (fits) {
 #pragma unroll 4
-    for (int i = tid; i < parts * n_rows; i += AT_CTHREADS)
-      ml[i] = ml_of(i / n_rows, i % n_rows);
-    named_bar_sync(1, AT_CTHREADS);
-  }
+  for (int i = tid; i < n * n_rows; i += AT_CTHREADS)
+    ml[i] = __ldcg(
+        reinterpret_cast<const float2 *>(part(i / n_rows) + M * DP + 2 * (i % n_rows)));
+  named_bar_sync(1, AT_CTHREADS);
   for (int i = tid; i < n_rows * cols; i += 2 * AT_CTHREADS) {
     // two blocks of four outputs at once
     const int blocks = i + AT_CTHREADS < n_rows * cols ? 2 : 1;
@@ -316,45 +348,103 @@ __device__ __forceinline__ void join_parts(const AttnParams &p, const float *par
       d[b] = 4 * (at - r[b] * cols);
       v[b] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
-    if (fits) {
-      for (int q0 = 0; q0 < parts; q0 += AHEAD) {
-        float4 u[2][AHEAD];
+    for (int q0 = 0; q0 < n; q0 += AHEAD) {
+      float4 u[2][AHEAD];
 #pragma unroll
-        for (int e = 0; e < AHEAD; ++e)
+      for (int e = 0; e < AHEAD; ++e)
 #pragma unroll
-          for (int b = 0; b < 2; ++b)
-            if (q0 + e < parts)
-              u[b][e] = __ldcg(
-                  reinterpret_cast<const float4 *>(part(q0 + e) + r[b] * DP + d[b]));
-        if (q0 == 0) {
+        for (int b = 0; b < 2; ++b)
+          if (q0 + e < n)
+            u[b][e] = __ldcg(reinterpret_cast<const float4 *>(part(q0 + e) + r[b] * DP + d[b]));
+      if (q0 == 0) {
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < 2; ++b) {
 #pragma unroll 4
-            for (int q = 0; q < parts; ++q) m[b] = fmaxf(m[b], ml[q * n_rows + r[b]].x);
-            base[b] = m[b] == -INFINITY ? 0.0f : m[b];
-          }
+          for (int q = 0; q < n; ++q) m[b] = fmaxf(m[b], ml[q * n_rows + r[b]].x);
+          base[b] = m[b] == -INFINITY ? 0.0f : m[b];
         }
-#pragma unroll
-        for (int e = 0; e < AHEAD; ++e)
-#pragma unroll
-          for (int b = 0; b < 2; ++b)
-            if (q0 + e < parts)
-              add(v[b], l[b], u[b][e], ml[(q0 + e) * n_rows + r[b]], base[b]);
       }
-    } else {
-#pragma unroll 1
-      for (int b = 0; b < 2; ++b) {
-        for (int q = 0; q < parts; ++q) m[b] = fmaxf(m[b], ml_of(q, r[b]).x);
-        base[b] = m[b] == -INFINITY ? 0.0f : m[b];
-        for (int q = 0; q < parts; ++q)
-          add(v[b], l[b],
-              __ldcg(reinterpret_cast<const float4 *>(part(q) + r[b] * DP + d[b])),
-              ml_of(q, r[b]), base[b]);
-      }
+#pragma unroll
+      for (int e = 0; e < AHEAD; ++e)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+          if (q0 + e < n) {
+            const float2 y = ml[(q0 + e) * n_rows + r[b]];
+            const float f = ex2(y.x - base[b]);
+            l[b] += f * y.y;
+            v[b].x += f * u[b][e].x;
+            v[b].y += f * u[b][e].y;
+            v[b].z += f * u[b][e].z;
+            v[b].w += f * u[b][e].w;
+          }
     }
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
-      if (b < blocks) dst.put(p, r[b], d[b], v[b], m[b], l[b]);
+    for (int b = 0; b < 2; ++b) {
+      if (b >= blocks) continue;
+      if (to == nullptr) {
+        dst.put(p, r[b], d[b], v[b], m[b], l[b]);
+      } else {  // `to` may be the first part: only this thread reads or writes these four
+        *reinterpret_cast<float4 *>(to + r[b] * DP + d[b]) = v[b];
+        if (d[b] == 0)
+          *reinterpret_cast<float2 *>(to + M * DP + 2 * r[b]) = make_float2(m[b], l[b]);
+      }
+    }
+  }
+}
+
+// A worker's part of a split item is stored (by all of the multiplying threads): count it.
+// The last to arrive joins the item, once its own range is done. With many parts the last
+// of each 16 neighbours joins those (in parallel on as many SMs: a single one would read
+// them for longer than the products took), and the last group the groups.
+__device__ __forceinline__ void part_stored(const AttnPlan &pl, int me, int c0, int c1,
+                                            int n_rows, const ItemOut &dst,
+                                            PendingJoin *pending, int *n_pending) {
+  named_bar_sync(1, AT_CTHREADS);
+  if (threadIdx.x != 0) return;
+  const int parts = c1 - c0 + 1, q = me - c0;
+  const bool grouped = parts > 2 * AT_GROUP;
+  const int lead = q / AT_GROUP * AT_GROUP;
+  int *counter = grouped ? pl.group_counters + part_slot(c0, lead) : pl.counters + c0;
+  const int expected = grouped ? min(AT_GROUP, parts - lead) : parts;
+  if (atom_add_acq_rel_gpu(counter, 1) == expected - 1) {
+    *counter = 0;
+    pending[(*n_pending)++] = {c0, parts, grouped ? lead : -1, n_rows, dst};
+  }
+}
+
+// The joins that fell to this worker, after its last segment, when neither registers nor
+// stages hold anything else. `ml`: 2 AT_GROUP M pairs of shared memory.
+template <int M, int DP>
+__device__ __forceinline__ void run_joins(const AttnParams &p, const AttnPlan &pl, float2 *ml,
+                                          const PendingJoin *pending, const int *n_pending,
+                                          int *is_last) {
+  constexpr int SLOT = M * DP + 2 * M;
+  named_bar_sync(1, AT_CTHREADS);
+  for (int i = 0; i < *n_pending; ++i) {
+    const PendingJoin j = pending[i];
+    const int groups = (j.parts - 1) / AT_GROUP + 1;
+    float *to = nullptr;
+    int first = 0, every = 1, n = j.parts;
+    if (j.group >= 0) {
+      to = pl.partials + static_cast<size_t>(part_slot(j.c0, j.group)) * SLOT;
+      first = j.group;
+      n = min(AT_GROUP, j.parts - j.group);
+    }
+    for (;;) {  // one place of the join in the code: its first use is paid in fetches
+      join_parts<M, DP>(p, pl.partials, ml, j.c0, first, every, n, j.n_rows, to, j.dst);
+      named_bar_sync(1, AT_CTHREADS);
+      if (to == nullptr) break;
+      if (threadIdx.x == 0) {
+        *is_last = atom_add_acq_rel_gpu(pl.counters + j.c0, 1) == groups - 1;
+        if (*is_last) pl.counters[j.c0] = 0;
+      }
+      named_bar_sync(1, AT_CTHREADS);
+      if (!*is_last) break;
+      to = nullptr;
+      first = 0;
+      every = AT_GROUP;
+      n = groups;
+    }
   }
 }
 
@@ -372,7 +462,7 @@ __global__ void __launch_bounds__(AT_THREADS, (AttnCfg<E4M3, DP, NR, WR>::CTAS))
   __shared__ __align__(8) uint64_t full[ST], empty[ST], qempty[C::QB];
   __shared__ float join_ml[AT_CWARPS * MW][2];         // m, l of each warp's rows
   __shared__ uint32_t stage_valid[ST][TOK / 32];       // tokens of the stage that exist
-  __shared__ int start_seq, abort_flag, n_pending;
+  __shared__ int start_seq, abort_flag, n_pending, is_last;
   __shared__ PendingJoin pending[2];  // a range splits at most its first and last item
   uint8_t *q_smem = at_smem + ST * C::STAGE;
 
@@ -414,7 +504,7 @@ __global__ void __launch_bounds__(AT_THREADS, (AttnCfg<E4M3, DP, NR, WR>::CTAS))
     if (w < warp) before += warp_sum[w];
     total += warp_sum[w];
   }
-  const long long most = (total + pl.min_units - 1) / pl.min_units;
+  const long long most = (total + AT_MIN_UNITS - 1) / AT_MIN_UNITS;
   const int workers = static_cast<int>(most < gridDim.x ? most : gridDim.x);
   const int me = blockIdx.x;
   if (me >= workers) return;
@@ -450,14 +540,10 @@ __global__ void __launch_bounds__(AT_THREADS, (AttnCfg<E4M3, DP, NR, WR>::CTAS))
     // ================================================================ copying warps
     constexpr int HALF = TOK / AT_PWARPS;  // tokens of this warp
     constexpr int WORDS = HALF / 32;
-    constexpr int SLABS = RB == 64 ? 1 : RB / 128;
     const int pw = warp - AT_CWARPS;
     const char *kbase = static_cast<const char *>(p.c.k);
     const char *vbase = static_cast<const char *>(p.c.v);
-    // boxes: lane -> (block of `box` tokens, slab, K or V); at most 32
-    const int box = min(p.box, HALF), per_block = 2 * SLABS;
-    const int block = lane / per_block, slab = (lane >> 1) % SLABS;
-    const bool has_box = p.box > 0 && block * box < HALF;
+    const BoxLane<RB, TOK, C::ES> boxes(p.box > 0 ? min(p.box, HALF) : HALF, lane);
     int k = 0, seg = 0;  // stages and segments so far
     while (c.next(p, G)) {
       const int32_t *table = p.block_table + static_cast<long long>(c.s) * p.max_pages;
@@ -467,8 +553,8 @@ __global__ void __launch_bounds__(AT_THREADS, (AttnCfg<E4M3, DP, NR, WR>::CTAS))
       auto look_up = [&](int t, int (&to)[WORDS]) {
 #pragma unroll
         for (int q = 0; q < WORDS; ++q) {
-          const int j = token0(t) + (p.box > 0 ? block * box : q * 32 + lane);
-          to[q] = t < c.t1 && j < c.x.len && (p.box == 0 || (has_box && q == 0))
+          const int j = token0(t) + (p.box > 0 ? boxes.block * boxes.box : q * 32 + lane);
+          to[q] = t < c.t1 && j < c.x.len && (p.box == 0 || (boxes.has && q == 0))
                         ? table[j / p.c.page_size]
                         : -1;
         }
@@ -481,27 +567,9 @@ __global__ void __launch_bounds__(AT_THREADS, (AttnCfg<E4M3, DP, NR, WR>::CTAS))
           mbar_wait_bounded(&empty[st], ((k / ST) - 1) & 1, pl.status, &abort_flag,
                             pl.wait_limit_ns);
         const uint32_t dst = smem_u32(at_smem + st * C::STAGE);
-        uint32_t tx = 0;  // bytes that boxes will bring
         if (p.box > 0) {
-          const bool ok = page[0] >= 0 && page[0] < p.c.num_pages;
-          const uint32_t blocks = __ballot_sync(0xffffffffu, ok);
-          tx = __popc(blocks) * box * (RB == 64 ? 64 : 128);
-#pragma unroll
-          for (int q = 0; q < WORDS; ++q) {
-            const int tok = q * 32 + lane;
-            const uint32_t valid = __ballot_sync(
-                0xffffffffu, (blocks >> (tok / box * per_block) & 1) && j0 + tok < c.x.len);
-            if (lane == 0) stage_valid[st][pw * WORDS + q] = valid;
-          }
-          if (lane == 0) mbar_arrive_expect_tx(&full[st], tx);
-          __syncwarp();
-          if (ok) {
-            const bool val = lane & 1;
-            tma_load_4d(dst + (val ? TOK * RB : 0) + slab * (TOK * 128) +
-                            (pw * HALF + block * box) * (RB == 64 ? 64 : 128),
-                        val ? &vmap : &kmap, &full[st], slab * (128 / C::ES),
-                        (j0 + block * box) % p.c.page_size, c.hk, page[0]);
-          }
+          boxes.issue(&kmap, &vmap, p.c, dst, &full[st], stage_valid[st], pw, lane, j0, c.x.len,
+                      c.hk, page[0]);
         } else {
 #pragma unroll
           for (int q = 0; q < WORDS; ++q) {
@@ -956,29 +1024,17 @@ __global__ void __launch_bounds__(AT_THREADS, (AttnCfg<E4M3, DP, NR, WR>::CTAS))
     fence_proxy_async_smem();  // before later boxes overwrite the join's stores
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[last_st]);
-    // ---- a split item: the last CTA to arrive joins it, once its own range is done
-    if (c0 != c1) {
-      named_bar_sync(1, AT_CTHREADS);
-      if (tid == 0 && atom_add_acq_rel_gpu(pl.counters + c0, 1) == c1 - c0) {
-        pl.counters[c0] = 0;
-        pending[n_pending++] = {c0, c1 - c0 + 1, n_rows, dst};
-      }
-    }
+    if (c0 != c1) part_stored(pl, me, c0, c1, n_rows, dst, pending, &n_pending);
   }
-  named_bar_sync(1, AT_CTHREADS);
-  for (int i = 0; i < n_pending; ++i) {
-    join_parts<M, DP, ST * C::STAGE / 8>(p, pl.partials, reinterpret_cast<float2 *>(at_smem),
-                                         pending[i].c0, pending[i].parts, pending[i].n_rows,
-                                         pending[i].dst);
-    named_bar_sync(1, AT_CTHREADS);
-  }
+  static_assert(ST * C::STAGE >= 2 * AT_GROUP * M * 8, "ml of a join");
+  run_joins<M, DP>(p, pl, reinterpret_cast<float2 *>(at_smem), pending, &n_pending, &is_last);
 }
 
 // CTAs: two per SM by shared memory, one above D = 128.
 inline int attn_grid(int DP, int num_sms) { return DP <= 128 ? 2 * num_sms : num_sms; }
 
 inline size_t counter_bytes(int grid) {
-  return (static_cast<size_t>(grid) * sizeof(int) + 255) / 256 * 256;
+  return (static_cast<size_t>(3) * grid * sizeof(int) + 255) / 256 * 256;
 }
 
 template <bool E4M3, int DP, int NR, int WR>
@@ -990,8 +1046,8 @@ cudaError_t launch_shape(const AttnParams &p, void *ws, const AttnLaunch &a, cud
   if (e != cudaSuccess) return e;
   const int grid = attn_grid(DP, a.num_sms);
   AttnPlan pl;
-  pl.min_units = 1 + AT_ITEM_COST;
   pl.counters = static_cast<int *>(ws);
+  pl.group_counters = pl.counters + grid;
   pl.partials = reinterpret_cast<float *>(static_cast<char *>(ws) + counter_bytes(grid));
   pl.status = a.status;
   pl.wait_limit_ns = a.wait_limit_ns;
