@@ -68,6 +68,12 @@ struct AttnLaunch {
   unsigned *status;
   uint64_t wait_limit_ns;
 };
+// Workers (CTAs) of a launch at most, and the workspace's counters: one per worker for items,
+// two for groups of workers.
+inline int attn_max_workers(int num_sms) { return 2 * num_sms; }
+inline size_t attn_counter_bytes(int num_sms) {
+  return (static_cast<size_t>(3) * attn_max_workers(num_sms) * sizeof(int) + 255) / 256 * 256;
+}
 // One kernel per padded head size (attn_d64.cu, attn_d128.cu, attn_d256.cu); nr groups of 8
 // rows a warp, wr warps sharing the rows.
 cudaError_t launch_attn_d64(const AttnParams &p, bool e4m3, int nr, int wr, void *ws,
@@ -76,6 +82,9 @@ cudaError_t launch_attn_d128(const AttnParams &p, bool e4m3, int nr, int wr, voi
                              const AttnLaunch &a, cudaStream_t s);
 cudaError_t launch_attn_d256(const AttnParams &p, bool e4m3, int nr, int wr, void *ws,
                              const AttnLaunch &a, cudaStream_t s);
+// attn_tc.cu: bf16 caches in boxes, items of 32, 64 or 128 rows.
+cudaError_t launch_attn_tc(const AttnParams &p, int padded, int rows, void *ws,
+                           const AttnLaunch &a, cudaStream_t s);
 // api.cu: a 4-D map (head element, token of the page, kv head, page) of a cache, boxes of
 // 128 bytes (64 where a padded head has 64 bytes) x box tokens, swizzled accordingly.
 bool host_cache_map(CUtensorMap *m, const PagedCache &c, const void *base, bool e4m3, int D,

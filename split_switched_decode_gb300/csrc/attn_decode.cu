@@ -12,14 +12,21 @@ struct AttnShape {
   int rows() const { return 8 * nr * wr; }
 };
 
-// Rows of an item, from what the host knows: the rows of an average sequence. More rows than
-// an item holds read the keys once more per item (mostly from L2).
-AttnShape attn_shape(int S, int T, int Hq, int Hkv) {
-  const long long rows = static_cast<long long>((T + S - 1) / S) * (Hq / Hkv);
+// Rows of an average sequence, which is what the host knows. More rows than an item holds
+// read the keys once more per item (mostly from L2).
+int mean_rows(int S, int T, int Hq, int Hkv) {
+  return static_cast<int>(static_cast<long long>((T + S - 1) / S) * (Hq / Hkv));
+}
+
+AttnShape attn_shape(int rows) {
   return rows <= 8 ? AttnShape{1, 1}
                    : (rows <= 16 ? AttnShape{2, 1}
                                  : (rows <= 32 ? AttnShape{2, 2} : AttnShape{2, 4}));
 }
+
+// Rows of an item on tcgen05 tensor cores, 0 for the legacy products: up to 8 rows those are
+// not what bounds it.
+int tc_rows(int rows) { return rows <= 8 ? 0 : (rows <= 32 ? 32 : (rows <= 64 ? 64 : 128)); }
 
 // Tokens of a TMA box: the largest power of two in the page size, up to what a copying warp
 // brings of a stage; below 8 (a swizzle group) none.
@@ -32,13 +39,11 @@ int box_tokens(int page_size, bool e4m3) {
 
 }  // namespace
 
-// Counters (one per worker for items, two for groups of workers, zero between calls), then two
-// partial slots per worker.
 size_t attn_workspace_bytes(int S, int T, int Hq, int Hkv, int D, int num_sms) {
-  const int dp = padded_dim(D), grid = dp <= 128 ? 2 * num_sms : num_sms;
-  const size_t M = attn_shape(S, T, Hq, Hkv).rows();
-  const size_t counters = (static_cast<size_t>(3) * grid * sizeof(int) + 255) / 256 * 256;
-  return counters + 2 * grid * (M * dp + 2 * M) * sizeof(float);
+  const int dp = padded_dim(D), grid = dp <= 128 ? attn_max_workers(num_sms) : num_sms;
+  const int rows = mean_rows(S, T, Hq, Hkv);
+  const size_t M = tc_rows(rows) > 0 ? tc_rows(rows) : attn_shape(rows).rows();
+  return attn_counter_bytes(num_sms) + 2 * grid * (M * dp + 2 * M) * sizeof(float);
 }
 
 cudaError_t launch_attn_decode(const AttnParams &params, bool e4m3, void *ws, int num_sms,
@@ -57,7 +62,10 @@ cudaError_t launch_attn_decode(const AttnParams &params, bool e4m3, void *ws, in
                     host_cache_map(&a.vmap, p.c, p.c.v, e4m3, p.D, p.Hkv, p.box, dp);
     if (!ok) p.box = 0;
   }
-  const AttnShape sh = attn_shape(p.S, p.T, p.Hq, p.Hkv);
+  const int rows = mean_rows(p.S, p.T, p.Hq, p.Hkv);
+  if (!e4m3 && p.box > 0 && tc_rows(rows) > 0)
+    return launch_attn_tc(p, dp, tc_rows(rows), ws, a, s);
+  const AttnShape sh = attn_shape(rows);
   auto launch = dp == 64 ? launch_attn_d64 : (dp == 128 ? launch_attn_d128 : launch_attn_d256);
   return launch(p, e4m3, sh.nr, sh.wr, ws, a, s);
 }

@@ -248,6 +248,67 @@ struct Cursor {
   }
 };
 
+// This CTA's share of all units, found in one pass over the sequences by the whole CTA;
+// false: the work does not reach this CTA. Holds a barrier before any shared memory written
+// by one thread before the call is read by others after it.
+template <int THREADS>
+struct RangeStart {
+  long long warp_sum[THREADS / 32];
+  long long off;
+  int seq;
+};
+template <int THREADS, int TOK, int M>
+__device__ __forceinline__ bool begin_range(const AttnParams &p, int G,
+                                            RangeStart<THREADS> &start, Shares &sh,
+                                            Cursor<TOK, M> &c) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, me = blockIdx.x;
+  const int per = (p.S + THREADS - 1) / THREADS;
+  const int s_lo = min(tid * per, p.S), s_hi = min(s_lo + per, p.S);
+  long long mine = 0;
+  for (int s = s_lo; s < s_hi; ++s) mine += seq_info<TOK, M>(p, G, s).units(p.Hkv);
+  long long incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += y;
+  }
+  if (lane == 31) start.warp_sum[warp] = incl;
+  __syncthreads();
+  long long total = 0, before = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) before += start.warp_sum[w];
+    total += start.warp_sum[w];
+  }
+  const long long most = (total + AT_MIN_UNITS - 1) / AT_MIN_UNITS;
+  const int workers = static_cast<int>(most < gridDim.x ? most : gridDim.x);
+  if (me >= workers) return false;
+  sh.share_n = total / workers;
+  sh.share_r = total % workers;
+  c.cur = me * sh.share_n + min(static_cast<long long>(me), sh.share_r);
+  c.end = c.cur + sh.share_n + (me < sh.share_r ? 1 : 0);
+  long long at = before + incl - mine;  // units before this thread's sequences
+  if (at <= c.cur && c.cur < at + mine) {
+    for (int s = s_lo; s < s_hi; ++s) {
+      const long long n = seq_info<TOK, M>(p, G, s).units(p.Hkv);
+      if (c.cur < at + n) {
+        start.seq = s;
+        start.off = c.cur - at;
+        break;
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+  c.s = start.seq;
+  c.x = seq_info<TOK, M>(p, G, c.s);
+  const long long per_item = c.x.kt + AT_ITEM_COST, i = start.off / per_item;
+  c.hk = static_cast<int>(i / c.x.rt);
+  c.rt = static_cast<int>(i - static_cast<long long>(c.hk) * c.x.rt);
+  c.item = c.cur - (start.off - i * per_item);
+  return true;
+}
+
 // A copying warp's boxes of one stage: HALF tokens of K and V, lane -> (block of `box`
 // tokens, slab of 128 bytes, K or V), at most 32 boxes.
 template <int RB, int TOK, int ES>
@@ -457,12 +518,11 @@ __global__ void __launch_bounds__(AT_THREADS, (AttnCfg<E4M3, DP, NR, WR>::CTAS))
   constexpr int TOK = C::TOK, STEP = C::STEP, RB = C::RB, M = C::M, MW = C::MW, ST = C::ST;
   constexpr int MT = STEP / 16;  // 16-token tiles of a step
   extern __shared__ __align__(1024) uint8_t at_smem[];
-  __shared__ long long warp_sum[AT_CWARPS + AT_PWARPS];
-  __shared__ long long start_off;
+  __shared__ RangeStart<AT_THREADS> start;
   __shared__ __align__(8) uint64_t full[ST], empty[ST], qempty[C::QB];
   __shared__ float join_ml[AT_CWARPS * MW][2];         // m, l of each warp's rows
   __shared__ uint32_t stage_valid[ST][TOK / 32];       // tokens of the stage that exist
-  __shared__ int start_seq, abort_flag, n_pending, is_last;
+  __shared__ int abort_flag, n_pending, is_last;
   __shared__ PendingJoin pending[2];  // a range splits at most its first and last item
   uint8_t *q_smem = at_smem + ST * C::STAGE;
 
@@ -485,56 +545,9 @@ __global__ void __launch_bounds__(AT_THREADS, (AttnCfg<E4M3, DP, NR, WR>::CTAS))
   griddep_launch_dependents();
   const int G = p.Hq / p.Hkv;
 
-  // ---- this CTA's share of all units: one pass over the sequences
-  const int per = (p.S + AT_THREADS - 1) / AT_THREADS;
-  const int s_lo = min(tid * per, p.S), s_hi = min(s_lo + per, p.S);
-  long long mine = 0;
-  for (int s = s_lo; s < s_hi; ++s) mine += seq_info<TOK, M>(p, G, s).units(p.Hkv);
-  long long incl = mine;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += y;
-  }
-  if (lane == 31) warp_sum[warp] = incl;
-  __syncthreads();
-  long long total = 0, before = 0;
-#pragma unroll
-  for (int w = 0; w < AT_CWARPS + AT_PWARPS; ++w) {
-    if (w < warp) before += warp_sum[w];
-    total += warp_sum[w];
-  }
-  const long long most = (total + AT_MIN_UNITS - 1) / AT_MIN_UNITS;
-  const int workers = static_cast<int>(most < gridDim.x ? most : gridDim.x);
-  const int me = blockIdx.x;
-  if (me >= workers) return;
-  const Shares sh = {total / workers, total % workers};
+  Shares sh;
   Cursor<TOK, M> c;
-  c.cur = me * sh.share_n + min(static_cast<long long>(me), sh.share_r);
-  c.end = c.cur + sh.share_n + (me < sh.share_r ? 1 : 0);
-  {
-    long long at = before + incl - mine;  // units before this thread's sequences
-    if (at <= c.cur && c.cur < at + mine) {
-      for (int s = s_lo; s < s_hi; ++s) {
-        const long long n = seq_info<TOK, M>(p, G, s).units(p.Hkv);
-        if (c.cur < at + n) {
-          start_seq = s;
-          start_off = c.cur - at;
-          break;
-        }
-        at += n;
-      }
-    }
-  }
-  __syncthreads();
-  c.s = start_seq;
-  c.x = seq_info<TOK, M>(p, G, c.s);
-  {
-    const long long per_item = c.x.kt + AT_ITEM_COST, i = start_off / per_item;
-    c.hk = static_cast<int>(i / c.x.rt);
-    c.rt = static_cast<int>(i - static_cast<long long>(c.hk) * c.x.rt);
-    c.item = c.cur - (start_off - i * per_item);
-  }
+  if (!begin_range<AT_THREADS>(p, G, start, sh, c)) return;
 
   if (warp >= AT_CWARPS) {
     // ================================================================ copying warps
@@ -989,11 +1002,11 @@ __global__ void __launch_bounds__(AT_THREADS, (AttnCfg<E4M3, DP, NR, WR>::CTAS))
     named_bar_sync(1, AT_CTHREADS);
 
     const long long first = c.item + AT_ITEM_COST;  // the unit of the item's first stage
-    const int c0 = sh.worker_of(first), c1 = sh.worker_of(first + x.kt - 1);
+    const int me = blockIdx.x, c0 = sh.worker_of(first), c1 = sh.worker_of(first + x.kt - 1);
     const ItemOut dst = {x.q0, c.rt * M, c.hk * G, G,
                          p.c.v_scale ? p.c.v_scale[c.hk] : 1.0f};
     const int cols = p.D / 4;
-    float *slot = pl.partials + static_cast<size_t>(2 * me + (me == c0 ? 1 : 0)) * C::SLOT;
+    float *slot = pl.partials + static_cast<size_t>(part_slot(c0, me - c0)) * C::SLOT;
     for (int i = tid; i < n_rows * cols; i += AT_CTHREADS) {
       const int r = i / cols, d = 4 * (i - r * cols);
       float mr = -INFINITY;
@@ -1033,8 +1046,19 @@ __global__ void __launch_bounds__(AT_THREADS, (AttnCfg<E4M3, DP, NR, WR>::CTAS))
 // CTAs: two per SM by shared memory, one above D = 128.
 inline int attn_grid(int DP, int num_sms) { return DP <= 128 ? 2 * num_sms : num_sms; }
 
-inline size_t counter_bytes(int grid) {
-  return (static_cast<size_t>(3) * grid * sizeof(int) + 255) / 256 * 256;
+
+// The workspace: counters of items and of groups of workers (zero between calls; the same
+// place for every kernel, as calls of any of them may follow each other on one workspace),
+// then two partial slots per worker.
+inline AttnPlan make_plan(void *ws, const AttnLaunch &a) {
+  AttnPlan pl;
+  pl.counters = static_cast<int *>(ws);
+  pl.group_counters = pl.counters + attn_max_workers(a.num_sms);
+  pl.partials = reinterpret_cast<float *>(static_cast<char *>(ws) +
+                                          attn_counter_bytes(a.num_sms));
+  pl.status = a.status;
+  pl.wait_limit_ns = a.wait_limit_ns;
+  return pl;
 }
 
 template <bool E4M3, int DP, int NR, int WR>
@@ -1045,13 +1069,8 @@ cudaError_t launch_shape(const AttnParams &p, void *ws, const AttnLaunch &a, cud
                                              static_cast<int>(C::SMEM));
   if (e != cudaSuccess) return e;
   const int grid = attn_grid(DP, a.num_sms);
-  AttnPlan pl;
-  pl.counters = static_cast<int *>(ws);
-  pl.group_counters = pl.counters + grid;
-  pl.partials = reinterpret_cast<float *>(static_cast<char *>(ws) + counter_bytes(grid));
-  pl.status = a.status;
-  pl.wait_limit_ns = a.wait_limit_ns;
-  return launch_pdl(kernel, dim3(grid), dim3(AT_THREADS), C::SMEM, s, a.kmap, a.vmap, p, pl);
+  return launch_pdl(kernel, dim3(grid), dim3(AT_THREADS), C::SMEM, s, a.kmap, a.vmap, p,
+                    make_plan(ws, a));
 }
 
 // nr, wr: attn_shape's

@@ -1,0 +1,596 @@
+// attn_tc.cu -- attention over a paged bf16 cache for many rows a kv head (verification rows,
+// wide groups) on tcgen05 tensor cores.
+//
+// The legacy matrix instructions of attn_kernel.cuh run at a sixteenth of the tcgen05 rate:
+// from 9 rows a kv head their products take longer than the keys' and values' way from HBM
+// (64 rows: 435 us where the copy takes 160). Here a stage of 64 tokens costs 512 clocks of
+// the tensor core for up to 128 rows, and copying bounds it again. Division of the work, ring
+// of stages and joins are attn_kernel.cuh's; one CTA an SM has nine warps:
+//
+//   0-3  softmax: a thread a TMEM lane; MQ = 32, 64 or 128 rows an item
+//   4-5  TMA boxes of K and V into the ring
+//   6    one thread issues the products
+//   7-8  rows of q into shared memory
+//
+//     S[rows, 64 tokens] = Q . K^T    A = Q, B = K, both K-major in shared memory (the boxes'
+//                                     128-byte swizzle is the operand layout)
+//     O[rows, D]        += P . V      A = P from tensor memory, B = V as stored: rows of a
+//                                     token, elements contiguous (MN-major)
+//
+// S is double buffered and P (bf16) overwrites its S, so the softmax of stage k runs beside
+// the scores of k + 1 and the outputs of k - 1. M is 128 whatever the rows are: Q stands in
+// shared memory 128 / MQ times, and copy g of a row takes the softmax of the g-th part of
+// the stage's tokens with weights of zero for the others, a maximum, a sum and outputs of
+// its own, which are joined at the segment's end. So four warps share the exponentials at
+// any number of rows (with one copy and 32 rows a single warp took 2.4 us a stage, twice
+// what its bytes take).
+//
+// The running maximum that weights refer to is moved only when a row's maximum has grown by
+// more than 8 (weights then stay below 2^8, and their rounding to bf16 is relative), so the
+// outputs in tensor memory are rarely rescaled; sums refer to the same maximum.
+#include "attn_kernel.cuh"
+#include "tcgen05.cuh"
+
+namespace ssd {
+namespace {
+
+constexpr int TC_THREADS = 288;
+constexpr int TC_QTHREADS = 64;
+constexpr float TC_LAZY = 8.0f;
+
+template <int DP, int MQ>
+struct TcCfg {
+  static constexpr int TOK = 64, RB = DP * 2, STAGE = 2 * TOK * RB;
+  static constexpr int COPIES = 128 / MQ, TS = TOK / COPIES;  // tokens of a copy
+  static constexpr int QBYTES = 128 * DP * 2;
+  // One CTA an SM: with two, each ring would hold two stages beside Q's copies, and a stage
+  // came every 2.2 us where the copy rate gives two in 1.45.
+  static constexpr int ST = DP == 64 ? 8 : (DP == 128 ? 6 : 2);
+  static constexpr int QB = DP == 64 ? 2 : 1;
+  static constexpr size_t SMEM = QB * QBYTES + ST * STAGE;
+  static constexpr int COLS = DP <= 128 ? 256 : 512;  // O, then two S of 64 columns
+  static constexpr int SLOT = MQ * DP + 2 * MQ;
+};
+
+// True in one thread of the (converged) warp. Under this predicate the compiler knows that a
+// single thread issues the tensor-core instructions, whose operands are uniform registers;
+// under `lane == 0` it serialised them over the warp (125 clocks a product).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(yes));
+  return yes != 0;
+}
+// D[tmem] (+)= A[tmem] * B[smem], bf16, fp32 accumulate; one thread issues.
+__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *v) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+        "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr)
+               : "memory");
+  return r;
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// Descriptor of an operand whose M or N dimension is contiguous, in slabs of 64 elements (128
+// bytes, swizzled) x K rows: 8 rows of K are 1024 bytes (stride offset), the next 64 elements
+// `slab_bytes` on (leading offset).
+__device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t saddr, uint32_t slab_bytes) {
+  uint64_t d = static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>(slab_bytes >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
+template <int DP, int MQ>
+__global__ void __launch_bounds__(TC_THREADS, 1)
+    attn_tc_kernel(const __grid_constant__ CUtensorMap kmap,
+                   const __grid_constant__ CUtensorMap vmap,
+                   const __grid_constant__ AttnParams p, const AttnPlan pl) {
+  using C = TcCfg<DP, MQ>;
+  constexpr int TOK = C::TOK, RB = C::RB, ST = C::ST, TS = C::TS;
+  extern __shared__ __align__(1024) uint8_t at_smem[];  // q, then the ring
+  __shared__ RangeStart<TC_THREADS> start;
+  __shared__ __align__(8) uint64_t full[ST], empty[ST], qfull[C::QB], qempty[C::QB];
+  __shared__ __align__(8) uint64_t s_full[2], p_full[2], pv_done[2], clean;
+  __shared__ uint32_t stage_valid[ST][TOK / 32];
+  __shared__ PendingJoin pending[2];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag, n_pending, is_last, keep_first[2];
+  __shared__ float join_ml[128][2];
+  uint8_t *ring = at_smem + C::QB * C::QBYTES;
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    abort_flag = 0;
+    n_pending = 0;
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&full[i], AT_PWARPS);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < C::QB; ++i) {
+      mbar_init(&qfull[i], TC_QTHREADS);
+      mbar_init(&qempty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 128);
+      mbar_init(&pv_done[i], 1);
+      keep_first[i] = 0;
+    }
+    mbar_init(&clean, 128);
+    fence_mbar_init();
+    prefetch_tensormap(&kmap);
+    prefetch_tensormap(&vmap);
+  }
+  griddep_wait();
+  const int G = p.Hq / p.Hkv;
+  Shares sh;
+  Cursor<TOK, MQ> c;
+  if (!begin_range<TC_THREADS>(p, G, start, sh, c)) return;
+  if (warp == 6) {
+    tmem_alloc(&tmem_slot, C::COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  // after the allocation: a dependent grid's CTA cannot hold the columns this one waits for
+  griddep_launch_dependents();
+  const uint32_t tmem = tmem_slot, o_tmem = tmem, s_tmem = tmem + DP;
+  auto wait = [&](uint64_t *bar, int phase) {
+    mbar_wait_bounded(bar, phase & 1, pl.status, &abort_flag, pl.wait_limit_ns);
+  };
+  // Outputs of stage i added. Two barriers in turn: who waits for stage i knows that i - 2 is
+  // done (the scores of i were issued after it), not that i - 1 is, and a wait tells only
+  // neighbouring phases apart.
+  auto wait_pv = [&](int i) { wait(&pv_done[i & 1], i >> 1); };
+
+  if (warp == 4 || warp == 5) {
+    // ================================================================ K and V boxes
+    const int pw = warp - 4;
+    const BoxLane<RB, TOK, 2> boxes(min(p.box, TOK / AT_PWARPS), lane);
+    int k = 0;
+    while (c.next(p, G)) {
+      const int32_t *table = p.block_table + static_cast<long long>(c.s) * p.max_pages;
+      auto token0 = [&](int t) { return c.x.begin + t * TOK + pw * (TOK / AT_PWARPS); };
+      auto look_up = [&](int t) {
+        const int j = token0(t) + boxes.block * boxes.box;
+        return t < c.t1 && j < c.x.len && boxes.has ? table[j / p.c.page_size] : -1;
+      };
+      int page = look_up(c.t0), ahead = look_up(c.t0 + 1);
+      for (int t = c.t0; t < c.t1; ++t, ++k) {
+        const int st = k % ST;
+        if (k >= ST) wait(&empty[st], k / ST - 1);
+        boxes.issue(&kmap, &vmap, p.c, smem_u32(ring + st * C::STAGE), &full[st],
+                    stage_valid[st], pw, lane, token0(t), c.x.len, c.hk, page);
+        page = ahead;
+        ahead = look_up(t + 2);
+      }
+    }
+    if (*static_cast<volatile int *>(&abort_flag) && lane == 0) {
+      // after a time-out: boxes still on their way land before the CTA ends
+      for (int i = max(k - ST, 0); i < k; ++i)
+        mbar_wait_drain(&full[i % ST], (i / ST) & 1, 10000000ull);
+    }
+  } else if (warp >= 7) {
+    // ================================================================ rows of q
+    // A thread has one 16-byte column of the head and every PER_PASS-th row.
+    constexpr int CH = DP / 8, PER_PASS = TC_QTHREADS / CH;
+    const int at = tid - 7 * 32, ch = at % CH;
+    int seg = 0;
+    while (c.next(p, G)) {
+      const int qb = seg % C::QB;
+      if (seg >= C::QB) wait(&qempty[qb], seg / C::QB - 1);
+      const int n_rows = min(MQ, c.x.n * G - c.rt * MQ);
+      uint8_t *qd = at_smem + qb * C::QBYTES;
+      const uint16_t *head = p.q + static_cast<long long>(c.hk * G) * p.D + ch * 8;
+      constexpr int AHEAD = 8;
+      for (int r0 = at / CH; r0 < MQ; r0 += AHEAD * PER_PASS) {
+        uint4 v[AHEAD];
+#pragma unroll
+        for (int e = 0; e < AHEAD; ++e) {
+          const int r = r0 + e * PER_PASS;
+          v[e] = make_uint4(0, 0, 0, 0);  // past the rows and past D
+          if (r < n_rows && ch * 8 < p.D) {
+            const int rr = c.rt * MQ + r, tok = rr / G, g = rr - tok * G;
+            v[e] = *reinterpret_cast<const uint4 *>(head + (c.x.q0 + tok) * p.q_stride + g * p.D);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < AHEAD; ++e) {
+          const int r = r0 + e * PER_PASS;
+          if (r < MQ) {
+#pragma unroll
+            for (int copy = 0; copy < C::COPIES; ++copy)
+              *reinterpret_cast<uint4 *>(qd + swz<DP * 2, 128>(copy * MQ + r, ch)) = v[e];
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&qfull[qb]);
+      ++seg;
+    }
+  } else if (warp == 6) {
+    // ================================================================ products
+    const uint32_t id_s = (idesc_bf16(TOK)), id_o = idesc_bf16(p.D) | (1u << 16);
+    const uint32_t q_u = smem_u32(at_smem), ring_u = smem_u32(ring);
+    int k = 0, seg = 0;
+    bool first = false;  // stage k - 1 was its segment's first
+    auto outputs = [&](int i, bool start_new, bool last) {  // O += P . V of stage i
+      const int st = i % ST, sb = i & 1;
+      wait(&p_full[sb], i >> 1);
+      tc_fence_after();
+      const uint32_t acc = start_new && !*static_cast<volatile int *>(&keep_first[sb]) ? 0u : 1u;
+      const uint64_t v = sw128_mn_desc(ring_u + st * C::STAGE + TOK * RB, TOK * 128);
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < TOK / 16; ++kk)  // 16 tokens: 2048 bytes of V, 8 columns of P
+          tc_mma_ts(o_tmem, s_tmem + sb * 64 + kk * 8, v + (2048 >> 4) * kk, id_o,
+                    kk > 0 ? 1u : acc);
+        if (!last) tc_commit(&empty[st]);  // a segment's last stage is released after its join
+        tc_commit(&pv_done[sb]);
+      }
+      __syncwarp();
+    };
+    while (c.next(p, G)) {
+      const int qb = seg % C::QB;
+      for (int t = c.t0; t < c.t1; ++t, ++k) {
+        const int st = k % ST;
+        // scores before the last stage's outputs, so that the softmax goes on beside those;
+        // outputs first where the keys are not here yet or the item ends
+        const bool here = mbar_try_wait(&full[st], k / ST & 1);
+        const bool early = k > 0 && (t == c.t0 || !__all_sync(0xffffffffu, here));
+        if (early) outputs(k - 1, first, t == c.t0);
+        if (t == c.t0) wait(&qfull[qb], seg / C::QB);
+        wait(&full[st], k / ST);
+        if (k >= 2) wait_pv(k - 2);  // S of stage k - 2 held that product's weights
+        tc_fence_after();
+        if (elect_one()) {
+          // 16 elements a product: 32 bytes of a 128-byte slab
+#pragma unroll 1
+          for (int d = 0; d < p.D; d += 64) {
+            const uint32_t slab = d >> 6;
+            const uint64_t a = sw128_desc(q_u + qb * C::QBYTES + slab * (128 * 128));
+            const uint64_t b = sw128_desc(ring_u + st * C::STAGE + slab * (TOK * 128));
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              if (d + kk * 16 < p.D)
+                tc_mma(s_tmem + (k & 1) * 64, a + 2 * kk, b + 2 * kk, id_s,
+                       d + kk > 0 ? 1u : 0u);
+          }
+          tc_commit(&s_full[k & 1]);
+          if (t + 1 == c.t1) tc_commit(&qempty[qb]);
+        }
+        __syncwarp();
+        if (k > 0 && !early) outputs(k - 1, first, false);
+        first = t == c.t0;
+      }
+      ++seg;
+    }
+    if (k > 0) {
+      outputs(k - 1, first, true);
+      wait_pv(k - 1);  // nothing in flight when the columns are released
+    }
+  } else {
+    // ================================================================ softmax, a thread a lane
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    const int copy = tid / MQ, r = tid % MQ, first_tok = copy * TS;
+    int k = 0, cleans = 0;
+    while (c.next(p, G)) {
+      const SeqInfo &x = c.x;
+      const int n_rows = min(MQ, x.n * G - c.rt * MQ), row0 = c.rt * MQ;
+      // what this row sees, and what every row of the item sees
+      const int pos0 = x.len - x.n;
+      const int hi = pos0 + (row0 + min(r, n_rows - 1)) / G;
+      const int lo = p.window > 0 && hi >= p.window ? hi - p.window + 1 : 0;
+      const int hi_all = pos0 + row0 / G, hi_top = pos0 + (row0 + n_rows - 1) / G;
+      const int lo_all = p.window > 0 && hi_top >= p.window ? hi_top - p.window + 1 : 0;
+      const float zf = p.scale * LOG2E * (p.c.k_scale ? p.c.k_scale[c.hk] : 1.0f);
+      float m = -INFINITY, l = 0.0f;  // m: the maximum that weights refer to
+      for (int t = c.t0; t < c.t1; ++t, ++k) {
+        const int st = k % ST, sb = k & 1;
+        const uint32_t s_at = s_tmem + sb * 64 + lanes;
+        wait(&full[st], k / ST);  // (long since) the copying warps' bits and the values
+        wait(&s_full[sb], k >> 1);
+        tc_fence_after();
+        float z[TS];
+        if (TS == 16) tmem_ld16(s_at + first_tok, z);
+        else
+#pragma unroll
+          for (int i = 0; i < TS; i += 32) tmem_ld32(s_at + first_tok + i, z + i);
+        tmem_wait_ld();
+        const uint32_t valid[2] = {stage_valid[st][0], stage_valid[st][1]};
+        const int j0 = x.begin + t * TOK;
+        const bool whole = (valid[0] & valid[1]) == 0xffffffffu;
+        const bool plain = whole && j0 >= lo_all && j0 + TOK - 1 <= hi_all;
+#pragma unroll
+        for (int i = 0; i < TS; ++i) z[i] *= zf;
+        if (!plain) {
+#pragma unroll
+          for (int i = 0; i < TS; ++i) {
+            const int b = first_tok + i;
+            if (j0 + b < lo || j0 + b > hi || !(valid[b >> 5] >> (b & 31) & 1)) z[i] = -INFINITY;
+          }
+        }
+        float part[4] = {z[0], z[1], z[2], z[3]};  // short chains
+#pragma unroll
+        for (int i = 4; i < TS; ++i) part[i & 3] = fmaxf(part[i & 3], z[i]);
+        const float mx = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+        const bool begins = t == c.t0;
+        if (begins) {
+          m = mx;
+        } else if (__any_sync(0xffffffffu, mx > m + TC_LAZY)) {
+          // move every row's maximum: the outputs so far are rescaled in tensor memory,
+          // after the last product that adds to them
+          const float m_new = fmaxf(m, mx);
+          const float fade = ex2(m - (m_new == -INFINITY ? 0.0f : m_new));
+          m = m_new;
+          l *= fade;
+          wait_pv(k - 1);
+          tc_fence_after();
+          for (int d = 0; d < p.D; d += 16) {
+            float o[16];
+            uint32_t u[16];
+            tmem_ld16(o_tmem + lanes + d, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(o[e] * fade);
+            tmem_st16(o_tmem + lanes + d, u);
+          }
+          tmem_wait_st();
+        }
+        const float base = m == -INFINITY ? 0.0f : m;
+        uint32_t w[TS / 2];
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < TS / 2; ++i) {
+          const float a = ex2(z[2 * i] - base), b = ex2(z[2 * i + 1] - base);
+          sum[2 * (i & 1)] += a;
+          sum[2 * (i & 1) + 1] += b;
+          w[i] = pack2<false>(a, b);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        // the weights of this copy's tokens, zeros for the others'
+#pragma unroll
+        for (int b = 0; b < 32; b += 16) {
+          uint32_t u[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            u[e] = 0u;
+#pragma unroll
+            for (int g = 0; g < C::COPIES; ++g) {
+              const int i = b + e - g * (TS / 2);
+              if (i >= 0 && i < TS / 2 && (C::COPIES == 1 || copy == g)) u[e] = w[i];
+            }
+          }
+          tmem_st16(s_at + b, u);
+        }
+        tmem_wait_st();
+        int keep = 0;
+        if (!plain) {
+          // Weights of zero must not meet what is not finite. Tokens that do not exist (boxes
+          // bring what lies past the end) get values of zero ...
+          uint8_t *v = ring + st * C::STAGE + TOK * RB;
+          if (!whole) {
+            for (int i = lane; i < TOK * (RB / 16); i += 32) {
+              const int row = i / (RB / 16);
+              if (!(valid[row >> 5] >> (row & 31) & 1))
+                *reinterpret_cast<uint4 *>(v + swz<RB, TOK>(row, i % (RB / 16))) =
+                    make_uint4(0, 0, 0, 0);
+            }
+            __syncwarp();
+          }
+          // ... and values of tokens that some rows see and others do not are taken through
+          // the product without what is not finite in them, which is added where it is seen
+          // (a sequence's only row sees every token from its window's first on).
+          if (x.n > 1 || p.window > 0) {
+            bool bad = false;
+            for (int i = lane; i < TOK * (RB / 16); i += 32) {
+              const uint4 y = *reinterpret_cast<const uint4 *>(
+                  v + swz<RB, TOK>(i / (RB / 16), i % (RB / 16)));
+              bad |= (__vcmpeq2(y.x & 0x7f807f80u, 0x7f807f80u) |
+                      __vcmpeq2(y.y & 0x7f807f80u, 0x7f807f80u) |
+                      __vcmpeq2(y.z & 0x7f807f80u, 0x7f807f80u) |
+                      __vcmpeq2(y.w & 0x7f807f80u, 0x7f807f80u)) != 0;
+            }
+            if (__any_sync(0xffffffffu, bad)) {
+              if (!begins) wait_pv(k - 1);
+              tc_fence_after();
+              for (int d = 0; d < p.D; d += 16) {
+                float o[16];
+                uint32_t u[16];
+                tmem_ld16(o_tmem + lanes + d, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = begins ? 0.0f : o[e];
+                for (int i = 0; i < TOK; ++i) {
+                  const uint32_t pw2 = tmem_ld1(s_at + i / 2);
+                  tmem_wait_ld();
+                  const float pr = i & 1 ? bf16hi(pw2) : bf16lo(pw2);
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) {
+                    const uint16_t y = *reinterpret_cast<const uint16_t *>(
+                        v + swz<RB, TOK>(i, (d + e) >> 3) + ((d + e) & 7) * 2);
+                    if ((y & 0x7f80) == 0x7f80 && pr != 0.0f) o[e] += pr * bf16_to_f32(y);
+                  }
+                }
+#pragma unroll
+                for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(o[e]);
+                tmem_st16(o_tmem + lanes + d, u);
+              }
+              tmem_wait_st();
+              // every row has read the values (not a CTA barrier: this depends on data, and
+              // after a time-out the warps may see different bytes)
+              mbar_arrive(&clean);
+              wait(&clean, cleans++);
+              for (int i = tid; i < TOK * (RB / 16); i += 128) {
+                uint4 *at = reinterpret_cast<uint4 *>(
+                    v + swz<RB, TOK>(i / (RB / 16), i % (RB / 16)));
+                uint4 y = *at;
+                y.x &= ~__vcmpeq2(y.x & 0x7f807f80u, 0x7f807f80u);
+                y.y &= ~__vcmpeq2(y.y & 0x7f807f80u, 0x7f807f80u);
+                y.z &= ~__vcmpeq2(y.z & 0x7f807f80u, 0x7f807f80u);
+                y.w &= ~__vcmpeq2(y.w & 0x7f807f80u, 0x7f807f80u);
+                *at = y;
+              }
+              keep = 1;  // the segment's first outputs add to these
+            }
+          }
+          fence_proxy_async_smem();  // before the product (and later boxes) touch the values
+        }
+        if (tid == 0) keep_first[sb] = keep;
+        tc_fence_before();
+        mbar_arrive(&p_full[sb]);
+      }
+
+      // ---- the segment's outputs: the copies joined in the last stage's memory, half of the
+      // columns at a time (a row of DP / 2 floats a lane, 16-byte chunks permuted by the row)
+      const int last_st = (k - 1) % ST, me = blockIdx.x;
+      const long long unit = c.item + AT_ITEM_COST;
+      const int c0 = sh.worker_of(unit), c1 = sh.worker_of(unit + x.kt - 1);
+      const ItemOut dst = {x.q0, row0, c.hk * G, G, p.c.v_scale ? p.c.v_scale[c.hk] : 1.0f};
+      float *slot = pl.partials + static_cast<size_t>(part_slot(c0, me - c0)) * C::SLOT;
+      float *join = reinterpret_cast<float *>(ring + last_st * C::STAGE);
+      constexpr int HALF = DP / 2;
+      auto join_at = [&](int row, int chunk) {
+        return reinterpret_cast<float4 *>(join + row * HALF + ((chunk ^ (row & 7)) << 2));
+      };
+      join_ml[tid][0] = m;
+      join_ml[tid][1] = l;
+      wait_pv(k - 1);
+      tc_fence_after();
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        const int d0 = half * HALF, width = min(HALF, p.D - d0);  // a multiple of 16, or none
+        if (width <= 0) break;
+        for (int d = 0; d < width; d += 16) {
+          float o[16];
+          tmem_ld16(o_tmem + lanes + d0 + d, o);
+          tmem_wait_ld();
+          if (r < n_rows) {
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+              *join_at(tid, (d + e) >> 2) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          }
+        }
+        tc_fence_before();  // the next segment's products overwrite the columns
+        named_bar_sync(1, 128);
+        const int cols = width / 4;
+        for (int i = tid; i < n_rows * cols; i += 128) {
+          const int row = i / cols, d = i - row * cols;
+          float mr = -INFINITY, lr = 0.0f;
+#pragma unroll
+          for (int g = 0; g < C::COPIES; ++g) mr = fmaxf(mr, join_ml[g * MQ + row][0]);
+          const float b = mr == -INFINITY ? 0.0f : mr;
+          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+          for (int g = 0; g < C::COPIES; ++g) {
+            const float f = ex2(join_ml[g * MQ + row][0] - b);
+            const float4 y = *join_at(g * MQ + row, d);
+            lr += f * join_ml[g * MQ + row][1];
+            v.x += f * y.x;
+            v.y += f * y.y;
+            v.z += f * y.z;
+            v.w += f * y.w;
+          }
+          const int col = d0 + 4 * d;
+          if (c0 == c1) {
+            dst.put(p, row, col, v, mr, lr);
+          } else {
+            *reinterpret_cast<float4 *>(slot + row * DP + col) = v;
+            if (col == 0)
+              *reinterpret_cast<float2 *>(slot + MQ * DP + 2 * row) = make_float2(mr, lr);
+          }
+        }
+        fence_proxy_async_smem();  // before later boxes overwrite the join's stores
+        named_bar_sync(1, 128);
+      }
+      if (tid == 0) mbar_arrive(&empty[last_st]);
+      if (c0 != c1) part_stored(pl, me, c0, c1, n_rows, dst, pending, &n_pending);
+    }
+    static_assert(ST * C::STAGE >= 2 * AT_GROUP * MQ * 8, "ml of a join");
+    run_joins<MQ, DP>(p, pl, reinterpret_cast<float2 *>(ring), pending, &n_pending, &is_last);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 6) tmem_dealloc(tmem, C::COLS);
+}
+
+template <int DP, int MQ>
+cudaError_t launch_tc_shape(const AttnParams &p, void *ws, const AttnLaunch &a, cudaStream_t s) {
+  using C = TcCfg<DP, MQ>;
+  auto kernel = attn_tc_kernel<DP, MQ>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(C::SMEM));
+  if (e != cudaSuccess) return e;
+  const int grid = a.num_sms;
+  return launch_pdl(kernel, dim3(grid), dim3(TC_THREADS), C::SMEM, s, a.kmap, a.vmap, p,
+                    make_plan(ws, a));
+}
+
+template <int DP>
+cudaError_t launch_tc_dim(const AttnParams &p, int rows, void *ws, const AttnLaunch &a,
+                          cudaStream_t s) {
+  switch (rows) {
+    case 32:
+      return launch_tc_shape<DP, 32>(p, ws, a, s);
+    case 64:
+      return launch_tc_shape<DP, 64>(p, ws, a, s);
+    default:
+      return launch_tc_shape<DP, 128>(p, ws, a, s);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_attn_tc(const AttnParams &p, int padded, int rows, void *ws,
+                           const AttnLaunch &a, cudaStream_t s) {
+  switch (padded) {
+    case 64:
+      return launch_tc_dim<64>(p, rows, ws, a, s);
+    case 128:
+      return launch_tc_dim<128>(p, rows, ws, a, s);
+    default:
+      return launch_tc_dim<256>(p, rows, ws, a, s);
+  }
+}
+
+}  // namespace ssd
