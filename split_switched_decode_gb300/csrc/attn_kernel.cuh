@@ -353,19 +353,29 @@ struct BoxLane {
 struct ItemOut {
   int q0, row0, head0, G;  // first row of the sequence; of the item; its first head
   float v_scale;
-  __device__ __forceinline__ void put(const AttnParams &p, int r, int d, float4 v, float m,
-                                      float l) const {
+  // Four finished outputs.
+  __device__ __forceinline__ void put_out(const AttnParams &p, int r, int d, float4 v) const {
     const int rr = row0 + r, i = rr / G, g = rr - i * G;
-    const float inv = v_scale / l;
-    if (l == 0.0f) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // nothing seen
-    else v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
     uint2 u;
     u.x = pack2<false>(v.x, v.y);
     u.y = pack2<false>(v.z, v.w);
     const long long row = q0 + i, head = head0 + g;
     *reinterpret_cast<uint2 *>(p.out + row * p.out_stride + head * p.D + d) = u;
-    if (p.lse && d == 0)
-      p.lse[row * p.Hq + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * LN2;
+  }
+  __device__ __forceinline__ void put_lse(const AttnParams &p, int r, float m, float l) const {
+    const int rr = row0 + r, i = rr / G, g = rr - i * G;
+    if (p.lse)
+      p.lse[static_cast<long long>(q0 + i) * p.Hq + head0 + g] =
+          l == 0.0f ? -INFINITY : (m + log2f(l)) * LN2;
+  }
+  // Four outputs to be divided by the row's sum (zero: nothing seen), with the first the lse.
+  __device__ __forceinline__ void put(const AttnParams &p, int r, int d, float4 v, float m,
+                                      float l) const {
+    const float inv = v_scale / l;
+    if (l == 0.0f) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    else v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+    put_out(p, r, d, v);
+    if (d == 0) put_lse(p, r, m, l);
   }
 };
 

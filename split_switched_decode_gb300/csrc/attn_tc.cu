@@ -5,11 +5,11 @@
 // from 9 rows a kv head their products take longer than the keys' and values' way from HBM
 // (64 rows: 435 us where the copy takes 160). Here a stage of 64 tokens costs 512 clocks of
 // the tensor core for up to 128 rows, and copying bounds it again. Division of the work, ring
-// of stages and joins are attn_kernel.cuh's; one CTA an SM has nine warps:
+// of stages and joins are attn_kernel.cuh's; one CTA an SM has ten warps:
 //
 //   0-3  softmax: a thread a TMEM lane; MQ = 32, 64 or 128 rows an item
 //   4-5  TMA boxes of K and V into the ring
-//   6    one thread issues the products
+//   6, 9 a thread each issues the products below (one thread for both took 1 us a stage)
 //   7-8  rows of q into shared memory
 //
 //     S[rows, 64 tokens] = Q . K^T    A = Q, B = K, both K-major in shared memory (the boxes'
@@ -34,7 +34,7 @@
 namespace ssd {
 namespace {
 
-constexpr int TC_THREADS = 288;
+constexpr int TC_THREADS = 320;
 constexpr int TC_QTHREADS = 64;
 constexpr float TC_LAZY = 8.0f;
 
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       for (int i = max(k - ST, 0); i < k; ++i)
         mbar_wait_drain(&full[i % ST], (i / ST) & 1, 10000000ull);
     }
-  } else if (warp >= 7) {
+  } else if (warp == 7 || warp == 8) {
     // ================================================================ rows of q
     // A thread has one 16-byte column of the head and every PER_PASS-th row.
     constexpr int CH = DP / 8, PER_PASS = TC_QTHREADS / CH;
@@ -249,36 +249,14 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     }
   } else if (warp == 6) {
     // ================================================================ products
-    const uint32_t id_s = (idesc_bf16(TOK)), id_o = idesc_bf16(p.D) | (1u << 16);
-    const uint32_t q_u = smem_u32(at_smem), ring_u = smem_u32(ring);
+    // S = Q . K^T
+    const uint32_t id_s = idesc_bf16(TOK), q_u = smem_u32(at_smem), ring_u = smem_u32(ring);
     int k = 0, seg = 0;
-    bool first = false;  // stage k - 1 was its segment's first
-    auto outputs = [&](int i, bool start_new, bool last) {  // O += P . V of stage i
-      const int st = i % ST, sb = i & 1;
-      wait(&p_full[sb], i >> 1);
-      tc_fence_after();
-      const uint32_t acc = start_new && !*static_cast<volatile int *>(&keep_first[sb]) ? 0u : 1u;
-      const uint64_t v = sw128_mn_desc(ring_u + st * C::STAGE + TOK * RB, TOK * 128);
-      if (elect_one()) {
-#pragma unroll
-        for (int kk = 0; kk < TOK / 16; ++kk)  // 16 tokens: 2048 bytes of V, 8 columns of P
-          tc_mma_ts(o_tmem, s_tmem + sb * 64 + kk * 8, v + (2048 >> 4) * kk, id_o,
-                    kk > 0 ? 1u : acc);
-        if (!last) tc_commit(&empty[st]);  // a segment's last stage is released after its join
-        tc_commit(&pv_done[sb]);
-      }
-      __syncwarp();
-    };
     while (c.next(p, G)) {
       const int qb = seg % C::QB;
+      wait(&qfull[qb], seg / C::QB);
       for (int t = c.t0; t < c.t1; ++t, ++k) {
         const int st = k % ST;
-        // scores before the last stage's outputs, so that the softmax goes on beside those;
-        // outputs first where the keys are not here yet or the item ends
-        const bool here = mbar_try_wait(&full[st], k / ST & 1);
-        const bool early = k > 0 && (t == c.t0 || !__all_sync(0xffffffffu, here));
-        if (early) outputs(k - 1, first, t == c.t0);
-        if (t == c.t0) wait(&qfull[qb], seg / C::QB);
         wait(&full[st], k / ST);
         if (k >= 2) wait_pv(k - 2);  // S of stage k - 2 held that product's weights
         tc_fence_after();
@@ -299,15 +277,34 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           if (t + 1 == c.t1) tc_commit(&qempty[qb]);
         }
         __syncwarp();
-        if (k > 0 && !early) outputs(k - 1, first, false);
-        first = t == c.t0;
       }
       ++seg;
     }
-    if (k > 0) {
-      outputs(k - 1, first, true);
-      wait_pv(k - 1);  // nothing in flight when the columns are released
+  } else if (warp == 9) {
+    // O += P . V
+    const uint32_t id_o = idesc_bf16(p.D) | (1u << 16), ring_u = smem_u32(ring);
+    int k = 0;
+    while (c.next(p, G)) {
+      for (int t = c.t0; t < c.t1; ++t, ++k) {
+        const int st = k % ST, sb = k & 1;
+        wait(&p_full[sb], k >> 1);
+        tc_fence_after();
+        const bool keep = *static_cast<volatile int *>(&keep_first[sb]) != 0;
+        const uint32_t acc = t > c.t0 || keep ? 1u : 0u;
+        const uint64_t v = sw128_mn_desc(ring_u + st * C::STAGE + TOK * RB, TOK * 128);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < TOK / 16; ++kk)  // 16 tokens: 2048 bytes of V, 8 columns of P
+            tc_mma_ts(o_tmem, s_tmem + sb * 64 + kk * 8, v + (2048 >> 4) * kk, id_o,
+                      kk > 0 ? 1u : acc);
+          // a segment's last stage is released after its join
+          if (t + 1 < c.t1) tc_commit(&empty[st]);
+          tc_commit(&pv_done[sb]);
+        }
+        __syncwarp();
+      }
     }
+    if (k > 0) wait_pv(k - 1);  // nothing in flight when the columns are released
   } else {
     // ================================================================ softmax, a thread a lane
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
@@ -406,72 +403,67 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         int keep = 0;
         if (!plain) {
           // Weights of zero must not meet what is not finite. Tokens that do not exist (boxes
-          // bring what lies past the end) get values of zero ...
+          // bring what lies past the end) get values of zero. Where a value of a token that
+          // some row does not see is not finite, the stage's values go through the product
+          // without what is not finite in them, and that is added where it is seen.
           uint8_t *v = ring + st * C::STAGE + TOK * RB;
-          if (!whole) {
-            for (int i = lane; i < TOK * (RB / 16); i += 32) {
-              const int row = i / (RB / 16);
-              if (!(valid[row >> 5] >> (row & 31) & 1))
-                *reinterpret_cast<uint4 *>(v + swz<RB, TOK>(row, i % (RB / 16))) =
-                    make_uint4(0, 0, 0, 0);
-            }
-            __syncwarp();
-          }
-          // ... and values of tokens that some rows see and others do not are taken through
-          // the product without what is not finite in them, which is added where it is seen
-          // (a sequence's only row sees every token from its window's first on).
-          if (x.n > 1 || p.window > 0) {
-            bool bad = false;
-            for (int i = lane; i < TOK * (RB / 16); i += 32) {
-              const uint4 y = *reinterpret_cast<const uint4 *>(
-                  v + swz<RB, TOK>(i / (RB / 16), i % (RB / 16)));
+          bool bad = false;
+#pragma unroll 4
+          for (int i = lane; i < TOK * (RB / 16); i += 32) {
+            const int row = i / (RB / 16), j = j0 + row;
+            uint4 *at = reinterpret_cast<uint4 *>(v + swz<RB, TOK>(row, i % (RB / 16)));
+            if (!(valid[row >> 5] >> (row & 31) & 1)) {
+              *at = make_uint4(0, 0, 0, 0);
+            } else if (j < lo_all || j > hi_all) {
+              const uint4 y = *at;
               bad |= (__vcmpeq2(y.x & 0x7f807f80u, 0x7f807f80u) |
                       __vcmpeq2(y.y & 0x7f807f80u, 0x7f807f80u) |
                       __vcmpeq2(y.z & 0x7f807f80u, 0x7f807f80u) |
                       __vcmpeq2(y.w & 0x7f807f80u, 0x7f807f80u)) != 0;
             }
-            if (__any_sync(0xffffffffu, bad)) {
-              if (!begins) wait_pv(k - 1);
-              tc_fence_after();
-              for (int d = 0; d < p.D; d += 16) {
-                float o[16];
-                uint32_t u[16];
-                tmem_ld16(o_tmem + lanes + d, o);
+          }
+          __syncwarp();
+          if (__any_sync(0xffffffffu, bad)) {
+            if (!begins) wait_pv(k - 1);
+            tc_fence_after();
+            for (int d = 0; d < p.D; d += 16) {
+              float o[16];
+              uint32_t u[16];
+              tmem_ld16(o_tmem + lanes + d, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = begins ? 0.0f : o[e];
+              for (int i = 0; i < TOK; ++i) {
+                const uint32_t pw2 = tmem_ld1(s_at + i / 2);
                 tmem_wait_ld();
+                const float pr = i & 1 ? bf16hi(pw2) : bf16lo(pw2);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = begins ? 0.0f : o[e];
-                for (int i = 0; i < TOK; ++i) {
-                  const uint32_t pw2 = tmem_ld1(s_at + i / 2);
-                  tmem_wait_ld();
-                  const float pr = i & 1 ? bf16hi(pw2) : bf16lo(pw2);
-#pragma unroll
-                  for (int e = 0; e < 16; ++e) {
-                    const uint16_t y = *reinterpret_cast<const uint16_t *>(
-                        v + swz<RB, TOK>(i, (d + e) >> 3) + ((d + e) & 7) * 2);
-                    if ((y & 0x7f80) == 0x7f80 && pr != 0.0f) o[e] += pr * bf16_to_f32(y);
-                  }
+                for (int e = 0; e < 16; ++e) {
+                  const uint16_t y = *reinterpret_cast<const uint16_t *>(
+                      v + swz<RB, TOK>(i, (d + e) >> 3) + ((d + e) & 7) * 2);
+                  if ((y & 0x7f80) == 0x7f80 && pr != 0.0f) o[e] += pr * bf16_to_f32(y);
                 }
+              }
 #pragma unroll
-                for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(o[e]);
-                tmem_st16(o_tmem + lanes + d, u);
-              }
-              tmem_wait_st();
-              // every row has read the values (not a CTA barrier: this depends on data, and
-              // after a time-out the warps may see different bytes)
-              mbar_arrive(&clean);
-              wait(&clean, cleans++);
-              for (int i = tid; i < TOK * (RB / 16); i += 128) {
-                uint4 *at = reinterpret_cast<uint4 *>(
-                    v + swz<RB, TOK>(i / (RB / 16), i % (RB / 16)));
-                uint4 y = *at;
-                y.x &= ~__vcmpeq2(y.x & 0x7f807f80u, 0x7f807f80u);
-                y.y &= ~__vcmpeq2(y.y & 0x7f807f80u, 0x7f807f80u);
-                y.z &= ~__vcmpeq2(y.z & 0x7f807f80u, 0x7f807f80u);
-                y.w &= ~__vcmpeq2(y.w & 0x7f807f80u, 0x7f807f80u);
-                *at = y;
-              }
-              keep = 1;  // the segment's first outputs add to these
+              for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(o[e]);
+              tmem_st16(o_tmem + lanes + d, u);
             }
+            tmem_wait_st();
+            // every row has read the values (not a CTA barrier: this depends on data, and
+            // after a time-out the warps may see different bytes)
+            mbar_arrive(&clean);
+            wait(&clean, cleans++);
+            for (int i = tid; i < TOK * (RB / 16); i += 128) {
+              uint4 *at = reinterpret_cast<uint4 *>(
+                  v + swz<RB, TOK>(i / (RB / 16), i % (RB / 16)));
+              uint4 y = *at;
+              y.x &= ~__vcmpeq2(y.x & 0x7f807f80u, 0x7f807f80u);
+              y.y &= ~__vcmpeq2(y.y & 0x7f807f80u, 0x7f807f80u);
+              y.z &= ~__vcmpeq2(y.z & 0x7f807f80u, 0x7f807f80u);
+              y.w &= ~__vcmpeq2(y.w & 0x7f807f80u, 0x7f807f80u);
+              *at = y;
+            }
+            keep = 1;  // the segment's first outputs add to these
           }
           fence_proxy_async_smem();  // before the product (and later boxes) touch the values
         }
@@ -494,6 +486,31 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       };
       join_ml[tid][0] = m;
       join_ml[tid][1] = l;
+      named_bar_sync(1, 128);
+      // a row's thread: the copies' factors (with the division, where the item ends here), and
+      // the row's lse or (m, l)
+      float factor[C::COPIES];
+      if (tid < n_rows) {
+        float mr = -INFINITY, lr = 0.0f;
+#pragma unroll
+        for (int g = 0; g < C::COPIES; ++g) mr = fmaxf(mr, join_ml[g * MQ + tid][0]);
+        const float b = mr == -INFINITY ? 0.0f : mr;
+#pragma unroll
+        for (int g = 0; g < C::COPIES; ++g) {
+          factor[g] = ex2(join_ml[g * MQ + tid][0] - b);
+          lr += factor[g] * join_ml[g * MQ + tid][1];
+        }
+        if (c0 == c1) {
+          dst.put_lse(p, tid, mr, lr);
+          const float inv = lr == 0.0f ? 0.0f : dst.v_scale / lr;
+#pragma unroll
+          for (int g = 0; g < C::COPIES; ++g) factor[g] = lr == 0.0f ? 0.0f : factor[g] * inv;
+        } else {
+          *reinterpret_cast<float2 *>(slot + MQ * DP + 2 * tid) = make_float2(mr, lr);
+        }
+#pragma unroll
+        for (int g = 0; g < C::COPIES; ++g) join_ml[g * MQ + tid][0] = factor[g];
+      }
       wait_pv(k - 1);
       tc_fence_after();
 #pragma unroll 1
@@ -514,30 +531,21 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         named_bar_sync(1, 128);
         const int cols = width / 4;
         for (int i = tid; i < n_rows * cols; i += 128) {
-          const int row = i / cols, d = i - row * cols;
-          float mr = -INFINITY, lr = 0.0f;
-#pragma unroll
-          for (int g = 0; g < C::COPIES; ++g) mr = fmaxf(mr, join_ml[g * MQ + row][0]);
-          const float b = mr == -INFINITY ? 0.0f : mr;
+          const int row = i / cols, d = i - row * cols, col = d0 + 4 * d;
           float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
           for (int g = 0; g < C::COPIES; ++g) {
-            const float f = ex2(join_ml[g * MQ + row][0] - b);
+            const float f = join_ml[g * MQ + row][0];
             const float4 y = *join_at(g * MQ + row, d);
-            lr += f * join_ml[g * MQ + row][1];
-            v.x += f * y.x;
-            v.y += f * y.y;
-            v.z += f * y.z;
-            v.w += f * y.w;
+            if (f != 0.0f) {  // a copy that saw nothing, a row that saw nothing
+              v.x += f * y.x;
+              v.y += f * y.y;
+              v.z += f * y.z;
+              v.w += f * y.w;
+            }
           }
-          const int col = d0 + 4 * d;
-          if (c0 == c1) {
-            dst.put(p, row, col, v, mr, lr);
-          } else {
-            *reinterpret_cast<float4 *>(slot + row * DP + col) = v;
-            if (col == 0)
-              *reinterpret_cast<float2 *>(slot + MQ * DP + 2 * row) = make_float2(mr, lr);
-          }
+          if (c0 == c1) dst.put_out(p, row, col, v);
+          else *reinterpret_cast<float4 *>(slot + row * DP + col) = v;
         }
         fence_proxy_async_smem();  // before later boxes overwrite the join's stores
         named_bar_sync(1, 128);
