@@ -5,20 +5,21 @@
 // from 9 rows a kv head their products take longer than the keys' and values' way from HBM
 // (64 rows: 435 us where the copy takes 160). Here a stage of 64 tokens costs 512 clocks of
 // the tensor core for up to 128 rows, and copying bounds it again. Division of the work, ring
-// of stages and joins are attn_kernel.cuh's; one CTA an SM has ten warps:
+// of stages and joins are attn_kernel.cuh's; one CTA an SM has twelve warps:
 //
 //   0-3  softmax: a thread a TMEM lane; MQ = 32, 64 or 128 rows an item
-//   4-5  TMA boxes of K and V into the ring
-//   6, 9 a thread each issues the products below (one thread for both took 1 us a stage)
-//   7-8  rows of q into shared memory
+//   4-7  TMA boxes into the ring: half of a stage's tokens, of K or of V, each
+//   8, 9 a thread each issues the products below (one thread for both took 1 us a stage)
+//  10-11 rows of q into shared memory
 //
 //     S[rows, 64 tokens] = Q . K^T    A = Q, B = K, both K-major in shared memory (the boxes'
 //                                     128-byte swizzle is the operand layout)
 //     O[rows, D]        += P . V      A = P from tensor memory, B = V as stored: rows of a
 //                                     token, elements contiguous (MN-major)
 //
-// S is double buffered and P (bf16) overwrites its S, so the softmax of stage k runs beside
-// the scores of k + 1 and the outputs of k - 1. M is 128 whatever the rows are: Q stands in
+// There are four S, and P (bf16) overwrites its S: scores run up to three stages ahead of the
+// softmax, outputs behind it (with two S the way from one stage's weights through its outputs
+// to the scores two stages on set the pace). M is 128 whatever the rows are: Q stands in
 // shared memory 128 / MQ times, and copy g of a row takes the softmax of the g-th part of
 // the stage's tokens with weights of zero for the others, a maximum, a sum and outputs of
 // its own, which are joined at the segment's end. So four warps share the exponentials at
@@ -34,8 +35,10 @@
 namespace ssd {
 namespace {
 
-constexpr int TC_THREADS = 320;
+constexpr int TC_THREADS = 384;
 constexpr int TC_QTHREADS = 64;
+constexpr int TC_PWARPS = 4;
+constexpr int TC_NS = 4;  // buffers of scores
 constexpr float TC_LAZY = 8.0f;
 
 template <int DP, int MQ>
@@ -48,7 +51,8 @@ struct TcCfg {
   static constexpr int ST = DP == 64 ? 8 : (DP == 128 ? 6 : 2);
   static constexpr int QB = DP == 64 ? 2 : 1;
   static constexpr size_t SMEM = QB * QBYTES + ST * STAGE;
-  static constexpr int COLS = DP <= 128 ? 256 : 512;  // O, then two S of 64 columns
+  static constexpr int COLS = 512;  // all: O, then TC_NS S of 64 columns
+  static_assert(DP + TC_NS * 64 <= COLS, "tensor memory");
   static constexpr int SLOT = MQ * DP + 2 * MQ;
 };
 
@@ -87,6 +91,23 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *v) {
       : "memory");
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+// Two fp32 operations in one instruction: a * b + c, a + b.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mov.b64 z, {%6, %7};\n\tfma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
 }
 __device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
   uint32_t r;
@@ -128,12 +149,14 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   extern __shared__ __align__(1024) uint8_t at_smem[];  // q, then the ring
   __shared__ RangeStart<TC_THREADS> start;
   __shared__ __align__(8) uint64_t full[ST], empty[ST], qfull[C::QB], qempty[C::QB];
-  __shared__ __align__(8) uint64_t s_full[2], p_full[2], pv_done[2], clean;
+  __shared__ __align__(8) uint64_t s_full[TC_NS], p_full[TC_NS];
+  __shared__ __align__(8) uint64_t pv_done[TC_NS], clean;
   __shared__ uint32_t stage_valid[ST][TOK / 32];
   __shared__ PendingJoin pending[2];
   __shared__ uint32_t tmem_slot;
-  __shared__ int abort_flag, n_pending, is_last, keep_first[2];
+  __shared__ int abort_flag, n_pending, is_last, keep_first[TC_NS];
   __shared__ float join_ml[128][2];
+  __shared__ long long row_off[MQ];  // of the outputs
   uint8_t *ring = at_smem + C::QB * C::QBYTES;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -141,14 +164,14 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     abort_flag = 0;
     n_pending = 0;
     for (int i = 0; i < ST; ++i) {
-      mbar_init(&full[i], AT_PWARPS);
+      mbar_init(&full[i], TC_PWARPS);
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < C::QB; ++i) {
       mbar_init(&qfull[i], TC_QTHREADS);
       mbar_init(&qempty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < TC_NS; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 128);
       mbar_init(&pv_done[i], 1);
@@ -164,7 +187,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   Shares sh;
   Cursor<TOK, MQ> c;
   if (!begin_range<TC_THREADS>(p, G, start, sh, c)) return;
-  if (warp == 6) {
+  if (warp == 8) {
     tmem_alloc(&tmem_slot, C::COLS);
     tmem_relinquish();
   }
@@ -177,15 +200,16 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   auto wait = [&](uint64_t *bar, int phase) {
     mbar_wait_bounded(bar, phase & 1, pl.status, &abort_flag, pl.wait_limit_ns);
   };
-  // Outputs of stage i added. Two barriers in turn: who waits for stage i knows that i - 2 is
-  // done (the scores of i were issued after it), not that i - 1 is, and a wait tells only
-  // neighbouring phases apart.
-  auto wait_pv = [&](int i) { wait(&pv_done[i & 1], i >> 1); };
+  // Outputs of stage i added. As many barriers in turn as there are S: who waits for stage i
+  // knows that i - TC_NS is done (the scores of i were issued after it), and a wait tells
+  // only neighbouring phases apart.
+  auto wait_pv = [&](int i) { wait(&pv_done[i % TC_NS], i / TC_NS); };
 
-  if (warp == 4 || warp == 5) {
+  if (warp >= 4 && warp < 8) {
     // ================================================================ K and V boxes
-    const int pw = warp - 4;
-    const BoxLane<RB, TOK, 2> boxes(min(p.box, TOK / AT_PWARPS), lane);
+    const int pw = warp & 1;
+    const bool val = warp >= 6;
+    const BoxLane<RB, TOK, 2, true> boxes(min(p.box, TOK / AT_PWARPS), lane);
     int k = 0;
     while (c.next(p, G)) {
       const int32_t *table = p.block_table + static_cast<long long>(c.s) * p.max_pages;
@@ -198,8 +222,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       for (int t = c.t0; t < c.t1; ++t, ++k) {
         const int st = k % ST;
         if (k >= ST) wait(&empty[st], k / ST - 1);
-        boxes.issue(&kmap, &vmap, p.c, smem_u32(ring + st * C::STAGE), &full[st],
-                    stage_valid[st], pw, lane, token0(t), c.x.len, c.hk, page);
+        boxes.issue(val ? &vmap : &kmap, nullptr, p.c, smem_u32(ring + st * C::STAGE) +
+                    (val ? TOK * RB : 0), &full[st], val ? nullptr : stage_valid[st], pw, lane,
+                    token0(t), c.x.len, c.hk, page);
         page = ahead;
         ahead = look_up(t + 2);
       }
@@ -209,11 +234,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       for (int i = max(k - ST, 0); i < k; ++i)
         mbar_wait_drain(&full[i % ST], (i / ST) & 1, 10000000ull);
     }
-  } else if (warp == 7 || warp == 8) {
+  } else if (warp >= 10) {
     // ================================================================ rows of q
     // A thread has one 16-byte column of the head and every PER_PASS-th row.
     constexpr int CH = DP / 8, PER_PASS = TC_QTHREADS / CH;
-    const int at = tid - 7 * 32, ch = at % CH;
+    const int at = tid - 10 * 32, ch = at % CH;
     int seg = 0;
     while (c.next(p, G)) {
       const int qb = seg % C::QB;
@@ -247,7 +272,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       mbar_arrive(&qfull[qb]);
       ++seg;
     }
-  } else if (warp == 6) {
+  } else if (warp == 8) {
     // ================================================================ products
     // S = Q . K^T
     const uint32_t id_s = idesc_bf16(TOK), q_u = smem_u32(at_smem), ring_u = smem_u32(ring);
@@ -258,7 +283,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       for (int t = c.t0; t < c.t1; ++t, ++k) {
         const int st = k % ST;
         wait(&full[st], k / ST);
-        if (k >= 2) wait_pv(k - 2);  // S of stage k - 2 held that product's weights
+        if (k >= TC_NS) wait_pv(k - TC_NS);  // its S held that product's weights
         tc_fence_after();
         if (elect_one()) {
           // 16 elements a product: 32 bytes of a 128-byte slab
@@ -270,10 +295,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               if (d + kk * 16 < p.D)
-                tc_mma(s_tmem + (k & 1) * 64, a + 2 * kk, b + 2 * kk, id_s,
+                tc_mma(s_tmem + (k % TC_NS) * 64, a + 2 * kk, b + 2 * kk, id_s,
                        d + kk > 0 ? 1u : 0u);
           }
-          tc_commit(&s_full[k & 1]);
+          tc_commit(&s_full[k % TC_NS]);
           if (t + 1 == c.t1) tc_commit(&qempty[qb]);
         }
         __syncwarp();
@@ -286,8 +311,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     int k = 0;
     while (c.next(p, G)) {
       for (int t = c.t0; t < c.t1; ++t, ++k) {
-        const int st = k % ST, sb = k & 1;
-        wait(&p_full[sb], k >> 1);
+        const int st = k % ST, sb = k % TC_NS;
+        wait(&p_full[sb], k / TC_NS);
         tc_fence_after();
         const bool keep = *static_cast<volatile int *>(&keep_first[sb]) != 0;
         const uint32_t acc = t > c.t0 || keep ? 1u : 0u;
@@ -322,34 +347,42 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       const float zf = p.scale * LOG2E * (p.c.k_scale ? p.c.k_scale[c.hk] : 1.0f);
       float m = -INFINITY, l = 0.0f;  // m: the maximum that weights refer to
       for (int t = c.t0; t < c.t1; ++t, ++k) {
-        const int st = k % ST, sb = k & 1;
+        const int st = k % ST, sb = k % TC_NS;
         const uint32_t s_at = s_tmem + sb * 64 + lanes;
-        wait(&full[st], k / ST);  // (long since) the copying warps' bits and the values
-        wait(&s_full[sb], k >> 1);
+        wait(&s_full[sb], k / TC_NS);
         tc_fence_after();
         float z[TS];
         if (TS == 16) tmem_ld16(s_at + first_tok, z);
         else
 #pragma unroll
           for (int i = 0; i < TS; i += 32) tmem_ld32(s_at + first_tok + i, z + i);
-        tmem_wait_ld();
-        const uint32_t valid[2] = {stage_valid[st][0], stage_valid[st][1]};
+        wait(&full[st], k / ST);  // (long since) the copying warps' bits and the values
+        const uint64_t valid = stage_valid[st][0] | static_cast<uint64_t>(stage_valid[st][1]) << 32;
         const int j0 = x.begin + t * TOK;
-        const bool whole = (valid[0] & valid[1]) == 0xffffffffu;
-        const bool plain = whole && j0 >= lo_all && j0 + TOK - 1 <= hi_all;
-#pragma unroll
-        for (int i = 0; i < TS; ++i) z[i] *= zf;
+        const bool plain = valid == ~0ull && j0 >= lo_all && j0 + TOK - 1 <= hi_all;
+        tmem_wait_ld();
         if (!plain) {
+          const uint64_t mine = valid >> first_tok;
+          const int from = lo - j0 - first_tok, to = hi - j0 - first_tok;
 #pragma unroll
           for (int i = 0; i < TS; ++i) {
-            const int b = first_tok + i;
-            if (j0 + b < lo || j0 + b > hi || !(valid[b >> 5] >> (b & 31) & 1)) z[i] = -INFINITY;
+            z[i] *= zf;
+            if (i < from || i > to || !(mine >> i & 1)) z[i] = -INFINITY;
           }
         }
+        // the largest score; where every token counts, of the unscaled ones
         float part[4] = {z[0], z[1], z[2], z[3]};  // short chains
+        const bool least = plain && zf < 0.0f;
+        if (least) {
 #pragma unroll
-        for (int i = 4; i < TS; ++i) part[i & 3] = fmaxf(part[i & 3], z[i]);
-        const float mx = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+          for (int i = 4; i < TS; ++i) part[i & 3] = fminf(part[i & 3], z[i]);
+        } else {
+#pragma unroll
+          for (int i = 4; i < TS; ++i) part[i & 3] = fmaxf(part[i & 3], z[i]);
+        }
+        float mx = least ? fminf(fminf(part[0], part[1]), fminf(part[2], part[3]))
+                         : fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+        if (plain) mx *= zf;
         const bool begins = t == c.t0;
         if (begins) {
           m = mx;
@@ -373,17 +406,20 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           }
           tmem_wait_st();
         }
-        const float base = m == -INFINITY ? 0.0f : m;
+        const float base = m == -INFINITY ? 0.0f : m, by = plain ? zf : 1.0f;
         uint32_t w[TS / 2];
-        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
         for (int i = 0; i < TS / 2; ++i) {
-          const float a = ex2(z[2 * i] - base), b = ex2(z[2 * i + 1] - base);
-          sum[2 * (i & 1)] += a;
-          sum[2 * (i & 1) + 1] += b;
-          w[i] = pack2<false>(a, b);
+          float2 y = fma2(make_float2(z[2 * i], z[2 * i + 1]), make_float2(by, by),
+                          make_float2(-base, -base));
+          y.x = ex2(y.x);
+          y.y = ex2(y.y);
+          sum[i & 1] = add2(sum[i & 1], y);
+          w[i] = pack2<false>(y.x, y.y);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        sum[0] = add2(sum[0], sum[1]);
+        l += sum[0].x + sum[0].y;
         // the weights of this copy's tokens, zeros for the others'
 #pragma unroll
         for (int b = 0; b < 32; b += 16) {
@@ -408,19 +444,31 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           // without what is not finite in them, and that is added where it is seen.
           uint8_t *v = ring + st * C::STAGE + TOK * RB;
           bool bad = false;
-#pragma unroll 4
-          for (int i = lane; i < TOK * (RB / 16); i += 32) {
-            const int row = i / (RB / 16), j = j0 + row;
-            uint4 *at = reinterpret_cast<uint4 *>(v + swz<RB, TOK>(row, i % (RB / 16)));
-            if (!(valid[row >> 5] >> (row & 31) & 1)) {
-              *at = make_uint4(0, 0, 0, 0);
-            } else if (j < lo_all || j > hi_all) {
-              const uint4 y = *at;
-              bad |= (__vcmpeq2(y.x & 0x7f807f80u, 0x7f807f80u) |
-                      __vcmpeq2(y.y & 0x7f807f80u, 0x7f807f80u) |
-                      __vcmpeq2(y.z & 0x7f807f80u, 0x7f807f80u) |
-                      __vcmpeq2(y.w & 0x7f807f80u, 0x7f807f80u)) != 0;
+          constexpr int CH = RB / 16;
+          const int head = min(max(lo_all - j0, 0), TOK), tail = min(max(hi_all + 1 - j0, 0), TOK);
+          auto look = [&](int row0, int row1) {
+            for (int i = row0 * CH + lane; i < row1 * CH; i += 32) {
+              const int row = i / CH;
+              uint4 *at = reinterpret_cast<uint4 *>(v + swz<RB, TOK>(row, i % CH));
+              if (!(valid >> row & 1)) {
+                *at = make_uint4(0, 0, 0, 0);
+              } else if (row < head || row >= tail) {
+                const uint4 y = *at;
+                bad |= (__vcmpeq2(y.x & 0x7f807f80u, 0x7f807f80u) |
+                        __vcmpeq2(y.y & 0x7f807f80u, 0x7f807f80u) |
+                        __vcmpeq2(y.z & 0x7f807f80u, 0x7f807f80u) |
+                        __vcmpeq2(y.w & 0x7f807f80u, 0x7f807f80u)) != 0;
+              }
             }
+          };
+          // rows that all see and that exist need no look: only a missing page makes holes there
+          const bool holes = tail > head &&
+                             (~(valid >> head) & (~0ull >> (64 - (tail - head)))) != 0;
+          if (holes) {
+            look(0, TOK);
+          } else {
+            look(0, min(head, tail));
+            look(tail, TOK);
           }
           __syncwarp();
           if (__any_sync(0xffffffffu, bad)) {
@@ -500,6 +548,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           factor[g] = ex2(join_ml[g * MQ + tid][0] - b);
           lr += factor[g] * join_ml[g * MQ + tid][1];
         }
+        const int rr = row0 + tid, tok = rr / G;
+        row_off[tid] = (x.q0 + tok) * p.out_stride +
+                       static_cast<long long>(c.hk * G + rr - tok * G) * p.D;
         if (c0 == c1) {
           dst.put_lse(p, tid, mr, lr);
           const float inv = lr == 0.0f ? 0.0f : dst.v_scale / lr;
@@ -530,8 +581,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         tc_fence_before();  // the next segment's products overwrite the columns
         named_bar_sync(1, 128);
         const int cols = width / 4;
-        for (int i = tid; i < n_rows * cols; i += 128) {
-          const int row = i / cols, d = i - row * cols, col = d0 + 4 * d;
+        auto store = [&](int row, int d) {
+          const int col = d0 + 4 * d;
           float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
           for (int g = 0; g < C::COPIES; ++g) {
@@ -544,8 +595,20 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
               v.w += f * y.w;
             }
           }
-          if (c0 == c1) dst.put_out(p, row, col, v);
-          else *reinterpret_cast<float4 *>(slot + row * DP + col) = v;
+          if (c0 == c1) {
+            uint2 u;
+            u.x = pack2<false>(v.x, v.y);
+            u.y = pack2<false>(v.z, v.w);
+            *reinterpret_cast<uint2 *>(p.out + row_off[row] + col) = u;
+          } else {
+            *reinterpret_cast<float4 *>(slot + row * DP + col) = v;
+          }
+        };
+        if (width == HALF) {  // no division at run time
+#pragma unroll 2
+          for (int i = tid; i < n_rows * (HALF / 4); i += 128) store(i / (HALF / 4), i % (HALF / 4));
+        } else {
+          for (int i = tid; i < n_rows * cols; i += 128) store(i / cols, i % cols);
         }
         fence_proxy_async_smem();  // before later boxes overwrite the join's stores
         named_bar_sync(1, 128);
@@ -559,7 +622,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 6) tmem_dealloc(tmem, C::COLS);
+  if (warp == 8) tmem_dealloc(tmem, C::COLS);
 }
 
 template <int DP, int MQ>
