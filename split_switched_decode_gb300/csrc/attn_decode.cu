@@ -24,9 +24,10 @@ AttnShape attn_shape(int rows) {
                                  : (rows <= 32 ? AttnShape{2, 2} : AttnShape{2, 4}));
 }
 
-// Rows of an item on tcgen05 tensor cores, 0 for the legacy products: up to 8 rows those are
-// not what bounds it.
-int tc_rows(int rows) { return rows <= 8 ? 0 : (rows <= 32 ? 32 : (rows <= 64 ? 64 : 128)); }
+// Rows of an item on tcgen05 tensor cores, 0 for the legacy products. Up to 16 rows those keep up
+// with the copies (16 rows, 64 ragged sequences: 190 us, on tcgen05 207 with pages of 16
+// tokens and 182 with 32; 32 rows: 247 and 191; 64 rows: 458 and 211).
+int tc_rows(int rows) { return rows <= 16 ? 0 : (rows <= 32 ? 32 : (rows <= 64 ? 64 : 128)); }
 
 // Tokens of a TMA box: the largest power of two in the page size, up to what a copying warp
 // brings of a stage; below 8 (a swizzle group) none.

@@ -464,15 +464,13 @@ __device__ __forceinline__ void join_parts(const AttnParams &p, float *partials,
   }
 }
 
-// A worker's part of a split item is stored (by all of the multiplying threads): count it.
+// Counts a worker's part of a split item, which threads in order before this one have stored.
 // The last to arrive joins the item, once its own range is done. With many parts the last
 // of each 16 neighbours joins those (in parallel on as many SMs: a single one would read
 // them for longer than the products took), and the last group the groups.
-__device__ __forceinline__ void part_stored(const AttnPlan &pl, int me, int c0, int c1,
-                                            int n_rows, const ItemOut &dst,
-                                            PendingJoin *pending, int *n_pending) {
-  named_bar_sync(1, AT_CTHREADS);
-  if (threadIdx.x != 0) return;
+__device__ __forceinline__ void count_part(const AttnPlan &pl, int me, int c0, int c1, int n_rows,
+                                           const ItemOut &dst, PendingJoin *pending,
+                                           int *n_pending) {
   const int parts = c1 - c0 + 1, q = me - c0;
   const bool grouped = parts > 2 * AT_GROUP;
   const int lead = q / AT_GROUP * AT_GROUP;
@@ -1048,7 +1046,10 @@ __global__ void __launch_bounds__(AT_THREADS, (AttnCfg<E4M3, DP, NR, WR>::CTAS))
     fence_proxy_async_smem();  // before later boxes overwrite the join's stores
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[last_st]);
-    if (c0 != c1) part_stored(pl, me, c0, c1, n_rows, dst, pending, &n_pending);
+    if (c0 != c1) {
+      named_bar_sync(1, AT_CTHREADS);
+      if (tid == 0) count_part(pl, me, c0, c1, n_rows, dst, pending, &n_pending);
+    }
   }
   static_assert(ST * C::STAGE >= 2 * AT_GROUP * M * 8, "ml of a join");
   run_joins<M, DP>(p, pl, reinterpret_cast<float2 *>(at_smem), pending, &n_pending, &is_last);

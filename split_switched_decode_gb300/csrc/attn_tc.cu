@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   __shared__ RangeStart<TC_THREADS> start;
   __shared__ __align__(8) uint64_t full[ST], empty[ST], qfull[C::QB], qempty[C::QB];
   __shared__ __align__(8) uint64_t s_full[TC_NS], p_full[TC_NS];
-  __shared__ __align__(8) uint64_t pv_done[TC_NS], clean;
+  __shared__ __align__(8) uint64_t pv_done[TC_NS], clean, stored[2];
   __shared__ uint32_t stage_valid[ST][TOK / 32];
   __shared__ PendingJoin pending[2];
   __shared__ uint32_t tmem_slot;
@@ -178,6 +178,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       keep_first[i] = 0;
     }
     mbar_init(&clean, 128);
+    mbar_init(&stored[0], 128);
+    mbar_init(&stored[1], 128);
     fence_mbar_init();
     prefetch_tensormap(&kmap);
     prefetch_tensormap(&vmap);
@@ -240,6 +242,19 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     constexpr int CH = DP / 8, PER_PASS = TC_QTHREADS / CH;
     const int at = tid - 10 * 32, ch = at % CH;
     int seg = 0;
+    Cursor<TOK, MQ> last;  // the segment before this one
+    // Its part, if it is one of several, is stored: count it. (Two barriers in turn: the softmax
+    // can be one segment ahead of this warp, whose rows of q it needs for a second.)
+    auto count = [&](int done) {
+      wait(&stored[done & 1], done >> 1);
+      const long long unit = last.item + AT_ITEM_COST;
+      const int c0 = sh.worker_of(unit), c1 = sh.worker_of(unit + last.x.kt - 1);
+      if (c0 != c1 && lane == 0)
+        count_part(pl, blockIdx.x, c0, c1, min(MQ, last.x.n * G - last.rt * MQ),
+                   {last.x.q0, last.rt * MQ, last.hk * G, G,
+                    p.c.v_scale ? p.c.v_scale[last.hk] : 1.0f},
+                   pending, &n_pending);
+    };
     while (c.next(p, G)) {
       const int qb = seg % C::QB;
       if (seg >= C::QB) wait(&qempty[qb], seg / C::QB - 1);
@@ -270,7 +285,13 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       }
       fence_proxy_async_smem();
       mbar_arrive(&qfull[qb]);
+      if (warp == 11 && seg > 0) count(seg - 1);
+      last = c;
       ++seg;
+    }
+    if (warp == 11) {
+      if (seg > 0) count(seg - 1);
+      named_bar_sync(3, 160);
     }
   } else if (warp == 8) {
     // ================================================================ products
@@ -286,17 +307,26 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         if (k >= TC_NS) wait_pv(k - TC_NS);  // its S held that product's weights
         tc_fence_after();
         if (elect_one()) {
-          // 16 elements a product: 32 bytes of a 128-byte slab
+          // 16 elements a product: 32 bytes of a 128-byte slab; whole slabs, then the rest
+          const uint32_t d_tmem = s_tmem + (k % TC_NS) * 64;
+          uint64_t a = sw128_desc(q_u + qb * C::QBYTES);
+          uint64_t b = sw128_desc(ring_u + st * C::STAGE);
+          uint32_t acc = 0;
 #pragma unroll 1
-          for (int d = 0; d < p.D; d += 64) {
-            const uint32_t slab = d >> 6;
-            const uint64_t a = sw128_desc(q_u + qb * C::QBYTES + slab * (128 * 128));
-            const uint64_t b = sw128_desc(ring_u + st * C::STAGE + slab * (TOK * 128));
+          for (int slab = p.D >> 6; slab > 0; --slab) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              if (d + kk * 16 < p.D)
-                tc_mma(s_tmem + (k % TC_NS) * 64, a + 2 * kk, b + 2 * kk, id_s,
-                       d + kk > 0 ? 1u : 0u);
+              tc_mma(d_tmem, a + 2 * kk, b + 2 * kk, id_s, kk > 0 ? 1u : acc);
+            acc = 1;
+            a += 128 * 128 / 16;
+            b += TOK * 128 / 16;
+          }
+#pragma unroll 1
+          for (int kk = (p.D & 63) >> 4; kk > 0; --kk) {
+            tc_mma(d_tmem, a, b, id_s, acc);
+            acc = 1;
+            a += 2;
+            b += 2;
           }
           tc_commit(&s_full[k % TC_NS]);
           if (t + 1 == c.t1) tc_commit(&qempty[qb]);
@@ -334,7 +364,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     // ================================================================ softmax, a thread a lane
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
     const int copy = tid / MQ, r = tid % MQ, first_tok = copy * TS;
-    int k = 0, cleans = 0;
+    int k = 0, cleans = 0, segs = 0;
     while (c.next(p, G)) {
       const SeqInfo &x = c.x;
       const int n_rows = min(MQ, x.n * G - c.rt * MQ), row0 = c.rt * MQ;
@@ -614,8 +644,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         named_bar_sync(1, 128);
       }
       if (tid == 0) mbar_arrive(&empty[last_st]);
-      if (c0 != c1) part_stored(pl, me, c0, c1, n_rows, dst, pending, &n_pending);
+      // a split item's part is stored: warp 11 counts it, off the softmax's way
+      mbar_arrive(&stored[segs++ & 1]);
     }
+    named_bar_sync(3, 160);  // the counts are in
     static_assert(ST * C::STAGE >= 2 * AT_GROUP * MQ * 8, "ml of a join");
     run_joins<MQ, DP>(p, pl, reinterpret_cast<float2 *>(ring), pending, &n_pending, &is_last);
   }
