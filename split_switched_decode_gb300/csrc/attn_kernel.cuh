@@ -390,47 +390,50 @@ struct PendingJoin {
 __device__ __forceinline__ int part_slot(int c0, int q) { return 2 * (c0 + q) + (q == 0 ? 1 : 0); }
 
 // Parts first, first + every, ... of an item (n of them), added in their order, into dst or
-// (to != nullptr) as one part. Every (m, l) comes into shared memory `ml` in one round trip,
-// then the outputs with 16 loads of a thread on their way (a round trip to the other die's
-// L2 is 0.7 us; one load at a time took 0.25 us a part).
-template <int M, int DP>
+// (to != nullptr) as one part, by the first THREADS threads. Every (m, l) comes into shared memory `ml` in
+// one round trip, then the outputs with 16 loads of a thread on their way (a round trip to
+// the other die's L2 is 0.7 us; one load at a time took 0.25 us a part): NB blocks of four
+// outputs x AHEAD parts. The threads meet at named barrier 2.
+template <int M, int DP, int THREADS>
 __device__ __forceinline__ void join_parts(const AttnParams &p, float *partials, float2 *ml,
                                            int c0, int first, int every, int n, int n_rows,
                                            float *to, const ItemOut &dst) {
-  constexpr int SLOT = M * DP + 2 * M, AHEAD = 8;
+  constexpr int SLOT = M * DP + 2 * M, NB = M <= 16 ? 2 : 4, AHEAD = 16 / NB;
   const int tid = threadIdx.x, cols = p.D / 4;
   auto part = [&](int i) {
     return partials + static_cast<size_t>(part_slot(c0, first + i * every)) * SLOT;
   };
 #pragma unroll 4
-  for (int i = tid; i < n * n_rows; i += AT_CTHREADS)
+  for (int i = tid; i < n * n_rows; i += THREADS)
     ml[i] = __ldcg(
         reinterpret_cast<const float2 *>(part(i / n_rows) + M * DP + 2 * (i % n_rows)));
-  named_bar_sync(1, AT_CTHREADS);
-  for (int i = tid; i < n_rows * cols; i += 2 * AT_CTHREADS) {
-    // two blocks of four outputs at once
-    const int blocks = i + AT_CTHREADS < n_rows * cols ? 2 : 1;
-    int r[2], d[2];
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, base[2];
-    float4 v[2];
+  named_bar_sync(2, THREADS);
+  const int all = n_rows * cols;
+  for (int i = tid; i < all; i += NB * THREADS) {
+    const int blocks = min(NB, (all - i - 1) / THREADS + 1);
+    int r[NB], d[NB];
+    float m[NB], l[NB], base[NB];
+    float4 v[NB];
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const int at = i + (b < blocks ? b : 0) * AT_CTHREADS;
+    for (int b = 0; b < NB; ++b) {
+      const int at = i + (b < blocks ? b : 0) * THREADS;
       r[b] = at / cols;
       d[b] = 4 * (at - r[b] * cols);
       v[b] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      m[b] = -INFINITY;
+      l[b] = 0.0f;
     }
     for (int q0 = 0; q0 < n; q0 += AHEAD) {
-      float4 u[2][AHEAD];
+      float4 u[NB][AHEAD];
 #pragma unroll
       for (int e = 0; e < AHEAD; ++e)
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < NB; ++b)
           if (q0 + e < n)
             u[b][e] = __ldcg(reinterpret_cast<const float4 *>(part(q0 + e) + r[b] * DP + d[b]));
       if (q0 == 0) {
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < NB; ++b) {
 #pragma unroll 4
           for (int q = 0; q < n; ++q) m[b] = fmaxf(m[b], ml[q * n_rows + r[b]].x);
           base[b] = m[b] == -INFINITY ? 0.0f : m[b];
@@ -439,7 +442,7 @@ __device__ __forceinline__ void join_parts(const AttnParams &p, float *partials,
 #pragma unroll
       for (int e = 0; e < AHEAD; ++e)
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < NB; ++b)
           if (q0 + e < n) {
             const float2 y = ml[(q0 + e) * n_rows + r[b]];
             const float f = ex2(y.x - base[b]);
@@ -451,7 +454,7 @@ __device__ __forceinline__ void join_parts(const AttnParams &p, float *partials,
           }
     }
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < NB; ++b) {
       if (b >= blocks) continue;
       if (to == nullptr) {
         dst.put(p, r[b], d[b], v[b], m[b], l[b]);
@@ -482,14 +485,14 @@ __device__ __forceinline__ void count_part(const AttnPlan &pl, int me, int c0, i
   }
 }
 
-// The joins that fell to this worker, after its last segment, when neither registers nor
-// stages hold anything else. `ml`: 2 AT_GROUP M pairs of shared memory.
-template <int M, int DP>
+// The joins that fell to this worker, by its first THREADS threads after the last segment, when
+// neither registers nor stages hold anything else. `ml`: 2 AT_GROUP M pairs of shared memory.
+template <int M, int DP, int THREADS>
 __device__ __forceinline__ void run_joins(const AttnParams &p, const AttnPlan &pl, float2 *ml,
                                           const PendingJoin *pending, const int *n_pending,
                                           int *is_last) {
   constexpr int SLOT = M * DP + 2 * M;
-  named_bar_sync(1, AT_CTHREADS);
+  named_bar_sync(2, THREADS);
   for (int i = 0; i < *n_pending; ++i) {
     const PendingJoin j = pending[i];
     const int groups = (j.parts - 1) / AT_GROUP + 1;
@@ -501,14 +504,14 @@ __device__ __forceinline__ void run_joins(const AttnParams &p, const AttnPlan &p
       n = min(AT_GROUP, j.parts - j.group);
     }
     for (;;) {  // one place of the join in the code: its first use is paid in fetches
-      join_parts<M, DP>(p, pl.partials, ml, j.c0, first, every, n, j.n_rows, to, j.dst);
-      named_bar_sync(1, AT_CTHREADS);
+      join_parts<M, DP, THREADS>(p, pl.partials, ml, j.c0, first, every, n, j.n_rows, to, j.dst);
+      named_bar_sync(2, THREADS);
       if (to == nullptr) break;
       if (threadIdx.x == 0) {
         *is_last = atom_add_acq_rel_gpu(pl.counters + j.c0, 1) == groups - 1;
         if (*is_last) pl.counters[j.c0] = 0;
       }
-      named_bar_sync(1, AT_CTHREADS);
+      named_bar_sync(2, THREADS);
       if (!*is_last) break;
       to = nullptr;
       first = 0;
@@ -776,8 +779,10 @@ __global__ void __launch_bounds__(AT_THREADS, (AttnCfg<E4M3, DP, NR, WR>::CTAS))
               } else {
 #pragma unroll
                 for (int r = 0; r < NR; ++r) {
-                  if (NR * MT == 1 && (kk & 1)) mma16816<false>(z2, v, qf[r][kk][0], qf[r][kk][1]);
-                  else mma16816<false>(z[r][i], v, qf[r][kk][0], qf[r][kk][1]);
+                  if (NR * MT == 1 && (kk & 1))
+                    mma16816<false>(z2, v, qf[r][kk][0], qf[r][kk][1]);
+                  else
+                    mma16816<false>(z[r][i], v, qf[r][kk][0], qf[r][kk][1]);
                 }
               }
             }
@@ -1052,7 +1057,8 @@ __global__ void __launch_bounds__(AT_THREADS, (AttnCfg<E4M3, DP, NR, WR>::CTAS))
     }
   }
   static_assert(ST * C::STAGE >= 2 * AT_GROUP * M * 8, "ml of a join");
-  run_joins<M, DP>(p, pl, reinterpret_cast<float2 *>(at_smem), pending, &n_pending, &is_last);
+  run_joins<M, DP, AT_CTHREADS>(p, pl, reinterpret_cast<float2 *>(at_smem), pending, &n_pending,
+                                &is_last);
 }
 
 // CTAs: two per SM by shared memory, one above D = 128.

@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       const int n_rows = min(MQ, c.x.n * G - c.rt * MQ);
       uint8_t *qd = at_smem + qb * C::QBYTES;
       const uint16_t *head = p.q + static_cast<long long>(c.hk * G) * p.D + ch * 8;
-      constexpr int AHEAD = 8;
+      constexpr int AHEAD = MQ / PER_PASS < 16 ? MQ / PER_PASS : 16;
       for (int r0 = at / CH; r0 < MQ; r0 += AHEAD * PER_PASS) {
         uint4 v[AHEAD];
 #pragma unroll
@@ -289,10 +289,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       last = c;
       ++seg;
     }
-    if (warp == 11) {
-      if (seg > 0) count(seg - 1);
-      named_bar_sync(3, 160);
-    }
+    if (warp == 11 && seg > 0) count(seg - 1);
   } else if (warp == 8) {
     // ================================================================ products
     // S = Q . K^T
@@ -636,7 +633,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         };
         if (width == HALF) {  // no division at run time
 #pragma unroll 2
-          for (int i = tid; i < n_rows * (HALF / 4); i += 128) store(i / (HALF / 4), i % (HALF / 4));
+          for (int i = tid; i < n_rows * (HALF / 4); i += 128)
+            store(i / (HALF / 4), i % (HALF / 4));
         } else {
           for (int i = tid; i < n_rows * cols; i += 128) store(i / cols, i % cols);
         }
@@ -647,10 +645,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       // a split item's part is stored: warp 11 counts it, off the softmax's way
       mbar_arrive(&stored[segs++ & 1]);
     }
-    named_bar_sync(3, 160);  // the counts are in
-    static_assert(ST * C::STAGE >= 2 * AT_GROUP * MQ * 8, "ml of a join");
-    run_joins<MQ, DP>(p, pl, reinterpret_cast<float2 *>(ring), pending, &n_pending, &is_last);
   }
+  static_assert(ST * C::STAGE >= 2 * AT_GROUP * MQ * 8, "ml of a join");
+  run_joins<MQ, DP, TC_THREADS>(p, pl, reinterpret_cast<float2 *>(ring), pending, &n_pending,
+                                &is_last);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
