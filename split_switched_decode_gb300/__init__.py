@@ -395,72 +395,65 @@ def moe_layer(X, Wcat, E, L, topk, Wgu, Wd, Wgu_shared, Wd_shared, latent, topk_
 
 # ----------------------------------------------------------------- attention ----
 
-# These calls run once per layer and step, so their marshalling is kept short: torch is
-# looked up once, pointers go to ctypes as plain integers.
-_torch = None
+# These calls run once per layer and step, so their marshalling is kept short: torch's types
+# and the two functions behind "the current stream" are looked up once, pointers go to ctypes
+# as plain integers, and a check names its tensor only once it has failed.
+_I32 = _F32 = _BF16 = _F8 = _current_device = _current_stream = None
 
 
-def _th():
-    global _torch
-    if _torch is None:
+def _attention_lib():
+    global _I32, _F32, _BF16, _F8, _current_device, _current_stream
+    if _I32 is None:
         import torch
-        _torch = torch
-    return _torch
+        _I32, _F32, _BF16, _F8 = torch.int32, torch.float32, torch.bfloat16, torch.float8_e4m3fn
+        _current_device = torch._C._cuda_getDevice
+        _current_stream = torch._C._cuda_getCurrentRawStream
+    return _load()
 
 
-def _raw_stream(stream):
-    if stream is not None:
-        return stream.cuda_stream
-    c = _th()._C
-    return c._cuda_getCurrentRawStream(c._cuda_getDevice())
-
-
-def _int32(t, name, ndim=1):
-    if t.dtype != _th().int32 or not t.is_cuda or not t.is_contiguous() or t.dim() != ndim:
-        raise TypeError(f"{name} must be a contiguous int32 CUDA tensor of {ndim} dimension(s)")
+def _int32(t, name):
+    if t.dtype is not _I32 or not t.is_cuda or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous int32 CUDA tensor")
     return t.data_ptr()
 
 
 def _scales(t, name, heads):
     if t is None:
         return None
-    if t.dtype != _th().float32 or not t.is_cuda or not t.is_contiguous() or t.numel() != heads:
+    if t.dtype is not _F32 or not t.is_cuda or not t.is_contiguous() or t.numel() != heads:
         raise TypeError(f"{name} must be a contiguous float32 CUDA tensor of {heads} values")
     return t.data_ptr()
 
 
-def _rows(t, name, heads=None, dim=None):
-    """A bf16 [T, heads, D] tensor whose rows are contiguous (any row stride)."""
-    shape = t.shape
-    if t.dtype != _th().bfloat16 or not t.is_cuda or len(shape) != 3:
+def _rows(t, name, dim):
+    """(pointer, rows, heads, row stride) of a bf16 [T, heads, dim] tensor whose rows are
+    contiguous (any row stride)."""
+    if t.dtype is not _BF16 or not t.is_cuda or t.dim() != 3:
         raise TypeError(f"{name} must be a bfloat16 CUDA tensor [rows, heads, D]")
-    if (heads is not None and shape[1] != heads) or (dim is not None and shape[2] != dim):
-        raise ValueError(f"{name} has shape {tuple(shape)}")
+    T, heads, D = t.shape
+    if D != dim:
+        raise ValueError(f"{name} has heads of {D} elements, the caches of {dim}")
     row, head, one = t.stride()
-    if (one != 1 and shape[2] != 1) or (head != shape[2] and shape[1] != 1):
+    if one != 1 or (head != D and heads != 1):
         raise TypeError(f"{name}: heads must be contiguous within a row")
-    return t.data_ptr(), row
+    return t.data_ptr(), T, heads, row
 
 
 def _cache(k, v):
-    """(type, Hkv, D, pages, page size, strides) of the K and V caches, [pages, Hkv,
-    page size, D] tensors of equal type and strides (views of other orders are fine)."""
-    torch = _th()
-    if k.dtype == torch.bfloat16:
-        kind = KV_BF16
-    elif k.dtype == torch.float8_e4m3fn:
-        kind = KV_E4M3
-    else:
-        raise TypeError("the caches must be bfloat16 or float8_e4m3fn tensors")
-    if v.dtype != k.dtype or not k.is_cuda or not v.is_cuda:
-        raise TypeError("k_cache and v_cache must be CUDA tensors of the same type")
+    """(type, shape, strides) of the K and V caches: [pages, Hkv, page size, D] tensors of
+    equal type and strides (views of other orders are fine)."""
+    kind = k.dtype
+    if v.dtype is not kind or not k.is_cuda or not v.is_cuda or \
+            (kind is not _BF16 and kind is not _F8):
+        raise TypeError("k_cache and v_cache must be bfloat16 or float8_e4m3fn CUDA tensors of "
+                        "the same type")
     shape, stride = k.shape, k.stride()
     if len(shape) != 4 or v.shape != shape or v.stride() != stride:
         raise ValueError("k_cache and v_cache must be [pages, Hkv, page size, D] with equal "
                          "strides")
     if stride[3] != 1:
         raise TypeError("the last dimension of the caches must be contiguous")
-    return kind, shape[1], shape[3], shape[0], shape[2], stride
+    return (KV_BF16 if kind is _BF16 else KV_E4M3), shape, stride
 
 
 def kv_plan(kv_len, new_len, block_table, free_pages, free_used, page_size, seq_len, q_start,
@@ -470,20 +463,25 @@ def kv_plan(kv_len, new_len, block_table, free_pages, free_used, page_size, seq_
     summary [4] (rows, free pages used, tokens left out, pages lacking). new_len None: one
     token each; free_used None: none used yet. seq_len may be kv_len and free_used
     summary[1:2], which carries the state from call to call."""
-    tp = _int32(block_table, "block_table", 2)
+    lib = _attention_lib()
+    table = _int32(block_table, "block_table")
+    if block_table.dim() != 2:
+        raise TypeError("block_table must have two dimensions")
     S, max_pages = block_table.shape
     max_tokens = positions.numel()
-    if (kv_len.numel() != S or seq_len.numel() != S or q_start.numel() != S + 1
-            or (new_len is not None and new_len.numel() != S) or slots.numel() != max_tokens
-            or summary.numel() != 4):
+    if kv_len.numel() != S or seq_len.numel() != S or q_start.numel() != S + 1 \
+            or slots.numel() != max_tokens or summary.numel() != 4 \
+            or (new_len is not None and new_len.numel() != S):
         raise ValueError("kv_plan: sizes do not agree")
-    _check(_load().kv_plan(
+    status = lib.kv_plan(
         _int32(kv_len, "kv_len"), None if new_len is None else _int32(new_len, "new_len"), S,
-        page_size, tp, max_pages,
-        _int32(free_pages, "free_pages"), free_pages.numel(),
-        None if free_used is None else _int32(free_used, "free_used"), _int32(seq_len, "seq_len"),
-        _int32(q_start, "q_start"), _int32(positions, "positions"), _int32(slots, "slots"),
-        max_tokens, _int32(summary, "summary"), _raw_stream(stream)), "kv_plan")
+        page_size, table, max_pages, _int32(free_pages, "free_pages"), free_pages.numel(),
+        None if free_used is None else _int32(free_used, "free_used"),
+        _int32(seq_len, "seq_len"), _int32(q_start, "q_start"), _int32(positions, "positions"),
+        _int32(slots, "slots"), max_tokens, _int32(summary, "summary"),
+        _current_stream(_current_device()) if stream is None else stream.cuda_stream)
+    if status:
+        raise DecError(status, "kv_plan")
 
 
 def rope_frequencies(rot, base=10000.0, scaling=ROPE_PLAIN, factor=1.0, orig_len=4096,
@@ -503,23 +501,25 @@ def rope_append(q, k, v, positions, slots, inv_freq, q_out, k_cache, v_cache, in
     """Rotate q [T,Hq,D] into q_out (which may be q) and k [T,Hkv,D] into the cache, write v
     beside it; row t at positions[t] goes to slots[t] (-1: not cached). The first
     2 * len(inv_freq) elements of a head are rotated (inv_freq None: none)."""
-    kind, Hkv, D, pages, page, stride = _cache(k_cache, v_cache)
-    qp, qs = _rows(q, "q", None, D)
-    T, Hq, _ = q.shape
-    kp, ks = _rows(k, "k", Hkv, D)
-    vp, vs = _rows(v, "v", Hkv, D)
-    op, os_ = _rows(q_out, "q_out", Hq, D)
-    if k.shape[0] != T or v.shape[0] != T or q_out.shape[0] != T or positions.numel() != T \
-            or slots.numel() != T:
-        raise ValueError("rope_append: row counts do not agree")
-    fp, rot = (None, 0) if inv_freq is None else \
-        (_scales(inv_freq, "inv_freq", inv_freq.numel()), 2 * inv_freq.numel())
-    _check(_load().rope_append(
-        qp, qs, kp, ks, vp, vs, _int32(positions, "positions"), _int32(slots, "slots"), fp,
-        magnitude, T, Hq, Hkv, D, rot, int(interleaved), op, os_, k_cache.data_ptr(),
-        v_cache.data_ptr(), kind, _scales(k_scale, "k_scale", Hkv),
-        _scales(v_scale, "v_scale", Hkv), pages, page, stride[0], stride[1], stride[2],
-        _raw_stream(stream)), "rope_append")
+    lib = _attention_lib()
+    kind, (pages, Hkv, page, D), stride = _cache(k_cache, v_cache)
+    qp, T, Hq, qs = _rows(q, "q", D)
+    kp, Tk, Hk, ks = _rows(k, "k", D)
+    vp, Tv, Hv, vs = _rows(v, "v", D)
+    op, To, Ho, os_ = _rows(q_out, "q_out", D)
+    if Tk != T or Tv != T or To != T or Hk != Hkv or Hv != Hkv or Ho != Hq \
+            or positions.numel() != T or slots.numel() != T:
+        raise ValueError("rope_append: rows or heads do not agree")
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    status = lib.rope_append(
+        qp, qs, kp, ks, vp, vs, _int32(positions, "positions"), _int32(slots, "slots"),
+        _scales(inv_freq, "inv_freq", rot // 2), magnitude, T, Hq, Hkv, D, rot,
+        1 if interleaved else 0, op, os_, k_cache.data_ptr(), v_cache.data_ptr(), kind,
+        _scales(k_scale, "k_scale", Hkv), _scales(v_scale, "v_scale", Hkv), pages, page,
+        stride[0], stride[1], stride[2],
+        _current_stream(_current_device()) if stream is None else stream.cuda_stream)
+    if status:
+        raise DecError(status, "rope_append")
 
 
 def attn_decode_workspace_bytes(S, T, Hq, Hkv, D) -> int:
@@ -532,25 +532,24 @@ def attn_decode(q, k_cache, v_cache, block_table, seq_len, out, ws, q_start=None
     q_start[s] .. q_start[s+1]-1 are the last tokens of sequence s, which has seq_len[s]
     tokens in the pages block_table[s] (q_start None: one row each). scale: 1/sqrt(D) by
     default; window > 0: a row sees that many last tokens, its own included."""
-    kind, Hkv, D, pages, page, stride = _cache(k_cache, v_cache)
-    qp, qs = _rows(q, "q", None, D)
-    T, Hq, _ = q.shape
-    op, os_ = _rows(out, "out", Hq, D)
-    tp = _int32(block_table, "block_table", 2)
+    lib = _attention_lib()
+    kind, (pages, Hkv, page, D), stride = _cache(k_cache, v_cache)
+    qp, T, Hq, qs = _rows(q, "q", D)
+    op, To, Ho, os_ = _rows(out, "out", D)
+    table = _int32(block_table, "block_table")
+    if block_table.dim() != 2:
+        raise TypeError("block_table must have two dimensions")
     S, max_pages = block_table.shape
-    if out.shape[0] != T or seq_len.numel() != S or \
+    if To != T or Ho != Hq or seq_len.numel() != S or \
             (q_start is not None and q_start.numel() != S + 1):
         raise ValueError("attn_decode: sizes do not agree")
-    lp = None
-    if lse is not None:
-        if lse.dtype != _th().float32 or not lse.is_cuda or not lse.is_contiguous() \
-                or tuple(lse.shape) != (T, Hq):
-            raise TypeError("lse must be a contiguous float32 CUDA tensor [T, Hq]")
-        lp = lse.data_ptr()
-    _check(_load().attn_decode(
+    status = lib.attn_decode(
         qp, qs, k_cache.data_ptr(), v_cache.data_ptr(), kind, _scales(k_scale, "k_scale", Hkv),
-        _scales(v_scale, "v_scale", Hkv), pages, page, stride[0], stride[1], stride[2],
-        tp, max_pages, _int32(seq_len, "seq_len"),
+        _scales(v_scale, "v_scale", Hkv), pages, page, stride[0], stride[1], stride[2], table,
+        max_pages, _int32(seq_len, "seq_len"),
         None if q_start is None else _int32(q_start, "q_start"), S, T, Hq, Hkv, D,
-        D ** -0.5 if scale is None else scale, window, op, os_, lp, ws.data_ptr(),
-        ws.numel() * ws.element_size(), _raw_stream(stream)), "attn_decode")
+        D ** -0.5 if scale is None else scale, window, op, os_,
+        _scales(lse, "lse", T * Hq), ws.data_ptr(), ws.nbytes,
+        _current_stream(_current_device()) if stream is None else stream.cuda_stream)
+    if status:
+        raise DecError(status, "attn_decode")
