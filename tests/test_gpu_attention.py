@@ -635,6 +635,92 @@ def test_attn_on_another_stream_and_in_a_graph(env):
         assert torch.equal(out, want)
 
 
+# Many rows a kv head (verification rows, wide groups) on a bf16 cache with pages of whole
+# 8-token blocks run on their own kernel, with items of 32, 64 or 128 rows.
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("rows,Hq,Hkv,D,page", [
+    (8, 3, 1, 64, 8), (9, 2, 1, 16, 16), (5, 10, 2, 128, 24), (8, 8, 1, 128, 32),
+    (16, 16, 2, 96, 64), (3, 64, 2, 256, 16), (17, 7, 1, 144, 40), (40, 8, 1, 64, 128),
+    (20, 20, 1, 48, 16), (4, 8, 1, 80, 16),
+])
+def test_attn_many_rows(env, rows, Hq, Hkv, D, page, layout):
+    c = _Case(env, [rows, 63, 64, 65, 0, 700, 1, 130], [rows, rows, rows, rows, rows, rows, 1, 2],
+              Hq, Hkv, D, page, layout=layout, seed=rows + D)
+    c.check()
+
+
+@pytest.mark.parametrize("window", [1, 7, 64, 65, 200])
+def test_attn_many_rows_window(env, window):
+    c = _Case(env, [9, 64, 300, 1001, 0], [9, 9, 9, 9, 9], 8, 2, 128, 16, seed=window)
+    c.check(window)
+
+
+@pytest.mark.parametrize("rows", [1, 8])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_attn_scores_that_keep_growing(env, rows, e4m3):
+    """Scores in the hundreds over many stages: the running maximum moves again and again, and
+    with it what has been summed."""
+    c = _Case(env, [1500, 700], [rows, rows], 8, 1, 128, 16, e4m3, seed=31, spread=150.0)
+    c.check()
+
+
+@pytest.mark.parametrize("scale", [-0.3, 0.0])
+@pytest.mark.parametrize("rows", [1, 8])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_attn_negative_and_zero_scale(env, scale, rows, e4m3):
+    c = _Case(env, [200, 70, 0], [rows] * 3, 8, 1, 64, 16, e4m3, seed=32)
+    c.scale = scale
+    c.check()
+
+
+@pytest.mark.parametrize("lengths,rows", [([40, 700], 6), ([64, 130], 9), ([66, 200], 20)])
+def test_attn_many_rows_nan_in_unseen_places(env, lengths, rows):
+    """The newest token's key and value gone wrong: only the row that sees it is affected,
+    whether the token lies in the item's first stage or a later one."""
+    torch, ssd, dev = env
+    c = _Case(env, lengths, [rows, rows], 8, 1, 128, 16, seed=33 + rows)
+    want, want_lse = c.check()
+    for value in (float("nan"), float("inf")):
+        for s, n in enumerate(lengths):
+            page = int(c.table[s, (n - 1) // 16])
+            c.kc[page, :, (n - 1) % 16] = float("nan")
+            c.vc[page, :, (n - 1) % 16] = value
+        got, lse = c.run()
+        for s in range(2):
+            a, b = s * rows, (s + 1) * rows - 1
+            assert torch.equal(got[a:b], want[a:b]) and torch.equal(lse[a:b], want_lse[a:b])
+            assert bool(torch.isnan(got[b].float()).all()) and bool(torch.isnan(lse[b]).all())
+
+
+def test_attn_many_rows_missing_pages(env):
+    """Missing pages inside, at the end and everywhere."""
+    c = _Case(env, [200, 40, 500, 300], [9, 9, 9, 9], 8, 2, 128, 16, seed=34)
+    c.table[0, 3:5] = -1
+    c.table[1, :] = 10 ** 6
+    c.table[2, 31] = -2 ** 31
+    c.table[3, :12] = -1
+    c.check()
+    c.check(window=100)
+
+
+def test_attn_one_workspace_for_all(env):
+    """Calls with few and with many rows, of both cache types, in turn on one workspace: each
+    finds its counters at zero."""
+    torch, ssd, dev = env
+    cases = [_Case(env, [9000, 100], [rows] * 2, Hq, 1, 128, 16, e4m3, seed=35)
+             for rows, Hq, e4m3 in ((1, 8, False), (8, 8, False), (8, 8, True), (16, 8, False))]
+    ws = max((c.ws for c in cases), key=lambda t: t.numel())
+    for c in cases:
+        c.ws = ws
+    wants = [c.check() for c in cases]
+    for _ in range(2):
+        for c, (out, lse) in zip(cases, wants):
+            got, l = c.run()
+            assert torch.equal(got, out) and torch.equal(l, lse)
+    assert ssd.dec_sync_status() == ssd.DEC_OK
+
+
 # ----------------------------------------------------------------- refusals ----
 
 def test_binding_refusals(env):
