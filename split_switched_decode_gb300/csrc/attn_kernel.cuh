@@ -61,8 +61,11 @@ struct AttnCfg {
   static constexpr int ES = E4M3 ? 1 : 2;        // bytes of a cache element
   static constexpr int MW = 8 * NR;              // rows of a warp
   static constexpr int M = MW * WR;              // rows of an item
-  static constexpr int STEP = E4M3 ? 32 : 16;    // tokens of a warp's inner step
-  static constexpr int TOK = AT_CWARPS * STEP;   // tokens of a stage
+  static constexpr int SPAN = E4M3 ? 32 : 16;    // tokens of a stage for each warp
+  static constexpr int TOK = AT_CWARPS * SPAN;   // tokens of a stage
+  // tokens of an inner step: with 16 rows a warp, 32 would spill (0.5 KB a thread: 2.4 us a
+  // stage)
+  static constexpr int STEP = NR == 1 ? SPAN : 16;
   static constexpr int RB = DP * ES;             // bytes of a token's row in a stage
   static constexpr int CPR = RB / 16;            // 16-byte chunks of a row
   static constexpr int STAGE = 2 * TOK * RB;     // K then V
@@ -741,8 +744,8 @@ __global__ void __launch_bounds__(AT_THREADS, (AttnCfg<E4M3, DP, NR, WR>::CTAS))
       }
       if (my_rows > 0) {
 #pragma unroll 1
-        for (int sub = 0; sub < WR; ++sub) {
-          const int tok0 = (wt * WR + sub) * STEP;  // of the stage
+        for (int sub = 0; sub < WR * (C::SPAN / STEP); ++sub) {
+          const int tok0 = wt * WR * C::SPAN + sub * STEP;  // of the stage
           const uint32_t ks = smem_u32(stage), vs = ks + TOK * RB;
           const uint32_t valid = STEP == 32 ? stage_valid[st][tok0 >> 5]
                                             : stage_valid[st][tok0 >> 5] >> (tok0 & 31);
