@@ -51,9 +51,12 @@ constexpr int AT_CWARPS = 4;  // warps that multiply
 constexpr int AT_PWARPS = 2;  // warps that copy
 constexpr int AT_CTHREADS = 32 * AT_CWARPS;
 constexpr int AT_THREADS = 32 * (AT_CWARPS + AT_PWARPS);
-constexpr int AT_ITEM_COST = 1;  // stages that an item's start and end are charged as
-constexpr int AT_MIN_UNITS = 2;  // units a worker takes at least
 constexpr int AT_GROUP = 16;     // workers whose parts of a much split item are joined first
+// An item costs what four stages do (its q, partial results, the join): with a charge of one,
+// 28 sequences of 150 to 320 tokens with heads of 256 take 17.2 us instead of 16.1, 3 long ones under a
+// window 24.8 instead of 23.0. Shares of two stages and more: with four, a single
+// sequence of 1024 tokens takes 11.0 us instead of 9.8.
+constexpr int AT_ITEM_COST = 4, AT_LEAST = 2;
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
 template <bool E4M3, int DP, int NR, int WR>
@@ -175,8 +178,8 @@ struct SeqInfo {
   int len, begin;  // keys [begin, len) that some row can see
   int kt;          // stages of keys (at least 1: an empty row still has to be written)
   int rt;          // row tiles
-  __device__ __forceinline__ long long units(int Hkv) const {
-    return static_cast<long long>(Hkv) * rt * (kt + AT_ITEM_COST);
+  __device__ __forceinline__ long long units(int Hkv, int cost) const {
+    return static_cast<long long>(Hkv) * rt * (kt + cost);
   }
 };
 
@@ -208,7 +211,7 @@ struct AttnPlan {
   uint64_t wait_limit_ns;
 };
 
-// All items' units in order (an item: AT_ITEM_COST, then one per stage), and worker c's
+// All items' units in order (an item: its COST, then one per stage), and worker c's
 // share of them: share_n, one more for the first share_r workers.
 struct Shares {
   long long share_n, share_r;
@@ -219,8 +222,9 @@ struct Shares {
   }
 };
 
-// Walks the segments of one CTA's range.
-template <int TOK, int M>
+// Walks the segments of one CTA's range. TOK: tokens of a stage; M: rows of an item; COST:
+// stages that an item's start and end are charged as; LEAST: units of the smallest share.
+template <int TOK, int M, int COST, int LEAST>
 struct Cursor {
   long long cur, end, item;  // next unit, end of the range, first unit of the item
   int s, hk, rt, t0, t1;     // segment: stages [t0, t1) of item (s, hk, rt)
@@ -228,7 +232,7 @@ struct Cursor {
   // The next segment that has a stage; false at the end of the range.
   __device__ __forceinline__ bool next(const AttnParams &p, int G) {
     while (cur < end) {
-      const long long stop = item + AT_ITEM_COST + x.kt;
+      const long long stop = item + COST + x.kt;
       if (cur == stop) {  // the next item
         item = cur;
         if (++rt == x.rt) {
@@ -243,8 +247,8 @@ struct Cursor {
       }
       const long long from = cur, to = stop < end ? stop : end;
       cur = to;
-      t0 = static_cast<int>(max(from - item - AT_ITEM_COST, 0ll));
-      t1 = static_cast<int>(to - item - AT_ITEM_COST);
+      t0 = static_cast<int>(max(from - item - COST, 0ll));
+      t1 = static_cast<int>(to - item - COST);
       if (t1 > t0) return true;
     }
     return false;
@@ -260,15 +264,15 @@ struct RangeStart {
   long long off;
   int seq;
 };
-template <int THREADS, int TOK, int M>
+template <int THREADS, int TOK, int M, int COST, int LEAST>
 __device__ __forceinline__ bool begin_range(const AttnParams &p, int G,
                                             RangeStart<THREADS> &start, Shares &sh,
-                                            Cursor<TOK, M> &c) {
+                                            Cursor<TOK, M, COST, LEAST> &c) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, me = blockIdx.x;
   const int per = (p.S + THREADS - 1) / THREADS;
   const int s_lo = min(tid * per, p.S), s_hi = min(s_lo + per, p.S);
   long long mine = 0;
-  for (int s = s_lo; s < s_hi; ++s) mine += seq_info<TOK, M>(p, G, s).units(p.Hkv);
+  for (int s = s_lo; s < s_hi; ++s) mine += seq_info<TOK, M>(p, G, s).units(p.Hkv, COST);
   long long incl = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -283,7 +287,7 @@ __device__ __forceinline__ bool begin_range(const AttnParams &p, int G,
     if (w < warp) before += start.warp_sum[w];
     total += start.warp_sum[w];
   }
-  const long long most = (total + AT_MIN_UNITS - 1) / AT_MIN_UNITS;
+  const long long most = (total + LEAST - 1) / LEAST;
   const int workers = static_cast<int>(most < gridDim.x ? most : gridDim.x);
   if (me >= workers) return false;
   sh.share_n = total / workers;
@@ -293,7 +297,7 @@ __device__ __forceinline__ bool begin_range(const AttnParams &p, int G,
   long long at = before + incl - mine;  // units before this thread's sequences
   if (at <= c.cur && c.cur < at + mine) {
     for (int s = s_lo; s < s_hi; ++s) {
-      const long long n = seq_info<TOK, M>(p, G, s).units(p.Hkv);
+      const long long n = seq_info<TOK, M>(p, G, s).units(p.Hkv, COST);
       if (c.cur < at + n) {
         start.seq = s;
         start.off = c.cur - at;
@@ -305,7 +309,7 @@ __device__ __forceinline__ bool begin_range(const AttnParams &p, int G,
   __syncthreads();
   c.s = start.seq;
   c.x = seq_info<TOK, M>(p, G, c.s);
-  const long long per_item = c.x.kt + AT_ITEM_COST, i = start.off / per_item;
+  const long long per_item = c.x.kt + COST, i = start.off / per_item;
   c.hk = static_cast<int>(i / c.x.rt);
   c.rt = static_cast<int>(i - static_cast<long long>(c.hk) * c.x.rt);
   c.item = c.cur - (start.off - i * per_item);
@@ -561,7 +565,7 @@ __global__ void __launch_bounds__(AT_THREADS, (AttnCfg<E4M3, DP, NR, WR>::CTAS))
   const int G = p.Hq / p.Hkv;
 
   Shares sh;
-  Cursor<TOK, M> c;
+  Cursor<TOK, M, AT_ITEM_COST, AT_LEAST> c;
   if (!begin_range<AT_THREADS>(p, G, start, sh, c)) return;
 
   if (warp >= AT_CWARPS) {
