@@ -31,8 +31,7 @@ int tc_rows(int rows) { return rows <= 16 ? 0 : (rows <= 32 ? 32 : (rows <= 64 ?
 
 // Tokens of a TMA box: the largest power of two in the page size, up to what a copying warp
 // brings of a stage; below 8 (a swizzle group) none.
-int box_tokens(int page_size, bool e4m3) {
-  const int most = e4m3 ? 64 : 32;
+int box_tokens(int page_size, int most) {
   int box = page_size & -page_size;
   if (box > most) box = most;
   return box >= 8 ? box : 0;
@@ -55,7 +54,8 @@ cudaError_t launch_attn_decode(const AttnParams &params, bool e4m3, void *ws, in
   a.status = status;
   a.wait_limit_ns = wait_limit_ns;
   const int dp = padded_dim(p.D);
-  p.box = box_tokens(p.c.page_size, e4m3);
+  const int rows = mean_rows(p.S, p.T, p.Hq, p.Hkv), tc = e4m3 ? 0 : tc_rows(rows);
+  p.box = box_tokens(p.c.page_size, e4m3 || tc > 0 ? 64 : 32);
   if (p.box > 0) {
     // strides of zero (a broadcast cache) or an encoder that refuses: plain copies
     const bool ok = p.c.page_stride > 0 && p.c.head_stride > 0 && p.c.token_stride > 0 &&
@@ -63,9 +63,7 @@ cudaError_t launch_attn_decode(const AttnParams &params, bool e4m3, void *ws, in
                     host_cache_map(&a.vmap, p.c, p.c.v, e4m3, p.D, p.Hkv, p.box, dp);
     if (!ok) p.box = 0;
   }
-  const int rows = mean_rows(p.S, p.T, p.Hq, p.Hkv);
-  if (!e4m3 && p.box > 0 && tc_rows(rows) > 0)
-    return launch_attn_tc(p, dp, tc_rows(rows), ws, a, s);
+  if (tc > 0 && p.box > 0) return launch_attn_tc(p, dp, tc, ws, a, s);
   const AttnShape sh = attn_shape(rows);
   auto launch = dp == 64 ? launch_attn_d64 : (dp == 128 ? launch_attn_d128 : launch_attn_d256);
   return launch(p, e4m3, sh.nr, sh.wr, ws, a, s);

@@ -316,22 +316,21 @@ __device__ __forceinline__ bool begin_range(const AttnParams &p, int G,
   return true;
 }
 
-// A copying warp's boxes of one stage: HALF tokens of K and V (ONE: of one of the two), lane ->
-// (block of `box` tokens, slab of 128 bytes, K or V), at most 32 boxes.
-template <int RB, int TOK, int ES, bool ONE = false>
+// A copying warp's boxes of one stage: HALF tokens of K and V, lane -> (block of `box` tokens,
+// slab of 128 bytes, K or V), at most 32 boxes.
+template <int RB, int TOK, int ES>
 struct BoxLane {
   static constexpr int HALF = TOK / AT_PWARPS, WORDS = HALF / 32;
   static constexpr int SLABS = RB == 64 ? 1 : RB / 128, ROW = RB == 64 ? 64 : 128;
-  static constexpr int PER_BLOCK = (ONE ? 1 : 2) * SLABS;
+  static constexpr int PER_BLOCK = 2 * SLABS;
   int box, block, slab;
   bool has;
   __device__ __forceinline__ BoxLane(int tokens, int lane)
-      : box(tokens), block(lane / PER_BLOCK), slab((ONE ? lane : lane >> 1) % SLABS),
+      : box(tokens), block(lane / PER_BLOCK), slab((lane >> 1) % SLABS),
         has(block * tokens < HALF) {}
   // Into stage memory `dst` (K, then V TOK * RB bytes on); j0: the warp's first token, at
   // most `len` of the sequence exist; `page` the page of this lane's block, < 0 for none.
-  // Writes the bits of the tokens that exist (nullptr: not) and arrives on `full` with the
-  // bytes to come. ONE: `dst` and `kmap` are of K or of V.
+  // Writes the bits of the tokens that exist and arrives on `full` with the bytes to come.
   __device__ __forceinline__ void issue(const CUtensorMap *kmap, const CUtensorMap *vmap,
                                         const PagedCache &cache, uint32_t dst, uint64_t *full,
                                         uint32_t *valid_words, int pw, int lane, int j0, int len,
@@ -343,12 +342,12 @@ struct BoxLane {
       const int tok = q * 32 + lane;
       const uint32_t valid = __ballot_sync(
           0xffffffffu, (blocks >> (tok / box * PER_BLOCK) & 1) && j0 + tok < len);
-      if (lane == 0 && (!ONE || valid_words)) valid_words[pw * WORDS + q] = valid;
+      if (lane == 0) valid_words[pw * WORDS + q] = valid;
     }
     if (lane == 0) mbar_arrive_expect_tx(full, __popc(blocks) * box * ROW);
     __syncwarp();
     if (ok) {
-      const bool val = !ONE && (lane & 1);
+      const bool val = lane & 1;
       tma_load_4d(dst + (val ? TOK * RB : 0) + slab * (TOK * 128) +
                       (pw * HALF + block * box) * ROW,
                   val ? vmap : kmap, full, slab * (128 / ES),

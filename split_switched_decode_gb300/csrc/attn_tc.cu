@@ -8,7 +8,7 @@
 // of stages and joins are attn_kernel.cuh's; one CTA an SM has twelve warps:
 //
 //   0-3  softmax: a thread a TMEM lane; MQ = 32, 64 or 128 rows an item
-//   4-7  TMA boxes into the ring: half of a stage's tokens, of K or of V, each
+//   4-7  TMA boxes into the ring
 //   8, 9 a thread each issues the products below (one thread for both took 1 us a stage)
 //  10-11 rows of q into shared memory
 //
@@ -35,9 +35,7 @@
 namespace ssd {
 namespace {
 
-constexpr int TC_THREADS = 384;
 constexpr int TC_QTHREADS = 64;
-constexpr int TC_PWARPS = 4;
 constexpr int TC_NS = 4;  // buffers of scores
 constexpr float TC_LAZY = 8.0f;
 // An item costs what six stages do: with a charge of one, 64 ragged sequences of 64 rows a kv
@@ -55,8 +53,11 @@ struct TcCfg {
   static constexpr int ST = DP == 64 ? 8 : (DP == 128 ? 6 : 2);
   static constexpr int QB = DP == 64 ? 2 : 1;
   static constexpr size_t SMEM = QB * QBYTES + ST * STAGE;
-  static constexpr int COLS = 512;  // all: O, then TC_NS S of 64 columns
-  static_assert(DP + TC_NS * 64 <= COLS, "tensor memory");
+  // softmax warpgroups, which take the stages in turn, each with outputs of its own
+  static constexpr int GROUPS = DP <= 128 ? 2 : 1;
+  static constexpr int SW = 4 * GROUPS, THREADS = 32 * (SW + 8), PARTS = GROUPS * COPIES;
+  static constexpr int COLS = 512;  // all: the groups' O, then TC_NS S of 64 columns
+  static_assert(GROUPS * DP + TC_NS * 64 <= COLS, "tensor memory");
   static constexpr int SLOT = MQ * DP + 2 * MQ;
 };
 
@@ -144,23 +145,23 @@ __device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t saddr, uint32_t slab_
 }
 
 template <int DP, int MQ>
-__global__ void __launch_bounds__(TC_THREADS, 1)
+__global__ void __launch_bounds__((TcCfg<DP, MQ>::THREADS), 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap,
                    const __grid_constant__ AttnParams p, const AttnPlan pl) {
   using C = TcCfg<DP, MQ>;
-  constexpr int TOK = C::TOK, RB = C::RB, ST = C::ST, TS = C::TS;
+  constexpr int TOK = C::TOK, RB = C::RB, ST = C::ST, TS = C::TS, GROUPS = C::GROUPS, SW = C::SW;
   extern __shared__ __align__(1024) uint8_t at_smem[];  // q, then the ring
-  __shared__ RangeStart<TC_THREADS> start;
+  __shared__ RangeStart<C::THREADS> start;
   __shared__ __align__(8) uint64_t full[ST], empty[ST], qfull[C::QB], qempty[C::QB];
   __shared__ __align__(8) uint64_t s_full[TC_NS], p_full[TC_NS];
-  __shared__ __align__(8) uint64_t pv_done[TC_NS], clean, stored[2];
-  __shared__ uint32_t stage_valid[ST][TOK / 32];
+  __shared__ __align__(8) uint64_t pv_done[TC_NS], clean[GROUPS], stored[2];
+  __shared__ uint64_t stage_valid[ST];  // tokens of the stage that exist
   __shared__ PendingJoin pending[2];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag, n_pending, is_last, keep_first[TC_NS];
-  __shared__ float join_ml[128][2];
-  __shared__ long long row_off[MQ];  // of the outputs
+  __shared__ float join_ml[GROUPS * 128][2];
+  __shared__ uint8_t row_tok[MQ];  // a row's token, from the item's first
   uint8_t *ring = at_smem + C::QB * C::QBYTES;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -168,7 +169,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     abort_flag = 0;
     n_pending = 0;
     for (int i = 0; i < ST; ++i) {
-      mbar_init(&full[i], TC_PWARPS);
+      mbar_init(&full[i], 2);  // a warp of K, one of V
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < C::QB; ++i) {
@@ -181,9 +182,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       mbar_init(&pv_done[i], 1);
       keep_first[i] = 0;
     }
-    mbar_init(&clean, 128);
-    mbar_init(&stored[0], 128);
-    mbar_init(&stored[1], 128);
+    for (int i = 0; i < GROUPS; ++i) mbar_init(&clean[i], 128);
+    mbar_init(&stored[0], GROUPS * 128);
+    mbar_init(&stored[1], GROUPS * 128);
     fence_mbar_init();
     prefetch_tensormap(&kmap);
     prefetch_tensormap(&vmap);
@@ -192,8 +193,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   const int G = p.Hq / p.Hkv;
   Shares sh;
   Cursor<TOK, MQ, TC_ITEM_COST, TC_LEAST> c;
-  if (!begin_range<TC_THREADS>(p, G, start, sh, c)) return;
-  if (warp == 8) {
+  if (!begin_range<C::THREADS>(p, G, start, sh, c)) return;
+  if (warp == SW + 4) {
     tmem_alloc(&tmem_slot, C::COLS);
     tmem_relinquish();
   }
@@ -202,7 +203,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   tc_fence_after();
   // after the allocation: a dependent grid's CTA cannot hold the columns this one waits for
   griddep_launch_dependents();
-  const uint32_t tmem = tmem_slot, o_tmem = tmem, s_tmem = tmem + DP;
+  const uint32_t tmem = tmem_slot, o_tmem = tmem, s_tmem = tmem + GROUPS * DP;
   auto wait = [&](uint64_t *bar, int phase) {
     mbar_wait_bounded(bar, phase & 1, pl.status, &abort_flag, pl.wait_limit_ns);
   };
@@ -211,42 +212,87 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   // only neighbouring phases apart.
   auto wait_pv = [&](int i) { wait(&pv_done[i % TC_NS], i / TC_NS); };
 
-  if (warp >= 4 && warp < 8) {
+  if (warp >= SW && warp < SW + 4) {
     // ================================================================ K and V boxes
+    // K or V of every second stage. The pages of 32 blocks of `box` tokens are looked up in one
+    // step, a step ahead; the boxes leave from one thread with uniform operands. (With half of
+    // the tokens of every stage a warp, a look-up and a box a lane each time, the warps took
+    // 0.75 us a stage, however few bytes it had.)
+    constexpr int SLABS = RB / 128;
     const int pw = warp & 1;
-    const bool val = warp >= 6;
-    const BoxLane<RB, TOK, 2, true> boxes(min(p.box, TOK / AT_PWARPS), lane);
+    const bool val = warp >= SW + 2;
+    const CUtensorMap *map = val ? &vmap : &kmap;
+    const int lg = 31 - __clz(p.box), nb = TOK >> lg, per = 32 / nb;  // blocks, stages a step
     int k = 0;
     while (c.next(p, G)) {
       const int32_t *table = p.block_table + static_cast<long long>(c.s) * p.max_pages;
-      auto token0 = [&](int t) { return c.x.begin + t * TOK + pw * (TOK / AT_PWARPS); };
-      auto look_up = [&](int t) {
-        const int j = token0(t) + boxes.block * boxes.box;
-        return t < c.t1 && j < c.x.len && boxes.has ? table[j / p.c.page_size] : -1;
+      // lane: block lane % nb of the stage 2 (lane / nb) on from `from`: its page and the
+      // block's place in it
+      auto look_up = [&](int from, int &page, int &off) {
+        const int t = from + lane / nb * 2;
+        page = -1;
+        off = 0;
+        if (t < c.t1) {
+          const int j = c.x.begin + t * TOK + ((lane & (nb - 1)) << lg);
+          if (j < c.x.len) {
+            const int i = j / p.c.page_size;
+            off = j - i * p.c.page_size;
+            page = table[i];
+          }
+        }
       };
-      int page = look_up(c.t0), ahead = look_up(c.t0 + 1);
-      for (int t = c.t0; t < c.t1; ++t, ++k) {
-        const int st = k % ST;
-        if (k >= ST) wait(&empty[st], k / ST - 1);
-        boxes.issue(val ? &vmap : &kmap, nullptr, p.c, smem_u32(ring + st * C::STAGE) +
-                    (val ? TOK * RB : 0), &full[st], val ? nullptr : stage_valid[st], pw, lane,
-                    token0(t), c.x.len, c.hk, page);
-        page = ahead;
-        ahead = look_up(t + 2);
+      int t = c.t0 + ((k ^ pw) & 1), page, off, next_page, next_off;
+      look_up(t, page, off);
+      look_up(t + 2 * per, next_page, next_off);
+      while (t < c.t1) {
+        const uint32_t exist = __ballot_sync(0xffffffffu, page >= 0 && page < p.c.num_pages);
+        for (int i = 0; i < per && t < c.t1; ++i, t += 2) {
+          const int at = k + t - c.t0, st = at % ST;
+          const uint32_t all = (1u << nb) - 1, blocks = exist >> (i * nb) & all;
+          const int left = c.x.len - c.x.begin - t * TOK;
+          uint64_t bits = ~0ull;  // the tokens that exist
+          if (blocks != all || left < TOK) {
+            bits = 0;
+            for (int b = 0; b < nb; ++b)
+              if (blocks >> b & 1) bits |= (~0ull >> (64 - p.box)) << (b << lg);
+            if (left < TOK) bits &= (1ull << left) - 1;
+          }
+          if (at >= ST) wait(&empty[st], at / ST - 1);
+          if (elect_one()) {
+            if (!val) stage_valid[st] = bits;
+            mbar_arrive_expect_tx(&full[st], __popc(blocks) * p.box * RB);
+          }
+          const uint32_t dst = smem_u32(ring + st * C::STAGE) + (val ? TOK * RB : 0);
+          for (int b = 0; b < nb; ++b) {
+            const int pg = __shfl_sync(0xffffffffu, page, i * nb + b);
+            const int o = __shfl_sync(0xffffffffu, off, i * nb + b);
+            if ((blocks >> b & 1) && elect_one()) {
+#pragma unroll
+              for (int slab = 0; slab < SLABS; ++slab)
+                tma_load_4d(dst + slab * (TOK * 128) + (b << lg) * 128, map, &full[st],
+                            slab * 64, o, c.hk, pg);
+            }
+            __syncwarp();
+          }
+        }
+        page = next_page;
+        off = next_off;
+        look_up(t + 2 * per, next_page, next_off);
       }
+      k += c.t1 - c.t0;
     }
     if (*static_cast<volatile int *>(&abort_flag) && lane == 0) {
       // after a time-out: boxes still on their way land before the CTA ends
       for (int i = max(k - ST, 0); i < k; ++i)
         mbar_wait_drain(&full[i % ST], (i / ST) & 1, 10000000ull);
     }
-  } else if (warp >= 10) {
+  } else if (warp >= SW + 6) {
     // ================================================================ rows of q
     // A thread has one 16-byte column of the head and every PER_PASS-th row.
     constexpr int CH = DP / 8, PER_PASS = TC_QTHREADS / CH;
-    const int at = tid - 10 * 32, ch = at % CH;
+    const int at = tid - (SW + 6) * 32, ch = at % CH;
     int seg = 0;
-    decltype(c) last;  // the segment before this one
+    decltype(c) last = c;  // the segment before this one
     // Its part, if it is one of several, is stored: count it. (Two barriers in turn: the softmax
     // can be one segment ahead of this warp, whose rows of q it needs for a second.)
     auto count = [&](int done) {
@@ -289,12 +335,12 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       }
       fence_proxy_async_smem();
       mbar_arrive(&qfull[qb]);
-      if (warp == 11 && seg > 0) count(seg - 1);
+      if (warp == SW + 7 && seg > 0) count(seg - 1);
       last = c;
       ++seg;
     }
-    if (warp == 11 && seg > 0) count(seg - 1);
-  } else if (warp == 8) {
+    if (warp == SW + 7 && seg > 0) count(seg - 1);
+  } else if (warp == SW + 4) {
     // ================================================================ products
     // S = Q . K^T
     const uint32_t id_s = idesc_bf16(TOK), q_u = smem_u32(at_smem), ring_u = smem_u32(ring);
@@ -336,7 +382,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       }
       ++seg;
     }
-  } else if (warp == 9) {
+  } else if (warp == SW + 5) {
     // O += P . V
     const uint32_t id_o = idesc_bf16(p.D) | (1u << 16), ring_u = smem_u32(ring);
     int k = 0;
@@ -346,15 +392,16 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         wait(&p_full[sb], k / TC_NS);
         tc_fence_after();
         const bool keep = *static_cast<volatile int *>(&keep_first[sb]) != 0;
-        const uint32_t acc = t > c.t0 || keep ? 1u : 0u;
+        const uint32_t acc = t >= c.t0 + GROUPS || keep ? 1u : 0u;
+        const uint32_t to = o_tmem + k % GROUPS * DP;
         const uint64_t v = sw128_mn_desc(ring_u + st * C::STAGE + TOK * RB, TOK * 128);
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < TOK / 16; ++kk)  // 16 tokens: 2048 bytes of V, 8 columns of P
-            tc_mma_ts(o_tmem, s_tmem + sb * 64 + kk * 8, v + (2048 >> 4) * kk, id_o,
+            tc_mma_ts(to, s_tmem + sb * 64 + kk * 8, v + (2048 >> 4) * kk, id_o,
                       kk > 0 ? 1u : acc);
-          // a segment's last stage is released after its join
-          if (t + 1 < c.t1) tc_commit(&empty[st]);
+          // a segment's (each group's) last stage is released after its join
+          if (t + GROUPS < c.t1) tc_commit(&empty[st]);
           tc_commit(&pv_done[sb]);
         }
         __syncwarp();
@@ -363,8 +410,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     if (k > 0) wait_pv(k - 1);  // nothing in flight when the columns are released
   } else {
     // ================================================================ softmax, a thread a lane
-    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-    const int copy = tid / MQ, r = tid % MQ, first_tok = copy * TS;
+    const int grp = warp >> 2, gt = tid & 127;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t my_o = o_tmem + grp * DP + lanes;
+    const int copy = gt / MQ, r = gt % MQ, first_tok = copy * TS;
     int k = 0, cleans = 0, segs = 0;
     while (c.next(p, G)) {
       const SeqInfo &x = c.x;
@@ -378,6 +427,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       const float zf = p.scale * LOG2E * (p.c.k_scale ? p.c.k_scale[c.hk] : 1.0f);
       float m = -INFINITY, l = 0.0f;  // m: the maximum that weights refer to
       for (int t = c.t0; t < c.t1; ++t, ++k) {
+        if (k % GROUPS != grp) continue;
         const int st = k % ST, sb = k % TC_NS;
         const uint32_t s_at = s_tmem + sb * 64 + lanes;
         wait(&s_full[sb], k / TC_NS);
@@ -388,7 +438,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
 #pragma unroll
           for (int i = 0; i < TS; i += 32) tmem_ld32(s_at + first_tok + i, z + i);
         wait(&full[st], k / ST);  // (long since) the copying warps' bits and the values
-        const uint64_t valid = stage_valid[st][0] | static_cast<uint64_t>(stage_valid[st][1]) << 32;
+        const uint64_t valid = stage_valid[st];
         const int j0 = x.begin + t * TOK;
         const bool plain = valid == ~0ull && j0 >= lo_all && j0 + TOK - 1 <= hi_all;
         tmem_wait_ld();
@@ -414,7 +464,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         float mx = least ? fminf(fminf(part[0], part[1]), fminf(part[2], part[3]))
                          : fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
         if (plain) mx *= zf;
-        const bool begins = t == c.t0;
+        const bool begins = t < c.t0 + GROUPS;
         if (begins) {
           m = mx;
         } else if (__any_sync(0xffffffffu, mx > m + TC_LAZY)) {
@@ -424,16 +474,16 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           const float fade = ex2(m - (m_new == -INFINITY ? 0.0f : m_new));
           m = m_new;
           l *= fade;
-          wait_pv(k - 1);
+          wait_pv(k - GROUPS);
           tc_fence_after();
           for (int d = 0; d < p.D; d += 16) {
             float o[16];
             uint32_t u[16];
-            tmem_ld16(o_tmem + lanes + d, o);
+            tmem_ld16(my_o + d, o);
             tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(o[e] * fade);
-            tmem_st16(o_tmem + lanes + d, u);
+            tmem_st16(my_o + d, u);
           }
           tmem_wait_st();
         }
@@ -503,12 +553,12 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           }
           __syncwarp();
           if (__any_sync(0xffffffffu, bad)) {
-            if (!begins) wait_pv(k - 1);
+            if (!begins) wait_pv(k - GROUPS);
             tc_fence_after();
             for (int d = 0; d < p.D; d += 16) {
               float o[16];
               uint32_t u[16];
-              tmem_ld16(o_tmem + lanes + d, o);
+              tmem_ld16(my_o + d, o);
               tmem_wait_ld();
 #pragma unroll
               for (int e = 0; e < 16; ++e) o[e] = begins ? 0.0f : o[e];
@@ -525,14 +575,14 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
               }
 #pragma unroll
               for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(o[e]);
-              tmem_st16(o_tmem + lanes + d, u);
+              tmem_st16(my_o + d, u);
             }
             tmem_wait_st();
             // every row has read the values (not a CTA barrier: this depends on data, and
             // after a time-out the warps may see different bytes)
-            mbar_arrive(&clean);
-            wait(&clean, cleans++);
-            for (int i = tid; i < TOK * (RB / 16); i += 128) {
+            mbar_arrive(&clean[grp]);
+            wait(&clean[grp], cleans++);
+            for (int i = gt; i < TOK * (RB / 16); i += 128) {
               uint4 *at = reinterpret_cast<uint4 *>(
                   v + swz<RB, TOK>(i / (RB / 16), i % (RB / 16)));
               uint4 y = *at;
@@ -546,80 +596,85 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           }
           fence_proxy_async_smem();  // before the product (and later boxes) touch the values
         }
-        if (tid == 0) keep_first[sb] = keep;
+        if (gt == 0) keep_first[sb] = keep;
         tc_fence_before();
         mbar_arrive(&p_full[sb]);
       }
 
-      // ---- the segment's outputs: the copies joined in the last stage's memory, half of the
-      // columns at a time (a row of DP / 2 floats a lane, 16-byte chunks permuted by the row)
-      const int last_st = (k - 1) % ST, me = blockIdx.x;
+      // ---- the segment's outputs: the copies joined in the memory of each group's last stage,
+      // half of the columns at a time (a row of DP / 2 floats a lane, 16-byte chunks permuted
+      // by the row). In a segment of one stage one group has none.
+      auto last_of = [&](int g) { return k - 1 - ((k - 1 - g) & (GROUPS - 1)); };  // or -1
+      const int my_last = last_of(grp), me = blockIdx.x;
+      const bool has = my_last >= k - (c.t1 - c.t0);
       const long long unit = c.item + TC_ITEM_COST;
       const int c0 = sh.worker_of(unit), c1 = sh.worker_of(unit + x.kt - 1);
       const ItemOut dst = {x.q0, row0, c.hk * G, G, p.c.v_scale ? p.c.v_scale[c.hk] : 1.0f};
       float *slot = pl.partials + static_cast<size_t>(part_slot(c0, me - c0)) * C::SLOT;
-      float *join = reinterpret_cast<float *>(ring + last_st * C::STAGE);
+      float *join[GROUPS];
+#pragma unroll
+      for (int g = 0; g < GROUPS; ++g)
+        join[g] = reinterpret_cast<float *>(ring + max(last_of(g), 0) % ST * C::STAGE);
       constexpr int HALF = DP / 2;
-      auto join_at = [&](int row, int chunk) {
-        return reinterpret_cast<float4 *>(join + row * HALF + ((chunk ^ (row & 7)) << 2));
+      auto join_at = [&](int g, int row, int chunk) {
+        return reinterpret_cast<float4 *>(join[g] + row * HALF + ((chunk ^ (row & 7)) << 2));
       };
       join_ml[tid][0] = m;
       join_ml[tid][1] = l;
-      named_bar_sync(1, 128);
+      named_bar_sync(1, GROUPS * 128);
       // a row's thread: the copies' factors (with the division, where the item ends here), and
       // the row's lse or (m, l)
-      float factor[C::COPIES];
+      float factor[C::PARTS];
       if (tid < n_rows) {
         float mr = -INFINITY, lr = 0.0f;
 #pragma unroll
-        for (int g = 0; g < C::COPIES; ++g) mr = fmaxf(mr, join_ml[g * MQ + tid][0]);
+        for (int g = 0; g < C::PARTS; ++g) mr = fmaxf(mr, join_ml[g * MQ + tid][0]);
         const float b = mr == -INFINITY ? 0.0f : mr;
 #pragma unroll
-        for (int g = 0; g < C::COPIES; ++g) {
+        for (int g = 0; g < C::PARTS; ++g) {
           factor[g] = ex2(join_ml[g * MQ + tid][0] - b);
           lr += factor[g] * join_ml[g * MQ + tid][1];
         }
         const int rr = row0 + tid, tok = rr / G;
-        row_off[tid] = (x.q0 + tok) * p.out_stride +
-                       static_cast<long long>(c.hk * G + rr - tok * G) * p.D;
+        row_tok[tid] = static_cast<uint8_t>(tok - row0 / G);
         if (c0 == c1) {
           dst.put_lse(p, tid, mr, lr);
           const float inv = lr == 0.0f ? 0.0f : dst.v_scale / lr;
 #pragma unroll
-          for (int g = 0; g < C::COPIES; ++g) factor[g] = lr == 0.0f ? 0.0f : factor[g] * inv;
+          for (int g = 0; g < C::PARTS; ++g) factor[g] = lr == 0.0f ? 0.0f : factor[g] * inv;
         } else {
           *reinterpret_cast<float2 *>(slot + MQ * DP + 2 * tid) = make_float2(mr, lr);
         }
 #pragma unroll
-        for (int g = 0; g < C::COPIES; ++g) join_ml[g * MQ + tid][0] = factor[g];
+        for (int g = 0; g < C::PARTS; ++g) join_ml[g * MQ + tid][0] = factor[g];
       }
-      wait_pv(k - 1);
+      if (has) wait_pv(my_last);
       tc_fence_after();
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
         const int d0 = half * HALF, width = min(HALF, p.D - d0);  // a multiple of 16, or none
         if (width <= 0) break;
-        for (int d = 0; d < width; d += 16) {
+        for (int d = 0; has && d < width; d += 16) {
           float o[16];
-          tmem_ld16(o_tmem + lanes + d0 + d, o);
+          tmem_ld16(my_o + d0 + d, o);
           tmem_wait_ld();
           if (r < n_rows) {
 #pragma unroll
             for (int e = 0; e < 16; e += 4)
-              *join_at(tid, (d + e) >> 2) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+              *join_at(grp, gt, (d + e) >> 2) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
           }
         }
         tc_fence_before();  // the next segment's products overwrite the columns
-        named_bar_sync(1, 128);
+        named_bar_sync(1, GROUPS * 128);
         const int cols = width / 4;
         auto store = [&](int row, int d) {
           const int col = d0 + 4 * d;
           float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-          for (int g = 0; g < C::COPIES; ++g) {
+          for (int g = 0; g < C::PARTS; ++g) {
             const float f = join_ml[g * MQ + row][0];
-            const float4 y = *join_at(g * MQ + row, d);
-            if (f != 0.0f) {  // a copy that saw nothing, a row that saw nothing
+            const float4 y = *join_at(g / C::COPIES, g % C::COPIES * MQ + row, d);
+            if (f != 0.0f) {  // a part that saw nothing, a row that saw nothing
               v.x += f * y.x;
               v.y += f * y.y;
               v.z += f * y.z;
@@ -630,33 +685,36 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             uint2 u;
             u.x = pack2<false>(v.x, v.y);
             u.y = pack2<false>(v.z, v.w);
-            *reinterpret_cast<uint2 *>(p.out + row_off[row] + col) = u;
+            const int tok = row0 / G + row_tok[row];
+            *reinterpret_cast<uint2 *>(p.out + (x.q0 + tok) * p.out_stride +
+                                       static_cast<long long>(c.hk * G + row0 + row - tok * G) *
+                                           p.D + col) = u;
           } else {
             *reinterpret_cast<float4 *>(slot + row * DP + col) = v;
           }
         };
         if (width == HALF) {  // no division at run time
 #pragma unroll 2
-          for (int i = tid; i < n_rows * (HALF / 4); i += 128)
+          for (int i = tid; i < n_rows * (HALF / 4); i += GROUPS * 128)
             store(i / (HALF / 4), i % (HALF / 4));
         } else {
-          for (int i = tid; i < n_rows * cols; i += 128) store(i / cols, i % cols);
+          for (int i = tid; i < n_rows * cols; i += GROUPS * 128) store(i / cols, i % cols);
         }
         fence_proxy_async_smem();  // before later boxes overwrite the join's stores
-        named_bar_sync(1, 128);
+        named_bar_sync(1, GROUPS * 128);
       }
-      if (tid == 0) mbar_arrive(&empty[last_st]);
-      // a split item's part is stored: warp 11 counts it, off the softmax's way
+      if (gt == 0 && has) mbar_arrive(&empty[my_last % ST]);
+      // a split item's part is stored: the last warp counts it, off the softmax's way
       mbar_arrive(&stored[segs++ & 1]);
     }
   }
   static_assert(ST * C::STAGE >= 2 * AT_GROUP * MQ * 8, "ml of a join");
-  run_joins<MQ, DP, TC_THREADS>(p, pl, reinterpret_cast<float2 *>(ring), pending, &n_pending,
+  run_joins<MQ, DP, C::THREADS>(p, pl, reinterpret_cast<float2 *>(ring), pending, &n_pending,
                                 &is_last);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 8) tmem_dealloc(tmem, C::COLS);
+  if (warp == SW + 4) tmem_dealloc(tmem, C::COLS);
 }
 
 template <int DP, int MQ>
@@ -667,7 +725,7 @@ cudaError_t launch_tc_shape(const AttnParams &p, void *ws, const AttnLaunch &a, 
                                              static_cast<int>(C::SMEM));
   if (e != cudaSuccess) return e;
   const int grid = a.num_sms;
-  return launch_pdl(kernel, dim3(grid), dim3(TC_THREADS), C::SMEM, s, a.kmap, a.vmap, p,
+  return launch_pdl(kernel, dim3(grid), dim3(C::THREADS), C::SMEM, s, a.kmap, a.vmap, p,
                     make_plan(ws, a));
 }
 
