@@ -576,7 +576,8 @@ __global__ void __launch_bounds__(AT_THREADS, (AttnCfg<E4M3, DP, NR, WR>::CTAS))
     const char *vbase = static_cast<const char *>(p.c.v);
     const BoxLane<RB, TOK, C::ES> boxes(p.box > 0 ? min(p.box, HALF) : HALF, lane);
     int k = 0, seg = 0;  // stages and segments so far
-    while (c.next(p, G)) {
+    bool go = true;      // until a time-out: no copy into a stage that may be in use
+    while (go && c.next(p, G)) {
       const int32_t *table = p.block_table + static_cast<long long>(c.s) * p.max_pages;
       // first token of this warp in stage t, and the page of the token (or box) a lane copies
       auto token0 = [&](int t) { return c.x.begin + t * TOK + pw * HALF; };
@@ -594,9 +595,11 @@ __global__ void __launch_bounds__(AT_THREADS, (AttnCfg<E4M3, DP, NR, WR>::CTAS))
       look_up(c.t0 + 1, ahead);
       for (int t = c.t0; t < c.t1; ++t, ++k) {
         const int st = k % ST, j0 = token0(t);
-        if (k >= ST)
-          mbar_wait_bounded(&empty[st], ((k / ST) - 1) & 1, pl.status, &abort_flag,
-                            pl.wait_limit_ns);
+        if (k >= ST) {
+          go = __all_sync(0xffffffffu, mbar_wait_bounded(&empty[st], ((k / ST) - 1) & 1, pl.status,
+                                                         &abort_flag, pl.wait_limit_ns));
+          if (!go) break;
+        }
         const uint32_t dst = smem_u32(at_smem + st * C::STAGE);
         if (p.box > 0) {
           boxes.issue(&kmap, &vmap, p.c, dst, &full[st], stage_valid[st], pw, lane, j0, c.x.len,

@@ -51,6 +51,11 @@ struct TcCfg {
   // One CTA an SM: with two, each ring would hold two stages beside Q's copies, and a stage
   // came every 2.2 us where the copy rate gives two in 1.45.
   static constexpr int ST = DP == 64 ? 8 : (DP == 128 ? 6 : 2);
+  // Warps that copy, each every CW-th stage. A wait for a stage's release tells only
+  // neighbouring phases apart: stage k - ST, which a warp has seen released when it comes to
+  // k + CW, has to be k + CW - 2 ST or later.
+  static constexpr int CW = ST < 3 ? 2 : 3;
+  static_assert(CW <= ST, "a copying warp must not run two rounds of the ring ahead");
   static constexpr int QB = DP == 64 ? 2 : 1;
   static constexpr size_t SMEM = QB * QBYTES + ST * STAGE;
   // softmax warpgroups, which take the stages in turn, each with outputs of its own
@@ -169,12 +174,12 @@ __global__ void __launch_bounds__((TcCfg<DP, MQ>::THREADS), 1)
     abort_flag = 0;
     n_pending = 0;
     for (int i = 0; i < ST; ++i) {
-      mbar_init(&full[i], 2);  // a warp of K, one of V
+      mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < C::QB; ++i) {
       mbar_init(&qfull[i], TC_QTHREADS);
-      mbar_init(&qempty[i], 1);
+      mbar_init(&qempty[i], 2);
     }
     for (int i = 0; i < TC_NS; ++i) {
       mbar_init(&s_full[i], 1);
@@ -205,31 +210,30 @@ __global__ void __launch_bounds__((TcCfg<DP, MQ>::THREADS), 1)
   griddep_launch_dependents();
   const uint32_t tmem = tmem_slot, o_tmem = tmem, s_tmem = tmem + GROUPS * DP;
   auto wait = [&](uint64_t *bar, int phase) {
-    mbar_wait_bounded(bar, phase & 1, pl.status, &abort_flag, pl.wait_limit_ns);
+    return mbar_wait_bounded(bar, phase & 1, pl.status, &abort_flag, pl.wait_limit_ns);
   };
   // Outputs of stage i added. As many barriers in turn as there are S: who waits for stage i
   // knows that i - TC_NS is done (the scores of i were issued after it), and a wait tells
   // only neighbouring phases apart.
+  int issued = 0;  // a copying warp's stages: one past its last
   auto wait_pv = [&](int i) { wait(&pv_done[i % TC_NS], i / TC_NS); };
 
-  if (warp >= SW && warp < SW + 4) {
+  if (warp >= SW && warp < SW + 3) {
     // ================================================================ K and V boxes
-    // K or V of every second stage. The pages of 32 blocks of `box` tokens are looked up in one
-    // step, a step ahead; the boxes leave from one thread with uniform operands. (With half of
-    // the tokens of every stage a warp, a look-up and a box a lane each time, the warps took
-    // 0.75 us a stage, however few bytes it had.)
+    // The pages of 32 blocks of `box` tokens are looked up in one step, a step ahead, and the
+    // boxes leave from one thread with uniform operands. (With half of the tokens of every
+    // stage a warp, a look-up and a box a lane each time, the warps took 0.75 us a stage,
+    // however few bytes it had.)
     constexpr int SLABS = RB / 128;
-    const int pw = warp & 1;
-    const bool val = warp >= SW + 2;
-    const CUtensorMap *map = val ? &vmap : &kmap;
     const int lg = 31 - __clz(p.box), nb = TOK >> lg, per = 32 / nb;  // blocks, stages a step
     int k = 0;
-    while (c.next(p, G)) {
+    bool go = warp - SW < C::CW;  // until a time-out: no box into a stage that may be in use
+    while (go && c.next(p, G)) {
       const int32_t *table = p.block_table + static_cast<long long>(c.s) * p.max_pages;
-      // lane: block lane % nb of the stage 2 (lane / nb) on from `from`: its page and the
-      // block's place in it
+      // lane: block lane % nb of the (lane / nb)-th of this warp's stages from `from` on: its
+      // page and the block's place in it
       auto look_up = [&](int from, int &page, int &off) {
-        const int t = from + lane / nb * 2;
+        const int t = from + lane / nb * C::CW;
         page = -1;
         off = 0;
         if (t < c.t1) {
@@ -241,12 +245,13 @@ __global__ void __launch_bounds__((TcCfg<DP, MQ>::THREADS), 1)
           }
         }
       };
-      int t = c.t0 + ((k ^ pw) & 1), page, off, next_page, next_off;
+      int t = c.t0 + (warp - SW + C::CW - k % C::CW) % C::CW;
+      int page, off, next_page, next_off;
       look_up(t, page, off);
-      look_up(t + 2 * per, next_page, next_off);
-      while (t < c.t1) {
+      look_up(t + C::CW * per, next_page, next_off);
+      while (go && t < c.t1) {
         const uint32_t exist = __ballot_sync(0xffffffffu, page >= 0 && page < p.c.num_pages);
-        for (int i = 0; i < per && t < c.t1; ++i, t += 2) {
+        for (int i = 0; i < per && t < c.t1; ++i, t += C::CW) {
           const int at = k + t - c.t0, st = at % ST;
           const uint32_t all = (1u << nb) - 1, blocks = exist >> (i * nb) & all;
           const int left = c.x.len - c.x.begin - t * TOK;
@@ -257,34 +262,35 @@ __global__ void __launch_bounds__((TcCfg<DP, MQ>::THREADS), 1)
               if (blocks >> b & 1) bits |= (~0ull >> (64 - p.box)) << (b << lg);
             if (left < TOK) bits &= (1ull << left) - 1;
           }
-          if (at >= ST) wait(&empty[st], at / ST - 1);
-          if (elect_one()) {
-            if (!val) stage_valid[st] = bits;
-            mbar_arrive_expect_tx(&full[st], __popc(blocks) * p.box * RB);
+          if (at >= ST) {
+            go = __all_sync(0xffffffffu, wait(&empty[st], at / ST - 1));
+            if (!go) break;
           }
-          const uint32_t dst = smem_u32(ring + st * C::STAGE) + (val ? TOK * RB : 0);
+          issued = at + 1;
+          if (elect_one()) {
+            stage_valid[st] = bits;
+            mbar_arrive_expect_tx(&full[st], __popc(blocks) * p.box * 2 * RB);
+          }
+          const uint32_t dst = smem_u32(ring + st * C::STAGE);
           for (int b = 0; b < nb; ++b) {
             const int pg = __shfl_sync(0xffffffffu, page, i * nb + b);
             const int o = __shfl_sync(0xffffffffu, off, i * nb + b);
             if ((blocks >> b & 1) && elect_one()) {
 #pragma unroll
-              for (int slab = 0; slab < SLABS; ++slab)
-                tma_load_4d(dst + slab * (TOK * 128) + (b << lg) * 128, map, &full[st],
-                            slab * 64, o, c.hk, pg);
+              for (int slab = 0; slab < SLABS; ++slab) {
+                const uint32_t to = dst + slab * (TOK * 128) + (b << lg) * 128;
+                tma_load_4d(to, &kmap, &full[st], slab * 64, o, c.hk, pg);
+                tma_load_4d(to + TOK * RB, &vmap, &full[st], slab * 64, o, c.hk, pg);
+              }
             }
             __syncwarp();
           }
         }
         page = next_page;
         off = next_off;
-        look_up(t + 2 * per, next_page, next_off);
+        look_up(t + C::CW * per, next_page, next_off);
       }
       k += c.t1 - c.t0;
-    }
-    if (*static_cast<volatile int *>(&abort_flag) && lane == 0) {
-      // after a time-out: boxes still on their way land before the CTA ends
-      for (int i = max(k - ST, 0); i < k; ++i)
-        mbar_wait_drain(&full[i % ST], (i / ST) & 1, 10000000ull);
     }
   } else if (warp >= SW + 6) {
     // ================================================================ rows of q
@@ -340,15 +346,18 @@ __global__ void __launch_bounds__((TcCfg<DP, MQ>::THREADS), 1)
       ++seg;
     }
     if (warp == SW + 7 && seg > 0) count(seg - 1);
-  } else if (warp == SW + 4) {
+  } else if (warp >= SW && warp < SW + 5) {
     // ================================================================ products
-    // S = Q . K^T
+    // S = Q . K^T, every second stage a warp (one warp took 0.45 us a stage of heads of 64)
+    const int qk = warp - SW - 3;
     const uint32_t id_s = idesc_bf16(TOK), q_u = smem_u32(at_smem), ring_u = smem_u32(ring);
     int k = 0, seg = 0;
     while (c.next(p, G)) {
       const int qb = seg % C::QB;
       wait(&qfull[qb], seg / C::QB);
+      const int last = c.t1 - 1 - ((k + c.t1 - c.t0 - 1 - qk) & 1);  // of this warp, or before t0
       for (int t = c.t0; t < c.t1; ++t, ++k) {
+        if ((k & 1) != qk) continue;
         const int st = k % ST;
         wait(&full[st], k / ST);
         if (k >= TC_NS) wait_pv(k - TC_NS);  // its S held that product's weights
@@ -376,10 +385,11 @@ __global__ void __launch_bounds__((TcCfg<DP, MQ>::THREADS), 1)
             b += 2;
           }
           tc_commit(&s_full[k % TC_NS]);
-          if (t + 1 == c.t1) tc_commit(&qempty[qb]);
+          if (t == last) tc_commit(&qempty[qb]);
         }
         __syncwarp();
       }
+      if (last < c.t0 && lane == 0) mbar_arrive(&qempty[qb]);
       ++seg;
     }
   } else if (warp == SW + 5) {
@@ -715,6 +725,11 @@ __global__ void __launch_bounds__((TcCfg<DP, MQ>::THREADS), 1)
   __syncthreads();
   tc_fence_after();
   if (warp == SW + 4) tmem_dealloc(tmem, C::COLS);
+  if (abort_flag && lane == 0) {
+    // after a time-out: boxes still on their way land before the CTA ends
+    for (int i = issued - 1; i >= 0 && i >= issued - ST; i -= C::CW)
+      mbar_wait_drain(&full[i % ST], (i / ST) & 1, 10000000ull);
+  }
 }
 
 template <int DP, int MQ>
