@@ -38,10 +38,10 @@ namespace {
 constexpr int TC_QTHREADS = 64;
 constexpr int TC_NS = 4;  // buffers of scores
 constexpr float TC_LAZY = 8.0f;
-// An item costs what six stages do: with a charge of one, 64 ragged sequences of 64 rows a kv
-// head take 205 us instead of 190, 9 sequences of 64 rows and 420 to 870 tokens 28.5 instead
-// of 21.1. A share is one stage of an item at least.
-constexpr int TC_ITEM_COST = 6, TC_LEAST = 7;
+// An item costs what eight stages do (64 ragged sequences: 64 rows a kv head 179 us, with a
+// charge of six 182, of one 200; 128 rows 241, 251 with six, 231 with twelve, at which 32 rows
+// and short sequences lose up to 1 us). A share is one stage of an item at least.
+constexpr int TC_ITEM_COST = 8, TC_LEAST = 9;
 
 template <int DP, int MQ>
 struct TcCfg {
@@ -313,7 +313,6 @@ __global__ void __launch_bounds__((TcCfg<DP, MQ>::THREADS), 1)
     };
     while (c.next(p, G)) {
       const int qb = seg % C::QB;
-      if (seg >= C::QB) wait(&qempty[qb], seg / C::QB - 1);
       const int n_rows = min(MQ, c.x.n * G - c.rt * MQ);
       uint8_t *qd = at_smem + qb * C::QBYTES;
       const uint16_t *head = p.q + static_cast<long long>(c.hk * G) * p.D + ch * 8;
@@ -329,6 +328,8 @@ __global__ void __launch_bounds__((TcCfg<DP, MQ>::THREADS), 1)
             v[e] = *reinterpret_cast<const uint4 *>(head + (c.x.q0 + tok) * p.q_stride + g * p.D);
           }
         }
+        // (the first rows are on their way while the last segment's products read the buffer)
+        if (r0 < PER_PASS && seg >= C::QB) wait(&qempty[qb], seg / C::QB - 1);
 #pragma unroll
         for (int e = 0; e < AHEAD; ++e) {
           const int r = r0 + e * PER_PASS;
@@ -664,14 +665,19 @@ __global__ void __launch_bounds__((TcCfg<DP, MQ>::THREADS), 1)
       for (int half = 0; half < 2; ++half) {
         const int d0 = half * HALF, width = min(HALF, p.D - d0);  // a multiple of 16, or none
         if (width <= 0) break;
-        for (int d = 0; has && d < width; d += 16) {
-          float o[16];
-          tmem_ld16(my_o + d0 + d, o);
-          tmem_wait_ld();
-          if (r < n_rows) {
+        if (has) {  // past D: columns that hold nothing, which nobody reads
+          constexpr int CHUNK = HALF < 64 ? HALF : 64;
+#pragma unroll 1
+          for (int d = 0; d < HALF; d += CHUNK) {
+            float o[CHUNK];
 #pragma unroll
-            for (int e = 0; e < 16; e += 4)
-              *join_at(grp, gt, (d + e) >> 2) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            for (int e = 0; e < CHUNK; e += 32) tmem_ld32(my_o + d0 + d + e, o + e);
+            tmem_wait_ld();
+            if (r < n_rows) {
+#pragma unroll
+              for (int e = 0; e < CHUNK; e += 4)
+                *join_at(grp, gt, (d + e) >> 2) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            }
           }
         }
         tc_fence_before();  // the next segment's products overwrite the columns
@@ -704,7 +710,7 @@ __global__ void __launch_bounds__((TcCfg<DP, MQ>::THREADS), 1)
           }
         };
         if (width == HALF) {  // no division at run time
-#pragma unroll 2
+#pragma unroll 4
           for (int i = tid; i < n_rows * (HALF / 4); i += GROUPS * 128)
             store(i / (HALF / 4), i % (HALF / 4));
         } else {
