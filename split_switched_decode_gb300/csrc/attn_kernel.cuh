@@ -83,6 +83,16 @@ struct AttnCfg {
   static_assert(STAGE >= AT_CWARPS * MW * DP * 4, "join buffer");
 };
 
+// True in one thread of the (converged) warp. Under this predicate the compiler knows that a
+// single thread issues the copies and products, whose operands are uniform registers; under
+// `lane == 0` it serialised them over the warp (125 clocks a product).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(yes));
+  return yes != 0;
+}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -316,42 +326,96 @@ __device__ __forceinline__ bool begin_range(const AttnParams &p, int G,
   return true;
 }
 
-// A copying warp's boxes of one stage: HALF tokens of K and V, lane -> (block of `box` tokens,
-// slab of 128 bytes, K or V), at most 32 boxes.
-template <int RB, int TOK, int ES>
-struct BoxLane {
-  static constexpr int HALF = TOK / AT_PWARPS, WORDS = HALF / 32;
+// What a copying warp brings of a stage by TMA: HALF tokens of K and V in blocks of `box` tokens
+// of one page. The pages of 32 blocks are looked up in one step, a step ahead, and the boxes
+// leave from one thread with uniform operands. (With a look-up each stage and a box a lane, a
+// warp took 0.6 us a stage, however few bytes it had: 64 ragged sequences with heads of 64
+// and pages of 16 tokens took 100 us instead of 88.) Its loops stay loops: unrolled, their
+// instructions crowd out the multiplying warps' (e4m3 heads of 256: 113 us instead of 107).
+template <int RB, int TOK, int HALF, int ES>
+struct Boxes {
   static constexpr int SLABS = RB == 64 ? 1 : RB / 128, ROW = RB == 64 ? 64 : 128;
-  static constexpr int PER_BLOCK = 2 * SLABS;
-  int box, block, slab;
-  bool has;
-  __device__ __forceinline__ BoxLane(int tokens, int lane)
-      : box(tokens), block(lane / PER_BLOCK), slab((lane >> 1) % SLABS),
-        has(block * tokens < HALF) {}
-  // Into stage memory `dst` (K, then V TOK * RB bytes on); j0: the warp's first token, at
-  // most `len` of the sequence exist; `page` the page of this lane's block, < 0 for none.
-  // Writes the bits of the tokens that exist and arrives on `full` with the bytes to come.
-  __device__ __forceinline__ void issue(const CUtensorMap *kmap, const CUtensorMap *vmap,
-                                        const PagedCache &cache, uint32_t dst, uint64_t *full,
-                                        uint32_t *valid_words, int pw, int lane, int j0, int len,
-                                        int hk, int page) const {
-    const bool ok = page >= 0 && page < cache.num_pages;
-    const uint32_t blocks = __ballot_sync(0xffffffffu, ok);
-#pragma unroll
-    for (int q = 0; q < WORDS; ++q) {
-      const int tok = q * 32 + lane;
-      const uint32_t valid = __ballot_sync(
-          0xffffffffu, (blocks >> (tok / box * PER_BLOCK) & 1) && j0 + tok < len);
-      if (lane == 0) valid_words[pw * WORDS + q] = valid;
+  int lg, nb, per;  // log2 of the box, blocks of a stage, stages of a step
+  int page, off, next_page, next_off;  // lane: block lane % nb of the step's stage lane / nb
+  uint32_t exist;                      // blocks whose page exists
+  __device__ __forceinline__ explicit Boxes(int box) {
+    lg = 31 - __clz(box);
+    nb = HALF >> lg;
+    per = 32 / nb;
+  }
+  template <typename Cur>
+  __device__ __forceinline__ void look_up(const AttnParams &p, const Cur &c, int from, int pw,
+                                          int lane, int &pg, int &of) const {
+    const int t = from + lane / nb;
+    pg = -1;
+    of = 0;
+    if (t < c.t1) {
+      const int j = c.x.begin + t * TOK + pw * HALF + ((lane & (nb - 1)) << lg);
+      if (j < c.x.len) {
+        const int i = j / p.c.page_size;
+        of = j - i * p.c.page_size;
+        pg = p.block_table[static_cast<long long>(c.s) * p.max_pages + i];
+        if (pg >= p.c.num_pages) pg = -1;
+      }
     }
-    if (lane == 0) mbar_arrive_expect_tx(full, __popc(blocks) * box * ROW);
-    __syncwarp();
-    if (ok) {
-      const bool val = lane & 1;
-      tma_load_4d(dst + (val ? TOK * RB : 0) + slab * (TOK * 128) +
-                      (pw * HALF + block * box) * ROW,
-                  val ? vmap : kmap, full, slab * (128 / ES),
-                  (j0 + block * box) % cache.page_size, hk, page);
+  }
+  // At each stage of a segment in turn, before issue().
+  template <typename Cur>
+  __device__ __forceinline__ void step(const AttnParams &p, const Cur &c, int t, int pw,
+                                       int lane) {
+    const int i = (t - c.t0) & (per - 1);
+    if (i == 0) {
+      if (t == c.t0) {
+        look_up(p, c, t, pw, lane, page, off);
+      } else {
+        page = next_page;
+        off = next_off;
+      }
+      exist = __ballot_sync(0xffffffffu, page >= 0);
+    }
+  }
+  // After issue(): the next step's pages.
+  template <typename Cur>
+  __device__ __forceinline__ void ahead(const AttnParams &p, const Cur &c, int t, int pw,
+                                        int lane) {
+    if (((t - c.t0) & (per - 1)) == 0) look_up(p, c, t + per, pw, lane, next_page, next_off);
+  }
+  // The boxes of stage t into stage memory `dst` (K, then V TOK * RB bytes on). Writes the
+  // bits of the tokens that exist and arrives on `full` with the bytes to come.
+  template <typename Cur>
+  __device__ __forceinline__ void issue(const CUtensorMap *kmap, const CUtensorMap *vmap,
+                                        const Cur &c, int t, int pw, uint32_t dst,
+                                        uint64_t *full, uint32_t *valid) const {
+    const int i = (t - c.t0) & (per - 1);
+    const uint32_t all = (1u << nb) - 1, blocks = exist >> (i * nb) & all;
+    const int left = c.x.len - c.x.begin - t * TOK - pw * HALF;
+    uint64_t bits = ~0ull;
+    if (blocks != all || left < HALF) {
+      bits = 0;
+#pragma unroll 1
+      for (int b = 0; b < nb; ++b)
+        if (blocks >> b & 1) bits |= (~0ull >> (64 - (1 << lg))) << (b << lg);
+      if (left < HALF) bits &= (1ull << max(left, 0)) - 1;
+    }
+    if (elect_one()) {
+#pragma unroll
+      for (int w = 0; w < HALF / 32; ++w)
+        valid[pw * (HALF / 32) + w] = static_cast<uint32_t>(bits >> (32 * w));
+      mbar_arrive_expect_tx(full, __popc(blocks) * (2 * SLABS * ROW << lg));
+    }
+#pragma unroll 1
+    for (int b = 0; b < nb; ++b) {
+      const int pg = __shfl_sync(0xffffffffu, page, i * nb + b);
+      const int of = __shfl_sync(0xffffffffu, off, i * nb + b);
+      if ((blocks >> b & 1) && elect_one()) {
+#pragma unroll
+        for (int slab = 0; slab < SLABS; ++slab) {
+          const uint32_t to = dst + slab * (TOK * 128) + (pw * HALF + (b << lg)) * ROW;
+          tma_load_4d(to, kmap, full, slab * (128 / ES), of, c.hk, pg);
+          tma_load_4d(to + TOK * RB, vmap, full, slab * (128 / ES), of, c.hk, pg);
+        }
+      }
+      __syncwarp();
     }
   }
 };
@@ -574,27 +638,26 @@ __global__ void __launch_bounds__(AT_THREADS, (AttnCfg<E4M3, DP, NR, WR>::CTAS))
     const int pw = warp - AT_CWARPS;
     const char *kbase = static_cast<const char *>(p.c.k);
     const char *vbase = static_cast<const char *>(p.c.v);
-    const BoxLane<RB, TOK, C::ES> boxes(p.box > 0 ? min(p.box, HALF) : HALF, lane);
+    Boxes<RB, TOK, HALF, C::ES> boxes(p.box > 0 ? p.box : HALF);
     int k = 0, seg = 0;  // stages and segments so far
     bool go = true;      // until a time-out: no copy into a stage that may be in use
     while (go && c.next(p, G)) {
       const int32_t *table = p.block_table + static_cast<long long>(c.s) * p.max_pages;
-      // first token of this warp in stage t, and the page of the token (or box) a lane copies
+      // 16-byte copies: first token of this warp in stage t, and the page of a lane's token
       auto token0 = [&](int t) { return c.x.begin + t * TOK + pw * HALF; };
       int page[WORDS], ahead[WORDS];  // of this stage and the next
       auto look_up = [&](int t, int (&to)[WORDS]) {
 #pragma unroll
         for (int q = 0; q < WORDS; ++q) {
-          const int j = token0(t) + (p.box > 0 ? boxes.block * boxes.box : q * 32 + lane);
-          to[q] = t < c.t1 && j < c.x.len && (p.box == 0 || (boxes.has && q == 0))
-                        ? table[j / p.c.page_size]
-                        : -1;
+          const int j = token0(t) + q * 32 + lane;
+          to[q] = p.box == 0 && t < c.t1 && j < c.x.len ? table[j / p.c.page_size] : -1;
         }
       };
       look_up(c.t0, page);
       look_up(c.t0 + 1, ahead);
       for (int t = c.t0; t < c.t1; ++t, ++k) {
         const int st = k % ST, j0 = token0(t);
+        if (p.box > 0) boxes.step(p, c, t, pw, lane);
         if (k >= ST) {
           go = __all_sync(0xffffffffu, mbar_wait_bounded(&empty[st], ((k / ST) - 1) & 1, pl.status,
                                                          &abort_flag, pl.wait_limit_ns));
@@ -602,8 +665,8 @@ __global__ void __launch_bounds__(AT_THREADS, (AttnCfg<E4M3, DP, NR, WR>::CTAS))
         }
         const uint32_t dst = smem_u32(at_smem + st * C::STAGE);
         if (p.box > 0) {
-          boxes.issue(&kmap, &vmap, p.c, dst, &full[st], stage_valid[st], pw, lane, j0, c.x.len,
-                      c.hk, page[0]);
+          boxes.issue(&kmap, &vmap, c, t, pw, dst, &full[st], stage_valid[st]);
+          boxes.ahead(p, c, t, pw, lane);
         } else {
 #pragma unroll
           for (int q = 0; q < WORDS; ++q) {

@@ -66,16 +66,6 @@ struct TcCfg {
   static constexpr int SLOT = MQ * DP + 2 * MQ;
 };
 
-// True in one thread of the (converged) warp. Under this predicate the compiler knows that a
-// single thread issues the tensor-core instructions, whose operands are uniform registers;
-// under `lane == 0` it serialised them over the warp (125 clocks a product).
-__device__ __forceinline__ bool elect_one() {
-  uint32_t yes;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(yes));
-  return yes != 0;
-}
 // D[tmem] (+)= A[tmem] * B[smem], bf16, fp32 accumulate; one thread issues.
 __device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
                                           uint32_t idesc, uint32_t accumulate) {
@@ -258,6 +248,7 @@ __global__ void __launch_bounds__((TcCfg<DP, MQ>::THREADS), 1)
           uint64_t bits = ~0ull;  // the tokens that exist
           if (blocks != all || left < TOK) {
             bits = 0;
+#pragma unroll 1
             for (int b = 0; b < nb; ++b)
               if (blocks >> b & 1) bits |= (~0ull >> (64 - p.box)) << (b << lg);
             if (left < TOK) bits &= (1ull << left) - 1;
@@ -272,6 +263,7 @@ __global__ void __launch_bounds__((TcCfg<DP, MQ>::THREADS), 1)
             mbar_arrive_expect_tx(&full[st], __popc(blocks) * p.box * 2 * RB);
           }
           const uint32_t dst = smem_u32(ring + st * C::STAGE);
+#pragma unroll 1
           for (int b = 0; b < nb; ++b) {
             const int pg = __shfl_sync(0xffffffffu, page, i * nb + b);
             const int o = __shfl_sync(0xffffffffu, off, i * nb + b);
