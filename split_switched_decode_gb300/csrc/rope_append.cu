@@ -15,14 +15,32 @@ __device__ __forceinline__ uint8_t to_e4m3(float x) {
   return static_cast<uint8_t>(__nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3));
 }
 
-// magnitude * (cos, sin) of position * frequency. The turn count is reduced in double
-// precision (a fp32 product at position 131072 is off by up to 0.004 radians).
+// magnitude * (cos, sin) of position * frequency. The turns, position * frequency / (2 pi), are
+// taken modulo one in integers of 2^-64 turns: exact but for position * 2^-64 turns and
+// position * frequency * 2^-65, where a fp32 product at position 131072 is off by up to 0.004
+// radians. (In double precision the rows of a prompt waited for its few units: 57.4 us for
+// 8192 rows instead of 55.8.)
 __device__ __forceinline__ float2 rope_angle(int pos, float freq, float magnitude) {
-  const double turns = static_cast<double>(pos) * static_cast<double>(freq) *
-                       0.15915494309189533576888376337251;  // 1 / (2 pi)
-  const float r = static_cast<float>(turns - rint(turns));  // [-1/2, 1/2]
+  constexpr uint64_t PER_RADIAN = 2935890503282001226ull;  // 2^64 / (2 pi)
+  const uint32_t bits = __float_as_uint(freq), exponent = bits >> 23 & 255;
+  const uint32_t mant = (bits & 0x7fffffu) | (exponent ? 0x800000u : 0u);
+  // mant * PER_RADIAN, a point `shift` bits from the right: the turns of a step
+  const uint64_t lo = mant * PER_RADIAN, hi = __umul64hi(mant, PER_RADIAN);
+  const int shift = 150 - static_cast<int>(exponent ? exponent : 1u);
+  uint64_t step;
+  if (shift > 0 && shift < 64)
+    step = lo >> shift | hi << (64 - shift);
+  else if (shift >= 64)
+    step = shift < 128 ? hi >> (shift - 64) : 0;
+  else
+    step = shift > -64 ? lo << -shift : 0;
+  if (bits >> 31) step = 0 - step;
+  const int64_t turns = static_cast<int64_t>(step * static_cast<uint64_t>(
+                                                        static_cast<int64_t>(pos)));
+  float r = static_cast<float>(turns) * 0x1p-63f;  // in half turns, [-1, 1]
+  if (exponent == 255) r = freq - freq;            // not finite
   float s, c;
-  sincospif(2.0f * r, &s, &c);
+  sincospif(r, &s, &c);
   return make_float2(c * magnitude, s * magnitude);
 }
 
@@ -82,9 +100,12 @@ __device__ __forceinline__ void put8(const void *base, const float *scale, int h
 // bounds it, the launch's latency when rows are few. A thread's unit is a chunk of 8
 // elements with its partner half the rotary part away (half pairs), or alone (interleaved
 // pairs, elements that stay, values), so every thread owns what it overwrites and q_out may
-// be q. The row's angles are computed once per CTA into shared memory (FP64 is scarce: 2
-// multiply-adds a clock and SM) while the first unit's elements are on their way. Rows with
-// many CTAs to spare are cut over gridDim.y so that a thread has one unit.
+// be q. The row's angles are computed once per CTA into shared memory while the first unit's
+// elements are on their way. Rows with many CTAs to spare are cut over gridDim.y so that a
+// thread has one unit. Measured: 64 + 2 * 8 heads of 128, 8192 rows (335 MB read and written)
+// in 55.8 us, 6.0 TB/s, where a plain copy reaches 6.76; the rest is the starts of 8192 CTAs:
+// a second CTA a row costs 4.5 us more, so do 192 threads, 256 cost 8. 512 rows into an e4m3
+// cache take 4.3 us, one row 2.2.
 template <bool E4M3, bool INTER>
 __global__ void __launch_bounds__(RA_THREADS) rope_append_kernel(const RopeParams p) {
   __shared__ float2 cs[ATTN_MAX_D / 2];
