@@ -9,7 +9,6 @@ namespace ssd {
 namespace {
 
 constexpr int RA_THREADS = 128;
-constexpr float E4M3_MAX = 448.0f;
 
 __device__ __forceinline__ uint8_t to_e4m3(float x) {
   return static_cast<uint8_t>(__nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3));
@@ -99,90 +98,86 @@ __device__ __forceinline__ void put8(const void *base, const float *scale, int h
 // 16 bytes a thread. Read once and written once, 2 to 3 operations an element: the copy rate
 // bounds it, the launch's latency when rows are few. A thread's unit is a chunk of 8
 // elements with its partner half the rotary part away (half pairs), or alone (interleaved
-// pairs, elements that stay, values), so every thread owns what it overwrites and q_out may
+// pairs, elements that stay), so every thread owns what it overwrites and q_out may
 // be q. The row's angles are computed once per CTA into shared memory while the first unit's
 // elements are on their way. Rows with many CTAs to spare are cut over gridDim.y so that a
 // thread has one unit. Measured: 64 + 2 * 8 heads of 128, 8192 rows (335 MB read and written)
-// in 55.8 us, 6.0 TB/s, where a plain copy reaches 6.76; the rest is the starts of 8192 CTAs:
-// a second CTA a row costs 4.5 us more, so do 192 threads, 256 cost 8. 512 rows into an e4m3
-// cache take 4.3 us, one row 2.2.
+// in 54.8 us, 6.1 TB/s, where a plain copy reaches 6.76; the rest is the starts of 8192 CTAs:
+// a second CTA a row costs 4 us more, 192 threads a row 6 (96: the same, but 1 us more for
+// 1000 rows). 512 rows into an e4m3 cache take 3.9 us, one row 2.1.
 template <bool E4M3, bool INTER>
 __global__ void __launch_bounds__(RA_THREADS) rope_append_kernel(const RopeParams p) {
   __shared__ float2 cs[ATTN_MAX_D / 2];
   griddep_wait();
   griddep_launch_dependents();
   const int t = blockIdx.x, half = p.rot / 2;
-  // units of a q or k head: rotary pairs of chunks (half pairs) or chunks, then the rest
+  // units of a head: rotary pairs of chunks (half pairs) or chunks, then the rest; values are
+  // cut like the other heads
   const int turning = INTER ? p.rot / 8 : p.rot / 16;
-  const int per_head = turning + (p.D - p.rot) / 8, per_value = p.D / 8;
-  const int qk = (p.Hq + p.Hkv) * per_head, units = qk + p.Hkv * per_value;
+  const int per_head = turning + (p.D - p.rot) / 8, heads = p.Hq + 2 * p.Hkv;
   struct Unit {
     int h, d0, d1;  // head counted over q, k, v; first element, partner's (or -1)
     bool turns;
-  };
-  auto unit_of = [&](int u) {
-    Unit x;
-    if (u < qk) {
-      x.h = u / per_head;
-      const int i = u - x.h * per_head;
-      x.turns = i < turning;
-      x.d0 = x.turns || INTER ? 8 * i : p.rot + 8 * (i - turning);
-      x.d1 = x.turns && !INTER ? half + 8 * i : -1;
-    } else {
-      const int i = (u - qk) / per_value;
-      x.h = p.Hq + p.Hkv + i;
-      x.d0 = 8 * (u - qk - i * per_value);
-      x.d1 = -1;
-      x.turns = false;
-    }
-    return x;
   };
   auto source = [&](int h) {
     return h < p.Hq ? p.q + t * p.q_stride + h * p.D
            : h < p.Hq + p.Hkv ? p.k + t * p.k_stride + (h - p.Hq) * p.D
                               : p.v + t * p.v_stride + (h - p.Hq - p.Hkv) * p.D;
   };
-  const int step = gridDim.y * RA_THREADS;
-  int u = blockIdx.y * RA_THREADS + threadIdx.x;
+  // this thread's units, every `step`-th: head h, unit i of it (no division on the way)
+  const int step = gridDim.y * RA_THREADS, u = blockIdx.y * RA_THREADS + threadIdx.x;
+  const int step_h = step / per_head, step_i = step - step_h * per_head;
+  int h = u / per_head, i = u - h * per_head;
   // a unit's elements are requested one unit before they are used
   Unit next = {};
   uint4 next_a = {}, next_b = {};
   auto load = [&]() {
-    next = unit_of(u);
+    const bool paired = i < turning;
+    next.h = h;
+    next.d0 = paired || INTER ? 8 * i : p.rot + 8 * (i - turning);
+    next.d1 = paired && !INTER ? half + 8 * i : -1;
+    next.turns = paired && h < p.Hq + p.Hkv;
     const uint16_t *src = source(next.h);
     next_a = *reinterpret_cast<const uint4 *>(src + next.d0);
     if (next.d1 >= 0) next_b = *reinterpret_cast<const uint4 *>(src + next.d1);
+    h += step_h;
+    i += step_i;
+    if (i >= per_head) {
+      i -= per_head;
+      ++h;
+    }
   };
-  if (u < units) load();
+  bool more = h < heads;
+  if (more) load();
   const RowPlace place = row_place(p, t);
   if (threadIdx.x < half) {
     const int pos = p.positions[t];
-    for (int i = threadIdx.x; i < half; i += RA_THREADS)
-      cs[i] = rope_angle(pos, p.inv_freq[i], p.magnitude);
+    for (int j = threadIdx.x; j < half; j += RA_THREADS)
+      cs[j] = rope_angle(pos, p.inv_freq[j], p.magnitude);
   }
   __syncthreads();
-  while (u < units) {
+  while (more) {
     const Unit x = next;
     float y0[8], y1[8];
     unpack8(next_a, y0);
     unpack8(next_b, y1);
-    u += step;
-    if (u < units) load();
+    more = h < heads;
+    if (more) load();
     if (x.turns && INTER) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 w = cs[x.d0 / 2 + i];
-        const float r = y0[2 * i] * w.x - y0[2 * i + 1] * w.y;
-        y0[2 * i + 1] = y0[2 * i + 1] * w.x + y0[2 * i] * w.y;
-        y0[2 * i] = r;
+      for (int e = 0; e < 4; ++e) {
+        const float2 w = cs[x.d0 / 2 + e];
+        const float r = y0[2 * e] * w.x - y0[2 * e + 1] * w.y;
+        y0[2 * e + 1] = y0[2 * e + 1] * w.x + y0[2 * e] * w.y;
+        y0[2 * e] = r;
       }
     } else if (x.turns) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float2 w = cs[x.d0 + i];
-        const float r = y0[i] * w.x - y1[i] * w.y;
-        y1[i] = y1[i] * w.x + y0[i] * w.y;
-        y0[i] = r;
+      for (int e = 0; e < 8; ++e) {
+        const float2 w = cs[x.d0 + e];
+        const float r = y0[e] * w.x - y1[e] * w.y;
+        y1[e] = y1[e] * w.x + y0[e] * w.y;
+        y0[e] = r;
       }
     }
     if (x.h < p.Hq) {
@@ -191,12 +186,12 @@ __global__ void __launch_bounds__(RA_THREADS) rope_append_kernel(const RopeParam
       if (x.d1 >= 0) *reinterpret_cast<uint4 *>(o + x.d1) = pack8(y1);
     } else if (place.stored) {
       const bool key = x.h < p.Hq + p.Hkv;
-      const int h = key ? x.h - p.Hq : x.h - p.Hq - p.Hkv;
+      const int to = key ? x.h - p.Hq : x.h - p.Hq - p.Hkv;
       const void *base = key ? p.c.k : p.c.v;
       const float *scale = key ? p.c.k_scale : p.c.v_scale;
-      const long long at = place.at + h * p.c.head_stride;
-      put8<E4M3>(base, scale, h, at + x.d0, y0);
-      if (x.d1 >= 0) put8<E4M3>(base, scale, h, at + x.d1, y1);
+      const long long at = place.at + to * p.c.head_stride;
+      put8<E4M3>(base, scale, to, at + x.d0, y0);
+      if (x.d1 >= 0) put8<E4M3>(base, scale, to, at + x.d1, y1);
     }
   }
 }
@@ -261,10 +256,8 @@ cudaError_t launch_rope_append(const RopeParams &p, bool e4m3, int num_sms, cuda
   const int heads = p.Hq + 2 * p.Hkv;
   // units of a row, and CTAs for one unit a thread while the row count alone does not give
   // every SM two CTAs
-  const int units = chunks ? (p.Hq + p.Hkv) *
-                                     ((p.interleaved ? p.rot / 8 : p.rot / 16) + (p.D - p.rot) / 8) +
-                                 p.Hkv * (p.D / 8)
-                           : heads * (p.D / 2);
+  const int turning = p.interleaved ? p.rot / 8 : p.rot / 16;
+  const int units = heads * (chunks ? turning + (p.D - p.rot) / 8 : p.D / 2);
   const int cuts = (units + RA_THREADS - 1) / RA_THREADS;
   const dim3 grid(p.T, p.T < 2 * num_sms ? cuts : 1);
   void (*kernel)(const RopeParams);
