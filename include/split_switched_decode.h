@@ -492,8 +492,8 @@ DEC_API dec_status rope_frequencies(int rot, double base, int scaling, double fa
  *
  * for pair i of the first `rot` elements of every q and k head: elements (2i, 2i+1) with
  * interleaved = 1, (i, i + rot/2) with interleaved = 0; elements rot..D-1 unchanged. The
- * angle is reduced in double precision, so positions up to 2^31 - 1 lose nothing; the
- * rotation is fp32 and rounds once. Writes q_out, and K (rotated) and V (as they are, or
+ * angle is reduced to a turn in 64-bit integers, so positions up to 2^31 - 1 lose nothing;
+ * the rotation is fp32 and rounds once. Writes q_out, and K (rotated) and V (as they are, or
  * both divided by their head's scale and saturated to +-448 for DEC_KV_E4M3) to slot
  * slots[t] of the cache. A slot below 0 or not below num_pages * page_size is not written.
  * Two rows with the same slot leave one of the two there.
@@ -525,7 +525,8 @@ DEC_API dec_status rope_append(const dec_bf16 *q, int64_t q_stride, const dec_bf
  *
  * A row that sees no key (or whose scores are all -infinity) gives out = 0 and
  * lse = -infinity. Keys whose page is not in 0..num_pages-1 are not seen. What stands in
- * the cache at a place that a row does not see, NaN included, does not reach that row.
+ * the cache at a place that a row does not see, NaN included, does not reach that row; a
+ * value that is not finite makes that element of the rows that see it infinite or NaN.
  *
  * q and out [T,Hq,D] with row strides in elements (multiples of 8, 16-byte aligned; out may
  * not overlap q); block_table int32 [S, max_pages]; seq_len int32 [S], the new tokens

@@ -26,7 +26,7 @@ AttnShape attn_shape(int rows) {
 
 // Rows of an item on tcgen05 tensor cores, 0 for the legacy products. Up to 16 rows those keep up
 // with the copies (16 rows, 64 ragged sequences: 166 us, on tcgen05 199 with pages of 16
-// tokens and 170 with 64; 32 rows: 226 and 182; 64 rows: 403 and 190).
+// tokens and 170 with 64; 32 rows: 226 and 172; 64 rows: 403 and 179).
 int tc_rows(int rows) { return rows <= 16 ? 0 : (rows <= 32 ? 32 : (rows <= 64 ? 64 : 128)); }
 
 // Tokens of a TMA box: the largest power of two in the page size, up to what a copying warp

@@ -34,8 +34,16 @@
 // to f16: exact but for elements 2^-14 below the row's largest. The key scale joins the
 // score's factor, the value scale the last division.
 //
-// Every wait on an mbarrier is bounded; after a time-out the waits return at once and the
-// control flow, which depends on the lengths alone, runs to its end over stale data.
+// Measured with 8 rows a kv head (64 sequences of 0 to 8192 tokens, 8 kv heads of 128, 1045 MB):
+// 162 us, 6.4 TB/s, where a plain copy moves 6.76; an e4m3 cache over 1024 to 16384 tokens
+// (951 MB) 150 us; one sequence of 131072 tokens (537 MB) 89 us. Short calls are chains of
+// latencies: one sequence of 777 tokens takes 9.7 us where its bytes take 0.1 (start and
+// lengths, the first stage from HBM, a stage or two of products, partial results, the
+// counter, the join).
+//
+// Every wait on an mbarrier is bounded; after a time-out the waits return at once, nothing
+// more is copied, and the control flow, which depends on the lengths alone, runs to its end
+// over stale data.
 #pragma once
 
 #include <cuda_fp16.h>

@@ -1,16 +1,18 @@
 // attn_tc.cu -- attention over a paged bf16 cache for many rows a kv head (verification rows,
 // wide groups) on tcgen05 tensor cores.
 //
-// The legacy matrix instructions of attn_kernel.cuh run at a sixteenth of the tcgen05 rate:
-// from 9 rows a kv head their products take longer than the keys' and values' way from HBM
-// (64 rows: 435 us where the copy takes 160). Here a stage of 64 tokens costs 512 clocks of
-// the tensor core for up to 128 rows, and copying bounds it again. Division of the work, ring
-// of stages and joins are attn_kernel.cuh's; one CTA an SM has twelve warps:
+// The warps of attn_kernel.cuh take a stage's tokens against 8 rows at a time, and above 16
+// rows these chains of small products, exponentials and shuffles take longer than the keys'
+// and values' way from HBM (64 rows, 64 ragged sequences: 403 us where the copy takes 160).
+// Here a stage of 64 tokens is two products for up to 128 rows, 512 clocks of the tensor
+// core, and copying bounds it again: 179 us, 6.1 TB/s (32 rows: 172 us; 128 rows: 236 us,
+// with twice the outputs to join and write). Division of the work, ring of stages and joins are
+// attn_kernel.cuh's; one CTA an SM has sixteen warps (twelve for heads above 128):
 //
-//   0-3  softmax: a thread a TMEM lane; MQ = 32, 64 or 128 rows an item
-//   4-7  TMA boxes into the ring
-//   8, 9 a thread each issues the products below (one thread for both took 1 us a stage)
-//  10-11 rows of q into shared memory
+//   4 or 8  softmax: a thread a TMEM lane; MQ = 32, 64 or 128 rows an item
+//   3       TMA boxes into the ring, each every third stage
+//   2 + 1   a thread each issues the products below, the scores' in turn
+//   2       rows of q into shared memory
 //
 //     S[rows, 64 tokens] = Q . K^T    A = Q, B = K, both K-major in shared memory (the boxes'
 //                                     128-byte swizzle is the operand layout)
@@ -19,16 +21,25 @@
 //
 // There are four S, and P (bf16) overwrites its S: scores run up to three stages ahead of the
 // softmax, outputs behind it (with two S the way from one stage's weights through its outputs
-// to the scores two stages on set the pace). M is 128 whatever the rows are: Q stands in
-// shared memory 128 / MQ times, and copy g of a row takes the softmax of the g-th part of
-// the stage's tokens with weights of zero for the others, a maximum, a sum and outputs of
-// its own, which are joined at the segment's end. So four warps share the exponentials at
-// any number of rows (with one copy and 32 rows a single warp took 2.4 us a stage, twice
-// what its bytes take).
+// to the scores two stages on set the pace). A stage's softmax is a chain of 900 to 1300 clocks
+// (wait, tensor memory, maximum, exponentials, tensor memory, arrival) where the copy of a
+// stage of heads of 64 takes 600: two groups of four warps take the stages in turn, each
+// with a maximum, a sum and outputs of its own (heads above 128: one group, as two outputs
+// and the scores exceed tensor memory). M is 128 whatever the rows are: Q stands in shared
+// memory 128 / MQ times, and copy g of a row takes the softmax of the g-th part of the
+// stage's tokens with weights of zero for the others, again with outputs of its own. All
+// are joined at the segment's end. So four warps share the exponentials at any number of
+// rows (with one copy and 32 rows a single warp took 2.4 us a stage, twice what its bytes
+// take).
 //
 // The running maximum that weights refer to is moved only when a row's maximum has grown by
-// more than 8 (weights then stay below 2^8, and their rounding to bf16 is relative), so the
-// outputs in tensor memory are rarely rescaled; sums refer to the same maximum.
+// more than 8 (weights then stay below 2^8, and their rounding to bf16, relative 2^-9 as the
+// output's own, is not enlarged), so the outputs in tensor memory are rarely rescaled; sums
+// are fp32 of the weights before rounding and refer to the same maximum.
+//
+// What is left over the copy: a segment's end (join, stores, the next item's first scores)
+// stops the copies for about 3 us, as the ring of six stages is what they need in flight;
+// at 64 rows a CTA has four or five ends in its share.
 #include "attn_kernel.cuh"
 #include "tcgen05.cuh"
 

@@ -58,7 +58,8 @@ __device__ __forceinline__ int last_at_most(const int *first, int n, int x) {
 // page, store) bound it. One CTA does it all, or with many rows a cluster of 8, each with
 // the sums of all sequences and an eighth of the rows. Everything that may be overwritten is
 // read before the (cluster's) barrier and the first output is written after it, so seq_len
-// may be kv_len and free_used part of summary.
+// may be kv_len and free_used part of summary. Measured in a graph: 64 sequences 4.0 us,
+// 512 prompts with 65 thousand rows 12.4 us (one CTA: 70).
 template <bool CLUSTER>
 __global__ void __launch_bounds__(KP_THREADS) kv_plan_kernel(const KvPlanParams p) {
   extern __shared__ int kp_smem[];
