@@ -161,7 +161,7 @@ __global__ void __launch_bounds__((TcCfg<DP, MQ>::THREADS), 1)
   __shared__ RangeStart<C::THREADS> start;
   __shared__ __align__(8) uint64_t full[ST], empty[ST], qfull[C::QB], qempty[C::QB];
   __shared__ __align__(8) uint64_t s_full[TC_NS], p_full[TC_NS];
-  __shared__ __align__(8) uint64_t pv_done[TC_NS], clean[GROUPS], stored[2];
+  __shared__ __align__(8) uint64_t pv_done[TC_NS], clean[GROUPS], stored[2], drained[3];
   __shared__ uint64_t stage_valid[ST];  // tokens of the stage that exist
   __shared__ PendingJoin pending[2];
   __shared__ uint32_t tmem_slot;
@@ -189,6 +189,7 @@ __global__ void __launch_bounds__((TcCfg<DP, MQ>::THREADS), 1)
       keep_first[i] = 0;
     }
     for (int i = 0; i < GROUPS; ++i) mbar_init(&clean[i], 128);
+    for (int i = 0; i < 3; ++i) mbar_init(&drained[i], 1);
     mbar_init(&stored[0], GROUPS * 128);
     mbar_init(&stored[1], GROUPS * 128);
     fence_mbar_init();
@@ -217,6 +218,13 @@ __global__ void __launch_bounds__((TcCfg<DP, MQ>::THREADS), 1)
   // knows that i - TC_NS is done (the scores of i were issued after it), and a wait tells
   // only neighbouring phases apart.
   int issued = 0;  // a copying warp's stages: one past its last
+  // After a time-out: an issuing warp's products end before tensor memory is released.
+  auto drain = [&](int i) {
+    if (!__any_sync(0xffffffffu, *static_cast<volatile int *>(&abort_flag))) return;
+    if (elect_one()) tc_commit(&drained[i]);
+    __syncwarp();
+    mbar_wait_drain(&drained[i], 0, 10000000ull);
+  };
   auto wait_pv = [&](int i) { wait(&pv_done[i % TC_NS], i / TC_NS); };
 
   if (warp >= SW && warp < SW + 3) {
@@ -396,6 +404,7 @@ __global__ void __launch_bounds__((TcCfg<DP, MQ>::THREADS), 1)
       if (last < c.t0 && lane == 0) mbar_arrive(&qempty[qb]);
       ++seg;
     }
+    drain(qk);
   } else if (warp == SW + 5) {
     // O += P . V
     const uint32_t id_o = idesc_bf16(p.D) | (1u << 16), ring_u = smem_u32(ring);
@@ -422,6 +431,7 @@ __global__ void __launch_bounds__((TcCfg<DP, MQ>::THREADS), 1)
       }
     }
     if (k > 0) wait_pv(k - 1);  // nothing in flight when the columns are released
+    drain(2);
   } else {
     // ================================================================ softmax, a thread a lane
     const int grp = warp >> 2, gt = tid & 127;
