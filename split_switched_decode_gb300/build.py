@@ -21,9 +21,10 @@ LIB_PATH = os.path.join(OUT_DIR, LIB_NAME)
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "gemv_tiny.cu", "engine_cc.cu", "engine_tc.cu", "moe_aux.cu",
            "front_fused.cu", "engine_pair.cu", "api_attn.cu", "kv_plan.cu", "rope_append.cu",
-           "attn_decode.cu", "attn_d64.cu", "attn_d128.cu", "attn_d256.cu", "attn_tc.cu"]
+           "attn_decode.cu", "attn_d64.cu", "attn_d128.cu", "attn_d256.cu", "attn_tc.cu",
+           "attn_tc_e4m3.cu"]
 HEADERS = ["common.cuh", "engine.cuh", "routing.cuh", "tcgen05.cuh", "internal.h", "attn.h",
-           "attn_kernel.cuh"]
+           "attn_kernel.cuh", "attn_tc.cuh"]
 
 
 def _nvcc() -> str:

@@ -71,6 +71,16 @@ struct AttnLaunch {
 // Workers (CTAs) of a launch at most, and the workspace's counters: one per worker for items,
 // two for groups of workers.
 inline int attn_max_workers(int num_sms) { return 2 * num_sms; }
+// Rows of an average sequence and kv head up to which the legacy products are taken, by the
+// cache type and the padded head. bf16: up to 16 rows those keep up with the copies (16 rows, 64
+// ragged sequences: 166 us, on tcgen05 199 with pages of 16 tokens and 170 with 64; 32
+// rows: 226 and 172; 64 rows: 403 and 179). e4m3, where tcgen05 needs widened operands
+// (legacy, tcgen05; 64 ragged sequences with 1 to 4, 1 to 8 or 1 to 16 new rows of 8 heads a
+// kv head): heads of 128 230 and 209 us with 4, 422 and 225 with 8; of 64 144 and 207 with
+// 4, 256 and 180 with 8; of 256 (20 sequences) 222 and 251 with 8, 413 and 245 with 16.
+constexpr int tc_min_rows(bool e4m3, int dp) {
+  return !e4m3 || dp == 128 ? 16 : (dp == 64 ? 32 : 48);
+}
 inline size_t attn_counter_bytes(int num_sms) {
   return (static_cast<size_t>(3) * attn_max_workers(num_sms) * sizeof(int) + 255) / 256 * 256;
 }
@@ -84,6 +94,8 @@ cudaError_t launch_attn_d256(const AttnParams &p, bool e4m3, int nr, int wr, voi
                              const AttnLaunch &a, cudaStream_t s);
 // attn_tc.cu: bf16 caches in boxes, items of 32, 64 or 128 rows.
 cudaError_t launch_attn_tc(const AttnParams &p, int padded, int rows, void *ws,
+                           const AttnLaunch &a, cudaStream_t s);
+cudaError_t launch_attn_tc_e4m3(const AttnParams &p, int padded, int rows, void *ws,
                            const AttnLaunch &a, cudaStream_t s);
 // api.cu: a 4-D map (head element, token of the page, kv head, page) of a cache, boxes of
 // 128 bytes (64 where a padded head has 64 bytes) x box tokens, swizzled accordingly.

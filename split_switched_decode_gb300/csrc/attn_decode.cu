@@ -24,10 +24,11 @@ AttnShape attn_shape(int rows) {
                                  : (rows <= 32 ? AttnShape{2, 2} : AttnShape{2, 4}));
 }
 
-// Rows of an item on tcgen05 tensor cores, 0 for the legacy products. Up to 16 rows those keep up
-// with the copies (16 rows, 64 ragged sequences: 166 us, on tcgen05 199 with pages of 16
-// tokens and 170 with 64; 32 rows: 226 and 172; 64 rows: 403 and 179).
-int tc_rows(int rows) { return rows <= 16 ? 0 : (rows <= 32 ? 32 : (rows <= 64 ? 64 : 128)); }
+// Rows of an item on tcgen05 tensor cores, 0 for the legacy products, `dp` the padded head.
+int tc_rows(bool e4m3, int dp, int rows) {
+  if (rows <= tc_min_rows(e4m3, dp)) return 0;
+  return rows <= 32 ? 32 : (rows <= 64 ? 64 : 128);
+}
 
 // Tokens of a TMA box: the largest power of two in the page size, up to what a copying warp
 // brings of a stage; below 8 (a swizzle group) none.
@@ -41,8 +42,9 @@ int box_tokens(int page_size, int most) {
 
 size_t attn_workspace_bytes(int S, int T, int Hq, int Hkv, int D, int num_sms) {
   const int dp = padded_dim(D), grid = dp <= 128 ? attn_max_workers(num_sms) : num_sms;
-  const int rows = mean_rows(S, T, Hq, Hkv);
-  const size_t M = tc_rows(rows) > 0 ? tc_rows(rows) : attn_shape(rows).rows();
+  const int rows = mean_rows(S, T, Hq, Hkv);  // of whichever kernel and cache type has more
+  const size_t tc = tc_rows(false, dp, rows);
+  const size_t M = tc > 0 ? tc : attn_shape(rows).rows();
   return attn_counter_bytes(num_sms) + 2 * grid * (M * dp + 2 * M) * sizeof(float);
 }
 
@@ -54,7 +56,7 @@ cudaError_t launch_attn_decode(const AttnParams &params, bool e4m3, void *ws, in
   a.status = status;
   a.wait_limit_ns = wait_limit_ns;
   const int dp = padded_dim(p.D);
-  const int rows = mean_rows(p.S, p.T, p.Hq, p.Hkv), tc = e4m3 ? 0 : tc_rows(rows);
+  const int rows = mean_rows(p.S, p.T, p.Hq, p.Hkv), tc = tc_rows(e4m3, dp, rows);
   p.box = box_tokens(p.c.page_size, e4m3 || tc > 0 ? 64 : 32);
   if (p.box > 0) {
     // strides of zero (a broadcast cache) or an encoder that refuses: plain copies
@@ -63,7 +65,8 @@ cudaError_t launch_attn_decode(const AttnParams &params, bool e4m3, void *ws, in
                     host_cache_map(&a.vmap, p.c, p.c.v, e4m3, p.D, p.Hkv, p.box, dp);
     if (!ok) p.box = 0;
   }
-  if (tc > 0 && p.box > 0) return launch_attn_tc(p, dp, tc, ws, a, s);
+  if (tc > 0 && p.box > 0)
+    return (e4m3 ? launch_attn_tc_e4m3 : launch_attn_tc)(p, dp, tc, ws, a, s);
   const AttnShape sh = attn_shape(rows);
   auto launch = dp == 64 ? launch_attn_d64 : (dp == 128 ? launch_attn_d128 : launch_attn_d256);
   return launch(p, e4m3, sh.nr, sh.wr, ws, a, s);

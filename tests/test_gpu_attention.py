@@ -755,3 +755,47 @@ def test_binding_refusals(env):
     torch.cuda.synchronize()
     assert bool((out == 3.0).all()), "a refused call must not write its output"
     ssd.attn_decode(**ok)
+
+
+# The same on an e4m3 cache, whose elements are widened to f16 on the way.
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("rows,Hq,Hkv,D,page", [
+    (8, 3, 1, 64, 8), (9, 2, 1, 16, 16), (5, 10, 2, 128, 24), (8, 8, 1, 128, 32),
+    (16, 16, 2, 96, 64), (3, 64, 2, 256, 16), (17, 7, 1, 144, 40), (40, 8, 1, 64, 128),
+    (20, 20, 1, 48, 16), (4, 8, 1, 80, 16), (10, 8, 1, 256, 64),
+])
+def test_attn_many_rows_e4m3(env, rows, Hq, Hkv, D, page, layout):
+    c = _Case(env, [rows, 63, 64, 65, 0, 700, 1, 130], [rows, rows, rows, rows, rows, rows, 1, 2],
+              Hq, Hkv, D, page, True, layout=layout, seed=rows + D)
+    c.check()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("window", [1, 64, 200])
+def test_attn_many_rows_e4m3_window_and_missing_pages(env, window, D):
+    c = _Case(env, [9, 64, 300, 1001, 0, 500], [9] * 6, 8, 2, D, 16, True, seed=window)
+    c.check(window)
+    c.table[2, 3:5] = -1
+    c.table[1, :] = 10 ** 6
+    c.table[5, :12] = -1
+    c.check(window)
+    c.check()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("lengths,rows", [([40, 700], 6), ([66, 200], 20), ([9000, 100], 8)])
+def test_attn_many_rows_e4m3_nan_in_unseen_places(env, lengths, rows, D):
+    torch, ssd, dev = env
+    c = _Case(env, lengths, [rows, rows], 8, 1, D, 16, True, seed=36 + rows)
+    want, want_lse = c.check()
+    for s, n in enumerate(lengths):
+        page = int(c.table[s, (n - 1) // 16])
+        c.kc.view(torch.uint8)[page, :, (n - 1) % 16] = 0x7f  # NaN
+        c.vc.view(torch.uint8)[page, :, (n - 1) % 16] = 0x7f
+    got, lse = c.run()
+    for s in range(2):
+        a, b = s * rows, (s + 1) * rows - 1
+        assert torch.equal(got[a:b], want[a:b]) and torch.equal(lse[a:b], want_lse[a:b])
+        assert bool(torch.isnan(got[b].float()).all()) and bool(torch.isnan(lse[b]).all())
+    assert ssd.dec_sync_status() == ssd.DEC_OK
