@@ -8,6 +8,9 @@ namespace {
 constexpr int KP_THREADS = 1024;
 constexpr int KP_CLUSTER = 8;
 constexpr int KP_CLUSTER_TOKENS = 4096;  // rows from which a cluster is launched
+// Dynamic shared memory of a launch without the opt-in: 48 KB, less what the kernel has
+// statically (256 bytes of warps' sums) with room to spare.
+constexpr size_t KP_SMEM_DEFAULT = 47 * 1024;
 
 __device__ __forceinline__ int pages_of(int tokens, int page_size) {
   return tokens / page_size + (tokens % page_size != 0);
@@ -157,7 +160,7 @@ cudaError_t launch_kv_plan(const KvPlanParams &p, cudaStream_t s) {
   const size_t smem = static_cast<size_t>(4) * p.S * sizeof(int);
   const bool cluster = p.max_tokens > KP_CLUSTER_TOKENS;
   auto kernel = cluster ? kv_plan_kernel<true> : kv_plan_kernel<false>;
-  if (smem > 48 * 1024) {
+  if (smem > KP_SMEM_DEFAULT) {
     const cudaError_t e = cudaFuncSetAttribute(
         kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
