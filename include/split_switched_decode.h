@@ -129,6 +129,13 @@ DEC_API dec_status dec_sync_status(dec_stream_t s);
  * then sees DEC_ERR_TIMEOUT from dec_sync_status(). Nothing faults or traps. */
 DEC_API dec_status dec_debug_wait_timeout(uint64_t limit_ns, dec_stream_t s);
 
+/* Self-test of attn_decode's bounded waits: while `on` is 1 (0: off, the default), the warps
+ * that multiply in every attn_decode launch of this process first wait for an arrival that
+ * never comes. That wait runs out after the limit of dec_set_wait_limit_ns; the kernel
+ * records the time-out, waits for its copies and products in flight and returns with
+ * undefined outputs. Nothing faults or traps. */
+DEC_API dec_status dec_debug_attn_timeout(int on);
+
 /* ------------------------------------------------------ decode projection ---- */
 
 /*

@@ -43,6 +43,7 @@ EXPORTS = [
     "dec_pack_weight", "dec_gemv_packed", "dec_splitk_gemm_packed", "dec_linear_packed",
     "dec_pack_expert_weights", "moe_experts_packed", "moe_layer_packed",
     "dec_read_stream_bytes", "dec_read_stream",
+    "dec_debug_attn_timeout",
     "kv_plan", "rope_frequencies", "rope_append", "attn_decode_workspace_bytes", "attn_decode",
 ]
 
@@ -116,6 +117,7 @@ def _load():
         "l2_prefetch": (I, [P, S, I, P]),
         "dec_sim_comm_wait": (I, [U64, P]),
         "dec_splitk_gemm_noalloc": (I, [P, P, P, P, I, I, I, I, P]),
+        "dec_debug_attn_timeout": (I, [I]),
         "kv_plan": (I, [P, P, I, I, P, I, P, I, P, P, P, P, P, I, P, P]),
         "rope_frequencies": (I, [I, F64, I, F64, I, F64, F64, P, P]),
         "rope_append": (I, [P, L, P, L, P, L, P, P, P, F, I, I, I, I, I, I, P, L, P, P, I, P, P,
@@ -197,6 +199,10 @@ def dec_sync_status(stream=None) -> int:
 
 def dec_debug_wait_timeout(limit_ns: int, stream=None):
     _check(_load().dec_debug_wait_timeout(limit_ns, _stream(stream)), "dec_debug_wait_timeout")
+
+
+def dec_debug_attn_timeout(on: bool):
+    _check(_load().dec_debug_attn_timeout(1 if on else 0), "dec_debug_attn_timeout")
 
 
 # --------------------------------------------------------------- projection ----

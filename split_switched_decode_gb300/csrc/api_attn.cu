@@ -1,5 +1,6 @@
 // api_attn.cu -- host side of the attention entry points of
 // include/split_switched_decode.h: kv_plan, rope_frequencies, rope_append, attn_decode.
+#include <atomic>
 #include <cmath>
 
 #include "../../include/split_switched_decode.h"
@@ -9,6 +10,8 @@
 using namespace ssd;
 
 namespace {
+
+std::atomic<int> g_attn_hold{0};  // dec_debug_attn_timeout
 
 bool off(const void *p, unsigned bytes) {
   return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0;
@@ -258,7 +261,14 @@ dec_status attn_decode(const dec_bf16 *q, int64_t q_stride, const void *k_cache,
   uint64_t limit = 0;
   unsigned *status = host_wait_status(&limit);
   return status_of(launch_attn_decode(p, kv_type == DEC_KV_E4M3, ws, sms, status, limit,
+                                      g_attn_hold.load() != 0,
                                       reinterpret_cast<cudaStream_t>(s)));
+}
+
+dec_status dec_debug_attn_timeout(int on) {
+  if (on != 0 && on != 1) return DEC_ERR_INVALID_ARG;
+  g_attn_hold.store(on);
+  return DEC_OK;
 }
 
 }  // extern "C"

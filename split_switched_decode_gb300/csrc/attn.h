@@ -67,6 +67,7 @@ struct AttnLaunch {
   int num_sms;
   unsigned *status;
   uint64_t wait_limit_ns;
+  bool hold;  // self-test: waits that run out
 };
 // Workers (CTAs) of a launch at most, and the workspace's counters: one per worker for items,
 // two for groups of workers.
@@ -103,6 +104,7 @@ bool host_cache_map(CUtensorMap *m, const PagedCache &c, const void *base, bool 
                     int Hkv, int box, int padded);
 size_t attn_workspace_bytes(int S, int T, int Hq, int Hkv, int D, int num_sms);
 cudaError_t launch_attn_decode(const AttnParams &p, bool e4m3, void *ws, int num_sms,
-                               unsigned *status, uint64_t wait_limit_ns, cudaStream_t s);
+                               unsigned *status, uint64_t wait_limit_ns, bool hold,
+                               cudaStream_t s);
 
 }  // namespace ssd

@@ -49,12 +49,14 @@ size_t attn_workspace_bytes(int S, int T, int Hq, int Hkv, int D, int num_sms) {
 }
 
 cudaError_t launch_attn_decode(const AttnParams &params, bool e4m3, void *ws, int num_sms,
-                               unsigned *status, uint64_t wait_limit_ns, cudaStream_t s) {
+                               unsigned *status, uint64_t wait_limit_ns, bool hold,
+                               cudaStream_t s) {
   AttnParams p = params;
   AttnLaunch a = {};
   a.num_sms = num_sms;
   a.status = status;
   a.wait_limit_ns = wait_limit_ns;
+  a.hold = hold;
   const int dp = padded_dim(p.D);
   const int rows = mean_rows(p.S, p.T, p.Hq, p.Hkv), tc = tc_rows(e4m3, dp, rows);
   p.box = box_tokens(p.c.page_size, e4m3 || tc > 0 ? 64 : 32);

@@ -227,6 +227,7 @@ struct AttnPlan {
   int *counters, *group_counters;
   unsigned *status;
   uint64_t wait_limit_ns;
+  int hold;  // self-test: waits that run out (dec_debug_attn_timeout)
 };
 
 // All items' units in order (an item: its COST, then one per stage), and worker c's
@@ -726,8 +727,10 @@ __global__ void __launch_bounds__(AT_THREADS, (AttnCfg<E4M3, DP, NR, WR>::CTAS))
       }
     }
     cp_async_wait_all();
+    // The multiplying warps' waits are over as well: a time-out of theirs after this warp's last
+    // stage is known here, and boxes still on their way land before the CTA ends.
+    named_bar_sync(3, AT_THREADS);
     if (*static_cast<volatile int *>(&abort_flag) && lane == 0) {
-      // after a time-out: boxes still on their way land before the CTA ends
       for (int i = max(k - ST, 0); i < k; ++i)
         mbar_wait_drain(&full[i % ST], (i / ST) & 1, 10000000ull);
     }
@@ -738,6 +741,9 @@ __global__ void __launch_bounds__(AT_THREADS, (AttnCfg<E4M3, DP, NR, WR>::CTAS))
   const int wr = warp % WR, wt = warp / WR;  // which rows, which tokens of a stage
   const int g8 = lane >> 2, c4 = lane & 3;   // a lane's place in the fragments
   int k = 0, seg = 0;
+  // self-test: nobody but these warps, later, arrives here
+  if (pl.hold)
+    mbar_wait_bounded(&qempty[0], 0, pl.status, &abort_flag, pl.wait_limit_ns);
   while (c.next(p, G)) {
     const SeqInfo &x = c.x;
     const int n_rows = min(M, x.n * G - c.rt * M);   // of the item
@@ -1136,6 +1142,8 @@ __global__ void __launch_bounds__(AT_THREADS, (AttnCfg<E4M3, DP, NR, WR>::CTAS))
       if (tid == 0) count_part(pl, me, c0, c1, n_rows, dst, pending, &n_pending);
     }
   }
+  __syncwarp();
+  named_bar_arrive(3, AT_THREADS);  // no wait of these warps follows: see the copying warps' end
   static_assert(ST * C::STAGE >= 2 * AT_GROUP * M * 8, "ml of a join");
   run_joins<M, DP, AT_CTHREADS>(p, pl, reinterpret_cast<float2 *>(at_smem), pending, &n_pending,
                                 &is_last);
@@ -1156,6 +1164,7 @@ inline AttnPlan make_plan(void *ws, const AttnLaunch &a) {
                                           attn_counter_bytes(a.num_sms));
   pl.status = a.status;
   pl.wait_limit_ns = a.wait_limit_ns;
+  pl.hold = a.hold;
   return pl;
 }
 

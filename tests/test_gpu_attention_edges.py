@@ -5,7 +5,7 @@ import sys
 
 import pytest
 
-from test_gpu_attention import env  # noqa: F401
+from test_gpu_attention import _Case, env  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -30,3 +30,36 @@ print("plans agree")
 """.format(root=ROOT, tests=os.path.join(ROOT, "tests"))
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "plans agree" in r.stdout, r.stdout + r.stderr
+
+
+# ----------------------------------------------------------- waits that run out ----
+
+def _held(env, c, calls=1):
+    """Runs the case with the multiplying warps waiting for what never comes; then, on a
+    zero-filled workspace, as ever. Outputs have to be what they were, and the time-out known."""
+    torch, ssd, dev = env
+    want, want_lse = c.check()
+    assert ssd.dec_sync_status() == ssd.DEC_OK
+    ssd.dec_set_wait_limit_ns(1_000_000)
+    ssd.dec_debug_attn_timeout(True)
+    try:
+        for _ in range(calls):
+            c.run()
+            assert ssd.dec_sync_status() == ssd.DEC_ERR_TIMEOUT
+    finally:
+        ssd.dec_debug_attn_timeout(False)
+        ssd.dec_set_wait_limit_ns(2_000_000_000)
+    c.ws.zero_()
+    got, lse = c.run()
+    assert ssd.dec_sync_status() == ssd.DEC_OK
+    assert torch.equal(got, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("lengths", [[40], [300, 70, 0, 1000]])
+@pytest.mark.parametrize("page", [16, 13])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attn_wait_that_runs_out(env, D, e4m3, page, lengths):
+    """Boxes (pages of 16) and 16-byte copies (of 13); ranges that end before the time-out does
+    (the copying warps are done with their stages by then) and longer ones."""
+    _held(env, _Case(env, lengths, [1] * len(lengths), 8, 1, D, page, e4m3, seed=D))
