@@ -277,13 +277,6 @@ __global__ void __launch_bounds__((TcCfg<DP, MQ, E4M3>::THREADS), 1)
   // knows that i - TC_NS is done (the scores of i were issued after it), and a wait tells
   // only neighbouring phases apart.
   int issued = 0;  // a copying warp's stages: one past its last
-  // After a time-out: an issuing warp's products end before tensor memory is released.
-  auto drain = [&](int i) {
-    if (!__any_sync(0xffffffffu, *static_cast<volatile int *>(&abort_flag))) return;
-    if (elect_one()) tc_commit(&drained[i]);
-    __syncwarp();
-    mbar_wait_drain(&drained[i], 0, 10000000ull);
-  };
   auto wait_pv = [&](int i) { wait(&pv_done[i % TC_NS], i / TC_NS); };
 
   if (warp >= SW && warp < SW + 3) {
@@ -501,7 +494,6 @@ __global__ void __launch_bounds__((TcCfg<DP, MQ, E4M3>::THREADS), 1)
       if (last < c.t0 && lane == 0) mbar_arrive(&qempty[qb]);
       ++seg;
     }
-    drain(qk);
   } else if (warp == SW + 5) {
     // O += P . V
     const uint32_t id_o = tc_idesc<E4M3>(p.D) | (1u << 16), ring_u = smem_u32(ring);
@@ -528,7 +520,6 @@ __global__ void __launch_bounds__((TcCfg<DP, MQ, E4M3>::THREADS), 1)
       }
     }
     if (k > 0) wait_pv(k - 1);  // nothing in flight when the columns are released
-    drain(2);
   } else {
     // ================================================================ softmax, a thread a lane
     const int grp = warp >> 2, gt = tid & 127;
@@ -537,6 +528,7 @@ __global__ void __launch_bounds__((TcCfg<DP, MQ, E4M3>::THREADS), 1)
     const int copy = gt / MQ, r = gt % MQ, first_tok = copy * TS;
     constexpr uint32_t INF2 = E4M3 ? 0x7c007c00u : 0x7f807f80u;  // exponents of two values
     int k = 0, cleans = 0, segs = 0;
+    if (pl.hold) wait(&stored[0], 0);  // self-test: nobody but these warps, later, arrives here
     while (c.next(p, G)) {
       const SeqInfo &x = c.x;
       const int n_rows = min(MQ, x.n * G - c.rt * MQ), row0 = c.rt * MQ;
@@ -842,12 +834,22 @@ __global__ void __launch_bounds__((TcCfg<DP, MQ, E4M3>::THREADS), 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == SW + 4) tmem_dealloc(tmem, C::COLS);
-  if (abort_flag && lane == 0) {
-    // after a time-out: boxes still on their way land before the CTA ends
+  // Every wait of the CTA is over. If one ran out, products and boxes may still be on their way:
+  // products end before tensor memory is released, boxes land before the CTA ends.
+  if (*static_cast<volatile int *>(&abort_flag)) {
+    if (warp >= SW + 3 && warp < SW + 6) {
+      uint64_t *bar = &drained[warp - SW - 3];
+      if (elect_one()) tc_commit(bar);
+      __syncwarp();
+      mbar_wait_drain(bar, 0, 10000000ull);
+    }
     for (int i = issued - 1; i >= 0 && i >= issued - C::CST; i -= C::CW)
       mbar_wait_drain(&copy_full[i % C::CST], (i / C::CST) & 1, 10000000ull);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
   }
+  if (warp == SW + 4) tmem_dealloc(tmem, C::COLS);
 }
 
 template <bool E4M3, int DP, int MQ>

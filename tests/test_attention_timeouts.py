@@ -42,6 +42,20 @@ def test_copies_are_drained_after_the_last_wait_of_the_multiplying_warps():
     assert "return;" not in multiplying
 
 
+def test_products_and_copies_are_drained_before_tensor_memory_is_released():
+    body = _kernel("attn_tc_kernel", "attn_tc.cuh")
+    joins = _only(body, "run_joins<")          # by every thread, after the roles
+    met = body.index("__syncthreads();", joins)
+    flag = _only(body, FLAG)
+    assert "wait(" not in body[joins:] and "wait_pv(" not in body[joins:]
+    assert joins < met < flag < body.index("tc_commit(bar)", flag)
+    assert body.index("mbar_wait_drain(") > flag and body.count("mbar_wait_drain(") == 2
+    assert body.rindex("mbar_wait_drain(") < body.rindex("__syncthreads();")
+    assert body.rindex("__syncthreads();") < _only(body, "tmem_dealloc(")
+    # no role leaves before the joins (only a CTA without work, as a whole)
+    assert body.count("return;") == 1 and body.index("return;") < body.index("tmem_alloc(")
+
+
 @pytest.mark.parametrize("on,status", [(2, 1), (-1, 1), (1, 0), (0, 0)])
 def test_the_self_test_is_switched_on_and_off(on, status):
     import split_switched_decode_gb300 as ssd
