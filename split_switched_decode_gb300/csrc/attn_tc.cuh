@@ -273,6 +273,13 @@ __global__ void __launch_bounds__((TcCfg<DP, MQ, E4M3>::THREADS), 1)
   auto wait = [&](uint64_t *bar, int phase) {
     return mbar_wait_bounded(bar, phase & 1, pl.status, &abort_flag, pl.wait_limit_ns);
   };
+  // For what comes once a segment: the limit times the waits of all `stages` so far (four a
+  // stage, each with the limit to itself), as a segment may well take longer than the limit.
+  auto wait_stages = [&](uint64_t *bar, int phase, int stages) {
+    const uint64_t one = pl.wait_limit_ns;
+    const uint64_t limit = one >> 34 == 0 ? one * (4ull * stages + 4) : one;  // below 2^64
+    return mbar_wait_bounded(bar, phase & 1, pl.status, &abort_flag, limit);
+  };
   // Outputs of stage i added. As many barriers in turn as there are S: who waits for stage i
   // knows that i - TC_NS is done (the scores of i were issued after it), and a wait tells
   // only neighbouring phases apart.
@@ -395,13 +402,13 @@ __global__ void __launch_bounds__((TcCfg<DP, MQ, E4M3>::THREADS), 1)
     // A thread has one 16-byte column of the head and every PER_PASS-th row.
     constexpr int CH = DP / 8, PER_PASS = TC_QTHREADS / CH;
     const int at = tid - (SW + 6) * 32, ch = at % CH;
-    int seg = 0;
+    int seg = 0, stages = 0;
     decltype(c) last = c;  // the segment before this one
     // Its part, if it is one of several, is stored: the last warp counts it. (Two barriers in
     // turn: the softmax can be one segment ahead of this warp, whose rows of q it needs for a
     // second.) E4M3: both warps wait, as the softmax may then still read row_scale.
     auto count = [&](int done) {
-      wait(&stored[done & 1], done >> 1);
+      wait_stages(&stored[done & 1], done >> 1, stages);
       const long long unit = last.item + TC_ITEM_COST;
       const int c0 = sh.worker_of(unit), c1 = sh.worker_of(unit + last.x.kt - 1);
       if (c0 != c1 && lane == 0 && warp == SW + 7)
@@ -412,6 +419,7 @@ __global__ void __launch_bounds__((TcCfg<DP, MQ, E4M3>::THREADS), 1)
     };
     while (c.next(p, G)) {
       const int qb = seg % C::QB;
+      stages += c.t1 - c.t0;
       const int n_rows = min(MQ, c.x.n * G - c.rt * MQ);
       uint8_t *qd = at_smem + qb * C::QBYTES;
       const uint16_t *head = p.q + static_cast<long long>(c.hk * G) * p.D + ch * 8;
@@ -428,7 +436,7 @@ __global__ void __launch_bounds__((TcCfg<DP, MQ, E4M3>::THREADS), 1)
           }
         }
         // (the first rows are on their way while the last segment's products read the buffer)
-        if (r0 < PER_PASS && seg >= C::QB) wait(&qempty[qb], seg / C::QB - 1);
+        if (r0 < PER_PASS && seg >= C::QB) wait_stages(&qempty[qb], seg / C::QB - 1, stages);
 #pragma unroll
         for (int e = 0; e < AHEAD; ++e) {
           const int r = r0 + e * PER_PASS;

@@ -1,11 +1,14 @@
 """GPU tests of the attention entry points at their edges."""
+import math
 import os
 import subprocess
 import sys
 
+import numpy as np
 import pytest
 
-from test_gpu_attention import _Case, env  # noqa: F401
+import attn_ref
+from test_gpu_attention import U, _Case, _f64, _i32, env  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -71,3 +74,44 @@ def test_attn_wait_that_runs_out(env, D, e4m3, page, lengths):
 def test_attn_many_rows_wait_that_runs_out(env, D, e4m3, rows, lengths):
     """The same with products in flight as well, in items of 32, 64 and 128 rows."""
     _held(env, _Case(env, lengths, [rows] * len(lengths), 8, 1, D, 16, e4m3, seed=rows))
+
+
+@pytest.mark.parametrize("rows", [1, 8])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attn_segments_longer_than_the_wait_limit(env, D, e4m3, rows):
+    """Every stage comes in time, so nothing runs out, however long a CTA is at one item: some
+    117 million tokens (the same four pages again and again) take several milliseconds under
+    a limit of one. Repeated tokens change the sum of the weights, not the mean.
+
+    Tolerance: that of the other cases, and 2^-23 for each of the up to 12000 * 4 sums of
+    products that an output adds up (2^-24 for the 12000 of a row's sum)."""
+    torch, ssd, dev = env
+    page, pages, times, Hq = 4096, 4, 7168, 8
+    n = page * pages
+    g = torch.Generator(device=dev).manual_seed(D)
+    dt = torch.float8_e4m3fn if e4m3 else torch.bfloat16
+    kc, vc = (torch.randn((pages, 1, page, D), generator=g, device=dev).to(dt) for _ in range(2))
+    q = torch.randn((rows, Hq, D), generator=g, device=dev).to(torch.bfloat16)
+    table = torch.arange(pages * times, dtype=torch.int32, device=dev).view(1, -1) % pages
+    out = torch.zeros_like(q)
+    lse = torch.zeros((rows, Hq), dtype=torch.float32, device=dev)
+    ws = ssd.workspace(ssd.attn_decode_workspace_bytes(1, rows, Hq, 1, D))
+    ssd.dec_set_wait_limit_ns(1_000_000)
+    try:
+        ssd.attn_decode(q, kc, vc, table, _i32(torch, [n * times], dev), out, ws,
+                        q_start=_i32(torch, [0, rows], dev), lse=lse)
+        assert ssd.dec_sync_status() == ssd.DEC_OK
+    finally:
+        ssd.dec_set_wait_limit_ns(2_000_000_000)
+    k, v = (_f64(c).reshape(n, 1, D) for c in (kc, vc))
+    for i in range(rows):  # each alone over all tokens: what the others do not see is 2^-24
+        want, wl, size, reach = attn_ref.attention(_f64(q[i:i + 1]), k, v, np.ones(n, bool),
+                                                   D ** -0.5, 0)
+        score = (D + 16) * 2.0 ** -24 * reach
+        extra = 12000 * (4 * 2.0 ** -23 + 2.0 ** -24)
+        bound = U * np.abs(want) + (U + 2 * score[..., None] + 2.0 ** -18 + extra) * size
+        assert np.all(np.abs(_f64(out[i:i + 1]) - want) <= bound)
+        got = lse[i:i + 1].cpu().numpy().astype(np.float64)
+        assert np.all(np.abs(got - wl - math.log(times))
+                      <= score + 12000 * 2.0 ** -24 + 2.0 ** -18)
