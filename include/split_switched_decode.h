@@ -540,7 +540,9 @@ DEC_API dec_status rope_append(const dec_bf16 *q, int64_t q_stride, const dec_bf
  * included, taken as at most max_pages * page_size; q_start int32 [S+1], or NULL for one
  * row each (then T == S); lse_opt fp32 [T,Hq] or NULL. Rows of no sequence are not written.
  * S in 1..8192, T in 1..65536, Hq and Hkv 1..1024 with Hq % Hkv == 0. Scores, maxima, sums
- * and partial results are fp32; the weights p_j round to 16 bits for the product with V.
+ * and partial results are fp32; the weights p_j round to 16 bits for the product with V: bf16
+ * on a bf16 cache (off by 2^-8 of themselves), f16 on an e4m3 one (2^-11, or 2^-32 of the row's
+ * largest weight where that is more).
  * Deterministic: the split depends on the lengths, not on timing.
  */
 DEC_API size_t attn_decode_workspace_bytes(int S, int T, int Hq, int Hkv, int D);

@@ -65,6 +65,13 @@ constexpr int AT_GROUP = 16;     // workers whose parts of a much split item are
 // window 24.8 instead of 23.0. Shares of two stages and more: with four, a single
 // sequence of 1024 tokens takes 11.0 us instead of 9.8.
 constexpr int AT_ITEM_COST = 4, AT_LEAST = 2;
+// Weights are powers of two of a score less the running maximum, and as many times larger as
+// these powers say: those that round to f16 (8-bit caches) then keep 11 bits down to 2^-21 of the
+// largest, and are off by at most 2^-32 of it below (unscaled, 2^-25, and a long flat tail of
+// weights under that was lost to the outputs, not to the sum they are divided by). Seven: the
+// largest f16 is just below 2^16, weights under the maximum that lags by 8 (attn_tc.cuh) reach
+// 2^15, and no rounding of a huge maximum less seven can be off by as much again.
+constexpr float F16_POWERS = 7.0f;
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
 template <bool E4M3, int DP, int NR, int WR>
@@ -755,7 +762,8 @@ __global__ void __launch_bounds__(AT_THREADS, (AttnCfg<E4M3, DP, NR, WR>::CTAS))
     const int hi_top = pos0 + (row0 + max(my_rows, 1) - 1) / G;
     const int lo_all = p.window > 0 && hi_top >= p.window ? hi_top - p.window + 1 : 0;
 
-    // this thread's rows are nr * 8 + 2 c4 + e: score factor, maximum, sum, outputs
+    // this thread's rows are nr * 8 + 2 c4 + e: score factor, what weights refer to (the
+    // maximum, less F16_POWERS on an e4m3 cache), sum, outputs
     float zf[NR][2], m[NR][2], l[NR][2];
     float o[NR][DP / 16][4];
     const float z_all = p.scale * LOG2E * (p.c.k_scale ? p.c.k_scale[c.hk] : 1.0f);
@@ -910,12 +918,13 @@ __global__ void __launch_bounds__(AT_THREADS, (AttnCfg<E4M3, DP, NR, WR>::CTAS))
           for (int r = 0; r < NR; ++r)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float mx = m[r][e];
+              float mx = E4M3 ? -INFINITY : m[r][e];
 #pragma unroll
               for (int i = 0; i < MT; ++i) mx = fmaxf(mx, fmaxf(z[r][i][e], z[r][i][2 + e]));
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+              if (E4M3) mx = fmaxf(m[r][e], mx - F16_POWERS);
               base[r][e] = mx == -INFINITY ? 0.0f : mx;
               fade[r][e] = ex2(m[r][e] - base[r][e]);
               m[r][e] = mx;
@@ -930,9 +939,12 @@ __global__ void __launch_bounds__(AT_THREADS, (AttnCfg<E4M3, DP, NR, WR>::CTAS))
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[r][d][e] *= fade[r][e & 1];
           }
-          // ---- weights: summed in fp32, rounded to 16 bits for the product with V (relative
-          // error 2^-9 bf16, 2^-12 f16 for each, independent of one another: below the
-          // output's own rounding once summed), turned so that tokens are the inner dimension
+          // ---- weights: summed in fp32, rounded to 16 bits for the product with V, turned so
+          // that tokens are the inner dimension. Each is off by 2^-8 (bf16) or 2^-11 (f16) of
+          // itself at most, independently of the others. In bf16 that adds up to as much as
+          // the output's own rounding where few weights carry a row, to less where many do
+          // (relative error against 64 bits 0.0018 to 0.0023, with fp32 weights 0.0017);
+          // keeping 16 more bits would take a second product with V.
           uint32_t w[NR][MT][2];
 #pragma unroll
           for (int r = 0; r < NR; ++r)

@@ -33,9 +33,10 @@
 // take).
 //
 // The running maximum that weights refer to is moved only when a row's maximum has grown by
-// more than 8 (weights then stay below 2^8, and their rounding to bf16, relative 2^-9 as the
+// more than 8 (weights then stay below 2^8, and their rounding to bf16, relative 2^-8 as the
 // output's own, is not enlarged), so the outputs in tensor memory are rarely rescaled; sums
-// are fp32 of the weights before rounding and refer to the same maximum.
+// are fp32 of the weights before rounding and refer to the same maximum. (On e4m3 caches, whose
+// weights are f16, to one smaller by F16_POWERS: attn_kernel.cuh.)
 //
 // E4M3 caches: the boxes fill a ring of their own, and four warps widen its stages to f16 (every
 // e4m3 value is an f16 value) into a short ring of operands; q is scaled by a power of two a
@@ -588,9 +589,10 @@ __global__ void __launch_bounds__((TcCfg<DP, MQ, E4M3>::THREADS), 1)
         float mx = least ? fminf(fminf(part[0], part[1]), fminf(part[2], part[3]))
                          : fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
         if (plain) mx *= zf;
+        if (E4M3) mx -= F16_POWERS;
         if (begins) {
           m = mx;
-        } else if (__any_sync(0xffffffffu, mx > m + TC_LAZY)) {
+        } else if (__any_sync(0xffffffffu, mx - m >= TC_LAZY)) {
           // move every row's maximum: the outputs so far are rescaled in tensor memory,
           // after the last product that adds to them
           const float m_new = fmaxf(m, mx);

@@ -115,3 +115,49 @@ def test_attn_segments_longer_than_the_wait_limit(env, D, e4m3, rows):
         got = lse[i:i + 1].cpu().numpy().astype(np.float64)
         assert np.all(np.abs(got - wl - math.log(times))
                       <= score + 12000 * 2.0 ** -24 + 2.0 ** -18)
+
+
+# ------------------------------------------------------------------ flat tails ----
+
+@pytest.mark.parametrize("peak", [10.0, 14.0, 16.0, 18.0, 20.0])
+@pytest.mark.parametrize("rows,n", [(1, 100), (1, 1000), (2, 300), (4, 500), (8, 500), (16, 900)])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("D", [64, 256])
+def test_attn_flat_tail_under_a_peak(env, D, e4m3, rows, n, peak):
+    """One key 14 to 29 powers of two above all others, whose values alone count (the peak's is
+    zero): what is lost of the others' weights is lost of the outputs.
+
+    Weights round by 2^-8 (bf16) or 2^-11 of themselves or 2^-32 of the largest (f16), outputs
+    by 2^-8."""
+    torch, ssd, dev = env
+    c = _Case(env, [n], [rows], 8, 1, D, 16, e4m3, seed=n)
+    one = torch.ones(1, device=dev)
+    c.ks = c.vs = one if e4m3 else None
+    kind = torch.uint8 if e4m3 else torch.int16
+    keys = torch.zeros((n, D), device=dev)
+    keys[:, 0] = 0.125
+    keys[3, 0] = peak
+    values = torch.randint(8, 16, (n, D), device=dev, generator=torch.Generator(dev).manual_seed(1))
+    values = values.float() / 8                 # 1 to 2, in steps that both types have
+    values[3] = 0.0
+    for cache, x in ((c.kc, keys), (c.vc, values)):
+        x = x.to(cache.dtype).view(kind)
+        for i in range(0, n, 16):
+            cache[int(c.table[0, i // 16]), 0, :len(x[i:i + 16])].view(kind).copy_(x[i:i + 16])
+    c.q.zero_()
+    c.q[:, :, 0] = 1.0
+    c.scale = 1.0
+    got, lse = (_f64(t) for t in c.run())
+    w = np.exp(_f64(keys)[:, 0] - peak)
+    v = _f64(values)
+    u = 2.0 ** -11 if e4m3 else U
+    floor = 2.0 ** -32 if e4m3 else 0.0
+    for i in range(rows):
+        seen = n - rows + i + 1
+        total = w[:seen].sum()
+        want, size = w[:seen] @ v[:seen] / total, w[:seen] @ np.abs(v[:seen]) / total
+        # scores of one product each: 2^-22 |z| for the scaling and the difference
+        bound = U * want + (u + 2.0 ** -21 * peak + 2.0 ** -18) * size \
+            + floor * np.abs(v[:seen]).sum(0) / total
+        assert np.all(np.abs(got[i] - want) <= bound), i
+        assert np.all(np.abs(lse[i] - (peak + math.log(total))) <= 2.0 ** -21 * peak + 2.0 ** -18)
