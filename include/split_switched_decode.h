@@ -533,7 +533,8 @@ DEC_API dec_status rope_append(const dec_bf16 *q, int64_t q_stride, const dec_bf
  * A row that sees no key (or whose scores are all -infinity) gives out = 0 and
  * lse = -infinity. Keys whose page is not in 0..num_pages-1 are not seen. What stands in
  * the cache at a place that a row does not see, NaN included, does not reach that row; a
- * value that is not finite makes that element of the rows that see it infinite or NaN.
+ * value that is not finite makes that element of the rows that see it infinite or NaN, however
+ * little it weighs (short of a score of -infinity).
  *
  * q and out [T,Hq,D] with row strides in elements (multiples of 8, 16-byte aligned; out may
  * not overlap q); block_table int32 [S, max_pages]; seq_len int32 [S], the new tokens

@@ -939,6 +939,19 @@ __global__ void __launch_bounds__(AT_THREADS, (AttnCfg<E4M3, DP, NR, WR>::CTAS))
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[r][d][e] *= fade[r][e & 1];
           }
+          // A weight of zero is to mean that the row does not see the token (see `unclean`): the
+          // least that a seen one has is 2^-100.
+          if (!plain) {
+#pragma unroll
+            for (int r = 0; r < NR; ++r)
+#pragma unroll
+              for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float least = base[r][e & 1] - 100.0f;
+                  if (z[r][i][e] < least && z[r][i][e] != -INFINITY) z[r][i][e] = least;
+                }
+          }
           // ---- weights: summed in fp32, rounded to 16 bits for the product with V, turned so
           // that tokens are the inner dimension. Each is off by 2^-8 (bf16) or 2^-11 (f16) of
           // itself at most, independently of the others. In bf16 that adds up to as much as

@@ -50,6 +50,8 @@
 // at 64 rows a CTA has four or five ends in its share.
 #pragma once
 
+#include <float.h>
+
 #include "attn_kernel.cuh"
 #include "tcgen05.cuh"
 
@@ -690,12 +692,19 @@ __global__ void __launch_bounds__((TcCfg<DP, MQ, E4M3>::THREADS), 1)
               for (int i = 0; i < TOK; ++i) {
                 const uint32_t pw2 = tmem_ld1(s_at + i / 2);
                 tmem_wait_ld();
-                const float pr = to_f32<E4M3>(i & 1 ? pw2 >> 16 : pw2 & 0xffffu);
+                float pr = to_f32<E4M3>(i & 1 ? pw2 >> 16 : pw2 & 0xffffu);
+                // seen, in this copy? (a weight of zero does not tell: one far below the row's
+                // maximum is zero too, and is taken as the smallest number)
+                const int at = i - first_tok;
+                if (at < 0 || at >= TS || at < lo - j0 - first_tok || at > hi - j0 - first_tok ||
+                    !(valid >> i & 1))
+                  continue;
+                if (pr == 0.0f) pr = FLT_MIN;
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                   const uint16_t y = *reinterpret_cast<const uint16_t *>(
                       v + swz<RB, TOK>(i, (d + e) >> 3) + ((d + e) & 7) * 2);
-                  if ((y & INF2) == (INF2 & 0xffffu) && pr != 0.0f) o[e] += pr * to_f32<E4M3>(y);
+                  if ((y & INF2) == (INF2 & 0xffffu)) o[e] += pr * to_f32<E4M3>(y);
                 }
               }
 #pragma unroll

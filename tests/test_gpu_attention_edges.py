@@ -161,3 +161,48 @@ def test_attn_flat_tail_under_a_peak(env, D, e4m3, rows, n, peak):
             + floor * np.abs(v[:seen]).sum(0) / total
         assert np.all(np.abs(got[i] - want) <= bound), i
         assert np.all(np.abs(lse[i] - (peak + math.log(total))) <= 2.0 ** -21 * peak + 2.0 ** -18)
+
+
+# -------------------------------------------- values that are not finite, little weight ----
+
+def _peak_and_bad_value(env, n, rows, D, e4m3, peak, bad):
+    """Token `peak` 200 above all others, and a value that is not finite, in element 5 of token
+    `bad`: every row that sees it has an infinity or NaN there, little as the token weighs
+    (2^-288), and is left alone elsewhere; rows that do not see it are as without it."""
+    torch, ssd, dev = env
+    c = _Case(env, [n], [rows], 8, 1, D, 16, e4m3, seed=n + rows)
+    c.ks = None
+    kind = torch.uint8 if e4m3 else torch.int16
+    keys = torch.zeros((n, D), device=dev)
+    keys[peak, 0] = 20.0
+    keys = keys.to(c.kc.dtype).view(kind)
+    for i in range(0, n, 16):
+        page = c.kc[int(c.table[0, i // 16]), 0].view(kind)
+        page[:min(16, n - i)].copy_(keys[i:i + 16])
+    c.q.zero_()
+    c.q[:, :, 0] = 10.0
+    c.scale = 1.0
+    want, want_lse = c.run()
+    value = torch.full((1,), float("nan") if e4m3 else float("inf"), device=dev)
+    cell = c.vc[int(c.table[0, bad // 16]), 0, bad % 16].view(kind)
+    cell[5:6].copy_(value.to(c.vc.dtype).view(kind))
+    got, lse = c.run()
+    assert bool(torch.isfinite(want.float()).all())
+    assert torch.equal(lse, want_lse)
+    rest = [d for d in range(D) if d != 5]
+    for i in range(rows):
+        if n - rows + i >= bad:
+            assert not bool(torch.isfinite(got[i, :, 5].float()).any()), i
+            assert torch.equal(got[i][:, rest], want[i][:, rest]), i
+        else:
+            assert torch.equal(got[i], want[i]), i
+
+
+@pytest.mark.parametrize("n,rows,peak,bad", [
+    (100, 1, 97, 99), (100, 2, 97, 99), (100, 4, 96, 98), (100, 8, 96, 98), (104, 16, 96, 102),
+])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attn_bad_value_of_little_weight_that_some_rows_see(env, D, e4m3, n, rows, peak, bad):
+    """Among the new tokens, beside the peak."""
+    _peak_and_bad_value(env, n, rows, D, e4m3, peak, bad)
