@@ -757,7 +757,9 @@ __global__ void __launch_bounds__((TcCfg<DP, MQ, E4M3>::THREADS), 1)
       join_ml[tid][1] = l;
       named_bar_sync(1, GROUPS * 128);
       // a row's thread: the copies' factors (with the division, where the item ends here), and
-      // the row's lse or (m, l)
+      // the row's lse or (m, l). What is not to be read at all (a group without a stage: its
+      // memory holds anything; a finished row that saw nothing: zeros) has the factor -0; a
+      // factor that has become zero is +0, so that what is not finite in that part is not lost.
       float factor[C::PARTS];
       if (tid < n_rows) {
         float mr = -INFINITY, lr = 0.0f;
@@ -775,12 +777,15 @@ __global__ void __launch_bounds__((TcCfg<DP, MQ, E4M3>::THREADS), 1)
           dst.put_lse(p, tid, mr, lr);
           const float inv = lr == 0.0f ? 0.0f : dst.v_scale / lr;
 #pragma unroll
-          for (int g = 0; g < C::PARTS; ++g) factor[g] = lr == 0.0f ? 0.0f : factor[g] * inv;
+          for (int g = 0; g < C::PARTS; ++g) factor[g] *= inv;
         } else {
           *reinterpret_cast<float2 *>(slot + MQ * DP + 2 * tid) = make_float2(mr, lr);
         }
 #pragma unroll
-        for (int g = 0; g < C::PARTS; ++g) join_ml[g * MQ + tid][0] = factor[g];
+        for (int g = 0; g < C::PARTS; ++g) {
+          const bool none = last_of(g / C::COPIES) < k - (c.t1 - c.t0) || (c0 == c1 && lr == 0.0f);
+          join_ml[g * MQ + tid][0] = none ? -0.0f : (factor[g] == 0.0f ? 0.0f : factor[g]);
+        }
       }
       if (has) wait_pv(my_last);
       tc_fence_after();
@@ -813,7 +818,7 @@ __global__ void __launch_bounds__((TcCfg<DP, MQ, E4M3>::THREADS), 1)
           for (int g = 0; g < C::PARTS; ++g) {
             const float f = join_ml[g * MQ + row][0];
             const float4 y = *join_at(g / C::COPIES, g % C::COPIES * MQ + row, d);
-            if (f != 0.0f) {  // a part that saw nothing, a row that saw nothing
+            if (__float_as_uint(f) != 0x80000000u) {
               v.x += f * y.x;
               v.y += f * y.y;
               v.z += f * y.z;

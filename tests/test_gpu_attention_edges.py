@@ -206,3 +206,15 @@ def _peak_and_bad_value(env, n, rows, D, e4m3, peak, bad):
 def test_attn_bad_value_of_little_weight_that_some_rows_see(env, D, e4m3, n, rows, peak, bad):
     """Among the new tokens, beside the peak."""
     _peak_and_bad_value(env, n, rows, D, e4m3, peak, bad)
+
+
+@pytest.mark.parametrize("n,rows,peak,bad", [
+    (100, 1, 3, 40), (100, 4, 3, 40), (100, 8, 3, 40), (200, 8, 3, 70), (100, 16, 3, 40),
+    (700, 16, 3, 150), (100, 8, 90, 5),
+])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attn_bad_value_of_little_weight_in_another_part(env, D, e4m3, n, rows, peak, bad):
+    """Where the peak is another copy's, another softmax group's or another worker's, whose part
+    makes that of the value's own vanish when they are joined."""
+    _peak_and_bad_value(env, n, rows, D, e4m3, peak, bad)
