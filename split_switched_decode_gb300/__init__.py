@@ -549,6 +549,8 @@ def attn_decode(q, k_cache, v_cache, block_table, seq_len, out, ws, q_start=None
     if To != T or Ho != Hq or seq_len.numel() != S or \
             (q_start is not None and q_start.numel() != S + 1):
         raise ValueError("attn_decode: sizes do not agree")
+    if not ws.is_cuda or not ws.is_contiguous():
+        raise TypeError("ws must be a contiguous CUDA tensor")
     status = lib.attn_decode(
         qp, qs, k_cache.data_ptr(), v_cache.data_ptr(), kind, _scales(k_scale, "k_scale", Hkv),
         _scales(v_scale, "v_scale", Hkv), pages, page, stride[0], stride[1], stride[2], table,
