@@ -607,6 +607,13 @@ __device__ __forceinline__ void run_joins(const AttnParams &p, const AttnPlan &p
   }
 }
 
+// Whether a CTA's static shared memory (FIXED bytes of variables, 64 for gaps between them), which is
+// filled up to the 1024 bytes that the dynamic one is aligned to, and the dynamic one fit
+// the 227 KB that a CTA may have. Several shapes are full to the last KB, and a launch that
+// asks for more fails.
+template <size_t FIXED, size_t DYNAMIC>
+constexpr bool fits_shared = (FIXED + 64 + 1023) / 1024 * 1024 + DYNAMIC <= 227 * 1024;
+
 template <bool E4M3, int DP, int NR, int WR>
 __global__ void __launch_bounds__(AT_THREADS, (AttnCfg<E4M3, DP, NR, WR>::CTAS))
     attn_decode_kernel(const __grid_constant__ CUtensorMap kmap,
@@ -622,6 +629,11 @@ __global__ void __launch_bounds__(AT_THREADS, (AttnCfg<E4M3, DP, NR, WR>::CTAS))
   __shared__ uint32_t stage_valid[ST][TOK / 32];       // tokens of the stage that exist
   __shared__ int abort_flag, n_pending, is_last;
   __shared__ PendingJoin pending[2];  // a range splits at most its first and last item
+  static_assert(fits_shared<sizeof(start) + sizeof(full) + sizeof(empty) + sizeof(qempty) +
+                                sizeof(join_ml) + sizeof(stage_valid) + 3 * sizeof(int) +
+                                sizeof(pending),
+                            C::SMEM>,
+                "all of the above and the dynamic shared memory");
   uint8_t *q_smem = at_smem + ST * C::STAGE;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;

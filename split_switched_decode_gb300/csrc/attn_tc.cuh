@@ -222,6 +222,17 @@ __global__ void __launch_bounds__((TcCfg<DP, MQ, E4M3>::THREADS), 1)
   __shared__ int abort_flag, n_pending, is_last, keep_first[TC_NS];
   __shared__ float join_ml[GROUPS * 128][2];
   __shared__ uint8_t row_tok[MQ];  // a row's token, from the item's first
+  static_assert(
+      fits_shared<sizeof(start) + sizeof(full) + sizeof(empty) + sizeof(qfull) + sizeof(qempty) +
+                      sizeof(s_full) + sizeof(p_full) + sizeof(pv_done) + sizeof(clean) +
+                      sizeof(stored) + sizeof(drained) + sizeof(stage_valid) +
+                      (E4M3 ? sizeof(raw_full) + sizeof(raw_empty) + sizeof(raw_valid) +
+                                  sizeof(row_scale)
+                            : 0) +
+                      sizeof(pending) + 4 * sizeof(int) + sizeof(keep_first) + sizeof(join_ml) +
+                      sizeof(row_tok),
+                  C::SMEM>,
+      "all of the above and the dynamic shared memory");
   uint8_t *ring = at_smem + C::QB * C::QBYTES;
   // what the copying warps fill: the ring itself, or (E4M3) the one that is widened into it
   uint8_t *copied = E4M3 ? ring + ST * C::STAGE : ring;
