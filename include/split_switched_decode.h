@@ -21,9 +21,13 @@
  *    allocates or frees memory. Where a call needs scratch memory it takes a caller
  *    workspace whose size comes from the matching *_workspace_bytes() query; the
  *    workspace must be zero-filled once before its first use (cudaMemset), every
- *    completed call leaves it ready for the next (a call whose kernels timed out, see
- *    Errors, does not: zero-fill it again), and one workspace must not be used by two
- *    calls that can run at the same time.
+ *    completed call leaves it ready for the next of its kind (a call whose kernels timed
+ *    out, see Errors, does not: zero-fill it again), and one workspace must not be used
+ *    by two calls that can run at the same time. Of its kind: the same entry point
+ *    with the same sizes, or attn_decode with any sizes and cache type that the
+ *    workspace is large enough for. Between calls of different kinds zero-fill it, or
+ *    give each its own: counters that have to be zero stand where another kind has
+ *    its partial sums, and nothing detects the difference.
  *  - Alignment. X, W, Wcat, Wgu, Wd and every workspace must be 16-byte aligned; K and
  *    every other reduction length must be a multiple of 8 (rows are then 16-byte
  *    multiples). Other pointers need their natural alignment.

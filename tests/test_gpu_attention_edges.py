@@ -218,3 +218,24 @@ def test_attn_bad_value_of_little_weight_in_another_part(env, D, e4m3, n, rows, 
     """Where the peak is another copy's, another softmax group's or another worker's, whose part
     makes that of the value's own vanish when they are joined."""
     _peak_and_bad_value(env, n, rows, D, e4m3, peak, bad)
+
+
+# ------------------------------------------------------------------- workspaces ----
+
+def test_attn_one_workspace_for_calls_of_any_sizes(env):
+    """Counters stand at one place whatever the heads, rows, pages and cache type are."""
+    torch, ssd, dev = env
+    cases = [_Case(env, [2500, n], [rows, 1], Hq, Hkv, D, page, e4m3, seed=D + rows)
+             for n, rows, Hq, Hkv, D, page, e4m3 in (
+                 (3, 1, 8, 1, 64, 16, False), (90, 8, 8, 1, 256, 16, False),
+                 (700, 2, 6, 3, 128, 13, True), (40, 16, 8, 2, 128, 32, False),
+                 (1, 6, 16, 1, 256, 64, True), (500, 9, 8, 1, 64, 8, True))]
+    ws = max((c.ws for c in cases), key=lambda t: t.numel())
+    for c in cases:
+        c.ws = ws
+    wants = [c.check() for c in cases]
+    for _ in range(2):
+        for c, (out, lse) in zip(cases, wants):
+            got, l = c.run()
+            assert torch.equal(got, out) and torch.equal(l, lse)
+    assert ssd.dec_sync_status() == ssd.DEC_OK
