@@ -828,7 +828,8 @@ __global__ void __launch_bounds__(AT_THREADS, (AttnCfg<E4M3, DP, NR, WR>::CTAS))
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
             int e = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
-            if (mx == 0.0f || e > 127) e = 0;  // zeros, infinities: as they are
+            if (mx == 0.0f) e = 0;
+            if (e > 127) e = 113;  // infinities: so that finite elements stay finite in f16
             if (e < -126) e = -126;
             const float f = e == 127 ? 0.5f * __uint_as_float(1u << 23)
                                      : __uint_as_float(static_cast<uint32_t>(127 - e) << 23);

@@ -239,3 +239,27 @@ def test_attn_one_workspace_for_calls_of_any_sizes(env):
             got, l = c.run()
             assert torch.equal(got, out) and torch.equal(l, lse)
     assert ssd.dec_sync_status() == ssd.DEC_OK
+
+
+# ---------------------------------------------------------------- infinite queries ----
+
+@pytest.mark.parametrize("rows", [1, 2, 8])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attn_infinite_query_beside_large_ones(env, D, e4m3, rows):
+    """A query of -infinity in one element makes every score -infinity where the keys are
+    positive there, however large its other elements are: nothing is seen."""
+    torch, ssd, dev = env
+    c = _Case(env, [70, 300], [rows, rows], 8, 1, D, 16, e4m3, seed=D)
+    kind = torch.uint8 if e4m3 else torch.int16
+    for s, n in enumerate(c.lengths):
+        for i in range(0, n, 16):
+            cell = c.kc[int(c.table[s, i // 16]), 0, :min(16, n - i)]
+            ones = torch.ones(cell.shape, device=dev).to(c.kc.dtype)
+            cell.view(kind).copy_(ones.view(kind))
+    want, want_lse = c.run()
+    c.q[0] = 1e30
+    c.q[0, :, 1] = -math.inf
+    got, lse = c.run()
+    assert not got[0].any() and bool((lse[0] == -math.inf).all())
+    assert torch.equal(got[1:], want[1:]) and torch.equal(lse[1:], want_lse[1:])
