@@ -30,8 +30,8 @@
 //     counter adds them in CTA order: the result depends on the lengths only.
 //
 // e4m3 caches are widened to f16 in registers (every e4m3 value is an f16 value); q is
-// scaled by a power of two per row so that its largest element is in [1, 2) and converted
-// to f16: exact but for elements 2^-14 below the row's largest. The key scale joins the
+// scaled by a power of two per row so that its largest element is in [2^14, 2^15) and converted
+// to f16: exact but for elements 2^-31 below the row's largest. The key scale joins the
 // score's factor, the value scale the last division.
 //
 // Measured with 8 rows a kv head (64 sequences of 0 to 8192 tokens, 8 kv heads of 128, 1045 MB):
@@ -170,6 +170,16 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   if (F16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
   else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
   return y;
+}
+__device__ __forceinline__ float power_of_two(int e) {  // e in [-126, 127]
+  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+// The power of two that a row of q whose largest element is mx is divided by on its way to f16:
+// the largest is then in [2^14, 2^15) (smaller where mx is below 2^-112; infinities leave
+// finite elements finite), and elements down to 2^-31 of it are exact, as bf16's eight bits
+// end above f16's last, 2^-24. At most 114.
+__device__ __forceinline__ int q_exponent(float mx) {
+  return max(static_cast<int>(__float_as_uint(mx) >> 23) - 127 - 14, -126);
 }
 // Transposes an 8 x 8 matrix of 16-bit elements held as one register a lane.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -827,13 +837,8 @@ __global__ void __launch_bounds__(AT_THREADS, (AttnCfg<E4M3, DP, NR, WR>::CTAS))
             }
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            int e = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
-            if (mx == 0.0f) e = 0;
-            if (e > 127) e = 113;  // infinities: so that finite elements stay finite in f16
-            if (e < -126) e = -126;
-            const float f = e == 127 ? 0.5f * __uint_as_float(1u << 23)
-                                     : __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-            const float back = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+            const int e = q_exponent(mx);
+            const float f = power_of_two(-e), back = power_of_two(e);
             zf[r][0] *= __shfl_sync(0xffffffffu, back, 8 * c4);
             zf[r][1] *= __shfl_sync(0xffffffffu, back, 8 * c4 + 4);
 #pragma unroll

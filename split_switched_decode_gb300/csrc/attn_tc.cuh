@@ -181,21 +181,16 @@ __device__ __forceinline__ float to_f32(uint32_t bits) {
              : bf16_to_f32(static_cast<uint16_t>(bits));
 }
 // Eight bf16 elements of a row of q, `lanes` neighbouring lanes a row, as f16: divided by a power
-// of two so that the row's largest is in [1, 2), exact but for elements 2^-14 below it. The
-// power goes to `scale`.
+// of two (q_exponent), which goes to `scale`.
 __device__ __forceinline__ uint4 q_to_f16(uint4 v, int lanes, float *scale) {
   float mx = fmaxf(fmaxf(fmaxf(fabsf(bf16lo(v.x)), fabsf(bf16hi(v.x))),
                          fmaxf(fabsf(bf16lo(v.y)), fabsf(bf16hi(v.y)))),
                    fmaxf(fmaxf(fabsf(bf16lo(v.z)), fabsf(bf16hi(v.z))),
                          fmaxf(fabsf(bf16lo(v.w)), fabsf(bf16hi(v.w)))));
   for (int d = 1; d < lanes; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-  int e = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
-  if (mx == 0.0f) e = 0;
-  if (e > 127) e = 113;  // infinities: so that finite elements stay finite in f16
-  if (e < -126) e = -126;
-  const float f = e == 127 ? 0.5f * __uint_as_float(1u << 23)
-                           : __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-  if (scale) *scale = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+  const int e = q_exponent(mx);
+  const float f = power_of_two(-e);
+  if (scale) *scale = power_of_two(e);
   return make_uint4(pack2<true>(bf16lo(v.x) * f, bf16hi(v.x) * f),
                     pack2<true>(bf16lo(v.y) * f, bf16hi(v.y) * f),
                     pack2<true>(bf16lo(v.z) * f, bf16hi(v.z) * f),

@@ -263,3 +263,21 @@ def test_attn_infinite_query_beside_large_ones(env, D, e4m3, rows):
     got, lse = c.run()
     assert not got[0].any() and bool((lse[0] == -math.inf).all())
     assert torch.equal(got[1:], want[1:]) and torch.equal(lse[1:], want_lse[1:])
+
+
+@pytest.mark.parametrize("power", [10, 18, 24])
+@pytest.mark.parametrize("rows", [1, 2, 8])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("D", [64, 256])
+def test_attn_query_with_one_large_element(env, D, e4m3, rows, power):
+    """An element of q far above the others that meets keys of zero: what the others give is as
+    exact as without it."""
+    torch, ssd, dev = env
+    c = _Case(env, [70, 300], [rows, rows], 8, 1, D, 16, e4m3, seed=D + power)
+    kind = torch.uint8 if e4m3 else torch.int16
+    for s, n in enumerate(c.lengths):
+        c.k[s][:, :, 3] = 0.0
+        for i in range(0, n, 16):
+            c.kc[int(c.table[s, i // 16]), :, :min(16, n - i), 3].view(kind).zero_()
+    c.q[:, :, 3] = 2.0 ** power
+    c.check()
