@@ -957,9 +957,10 @@ __global__ void __launch_bounds__(AT_THREADS, (AttnCfg<E4M3, DP, NR, WR>::CTAS))
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[r][d][e] *= fade[r][e & 1];
           }
-          // A weight of zero is to mean that the row does not see the token (see `unclean`): the
-          // least that a seen one has is 2^-100.
-          if (!plain) {
+          // Where `unclean` is looked at, a weight of zero is to mean that the row does not see the
+          // token: the least that a seen one has is 2^-100. (Done in every step that is not
+          // plain, 16 rows on an e4m3 cache took 144.7 us instead of 140.0.)
+          if (!plain && (x.n > 1 || p.window > 0)) {
 #pragma unroll
             for (int r = 0; r < NR; ++r)
 #pragma unroll
