@@ -507,11 +507,11 @@ DEC_API dec_status rope_frequencies(int rot, double base, int scaling, double fa
  * the rotation is fp32 and rounds once. Writes q_out, and K (rotated) and V (as they are, or
  * both divided by their head's scale and saturated to +-448 for DEC_KV_E4M3) to slot
  * slots[t] of the cache. A slot below 0 or not below num_pages * page_size is not written.
- * Two rows with the same slot leave one of the two there.
+ * Two rows with the same slot leave a mix of the two there.
  *
  * q [T,Hq,D], k and v [T,Hkv,D], q_out [T,Hq,D] with the given row strides (in elements):
  * the three parts of one projection's rows fit, and q_out may be q with the same stride (in
- * place). Heads are contiguous within a row. positions and slots int32 [T]; inv_freq fp32
+ * place); no other output may overlap an input. Heads are contiguous within a row. positions and slots int32 [T]; inv_freq fp32
  * [rot/2] on the device; rot even, 0..D. Row pointers are 16-byte aligned and strides
  * multiples of 8. T >= 1 (up to 2^20), Hq and Hkv 1..1024. No workspace.
  */
@@ -547,7 +547,8 @@ DEC_API dec_status rope_append(const dec_bf16 *q, int64_t q_stride, const dec_bf
  * S in 1..8192, T in 1..65536, Hq and Hkv 1..1024 with Hq % Hkv == 0. Scores, maxima, sums
  * and partial results are fp32; the weights p_j round to 16 bits for the product with V: bf16
  * on a bf16 cache (off by 2^-8 of themselves), f16 on an e4m3 one (2^-11, or 2^-32 of the row's
- * largest weight where that is more).
+ * largest weight where that is more). On an e4m3 cache elements of q below 2^-31 of their
+ * row's largest lose bits.
  * Deterministic: the split depends on the lengths, not on timing.
  */
 DEC_API size_t attn_decode_workspace_bytes(int S, int T, int Hq, int Hkv, int D);

@@ -73,12 +73,14 @@ struct AttnLaunch {
 // two for groups of workers.
 inline int attn_max_workers(int num_sms) { return 2 * num_sms; }
 // Rows of an average sequence and kv head up to which the legacy products are taken, by the
-// cache type and the padded head. bf16: up to 16 rows those keep up with the copies (16 rows, 64
-// ragged sequences: 166 us, on tcgen05 199 with pages of 16 tokens and 170 with 64; 32
-// rows: 226 and 172; 64 rows: 403 and 179). e4m3, where tcgen05 needs widened operands
-// (legacy, tcgen05; 64 ragged sequences with 1 to 4, 1 to 8 or 1 to 16 new rows of 8 heads a
-// kv head): heads of 128 230 and 209 us with 4, 422 and 225 with 8; of 64 144 and 207 with
-// 4, 256 and 180 with 8; of 256 (20 sequences) 222 and 251 with 8, 413 and 245 with 16.
+// cache type and the padded head: up to 16 rows those keep up with the copies of a bf16 cache, and
+// on an e4m3 one tcgen05 needs widened operands. Legacy / tcgen05 in us, 64 sequences (heads of
+// 256: 24) of 512 to 8192 tokens, 8 kv heads, pages of 32:
+//
+//              bf16: 16 rows     32          64          e4m3: 16     32          64
+//   heads of 64     98.7/100.9  165/103    292/112      91.7/198   156/200    289/198
+//   128              170/170    229/173    406/179       140/211   245/213    452/227
+//   256              137/137    237/142    408/152       127/231   219/233    405/235
 constexpr int tc_min_rows(bool e4m3, int dp) {
   return !e4m3 || dp == 128 ? 16 : (dp == 64 ? 32 : 48);
 }

@@ -13,7 +13,10 @@ struct AttnShape {
 };
 
 // Rows of an average sequence, which is what the host knows. More rows than an item holds
-// read the keys once more per item (mostly from L2).
+// read the keys once more per item (mostly from L2), and fewer compute on rows that are not
+// there: a batch of very unequal rows is better split into a call for each kind (63 sequences
+// of 4096 tokens with a row each beside one with a chunk of 512 rows: 464 us in one call, 165 and
+// 73 in two).
 int mean_rows(int S, int T, int Hq, int Hkv) {
   return static_cast<int>(static_cast<long long>((T + S - 1) / S) * (Hq / Hkv));
 }

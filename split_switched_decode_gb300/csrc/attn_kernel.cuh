@@ -35,15 +35,15 @@
 // score's factor, the value scale the last division.
 //
 // Measured with 8 rows a kv head (64 sequences of 0 to 8192 tokens, 8 kv heads of 128, 1045 MB):
-// 162 us, 6.4 TB/s, where a plain copy moves 6.76; an e4m3 cache over 1024 to 16384 tokens
-// (951 MB) 150 us; one sequence of 131072 tokens (537 MB) 89 us. Short calls are chains of
-// latencies: one sequence of 777 tokens takes 9.7 us where its bytes take 0.1 (start and
-// lengths, the first stage from HBM, a stage or two of products, partial results, the
-// counter, the join).
+// 161 to 163 us, 6.4 TB/s, where a plain copy moves 6.76; an e4m3 cache over 1024 to 16384
+// tokens (951 MB) 150 to 152 us; one sequence of 131072 tokens (537 MB) 90 us. Short calls are
+// chains of latencies: one sequence of 777 tokens takes 9.8 us where its bytes take 0.1 (start
+// and lengths, the first stage from HBM, a stage or two of products, and the join's way
+// through global memory: partial results, the counter, the parts read back).
 //
 // Every wait on an mbarrier is bounded; after a time-out the waits return at once, nothing
 // more is copied, and the control flow, which depends on the lengths alone, runs to its end
-// over stale data.
+// over stale data. Copies still on their way are waited for after the last wait of any warp.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -81,8 +81,10 @@ struct AttnCfg {
   static constexpr int M = MW * WR;              // rows of an item
   static constexpr int SPAN = E4M3 ? 32 : 16;    // tokens of a stage for each warp
   static constexpr int TOK = AT_CWARPS * SPAN;   // tokens of a stage
-  // tokens of an inner step: with 16 rows a warp, 32 would spill (0.5 KB a thread: 2.4 us a
-  // stage)
+  // Tokens of an inner step (e4m3, 16 rows a warp, 64 or, heads of 256, 24 ragged sequences; in
+  // brackets bytes of spill stores a thread): heads of 128 140 us with 16 (56 to 76), 199 with
+  // 32 (336 to 524); heads of 256 127 (432) and 200 (396 to 840). Heads up to 64 spill in
+  // neither, and there 32 is the faster one, 73 us where 16 takes 92: not yet told apart.
   static constexpr int STEP = NR == 1 ? SPAN : 16;
   static constexpr int RB = DP * ES;             // bytes of a token's row in a stage
   static constexpr int CPR = RB / 16;            // 16-byte chunks of a row

@@ -1,13 +1,15 @@
 // attn_tc.cuh -- attention over a paged cache for many rows a kv head (verification rows,
 // wide groups) on tcgen05 tensor cores.
 //
-// (bf16; e4m3 below.) The warps of attn_kernel.cuh take a stage's tokens against 8 rows at a time, and above 16
-// rows these chains of small products, exponentials and shuffles take longer than the keys'
-// and values' way from HBM (64 rows, 64 ragged sequences: 403 us where the copy takes 160).
-// Here a stage of 64 tokens is two products for up to 128 rows, 512 clocks of the tensor
-// core, and copying bounds it again: 179 us, 6.1 TB/s (32 rows: 172 us; 128 rows: 236 us,
-// with twice the outputs to join and write). Division of the work, ring of stages and joins are
-// attn_kernel.cuh's; one CTA an SM has sixteen warps (twelve for heads above 128):
+// (bf16; e4m3 below.) The warps of attn_kernel.cuh take a stage's tokens against 8 rows at a
+// time, and above 16 rows these chains of small products, exponentials and shuffles take longer
+// than the keys' and values' way from HBM (64 rows, 64 ragged sequences: 406 us where the copy
+// takes 160). Here a stage of 64 tokens is two products for up to 128 rows, 512 clocks of the
+// tensor core. Up to 64 rows copying bounds it: 32 rows 173 us, 64 rows 179, 6.1 TB/s. With 128
+// rows (232 us) twice the exponentials, spilled registers and twice the outputs to join and
+// write come before it; heads of 64 (64 rows: 112 us, copy 80) stop at the softmax's chain.
+// Division of the work, ring of stages and joins are attn_kernel.cuh's; one CTA an SM has sixteen
+// warps (twelve for heads above 128):
 //
 //   4 or 8  softmax: a thread a TMEM lane; MQ = 32, 64 or 128 rows an item
 //   3       TMA boxes into the ring, each every third stage
@@ -33,7 +35,7 @@
 // take).
 //
 // The running maximum that weights refer to is moved only when a row's maximum has grown by
-// more than 8 (weights then stay below 2^8, and their rounding to bf16, relative 2^-8 as the
+// 8 or more (weights then stay below 2^8, and their rounding to bf16, relative 2^-8 as the
 // output's own, is not enlarged), so the outputs in tensor memory are rarely rescaled; sums
 // are fp32 of the weights before rounding and refer to the same maximum. (On e4m3 caches, whose
 // weights are f16, to one smaller by F16_POWERS: attn_kernel.cuh.)
@@ -42,8 +44,8 @@
 // e4m3 value is an f16 value) into a short ring of operands; q is scaled by a power of two a
 // row and converted to f16, the weights are f16, the rest is the same with one softmax
 // group (a second one's registers went to the widening warps). A stage then costs about 0.8
-// us of widening, products and softmax in turn: 64 ragged sequences of 1024 to 8192 tokens with
-// up to 64 rows a kv head 225 us where the kernel of attn_kernel.cuh takes 422 (copy: 77).
+// us of widening, products and softmax in turn: 64 ragged sequences with 64 rows a kv head 225
+// to 231 us where the kernel of attn_kernel.cuh takes 437 to 452 (copy: 82).
 //
 // What is left over the copy: a segment's end (join, stores, the next item's first scores)
 // stops the copies for about 3 us, as the ring of six stages is what they need in flight;
@@ -63,7 +65,8 @@ constexpr int TC_NS = 4;  // buffers of scores
 constexpr float TC_LAZY = 8.0f;
 // An item costs what eight stages do (64 ragged sequences: 64 rows a kv head 179 us, with a
 // charge of six 182, of one 200; 128 rows 241, 251 with six, 231 with twelve, at which 32 rows
-// and short sequences lose up to 1 us). A share is one stage of an item at least.
+// and short sequences lose up to 1 us). Work that does not fill the SMs is cut into shares of
+// up to 9 units, 5 at least: one that holds only an item's charge does nothing.
 constexpr int TC_ITEM_COST = 8, TC_LEAST = 9;
 
 template <int DP, int MQ, bool E4M3>

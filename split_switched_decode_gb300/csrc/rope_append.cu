@@ -197,7 +197,8 @@ __global__ void __launch_bounds__(RA_THREADS) rope_append_kernel(const RopeParam
 }
 
 // Rotary parts that chunks of 8 do not fit (rot % 16 with half pairs, rot % 8 interleaved): a
-// thread per pair of elements.
+// thread per pair of elements, two bytes at a time. 8192 rows of 64 + 2 * 8 heads of 128 with
+// 30 or 42 elements rotated take 139 us, where chunks take 55 to 60.
 template <bool E4M3>
 __global__ void __launch_bounds__(RA_THREADS) rope_append_pairs_kernel(const RopeParams p) {
   __shared__ float2 cs[ATTN_MAX_D / 2];
