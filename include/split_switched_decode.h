@@ -561,6 +561,124 @@ DEC_API dec_status attn_decode(const dec_bf16 *q, int64_t q_stride, const void *
                                float scale, int window, dec_bf16 *out, int64_t out_stride,
                                float *lse_opt, void *ws, size_t ws_bytes, dec_stream_t s);
 
+/* ------------------------------------------------- latent attention ---------------- */
+
+/*
+ * Attention whose keys and values come from one shared latent vector a token: a token's row
+ * of the cache is R latent elements and P rotary ones, [ c | r ]. A head's key is
+ * [ U_h c | r ] and its value V_h c, which gives two forms of the same attention:
+ *
+ *   absorbed (new tokens over a cache): U_h is moved to the query, V_h behind the attention,
+ *       so that every head reads the cache's rows themselves:
+ *       latent_project (q_nope -> latent), latent_decode, latent_project (latent -> V)
+ *   expanded (prompts): keys and values of every head are computed once from the latent
+ *       vectors (one projection of all heads), and attention runs over those: latent_prompt
+ *
+ * latent_append writes the cache before either. All are asynchronous on `s` and read lengths
+ * and tables from DEVICE memory, as above; kv_plan and rope_frequencies serve them too.
+ *
+ * Latent cache. Token `off` of page p is the R + P contiguous elements at
+ * cache + p * page_stride + off * token_stride (in elements), one row for all heads; slots,
+ * block tables, types (bf16, or e4m3 that stands for value * *cache_scale, an fp32 number on
+ * the device, NULL: 1) and alignment as for the paged cache above. R and P are multiples of
+ * 64, R 64..512, P from 0, R + P at most 576 (fewer rotary elements: fill up with zeros in
+ * queries and keys, and pass fewer frequencies).
+ */
+
+/*
+ * Norm, rotary positions and the write of new tokens into the latent cache, one launch:
+ *
+ *     row t = [ c_t / sqrt(mean(c_t^2) + eps) * weight | rotated k_rope_t ]
+ *
+ * to slots[t] of the cache (rounded once to bf16, or divided by the scale, saturated to +-448
+ * and rounded to e4m3), and as bf16 to rows_opt[t] where that is not NULL; weight bf16 [R], or
+ * NULL: c is taken as it is. The rotation is rope_append's, over the first `rot` of the P
+ * elements; the same rotation of q_rope [T,H,P] goes to q_out. A slot below 0 or not below
+ * num_pages * page_size is not written; two rows with the same slot leave a mix of the two
+ * there. Sums, norm and rotation are fp32.
+ *
+ * c [T,R], k_rope [T,P], q_rope and q_out [T,H,P], rows_opt [T,R+P] with the given row (and
+ * head) strides in elements, multiples of 8, pointers 16-byte aligned: the parts of one
+ * projection's rows fit, and q_out may be the rotary part of latent_decode's queries, or q_rope
+ * itself with the same strides (in place); no other output may overlap an input or another
+ * output. H 0: no queries (P 0: H counts as 0, and k_rope may be NULL). positions and slots
+ * int32 [T]; inv_freq fp32 [rot/2]; rot a multiple of 16, 0..P. T 1..2^20, H up to 1024. No
+ * workspace.
+ */
+DEC_API dec_status latent_append(const dec_bf16 *c, int64_t c_stride, const dec_bf16 *weight,
+                                 float eps, const dec_bf16 *k_rope, int64_t k_stride,
+                                 const dec_bf16 *q_rope, int64_t q_stride, int64_t q_head,
+                                 const int32_t *positions, const int32_t *slots,
+                                 const float *inv_freq, float magnitude, int T, int H, int R,
+                                 int P, int rot, int interleaved, dec_bf16 *q_out,
+                                 int64_t q_out_stride, int64_t q_out_head, dec_bf16 *rows_opt,
+                                 int64_t rows_stride, void *cache, int kv_type,
+                                 const float *cache_scale, int num_pages, int page_size,
+                                 int64_t page_stride, int64_t token_stride, dec_stream_t s);
+
+/*
+ * One matrix a head: y[t,h,n] = sum_k x[t,h,k] W[h,n,k], fp32 sums, rounded once. Queries into
+ * the latent space (N = R) and latent outputs back to a head's elements (K = R); y may be the
+ * latent part of latent_decode's queries.
+ *
+ * x [T,H,K] and y [T,H,N] with row and head strides in elements (multiples of 8), W [H,N,K]
+ * contiguous, pointers 16-byte aligned, no overlap with y. K and N multiples of 8, up to 4096;
+ * T 1..2^20, H 1..1024. No workspace.
+ */
+DEC_API dec_status latent_project(const dec_bf16 *x, int64_t x_stride, int64_t x_head,
+                                  const dec_bf16 *W, dec_bf16 *y, int64_t y_stride,
+                                  int64_t y_head, int T, int H, int K, int N, dec_stream_t s);
+
+/*
+ * Attention of new tokens over the latent cache (absorbed form). Rows, positions, visible keys,
+ * window, missing pages, rows that see nothing, lse, determinism and limits as attn_decode:
+ *
+ *     out = sum_j p_j c_j / sum_j p_j,   p_j = exp(scale * q . [c_j | r_j] - m)
+ *
+ * for each of H heads, q [T,H,R+P] and out [T,H,R] with row strides in elements (heads
+ * contiguous). What stands in the cache at a place that a row does not see, NaN included, does
+ * not reach that row; a row that sees an element that is not finite becomes NaN, as its score
+ * is not finite (short of a score of -infinity: that token then weighs nothing, or makes the
+ * element NaN). Rounding of the weights and, for e4m3 caches, of q as attn_decode.
+ */
+DEC_API size_t latent_decode_workspace_bytes(int S, int T, int H, int R, int P);
+DEC_API dec_status latent_decode(const dec_bf16 *q, int64_t q_stride, const void *cache,
+                                 int kv_type, const float *cache_scale, int num_pages,
+                                 int page_size, int64_t page_stride, int64_t token_stride,
+                                 const int32_t *block_table, int max_pages,
+                                 const int32_t *seq_len, const int32_t *q_start, int S, int T,
+                                 int H, int R, int P, float scale, int window, dec_bf16 *out,
+                                 int64_t out_stride, float *lse_opt, void *ws, size_t ws_bytes,
+                                 dec_stream_t s);
+
+/*
+ * Causal attention of prompts (expanded form), ragged: sequence s has the rows q_start[s] ..
+ * q_start[s+1]-1 of q and the keys k_start[s] .. k_start[s+1]-1 (k_start NULL: the same, then
+ * Tk == T); its n rows stand behind the other keys, as a chunk behind what is cached: row i of
+ * n sees keys j <= len - n + i.
+ *
+ *     out = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale * (q[:N] . k_nope_j + q[N:] . k_rope_j) - m)
+ *     lse = ln sum_j exp(scale * ...)
+ *
+ * q [T,H,N+P] and out [T,H,V] with row strides (heads contiguous), k_nope [Tk,H,N] and
+ * v [Tk,H,V] with row and head strides (the two parts of one projection's rows fit), k_rope
+ * [Tk,P], shared by the heads, with a row stride; elements, multiples of 8; pointers 16-byte
+ * aligned; out overlaps no input. q_start and k_start int32 [S+1], values taken as at most T
+ * and Tk. N and V 64 or 128, P 0 (k_rope NULL allowed) or 64; lse_opt fp32 [T,H] or NULL.
+ * S 1..8192, T and Tk 1..2^20, H 1..1024. Rows of no sequence are not written; rows that see
+ * no key give 0 and -infinity. What is not finite at a key that a row does not see does not
+ * reach it; a value that is not finite makes that element of the rows that see it infinite or
+ * NaN. Scores, maxima and sums are fp32, the weights round to bf16 for the product with v.
+ * Deterministic. No workspace.
+ */
+DEC_API dec_status latent_prompt(const dec_bf16 *q, int64_t q_stride, const dec_bf16 *k_nope,
+                                 int64_t k_stride, int64_t k_head, const dec_bf16 *k_rope,
+                                 int64_t r_stride, const dec_bf16 *v, int64_t v_stride,
+                                 int64_t v_head, const int32_t *q_start, const int32_t *k_start,
+                                 int S, int T, int Tk, int H, int N, int P, int V, float scale,
+                                 dec_bf16 *out, int64_t out_stride, float *lse_opt,
+                                 dec_stream_t s);
+
 /* ------------------------------------------------------------ read stream ----- */
 
 /*

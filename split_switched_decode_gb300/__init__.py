@@ -45,6 +45,8 @@ EXPORTS = [
     "dec_read_stream_bytes", "dec_read_stream",
     "dec_debug_attn_timeout",
     "kv_plan", "rope_frequencies", "rope_append", "attn_decode_workspace_bytes", "attn_decode",
+    "latent_append", "latent_project", "latent_decode_workspace_bytes", "latent_decode",
+    "latent_prompt",
 ]
 
 KV_BF16 = 0
@@ -125,6 +127,14 @@ def _load():
         "attn_decode_workspace_bytes": (S, [I, I, I, I, I]),
         "attn_decode": (I, [P, L, P, P, I, P, P, I, I, L, L, L, P, I, P, P, I, I, I, I, I, F, I,
                             P, L, P, P, S, P]),
+        "latent_append": (I, [P, L, P, F, P, L, P, L, L, P, P, P, F, I, I, I, I, I, I, P, L, L,
+                              P, L, P, I, P, I, I, L, L, P]),
+        "latent_project": (I, [P, L, L, P, P, L, L, I, I, I, I, P]),
+        "latent_decode_workspace_bytes": (S, [I, I, I, I, I]),
+        "latent_decode": (I, [P, L, P, I, P, I, I, L, L, P, I, P, P, I, I, I, I, I, F, I, P, L,
+                              P, P, S, P]),
+        "latent_prompt": (I, [P, L, P, L, L, P, L, P, L, L, P, P, I, I, I, I, I, I, I, F, P, L,
+                              P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -561,3 +571,169 @@ def attn_decode(q, k_cache, v_cache, block_table, seq_len, out, ws, q_start=None
         _current_stream(_current_device()) if stream is None else stream.cuda_stream)
     if status:
         raise DecError(status, "attn_decode")
+
+
+# ---------------------------------------------------------- latent attention ----
+
+def _part(t, name, dims):
+    """(pointer, shape, strides) of a bf16 tensor of `dims` dimensions, the last contiguous, on
+    the current device."""
+    if t.dtype is not _BF16 or not t.is_cuda or t.dim() != dims:
+        raise TypeError(f"{name} must be a bfloat16 CUDA tensor of {dims} dimensions")
+    if t.get_device() != _current_device():
+        raise ValueError(f"{name} is not on the current device")
+    stride = t.stride()
+    if stride[-1] != 1:
+        raise TypeError(f"the last dimension of {name} must be contiguous")
+    return t.data_ptr(), t.shape, stride
+
+
+def _latent_cache(t):
+    """(type, pages, page size, width, page stride, token stride) of a [pages, page size, R + P]
+    cache."""
+    kind = t.dtype
+    if (kind is not _BF16 and kind is not _F8) or not t.is_cuda or t.dim() != 3:
+        raise TypeError("cache must be a bfloat16 or float8_e4m3fn CUDA tensor "
+                        "[pages, page size, R + P]")
+    if t.get_device() != _current_device():
+        raise ValueError("cache is not on the current device")
+    stride = t.stride()
+    if stride[2] != 1:
+        raise TypeError("the last dimension of the cache must be contiguous")
+    pages, page, width = t.shape
+    return (KV_BF16 if kind is _BF16 else KV_E4M3), pages, page, width, stride[0], stride[1]
+
+
+def latent_append(c, k_rope, positions, slots, inv_freq, cache, weight=None, eps=1e-6,
+                  q_rope=None, q_out=None, rows=None, interleaved=False, magnitude=1.0,
+                  cache_scale=None, stream=None):
+    """Write new tokens into a latent cache [pages, page size, R + P]: c [T,R], normalised with
+    `weight` [R] (None: as it is), beside k_rope [T,P] rotated; row t at positions[t] goes to
+    slots[t] (-1: not cached) and, in bf16, to rows[t]. q_rope [T,H,P] is rotated into q_out
+    (which may be q_rope). The first 2 * len(inv_freq) elements are rotated (inv_freq None:
+    none); k_rope None: a cache of R elements."""
+    lib = _attention_lib()
+    kind, pages, page, width, page_stride, token_stride = _latent_cache(cache)
+    cp, (T, R), cs = _part(c, "c", 2)
+    P = width - R
+    kp, ks, qp, qs, op, os_, rp, rs, H = None, 0, None, (0, 0), None, (0, 0), None, 0, 0
+    if k_rope is not None:
+        kp, shape, st = _part(k_rope, "k_rope", 2)
+        ks = st[0]
+        if tuple(shape) != (T, P):
+            raise ValueError("latent_append: k_rope must be [T, width of the cache - R]")
+    elif P:
+        raise ValueError("latent_append: the cache is wider than c, and k_rope is missing")
+    if q_rope is not None:
+        qp, shape, qs = _part(q_rope, "q_rope", 3)
+        op, shape2, os_ = _part(q_out, "q_out", 3)
+        H = shape[1]
+        if tuple(shape) != (T, H, P) or tuple(shape2) != (T, H, P):
+            raise ValueError("latent_append: q_rope and q_out must be [T, H, P]")
+    if rows is not None:
+        rp, shape, st = _part(rows, "rows", 2)
+        rs = st[0]
+        if tuple(shape) != (T, width):
+            raise ValueError("latent_append: rows must be [T, width of the cache]")
+    if positions.numel() != T or slots.numel() != T or \
+            (weight is not None and tuple(weight.shape) != (R,)):
+        raise ValueError("latent_append: sizes do not agree")
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    status = lib.latent_append(
+        cp, cs[0], None if weight is None else _part(weight, "weight", 1)[0], eps, kp, ks, qp,
+        qs[0], qs[1], _int32(positions, "positions"), _int32(slots, "slots"),
+        _scales(inv_freq, "inv_freq", rot // 2), magnitude, T, H, R, P, rot,
+        1 if interleaved else 0, op, os_[0], os_[1], rp, rs, cache.data_ptr(), kind,
+        _scales(cache_scale, "cache_scale", 1), pages, page, page_stride, token_stride,
+        _current_stream(_current_device()) if stream is None else stream.cuda_stream)
+    if status:
+        raise DecError(status, "latent_append")
+
+
+def latent_project(x, W, y, stream=None):
+    """y[t, h] = W[h] x[t, h] for x [T,H,K], W [H,N,K] (contiguous) and y [T,H,N]; x and y may be
+    parts of wider rows or heads, or [H,T,...] tensors transposed."""
+    lib = _attention_lib()
+    xp, (T, H, K), xs = _part(x, "x", 3)
+    wp, wshape, _ = _part(W, "W", 3)
+    yp, yshape, ys = _part(y, "y", 3)
+    N = wshape[1]
+    if tuple(wshape) != (H, N, K) or tuple(yshape) != (T, H, N):
+        raise ValueError("latent_project: sizes do not agree")
+    if not W.is_contiguous():
+        raise TypeError("W must be contiguous")
+    status = lib.latent_project(
+        xp, xs[0], xs[1], wp, yp, ys[0], ys[1], T, H, K, N,
+        _current_stream(_current_device()) if stream is None else stream.cuda_stream)
+    if status:
+        raise DecError(status, "latent_project")
+
+
+def latent_decode_workspace_bytes(S, T, H, R, P) -> int:
+    return int(_load().latent_decode_workspace_bytes(S, T, H, R, P))
+
+
+def latent_decode(q, cache, block_table, seq_len, out, ws, scale, q_start=None, window=0,
+                  lse=None, cache_scale=None, stream=None):
+    """Attention of the rows q [T,H,R+P] over a latent cache [pages, page size, R + P] into out
+    [T,H,R] (and lse [T,H]); rows, lengths, pages and window as attn_decode. `scale` has no
+    default: it belongs to the expanded heads, 1/sqrt of their elements."""
+    lib = _attention_lib()
+    kind, pages, page, width, page_stride, token_stride = _latent_cache(cache)
+    qp, (T, H, Wq), qs = _part(q, "q", 3)
+    op, (To, Ho, R), os_ = _part(out, "out", 3)
+    table = _int32(block_table, "block_table")
+    if block_table.dim() != 2:
+        raise TypeError("block_table must have two dimensions")
+    S, max_pages = block_table.shape
+    if Wq != width or R > width or To != T or Ho != H or seq_len.numel() != S or \
+            (q_start is not None and q_start.numel() != S + 1):
+        raise ValueError("latent_decode: sizes do not agree")
+    if H > 1 and (qs[1] != width or os_[1] != R):
+        raise TypeError("latent_decode: heads must be contiguous within a row")
+    if not ws.is_cuda or not ws.is_contiguous():
+        raise TypeError("ws must be a contiguous CUDA tensor")
+    status = lib.latent_decode(
+        qp, qs[0], cache.data_ptr(), kind, _scales(cache_scale, "cache_scale", 1), pages, page,
+        page_stride, token_stride, table, max_pages, _int32(seq_len, "seq_len"),
+        None if q_start is None else _int32(q_start, "q_start"), S, T, H, R, width - R, scale,
+        window, op, os_[0], _scales(lse, "lse", T * H), ws.data_ptr(), ws.nbytes,
+        _current_stream(_current_device()) if stream is None else stream.cuda_stream)
+    if status:
+        raise DecError(status, "latent_decode")
+
+
+def latent_prompt(q, k_nope, k_rope, v, q_start, out, scale, k_start=None, lse=None, stream=None):
+    """Causal attention of ragged prompts over expanded keys and values: q [T,H,N+P], k_nope
+    [Tk,H,N] and v [Tk,H,V] (parts of one [Tk,H,N+V] tensor fit), k_rope [Tk,P] for all heads
+    (None: P is 0) into out [T,H,V] (and lse [T,H]). Sequence s has the rows q_start[s] ..
+    q_start[s+1]-1 and the keys k_start[s] .. k_start[s+1]-1 (None: the same), the last of
+    which are its rows'."""
+    lib = _attention_lib()
+    qp, (T, H, D), qs = _part(q, "q", 3)
+    kp, (Tk, Hk, N), ks = _part(k_nope, "k_nope", 3)
+    vp, (Tv, Hv, V), vs = _part(v, "v", 3)
+    op, (To, Ho, Vo), os_ = _part(out, "out", 3)
+    P = D - N
+    rp, rs = None, 0
+    if k_rope is not None:
+        rp, shape, st = _part(k_rope, "k_rope", 2)
+        rs = st[0]
+        if tuple(shape) != (Tk, P):
+            raise ValueError("latent_prompt: k_rope must be [Tk, P]")
+    elif P:
+        raise ValueError("latent_prompt: q is wider than k_nope, and k_rope is missing")
+    if (Tv, Hv, Hk, To, Ho, Vo) != (Tk, H, H, T, H, V):
+        raise ValueError("latent_prompt: sizes do not agree")
+    S = q_start.numel() - 1
+    if k_start is not None and k_start.numel() != S + 1:
+        raise ValueError("latent_prompt: q_start and k_start do not agree")
+    if H > 1 and (qs[1] != D or os_[1] != V):
+        raise TypeError("latent_prompt: heads of q and out must be contiguous within a row")
+    status = lib.latent_prompt(
+        qp, qs[0], kp, ks[0], ks[1], rp, rs, vp, vs[0], vs[1], _int32(q_start, "q_start"),
+        None if k_start is None else _int32(k_start, "k_start"), S, T, Tk, H, N, P, V, scale, op,
+        os_[0], _scales(lse, "lse", T * H),
+        _current_stream(_current_device()) if stream is None else stream.cuda_stream)
+    if status:
+        raise DecError(status, "latent_prompt")

@@ -12,6 +12,8 @@
 #include "attn.h"
 #include "common.cuh"
 #include "internal.h"
+#include "latent.h"
+#include "latent.h"
 
 using namespace ssd;
 
@@ -183,6 +185,23 @@ bool host_cache_map(CUtensorMap *m, const PagedCache &c, const void *base, bool 
                   const_cast<void *>(base), dims, strides, boxes, one,
                   CU_TENSOR_MAP_INTERLEAVE_NONE,
                   row == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool host_map(CUtensorMap *m, const void *base, int es, int rank, const long long *dims,
+              const long long *strides, const int *box, bool swizzled) {
+  if (!encoder_ready()) return false;
+  cuuint64_t d[5], st[4];
+  cuuint32_t b[5], one[5] = {1, 1, 1, 1, 1};
+  for (int i = 0; i < rank; ++i) {
+    d[i] = static_cast<cuuint64_t>(dims[i]);
+    b[i] = static_cast<cuuint32_t>(box[i]);
+    if (i + 1 < rank) st[i] = static_cast<cuuint64_t>(strides[i]) * es;
+  }
+  return g_encode(m, es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                  rank, const_cast<void *>(base), d, st, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

@@ -57,6 +57,10 @@ PagedCache cache_of(const void *k, const void *v, const float *k_scale, const fl
 
 }  // namespace
 
+namespace ssd {
+bool host_attn_hold() { return g_attn_hold.load() != 0; }
+}  // namespace ssd
+
 extern "C" {
 
 dec_status kv_plan(const int32_t *kv_len, const int32_t *new_len, int S, int page_size,
@@ -261,7 +265,7 @@ dec_status attn_decode(const dec_bf16 *q, int64_t q_stride, const void *k_cache,
   uint64_t limit = 0;
   unsigned *status = host_wait_status(&limit);
   return status_of(launch_attn_decode(p, kv_type == DEC_KV_E4M3, ws, sms, status, limit,
-                                      g_attn_hold.load() != 0,
+                                      host_attn_hold(),
                                       reinterpret_cast<cudaStream_t>(s)));
 }
 

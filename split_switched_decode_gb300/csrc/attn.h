@@ -104,6 +104,8 @@ cudaError_t launch_attn_tc_e4m3(const AttnParams &p, int padded, int rows, void 
 // 128 bytes (64 where a padded head has 64 bytes) x box tokens, swizzled accordingly.
 bool host_cache_map(CUtensorMap *m, const PagedCache &c, const void *base, bool e4m3, int D,
                     int Hkv, int box, int padded);
+// api_attn.cu: whether dec_debug_attn_timeout is on.
+bool host_attn_hold();
 size_t attn_workspace_bytes(int S, int T, int Hq, int Hkv, int D, int num_sms);
 cudaError_t launch_attn_decode(const AttnParams &p, bool e4m3, void *ws, int num_sms,
                                unsigned *status, uint64_t wait_limit_ns, bool hold,

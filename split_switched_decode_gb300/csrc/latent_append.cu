@@ -1,0 +1,139 @@
+// latent_append.cu -- norm, rotary positions and the write of new tokens' latent vectors into
+// the paged latent cache.
+#include "latent.h"
+#include "rope.cuh"
+
+namespace ssd {
+namespace {
+
+constexpr int LA_THREADS = 128;
+
+// Elements 8i.. of a rotated part of `rot` elements, from its row x; cs: the row's angles.
+template <bool INTER>
+__device__ __forceinline__ void turn8(const uint16_t *x, int i, int rot, const float2 *cs,
+                                      float (&y)[8]) {
+  unpack8(*reinterpret_cast<const uint4 *>(x + 8 * i), y);
+  if (8 * i >= rot) return;
+  if (INTER) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 w = cs[4 * i + e];
+      const float r = y[2 * e] * w.x - y[2 * e + 1] * w.y;
+      y[2 * e + 1] = y[2 * e + 1] * w.x + y[2 * e] * w.y;
+      y[2 * e] = r;
+    }
+  } else {
+    const int half = rot / 2, d = 8 * i;
+    const bool low = d < half;
+    float o[8];
+    unpack8(*reinterpret_cast<const uint4 *>(x + (low ? d + half : d - half)), o);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float2 w = cs[low ? d + e : d - half + e];
+      y[e] = low ? y[e] * w.x - o[e] * w.y : y[e] * w.x + o[e] * w.y;
+    }
+  }
+}
+
+// Eight elements of a token's row of the cache at element `at`.
+template <bool E4M3>
+__device__ __forceinline__ void put_cache8(const LatentAppendParams &p, long long at,
+                                           const float (&x)[8]) {
+  if (!E4M3) {
+    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.cache) + at) = pack8(x);
+    return;
+  }
+  const float s = p.scale ? *p.scale : 1.0f;
+  uint32_t w[2] = {0u, 0u};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 y = make_float2(x[2 * k] / s, x[2 * k + 1] / s);
+    w[k >> 1] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3))
+                 << (16 * (k & 1));
+  }
+  *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.cache) + at) = make_uint2(w[0], w[1]);
+}
+
+// A CTA a token. Its latent row is one 16-byte chunk a thread (R + P is at most 576), read
+// once: the squares are summed over the CTA while the angles are computed. Its query heads are
+// units of a thread: a chunk (interleaved pairs, elements that stay) or two chunks half the
+// rotary part apart, so that every thread owns what it overwrites and q_out may be q_rope.
+// Read once and written once: the copy rate bounds it, the launch's latency when rows are few;
+// then a row's heads are cut over gridDim.y, whose first CTA has the latent row.
+template <bool E4M3, bool INTER>
+__global__ void __launch_bounds__(LA_THREADS) latent_append_kernel(const LatentAppendParams p) {
+  __shared__ float2 cs[LATENT_MAX_W / 2];
+  __shared__ float sums[LA_THREADS / 32];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int t = blockIdx.x, tid = threadIdx.x, half = p.rot / 2;
+  const bool row = blockIdx.y == 0, heads = p.H > 0 && (gridDim.y == 1 || blockIdx.y > 0);
+  const int rc = p.R / 8, wc = (p.R + p.P) / 8;
+  float y[8] = {}, sum = 0.0f;
+  if (row && tid < rc) {
+    unpack8(*reinterpret_cast<const uint4 *>(p.c + t * p.c_stride + 8 * tid), y);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum += y[e] * y[e];
+  }
+  // the threads after the latent row's have the angles
+  const int pos = p.positions[t];
+  for (int j = tid >= 64 ? tid - 64 : tid + 64; j < half; j += LA_THREADS)
+    cs[j] = rope_angle(pos, p.inv_freq[j], p.magnitude);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  if ((tid & 31) == 0) sums[tid >> 5] = sum;
+  __syncthreads();
+  if (row && tid < wc) {
+    if (tid < rc) {
+      if (p.weight) {
+        float w[8];
+        unpack8(*reinterpret_cast<const uint4 *>(p.weight + 8 * tid), w);
+        const float mean = ((sums[0] + sums[1]) + (sums[2] + sums[3])) / p.R;
+        const float inv = rsqrtf(mean + p.eps);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = y[e] * inv * w[e];
+      }
+    } else {
+      turn8<INTER>(p.k_rope + t * p.k_stride, tid - rc, p.rot, cs, y);
+    }
+    if (p.rows) *reinterpret_cast<uint4 *>(p.rows + t * p.rows_stride + 8 * tid) = pack8(y);
+    const int slot = p.slots[t];
+    // num_pages * page_size fits an int (checked on the host)
+    if (slot >= 0 && slot < p.num_pages * p.page_size) {
+      const int page = slot / p.page_size;
+      put_cache8<E4M3>(p, page * p.page_stride + (slot - page * p.page_size) * p.token_stride +
+                              8 * tid, y);
+    }
+  }
+  if (!heads) return;
+  const int turning = INTER ? p.rot / 8 : p.rot / 16, per = turning + (p.P - p.rot) / 8;
+  const int first = gridDim.y == 1 ? 0 : blockIdx.y - 1, every = gridDim.y == 1 ? 1 : gridDim.y - 1;
+  for (int u = first * LA_THREADS + tid; u < p.H * per; u += every * LA_THREADS) {
+    const int h = u / per, i = u - h * per;
+    const uint16_t *x = p.q_rope + t * p.q_stride + h * p.q_head;
+    uint16_t *o = p.q_out + t * p.out_stride + h * p.out_head;
+    const int c0 = INTER || i < turning ? i : p.rot / 8 + i - turning;  // first chunk
+    float a[8], b[8];
+    turn8<INTER>(x, c0, p.rot, cs, a);
+    if (!INTER && i < turning) turn8<INTER>(x, c0 + turning, p.rot, cs, b);
+    *reinterpret_cast<uint4 *>(o + 8 * c0) = pack8(a);
+    if (!INTER && i < turning)
+      *reinterpret_cast<uint4 *>(o + 8 * (c0 + turning)) = pack8(b);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_latent_append(const LatentAppendParams &p, bool e4m3, bool interleaved,
+                                 int num_sms, cudaStream_t s) {
+  // CTAs for one unit a thread while the row count alone does not give every SM two CTAs
+  const int turning = interleaved ? p.rot / 8 : p.rot / 16;
+  const int units = p.H * (turning + (p.P - p.rot) / 8);
+  const int cuts = p.T < 2 * num_sms && units > 0 ? 1 + (units + LA_THREADS - 1) / LA_THREADS : 1;
+  void (*kernel)(const LatentAppendParams);
+  if (interleaved) kernel = e4m3 ? latent_append_kernel<true, true> : latent_append_kernel<false, true>;
+  else kernel = e4m3 ? latent_append_kernel<true, false> : latent_append_kernel<false, false>;
+  return launch_pdl(kernel, dim3(p.T, cuts), dim3(LA_THREADS), 0, s, p);
+}
+
+}  // namespace ssd

@@ -1,0 +1,50 @@
+// latent_decode.cu -- host side of the latent attention kernel (latent_decode.cuh): rows of an
+// item, workspace and tensor map; and the kernel for bf16 caches.
+#include "latent_decode.cuh"
+
+namespace ssd {
+
+cudaError_t launch_latent_e4m3(const AttnParams &p, int width, int rows, void *ws,
+                               const AttnLaunch &a, cudaStream_t s);
+
+namespace {
+
+// Rows of an item, from those of an average sequence (what the host knows).
+int latent_rows(int S, int T, int H) {
+  const long long rows = static_cast<long long>((T + S - 1) / S) * H;
+  return rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
+}
+
+}  // namespace
+
+size_t latent_workspace_bytes(int S, int T, int H, int R, int num_sms) {
+  (void)R;  // parts are LATENT_MAX_R wide
+  const size_t M = latent_rows(S, T, H);
+  return attn_counter_bytes(num_sms) +
+         2 * static_cast<size_t>(num_sms) * (M * LATENT_MAX_R + 2 * M) * sizeof(float);
+}
+
+cudaError_t launch_latent_decode(const AttnParams &params, int width, bool e4m3, void *ws,
+                                 int num_sms, unsigned *status, uint64_t wait_limit_ns, bool hold,
+                                 cudaStream_t s) {
+  AttnParams p = params;
+  AttnLaunch a = {};
+  a.num_sms = num_sms;
+  a.status = status;
+  a.wait_limit_ns = wait_limit_ns;
+  a.hold = hold;
+  p.box = 0;
+  // boxes of 8 tokens of a page; strides of zero (a broadcast cache) or an encoder that
+  // refuses: copies by hand
+  if (p.c.page_size % 8 == 0 && p.c.page_stride > 0 && p.c.token_stride > 0) {
+    const long long dims[4] = {64, p.c.page_size, width / 64, p.c.num_pages};
+    const long long strides[3] = {p.c.token_stride, 64, p.c.page_stride};
+    const int box[4] = {64, 8, width / 64, 1};
+    if (host_map(&a.kmap, p.c.k, e4m3 ? 1 : 2, 4, dims, strides, box, !e4m3)) p.box = 8;
+  }
+  const int rows = latent_rows(p.S, p.T, p.Hq);
+  return e4m3 ? launch_latent_e4m3(p, width, rows, ws, a, s)
+              : launch_latent<false>(p, width, rows, ws, a, s);
+}
+
+}  // namespace ssd

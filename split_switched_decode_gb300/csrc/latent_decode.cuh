@@ -1,0 +1,777 @@
+// latent_decode.cuh -- attention of new tokens over a paged cache of latent vectors, on tcgen05
+// tensor cores.
+//
+// Each cached token is one row c_j of R + P elements, key of every head, and its first R
+// elements are its value:
+//
+//     out_r = sum_j p_rj c_j[:R] / sum_j p_rj,   p_rj = 2^(z_rj - m_r),   z = scale log2(e) q.c
+//
+// A row of the cache is read once for up to MQ rows (new tokens x heads) and carries
+// 2 (2R + P) MQ / (R + P) / 2 operations a byte: with 64 rows the copy rate bounds it, with 128
+// and more the tensor cores.
+//
+// Both products have the rows as N. With the rows as M the outputs, 128 x 512 in fp32, would
+// fill tensor memory, and a few heads would leave most of it empty:
+//
+//     S[64 tokens, MQ]  = C . Q^T      A = C, B = Q, both K-major in shared memory
+//     O[R, MQ]         += C^T . P      A = C as stored (MN-major), B = P[tokens, MQ] in shared
+//                                      memory, rows contiguous; four M blocks of 128 elements
+//
+// so O takes 4 MQ columns and S MQ. The tokens lie in the lanes of S; its 64 are in 16 lanes
+// of each warp's quarter (M = 64), and a thread reads four elements of each 16 x 8 block (two
+// tokens, two rows), so the four warps share the exponentials evenly and a thread holds the
+// running maximum and its tokens' part of the sum of MQ / 4 rows. The maximum is moved only
+// when a row's has grown by 8 or more (weights then stay below 2^8, and their rounding to
+// bf16, relative 2^-8, is not enlarged): the common stage needs one vote over the group and
+// no exchange of maxima. Sums are fp32, of the weights before rounding, added over lanes and
+// warps at the segment's end.
+//
+// A stage is 64 tokens: eight boxes of 8 tokens x the whole row, so any page of whole blocks
+// of 8 tokens comes in boxes; a box is laid out as one swizzle group per 64 elements (1 KB
+// each), which is the operand layout of both products with strides of a box. Other pages are
+// copied in 16-byte loads by four warps into the same layout.
+//
+// Warps: 4 softmax, 1 each for S, O and the boxes, 4 that bring the rows of q and
+//   (E4M3) widen the stages to f16, or copy the stages that boxes do not fit.
+//
+// E4M3 caches: every e4m3 value is an f16 value; q is scaled by a power of two a row and
+// converted to f16, the weights are f16 and refer to F16_POWERS below the maximum.
+//
+// Division of the work, joins and what they rely on are attn_kernel.cuh's (one kv head).
+#pragma once
+
+#include "attn_tc.cuh"
+#include "latent.h"
+
+namespace ssd {
+namespace {
+
+constexpr int LD_THREADS = 384;
+// An item is charged eight stages: its q, partial results and the join.
+constexpr int LD_ITEM_COST = 8, LD_LEAST = 9;
+
+template <int MQ, bool E4M3>
+struct LdCfg {
+  static constexpr int TOK = 64, DP = LATENT_MAX_R, SLABS = LATENT_MAX_W / 64;
+  static constexpr int STAGE = TOK * LATENT_MAX_W * 2, RAW = TOK * LATENT_MAX_W;
+  static constexpr int QBYTES = MQ * LATENT_MAX_W * 2;
+  static constexpr int PBYTES = TOK * 128;  // a token's weights in 128 bytes
+  static constexpr int QB = MQ == 64 || E4M3 ? 1 : 2;
+  static constexpr int ST = E4M3 ? 1 : 2;
+  static constexpr int RST = E4M3 ? (MQ == 64 ? 2 : 3) : 0;
+  static constexpr int NS = 4;  // buffers of scores
+  static constexpr int COLS = 8 * MQ;  // O: 4 MQ, then NS S
+  static constexpr size_t SMEM = ST * STAGE + RST * RAW + QB * QBYTES + PBYTES;
+  static constexpr int SLOT = MQ * DP + 2 * MQ;
+};
+
+// 16 lanes x 8 B columns: element (row l / 4 (+ 8), column 8 b + 2 (l % 4) (+ 1)) of block b is
+// in v[4 b + 2 (second row) + (second column)] of lane l.
+template <int B>
+__device__ __forceinline__ void tmem_ld_blocks(uint32_t taddr, float *v) {
+  uint32_t r[32];
+  if constexpr (B == 2) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7])
+        : "r"(taddr)
+        : "memory");
+  } else if constexpr (B == 4) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+  } else {
+    static_assert(B == 8, "blocks");
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+          "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+  }
+#pragma unroll
+  for (int i = 0; i < 4 * B; ++i) v[i] = __uint_as_float(r[i]);
+}
+// Whether any of the `n` threads at named barrier `id` says so.
+__device__ __forceinline__ bool named_bar_any(int id, int n, bool mine) {
+  uint32_t y;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(y)
+      : "r"(id), "r"(n), "r"(mine ? 1u : 0u)
+      : "memory");
+  return y != 0;
+}
+// Operand descriptor (128-byte swizzle): `leading` and `stride` offsets in bytes.
+__device__ __forceinline__ uint64_t sw128_any(uint32_t saddr, uint32_t leading, uint32_t stride) {
+  uint64_t d = static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>(leading >> 4) << 16;
+  d |= static_cast<uint64_t>(stride >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
+template <int MQ, bool E4M3>
+__global__ void __launch_bounds__(LD_THREADS, 1)
+    latent_decode_kernel(const __grid_constant__ CUtensorMap map,
+                         const __grid_constant__ AttnParams p, const AttnPlan pl, const int width) {
+  using C = LdCfg<MQ, E4M3>;
+  constexpr int TOK = C::TOK, ST = C::ST, QB = C::QB, NS = C::NS, DP = C::DP;
+  constexpr int NB = MQ / 8, NC = MQ / 4;  // 8-column blocks; rows of a thread
+  extern __shared__ __align__(1024) uint8_t ld_smem[];  // ring, raw ring, q, weights
+  __shared__ RangeStart<LD_THREADS> start;
+  __shared__ __align__(8) uint64_t full[ST], empty[ST], qfull[QB], qempty[QB];
+  __shared__ __align__(8) uint64_t raw_full[C::RST + 1], raw_empty[C::RST + 1];
+  __shared__ __align__(8) uint64_t s_full[NS], p_full, pv_done[NS], hold, drained[2];
+  __shared__ uint64_t stage_valid[ST], raw_valid[C::RST + 1];  // tokens that exist
+  __shared__ float part[4][MQ], top[MQ], by_row[MQ], row_scale[2][MQ];
+  __shared__ int row_pos[MQ], row_out[MQ];
+  __shared__ PendingJoin pending[2];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag, n_pending, is_last;
+  static_assert(
+      fits_shared<sizeof(start) + sizeof(full) + sizeof(empty) + sizeof(qfull) + sizeof(qempty) +
+                      2 * sizeof(raw_full) + sizeof(s_full) + sizeof(pv_done) + 8 * 4 +
+                      sizeof(stage_valid) + sizeof(raw_valid) + sizeof(part) + sizeof(top) +
+                      sizeof(by_row) + sizeof(row_scale) + sizeof(row_pos) + sizeof(row_out) +
+                      sizeof(pending) + 4 * sizeof(int),
+                  C::SMEM>,
+      "all of the above and the dynamic shared memory");
+  const int slabs = width >> 6, group_bytes = slabs << 10, stage_bytes = 8 * group_bytes;
+  uint8_t *const ring = ld_smem, *const raw = ring + ST * C::STAGE;
+  uint8_t *const q_smem = raw + C::RST * C::RAW, *const w_smem = q_smem + QB * C::QBYTES;
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bool boxes = p.box > 0;
+  const bool by_hand = E4M3 || !boxes;  // helpers fill the ring
+  if (tid == 0) {
+    abort_flag = 0;
+    n_pending = 0;
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&full[i], by_hand ? 4 : 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < C::RST; ++i) {
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_empty[i], 4);
+    }
+    for (int i = 0; i < QB; ++i) {
+      mbar_init(&qfull[i], 4);
+      mbar_init(&qempty[i], 1);
+    }
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&pv_done[i], 1);
+    }
+    mbar_init(&p_full, 128);
+    mbar_init(&hold, 1);
+    mbar_init(&drained[0], 1);
+    mbar_init(&drained[1], 1);
+    fence_mbar_init();
+    if (boxes) prefetch_tensormap(&map);
+  }
+  griddep_wait();
+  const int H = p.Hq;
+  Shares sh;
+  Cursor<TOK, MQ, LD_ITEM_COST, LD_LEAST> c;
+  if (!begin_range<LD_THREADS>(p, H, start, sh, c)) return;
+  if (warp == 4) {
+    tmem_alloc(&tmem_slot, C::COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  // after the allocation: a dependent grid's CTA cannot hold the columns this one waits for
+  griddep_launch_dependents();
+  const uint32_t tmem = tmem_slot, s_tmem = tmem + 4 * MQ;
+  auto wait = [&](uint64_t *bar, int phase) {
+    return mbar_wait_bounded(bar, phase & 1, pl.status, &abort_flag, pl.wait_limit_ns);
+  };
+  // As many barriers in turn as there are S: who waits for stage i knows that i - NS is done.
+  auto wait_pv = [&](int i) { wait(&pv_done[i % NS], i / NS); };
+  int issued = 0;  // boxes: stages that were begun
+
+  if (warp == 6) {
+    // ================================================================ boxes of the cache
+    // The pages of 32 blocks of 8 tokens are looked up in one step (four stages), a step ahead;
+    // the boxes leave from one thread.
+    constexpr int CST = E4M3 ? C::RST : ST;
+    uint64_t *const bar_full = E4M3 ? raw_full : full, *const bar_empty = E4M3 ? raw_empty : empty;
+    uint64_t *const bits_of = E4M3 ? raw_valid : stage_valid;
+    const int box_bytes = E4M3 ? group_bytes / 2 : group_bytes;
+    const uint32_t base = smem_u32(E4M3 ? raw : ring);
+    constexpr int PITCH = E4M3 ? C::RAW : C::STAGE;
+    int k = 0;
+    bool go = boxes;
+    while (go && c.next(p, H)) {
+      const int32_t *table = p.block_table + static_cast<long long>(c.s) * p.max_pages;
+      auto look_up = [&](int from, int &page, int &off) {
+        const int t = from + (lane >> 3);
+        page = -1;
+        off = 0;
+        if (t < c.t1) {
+          const int j = c.x.begin + t * TOK + ((lane & 7) << 3);
+          if (j < c.x.len) {
+            const int i = j / p.c.page_size;
+            off = j - i * p.c.page_size;
+            page = table[i];
+          }
+        }
+      };
+      int t = c.t0, page, off, next_page, next_off;
+      look_up(t, page, off);
+      look_up(t + 4, next_page, next_off);
+      while (go && t < c.t1) {
+        const uint32_t exist = __ballot_sync(0xffffffffu, page >= 0 && page < p.c.num_pages);
+        for (int i = 0; i < 4 && t < c.t1; ++i, ++t) {
+          const int at = k + t - c.t0, st = at % CST;
+          const uint32_t blocks = exist >> (8 * i) & 255u;
+          const int left = c.x.len - c.x.begin - t * TOK;
+          uint64_t bits = 0;
+#pragma unroll
+          for (int b = 0; b < 8; ++b)
+            if (blocks >> b & 1) bits |= 255ull << (8 * b);
+          if (left < TOK) bits &= (1ull << max(left, 0)) - 1;
+          if (at >= CST) {
+            go = __all_sync(0xffffffffu, wait(&bar_empty[st], at / CST - 1));
+            if (!go) break;
+          }
+          issued = at + 1;
+          if (elect_one()) {
+            bits_of[st] = bits;
+            mbar_arrive_expect_tx(&bar_full[st], __popc(blocks) * box_bytes);
+          }
+#pragma unroll 1
+          for (int b = 0; b < 8; ++b) {
+            const int pg = __shfl_sync(0xffffffffu, page, i * 8 + b);
+            const int o = __shfl_sync(0xffffffffu, off, i * 8 + b);
+            if ((blocks >> b & 1) && elect_one())
+              tma_load_4d(base + st * PITCH + b * box_bytes, &map, &bar_full[st], 0, o, 0, pg);
+            __syncwarp();
+          }
+        }
+        page = next_page;
+        off = next_off;
+        look_up(t + 4, next_page, next_off);
+      }
+      k += c.t1 - c.t0;
+    }
+  } else if (warp >= 8) {
+    // ================================================================ rows of q, stages by hand
+    const int hw = warp - 8;
+    const int chunks = width >> 3;  // 16-byte chunks of a row: at most 72
+    int k = 0, seg = 0;
+    while (c.next(p, H)) {
+      // q: a warp a row, four rows at a time
+      const int qb = seg % QB;
+      const int n_rows = min(MQ, c.x.n * H - c.rt * MQ);
+      uint8_t *qd = q_smem + qb * C::QBYTES;
+      bool waited = seg < QB;
+#pragma unroll 1
+      for (int r0 = hw; r0 < MQ; r0 += 16) {
+        uint4 v[4][3];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = r0 + 4 * e;
+          const int rr = c.rt * MQ + r, tok = rr / H, g = rr - tok * H;
+          const uint16_t *src = p.q + (c.x.q0 + tok) * p.q_stride + static_cast<long long>(g) * width;
+#pragma unroll
+          for (int i = 0; i < 3; ++i) {
+            const int ch = lane + 32 * i;
+            v[e][i] = make_uint4(0, 0, 0, 0);
+            if (r < n_rows && ch < chunks)
+              v[e][i] = *reinterpret_cast<const uint4 *>(src + ch * 8);
+          }
+        }
+        if (!waited) {
+          wait(&qempty[qb], seg / QB - 1);
+          waited = true;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = r0 + 4 * e;
+          if (E4M3) {
+            float mx = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+              const uint32_t u[4] = {v[e][i].x, v[e][i].y, v[e][i].z, v[e][i].w};
+#pragma unroll
+              for (int d = 0; d < 4; ++d) mx = fmaxf(mx, fmaxf(fabsf(bf16lo(u[d])), fabsf(bf16hi(u[d]))));
+            }
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+            const int ex = q_exponent(mx);
+            const float f = power_of_two(-ex);
+            if (lane == 0) row_scale[seg & 1][r] = power_of_two(ex);
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+              v[e][i] = make_uint4(pack2<true>(bf16lo(v[e][i].x) * f, bf16hi(v[e][i].x) * f),
+                                   pack2<true>(bf16lo(v[e][i].y) * f, bf16hi(v[e][i].y) * f),
+                                   pack2<true>(bf16lo(v[e][i].z) * f, bf16hi(v[e][i].z) * f),
+                                   pack2<true>(bf16lo(v[e][i].w) * f, bf16hi(v[e][i].w) * f));
+          }
+#pragma unroll
+          for (int i = 0; i < 3; ++i) {
+            const int ch = lane + 32 * i;
+            if (ch < chunks)
+              *reinterpret_cast<uint4 *>(qd + (ch >> 3) * (MQ * 128) + r * 128 +
+                                         (((ch & 7) ^ (r & 7)) << 4)) = v[e][i];
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&qfull[qb]);
+      ++seg;
+      if (!by_hand) continue;
+      const int32_t *table = p.block_table + static_cast<long long>(c.s) * p.max_pages;
+      for (int t = c.t0; t < c.t1; ++t, ++k) {
+        const int st = k % ST;
+        uint8_t *to = ring + st * C::STAGE;
+        if (E4M3 && boxes) {
+          const int rs = k % (C::RST + (C::RST == 0));
+          wait(&raw_full[rs], k / (C::RST + (C::RST == 0)));
+          if (k >= ST) wait(&empty[st], k / ST - 1);
+          const uint8_t *from = raw + rs * C::RAW;
+          const int n = stage_bytes / 32;  // 16-byte chunks as they came
+#pragma unroll 4
+          for (int i = tid - 256; i < n; i += 128) {
+            // chunk (slab, row, quarter) of box g
+            const int g = i / (32 * slabs), y = i - g * 32 * slabs;
+            const int slab = y >> 5, r = y >> 2 & 7, ch = (y & 3) * 2;
+            const uint4 v = *reinterpret_cast<const uint4 *>(from + i * 16);
+            uint8_t *d = to + g * group_bytes + slab * 1024 + r * 128;
+            *reinterpret_cast<uint4 *>(d + ((ch ^ r) << 4)) =
+                make_uint4(e4m3x2_to_f16x2(v.x), e4m3x2_to_f16x2(v.x >> 16),
+                           e4m3x2_to_f16x2(v.y), e4m3x2_to_f16x2(v.y >> 16));
+            *reinterpret_cast<uint4 *>(d + (((ch + 1) ^ r) << 4)) =
+                make_uint4(e4m3x2_to_f16x2(v.z), e4m3x2_to_f16x2(v.z >> 16),
+                           e4m3x2_to_f16x2(v.w), e4m3x2_to_f16x2(v.w >> 16));
+          }
+          if (tid == 256) stage_valid[st] = raw_valid[rs];
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&full[st]);
+            mbar_arrive(&raw_empty[rs]);
+          }
+        } else {
+          // 16 tokens a warp, each looked up by itself
+          const int j = c.x.begin + t * TOK + hw * 16 + (lane & 15);
+          long long at = -1;
+          if (j < c.x.len) {
+            const int i = j / p.c.page_size, pg = table[i];
+            if (pg >= 0 && pg < p.c.num_pages)
+              at = pg * p.c.page_stride + (j - i * p.c.page_size) * p.c.token_stride;
+          }
+          const uint32_t exist = __ballot_sync(0xffffffffu, at >= 0) & 0xffffu;
+          if (k >= ST) wait(&empty[st], k / ST - 1);
+          constexpr int ES = E4M3 ? 1 : 2, PER = E4M3 ? 2 : 3;  // 16-byte loads of a lane
+          const int loads = width * ES / 16;
+#pragma unroll 1
+          for (int x0 = 0; x0 < 16; x0 += 4) {
+            uint4 v[4][PER];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const long long src = __shfl_sync(0xffffffffu, at, x0 + e);
+#pragma unroll
+              for (int i = 0; i < PER; ++i) {
+                v[e][i] = make_uint4(0, 0, 0, 0);
+                if (src >= 0 && lane + 32 * i < loads)
+                  v[e][i] = *reinterpret_cast<const uint4 *>(
+                      static_cast<const uint8_t *>(p.c.k) + src * ES + (lane + 32 * i) * 16);
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int tok = hw * 16 + x0 + e, r = tok & 7;
+              uint8_t *d = to + (tok >> 3) * group_bytes + r * 128;
+#pragma unroll
+              for (int i = 0; i < PER; ++i) {
+                const int l = lane + 32 * i;
+                if (l >= loads) continue;
+                const uint4 y = v[e][i];
+                if (E4M3) {
+                  uint8_t *s = d + (l >> 2) * 1024;
+                  const int ch = (l & 3) * 2;
+                  *reinterpret_cast<uint4 *>(s + ((ch ^ r) << 4)) =
+                      make_uint4(e4m3x2_to_f16x2(y.x), e4m3x2_to_f16x2(y.x >> 16),
+                                 e4m3x2_to_f16x2(y.y), e4m3x2_to_f16x2(y.y >> 16));
+                  *reinterpret_cast<uint4 *>(s + (((ch + 1) ^ r) << 4)) =
+                      make_uint4(e4m3x2_to_f16x2(y.z), e4m3x2_to_f16x2(y.z >> 16),
+                                 e4m3x2_to_f16x2(y.w), e4m3x2_to_f16x2(y.w >> 16));
+                } else {
+                  *reinterpret_cast<uint4 *>(d + (l >> 3) * 1024 + (((l & 7) ^ r) << 4)) = y;
+                }
+              }
+            }
+          }
+          if (lane == 0)
+            reinterpret_cast<volatile uint16_t *>(&stage_valid[st])[hw] =
+                static_cast<uint16_t>(exist);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[st]);
+        }
+      }
+    }
+  } else if (warp == 4) {
+    // ================================================================ S = C . Q^T
+    const uint32_t id = (tc_idesc<E4M3>(MQ) & ~(31u << 24)) | (64u >> 4) << 24;
+    const uint32_t q_u = smem_u32(q_smem), ring_u = smem_u32(ring);
+    int k = 0, seg = 0;
+    while (c.next(p, H)) {
+      const int qb = seg % QB;
+      wait(&qfull[qb], seg / QB);
+      for (int t = c.t0; t < c.t1; ++t, ++k) {
+        const int st = k % ST;
+        wait(&full[st], k / ST);
+        if (k >= NS) wait_pv(k - NS);  // its S has been read
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t d = s_tmem + (k % NS) * MQ;
+          uint64_t a = sw128_any(ring_u + st * C::STAGE, 16, group_bytes);
+          uint64_t b = sw128_any(q_u + qb * C::QBYTES, 16, 1024);
+#pragma unroll 1
+          for (int slab = 0; slab < slabs; ++slab) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tc_mma(d, a + 2 * kk, b + 2 * kk, id, kk > 0 || slab > 0 ? 1u : 0u);
+            a += 1024 >> 4;
+            b += (MQ * 128) >> 4;
+          }
+          tc_commit(&s_full[k % NS]);
+          if (t + 1 == c.t1) tc_commit(&qempty[qb]);
+        }
+        __syncwarp();
+      }
+      ++seg;
+    }
+  } else if (warp == 5) {
+    // ================================================================ O += C^T . P
+    const uint32_t id = tc_idesc<E4M3>(MQ) | (1u << 15) | (1u << 16);
+    const uint32_t ring_u = smem_u32(ring);
+    const uint64_t b = sw128_any(smem_u32(w_smem), 1024, 1024);
+    const int blocks = (p.D + 127) >> 7;
+    int k = 0;
+    while (c.next(p, H)) {
+      for (int t = c.t0; t < c.t1; ++t, ++k) {
+        const int st = k % ST;
+        wait(&p_full, k);
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t acc = t > c.t0 ? 1u : 0u;
+          const uint64_t a = sw128_any(ring_u + st * C::STAGE, 1024, group_bytes);
+#pragma unroll
+          for (int kk = 0; kk < TOK / 16; ++kk)  // two boxes of tokens
+#pragma unroll 1
+            for (int blk = 0; blk < blocks; ++blk)
+              tc_mma(tmem + blk * MQ, a + ((2 * kk * group_bytes + blk * 2048) >> 4),
+                     b + ((kk * 2048) >> 4), id, kk > 0 ? 1u : acc);
+          tc_commit(&empty[st]);
+          tc_commit(&pv_done[k % NS]);
+        }
+        __syncwarp();
+      }
+    }
+    if (k > 0) wait_pv(k - 1);  // nothing in flight when the columns are released
+  } else if (warp < 4) {
+    // ================================================================ softmax
+    constexpr uint32_t INF2 = E4M3 ? 0x7c007c00u : 0x7f807f80u;  // exponents of two values
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    const int col = 2 * (lane & 3), tok0 = warp * 16 + (lane >> 2);  // and 8 b + col + 1, tok0 + 8
+    const float scale = p.scale * LOG2E * (p.c.k_scale ? p.c.k_scale[0] : 1.0f);
+    int k = 0, seg = 0;
+    if (pl.hold) wait(&hold, 0);  // self-test: nobody arrives
+    while (c.next(p, H)) {
+      const SeqInfo &x = c.x;
+      const int n_rows = min(MQ, x.n * H - c.rt * MQ), row0 = c.rt * MQ;
+      const int pos0 = x.len - x.n;
+      // the last key that a row sees; what every row sees
+      if (tid < MQ) row_pos[tid] = pos0 + (row0 + min(tid, n_rows - 1)) / H;
+      const int hi_all = pos0 + row0 / H, hi_top = pos0 + (row0 + n_rows - 1) / H;
+      const int lo_all = p.window > 0 && hi_top >= p.window ? hi_top - p.window + 1 : 0;
+      named_bar_sync(1, 128);
+      float m[NC], l[NC];  // rows 8 b + col, 8 b + col + 1
+#pragma unroll
+      for (int i = 0; i < NC; ++i) m[i] = -INFINITY, l[i] = 0.0f;
+      for (int t = c.t0; t < c.t1; ++t, ++k) {
+        const int st = k % ST;
+        wait(&s_full[k % NS], k / NS);
+        tc_fence_after();
+        float z[4 * NB];
+        tmem_ld_blocks<NB>(s_tmem + (k % NS) * MQ + lanes, z);
+        wait(&full[st], k / ST);  // (long since) the copying warps' bits and the values
+        const uint64_t valid = stage_valid[st];
+        const int j0 = x.begin + t * TOK;
+        const bool plain = valid == ~0ull && j0 >= lo_all && j0 + TOK - 1 <= hi_all;
+        tmem_wait_ld();
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float f = scale;
+            if (E4M3) f *= row_scale[seg & 1][8 * b + col + (e & 1)];
+            z[4 * b + e] *= f;
+          }
+        if (!plain) {
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int tok = tok0 + 8 * (e >> 1), j = j0 + tok;
+              const int hi = row_pos[8 * b + col + (e & 1)];
+              const int lo = p.window > 0 && hi >= p.window ? hi - p.window + 1 : 0;
+              if (j < lo || j > hi || !(valid >> tok & 1)) z[4 * b + e] = -INFINITY;
+            }
+        }
+        bool grows = false;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float mx = fmaxf(z[4 * b + e], z[4 * b + 2 + e]);
+            if (E4M3) mx -= F16_POWERS;
+            grows |= mx - m[2 * b + e] >= TC_LAZY;
+          }
+        const bool begins = t == c.t0;
+        if (named_bar_any(1, 128, grows || begins)) {
+          // move the maxima that grew; the outputs so far are rescaled in tensor memory, after
+          // the last product that adds to them
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float mx = fmaxf(z[4 * b + e], z[4 * b + 2 + e]);
+#pragma unroll
+              for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+              if (lane < 4) part[warp][8 * b + col + e] = mx;
+            }
+          named_bar_sync(1, 128);
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int r = 8 * b + col + e;
+              float mx = fmaxf(fmaxf(part[0][r], part[1][r]), fmaxf(part[2][r], part[3][r]));
+              if (E4M3) mx -= F16_POWERS;
+              // (each by itself: a row's bits do not depend on what only other rows see)
+              const float old = m[2 * b + e], now = mx - old >= TC_LAZY ? mx : old;
+              const float fade = ex2(old - (now == -INFINITY ? 0.0f : now));
+              m[2 * b + e] = now;
+              l[2 * b + e] *= fade;
+              if (warp == 0 && lane < 4) by_row[r] = fade;
+            }
+          if (!begins) {
+            named_bar_sync(1, 128);
+            wait_pv(k - 1);
+            tc_fence_after();
+#pragma unroll 1
+            for (int i = 0; i < (p.D + 127) / 128 * MQ; i += 16) {
+              float o[16];
+              uint32_t u[16];
+              tmem_ld16(tmem + lanes + i, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                u[e] = __float_as_uint(o[e] * by_row[(i + e) % MQ]);
+              tmem_st16(tmem + lanes + i, u);
+            }
+            tmem_wait_st();
+          }
+        }
+        uint32_t w[2 * NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const float b0 = m[2 * b] == -INFINITY ? 0.0f : m[2 * b];
+          const float b1 = m[2 * b + 1] == -INFINITY ? 0.0f : m[2 * b + 1];
+          const float y0 = ex2(z[4 * b] - b0), y1 = ex2(z[4 * b + 1] - b1);
+          const float y2 = ex2(z[4 * b + 2] - b0), y3 = ex2(z[4 * b + 3] - b1);
+          l[2 * b] += y0 + y2;
+          l[2 * b + 1] += y1 + y3;
+          w[2 * b] = pack2<E4M3>(y0, y1);
+          w[2 * b + 1] = pack2<E4M3>(y2, y3);
+        }
+        if (k > 0) wait_pv(k - 1);  // it reads the weights
+        const int r = lane >> 2;
+        uint8_t *d = w_smem + tok0 * 128 + (lane & 3) * 4;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          *reinterpret_cast<uint32_t *>(d + ((b ^ r) << 4)) = w[2 * b];
+          *reinterpret_cast<uint32_t *>(d + 1024 + ((b ^ r) << 4)) = w[2 * b + 1];
+        }
+        if (!plain) {
+          // Weights of zero must not meet what is not finite: tokens that do not exist get
+          // zeros, and so does what is not finite in a token that some row does not see. (A
+          // row that sees it has a score that is not finite either: its weight is NaN, or
+          // zero where the score is -infinity.)
+          uint8_t *v = ring + st * C::STAGE;
+          const int cpr = p.D >> 3;  // chunks of a value
+          const int head = min(max(lo_all - j0, 0), TOK), tail = min(max(hi_all + 1 - j0, 0), TOK);
+          auto clean = [&](int row) {
+            const bool gone = !(valid >> row & 1);
+            uint8_t *at = v + (row >> 3) * group_bytes + (row & 7) * 128;
+            for (int i = lane; i < cpr; i += 32) {
+              uint4 *y = reinterpret_cast<uint4 *>(at + (i >> 3) * 1024 +
+                                                   (((i & 7) ^ (row & 7)) << 4));
+              if (gone) {
+                *y = make_uint4(0, 0, 0, 0);
+              } else {
+                const uint4 u = *y;
+                const uint4 bad = make_uint4(
+                    __vcmpeq2(u.x & INF2, INF2), __vcmpeq2(u.y & INF2, INF2),
+                    __vcmpeq2(u.z & INF2, INF2), __vcmpeq2(u.w & INF2, INF2));
+                if (bad.x | bad.y | bad.z | bad.w)
+                  *y = make_uint4(u.x & ~bad.x, u.y & ~bad.y, u.z & ~bad.z, u.w & ~bad.w);
+              }
+            }
+          };
+          // tokens that all rows see and that exist need no look
+          for (int row = warp; row < TOK; row += 4)
+            if (row < head || row >= tail || !(valid >> row & 1)) clean(row);
+        }
+        fence_proxy_async_smem();  // before the product (and later boxes) touch either
+        tc_fence_before();
+        mbar_arrive(&p_full);
+      }
+
+      // ---- the segment's outputs: sums over lanes and warps, then a thread a latent element
+      const int me = blockIdx.x;
+      const long long unit = c.item + LD_ITEM_COST;
+      const int c0 = sh.worker_of(unit), c1 = sh.worker_of(unit + x.kt - 1);
+      const float v_scale = p.c.v_scale ? p.c.v_scale[0] : 1.0f;
+      const ItemOut dst = {x.q0, row0, 0, H, v_scale};
+      float *slot = pl.partials + static_cast<size_t>(part_slot(c0, me - c0)) * C::SLOT;
+      named_bar_sync(1, 128);  // `part` may still be read
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        float s = l[i];
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+        const int r = 8 * (i >> 1) + col + (i & 1);
+        if (lane < 4) {
+          part[warp][r] = s;
+          if (warp == 0) top[r] = m[i];
+        }
+      }
+      named_bar_sync(1, 128);
+      if (tid < n_rows) {
+        const float mr = top[tid];
+        const float lr = (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]);
+        if (c0 == c1) {
+          dst.put_lse(p, tid, mr, lr);
+          by_row[tid] = lr == 0.0f ? 0.0f : v_scale / lr;
+        } else {
+          *reinterpret_cast<float2 *>(slot + MQ * DP + 2 * tid) = make_float2(mr, lr);
+        }
+        row_out[tid] = (row0 + tid) / H;
+      }
+      if (k > 0) wait_pv(k - 1);
+      tc_fence_after();
+      named_bar_sync(1, 128);
+#pragma unroll 1
+      for (int d0 = 0; d0 < p.D; d0 += 128) {
+        const int dim = d0 + tid;  // past D in a last half block
+#pragma unroll 1
+        for (int r0 = 0; r0 < n_rows; r0 += 16) {
+          float o[16];
+          tmem_ld16(tmem + lanes + (d0 >> 7) * MQ + r0, o);
+          tmem_wait_ld();
+          if (c0 == c1) {
+            // two rows at a time: an even lane has two elements of the first, an odd one of
+            // the second
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const float f0 = by_row[r0 + e], f1 = by_row[r0 + e + 1];
+              // a row that saw nothing: zeros, whatever its columns hold
+              const float y0 = f0 == 0.0f ? 0.0f : o[e] * f0;
+              const float y1 = f1 == 0.0f ? 0.0f : o[e + 1] * f1;
+              const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? y0 : y1, 1);
+              const int r = r0 + e + (lane & 1);
+              if (r < n_rows && dim < p.D) {
+                const int tok = row_out[r], head = row0 + r - tok * H;
+                *reinterpret_cast<uint32_t *>(p.out + (x.q0 + tok) * p.out_stride +
+                                              static_cast<long long>(head) * p.D + (dim & ~1)) =
+                    lane & 1 ? pack2<false>(got, y1) : pack2<false>(y0, got);
+              }
+            }
+          } else if (dim < p.D) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (r0 + e < n_rows) slot[(r0 + e) * DP + dim] = o[e];
+          }
+        }
+      }
+      tc_fence_before();  // the next segment's products overwrite the columns
+      named_bar_sync(1, 128);
+      if (c0 != c1 && tid == 0) count_part(pl, me, c0, c1, n_rows, dst, pending, &n_pending);
+      ++seg;
+    }
+  }
+  static_assert(ST * C::STAGE >= 2 * AT_GROUP * MQ * 8, "ml of a join");
+  run_joins<MQ, DP, LD_THREADS>(p, pl, reinterpret_cast<float2 *>(ring), pending, &n_pending,
+                                &is_last);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  // Every wait of the CTA is over. If one ran out, products and boxes may still be on their way:
+  // products end before tensor memory is released, boxes land before the CTA ends.
+  if (*static_cast<volatile int *>(&abort_flag)) {
+    if (warp == 4 || warp == 5) {
+      uint64_t *bar = &drained[warp - 4];
+      if (elect_one()) tc_commit(bar);
+      __syncwarp();
+      mbar_wait_drain(bar, 0, 10000000ull);
+    }
+    constexpr int CST = E4M3 ? C::RST : ST;
+    uint64_t *const bar_full = E4M3 ? raw_full : full;
+    for (int i = issued - 1; i >= 0 && i >= issued - CST; --i)
+      mbar_wait_drain(&bar_full[i % CST], (i / CST) & 1, 10000000ull);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+  }
+  if (warp == 4) tmem_dealloc(tmem, C::COLS);
+}
+
+template <int MQ, bool E4M3>
+cudaError_t launch_latent_shape(const AttnParams &p, int width, void *ws, const AttnLaunch &a,
+                                cudaStream_t s) {
+  using C = LdCfg<MQ, E4M3>;
+  auto kernel = latent_decode_kernel<MQ, E4M3>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(C::SMEM));
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kernel, dim3(a.num_sms), dim3(LD_THREADS), C::SMEM, s, a.kmap, p,
+                    make_plan(ws, a), width);
+}
+
+template <bool E4M3>
+cudaError_t launch_latent(const AttnParams &p, int width, int rows, void *ws,
+                          const AttnLaunch &a, cudaStream_t s) {
+  switch (rows) {
+    case 16:
+      return launch_latent_shape<16, E4M3>(p, width, ws, a, s);
+    case 32:
+      return launch_latent_shape<32, E4M3>(p, width, ws, a, s);
+    default:
+      return launch_latent_shape<64, E4M3>(p, width, ws, a, s);
+  }
+}
+
+}  // namespace
+}  // namespace ssd

@@ -1,0 +1,11 @@
+// latent_decode_e4m3.cu -- the latent attention kernel for e4m3 caches.
+#include "latent_decode.cuh"
+
+namespace ssd {
+
+cudaError_t launch_latent_e4m3(const AttnParams &p, int width, int rows, void *ws,
+                               const AttnLaunch &a, cudaStream_t s) {
+  return launch_latent<true>(p, width, rows, ws, a, s);
+}
+
+}  // namespace ssd

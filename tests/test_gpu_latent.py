@@ -1,0 +1,713 @@
+"""GPU parity of latent_append, latent_project, latent_decode and latent_prompt with plain 64-bit
+forms.
+
+Tolerances, derived from the arithmetic (u = 2^-8 is bf16's unit roundoff):
+  - latent_append: u |y| for the rounding, plus 2^-18 |y| for a fp32 norm (a sum of squares in
+    chains of 15 additions, a reciprocal root, two products), or 2^-20 (|x0| + |x1|) for a fp32
+    rotation; e4m3: unit roundoff 2^-4, half of the smallest step 2^-10.
+  - latent_project: u |y| plus (K + 2) 2^-24 sum_k |x_k W_k| for fp32 sums.
+  - latent_decode, latent_prompt: u |out| for the last rounding; u sum_j w_j |v_j| for weights
+    that round to 16 bits before the product; and twice the relative error of the weights, which
+    is the absolute error of a fp32 score, (D + 16) 2^-24 scale sum_d |q_d k_d|, plus 2^-18 for
+    exponentials and sums. lse: the score's error, 2^-18, and 2^-22 |lse|.
+"""
+import math
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -8
+
+
+@pytest.fixture(scope="module")
+def env():
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import split_switched_decode_gb300 as ssd
+    ssd.build()
+    dev = torch.device("cuda:0")
+    torch.cuda.set_device(dev)
+    return torch, ssd, dev
+
+
+def _gen(torch, dev, seed):
+    g = torch.Generator(device=dev)
+    g.manual_seed(seed)
+    return g
+
+
+def _randn(torch, dev, g, *shape):
+    return torch.randn(shape, generator=g, device=dev).to(torch.bfloat16)
+
+
+def _i32(torch, x, dev):
+    return torch.tensor(list(x), dtype=torch.int32, device=dev)
+
+
+def _starts(counts):
+    at = [0]
+    for n in counts:
+        at.append(at[-1] + n)
+    return at
+
+
+def _within(got, want, bound, what):
+    err = (got.double() - want).abs()
+    ok = (err <= bound) | ((got.double() == want) & want.isinf()) | (got.isnan() & want.isnan())
+    assert bool(ok.all()), (what, int((~ok).sum()), ok.numel(),
+                            float((err / bound.clamp(min=1e-300))[~ok].max()))
+
+
+# ----------------------------------------------------------------- append ----
+
+def _append(env, T, H, R, P, rot, interleaved, e4m3, page, rows, norm=True, seed=0, max_pos=131072,
+            pad=0):
+    torch, ssd, dev = env
+    import latent_ref
+    g = _gen(torch, dev, 100 + seed + T + R)
+    down = _randn(torch, dev, g, T, R + P + pad)
+    up = _randn(torch, dev, g, T, max(H, 1), 32 + P)
+    c, k_rope = down[:, :R], down[:, R:R + P] if P else None
+    q_rope = up[..., 32:] if H and P else None
+    pages = -(-T // page) + 1
+    dtype = torch.float8_e4m3fn if e4m3 else torch.bfloat16
+    cache = torch.zeros((pages, page, R + P), device=dev).to(dtype)
+    scale = torch.full((1,), 0.0173, device=dev) if e4m3 else None
+    weight = (torch.rand(R, generator=g, device=dev) + 0.5).to(torch.bfloat16) if norm else None
+    positions = torch.randint(0, max_pos, (T,), generator=g, device=dev, dtype=torch.int32)
+    slots = torch.randperm(pages * page, generator=g, device=dev)[:T].to(torch.int32)
+    skipped = T > 2
+    if skipped:
+        slots[1], slots[2] = -1, pages * page  # neither is written
+    inv, mag = ssd.rope_frequencies(rot, device=dev) if rot else (None, 1.0)
+    mag = 1.25 if rot else 1.0
+    q = torch.full((T, max(H, 1), R + P), 7.0, device=dev).to(torch.bfloat16)
+    kept = torch.full((T, R + P), 7.0, device=dev).to(torch.bfloat16) if rows else None
+    ssd.latent_append(c, k_rope, positions, slots, inv, cache, weight=weight, eps=1e-5,
+                      q_rope=q_rope, q_out=q[..., R:] if q_rope is not None else None, rows=kept,
+                      interleaved=interleaved, magnitude=mag, cache_scale=scale)
+    torch.cuda.synchronize()
+    want = latent_ref.normed(c, weight, 1e-5) if norm else c.double()
+    size = want.abs() * 2.0 ** -18
+    freq = inv if inv is not None else torch.zeros(0, device=dev)
+    if P:
+        r, rs = latent_ref.rotate(k_rope.double(), positions, freq, mag, interleaved)
+        want, size = torch.cat([want, r], -1), torch.cat([size, rs * 2.0 ** -20], -1)
+    if rows:
+        _within(kept, want, U * want.abs() + size + 1e-38, "rows")
+    flat = cache.float().double().view(-1, R + P)
+    held = want / scale.double() if e4m3 else want
+    size = size / scale.double() if e4m3 else size
+    if e4m3:
+        held = held.clamp(-448, 448)
+    unit, least = (2.0 ** -4, 2.0 ** -10) if e4m3 else (U, 1e-38)
+    live = torch.ones(T, dtype=torch.bool, device=dev)
+    if skipped:
+        live[1:3] = False
+    at = slots[live].long()
+    _within(flat[at], held[live], unit * held[live].abs() + size[live] + least, "cache")
+    rest = torch.ones(flat.shape[0], dtype=torch.bool, device=dev)
+    rest[at] = False
+    assert bool((flat[rest] == 0).all())
+    if q_rope is not None:
+        w, s = latent_ref.rotate(q_rope.double(), positions, freq, mag, interleaved)
+        _within(q[..., R:], w, U * w.abs() + s * 2.0 ** -20 + 1e-38, "q")
+        assert bool((q[..., :R] == 7.0).all())
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("T,H,R,P,rot,page", [
+    (1, 64, 512, 64, 64, 16), (1, 1, 64, 64, 32, 1), (3, 16, 512, 64, 64, 7), (37, 128, 256, 64, 48, 16),
+    (303, 5, 448, 128, 128, 64), (304, 8, 512, 64, 16, 16), (700, 16, 192, 64, 0, 48),
+])
+def test_append(env, T, H, R, P, rot, page, interleaved, e4m3):
+    _append(env, T, H, R, P, rot, interleaved, e4m3, page, rows=T % 2 == 1, pad=16 * (T % 3))
+
+
+def test_append_no_rotary_part_no_queries_no_norm(env):
+    _append(env, 5, 0, 512, 0, 0, False, False, 16, rows=True)
+    _append(env, 5, 0, 512, 64, 64, True, True, 16, rows=True, norm=False)
+    _append(env, 2000, 0, 512, 64, 64, False, False, 16, rows=False)
+
+
+def test_append_far_positions_and_in_place(env):
+    torch, ssd, dev = env
+    import latent_ref
+    g = _gen(torch, dev, 5)
+    T, H = 9, 12
+    c, r, q = (_randn(torch, dev, g, *s) for s in ((T, 512), (T, 64), (T, H, 192)))
+    positions = _i32(torch, [0, 1, 2 ** 31 - 1, 2 ** 30 + 1, 999999937, 131071, 17, 2 ** 24 + 1, 5], dev)
+    inv, _ = ssd.rope_frequencies(64, device=dev)
+    cache = torch.zeros((2, 8, 576), device=dev).to(torch.bfloat16)
+    for interleaved in (False, True):
+        x = q.clone()
+        ssd.latent_append(c, r, positions, torch.arange(T, dtype=torch.int32, device=dev), inv, cache,
+                          q_rope=x[..., 128:], q_out=x[..., 128:], interleaved=interleaved)
+        w, s = latent_ref.rotate(q[..., 128:].double(), positions, inv, 1.0, interleaved)
+        _within(x[..., 128:], w, U * w.abs() + s * 2.0 ** -20, "q")
+        assert torch.equal(x[..., :128], q[..., :128])
+        assert torch.equal(cache.view(-1, 576)[:T, :512], c)
+
+
+# ---------------------------------------------------------------- project ----
+
+def _project(env, T, H, K, N, x_pad=0, y_pad=0, heads_first=False, seed=0):
+    torch, ssd, dev = env
+    g = _gen(torch, dev, 200 + seed + T + K + N)
+    x = _randn(torch, dev, g, T, H, K + x_pad)[..., x_pad:]
+    w = _randn(torch, dev, g, H, N, K)
+    whole = torch.full((H, T, N + y_pad) if heads_first else (T, H, N + y_pad), 3.0, device=dev) \
+        .to(torch.bfloat16)
+    y = (whole.transpose(0, 1) if heads_first else whole)[..., :N]
+    ssd.latent_project(x, w, y)
+    torch.cuda.synchronize()
+    want = torch.einsum("thk,hnk->thn", x.double(), w.double())
+    size = torch.einsum("thk,hnk->thn", x.double().abs(), w.double().abs())
+    _within(y, want, U * want.abs() + (K + 2) * 2.0 ** -24 * size, "y")
+    if y_pad:
+        assert bool((whole[..., N:] == 3.0).all())
+
+
+@pytest.mark.parametrize("T,H,K,N", [
+    (1, 64, 128, 512), (1, 1, 8, 8), (2, 3, 512, 128), (17, 16, 72, 200), (63, 5, 512, 128),
+    (64, 64, 512, 128), (65, 4, 128, 512), (127, 3, 192, 256), (128, 2, 64, 64), (129, 7, 136, 264),
+    (300, 16, 128, 512), (1000, 2, 512, 136), (513, 1, 1024, 8), (33, 2, 4096, 64),
+])
+def test_project(env, T, H, K, N):
+    _project(env, T, H, K, N)
+
+
+@pytest.mark.parametrize("T", [1, 50, 200])
+def test_project_strides(env, T):
+    _project(env, T, 6, 128, 512, x_pad=64, y_pad=64)
+    _project(env, T, 6, 512, 128, y_pad=8, heads_first=True)
+    _project(env, T, 1, 128, 256, x_pad=8, y_pad=16)
+
+
+# ----------------------------------------------------------------- decode ----
+
+def _cache_of(torch, dev, g, tokens, e4m3, scale):
+    x = torch.randn(tokens, generator=g, device=dev)
+    if not e4m3:
+        return x.to(torch.bfloat16)
+    return (x / scale).clamp(-448, 448).to(torch.float8_e4m3fn)
+
+
+def _values(torch, cache):
+    return cache.float().double()
+
+
+class _Decode:
+    """One batch: ragged lengths and rows over a paged cache, and its reference."""
+
+    def __init__(self, env, lens, rows, H, R=512, P=64, page=16, e4m3=False, window=0, scale=0.06,
+                 seed=0, pad=0, grow=0.0, poison=False, drop=()):
+        torch, ssd, dev = env
+        self.env, self.H, self.R, self.W, self.page = env, H, R, R + P, page
+        self.lens, self.rows, self.window, self.scale = list(lens), list(rows), window, scale
+        g = _gen(torch, dev, 300 + seed + sum(lens) + H)
+        used = [-(-n // page) for n in lens]
+        total = sum(used) + 3
+        width = max(1, max(used)) + 1
+        self.c_scale = torch.full((1,), 0.013, device=dev) if e4m3 else None
+        store = _cache_of(torch, dev, g, (total, page, self.W + pad), e4m3, 0.013)
+        self.cache = store[..., :self.W]
+        ids = torch.randperm(total, generator=g, device=dev).to(torch.int32)
+        table = torch.full((len(lens), width), -1, dtype=torch.int32, device=dev)
+        at = 0
+        for s, n in enumerate(used):
+            table[s, :n] = ids[at:at + n]
+            at += n
+        if grow:  # later tokens score higher and higher
+            q_dir = torch.randn(self.W, generator=g, device=dev)
+            for s, n in enumerate(lens):
+                for i in range(used[s]):
+                    p = int(table[s, i])
+                    j = torch.arange(i * page, (i + 1) * page, device=dev)
+                    x = self.cache[p].float() * 0.1 + q_dir * (grow * j[:, None])
+                    self.cache[p] = x.to(store.dtype)
+        self.exists = []
+        for s, n in enumerate(lens):
+            e = torch.ones(n, dtype=torch.bool, device=dev)
+            for i in range(used[s]):
+                if (s, i) in drop:
+                    table[s, i] = -1 if i % 2 else total
+                    e[i * page:(i + 1) * page] = False
+            self.exists.append(e)
+        if poison:  # everything that no row sees
+            mark = torch.zeros((total, page), dtype=torch.bool, device=dev)
+            for s, n in enumerate(lens):
+                first = max(0, n - rows[s] - window + 1) if window else 0
+                for j in range(first, n):
+                    p = int(table[s, j // page])
+                    if 0 <= p < total:
+                        mark[p, j % page] = True
+            raw = store.view(torch.uint8) if e4m3 else store.view(torch.int16)
+            raw[~mark] = 0x7f if e4m3 else 0x7fc0
+        self.table = table
+        T = sum(rows)
+        self.T = T
+        self.q = _randn(torch, dev, g, T + 2, H, self.W)
+        if grow:
+            self.q = (self.q.float() * 0.1 + q_dir).to(torch.bfloat16)
+        self.seq_len = _i32(torch, lens, dev)
+        self.q_start = _i32(torch, _starts(rows), dev)
+        self.out = torch.full((T + 2, H, R), 5.0, device=dev).to(torch.bfloat16)
+        self.lse = torch.full((T + 2, H), 5.0, device=dev)
+        self.ws = ssd.workspace(ssd.latent_decode_workspace_bytes(len(lens), T + 2, H, R, P), dev)
+
+    def run(self, stream=None):
+        self.env[1].latent_decode(self.q, self.cache, self.table, self.seq_len, self.out, self.ws,
+                                  self.scale, q_start=self.q_start, window=self.window,
+                                  lse=self.lse, cache_scale=self.c_scale, stream=stream)
+
+    def reference(self):
+        torch, ssd, dev = self.env
+        import latent_ref
+        parts = []
+        t = 0
+        for s, (n, r) in enumerate(zip(self.lens, self.rows)):
+            pages = self.table[s, :-(-n // self.page)].long()
+            ok = (pages >= 0) & (pages < self.cache.shape[0])
+            raw = self.cache.contiguous()
+            raw = raw.view(torch.uint8)[pages.clamp(0, raw.shape[0] - 1)].view(raw.dtype)
+            keys = _values(torch, raw).reshape(-1, self.W)[:n]
+            if self.c_scale is not None:
+                keys = keys * self.c_scale.double()
+            keys = torch.where(self.exists[s][:, None], keys, torch.zeros_like(keys))
+            first = max(0, n - r - self.window + 1) if self.window else 0
+            keys[:first] = keys[:first].nan_to_num(0.0)  # seen by no row
+            pos = torch.arange(r, device=dev) + n - r
+            parts.append(latent_ref.attend(self.q[t:t + r].double(), keys[None], keys[None, :, :self.R],
+                                           pos, self.scale, self.window, self.exists[s]))
+            t += r
+        return [torch.cat(x) for x in zip(*parts)]
+
+    def check(self):
+        torch = self.env[0]
+        torch.cuda.synchronize()
+        out, lse, size, reach = self.reference()
+        T = self.T
+        score = (self.W + 16) * 2.0 ** -24 * reach + 2.0 ** -18
+        bound = U * out.abs() + (U + 2 * score[..., None]) * size + 1e-30
+        _within(self.out[:T], out, bound, "out")
+        _within(self.lse[:T], lse, score + 2.0 ** -22 * lse.abs().nan_to_num(0, 0, 0), "lse")
+        assert bool((self.out[T:] == 5.0).all()) and bool((self.lse[T:] == 5.0).all())
+
+
+LENS = [1, 63, 64, 65, 777, 0, 128, 300]
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("H", [1, 16, 20, 32, 64, 128])
+def test_decode_heads(env, H, e4m3):
+    d = _Decode(env, LENS, [1] * len(LENS), H, e4m3=e4m3)
+    d.run()
+    d.check()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("R,P", [(64, 0), (64, 64), (192, 0), (256, 64), (320, 64), (448, 128), (512, 0),
+                                 (512, 64)])
+def test_decode_widths(env, R, P, e4m3):
+    for H in (16, 40):
+        d = _Decode(env, [5, 200, 1000], [1, 1, 2], H, R=R, P=P, e4m3=e4m3)
+        d.run()
+        d.check()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("page", [1, 7, 8, 13, 24, 48, 128, 1000])
+def test_decode_pages(env, page, e4m3):
+    for H in (16, 64):
+        d = _Decode(env, [3, 129, 500, 1024], [1, 2, 1, 3], H, page=page, e4m3=e4m3, pad=64)
+        d.run()
+        d.check()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("rows", [[1, 2, 3, 4], [8, 8, 8, 8], [9, 0, 70, 1], [40, 5, 2, 30]])
+def test_decode_rows(env, rows, e4m3):
+    for H in (8, 24):
+        d = _Decode(env, [40, 7, 300, 29], rows, H, e4m3=e4m3, poison=True)  # rows before the first key too
+        d.run()
+        d.check()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("window", [1, 5, 64, 100, 4096])
+def test_decode_window(env, window, e4m3):
+    d = _Decode(env, [1, 64, 333, 900], [1, 2, 5, 3], 16, window=window, e4m3=e4m3, poison=True)
+    d.run()
+    d.check()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("H", [16, 32, 64])
+def test_decode_long(env, H, e4m3):
+    d = _Decode(env, [40000, 3, 9001], [1, 1, 2], H, page=64, e4m3=e4m3)
+    for _ in range(2):  # the counters are back at zero
+        d.run()
+        d.check()
+
+
+# (the last: elements past 448 that are cast to e4m3 are NaN, and so is the row that sees them)
+@pytest.mark.parametrize("e4m3,grow", [(False, 0.004), (True, 0.09), (True, 0.15)])
+@pytest.mark.parametrize("H", [16, 64])
+def test_decode_growing_scores(env, H, e4m3, grow):
+    d = _Decode(env, [700, 90], [1, 2], H, grow=grow, e4m3=e4m3)
+    d.run()
+    d.check()
+    d.scale = -d.scale
+    d.run()
+    d.check()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("page", [7, 16])
+def test_decode_missing_pages(env, page, e4m3):
+    d = _Decode(env, [100, 64, 200], [1, 2, 1], 16, page=page, e4m3=e4m3, poison=True,
+                drop={(0, 0), (0, 3), (1, 0), (1, 1), (1, 2), (1, 3), (1, 4), (1, 5), (1, 6), (1, 7),
+                      (1, 8), (1, 9), (2, 5)})
+    d.run()
+    d.check()
+
+
+def test_decode_not_finite(env):
+    """An infinity or NaN makes the rows that see it NaN, in a stage that all rows see and in
+    one that some do not; the rows before it stay."""
+    torch, ssd, dev = env
+    for at, value in ((70, math.nan), (198, math.nan), (197, math.inf), (198, -math.inf), (10, math.inf)):
+        d = _Decode(env, [200], [4], 16, page=8)
+        p, o = int(d.table[0, at // 8]), at % 8
+        d.run()
+        clean = d.out[:4].clone()
+        d.cache[p, o, 5] = value
+        d.run()
+        torch.cuda.synchronize()
+        for i in range(4):
+            if 196 + i < at:
+                assert torch.equal(d.out[i], clean[i])
+                continue
+            for h in range(16):
+                score = float(d.q[i, h, 5]) * value
+                if math.isnan(score) or score > 0:
+                    assert bool(d.out[i, h].isnan().all()) and math.isnan(float(d.lse[i, h]))
+                else:  # a score of -infinity
+                    keep = [e for e in range(512) if e != 5]
+                    assert bool(d.out[i, h, keep].isfinite().all())
+
+
+def test_decode_queries_with_large_elements(env):
+    """e4m3: a large element of q beside small ones that decide the scores."""
+    torch, ssd, dev = env
+    d = _Decode(env, [300], [1], 16, e4m3=True)
+    zero = d.cache.view(torch.uint8)
+    zero[..., 3] = 0
+    d.q[:, :, 3] = 2.0 ** 18
+    d.run()
+    d.check()
+
+
+def test_decode_one_row_each_by_default_and_lse_optional(env):
+    torch, ssd, dev = env
+    d = _Decode(env, LENS, [1] * len(LENS), 16)
+    d.run()
+    out = torch.empty_like(d.out[:d.T])
+    ssd.latent_decode(d.q[:d.T], d.cache, d.table, d.seq_len, out, d.ws, d.scale)
+    assert torch.equal(out, d.out[:d.T])
+
+
+def test_decode_same_bits_every_time_and_on_another_stream(env):
+    torch, ssd, dev = env
+    d = _Decode(env, [9000, 40, 3000], [2, 1, 4], 32)
+    d.run()
+    first = d.out.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        d.out.fill_(5.0)
+        side.wait_stream(torch.cuda.current_stream())
+        d.run(stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(first, d.out)
+
+
+def test_decode_strided_rows(env):
+    torch, ssd, dev = env
+    d = _Decode(env, [100, 30], [2, 1], 8)
+    q = torch.zeros((d.T, 8 * 576 + 64), dtype=torch.bfloat16, device=dev)
+    out = torch.zeros((d.T, 8 * 512 + 8), dtype=torch.bfloat16, device=dev)
+    q[:, 64:] = d.q[:d.T].reshape(d.T, -1)
+    d.run()
+    ssd.latent_decode(q[:, 64:].unflatten(1, (8, 576)), d.cache,
+                      d.table, d.seq_len, out[:, :4096].unflatten(1, (8, 512)), d.ws, d.scale,
+                      q_start=d.q_start)
+    assert torch.equal(out[:, :4096], d.out[:d.T].reshape(d.T, -1))
+    assert bool((out[:, 4096:] == 0).all())
+
+
+def test_decode_wait_that_runs_out(env):
+    """A wait that nothing ends gives a status, and the context goes on."""
+    torch, ssd, dev = env
+    for e4m3 in (False, True):
+        d = _Decode(env, [9000, 40], [1, 2], 16, e4m3=e4m3)
+        ssd.dec_set_wait_limit_ns(2_000_000)
+        ssd.dec_debug_attn_timeout(True)
+        try:
+            d.run()
+            assert ssd.dec_sync_status() == ssd.DEC_ERR_TIMEOUT
+        finally:
+            ssd.dec_debug_attn_timeout(False)
+            ssd.dec_set_wait_limit_ns(2_000_000_000)
+        d.ws.zero_()
+        d.out.fill_(5.0)
+        d.lse.fill_(5.0)
+        d.run()
+        assert ssd.dec_sync_status() == ssd.DEC_OK
+        d.check()
+
+
+# ----------------------------------------------------------------- prompt ----
+
+class _Prompt:
+    def __init__(self, env, rows, keys, H, N=128, P=64, V=128, scale=0.09, seed=0, joint=True, extra=1):
+        torch, ssd, dev = env
+        self.env, self.rows, self.keys, self.H = env, list(rows), list(keys), H
+        self.N, self.P, self.V, self.scale = N, P, V, scale
+        g = _gen(torch, dev, 400 + seed + sum(keys) + H)
+        self.T, self.Tk = sum(rows), sum(keys)
+        T, Tk = self.T + extra, self.Tk + extra
+        self.q = _randn(torch, dev, g, T, H, N + P)
+        if joint:
+            kv = _randn(torch, dev, g, Tk, H, N + V)
+            self.k, self.v = kv[..., :N], kv[..., N:]
+        else:
+            self.k = _randn(torch, dev, g, H, Tk, N).transpose(0, 1)
+            self.v = _randn(torch, dev, g, Tk, H, V + 8)[..., :V]
+        self.r = _randn(torch, dev, g, Tk, P + 16)[:, :P] if P else None
+        self.q_start = _i32(torch, _starts(rows), dev)
+        self.k_start = _i32(torch, _starts(keys), dev)
+        self.out = torch.full((T, H, V), 5.0, device=dev).to(torch.bfloat16)
+        self.lse = torch.full((T, H), 5.0, device=dev)
+
+    def run(self, **kw):
+        self.env[1].latent_prompt(self.q, self.k, self.r, self.v, self.q_start, self.out, self.scale,
+                                  k_start=self.k_start, lse=self.lse, **kw)
+
+    def check(self):
+        torch, ssd, dev = self.env
+        import latent_ref
+        torch.cuda.synchronize()
+        t = j = 0
+        for s, (n, L) in enumerate(zip(self.rows, self.keys)):
+            k = self.k[j:j + L].double().transpose(0, 1)
+            if self.P:
+                k = torch.cat([k, self.r[j:j + L].double()[None].expand(self.H, L, self.P)], -1)
+            v = self.v[j:j + L].double().transpose(0, 1)
+            pos = torch.arange(n, device=dev) + L - n
+            if n:
+                out, lse, size, reach = latent_ref.attend(self.q[t:t + n].double(), k, v, pos, self.scale)
+                score = (self.N + self.P + 16) * 2.0 ** -24 * reach + 2.0 ** -18
+                bound = U * out.abs() + (U + 2 * score[..., None]) * size + 1e-30
+                _within(self.out[t:t + n], out, bound, f"out {s}")
+                _within(self.lse[t:t + n], lse, score + 2.0 ** -22 * lse.abs().nan_to_num(0, 0, 0),
+                        f"lse {s}")
+            t, j = t + n, j + L
+        assert bool((self.out[t:] == 5.0).all()) and bool((self.lse[t:] == 5.0).all())
+
+
+@pytest.mark.parametrize("rows,keys", [
+    ([1], [1]), ([1], [500]), ([127], [127]), ([128], [128]), ([129], [129]), ([255, 256, 257], [255, 256, 257]),
+    ([777], [777]), ([5, 0, 300], [5, 40, 300]), ([130, 3], [400, 1000]), ([60, 200], [10, 150]),
+    ([40, 7], [0, 0]), ([513], [1200]),
+])
+def test_prompt(env, rows, keys):
+    for H in (1, 5):
+        p = _Prompt(env, rows, keys, H)
+        p.run()
+        p.check()
+
+
+@pytest.mark.parametrize("N,P,V", [(64, 64, 64), (64, 0, 64), (128, 0, 128), (128, 64, 64), (64, 64, 128)])
+def test_prompt_widths(env, N, P, V):
+    for joint in (True, False):
+        p = _Prompt(env, [300, 20], [300, 220], 3, N, P, V, joint=joint)
+        p.run()
+        p.check()
+
+
+def test_prompt_many_sequences(env):
+    rows = [(7 * i) % 5 for i in range(900)]
+    p = _Prompt(env, rows, [n + (i % 3) for i, n in enumerate(rows)], 2)
+    p.run()
+    p.check()
+
+
+def test_prompt_keys_by_default(env):
+    torch, ssd, dev = env
+    p = _Prompt(env, [200, 77], [200, 77], 4, extra=0)
+    p.run()
+    out = torch.empty_like(p.out)
+    ssd.latent_prompt(p.q, p.k, p.r, p.v, p.q_start, out, p.scale)
+    assert torch.equal(out, p.out)
+
+
+def test_prompt_growing_scores(env):
+    torch, ssd, dev = env
+    p = _Prompt(env, [600], [600], 2)
+    ramp = torch.linspace(0, 2, p.Tk + 1, device=dev)[:, None, None]
+    p.k.copy_((p.k.float() * 0.1 + ramp).to(torch.bfloat16))
+    p.q.copy_((p.q.float() * 0.1 + 0.5).to(torch.bfloat16))
+    for scale in (0.09, -0.09, 1.5):
+        p.scale = scale
+        p.run()
+        p.check()
+
+
+def test_prompt_not_finite_where_not_seen(env):
+    """NaN in keys and values of later tokens and of other sequences does not reach a row; a value
+    that is seen makes its element what the sum makes it."""
+    torch, ssd, dev = env
+    for at in (150, 40, 299, 128, 255):
+        p = _Prompt(env, [300, 90], [300, 90], 2)
+        p.run()
+        clean = p.out.clone()
+        p.k[300:] = math.nan
+        p.v[300:] = math.nan
+        p.run()
+        assert torch.equal(p.out[:300], clean[:300])
+        p = _Prompt(env, [300, 90], [300, 90], 2)
+        p.v[at, 1, 17] = math.inf
+        p.v[at, 1, 18] = math.nan
+        p.run()
+        torch.cuda.synchronize()
+        want = clean.clone()
+        got = p.out
+        rows = slice(at, 300)
+        assert bool((got[rows, 1, 17] == math.inf).all()), at
+        assert bool(got[rows, 1, 18].isnan().all()), at
+        got[rows, 1, 17:19] = want[rows, 1, 17:19]
+        # rows that see it hold its weight in the sum all the same: the others' elements stay
+        assert bool((got.float() - want.float()).abs().max() <= 2.0 ** -7 * want.float().abs().max())
+        assert torch.equal(got[:at], want[:at]) and torch.equal(got[300:], want[300:])
+        p = _Prompt(env, [300, 90], [300, 90], 2)
+        p.k[at, 0, 3] = math.nan
+        p.run()
+        assert bool(p.out[at:300, 0].isnan().all()) and torch.equal(p.out[:at], clean[:at])
+
+
+# ------------------------------------------------------------ used together ----
+
+def _layer(env, prompt, steps, H=16, R=512, N=128, P=64, V=128, page=16, e4m3=False, graph=True):
+    """A prompt in the expanded form, then single tokens in the absorbed one from a captured
+    graph: both against plain attention over the same latent vectors."""
+    torch, ssd, dev = env
+    import latent_ref
+    g = _gen(torch, dev, 77)
+    S, total = len(prompt), sum(prompt)
+    longest = max(prompt) + steps
+    max_pages = -(-longest // page)
+    w_uk = (_randn(torch, dev, g, H, R, N).float() * N ** -0.5).to(torch.bfloat16)   # into latent
+    w_uv = (_randn(torch, dev, g, H, V, R).float() * R ** -0.5).to(torch.bfloat16)   # back
+    weight = torch.ones(R, device=dev).to(torch.bfloat16)
+    inv, mag = ssd.rope_frequencies(P, device=dev)
+    scale = (N + P) ** -0.5
+    dtype = torch.float8_e4m3fn if e4m3 else torch.bfloat16
+    cache = torch.zeros((S * max_pages + 1, page, R + P), device=dev).to(dtype)
+    c_scale = torch.full((1,), 0.02, device=dev) if e4m3 else None
+    table = torch.full((S, max_pages), -1, dtype=torch.int32, device=dev)
+    free = torch.randperm(S * max_pages, generator=g, device=dev).to(torch.int32)
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device=dev)
+
+    # the prompt
+    down, up = _randn(torch, dev, g, total, R + P), _randn(torch, dev, g, total, H, N + P)
+    kv_len, summary = i32(S), i32(4)
+    q_start, pos, slots = i32(S + 1), i32(total), i32(total)
+    ssd.kv_plan(kv_len, _i32(torch, prompt, dev), table, free, summary[1:2], page, kv_len, q_start, pos,
+                slots, summary)
+    q, rows = up.clone(), torch.empty_like(down)
+    ssd.latent_append(down[:, :R], down[:, R:], pos, slots, inv, cache, weight=weight, q_rope=q[..., N:],
+                      q_out=q[..., N:], rows=rows, cache_scale=c_scale)
+    # keys and values of every head from the latent vectors: one matrix a head
+    k, v = (torch.empty((total, H, d), dtype=torch.bfloat16, device=dev) for d in (N, V))
+    lat = rows[:, None, :R].expand(total, H, R).contiguous()
+    ssd.latent_project(lat, w_uk.transpose(1, 2).contiguous(), k)
+    ssd.latent_project(lat, w_uv, v)
+    out = torch.empty((total, H, V), dtype=torch.bfloat16, device=dev)
+    ssd.latent_prompt(q, k, rows[:, R:], v, q_start, out, scale)
+    torch.cuda.synchronize()
+    x = rows[:, :R].double()
+    for got, w in ((k, w_uk.transpose(1, 2)), (v, w_uv)):
+        w = w.double()
+        _within(got, torch.einsum("jr,hdr->jhd", x, w),
+                U * torch.einsum("jr,hdr->jhd", x, w).abs()
+                + (R + 2) * 2.0 ** -24 * torch.einsum("jr,hdr->jhd", x.abs(), w.abs()), "expanded")
+
+    def near(got, query, keys, values, at, lse=None):
+        want, _, size, reach = latent_ref.attend(query.double(), keys, values, at, scale)
+        score = (query.shape[-1] + 16) * 2.0 ** -24 * reach + 2.0 ** -18
+        _within(got, want, U * want.abs() + (U + 2 * score[..., None]) * size + 1e-30, "attention")
+
+    t = 0
+    for s, n in enumerate(prompt):
+        kk = torch.cat([k[t:t + n].double(), rows[t:t + n, None, R:].double().expand(n, H, P)], -1)
+        near(out[t:t + n], q[t:t + n], kk.transpose(0, 1), v[t:t + n].double().transpose(0, 1),
+             torch.arange(n, device=dev))
+        t += n
+
+    # single tokens
+    new_down, new_up = _randn(torch, dev, g, S, R + P), _randn(torch, dev, g, S, H, N + P)
+    q_lat = torch.empty((S, H, R + P), dtype=torch.bfloat16, device=dev)
+    o_lat = torch.empty((S, H, R), dtype=torch.bfloat16, device=dev)
+    o = torch.empty((S, H, V), dtype=torch.bfloat16, device=dev)
+    kept = torch.empty_like(new_down)
+    q_start, pos, slots = i32(S + 1), i32(S), i32(S)
+    ws = ssd.workspace(ssd.latent_decode_workspace_bytes(S, S, H, R, P), dev)
+    w_in = w_uk  # [H, R, N]: q[t, h] . (U_h c) = (U_h^T q) . c
+
+    def step():
+        ssd.kv_plan(kv_len, None, table, free, summary[1:2], page, kv_len, q_start, pos, slots, summary)
+        ssd.latent_append(new_down[:, :R], new_down[:, R:], pos, slots, inv, cache, weight=weight,
+                          q_rope=new_up[..., N:], q_out=q_lat[..., R:], rows=kept, cache_scale=c_scale)
+        ssd.latent_project(new_up[..., :N], w_in, q_lat[..., :R])
+        ssd.latent_decode(q_lat, cache, table, kv_len, o_lat, ws, scale, q_start=q_start,
+                          cache_scale=c_scale)
+        ssd.latent_project(o_lat, w_uv, o)
+
+    cg = None
+    for i in range(steps):
+        new_down.copy_(_randn(torch, dev, g, S, R + P))
+        new_up.copy_(_randn(torch, dev, g, S, H, N + P))
+        if graph and i == 1:
+            torch.cuda.synchronize()
+            cg = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(cg):
+                step()
+        cg.replay() if cg is not None else step()
+        torch.cuda.synchronize()
+        held = cache.float().double() * (c_scale.double() if e4m3 else 1.0)
+        for s, n in enumerate(prompt):
+            n += i + 1
+            h = held[table[s, :-(-n // page)].long()].reshape(-1, R + P)[:n]
+            assert bool((h.abs().sum(-1) > 0).all())
+            err = (h[-1] - kept[s].double()).abs()
+            assert bool((err <= (2.0 ** -4 * h[-1].abs() + 2.0 ** -9 if e4m3 else 0)).all())
+            near(o_lat[s:s + 1], q_lat[s:s + 1], h[None], h[None, :, :R],
+                 torch.full((1,), n - 1, device=dev))
+        w = w_uv.double()
+        back = torch.einsum("shr,hvr->shv", o_lat.double(), w)
+        size = torch.einsum("shr,hvr->shv", o_lat.double().abs(), w.abs())
+        _within(o, back, U * back.abs() + (R + 2) * 2.0 ** -24 * size, "back")
+    assert kv_len.tolist() == [n + steps for n in prompt]
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_layer_prompt_then_tokens(env, e4m3):
+    _layer(env, [70, 1, 300, 15], 20, e4m3=e4m3)
+
+
+def test_layer_many_heads(env):
+    _layer(env, [33, 130], 5, H=128)
