@@ -23,7 +23,7 @@ SOURCES = ["api.cu", "gemv_tiny.cu", "engine_cc.cu", "engine_tc.cu", "moe_aux.cu
            "front_fused.cu", "engine_pair.cu", "api_attn.cu", "kv_plan.cu", "rope_append.cu",
            "attn_decode.cu", "attn_d64.cu", "attn_d128.cu", "attn_d256.cu", "attn_tc.cu",
            "attn_tc_e4m3.cu", "api_latent.cu", "latent_append.cu", "latent_project.cu",
-           "latent_decode.cu", "latent_decode_e4m3.cu", "latent_prompt.cu"]
+           "latent_decode.cu", "latent_decode_e4m3.cu", "latent_join.cu", "latent_prompt.cu"]
 HEADERS = ["common.cuh", "engine.cuh", "routing.cuh", "tcgen05.cuh", "internal.h", "attn.h",
            "attn_kernel.cuh", "attn_tc.cuh", "rope.cuh", "latent.h", "latent_decode.cuh",
            "tma3.cuh"]

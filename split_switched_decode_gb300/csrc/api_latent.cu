@@ -148,7 +148,7 @@ size_t latent_decode_workspace_bytes(int S, int T, int H, int R, int P) {
     return 0;
   cudaError_t ce;
   const int sms = host_num_sms(&ce);
-  return sms > 0 ? latent_workspace_bytes(S, T, H, R, sms) : 0;
+  return sms > 0 ? latent_workspace_bytes(S, T, H, sms) : 0;
 }
 
 dec_status latent_decode(const dec_bf16 *q, int64_t q_stride, const void *cache, int kv_type,
@@ -176,7 +176,7 @@ dec_status latent_decode(const dec_bf16 *q, int64_t q_stride, const void *cache,
   cudaError_t ce;
   const int sms = host_num_sms(&ce);
   if (sms <= 0) return DEC_ERR_CUDA;
-  if (ws_bytes < latent_workspace_bytes(S, T, H, R, sms)) return DEC_ERR_WORKSPACE_TOO_SMALL;
+  if (ws_bytes < latent_workspace_bytes(S, T, H, sms)) return DEC_ERR_WORKSPACE_TOO_SMALL;
   if (host_consume_fault()) return DEC_ERR_CUDA;
   AttnParams p = {};
   p.q = q;

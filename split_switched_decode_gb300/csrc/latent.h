@@ -43,10 +43,26 @@ cudaError_t launch_latent_project(const uint16_t *x, long long x_stride, long lo
 
 // ---------------------------------------------------------- latent_decode.cu --
 // AttnParams with one kv head of D = R elements, the first of a row of R + P in the cache.
-size_t latent_workspace_bytes(int S, int T, int H, int R, int num_sms);
+struct LatentLaunch {
+  CUtensorMap map, qmap;  // of the cache where AttnParams::box > 0; of q where q_boxes
+  bool q_boxes;
+  int num_sms;
+  void *rows;       // workspace: a table entry a row of q and head,
+  float *partials;  // then two parts a worker
+  unsigned *status;
+  uint64_t wait_limit_ns;
+  bool hold;  // self-test: waits that run out
+};
+size_t latent_workspace_bytes(int S, int T, int H, int num_sms);
 cudaError_t launch_latent_decode(const AttnParams &p, int width, bool e4m3, void *ws, int num_sms,
                                  unsigned *status, uint64_t wait_limit_ns, bool hold,
                                  cudaStream_t s);
+// latent_decode_e4m3.cu
+cudaError_t launch_latent_e4m3(const AttnParams &p, int width, int rows, const LatentLaunch &a,
+                               cudaStream_t s);
+// latent_join.cu: parts of `rows` rows each.
+cudaError_t launch_latent_join(const AttnParams &p, int rows, const LatentLaunch &a,
+                               cudaStream_t s);
 
 // ---------------------------------------------------------- latent_prompt.cu --
 struct LatentPromptParams {

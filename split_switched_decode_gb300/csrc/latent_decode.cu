@@ -1,12 +1,8 @@
 // latent_decode.cu -- host side of the latent attention kernel (latent_decode.cuh): rows of an
-// item, workspace and tensor map; and the kernel for bf16 caches.
+// item, workspace and tensor maps; and the kernel for bf16 caches.
 #include "latent_decode.cuh"
 
 namespace ssd {
-
-cudaError_t launch_latent_e4m3(const AttnParams &p, int width, int rows, void *ws,
-                               const AttnLaunch &a, cudaStream_t s);
-
 namespace {
 
 // Rows of an item, from those of an average sequence (what the host knows).
@@ -14,13 +10,15 @@ int latent_rows(int S, int T, int H) {
   const long long rows = static_cast<long long>((T + S - 1) / S) * H;
   return rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
 }
+size_t table_bytes(int T, int H) {
+  return (static_cast<size_t>(T) * H * sizeof(int2) + 255) / 256 * 256;
+}
 
 }  // namespace
 
-size_t latent_workspace_bytes(int S, int T, int H, int R, int num_sms) {
-  (void)R;  // parts are LATENT_MAX_R wide
+size_t latent_workspace_bytes(int S, int T, int H, int num_sms) {
   const size_t M = latent_rows(S, T, H);
-  return attn_counter_bytes(num_sms) +
+  return table_bytes(T, H) +
          2 * static_cast<size_t>(num_sms) * (M * LATENT_MAX_R + 2 * M) * sizeof(float);
 }
 
@@ -28,11 +26,14 @@ cudaError_t launch_latent_decode(const AttnParams &params, int width, bool e4m3,
                                  int num_sms, unsigned *status, uint64_t wait_limit_ns, bool hold,
                                  cudaStream_t s) {
   AttnParams p = params;
-  AttnLaunch a = {};
+  LatentLaunch a = {};
   a.num_sms = num_sms;
+  a.rows = ws;
+  a.partials = reinterpret_cast<float *>(static_cast<char *>(ws) + table_bytes(p.T, p.Hq));
   a.status = status;
   a.wait_limit_ns = wait_limit_ns;
   a.hold = hold;
+  const int rows = latent_rows(p.S, p.T, p.Hq);
   p.box = 0;
   // boxes of 8 tokens of a page; strides of zero (a broadcast cache) or an encoder that
   // refuses: copies by hand
@@ -40,11 +41,19 @@ cudaError_t launch_latent_decode(const AttnParams &params, int width, bool e4m3,
     const long long dims[4] = {64, p.c.page_size, width / 64, p.c.num_pages};
     const long long strides[3] = {p.c.token_stride, 64, p.c.page_stride};
     const int box[4] = {64, 8, width / 64, 1};
-    if (host_map(&a.kmap, p.c.k, e4m3 ? 1 : 2, 4, dims, strides, box, !e4m3)) p.box = 8;
+    if (host_map(&a.map, p.c.k, e4m3 ? 1 : 2, 4, dims, strides, box, !e4m3)) p.box = 8;
   }
-  const int rows = latent_rows(p.S, p.T, p.Hq);
-  return e4m3 ? launch_latent_e4m3(p, width, rows, ws, a, s)
-              : launch_latent<false>(p, width, rows, ws, a, s);
+  // rows of q without gaps between tokens: boxes of an item's rows (for e4m3 caches they are
+  // converted on the way)
+  if (!e4m3 && (p.T == 1 || p.q_stride == static_cast<long long>(p.Hq) * width)) {
+    const long long dims[2] = {width, static_cast<long long>(p.T) * p.Hq};
+    const long long strides[1] = {width};
+    const int box[2] = {64, rows};
+    a.q_boxes = host_map(&a.qmap, p.q, 2, 2, dims, strides, box, true);
+  }
+  const cudaError_t e = e4m3 ? launch_latent_e4m3(p, width, rows, a, s)
+                             : launch_latent<false>(p, width, rows, a, s);
+  return e != cudaSuccess ? e : launch_latent_join(p, rows, a, s);
 }
 
 }  // namespace ssd

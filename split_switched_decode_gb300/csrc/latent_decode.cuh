@@ -19,25 +19,28 @@
 //
 // so O takes 4 MQ columns and S MQ. The tokens lie in the lanes of S; its 64 are in 16 lanes
 // of each warp's quarter (M = 64), and a thread reads four elements of each 16 x 8 block (two
-// tokens, two rows), so the four warps share the exponentials evenly and a thread holds the
-// running maximum and its tokens' part of the sum of MQ / 4 rows. The maximum is moved only
-// when a row's has grown by 8 or more (weights then stay below 2^8, and their rounding to
-// bf16, relative 2^-8, is not enlarged): the common stage needs one vote over the group and
-// no exchange of maxima. Sums are fp32, of the weights before rounding, added over lanes and
-// warps at the segment's end.
+// tokens, two rows). Two groups of four warps have half of the rows each and share nothing; a
+// thread holds the running maximum and its tokens' part of the sum of MQ / 8 rows. The maximum
+// is moved only when a row's has grown by 8 or more (weights then stay below 2^8, and their
+// rounding to bf16, relative 2^-8, is not enlarged): the common stage needs one vote over the
+// group and no exchange of maxima. Sums are fp32, of the weights before rounding, added over
+// lanes and warps at the segment's end.
 //
 // A stage is 64 tokens: eight boxes of 8 tokens x the whole row, so any page of whole blocks
 // of 8 tokens comes in boxes; a box is laid out as one swizzle group per 64 elements (1 KB
 // each), which is the operand layout of both products with strides of a box. Other pages are
 // copied in 16-byte loads by four warps into the same layout.
 //
-// Warps: 4 softmax, 1 each for S, O and the boxes, 4 that bring the rows of q and
-//   (E4M3) widen the stages to f16, or copy the stages that boxes do not fit.
+// Warps: 8 softmax, 1 each for S, O, the boxes and (bf16) the boxes of q, 4 that bring the rows
+// of q where boxes do not and widen the stages to f16 (E4M3) or copy those that boxes do not fit.
 //
 // E4M3 caches: every e4m3 value is an f16 value; q is scaled by a power of two a row and
 // converted to f16, the weights are f16 and refer to F16_POWERS below the maximum.
 //
-// Division of the work, joins and what they rely on are attn_kernel.cuh's (one kv head).
+// Division of the work: attn_kernel.cuh's (one kv head). An item that lies in several CTAs leaves
+// a part in each (fp32, unscaled, with its maximum and sum), and where those are in a table by row;
+// a second kernel joins them: with 64 rows a part is 132 KB, and the last CTA of an item alone
+// would read for longer (16 parts: 20 us) than the products take.
 #pragma once
 
 #include "attn_tc.cuh"
@@ -46,9 +49,9 @@
 namespace ssd {
 namespace {
 
-constexpr int LD_THREADS = 384;
-// An item is charged eight stages: its q, partial results and the join.
-constexpr int LD_ITEM_COST = 8, LD_LEAST = 9;
+constexpr int LD_THREADS = 512;
+// Units that an item is charged (its q and outputs), and the smallest share.
+constexpr int LD_ITEM_COST = 4, LD_LEAST = 1;
 
 template <int MQ, bool E4M3>
 struct LdCfg {
@@ -61,23 +64,48 @@ struct LdCfg {
   static constexpr int RST = E4M3 ? (MQ == 64 ? 2 : 3) : 0;
   static constexpr int NS = 4;  // buffers of scores
   static constexpr int COLS = 8 * MQ;  // O: 4 MQ, then NS S
+  static constexpr int GR = MQ / 2;    // rows of a softmax group
   static constexpr size_t SMEM = ST * STAGE + RST * RAW + QB * QBYTES + PBYTES;
   static constexpr int SLOT = MQ * DP + 2 * MQ;
 };
+
+struct LatentPlan {
+  int2 *rows;  // [T * H]: a row's first worker, number of parts
+  float *partials;
+  unsigned *status;
+  uint64_t wait_limit_ns;
+  int hold;     // self-test: waits that run out (dec_debug_attn_timeout)
+  int q_boxes;  // rows of q in boxes
+};
+
+__device__ __forceinline__ void tma_load_2d_to(uint32_t dst, const CUtensorMap *map, uint64_t *bar,
+                                               int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
+      : "memory");
+}
 
 // 16 lanes x 8 B columns: element (row l / 4 (+ 8), column 8 b + 2 (l % 4) (+ 1)) of block b is
 // in v[4 b + 2 (second row) + (second column)] of lane l.
 template <int B>
 __device__ __forceinline__ void tmem_ld_blocks(uint32_t taddr, float *v) {
   uint32_t r[32];
-  if constexpr (B == 2) {
+  if constexpr (B == 1) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(taddr)
+                 : "memory");
+  } else if constexpr (B == 2) {
     asm volatile(
         "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
           "=r"(r[7])
         : "r"(taddr)
         : "memory");
-  } else if constexpr (B == 4) {
+  } else {
+    static_assert(B == 4, "blocks");
     asm volatile(
         "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
         "%14,%15}, [%16];"
@@ -86,22 +114,37 @@ __device__ __forceinline__ void tmem_ld_blocks(uint32_t taddr, float *v) {
           "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr)
         : "memory");
-  } else {
-    static_assert(B == 8, "blocks");
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-        "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
-          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
-          "=r"(r[31])
-        : "r"(taddr)
-        : "memory");
   }
 #pragma unroll
   for (int i = 0; i < 4 * B; ++i) v[i] = __uint_as_float(r[i]);
+}
+// C consecutive columns of this thread's lane.
+template <int C>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float *v) {
+  if constexpr (C == 8) {
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                   "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+  } else {
+    static_assert(C == 16, "columns");
+    tmem_ld16(taddr, v);
+  }
+}
+template <int C>
+__device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const uint32_t *r) {
+  if constexpr (C == 8)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(
+                     taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+                 "r"(r[7])
+                 : "memory");
+  else
+    tmem_st16(taddr, r);
 }
 // Whether any of the `n` threads at named barrier `id` says so.
 __device__ __forceinline__ bool named_bar_any(int id, int n, bool mine) {
@@ -127,10 +170,13 @@ __device__ __forceinline__ uint64_t sw128_any(uint32_t saddr, uint32_t leading, 
 template <int MQ, bool E4M3>
 __global__ void __launch_bounds__(LD_THREADS, 1)
     latent_decode_kernel(const __grid_constant__ CUtensorMap map,
-                         const __grid_constant__ AttnParams p, const AttnPlan pl, const int width) {
+                         const __grid_constant__ CUtensorMap qmap,
+                         const __grid_constant__ AttnParams p, const LatentPlan pl,
+                         const int width) {
   using C = LdCfg<MQ, E4M3>;
   constexpr int TOK = C::TOK, ST = C::ST, QB = C::QB, NS = C::NS, DP = C::DP;
-  constexpr int NB = MQ / 8, NC = MQ / 4;  // 8-column blocks; rows of a thread
+  constexpr int GR = C::GR, NB = GR / 8, NC = GR / 4;  // of a group: rows, blocks; of a thread: rows
+  constexpr int CH = GR < 16 ? GR : 16;  // columns of O at a time
   extern __shared__ __align__(1024) uint8_t ld_smem[];  // ring, raw ring, q, weights
   __shared__ RangeStart<LD_THREADS> start;
   __shared__ __align__(8) uint64_t full[ST], empty[ST], qfull[QB], qempty[QB];
@@ -139,15 +185,14 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
   __shared__ uint64_t stage_valid[ST], raw_valid[C::RST + 1];  // tokens that exist
   __shared__ float part[4][MQ], top[MQ], by_row[MQ], row_scale[2][MQ];
   __shared__ int row_pos[MQ], row_out[MQ];
-  __shared__ PendingJoin pending[2];
   __shared__ uint32_t tmem_slot;
-  __shared__ int abort_flag, n_pending, is_last;
+  __shared__ int abort_flag;
   static_assert(
       fits_shared<sizeof(start) + sizeof(full) + sizeof(empty) + sizeof(qfull) + sizeof(qempty) +
                       2 * sizeof(raw_full) + sizeof(s_full) + sizeof(pv_done) + 8 * 4 +
                       sizeof(stage_valid) + sizeof(raw_valid) + sizeof(part) + sizeof(top) +
                       sizeof(by_row) + sizeof(row_scale) + sizeof(row_pos) + sizeof(row_out) +
-                      sizeof(pending) + 4 * sizeof(int),
+                      2 * sizeof(int),
                   C::SMEM>,
       "all of the above and the dynamic shared memory");
   const int slabs = width >> 6, group_bytes = slabs << 10, stage_bytes = 8 * group_bytes;
@@ -159,7 +204,6 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
   const bool by_hand = E4M3 || !boxes;  // helpers fill the ring
   if (tid == 0) {
     abort_flag = 0;
-    n_pending = 0;
     for (int i = 0; i < ST; ++i) {
       mbar_init(&full[i], by_hand ? 4 : 1);
       mbar_init(&empty[i], 1);
@@ -169,26 +213,27 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
       mbar_init(&raw_empty[i], 4);
     }
     for (int i = 0; i < QB; ++i) {
-      mbar_init(&qfull[i], 4);
+      mbar_init(&qfull[i], pl.q_boxes ? 1 : 4);
       mbar_init(&qempty[i], 1);
     }
     for (int i = 0; i < NS; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&pv_done[i], 1);
     }
-    mbar_init(&p_full, 128);
+    mbar_init(&p_full, 256);
     mbar_init(&hold, 1);
     mbar_init(&drained[0], 1);
     mbar_init(&drained[1], 1);
     fence_mbar_init();
     if (boxes) prefetch_tensormap(&map);
+    if (pl.q_boxes) prefetch_tensormap(&qmap);
   }
   griddep_wait();
   const int H = p.Hq;
   Shares sh;
   Cursor<TOK, MQ, LD_ITEM_COST, LD_LEAST> c;
   if (!begin_range<LD_THREADS>(p, H, start, sh, c)) return;
-  if (warp == 4) {
+  if (warp == 8) {
     tmem_alloc(&tmem_slot, C::COLS);
     tmem_relinquish();
   }
@@ -203,9 +248,9 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
   };
   // As many barriers in turn as there are S: who waits for stage i knows that i - NS is done.
   auto wait_pv = [&](int i) { wait(&pv_done[i % NS], i / NS); };
-  int issued = 0;  // boxes: stages that were begun
+  int issued = 0, q_issued = 0;  // boxes: stages, items' q that were begun
 
-  if (warp == 6) {
+  if (warp == 10) {
     // ================================================================ boxes of the cache
     // The pages of 32 blocks of 8 tokens are looked up in one step (four stages), a step ahead;
     // the boxes leave from one thread.
@@ -270,19 +315,40 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
       }
       k += c.t1 - c.t0;
     }
-  } else if (warp >= 8) {
+  } else if (warp == 11) {
+    // ================================================================ boxes of q
+    // Rows past the item's, of other sequences, fill columns that nobody reads.
+    int seg = 0;
+    bool go = pl.q_boxes;
+    while (go && c.next(p, H)) {
+      const int qb = seg % QB;
+      if (seg >= QB) go = __all_sync(0xffffffffu, wait(&qempty[qb], seg / QB - 1));
+      if (!go) break;
+      q_issued = seg + 1;
+      if (elect_one()) {
+        const uint32_t to = smem_u32(q_smem + qb * C::QBYTES);
+        mbar_arrive_expect_tx(&qfull[qb], slabs * MQ * 128);
+        for (int slab = 0; slab < slabs; ++slab)
+          tma_load_2d_to(to + slab * MQ * 128, &qmap, &qfull[qb], slab * 64,
+                         c.x.q0 * H + c.rt * MQ);
+      }
+      __syncwarp();
+      ++seg;
+    }
+  } else if (warp >= 12) {
     // ================================================================ rows of q, stages by hand
-    const int hw = warp - 8;
+    const int hw = warp - 12;
+    const bool q_by_hand = !pl.q_boxes;
     const int chunks = width >> 3;  // 16-byte chunks of a row: at most 72
     int k = 0, seg = 0;
-    while (c.next(p, H)) {
+    while ((by_hand || q_by_hand) && c.next(p, H)) {
       // q: a warp a row, four rows at a time
       const int qb = seg % QB;
       const int n_rows = min(MQ, c.x.n * H - c.rt * MQ);
       uint8_t *qd = q_smem + qb * C::QBYTES;
       bool waited = seg < QB;
 #pragma unroll 1
-      for (int r0 = hw; r0 < MQ; r0 += 16) {
+      for (int r0 = hw; q_by_hand && r0 < MQ; r0 += 16) {
         uint4 v[4][3];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -333,9 +399,11 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
           }
         }
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&qfull[qb]);
+      if (q_by_hand) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&qfull[qb]);
+      }
       ++seg;
       if (!by_hand) continue;
       const int32_t *table = p.block_table + static_cast<long long>(c.s) * p.max_pages;
@@ -349,7 +417,7 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
           const uint8_t *from = raw + rs * C::RAW;
           const int n = stage_bytes / 32;  // 16-byte chunks as they came
 #pragma unroll 4
-          for (int i = tid - 256; i < n; i += 128) {
+          for (int i = tid - 384; i < n; i += 128) {
             // chunk (slab, row, quarter) of box g
             const int g = i / (32 * slabs), y = i - g * 32 * slabs;
             const int slab = y >> 5, r = y >> 2 & 7, ch = (y & 3) * 2;
@@ -362,7 +430,7 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
                 make_uint4(e4m3x2_to_f16x2(v.z), e4m3x2_to_f16x2(v.z >> 16),
                            e4m3x2_to_f16x2(v.w), e4m3x2_to_f16x2(v.w >> 16));
           }
-          if (tid == 256) stage_valid[st] = raw_valid[rs];
+          if (tid == 384) stage_valid[st] = raw_valid[rs];
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -429,7 +497,7 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
         }
       }
     }
-  } else if (warp == 4) {
+  } else if (warp == 8) {
     // ================================================================ S = C . Q^T
     const uint32_t id = (tc_idesc<E4M3>(MQ) & ~(31u << 24)) | (64u >> 4) << 24;
     const uint32_t q_u = smem_u32(q_smem), ring_u = smem_u32(ring);
@@ -461,7 +529,7 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
       }
       ++seg;
     }
-  } else if (warp == 5) {
+  } else if (warp == 9) {
     // ================================================================ O += C^T . P
     const uint32_t id = tc_idesc<E4M3>(MQ) | (1u << 15) | (1u << 16);
     const uint32_t ring_u = smem_u32(ring);
@@ -489,11 +557,13 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
       }
     }
     if (k > 0) wait_pv(k - 1);  // nothing in flight when the columns are released
-  } else if (warp < 4) {
+  } else {
     // ================================================================ softmax
     constexpr uint32_t INF2 = E4M3 ? 0x7c007c00u : 0x7f807f80u;  // exponents of two values
-    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-    const int col = 2 * (lane & 3), tok0 = warp * 16 + (lane >> 2);  // and 8 b + col + 1, tok0 + 8
+    const int grp = warp >> 2, w4 = warp & 3, gt = tid & 127, bar = 1 + grp, g0 = grp * GR;
+    const uint32_t lanes = static_cast<uint32_t>(w4 * 32) << 16;
+    // rows g0 + 8 b + col (+ 1), tokens tok0 (+ 8)
+    const int col = 2 * (lane & 3), tok0 = w4 * 16 + (lane >> 2);
     const float scale = p.scale * LOG2E * (p.c.k_scale ? p.c.k_scale[0] : 1.0f);
     int k = 0, seg = 0;
     if (pl.hold) wait(&hold, 0);  // self-test: nobody arrives
@@ -501,40 +571,46 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
       const SeqInfo &x = c.x;
       const int n_rows = min(MQ, x.n * H - c.rt * MQ), row0 = c.rt * MQ;
       const int pos0 = x.len - x.n;
-      // the last key that a row sees; what every row sees
-      if (tid < MQ) row_pos[tid] = pos0 + (row0 + min(tid, n_rows - 1)) / H;
+      // the last key that a row sees, and its token; what every row sees
+      if (gt < GR) {
+        const int r = g0 + gt, tok = (row0 + min(r, n_rows - 1)) / H;
+        row_pos[r] = pos0 + tok;
+        row_out[r] = tok;
+      }
       const int hi_all = pos0 + row0 / H, hi_top = pos0 + (row0 + n_rows - 1) / H;
       const int lo_all = p.window > 0 && hi_top >= p.window ? hi_top - p.window + 1 : 0;
-      named_bar_sync(1, 128);
-      float m[NC], l[NC];  // rows 8 b + col, 8 b + col + 1
+      named_bar_sync(bar, 128);
+      float m[NC], l[NC], zf[NC];
 #pragma unroll
-      for (int i = 0; i < NC; ++i) m[i] = -INFINITY, l[i] = 0.0f;
+      for (int i = 0; i < NC; ++i) m[i] = -INFINITY, l[i] = 0.0f, zf[i] = scale;
       for (int t = c.t0; t < c.t1; ++t, ++k) {
         const int st = k % ST;
         wait(&s_full[k % NS], k / NS);
         tc_fence_after();
         float z[4 * NB];
-        tmem_ld_blocks<NB>(s_tmem + (k % NS) * MQ + lanes, z);
+        tmem_ld_blocks<NB>(s_tmem + (k % NS) * MQ + g0 + lanes, z);
         wait(&full[st], k / ST);  // (long since) the copying warps' bits and the values
         const uint64_t valid = stage_valid[st];
         const int j0 = x.begin + t * TOK;
         const bool plain = valid == ~0ull && j0 >= lo_all && j0 + TOK - 1 <= hi_all;
+        const bool begins = t == c.t0;
+        if (E4M3 && begins) {
+#pragma unroll
+          for (int i = 0; i < NC; ++i)
+            zf[i] = scale * row_scale[seg & 1][g0 + 8 * (i >> 1) + col + (i & 1)];
+        }
         tmem_wait_ld();
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float f = scale;
-            if (E4M3) f *= row_scale[seg & 1][8 * b + col + (e & 1)];
-            z[4 * b + e] *= f;
-          }
+          for (int e = 0; e < 4; ++e) z[4 * b + e] *= zf[2 * b + (e & 1)];
         if (!plain) {
 #pragma unroll
           for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int tok = tok0 + 8 * (e >> 1), j = j0 + tok;
-              const int hi = row_pos[8 * b + col + (e & 1)];
+              const int hi = row_pos[g0 + 8 * b + col + (e & 1)];
               const int lo = p.window > 0 && hi >= p.window ? hi - p.window + 1 : 0;
               if (j < lo || j > hi || !(valid >> tok & 1)) z[4 * b + e] = -INFINITY;
             }
@@ -548,8 +624,7 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
             if (E4M3) mx -= F16_POWERS;
             grows |= mx - m[2 * b + e] >= TC_LAZY;
           }
-        const bool begins = t == c.t0;
-        if (named_bar_any(1, 128, grows || begins)) {
+        if (named_bar_any(bar, 128, grows || begins)) {
           // move the maxima that grew; the outputs so far are rescaled in tensor memory, after
           // the last product that adds to them
 #pragma unroll
@@ -559,14 +634,14 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
               float mx = fmaxf(z[4 * b + e], z[4 * b + 2 + e]);
 #pragma unroll
               for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-              if (lane < 4) part[warp][8 * b + col + e] = mx;
+              if (lane < 4) part[w4][g0 + 8 * b + col + e] = mx;
             }
-          named_bar_sync(1, 128);
+          named_bar_sync(bar, 128);
 #pragma unroll
           for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int r = 8 * b + col + e;
+              const int r = g0 + 8 * b + col + e;
               float mx = fmaxf(fmaxf(part[0][r], part[1][r]), fmaxf(part[2][r], part[3][r]));
               if (E4M3) mx -= F16_POWERS;
               // (each by itself: a row's bits do not depend on what only other rows see)
@@ -574,23 +649,24 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
               const float fade = ex2(old - (now == -INFINITY ? 0.0f : now));
               m[2 * b + e] = now;
               l[2 * b + e] *= fade;
-              if (warp == 0 && lane < 4) by_row[r] = fade;
+              if (w4 == 0 && lane < 4) by_row[r] = fade;
             }
           if (!begins) {
-            named_bar_sync(1, 128);
+            named_bar_sync(bar, 128);
             wait_pv(k - 1);
             tc_fence_after();
 #pragma unroll 1
-            for (int i = 0; i < (p.D + 127) / 128 * MQ; i += 16) {
-              float o[16];
-              uint32_t u[16];
-              tmem_ld16(tmem + lanes + i, o);
-              tmem_wait_ld();
+            for (int blk = 0; blk < (p.D + 127) >> 7; ++blk)
+#pragma unroll 1
+              for (int i = g0; i < g0 + GR; i += CH) {
+                float o[CH];
+                uint32_t u[CH];
+                tmem_ld_cols<CH>(tmem + lanes + blk * MQ + i, o);
+                tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 16; ++e)
-                u[e] = __float_as_uint(o[e] * by_row[(i + e) % MQ]);
-              tmem_st16(tmem + lanes + i, u);
-            }
+                for (int e = 0; e < CH; ++e) u[e] = __float_as_uint(o[e] * by_row[i + e]);
+                tmem_st_cols<CH>(tmem + lanes + blk * MQ + i, u);
+              }
             tmem_wait_st();
           }
         }
@@ -611,8 +687,9 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
         uint8_t *d = w_smem + tok0 * 128 + (lane & 3) * 4;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          *reinterpret_cast<uint32_t *>(d + ((b ^ r) << 4)) = w[2 * b];
-          *reinterpret_cast<uint32_t *>(d + 1024 + ((b ^ r) << 4)) = w[2 * b + 1];
+          const int at = ((grp * NB + b) ^ r) << 4;
+          *reinterpret_cast<uint32_t *>(d + at) = w[2 * b];
+          *reinterpret_cast<uint32_t *>(d + 1024 + at) = w[2 * b + 1];
         }
         if (!plain) {
           // Weights of zero must not meet what is not finite: tokens that do not exist get
@@ -641,7 +718,7 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
             }
           };
           // tokens that all rows see and that exist need no look
-          for (int row = warp; row < TOK; row += 4)
+          for (int row = warp; row < TOK; row += 8)
             if (row < head || row >= tail || !(valid >> row & 1)) clean(row);
         }
         fence_proxy_async_smem();  // before the product (and later boxes) touch either
@@ -656,46 +733,49 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
       const float v_scale = p.c.v_scale ? p.c.v_scale[0] : 1.0f;
       const ItemOut dst = {x.q0, row0, 0, H, v_scale};
       float *slot = pl.partials + static_cast<size_t>(part_slot(c0, me - c0)) * C::SLOT;
-      named_bar_sync(1, 128);  // `part` may still be read
+      named_bar_sync(bar, 128);  // `part` may still be read
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         float s = l[i];
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-        const int r = 8 * (i >> 1) + col + (i & 1);
+        const int r = g0 + 8 * (i >> 1) + col + (i & 1);
         if (lane < 4) {
-          part[warp][r] = s;
-          if (warp == 0) top[r] = m[i];
+          part[w4][r] = s;
+          if (w4 == 0) top[r] = m[i];
         }
       }
-      named_bar_sync(1, 128);
-      if (tid < n_rows) {
-        const float mr = top[tid];
-        const float lr = (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]);
+      named_bar_sync(bar, 128);
+      if (gt < GR && g0 + gt < n_rows) {
+        const int r = g0 + gt;
+        const float mr = top[r];
+        const float lr = (part[0][r] + part[1][r]) + (part[2][r] + part[3][r]);
         if (c0 == c1) {
-          dst.put_lse(p, tid, mr, lr);
-          by_row[tid] = lr == 0.0f ? 0.0f : v_scale / lr;
+          dst.put_lse(p, r, mr, lr);
+          by_row[r] = lr == 0.0f ? 0.0f : v_scale / lr;
         } else {
-          *reinterpret_cast<float2 *>(slot + MQ * DP + 2 * tid) = make_float2(mr, lr);
+          *reinterpret_cast<float2 *>(slot + MQ * DP + 2 * r) = make_float2(mr, lr);
         }
-        row_out[tid] = (row0 + tid) / H;
+        // where the row's parts are
+        if (me == c0)
+          pl.rows[static_cast<long long>(x.q0) * H + row0 + r] = make_int2(c0, c1 - c0 + 1);
       }
       if (k > 0) wait_pv(k - 1);
       tc_fence_after();
-      named_bar_sync(1, 128);
+      named_bar_sync(bar, 128);
 #pragma unroll 1
       for (int d0 = 0; d0 < p.D; d0 += 128) {
-        const int dim = d0 + tid;  // past D in a last half block
+        const int dim = d0 + gt;  // past D in a last half block
 #pragma unroll 1
-        for (int r0 = 0; r0 < n_rows; r0 += 16) {
-          float o[16];
-          tmem_ld16(tmem + lanes + (d0 >> 7) * MQ + r0, o);
+        for (int r0 = g0; r0 < min(n_rows, g0 + GR); r0 += CH) {
+          float o[CH];
+          tmem_ld_cols<CH>(tmem + lanes + (d0 >> 7) * MQ + r0, o);
           tmem_wait_ld();
           if (c0 == c1) {
             // two rows at a time: an even lane has two elements of the first, an odd one of
             // the second
 #pragma unroll
-            for (int e = 0; e < 16; e += 2) {
+            for (int e = 0; e < CH; e += 2) {
               const float f0 = by_row[r0 + e], f1 = by_row[r0 + e + 1];
               // a row that saw nothing: zeros, whatever its columns hold
               const float y0 = f0 == 0.0f ? 0.0f : o[e] * f0;
@@ -711,28 +791,24 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
             }
           } else if (dim < p.D) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
+            for (int e = 0; e < CH; ++e)
               if (r0 + e < n_rows) slot[(r0 + e) * DP + dim] = o[e];
           }
         }
       }
       tc_fence_before();  // the next segment's products overwrite the columns
-      named_bar_sync(1, 128);
-      if (c0 != c1 && tid == 0) count_part(pl, me, c0, c1, n_rows, dst, pending, &n_pending);
+      named_bar_sync(bar, 128);
       ++seg;
     }
   }
-  static_assert(ST * C::STAGE >= 2 * AT_GROUP * MQ * 8, "ml of a join");
-  run_joins<MQ, DP, LD_THREADS>(p, pl, reinterpret_cast<float2 *>(ring), pending, &n_pending,
-                                &is_last);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   // Every wait of the CTA is over. If one ran out, products and boxes may still be on their way:
   // products end before tensor memory is released, boxes land before the CTA ends.
   if (*static_cast<volatile int *>(&abort_flag)) {
-    if (warp == 4 || warp == 5) {
-      uint64_t *bar = &drained[warp - 4];
+    if (warp == 8 || warp == 9) {
+      uint64_t *bar = &drained[warp - 8];
       if (elect_one()) tc_commit(bar);
       __syncwarp();
       mbar_wait_drain(bar, 0, 10000000ull);
@@ -741,35 +817,44 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
     uint64_t *const bar_full = E4M3 ? raw_full : full;
     for (int i = issued - 1; i >= 0 && i >= issued - CST; --i)
       mbar_wait_drain(&bar_full[i % CST], (i / CST) & 1, 10000000ull);
+    for (int i = q_issued - 1; i >= 0 && i >= q_issued - QB; --i)
+      mbar_wait_drain(&qfull[i % QB], (i / QB) & 1, 10000000ull);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
   }
-  if (warp == 4) tmem_dealloc(tmem, C::COLS);
+  if (warp == 8) tmem_dealloc(tmem, C::COLS);
 }
 
 template <int MQ, bool E4M3>
-cudaError_t launch_latent_shape(const AttnParams &p, int width, void *ws, const AttnLaunch &a,
+cudaError_t launch_latent_shape(const AttnParams &p, int width, const LatentLaunch &a,
                                 cudaStream_t s) {
   using C = LdCfg<MQ, E4M3>;
   auto kernel = latent_decode_kernel<MQ, E4M3>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(C::SMEM));
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3(a.num_sms), dim3(LD_THREADS), C::SMEM, s, a.kmap, p,
-                    make_plan(ws, a), width);
+  LatentPlan pl;
+  pl.rows = static_cast<int2 *>(a.rows);
+  pl.partials = a.partials;
+  pl.status = a.status;
+  pl.wait_limit_ns = a.wait_limit_ns;
+  pl.hold = a.hold;
+  pl.q_boxes = !E4M3 && a.q_boxes;
+  return launch_pdl(kernel, dim3(a.num_sms), dim3(LD_THREADS), C::SMEM, s, a.map, a.qmap, p, pl,
+                    width);
 }
 
 template <bool E4M3>
-cudaError_t launch_latent(const AttnParams &p, int width, int rows, void *ws,
-                          const AttnLaunch &a, cudaStream_t s) {
+cudaError_t launch_latent(const AttnParams &p, int width, int rows, const LatentLaunch &a,
+                          cudaStream_t s) {
   switch (rows) {
     case 16:
-      return launch_latent_shape<16, E4M3>(p, width, ws, a, s);
+      return launch_latent_shape<16, E4M3>(p, width, a, s);
     case 32:
-      return launch_latent_shape<32, E4M3>(p, width, ws, a, s);
+      return launch_latent_shape<32, E4M3>(p, width, a, s);
     default:
-      return launch_latent_shape<64, E4M3>(p, width, ws, a, s);
+      return launch_latent_shape<64, E4M3>(p, width, a, s);
   }
 }
 

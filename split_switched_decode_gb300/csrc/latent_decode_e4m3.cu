@@ -3,9 +3,9 @@
 
 namespace ssd {
 
-cudaError_t launch_latent_e4m3(const AttnParams &p, int width, int rows, void *ws,
-                               const AttnLaunch &a, cudaStream_t s) {
-  return launch_latent<true>(p, width, rows, ws, a, s);
+cudaError_t launch_latent_e4m3(const AttnParams &p, int width, int rows, const LatentLaunch &a,
+                               cudaStream_t s) {
+  return launch_latent<true>(p, width, rows, a, s);
 }
 
 }  // namespace ssd
