@@ -50,6 +50,9 @@ namespace ssd {
 namespace {
 
 constexpr int LD_THREADS = 512;
+// Stages ahead of their copy at which boxes are requested into L2: the ring holds two stages, and
+// the one that is on its way (74 KB an SM) is too little for HBM's latency under load.
+constexpr int LD_AHEAD = 2;
 // Units that an item is charged (its q and outputs), and the smallest share.
 constexpr int LD_ITEM_COST = 4, LD_LEAST = 1;
 
@@ -70,7 +73,7 @@ struct LdCfg {
 };
 
 struct LatentPlan {
-  int2 *rows;  // [T * H]: a row's first worker, number of parts
+  int2 *rows;  // [T * H]: a row's first worker + 65536 * its place in the parts, number of parts
   float *partials;
   unsigned *status;
   uint64_t wait_limit_ns;
@@ -85,6 +88,14 @@ __device__ __forceinline__ void tma_load_2d_to(uint32_t dst, const CUtensorMap *
       " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
       : "memory");
+}
+
+__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap *map, int c0, int c1, int c2,
+                                                int c3) {
+  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+               : "memory");
 }
 
 // 16 lanes x 8 B columns: element (row l / 4 (+ 8), column 8 b + 2 (l % 4) (+ 1)) of block b is
@@ -179,7 +190,7 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
   constexpr int CH = GR < 16 ? GR : 16;  // columns of O at a time
   extern __shared__ __align__(1024) uint8_t ld_smem[];  // ring, raw ring, q, weights
   __shared__ RangeStart<LD_THREADS> start;
-  __shared__ __align__(8) uint64_t full[ST], empty[ST], qfull[QB], qempty[QB];
+  __shared__ __align__(8) uint64_t full[ST], empty[4 * ST], qfull[QB], qempty[QB];
   __shared__ __align__(8) uint64_t raw_full[C::RST + 1], raw_empty[C::RST + 1];
   __shared__ __align__(8) uint64_t s_full[NS], p_full, pv_done[NS], hold, drained[2];
   __shared__ uint64_t stage_valid[ST], raw_valid[C::RST + 1];  // tokens that exist
@@ -206,7 +217,7 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
     abort_flag = 0;
     for (int i = 0; i < ST; ++i) {
       mbar_init(&full[i], by_hand ? 4 : 1);
-      mbar_init(&empty[i], 1);
+      for (int y = 0; y < 4; ++y) mbar_init(&empty[4 * i + y], 1);
     }
     for (int i = 0; i < C::RST; ++i) {
       mbar_init(&raw_full[i], 1);
@@ -230,6 +241,12 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
   }
   griddep_wait();
   const int H = p.Hq;
+  if (p.q_start) {  // rows behind the last sequence: no parts
+    const long long first = static_cast<long long>(min(max(p.q_start[p.S], 0), p.T)) * H;
+    for (long long i = first + blockIdx.x * LD_THREADS + tid; i < static_cast<long long>(p.T) * H;
+         i += gridDim.x * LD_THREADS)
+      pl.rows[i] = make_int2(0, 0);
+  }
   Shares sh;
   Cursor<TOK, MQ, LD_ITEM_COST, LD_LEAST> c;
   if (!begin_range<LD_THREADS>(p, H, start, sh, c)) return;
@@ -255,7 +272,7 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
     // The pages of 32 blocks of 8 tokens are looked up in one step (four stages), a step ahead;
     // the boxes leave from one thread.
     constexpr int CST = E4M3 ? C::RST : ST;
-    uint64_t *const bar_full = E4M3 ? raw_full : full, *const bar_empty = E4M3 ? raw_empty : empty;
+    uint64_t *const bar_full = E4M3 ? raw_full : full;
     uint64_t *const bits_of = E4M3 ? raw_valid : stage_valid;
     const int box_bytes = E4M3 ? group_bytes / 2 : group_bytes;
     const uint32_t base = smem_u32(E4M3 ? raw : ring);
@@ -291,23 +308,37 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
           for (int b = 0; b < 8; ++b)
             if (blocks >> b & 1) bits |= 255ull << (8 * b);
           if (left < TOK) bits &= (1ull << max(left, 0)) - 1;
-          if (at >= CST) {
-            go = __all_sync(0xffffffffu, wait(&bar_empty[st], at / CST - 1));
+          // the boxes LD_AHEAD stages on, toward L2
+          const int far = i + LD_AHEAD;
+          if (lane >> 3 == (far & 3)) {
+            const int pg = far < 4 ? page : next_page;
+            if (pg >= 0 && pg < p.c.num_pages) tma_prefetch_4d(&map, 0, far < 4 ? off : next_off, 0, pg);
+          }
+          __syncwarp();
+          // a quarter of the stage as soon as the last product that reads it is done
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            if (at >= CST && (!E4M3 || y == 0))
+              go = __all_sync(0xffffffffu,
+                              wait(E4M3 ? &raw_empty[st] : &empty[4 * st + y], at / CST - 1));
             if (!go) break;
+            if (y == 0) {
+              issued = at + 1;
+              if (elect_one()) {
+                bits_of[st] = bits;
+                mbar_arrive_expect_tx(&bar_full[st], __popc(blocks) * box_bytes);
+              }
+            }
+#pragma unroll
+            for (int b = 2 * y; b < 2 * y + 2; ++b) {
+              const int pg = __shfl_sync(0xffffffffu, page, i * 8 + b);
+              const int o = __shfl_sync(0xffffffffu, off, i * 8 + b);
+              if ((blocks >> b & 1) && elect_one())
+                tma_load_4d(base + st * PITCH + b * box_bytes, &map, &bar_full[st], 0, o, 0, pg);
+              __syncwarp();
+            }
           }
-          issued = at + 1;
-          if (elect_one()) {
-            bits_of[st] = bits;
-            mbar_arrive_expect_tx(&bar_full[st], __popc(blocks) * box_bytes);
-          }
-#pragma unroll 1
-          for (int b = 0; b < 8; ++b) {
-            const int pg = __shfl_sync(0xffffffffu, page, i * 8 + b);
-            const int o = __shfl_sync(0xffffffffu, off, i * 8 + b);
-            if ((blocks >> b & 1) && elect_one())
-              tma_load_4d(base + st * PITCH + b * box_bytes, &map, &bar_full[st], 0, o, 0, pg);
-            __syncwarp();
-          }
+          if (!go) break;
         }
         page = next_page;
         off = next_off;
@@ -413,7 +444,7 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
         if (E4M3 && boxes) {
           const int rs = k % (C::RST + (C::RST == 0));
           wait(&raw_full[rs], k / (C::RST + (C::RST == 0)));
-          if (k >= ST) wait(&empty[st], k / ST - 1);
+          if (k >= ST) wait(&empty[4 * st + 3], k / ST - 1);
           const uint8_t *from = raw + rs * C::RAW;
           const int n = stage_bytes / 32;  // 16-byte chunks as they came
 #pragma unroll 4
@@ -447,7 +478,7 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
               at = pg * p.c.page_stride + (j - i * p.c.page_size) * p.c.token_stride;
           }
           const uint32_t exist = __ballot_sync(0xffffffffu, at >= 0) & 0xffffu;
-          if (k >= ST) wait(&empty[st], k / ST - 1);
+          if (k >= ST) wait(&empty[4 * st + 3], k / ST - 1);
           constexpr int ES = E4M3 ? 1 : 2, PER = E4M3 ? 2 : 3;  // 16-byte loads of a lane
           const int loads = width * ES / 16;
 #pragma unroll 1
@@ -545,12 +576,13 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
           const uint32_t acc = t > c.t0 ? 1u : 0u;
           const uint64_t a = sw128_any(ring_u + st * C::STAGE, 1024, group_bytes);
 #pragma unroll
-          for (int kk = 0; kk < TOK / 16; ++kk)  // two boxes of tokens
+          for (int kk = 0; kk < TOK / 16; ++kk) {  // two boxes of tokens
 #pragma unroll 1
             for (int blk = 0; blk < blocks; ++blk)
               tc_mma(tmem + blk * MQ, a + ((2 * kk * group_bytes + blk * 2048) >> 4),
                      b + ((kk * 2048) >> 4), id, kk > 0 ? 1u : acc);
-          tc_commit(&empty[st]);
+            tc_commit(&empty[4 * st + kk]);
+          }
           tc_commit(&pv_done[k % NS]);
         }
         __syncwarp();
@@ -758,7 +790,8 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
         }
         // where the row's parts are
         if (me == c0)
-          pl.rows[static_cast<long long>(x.q0) * H + row0 + r] = make_int2(c0, c1 - c0 + 1);
+          pl.rows[static_cast<long long>(x.q0) * H + row0 + r] =
+              make_int2(c0 | r << 16, c1 - c0 + 1);
       }
       if (k > 0) wait_pv(k - 1);
       tc_fence_after();

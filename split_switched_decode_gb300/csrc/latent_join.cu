@@ -12,18 +12,6 @@ namespace {
 
 constexpr int LJ_THREADS = 512, LJ_WARPS = LJ_THREADS / 32, LJ_FEW = 8;
 
-// The sequence of token row t, -1: none.
-__device__ __forceinline__ int sequence_of(const AttnParams &p, int t) {
-  if (!p.q_start) return t < p.S ? t : -1;
-  int lo = 0, hi = p.S;  // the last s with q_start[s] <= t
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (p.q_start[mid] <= t) lo = mid;
-    else hi = mid;
-  }
-  return p.q_start[lo] <= t && t < p.q_start[lo + 1] ? lo : -1;
-}
-
 template <int MQ>
 __global__ void __launch_bounds__(LJ_THREADS, 1) latent_join_kernel(
     const __grid_constant__ AttnParams p, const int2 *rows, const float *partials,
@@ -44,14 +32,10 @@ __global__ void __launch_bounds__(LJ_THREADS, 1) latent_join_kernel(
     const int row = base + warp * gridDim.x;
     int c0 = 0, parts = 0, r = 0;
     if (row < all) {
-      const int t = row / H, s = sequence_of(p, t);
-      if (s >= 0) {
-        const int q0 = p.q_start ? max(p.q_start[s], 0) : s;
-        r = (row - q0 * H) % MQ;
-        const int2 x = rows[row];
-        c0 = min(max(x.x, 0), workers - 1);
-        parts = min(x.y, workers - c0);
-      }
+      const int2 x = __ldcg(rows + row);  // kept in bounds, whatever stands there
+      r = (x.x >> 16) & (MQ - 1);
+      c0 = min(x.x & 0xffff, workers - 1);
+      parts = min(x.y, workers - c0);
     }
     auto part = [&](int first, int i, int at) {
       return partials + static_cast<size_t>(part_slot(first, i)) * SLOT + at;
@@ -71,7 +55,7 @@ __global__ void __launch_bounds__(LJ_THREADS, 1) latent_join_kernel(
     if (parts > LJ_FEW) {
       if (lane == 0) {
         const int i = atomicAdd(&n_many, 1);
-        many[i] = make_int2(row, c0);
+        many[i] = make_int2(row, c0 | r << 16);
         many_parts[i] = parts;
       }
     } else if (parts > 1) {
@@ -116,9 +100,8 @@ __global__ void __launch_bounds__(LJ_THREADS, 1) latent_join_kernel(
     __syncthreads();
     for (int x = 0; x < n_many; ++x) {
       // the row by all threads: factors, then a quarter of the parts each 128 threads
-      const int at = many[x].x, first = many[x].y, n = many_parts[x], t = at / H;
-      const int q0 = p.q_start ? max(p.q_start[sequence_of(p, t)], 0) : t;
-      const int mr = (at - q0 * H) % MQ;
+      const int at = many[x].x, first = many[x].y & 0xffff, mr = many[x].y >> 16;
+      const int n = many_parts[x];
       float m = -INFINITY, l = 0.0f;
       float2 mine[4];  // at most 2048 parts
 #pragma unroll
