@@ -48,7 +48,8 @@ struct LatentLaunch {
   bool q_boxes;
   int num_sms;
   void *rows;       // workspace: a table entry a row of q and head,
-  float *partials;  // then two parts a worker
+  float2 *ml;       // two maxima and sums a worker and row of an item,
+  float *partials;  // two parts a worker
   unsigned *status;
   uint64_t wait_limit_ns;
   bool hold;  // self-test: waits that run out

@@ -13,13 +13,16 @@ int latent_rows(int S, int T, int H) {
 size_t table_bytes(int T, int H) {
   return (static_cast<size_t>(T) * H * sizeof(int2) + 255) / 256 * 256;
 }
+size_t ml_bytes(int rows, int num_sms) {
+  return (2 * static_cast<size_t>(rows) * num_sms * sizeof(float2) + 255) / 256 * 256;
+}
 
 }  // namespace
 
 size_t latent_workspace_bytes(int S, int T, int H, int num_sms) {
   const size_t M = latent_rows(S, T, H);
-  return table_bytes(T, H) +
-         2 * static_cast<size_t>(num_sms) * (M * LATENT_MAX_R + 2 * M) * sizeof(float);
+  return table_bytes(T, H) + ml_bytes(static_cast<int>(M), num_sms) +
+         2 * static_cast<size_t>(num_sms) * M * LATENT_MAX_R * sizeof(float);
 }
 
 cudaError_t launch_latent_decode(const AttnParams &params, int width, bool e4m3, void *ws,
@@ -29,19 +32,21 @@ cudaError_t launch_latent_decode(const AttnParams &params, int width, bool e4m3,
   LatentLaunch a = {};
   a.num_sms = num_sms;
   a.rows = ws;
-  a.partials = reinterpret_cast<float *>(static_cast<char *>(ws) + table_bytes(p.T, p.Hq));
+  const int rows = latent_rows(p.S, p.T, p.Hq);
+  char *const at = static_cast<char *>(ws) + table_bytes(p.T, p.Hq);
+  a.ml = reinterpret_cast<float2 *>(at);
+  a.partials = reinterpret_cast<float *>(at + ml_bytes(rows, num_sms));
   a.status = status;
   a.wait_limit_ns = wait_limit_ns;
   a.hold = hold;
-  const int rows = latent_rows(p.S, p.T, p.Hq);
   p.box = 0;
   // boxes of 8 tokens of a page; strides of zero (a broadcast cache) or an encoder that
   // refuses: copies by hand
-  if (p.c.page_size % 8 == 0 && p.c.page_stride > 0 && p.c.token_stride > 0) {
+  if (!e4m3 && p.c.page_size % 8 == 0 && p.c.page_stride > 0 && p.c.token_stride > 0) {
     const long long dims[4] = {64, p.c.page_size, width / 64, p.c.num_pages};
     const long long strides[3] = {p.c.token_stride, 64, p.c.page_stride};
     const int box[4] = {64, 8, width / 64, 1};
-    if (host_map(&a.map, p.c.k, e4m3 ? 1 : 2, 4, dims, strides, box, !e4m3)) p.box = 8;
+    if (host_map(&a.map, p.c.k, 2, 4, dims, strides, box, true)) p.box = 8;
   }
   // rows of q without gaps between tokens: boxes of an item's rows (for e4m3 caches they are
   // converted on the way)

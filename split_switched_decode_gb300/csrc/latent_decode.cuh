@@ -31,8 +31,10 @@
 // each), which is the operand layout of both products with strides of a box. Other pages are
 // copied in 16-byte loads by four warps into the same layout.
 //
-// Warps: 8 softmax, 1 each for S, O, the boxes and (bf16) the boxes of q, 4 that bring the rows
-// of q where boxes do not and widen the stages to f16 (E4M3) or copy those that boxes do not fit.
+// Warps: 8 softmax, 1 each for S, O, the boxes and the boxes of q, 4 that bring the rows of q
+// and the stages where boxes do not. E4M3: 8 of those, which widen every stage to f16 on its way
+// from global memory through registers (a ring of bytes as they come beside that of the operands
+// has no room: with one operand stage, widening, products and softmax took turns, 3.5 us a stage).
 //
 // E4M3 caches: every e4m3 value is an f16 value; q is scaled by a power of two a row and
 // converted to f16, the weights are f16 and refer to F16_POWERS below the maximum.
@@ -49,7 +51,6 @@
 namespace ssd {
 namespace {
 
-constexpr int LD_THREADS = 512;
 // Stages ahead of their copy at which boxes are requested into L2: the ring holds two stages, and
 // the one that is on its way (74 KB an SM) is too little for HBM's latency under load.
 constexpr int LD_AHEAD = 2;
@@ -58,21 +59,93 @@ constexpr int LD_ITEM_COST = 4, LD_LEAST = 1;
 
 template <int MQ, bool E4M3>
 struct LdCfg {
-  static constexpr int TOK = 64, DP = LATENT_MAX_R, SLABS = LATENT_MAX_W / 64;
-  static constexpr int STAGE = TOK * LATENT_MAX_W * 2, RAW = TOK * LATENT_MAX_W;
+  static constexpr int TOK = 64, DP = LATENT_MAX_R;
+  static constexpr int STAGE = TOK * LATENT_MAX_W * 2;
   static constexpr int QBYTES = MQ * LATENT_MAX_W * 2;
   static constexpr int PBYTES = TOK * 128;  // a token's weights in 128 bytes
-  static constexpr int QB = MQ == 64 || E4M3 ? 1 : 2;
-  static constexpr int ST = E4M3 ? 1 : 2;
-  static constexpr int RST = E4M3 ? (MQ == 64 ? 2 : 3) : 0;
+  static constexpr int QB = MQ == 64 ? 1 : 2, ST = 2;
   static constexpr int NS = 4;  // buffers of scores
   static constexpr int COLS = 8 * MQ;  // O: 4 MQ, then NS S
   static constexpr int GR = MQ / 2;    // rows of a softmax group
-  static constexpr size_t SMEM = ST * STAGE + RST * RAW + QB * QBYTES + PBYTES;
-  static constexpr int SLOT = MQ * DP + 2 * MQ;
+  static constexpr int HW = E4M3 ? 8 : 4;  // helping warps
+  static constexpr int THREADS = 32 * (12 + HW);
+  static constexpr size_t SMEM = ST * STAGE + QB * QBYTES + PBYTES;
+  static constexpr int SLOT = MQ * DP;
 };
 
+// Shares (attn_kernel.cuh) with divisions in 32 bits where the work has fewer units than 2^31: one
+// in 64 bits takes 400 clocks, and a short call waits for several.
+struct LdShares {
+  long long share_n, share_r;
+  bool narrow;
+  __device__ __forceinline__ void set(long long total, int workers) {
+    narrow = total < 0x7fffffffll;
+    if (narrow) {
+      const uint32_t t = static_cast<uint32_t>(total), w = workers, n = t / w;
+      share_n = n;
+      share_r = t - n * w;
+    } else {
+      share_n = total / workers;
+      share_r = total % workers;
+    }
+  }
+  __device__ __forceinline__ int worker_of(long long unit) const {
+    const long long longer = share_r * (share_n + 1);
+    if (narrow) {
+      const uint32_t u = static_cast<uint32_t>(unit), n = static_cast<uint32_t>(share_n);
+      return unit < longer ? u / (n + 1)
+                           : static_cast<uint32_t>(share_r) +
+                                 (u - static_cast<uint32_t>(longer)) / n;
+    }
+    return static_cast<int>(unit < longer ? unit / (share_n + 1)
+                                          : share_r + (unit - longer) / share_n);
+  }
+};
+// begin_range for batches of up to 32 sequences: every warp finds the CTA's range by itself.
+template <int TOK, int M, int COST, int LEAST>
+__device__ __forceinline__ bool begin_range_small(const AttnParams &p, int H, LdShares &sh,
+                                                  Cursor<TOK, M, COST, LEAST> &c) {
+  const int lane = threadIdx.x & 31, me = blockIdx.x;
+  SeqInfo x = {};
+  long long mine = 0;
+  if (lane < p.S) {
+    x = seq_info<TOK, M>(p, H, lane);
+    mine = x.units(1, COST);
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += y;
+  }
+  const long long total = __shfl_sync(0xffffffffu, incl, 31);
+  const long long most = (total + LEAST - 1) / LEAST;
+  const int workers = static_cast<int>(most < gridDim.x ? most : gridDim.x);
+  if (me >= workers) return false;
+  sh.set(total, workers);
+  c.cur = me * sh.share_n + min(static_cast<long long>(me), sh.share_r);
+  c.end = c.cur + sh.share_n + (me < sh.share_r ? 1 : 0);
+  const long long at = incl - mine;  // units before this lane's sequence
+  const int from = __ffs(__ballot_sync(0xffffffffu, at <= c.cur && c.cur < incl)) - 1;
+  const long long off = c.cur - __shfl_sync(0xffffffffu, at, from);
+  c.s = from;
+  c.x.q0 = __shfl_sync(0xffffffffu, x.q0, from);
+  c.x.n = __shfl_sync(0xffffffffu, x.n, from);
+  c.x.len = __shfl_sync(0xffffffffu, x.len, from);
+  c.x.begin = __shfl_sync(0xffffffffu, x.begin, from);
+  c.x.kt = __shfl_sync(0xffffffffu, x.kt, from);
+  c.x.rt = __shfl_sync(0xffffffffu, x.rt, from);
+  const int per_item = c.x.kt + COST;
+  const long long i = sh.narrow ? static_cast<uint32_t>(off) / static_cast<uint32_t>(per_item)
+                                : off / per_item;
+  c.hk = 0;
+  c.rt = static_cast<int>(i);
+  c.item = c.cur - (off - i * per_item);
+  return true;
+}
+
 struct LatentPlan {
+  float2 *ml;  // maxima and sums of parts: [row of the part][begun before or in the range][worker]
   int2 *rows;  // [T * H]: a row's first worker + 65536 * its place in the parts, number of parts
   float *partials;
   unsigned *status;
@@ -179,7 +252,7 @@ __device__ __forceinline__ uint64_t sw128_any(uint32_t saddr, uint32_t leading, 
 }
 
 template <int MQ, bool E4M3>
-__global__ void __launch_bounds__(LD_THREADS, 1)
+__global__ void __launch_bounds__((LdCfg<MQ, E4M3>::THREADS), 1)
     latent_decode_kernel(const __grid_constant__ CUtensorMap map,
                          const __grid_constant__ CUtensorMap qmap,
                          const __grid_constant__ AttnParams p, const LatentPlan pl,
@@ -188,43 +261,36 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
   constexpr int TOK = C::TOK, ST = C::ST, QB = C::QB, NS = C::NS, DP = C::DP;
   constexpr int GR = C::GR, NB = GR / 8, NC = GR / 4;  // of a group: rows, blocks; of a thread: rows
   constexpr int CH = GR < 16 ? GR : 16;  // columns of O at a time
-  extern __shared__ __align__(1024) uint8_t ld_smem[];  // ring, raw ring, q, weights
-  __shared__ RangeStart<LD_THREADS> start;
+  extern __shared__ __align__(1024) uint8_t ld_smem[];  // ring, q, weights
+  __shared__ RangeStart<C::THREADS> start;
   __shared__ __align__(8) uint64_t full[ST], empty[4 * ST], qfull[QB], qempty[QB];
-  __shared__ __align__(8) uint64_t raw_full[C::RST + 1], raw_empty[C::RST + 1];
   __shared__ __align__(8) uint64_t s_full[NS], p_full, pv_done[NS], hold, drained[2];
-  __shared__ uint64_t stage_valid[ST], raw_valid[C::RST + 1];  // tokens that exist
-  __shared__ float part[4][MQ], top[MQ], by_row[MQ], row_scale[2][MQ];
-  __shared__ int row_pos[MQ], row_out[MQ];
+  __shared__ uint64_t stage_valid[ST];  // tokens that exist
+  __shared__ float part[4][MQ], by_row[MQ], row_scale[E4M3 ? 4 : 1][MQ];
+  __shared__ int row_pos[MQ];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   static_assert(
       fits_shared<sizeof(start) + sizeof(full) + sizeof(empty) + sizeof(qfull) + sizeof(qempty) +
-                      2 * sizeof(raw_full) + sizeof(s_full) + sizeof(pv_done) + 8 * 4 +
-                      sizeof(stage_valid) + sizeof(raw_valid) + sizeof(part) + sizeof(top) +
-                      sizeof(by_row) + sizeof(row_scale) + sizeof(row_pos) + sizeof(row_out) +
+                      sizeof(s_full) + sizeof(pv_done) + 4 * 8 + sizeof(stage_valid) +
+                      sizeof(part) + sizeof(by_row) + sizeof(row_scale) + sizeof(row_pos) +
                       2 * sizeof(int),
                   C::SMEM>,
       "all of the above and the dynamic shared memory");
-  const int slabs = width >> 6, group_bytes = slabs << 10, stage_bytes = 8 * group_bytes;
-  uint8_t *const ring = ld_smem, *const raw = ring + ST * C::STAGE;
-  uint8_t *const q_smem = raw + C::RST * C::RAW, *const w_smem = q_smem + QB * C::QBYTES;
+  const int slabs = width >> 6, group_bytes = slabs << 10;
+  uint8_t *const ring = ld_smem, *const q_smem = ring + ST * C::STAGE;
+  uint8_t *const w_smem = q_smem + QB * C::QBYTES;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const bool boxes = p.box > 0;
-  const bool by_hand = E4M3 || !boxes;  // helpers fill the ring
+  const bool boxes = !E4M3 && p.box > 0;  // or helpers fill the ring
   if (tid == 0) {
     abort_flag = 0;
     for (int i = 0; i < ST; ++i) {
-      mbar_init(&full[i], by_hand ? 4 : 1);
+      mbar_init(&full[i], boxes ? 1 : C::HW);
       for (int y = 0; y < 4; ++y) mbar_init(&empty[4 * i + y], 1);
     }
-    for (int i = 0; i < C::RST; ++i) {
-      mbar_init(&raw_full[i], 1);
-      mbar_init(&raw_empty[i], 4);
-    }
     for (int i = 0; i < QB; ++i) {
-      mbar_init(&qfull[i], pl.q_boxes ? 1 : 4);
+      mbar_init(&qfull[i], pl.q_boxes ? 1 : C::HW);
       mbar_init(&qempty[i], 1);
     }
     for (int i = 0; i < NS; ++i) {
@@ -241,15 +307,17 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
   }
   griddep_wait();
   const int H = p.Hq;
-  if (p.q_start) {  // rows behind the last sequence: no parts
-    const long long first = static_cast<long long>(min(max(p.q_start[p.S], 0), p.T)) * H;
-    for (long long i = first + blockIdx.x * LD_THREADS + tid; i < static_cast<long long>(p.T) * H;
-         i += gridDim.x * LD_THREADS)
-      pl.rows[i] = make_int2(0, 0);
-  }
-  Shares sh;
+  LdShares sh;
   Cursor<TOK, MQ, LD_ITEM_COST, LD_LEAST> c;
-  if (!begin_range<LD_THREADS>(p, H, start, sh, c)) return;
+  if (p.S <= 32) {
+    if (!begin_range_small(p, H, sh, c)) return;
+  } else {
+    Shares wide;
+    if (!begin_range<C::THREADS>(p, H, start, wide, c)) return;
+    sh.share_n = wide.share_n;
+    sh.share_r = wide.share_r;
+    sh.narrow = (wide.share_n + 1) * gridDim.x < 0x7fffffffll;
+  }
   if (warp == 8) {
     tmem_alloc(&tmem_slot, C::COLS);
     tmem_relinquish();
@@ -271,12 +339,7 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
     // ================================================================ boxes of the cache
     // The pages of 32 blocks of 8 tokens are looked up in one step (four stages), a step ahead;
     // the boxes leave from one thread.
-    constexpr int CST = E4M3 ? C::RST : ST;
-    uint64_t *const bar_full = E4M3 ? raw_full : full;
-    uint64_t *const bits_of = E4M3 ? raw_valid : stage_valid;
-    const int box_bytes = E4M3 ? group_bytes / 2 : group_bytes;
-    const uint32_t base = smem_u32(E4M3 ? raw : ring);
-    constexpr int PITCH = E4M3 ? C::RAW : C::STAGE;
+    const uint32_t base = smem_u32(ring);
     int k = 0;
     bool go = boxes;
     while (go && c.next(p, H)) {
@@ -300,7 +363,7 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
       while (go && t < c.t1) {
         const uint32_t exist = __ballot_sync(0xffffffffu, page >= 0 && page < p.c.num_pages);
         for (int i = 0; i < 4 && t < c.t1; ++i, ++t) {
-          const int at = k + t - c.t0, st = at % CST;
+          const int at = k + t - c.t0, st = at % ST;
           const uint32_t blocks = exist >> (8 * i) & 255u;
           const int left = c.x.len - c.x.begin - t * TOK;
           uint64_t bits = 0;
@@ -318,15 +381,14 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
           // a quarter of the stage as soon as the last product that reads it is done
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
-            if (at >= CST && (!E4M3 || y == 0))
-              go = __all_sync(0xffffffffu,
-                              wait(E4M3 ? &raw_empty[st] : &empty[4 * st + y], at / CST - 1));
+            if (at >= ST)
+              go = __all_sync(0xffffffffu, wait(&empty[4 * st + y], at / ST - 1));
             if (!go) break;
             if (y == 0) {
               issued = at + 1;
               if (elect_one()) {
-                bits_of[st] = bits;
-                mbar_arrive_expect_tx(&bar_full[st], __popc(blocks) * box_bytes);
+                stage_valid[st] = bits;
+                mbar_arrive_expect_tx(&full[st], __popc(blocks) * group_bytes);
               }
             }
 #pragma unroll
@@ -334,7 +396,7 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
               const int pg = __shfl_sync(0xffffffffu, page, i * 8 + b);
               const int o = __shfl_sync(0xffffffffu, off, i * 8 + b);
               if ((blocks >> b & 1) && elect_one())
-                tma_load_4d(base + st * PITCH + b * box_bytes, &map, &bar_full[st], 0, o, 0, pg);
+                tma_load_4d(base + st * C::STAGE + b * group_bytes, &map, &full[st], 0, o, 0, pg);
               __syncwarp();
             }
           }
@@ -366,24 +428,30 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
       __syncwarp();
       ++seg;
     }
+    if (p.q_start) {  // rows behind the last sequence: no parts
+      const long long first = static_cast<long long>(min(max(p.q_start[p.S], 0), p.T)) * H;
+      const long long all = static_cast<long long>(p.T) * H;
+      for (long long i = first + blockIdx.x * 32 + lane; i < all; i += gridDim.x * 32)
+        pl.rows[i] = make_int2(0, 0);
+    }
   } else if (warp >= 12) {
     // ================================================================ rows of q, stages by hand
     const int hw = warp - 12;
     const bool q_by_hand = !pl.q_boxes;
     const int chunks = width >> 3;  // 16-byte chunks of a row: at most 72
     int k = 0, seg = 0;
-    while ((by_hand || q_by_hand) && c.next(p, H)) {
+    while ((!boxes || q_by_hand) && c.next(p, H)) {
       // q: a warp a row, four rows at a time
       const int qb = seg % QB;
       const int n_rows = min(MQ, c.x.n * H - c.rt * MQ);
       uint8_t *qd = q_smem + qb * C::QBYTES;
       bool waited = seg < QB;
 #pragma unroll 1
-      for (int r0 = hw; q_by_hand && r0 < MQ; r0 += 16) {
+      for (int r0 = hw; q_by_hand && r0 < MQ; r0 += 4 * C::HW) {
         uint4 v[4][3];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int r = r0 + 4 * e;
+          const int r = r0 + C::HW * e;
           const int rr = c.rt * MQ + r, tok = rr / H, g = rr - tok * H;
           const uint16_t *src = p.q + (c.x.q0 + tok) * p.q_stride + static_cast<long long>(g) * width;
 #pragma unroll
@@ -400,7 +468,8 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int r = r0 + 4 * e;
+          const int r = r0 + C::HW * e;
+          if (r >= MQ) break;
           if (E4M3) {
             float mx = 0.0f;
 #pragma unroll
@@ -413,7 +482,7 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
             for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
             const int ex = q_exponent(mx);
             const float f = power_of_two(-ex);
-            if (lane == 0) row_scale[seg & 1][r] = power_of_two(ex);
+            if (lane == 0) row_scale[seg & 3][r] = power_of_two(ex);
 #pragma unroll
             for (int i = 0; i < 3; ++i)
               v[e][i] = make_uint4(pack2<true>(bf16lo(v[e][i].x) * f, bf16hi(v[e][i].x) * f),
@@ -436,40 +505,69 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
         if (lane == 0) mbar_arrive(&qfull[qb]);
       }
       ++seg;
-      if (!by_hand) continue;
+      if (boxes) continue;
       const int32_t *table = p.block_table + static_cast<long long>(c.s) * p.max_pages;
-      for (int t = c.t0; t < c.t1; ++t, ++k) {
-        const int st = k % ST;
-        uint8_t *to = ring + st * C::STAGE;
-        if (E4M3 && boxes) {
-          const int rs = k % (C::RST + (C::RST == 0));
-          wait(&raw_full[rs], k / (C::RST + (C::RST == 0)));
-          if (k >= ST) wait(&empty[4 * st + 3], k / ST - 1);
-          const uint8_t *from = raw + rs * C::RAW;
-          const int n = stage_bytes / 32;  // 16-byte chunks as they came
-#pragma unroll 4
-          for (int i = tid - 384; i < n; i += 128) {
-            // chunk (slab, row, quarter) of box g
-            const int g = i / (32 * slabs), y = i - g * 32 * slabs;
-            const int slab = y >> 5, r = y >> 2 & 7, ch = (y & 3) * 2;
-            const uint4 v = *reinterpret_cast<const uint4 *>(from + i * 16);
-            uint8_t *d = to + g * group_bytes + slab * 1024 + r * 128;
-            *reinterpret_cast<uint4 *>(d + ((ch ^ r) << 4)) =
-                make_uint4(e4m3x2_to_f16x2(v.x), e4m3x2_to_f16x2(v.x >> 16),
-                           e4m3x2_to_f16x2(v.y), e4m3x2_to_f16x2(v.y >> 16));
-            *reinterpret_cast<uint4 *>(d + (((ch + 1) ^ r) << 4)) =
-                make_uint4(e4m3x2_to_f16x2(v.z), e4m3x2_to_f16x2(v.z >> 16),
-                           e4m3x2_to_f16x2(v.w), e4m3x2_to_f16x2(v.w >> 16));
+      if constexpr (E4M3) {
+        // A warp has eight tokens, one swizzle group; a lane 16 bytes of every 64 of one token.
+        // The next stage's bytes are on their way in registers while this one is in use, and
+        // those of the one after it are requested into L2.
+        const int r = lane >> 2, ch = (lane & 3) * 2;
+        auto place = [&](int t) -> long long {  // this lane's token: its element, -1: none
+          const int j = c.x.begin + t * TOK + hw * 8 + r;
+          if (t >= c.t1 || j >= c.x.len) return -1;
+          const int i = j / p.c.page_size, pg = table[i];
+          if (pg < 0 || pg >= p.c.num_pages) return -1;
+          return pg * p.c.page_stride + (j - i * p.c.page_size) * p.c.token_stride;
+        };
+        const uint8_t *const bytes = static_cast<const uint8_t *>(p.c.k);
+        uint4 v[LATENT_MAX_W / 64];
+        auto load = [&](long long at) {
+#pragma unroll
+          for (int i = 0; i < LATENT_MAX_W / 64; ++i) {
+            v[i] = make_uint4(0, 0, 0, 0);
+            if (at >= 0 && i < slabs)
+              v[i] = *reinterpret_cast<const uint4 *>(bytes + at + i * 64 + ch * 8);
           }
-          if (tid == 384) stage_valid[st] = raw_valid[rs];
+        };
+        long long here = place(c.t0), next = place(c.t0 + 1);
+        load(here);
+        for (int t = c.t0; t < c.t1; ++t, ++k) {
+          const int st = k % ST;
+          const uint32_t exist = __ballot_sync(0xffffffffu, here >= 0);
+          const long long after = place(t + 2);
+          if (after >= 0 && (lane & 3) == 0) prefetch_l2_bulk(bytes + after, width);
+          if (k >= ST) wait(&empty[4 * st + 3], k / ST - 1);
+          uint8_t *d = ring + st * C::STAGE + hw * group_bytes + r * 128;
+#pragma unroll
+          for (int i = 0; i < LATENT_MAX_W / 64; ++i) {
+            if (i >= slabs) break;
+            const uint4 y = v[i];
+            *reinterpret_cast<uint4 *>(d + i * 1024 + ((ch ^ r) << 4)) =
+                make_uint4(e4m3x2_to_f16x2(y.x), e4m3x2_to_f16x2(y.x >> 16),
+                           e4m3x2_to_f16x2(y.y), e4m3x2_to_f16x2(y.y >> 16));
+            *reinterpret_cast<uint4 *>(d + i * 1024 + (((ch + 1) ^ r) << 4)) =
+                make_uint4(e4m3x2_to_f16x2(y.z), e4m3x2_to_f16x2(y.z >> 16),
+                           e4m3x2_to_f16x2(y.w), e4m3x2_to_f16x2(y.w >> 16));
+          }
+          if (lane == 0) {
+            uint32_t bits = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) bits |= (exist >> (4 * i) & 1u) << i;
+            reinterpret_cast<volatile uint8_t *>(&stage_valid[st])[hw] =
+                static_cast<uint8_t>(bits);
+          }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&full[st]);
-            mbar_arrive(&raw_empty[rs]);
-          }
-        } else {
-          // 16 tokens a warp, each looked up by itself
+          if (lane == 0) mbar_arrive(&full[st]);
+          here = next;
+          next = after;
+          if (t + 1 < c.t1) load(here);
+        }
+      } else {
+        // 16 tokens a warp, each looked up by itself
+        for (int t = c.t0; t < c.t1; ++t, ++k) {
+          const int st = k % ST;
+          uint8_t *to = ring + st * C::STAGE;
           const int j = c.x.begin + t * TOK + hw * 16 + (lane & 15);
           long long at = -1;
           if (j < c.x.len) {
@@ -479,20 +577,18 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
           }
           const uint32_t exist = __ballot_sync(0xffffffffu, at >= 0) & 0xffffu;
           if (k >= ST) wait(&empty[4 * st + 3], k / ST - 1);
-          constexpr int ES = E4M3 ? 1 : 2, PER = E4M3 ? 2 : 3;  // 16-byte loads of a lane
-          const int loads = width * ES / 16;
 #pragma unroll 1
           for (int x0 = 0; x0 < 16; x0 += 4) {
-            uint4 v[4][PER];
+            uint4 v[4][3];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const long long src = __shfl_sync(0xffffffffu, at, x0 + e);
 #pragma unroll
-              for (int i = 0; i < PER; ++i) {
+              for (int i = 0; i < 3; ++i) {
                 v[e][i] = make_uint4(0, 0, 0, 0);
-                if (src >= 0 && lane + 32 * i < loads)
+                if (src >= 0 && lane + 32 * i < chunks)
                   v[e][i] = *reinterpret_cast<const uint4 *>(
-                      static_cast<const uint8_t *>(p.c.k) + src * ES + (lane + 32 * i) * 16);
+                      static_cast<const uint16_t *>(p.c.k) + src + (lane + 32 * i) * 8);
               }
             }
 #pragma unroll
@@ -500,22 +596,10 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
               const int tok = hw * 16 + x0 + e, r = tok & 7;
               uint8_t *d = to + (tok >> 3) * group_bytes + r * 128;
 #pragma unroll
-              for (int i = 0; i < PER; ++i) {
+              for (int i = 0; i < 3; ++i) {
                 const int l = lane + 32 * i;
-                if (l >= loads) continue;
-                const uint4 y = v[e][i];
-                if (E4M3) {
-                  uint8_t *s = d + (l >> 2) * 1024;
-                  const int ch = (l & 3) * 2;
-                  *reinterpret_cast<uint4 *>(s + ((ch ^ r) << 4)) =
-                      make_uint4(e4m3x2_to_f16x2(y.x), e4m3x2_to_f16x2(y.x >> 16),
-                                 e4m3x2_to_f16x2(y.y), e4m3x2_to_f16x2(y.y >> 16));
-                  *reinterpret_cast<uint4 *>(s + (((ch + 1) ^ r) << 4)) =
-                      make_uint4(e4m3x2_to_f16x2(y.z), e4m3x2_to_f16x2(y.z >> 16),
-                                 e4m3x2_to_f16x2(y.w), e4m3x2_to_f16x2(y.w >> 16));
-                } else {
-                  *reinterpret_cast<uint4 *>(d + (l >> 3) * 1024 + (((l & 7) ^ r) << 4)) = y;
-                }
+                if (l < chunks)
+                  *reinterpret_cast<uint4 *>(d + (l >> 3) * 1024 + (((l & 7) ^ r) << 4)) = v[e][i];
               }
             }
           }
@@ -603,11 +687,10 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
       const SeqInfo &x = c.x;
       const int n_rows = min(MQ, x.n * H - c.rt * MQ), row0 = c.rt * MQ;
       const int pos0 = x.len - x.n;
-      // the last key that a row sees, and its token; what every row sees
+      // the last key that a row sees (its token's position); what every row sees
       if (gt < GR) {
         const int r = g0 + gt, tok = (row0 + min(r, n_rows - 1)) / H;
         row_pos[r] = pos0 + tok;
-        row_out[r] = tok;
       }
       const int hi_all = pos0 + row0 / H, hi_top = pos0 + (row0 + n_rows - 1) / H;
       const int lo_all = p.window > 0 && hi_top >= p.window ? hi_top - p.window + 1 : 0;
@@ -629,7 +712,7 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
         if (E4M3 && begins) {
 #pragma unroll
           for (int i = 0; i < NC; ++i)
-            zf[i] = scale * row_scale[seg & 1][g0 + 8 * (i >> 1) + col + (i & 1)];
+            zf[i] = scale * row_scale[seg & 3][g0 + 8 * (i >> 1) + col + (i & 1)];
         }
         tmem_wait_ld();
 #pragma unroll
@@ -774,19 +857,19 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
         const int r = g0 + 8 * (i >> 1) + col + (i & 1);
         if (lane < 4) {
           part[w4][r] = s;
-          if (w4 == 0) top[r] = m[i];
+          if (w4 == 0) by_row[r] = m[i];
         }
       }
       named_bar_sync(bar, 128);
       if (gt < GR && g0 + gt < n_rows) {
         const int r = g0 + gt;
-        const float mr = top[r];
+        const float mr = by_row[r];
         const float lr = (part[0][r] + part[1][r]) + (part[2][r] + part[3][r]);
         if (c0 == c1) {
           dst.put_lse(p, r, mr, lr);
           by_row[r] = lr == 0.0f ? 0.0f : v_scale / lr;
         } else {
-          *reinterpret_cast<float2 *>(slot + MQ * DP + 2 * r) = make_float2(mr, lr);
+          pl.ml[(2 * r + (me == c0 ? 1 : 0)) * gridDim.x + me] = make_float2(mr, lr);
         }
         // where the row's parts are
         if (me == c0)
@@ -816,7 +899,7 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
               const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? y0 : y1, 1);
               const int r = r0 + e + (lane & 1);
               if (r < n_rows && dim < p.D) {
-                const int tok = row_out[r], head = row0 + r - tok * H;
+                const int tok = row_pos[r] - pos0, head = row0 + r - tok * H;
                 *reinterpret_cast<uint32_t *>(p.out + (x.q0 + tok) * p.out_stride +
                                               static_cast<long long>(head) * p.D + (dim & ~1)) =
                     lane & 1 ? pack2<false>(got, y1) : pack2<false>(y0, got);
@@ -846,10 +929,8 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
       __syncwarp();
       mbar_wait_drain(bar, 0, 10000000ull);
     }
-    constexpr int CST = E4M3 ? C::RST : ST;
-    uint64_t *const bar_full = E4M3 ? raw_full : full;
-    for (int i = issued - 1; i >= 0 && i >= issued - CST; --i)
-      mbar_wait_drain(&bar_full[i % CST], (i / CST) & 1, 10000000ull);
+    for (int i = issued - 1; i >= 0 && i >= issued - ST; --i)
+      mbar_wait_drain(&full[i % ST], (i / ST) & 1, 10000000ull);
     for (int i = q_issued - 1; i >= 0 && i >= q_issued - QB; --i)
       mbar_wait_drain(&qfull[i % QB], (i / QB) & 1, 10000000ull);
     tc_fence_before();
@@ -868,13 +949,14 @@ cudaError_t launch_latent_shape(const AttnParams &p, int width, const LatentLaun
                                              static_cast<int>(C::SMEM));
   if (e != cudaSuccess) return e;
   LatentPlan pl;
+  pl.ml = a.ml;
   pl.rows = static_cast<int2 *>(a.rows);
   pl.partials = a.partials;
   pl.status = a.status;
   pl.wait_limit_ns = a.wait_limit_ns;
   pl.hold = a.hold;
   pl.q_boxes = !E4M3 && a.q_boxes;
-  return launch_pdl(kernel, dim3(a.num_sms), dim3(LD_THREADS), C::SMEM, s, a.map, a.qmap, p, pl,
+  return launch_pdl(kernel, dim3(a.num_sms), dim3(C::THREADS), C::SMEM, s, a.map, a.qmap, p, pl,
                     width);
 }
 
