@@ -262,10 +262,11 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
     // ================================================================ values
     const int w = warp - 10;
     for (int j = 0; j < nt; ++j) {
-      for (int i = 0; i < vn; ++i) {
-        const int at = j * step + kn + i;
-        wait(&full[at % PR_SLOTS], at / PR_SLOTS);
-      }
+      // Every slab in turn, the keys' too: a wait tells only neighbouring phases apart, and a slot
+      // whose last slab has not landed would pass for one that holds the next (values that landed
+      // before the first keys let these warps run ahead of the products, which then never
+      // saw v_ready's phase).
+      for (int at = j * step; at < (j + 1) * step; ++at) wait(&full[at % PR_SLOTS], at / PR_SLOTS);
       if (partial(0, j) || partial(1, j)) {
         // 64 tokens a warp, four rows of eight chunks a step
 #pragma unroll 1

@@ -546,6 +546,18 @@ def test_prompt_many_sequences(env):
     p.check()
 
 
+def test_prompt_many_calls(env):
+    """The same bits and no wait that runs out over a thousand blocks of rows, 300 times."""
+    torch, ssd, dev = env
+    p = _Prompt(env, [4096], [4096], 64, extra=0)
+    p.run()
+    first = p.out.clone()
+    for _ in range(300):
+        p.run()
+    assert ssd.dec_sync_status() == ssd.DEC_OK
+    assert torch.equal(first, p.out)
+
+
 def test_prompt_keys_by_default(env):
     torch, ssd, dev = env
     p = _Prompt(env, [200, 77], [200, 77], 4, extra=0)
