@@ -16,12 +16,21 @@
 //
 // in the order PV0(j) S0(j+1) PV1(j) S1(j+1). Products of a thread run in order, so the scores
 // of j + 1 may overwrite the weights of j, and their arrival tells the softmax that O is whole.
-// Keys and values stream through a ring of eight slabs (128 tokens x 64 elements, 16 KB): K(j),
-// V(j), K(j+1), ...; V's two slabs are products of 64 columns each, as they need not be
-// neighbours.
+// The tensor core holds a few products ahead of their execution, so what the issuing thread does
+// between two lots has to stay below 300 clocks: it waits alone, for whole tiles, with the shape
+// known at compile time.
 //
-// The running maximum is moved only when it has grown by 8 or more (attn_tc.cuh); sums are
-// fp32 of the weights before rounding to bf16 (off by 2^-8 of themselves).
+// Keys and values stream through a ring of eight slabs (128 tokens x 64 elements, 16 KB): K(j),
+// V(j), K(j+1), ... The two slabs of a V tile are one product of 128 columns where they are
+// neighbours, two of 64 where the ring's end is between them.
+//
+// A thread's 128 scores come 64 at a time. The first half's maximum decides whether the running
+// maximum moves (by 8 or more; attn_tc.cuh), its weights are stored and their product starts;
+// the second half refers to the same maximum unless it exceeds it by 16 or more: larger weights
+// cost no bits, as their rounding is relative (2^-8, to bf16) and sums are fp32, and stay far
+// below what overflows. Only then O is rescaled once more, behind the first half's product. (With a
+// pass for the maximum of all 128 first, the way from scores to weights took 1800 clocks
+// instead of 1150, longer than the other group's products.)
 //
 // What is not finite in values: in tiles that some row does not see whole, two warps take it
 // out of shared memory and note the tokens; rows that see such a token add it from global
@@ -39,8 +48,12 @@ namespace ssd {
 namespace {
 
 constexpr int PR_THREADS = 384;  // 8 softmax warps, boxes, products, 2 that look at values
-constexpr int PR_SLOTS = 8, PR_SLAB = 128 * 128, PR_ROWS = 256, PR_VB = 4;
+constexpr int PR_SLOTS = 8, PR_SLAB = 128 * 128, PR_ROWS = 256;
+// Barriers of tiles, taken in turn: as many as there are tiles in the ring (two slabs each at least),
+// so that the last use of one is over when it is armed again.
+constexpr int PR_TB = 4;
 constexpr int PR_MAX_Q = 3;  // slabs of q and k
+constexpr float PR_LATE = 16.0f;  // growth in the second half that moves the maximum
 constexpr size_t PR_SMEM = (2 * PR_MAX_Q + PR_SLOTS) * static_cast<size_t>(PR_SLAB);
 
 struct PromptBlock {
@@ -103,6 +116,7 @@ __device__ __forceinline__ bool find_block(const LatentPromptParams &p, int blk,
   return true;
 }
 
+template <int KN, int VN>  // slabs of a key tile, of a value tile
 __global__ void __launch_bounds__(PR_THREADS, 1)
     latent_prompt_kernel(const __grid_constant__ CUtensorMap qmap,
                          const __grid_constant__ CUtensorMap kmap,
@@ -112,23 +126,28 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                          const long long v_stride, const long long v_head) {
   extern __shared__ __align__(1024) uint8_t pr_smem[];  // Q0, Q1, the ring
   __shared__ PromptSearch search;
-  __shared__ __align__(8) uint64_t qfull[2], full[PR_SLOTS], empty[PR_SLOTS], v_ready[PR_VB];
-  __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_full[2], drained;
-  __shared__ uint32_t bad[PR_VB][4];  // tokens with values that are not finite
+  __shared__ __align__(8) uint64_t k_full[PR_TB], k_empty[PR_TB], v_full[PR_TB], v_empty[PR_TB];
+  __shared__ __align__(8) uint64_t v_ready[PR_TB], qfull[2], s_full[2], p_half[2], p_full[2], h_done[2];
+  __shared__ __align__(8) uint64_t o_full[2], drained;
+  __shared__ uint32_t bad[PR_TB][4];  // tokens with values that are not finite
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag, keep_first[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     abort_flag = 0;
-    for (int i = 0; i < PR_SLOTS; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+    for (int i = 0; i < PR_TB; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
+      mbar_init(&v_ready[i], 2);
     }
-    for (int i = 0; i < PR_VB; ++i) mbar_init(&v_ready[i], 2);
     for (int g = 0; g < 2; ++g) {
       mbar_init(&qfull[g], 1);
       mbar_init(&s_full[g], 1);
+      mbar_init(&p_half[g], 128);
       mbar_init(&p_full[g], 128);
+      mbar_init(&h_done[g], 1);
       mbar_init(&o_full[g], 1);
       keep_first[g] = 0;
     }
@@ -153,7 +172,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
   // after the allocation: a dependent grid's CTA cannot hold the columns this one waits for
   griddep_launch_dependents();
   const uint32_t tmem = tmem_slot;  // S0, S1, O0, O1
-  const int kn = (p.N + p.P) >> 6, vn = p.V >> 6, step = kn + vn;
+  constexpr int STEP = KN + VN;
   // position of row i is shift + i; tiles of 128 keys that some row of a group sees
   const int shift = b.len - b.n;
   auto rows_of = [&](int g) { return min(128, b.n - b.row0 - 128 * g); };
@@ -178,102 +197,120 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
     if (elect_one()) {
       for (int g = 0; g < 2; ++g) {
         if ((g ? nt1 : nt0) == 0) continue;
-        mbar_arrive_expect_tx(&qfull[g], kn * PR_SLAB);
-        for (int i = 0; i < kn; ++i)
+        mbar_arrive_expect_tx(&qfull[g], KN * PR_SLAB);
+        for (int i = 0; i < KN; ++i)
           tma_load_3d(smem_u32(pr_smem + (g * PR_MAX_Q + i) * PR_SLAB), &qmap, &qfull[g], i * 64, h,
                       b.q0 + b.row0 + 128 * g);
       }
     }
     __syncwarp();
-    for (int i = 0; go && i < nt * step; ++i) {
-      const int slot = i % PR_SLOTS, j = i / step, x = i - j * step, tok = b.k0 + j * 128;
-      if (i >= PR_SLOTS) go = __all_sync(0xffffffffu, wait(&empty[slot], i / PR_SLOTS - 1));
-      if (!go) break;
-      issued = i + 1;
-      if (elect_one()) {
-        const uint32_t to = smem_u32(ring + slot * PR_SLAB);
-        mbar_arrive_expect_tx(&full[slot], PR_SLAB);
-        if (x * 64 < p.N) tma_load_3d(to, &kmap, &full[slot], x * 64, h, tok);
-        else if (x < kn) tma_load_3d(to, &rmap, &full[slot], x * 64 - p.N, 0, tok);
-        else tma_load_3d(to, &vmap, &full[slot], (x - kn) * 64, h, tok);
+    for (int i = 0, j = 0; go && j < nt; ++j) {
+      const int tok = b.k0 + j * 128;
+#pragma unroll 1
+      for (int x = 0; x < STEP; ++x, ++i) {
+        if (i >= PR_SLOTS) {  // what held the slot: a slab of tile j2's keys or values
+          const int j2 = (i - PR_SLOTS) / STEP, x2 = i - PR_SLOTS - j2 * STEP;
+          uint64_t *const bar = x2 < KN ? &k_empty[j2 % PR_TB] : &v_empty[j2 % PR_TB];
+          go = __all_sync(0xffffffffu, wait(bar, j2 / PR_TB));
+          if (!go) break;
+        }
+        issued = i + 1;
+        if (elect_one()) {
+          const uint32_t to = smem_u32(ring + i % PR_SLOTS * PR_SLAB);
+          uint64_t *const bar = x < KN ? &k_full[j % PR_TB] : &v_full[j % PR_TB];
+          if (x == 0) mbar_arrive_expect_tx(bar, KN * PR_SLAB);
+          if (x == KN) mbar_arrive_expect_tx(bar, VN * PR_SLAB);
+          if (x * 64 < p.N) tma_load_3d(to, &kmap, bar, x * 64, h, tok);
+          else if (x < KN) tma_load_3d(to, &rmap, bar, x * 64 - p.N, 0, tok);
+          else tma_load_3d(to, &vmap, bar, (x - KN) * 64, h, tok);
+        }
+        __syncwarp();
       }
-      __syncwarp();
     }
   } else if (warp == 9) {
     // ================================================================ products
-    const uint32_t id_s = idesc_bf16(128), id_o = idesc_bf16(64) | (1u << 16);
-    const uint32_t ring_u = smem_u32(ring), q_u = smem_u32(pr_smem);
-    auto scores = [&](int g, int j, bool last) {
-      for (int i = 0; i < kn; ++i) {
-        const int at = j * step + i;
-        wait(&full[at % PR_SLOTS], at / PR_SLOTS);
-      }
-      tc_fence_after();
-      if (elect_one()) {
-#pragma unroll 1
-        for (int i = 0; i < kn; ++i) {
-          const int slot = (j * step + i) % PR_SLOTS;
-          const uint64_t a = sw128_desc(q_u + (g * PR_MAX_Q + i) * PR_SLAB);
-          const uint64_t k = sw128_desc(ring_u + slot * PR_SLAB);
+    if (elect_one()) {
+      const uint32_t id_s = idesc_bf16(128), id_o = idesc_bf16(64 * VN) | (1u << 16);
+      const uint32_t id_o64 = idesc_bf16(64) | (1u << 16);
+      const uint64_t ring_k = sw128_desc(smem_u32(ring));
+      const uint64_t ring_v = sw128_mn_desc(smem_u32(ring), PR_SLAB);
+      auto scores = [&](int g, int j, bool last) {
+        const uint64_t q = sw128_desc(smem_u32(pr_smem) + g * PR_MAX_Q * PR_SLAB);
+        if (g == 0 || j >= nt0) wait(&k_full[j % PR_TB], j / PR_TB);
+        tc_fence_after();
+#pragma unroll
+        for (int i = 0; i < KN; ++i) {
+          const uint64_t a = q + i * (PR_SLAB >> 4);
+          const uint64_t k = ring_k + static_cast<uint32_t>((j * STEP + i) % PR_SLOTS) * (PR_SLAB >> 4);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             tc_mma(tmem + g * 128, a + 2 * kk, k + 2 * kk, id_s, i > 0 || kk > 0 ? 1u : 0u);
-          if (last) tc_commit(&empty[slot]);
         }
         tc_commit(&s_full[g]);
-      }
-      __syncwarp();
-    };
-    auto outputs = [&](int g, int j, bool last) {
-      wait(&p_full[g], j);
-      wait(&v_ready[j % PR_VB], j / PR_VB);
-      tc_fence_after();
-      const uint32_t acc = j > 0 || *static_cast<volatile int *>(&keep_first[g]) != 0 ? 1u : 0u;
-      if (elect_one()) {
-#pragma unroll 1
-        for (int i = 0; i < vn; ++i) {
-          const int slot = (j * step + kn + i) % PR_SLOTS;
-          const uint64_t v = sw128_mn_desc(ring_u + slot * PR_SLAB, PR_SLAB);
+        if (last) tc_commit(&k_empty[j % PR_TB]);
+      };
+      auto outputs = [&](int g, int j, bool last) {
+        const uint32_t slot = static_cast<uint32_t>(j * STEP + KN) % PR_SLOTS;
+        const uint64_t v = ring_v + slot * (PR_SLAB >> 4);
+        const bool split = VN == 2 && slot == PR_SLOTS - 1;  // the second slab is slot 0
+        const uint32_t o = tmem + 256 + g * 128, w = tmem + g * 128;
+        if (g == 0 || j >= nt0) wait(&v_ready[j % PR_TB], j / PR_TB);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            tc_mma_ts(tmem + 256 + g * 128 + i * 64, tmem + g * 128 + kk * 8,
-                      v + (2048 >> 4) * kk, id_o, kk > 0 ? 1u : acc);
-          if (last) tc_commit(&empty[slot]);
+        for (int half = 0; half < 2; ++half) {
+          wait(half ? &p_full[g] : &p_half[g], j);
+          tc_fence_after();
+          const uint32_t acc =
+              half || j > 0 || *static_cast<volatile int *>(&keep_first[g]) != 0 ? 1u : 0u;
+          if (!split) {
+#pragma unroll
+            for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+              tc_mma_ts(o, w + kk * 8, v + (2048 >> 4) * kk, id_o, (kk & 3) > 0 ? 1u : acc);
+          } else {
+#pragma unroll
+            for (int kk = 4 * half; kk < 4 * half + 4; ++kk) {
+              tc_mma_ts(o, w + kk * 8, v + (2048 >> 4) * kk, id_o64, (kk & 3) > 0 ? 1u : acc);
+              tc_mma_ts(o + 64, w + kk * 8, ring_v + (2048 >> 4) * kk, id_o64,
+                        (kk & 3) > 0 ? 1u : acc);
+            }
+          }
+          if (half == 0) tc_commit(&h_done[g]);
         }
+        if (last) tc_commit(&v_empty[j % PR_TB]);
         if (j + 1 == (g ? nt1 : nt0)) tc_commit(&o_full[g]);
+      };
+      if (nt0 > 0) {
+        wait(&qfull[0], 0);
+        scores(0, 0, nt1 == 0);
       }
-      __syncwarp();
-    };
-    if (nt0 > 0) {
-      wait(&qfull[0], 0);
-      scores(0, 0, nt1 == 0);
+      if (nt1 > 0) {
+        wait(&qfull[1], 0);
+        scores(1, 0, true);
+      }
+#pragma unroll 1
+      for (int j = 0; j < nt; ++j) {
+        if (j < nt0) outputs(0, j, j >= nt1);
+        if (j + 1 < nt0) scores(0, j + 1, j + 1 >= nt1);
+        if (j < nt1) outputs(1, j, true);
+        if (j + 1 < nt1) scores(1, j + 1, true);
+      }
     }
-    if (nt1 > 0) {
-      wait(&qfull[1], 0);
-      scores(1, 0, true);
-    }
-    for (int j = 0; j < nt; ++j) {
-      if (j < nt0) outputs(0, j, j >= nt1);
-      if (j + 1 < nt0) scores(0, j + 1, j + 1 >= nt1);
-      if (j < nt1) outputs(1, j, true);
-      if (j + 1 < nt1) scores(1, j + 1, true);
-    }
+    __syncwarp();
   } else if (warp >= 10) {
     // ================================================================ values
     const int w = warp - 10;
     for (int j = 0; j < nt; ++j) {
-      // Every slab in turn, the keys' too: a wait tells only neighbouring phases apart, and a slot
-      // whose last slab has not landed would pass for one that holds the next (values that landed
-      // before the first keys let these warps run ahead of the products, which then never
-      // saw v_ready's phase).
-      for (int at = j * step; at < (j + 1) * step; ++at) wait(&full[at % PR_SLOTS], at / PR_SLOTS);
+      // Every tile in turn: a wait tells only neighbouring phases apart. (These warps once waited
+      // for slots in which keys stood before, without waiting for the keys; values that landed
+      // first let them run ahead, and the products never saw v_ready's phase.)
+      wait(&v_full[j % PR_TB], j / PR_TB);
       if (partial(0, j) || partial(1, j)) {
         // 64 tokens a warp, four rows of eight chunks a step
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
           uint32_t seen = 0;
-          for (int i = 0; i < vn; ++i) {
-            uint8_t *slab = ring + (j * step + kn + i) % PR_SLOTS * PR_SLAB;
+#pragma unroll
+          for (int i = 0; i < VN; ++i) {
+            uint8_t *slab = ring + (j * STEP + KN + i) % PR_SLOTS * PR_SLAB;
 #pragma unroll 4
             for (int x = 0; x < 8; ++x) {
               const int tok = w * 64 + half * 32 + x * 4 + (lane >> 3);
@@ -290,12 +327,12 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                 if (vote >> (8 * r) & 255u) seen |= 1u << (x * 4 + r);
             }
           }
-          if (lane == 0) bad[j % PR_VB][2 * w + half] = seen;
+          if (lane == 0) bad[j % PR_TB][2 * w + half] = seen;
         }
         fence_proxy_async_smem();
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&v_ready[j % PR_VB]);
+      if (lane == 0) mbar_arrive(&v_ready[j % PR_TB]);
     }
   } else {
     // ================================================================ softmax, a thread a row
@@ -304,44 +341,50 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
     const uint32_t s_at = tmem + g * 128 + lanes, o_at = tmem + 256 + g * 128 + lanes;
     const int mine = g ? nt1 : nt0, row = b.row0 + 128 * g + r, pos = shift + row;
     const float zf = p.scale * LOG2E;
+    const bool least = zf < 0.0f;
     float m = -INFINITY, l = 0.0f;
+    float z[2][32];
+    float2 sum[2];
     for (int j = 0; j < mine; ++j) {
       wait(&s_full[g], j);
       tc_fence_after();
       const bool whole = !partial(g, j);
       const int to = pos - j * 128;  // the last key seen, in the tile
-      const bool least = zf < 0.0f;
-      float best[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) best[i] = least ? INFINITY : -INFINITY;
-#pragma unroll
-      for (int c0 = 0; c0 < 128; c0 += 32) {
-        float z[32];
-        tmem_ld32(s_at + c0, z);
-        tmem_wait_ld();
+      // in a tile that some row does not see whole: tokens whose values were taken out
+      const volatile uint32_t *words = bad[j % PR_TB];
+      bool taken = false;
+      if (partial(0, j) || partial(1, j)) {
+        wait(&v_ready[j % PR_TB], j / PR_TB);
+        taken = (words[0] | words[1] | words[2] | words[3]) != 0;
+      }
+      if (r == 0) keep_first[g] = taken;
+      // The largest of scores 64 half .. 64 half + 63, which are in z; those not seen are taken out.
+      auto largest = [&](int half) {
         if (!whole) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (c0 + i > to) z[i] = least ? INFINITY : -INFINITY;
+          for (int i = 0; i < 64; ++i)
+            if (64 * half + i > to) z[i >> 5][i & 31] = least ? INFINITY : -INFINITY;
         }
+        float best[4] = {z[0][0], z[0][1], z[0][2], z[0][3]};
         if (least) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) best[i & 3] = fminf(best[i & 3], z[i]);
+          for (int i = 4; i < 64; ++i) best[i & 3] = fminf(best[i & 3], z[i >> 5][i & 31]);
         } else {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) best[i & 3] = fmaxf(best[i & 3], z[i]);
+          for (int i = 4; i < 64; ++i) best[i & 3] = fmaxf(best[i & 3], z[i >> 5][i & 31]);
         }
-      }
-      float mx = least ? fminf(fminf(best[0], best[1]), fminf(best[2], best[3]))
-                       : fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3]));
-      mx = to < 0 ? -INFINITY : mx * zf;
-      if (j == 0) {
-        m = mx;
-      } else if (__any_sync(0xffffffffu, mx - m >= TC_LAZY)) {
-        const float now = mx - m >= TC_LAZY ? mx : m;
+        const float mx = least ? fminf(fminf(best[0], best[1]), fminf(best[2], best[3]))
+                               : fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3]));
+        return to < 64 * half ? -INFINITY : mx * zf;
+      };
+      // Moves the maximum of rows that grew by `by`, their sums and outputs with it.
+      auto move = [&](float mx, float by) {
+        const float now = mx - m >= by ? mx : m;
         const float fade = ex2(m - (now == -INFINITY ? 0.0f : now));
         m = now;
         l *= fade;
+        sum[0] = make_float2(sum[0].x * fade, sum[0].y * fade);
+        sum[1] = make_float2(sum[1].x * fade, sum[1].y * fade);
 #pragma unroll 1
         for (int d = 0; d < p.V; d += 16) {
           float o[16];
@@ -353,71 +396,93 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
           tmem_st16(o_at + d, u);
         }
         tmem_wait_st();
-      }
-      const float base = m == -INFINITY ? 0.0f : m;
-      float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll
-      for (int c0 = 0; c0 < 128; c0 += 32) {
-        float z[32];
-        uint32_t u[16];
-        tmem_ld32(s_at + c0, z);
+      };
+      sum[0] = sum[1] = make_float2(0.0f, 0.0f);
+      float mx;
+      if (taken) {  // no product before all weights are there: the maximum of all
+        tmem_ld32(s_at + 64, z[0]);
+        tmem_ld32(s_at + 96, z[1]);
         tmem_wait_ld();
+        mx = largest(1);
+      } else {
+        mx = -INFINITY;
+      }
+      tmem_ld32(s_at, z[0]);
+      tmem_ld32(s_at + 32, z[1]);
+      tmem_wait_ld();
+      mx = fmaxf(mx, largest(0));
+      if (j == 0) m = mx;
+      else if (__any_sync(0xffffffffu, mx - m >= TC_LAZY)) move(mx, TC_LAZY);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (c == 2) {
+          tmem_wait_ld();
+          mx = largest(1);
+          if (!taken && __any_sync(0xffffffffu, mx - m >= PR_LATE)) {
+            wait(&h_done[g], j);
+            tc_fence_after();
+            move(mx, PR_LATE);
+          }
+        }
+        float *const x = z[c & 1];
+        const float base = m == -INFINITY ? 0.0f : m;
+        uint32_t u[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          float2 y = fma2(make_float2(z[2 * i], z[2 * i + 1]), make_float2(zf, zf),
+          float2 y = fma2(make_float2(x[2 * i], x[2 * i + 1]), make_float2(zf, zf),
                           make_float2(-base, -base));
           y.x = ex2(y.x);
           y.y = ex2(y.y);
           if (!whole) {
-            if (c0 + 2 * i > to) y.x = 0.0f;
-            if (c0 + 2 * i + 1 > to) y.y = 0.0f;
+            if (32 * c + 2 * i > to) y.x = 0.0f;
+            if (32 * c + 2 * i + 1 > to) y.y = 0.0f;
           }
           sum[i & 1] = add2(sum[i & 1], y);
           u[i] = pack2<false>(y.x, y.y);
         }
-        tmem_st16(s_at + c0 / 2, u);
+        tmem_st16(s_at + 16 * c, u);  // over scores that have been read
+        if (c < 2) tmem_ld32(s_at + 64 + 32 * c, x);
+        if (c == 1) {  // the first half of the keys: their products begin
+          tmem_wait_st();
+          tc_fence_before();
+          if (!taken) mbar_arrive(&p_half[g]);
+        }
       }
       sum[0] = add2(sum[0], sum[1]);
       l += sum[0].x + sum[0].y;
       tmem_wait_st();
-      int keep = 0;
-      if (partial(0, j) || partial(1, j)) {
-        wait(&v_ready[j % PR_VB], j / PR_VB);
-        const volatile uint32_t *from = bad[j % PR_VB];
-        const uint32_t words[4] = {from[0], from[1], from[2], from[3]};
-        if (words[0] | words[1] | words[2] | words[3]) {
-          // values that were taken out: added where they are seen (a weight of zero is taken
-          // as the smallest number)
-          keep = 1;
+      if (taken) {
+        // values that were taken out: added where they are seen (a weight of zero is taken as
+        // the smallest number)
 #pragma unroll 1
-          for (int d = 0; d < p.V; d += 16) {
-            float o[16];
-            uint32_t u[16];
-            tmem_ld16(o_at + d, o);
+        for (int d = 0; d < p.V; d += 16) {
+          float o[16];
+          uint32_t u[16];
+          tmem_ld16(o_at + d, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = j == 0 ? 0.0f : o[e];
+#pragma unroll 1
+          for (int t = 0; t < 128; ++t) {
+            if (!(words[t >> 5] >> (t & 31) & 1) || j * 128 + t >= b.len) continue;
+            const uint32_t two = tmem_ld1(s_at + t / 2);
             tmem_wait_ld();
+            float w = bf16_to_f32(static_cast<uint16_t>(t & 1 ? two >> 16 : two & 0xffffu));
+            if (t > to) continue;
+            if (w == 0.0f) w = FLT_MIN;
+            const uint16_t *v = values + (b.k0 + j * 128 + t) * v_stride + h * v_head + d;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = j == 0 ? 0.0f : o[e];
-#pragma unroll 1
-            for (int t = 0; t < 128; ++t) {
-              if (!(words[t >> 5] >> (t & 31) & 1) || j * 128 + t >= b.len) continue;
-              const uint32_t two = tmem_ld1(s_at + t / 2);
-              tmem_wait_ld();
-              float w = bf16_to_f32(static_cast<uint16_t>(t & 1 ? two >> 16 : two & 0xffffu));
-              if (t > to) continue;
-              if (w == 0.0f) w = FLT_MIN;
-              const uint16_t *v = values + (b.k0 + j * 128 + t) * v_stride + h * v_head + d;
-#pragma unroll
-              for (int e = 0; e < 16; ++e)
-                if ((v[e] & 0x7f80u) == 0x7f80u) o[e] += w * bf16_to_f32(v[e]);
-            }
-#pragma unroll
-            for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(o[e]);
-            tmem_st16(o_at + d, u);
+            for (int e = 0; e < 16; ++e)
+              if ((v[e] & 0x7f80u) == 0x7f80u) o[e] += w * bf16_to_f32(v[e]);
           }
-          tmem_wait_st();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(o[e]);
+          tmem_st16(o_at + d, u);
         }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&p_half[g]);
       }
-      if (r == 0) keep_first[g] = keep;
       tc_fence_before();
       mbar_arrive(&p_full[g]);
     }
@@ -462,8 +527,12 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
     if (warp == 8) {
       for (int g = 0; g < 2; ++g)
         if ((g ? nt1 : nt0) > 0) mbar_wait_drain(&qfull[g], 0, 10000000ull);
-      for (int i = issued - 1; i >= 0 && i >= issued - PR_SLOTS; --i)
-        mbar_wait_drain(&full[i % PR_SLOTS], (i / PR_SLOTS) & 1, 10000000ull);
+      // (a tile of which only some slabs were requested never completes: short waits)
+      const int last = (issued - 1) / STEP;
+      for (int j = last; issued > 0 && j >= 0 && j > last - PR_TB; --j) {
+        mbar_wait_drain(&k_full[j % PR_TB], (j / PR_TB) & 1, 5000000ull);
+        if (issued > j * STEP + KN) mbar_wait_drain(&v_full[j % PR_TB], (j / PR_TB) & 1, 5000000ull);
+      }
     }
     tc_fence_before();
     __syncthreads();
@@ -495,13 +564,23 @@ cudaError_t launch_latent_prompt(const LatentPromptParams &p, const uint16_t *q,
       (p.P > 0 && !host_map(&rm, k_rope, 2, 3, rd, rs, box, true)) ||
       !host_map(&vm, v, 2, 3, vd, vs, box, true))
     return cudaErrorInvalidValue;
-  const cudaError_t e = cudaFuncSetAttribute(
-      latent_prompt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(PR_SMEM));
+  void (*kernel)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, LatentPromptParams,
+                 const uint16_t *, long long, long long) = nullptr;
+  switch (D / 64 * 2 + p.V / 64 - 1) {
+    case 2: kernel = latent_prompt_kernel<1, 1>; break;
+    case 3: kernel = latent_prompt_kernel<1, 2>; break;
+    case 4: kernel = latent_prompt_kernel<2, 1>; break;
+    case 5: kernel = latent_prompt_kernel<2, 2>; break;
+    case 6: kernel = latent_prompt_kernel<3, 1>; break;
+    default: kernel = latent_prompt_kernel<3, 2>; break;
+  }
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(PR_SMEM));
   if (e != cudaSuccess) return e;
   // as many blocks of rows as there can be: a part of one a sequence
   const long long blocks = p.T / PR_ROWS + p.S;
-  return launch_pdl(latent_prompt_kernel, dim3(static_cast<unsigned>(blocks * p.H)),
-                    dim3(PR_THREADS), PR_SMEM, s, qm, km, rm, vm, p, v, v_stride, v_head);
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks * p.H)), dim3(PR_THREADS), PR_SMEM, s,
+                    qm, km, rm, vm, p, v, v_stride, v_head);
 }
 
 }  // namespace ssd
