@@ -8,11 +8,12 @@ namespace {
 
 constexpr int LA_THREADS = 128;
 
-// Elements 8i.. of a rotated part of `rot` elements, from its row x; cs: the row's angles.
+// Elements 8i.. of a rotated part of `rot` elements; x: those, o: those half of the part away (half
+// pairs); cs: the row's angles.
 template <bool INTER>
-__device__ __forceinline__ void turn8(const uint16_t *x, int i, int rot, const float2 *cs,
+__device__ __forceinline__ void turn8(uint4 x, uint4 o, int i, int rot, const float2 *cs,
                                       float (&y)[8]) {
-  unpack8(*reinterpret_cast<const uint4 *>(x + 8 * i), y);
+  unpack8(x, y);
   if (8 * i >= rot) return;
   if (INTER) {
 #pragma unroll
@@ -25,14 +26,17 @@ __device__ __forceinline__ void turn8(const uint16_t *x, int i, int rot, const f
   } else {
     const int half = rot / 2, d = 8 * i;
     const bool low = d < half;
-    float o[8];
-    unpack8(*reinterpret_cast<const uint4 *>(x + (low ? d + half : d - half)), o);
+    float z[8];
+    unpack8(o, z);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float2 w = cs[low ? d + e : d - half + e];
-      y[e] = low ? y[e] * w.x - o[e] * w.y : y[e] * w.x + o[e] * w.y;
+      y[e] = low ? y[e] * w.x - z[e] * w.y : y[e] * w.x + z[e] * w.y;
     }
   }
+}
+__device__ __forceinline__ uint4 chunk(const uint16_t *x, int i) {
+  return *reinterpret_cast<const uint4 *>(x + 8 * i);
 }
 
 // Eight elements of a token's row of the cache at element `at`.
@@ -59,9 +63,11 @@ __device__ __forceinline__ void put_cache8(const LatentAppendParams &p, long lon
 // units of a thread: a chunk (interleaved pairs, elements that stay) or two chunks half the
 // rotary part apart, so that every thread owns what it overwrites and q_out may be q_rope.
 // Read once and written once: the copy rate bounds it, the launch's latency when rows are few;
-// then a row's heads are cut over gridDim.y, whose first CTA has the latent row.
+// then a row's heads are cut over gridDim.y, whose first CTA has the latent row. A thread requests
+// AHEAD units at a time, the first before the CTA meets.
 template <bool E4M3, bool INTER>
 __global__ void __launch_bounds__(LA_THREADS) latent_append_kernel(const LatentAppendParams p) {
+  constexpr int AHEAD = INTER ? 4 : 2;
   __shared__ float2 cs[LATENT_MAX_W / 2];
   __shared__ float sums[LA_THREADS / 32];
   griddep_wait();
@@ -69,16 +75,52 @@ __global__ void __launch_bounds__(LA_THREADS) latent_append_kernel(const LatentA
   const int t = blockIdx.x, tid = threadIdx.x, half = p.rot / 2;
   const bool row = blockIdx.y == 0, heads = p.H > 0 && (gridDim.y == 1 || blockIdx.y > 0);
   const int rc = p.R / 8, wc = (p.R + p.P) / 8;
-  float y[8] = {}, sum = 0.0f;
-  if (row && tid < rc) {
-    unpack8(*reinterpret_cast<const uint4 *>(p.c + t * p.c_stride + 8 * tid), y);
+  const int turning = INTER ? p.rot / 8 : p.rot / 16, per = turning + (p.P - p.rot) / 8;
+  const int first = gridDim.y == 1 ? 0 : blockIdx.y - 1, every = gridDim.y == 1 ? 1 : gridDim.y - 1;
+  const int units = heads ? p.H * per : 0, stride = every * LA_THREADS;
+  // unit u: head, chunk, whether its partner half the rotary part on belongs to it
+  auto place = [&](int u, int &h, int &c, bool &pair) {
+    h = u / per;
+    const int i = u - h * per;
+    c = INTER || i < turning ? i : p.rot / 8 + i - turning;
+    pair = !INTER && i < turning;
+  };
+  uint4 a[AHEAD], b[INTER ? 1 : AHEAD];
+  auto load = [&](int u0) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sum += y[e] * y[e];
+    for (int e = 0; e < AHEAD; ++e) {
+      const int u = u0 + e * stride;
+      if (u >= units) break;
+      int h, c;
+      bool pair;
+      place(u, h, c, pair);
+      const uint16_t *x = p.q_rope + t * p.q_stride + h * p.q_head;
+      a[e] = chunk(x, c);
+      if (!INTER && pair) b[INTER ? 0 : e] = chunk(x, c + turning);
+    }
+  };
+  // this row's part of the cache
+  uint4 mine = make_uint4(0, 0, 0, 0), partner = mine;
+  if (row && tid < rc) {
+    mine = chunk(p.c + t * p.c_stride, tid);
+  } else if (row && tid < wc) {
+    const uint16_t *x = p.k_rope + t * p.k_stride;
+    const int i = tid - rc;
+    mine = chunk(x, i);
+    if (!INTER && 8 * i < p.rot) partner = chunk(x, 8 * i < half ? i + turning : i - turning);
   }
+  int u0 = heads ? first * LA_THREADS + tid : units;
+  load(u0);
   // the threads after the latent row's have the angles
   const int pos = p.positions[t];
   for (int j = tid >= 64 ? tid - 64 : tid + 64; j < half; j += LA_THREADS)
     cs[j] = rope_angle(pos, p.inv_freq[j], p.magnitude);
+  float y[8], sum = 0.0f;
+  unpack8(mine, y);
+  if (tid < rc) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum += y[e] * y[e];
+  }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
   if ((tid & 31) == 0) sums[tid >> 5] = sum;
@@ -87,14 +129,14 @@ __global__ void __launch_bounds__(LA_THREADS) latent_append_kernel(const LatentA
     if (tid < rc) {
       if (p.weight) {
         float w[8];
-        unpack8(*reinterpret_cast<const uint4 *>(p.weight + 8 * tid), w);
+        unpack8(chunk(p.weight, tid), w);
         const float mean = ((sums[0] + sums[1]) + (sums[2] + sums[3])) / p.R;
         const float inv = rsqrtf(mean + p.eps);
 #pragma unroll
         for (int e = 0; e < 8; ++e) y[e] = y[e] * inv * w[e];
       }
     } else {
-      turn8<INTER>(p.k_rope + t * p.k_stride, tid - rc, p.rot, cs, y);
+      turn8<INTER>(mine, partner, tid - rc, p.rot, cs, y);
     }
     if (p.rows) *reinterpret_cast<uint4 *>(p.rows + t * p.rows_stride + 8 * tid) = pack8(y);
     const int slot = p.slots[t];
@@ -105,20 +147,25 @@ __global__ void __launch_bounds__(LA_THREADS) latent_append_kernel(const LatentA
                               8 * tid, y);
     }
   }
-  if (!heads) return;
-  const int turning = INTER ? p.rot / 8 : p.rot / 16, per = turning + (p.P - p.rot) / 8;
-  const int first = gridDim.y == 1 ? 0 : blockIdx.y - 1, every = gridDim.y == 1 ? 1 : gridDim.y - 1;
-  for (int u = first * LA_THREADS + tid; u < p.H * per; u += every * LA_THREADS) {
-    const int h = u / per, i = u - h * per;
-    const uint16_t *x = p.q_rope + t * p.q_stride + h * p.q_head;
-    uint16_t *o = p.q_out + t * p.out_stride + h * p.out_head;
-    const int c0 = INTER || i < turning ? i : p.rot / 8 + i - turning;  // first chunk
-    float a[8], b[8];
-    turn8<INTER>(x, c0, p.rot, cs, a);
-    if (!INTER && i < turning) turn8<INTER>(x, c0 + turning, p.rot, cs, b);
-    *reinterpret_cast<uint4 *>(o + 8 * c0) = pack8(a);
-    if (!INTER && i < turning)
-      *reinterpret_cast<uint4 *>(o + 8 * (c0 + turning)) = pack8(b);
+  while (u0 < units) {
+#pragma unroll
+    for (int e = 0; e < AHEAD; ++e) {
+      const int u = u0 + e * stride;
+      if (u >= units) break;
+      int h, c;
+      bool pair;
+      place(u, h, c, pair);
+      uint16_t *o = p.q_out + t * p.out_stride + h * p.out_head;
+      const uint4 other = INTER ? a[e] : b[INTER ? 0 : e];
+      turn8<INTER>(a[e], other, c, p.rot, cs, y);
+      *reinterpret_cast<uint4 *>(o + 8 * c) = pack8(y);
+      if (pair) {
+        turn8<INTER>(other, a[e], c + turning, p.rot, cs, y);
+        *reinterpret_cast<uint4 *>(o + 8 * (c + turning)) = pack8(y);
+      }
+    }
+    u0 += AHEAD * stride;
+    load(u0);
   }
 }
 

@@ -25,7 +25,7 @@ template <int BM, int BN>
 struct LpCfg {
   static constexpr int STAGE = (BM + BN) * 128;
   static constexpr int OUT = BM * BN * 2;
-  static constexpr int MAX_ST = BM == 64 ? 8 : 3;
+  static constexpr int MAX_ST = BN == 64 ? 8 : 3;
   static constexpr int COLS = 2 * BN;
   static constexpr int ROWS = BM / 4;  // rows of a warp
 };
@@ -194,7 +194,7 @@ cudaError_t launch_shape(LatentProjectParams p, const uint16_t *x, long long x_s
   p.nb = (p.N + BN - 1) / BN;
   p.tb = (p.T + BM - 1) / BM;
   p.items = static_cast<long long>(p.H) * p.tb * p.nb;
-  p.stages = p.kb < C::MAX_ST && BM == 64 ? p.kb : C::MAX_ST;
+  p.stages = p.kb < C::MAX_ST && BN == 64 ? p.kb : C::MAX_ST;
   CUtensorMap xm, wm, ym;
   const long long xd[3] = {p.K, p.H, p.T}, xs[2] = {x_head, x_stride};
   const long long wd[3] = {p.K, p.N, p.H}, wst[2] = {p.K, static_cast<long long>(p.N) * p.K};
@@ -233,8 +233,10 @@ cudaError_t launch_latent_project(const uint16_t *x, long long x_stride, long lo
   // strides of dimensions of one are never used, but have to be valid
   if (H == 1) x_head = K, y_head = N;
   if (T == 1) x_stride = x_head * H, y_stride = y_head * H;
-  return (T <= 64 ? launch_shape<64, 64> : launch_shape<128, 256>)(
-      p, x, x_stride, x_head, w, y, y_stride, y_head, num_sms, s);
+  const long long wide = static_cast<long long>(H) * ((T + 127) / 128) * ((N + 255) / 256);
+  auto launch = T <= 64 ? launch_shape<64, 64>
+                        : (wide < num_sms ? launch_shape<128, 64> : launch_shape<128, 256>);
+  return launch(p, x, x_stride, x_head, w, y, y_stride, y_head, num_sms, s);
 }
 
 }  // namespace ssd

@@ -579,6 +579,24 @@ def test_prompt_growing_scores(env):
         p.check()
 
 
+def test_prompt_scores_that_jump(env):
+    """Scores that grow by far more than what moves the maximum at once, within a tile's halves and from
+    tile to tile, for some rows only."""
+    torch, ssd, dev = env
+    p = _Prompt(env, [700], [700], 2)
+    for j, size in ((3, 1.0), (70, 8.0), (100, 20.0), (127, 30.0), (200, 45.0), (330, 60.0), (331, 61.0),
+                    (500, 90.0), (640, 130.0)):
+        p.k[j] = 0
+        p.k[j, :, 5] = size
+    p.q[:, :, 5] = 4.0
+    p.q[::3, :, 5] = -4.0
+    for scale in (0.09, 1.0, -1.0):
+        p.scale = scale
+        p.run()
+        assert ssd.dec_sync_status() == ssd.DEC_OK
+        p.check()
+
+
 def test_prompt_not_finite_where_not_seen(env):
     """NaN in keys and values of later tokens and of other sequences does not reach a row; a value
     that is seen makes its element what the sum makes it."""
