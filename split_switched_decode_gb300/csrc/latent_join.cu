@@ -2,16 +2,18 @@
 // out = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i over a row's parts, in their order.
 //
 // Reads what the parts hold (fp32, in L2 since just before) and writes the row: latencies bound
-// it. A warp has 128 elements of a row; of up to four parts everything is requested at once.
-// While rows are few, 16 warps share a row's parts. Sums are those of a sixteenth of the parts
-// each, added in order, either way: the bits of a row depend on its parts alone.
+// it. A warp has 128 elements of a row, in few registers, so that 40 warps an SM wait at once:
+// where the parts are, then maxima, sums and the first parts' elements together, then the others.
+// While rows are few, 16 warps share the parts of 128 elements of a row. Sums are those of a
+// sixteenth of the parts each, added in order, either way: the bits of a row depend on its
+// parts alone.
 #include "attn_kernel.cuh"
 #include "latent.h"
 
 namespace ssd {
 namespace {
 
-constexpr int LJ_SHARES = 16, LJ_FEW = 4;
+constexpr int LJ_SHARES = 16;
 
 __device__ __forceinline__ float4 scaled(float f, float4 u) {
   return make_float4(__fmul_rn(f, u.x), __fmul_rn(f, u.y), __fmul_rn(f, u.z), __fmul_rn(f, u.w));
@@ -25,137 +27,201 @@ __device__ __forceinline__ float4 plus(float4 u, float4 v) {
                      __fadd_rn(u.w, v.w));
 }
 
-template <int MQ, bool WIDE>
-__global__ void __launch_bounds__(WIDE ? 512 : 256, WIDE ? 1 : 4) latent_join_kernel(
-    const __grid_constant__ AttnParams p, const int2 *rows, const float2 *ml_at,
-    const float *partials, const int workers) {
-  constexpr int DP = LATENT_MAX_R, SLOT = MQ * DP, AHEAD = WIDE ? 8 : 4;
-  constexpr int PER_CTA = WIDE ? 1 : 8;
-  __shared__ float4 sums[WIDE ? LJ_SHARES : 1][32];
-  griddep_wait();
-  griddep_launch_dependents();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, H = p.Hq;
-  const int cuts = (p.D + 127) >> 7;  // 128-element parts of a row
-  const long long units = static_cast<long long>(p.T) * H * cuts;
-  const float v_scale = p.c.v_scale ? p.c.v_scale[0] : 1.0f;
-  for (long long base = static_cast<long long>(blockIdx.x) * PER_CTA; base < units;
-       base += static_cast<long long>(gridDim.x) * PER_CTA) {
-    const long long unit = WIDE ? base : base + warp;
-    int row = 0, d = 0, c0 = 0, n = 0, r = 0;
-    if (unit < units) {
-      row = static_cast<int>(unit / cuts);
-      d = static_cast<int>(unit - static_cast<long long>(row) * cuts) * 128 + 4 * lane;
-      const int2 x = __ldcg(rows + row);  // kept in bounds, whatever stands there
-      r = (x.x >> 16) & (MQ - 1);
-      c0 = min(x.x & 0xffff, workers - 1);
-      n = max(min(x.y, workers - c0), 0);
+// The parts of a row.
+template <int MQ>
+struct RowParts {
+  const float2 *ml_at;
+  const float *partials;
+  int workers, c0, n, r;
+  __device__ __forceinline__ RowParts(const int2 *rows, int row, const float2 *ml,
+                                      const float *parts, int most)
+      : ml_at(ml), partials(parts), workers(most) {
+    const int2 x = __ldcg(rows + row);  // kept in bounds, whatever stands there
+    r = (x.x >> 16) & (MQ - 1);
+    c0 = min(x.x & 0xffff, workers - 1);
+    n = max(min(x.y, workers - c0), 0);
+  }
+  __device__ __forceinline__ float4 out(int i, int d) const {
+    return __ldcg(reinterpret_cast<const float4 *>(
+        partials + (static_cast<size_t>(part_slot(c0, i)) * MQ + r) * LATENT_MAX_R + d));
+  }
+  __device__ __forceinline__ float2 ml(int i) const {
+    return __ldcg(ml_at + (2 * r + (i == 0 ? 1 : 0)) * workers + c0 + i);
+  }
+};
+
+__device__ __forceinline__ void put_row(const AttnParams &p, int row, int d, float4 v, float m,
+                                        float l) {
+  const int t = row / p.Hq, h = row - t * p.Hq;
+  const float inv = l == 0.0f ? 0.0f : (p.c.v_scale ? p.c.v_scale[0] : 1.0f) / l;
+  uint2 u = make_uint2(0u, 0u);  // a row that saw nothing
+  if (l != 0.0f) {
+    u.x = pack2<false>(v.x * inv, v.y * inv);
+    u.y = pack2<false>(v.z * inv, v.w * inv);
+  }
+  if (d < p.D)
+    *reinterpret_cast<uint2 *>(p.out + t * p.out_stride + static_cast<long long>(h) * p.D + d) = u;
+  if (d == 0 && p.lse) p.lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * LN2;
+}
+
+// Rows of up to 16 parts: a part a share.
+template <int MQ>
+__device__ __forceinline__ void join_row(const AttnParams &p, const RowParts<MQ> &x, int row, int d,
+                                         int lane) {
+  constexpr int AHEAD = 4;
+  const bool in = d < p.D;
+  float4 u[AHEAD], v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+  for (int e = 0; e < AHEAD; ++e)
+    if (e < x.n && in) u[e] = x.out(e, d);
+  const float2 one = lane < x.n ? x.ml(lane) : make_float2(-INFINITY, 0.0f);
+  float m = one.x;
+#pragma unroll
+  for (int e = 16; e > 0; e >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, e));
+  const float f = ex2(one.x - (m == -INFINITY ? 0.0f : m));
+  float l = __fmul_rn(f, one.y);
+#pragma unroll
+  for (int e = 16; e > 0; e >>= 1) l = __fadd_rn(l, __shfl_xor_sync(0xffffffffu, l, e));
+  for (int i0 = 0;;) {
+#pragma unroll
+    for (int e = 0; e < AHEAD; ++e) {
+      const float g = __shfl_sync(0xffffffffu, f, (i0 + e) & 31);
+      if (i0 + e < x.n && in) v = plus(v, scaled(g, u[e]));
     }
-    if (n < 2 && !WIDE) continue;
-    auto part = [&](int i) {
-      return reinterpret_cast<const float4 *>(
-          partials + static_cast<size_t>(part_slot(c0, i)) * SLOT + r * DP + d);
-    };
-    auto ml_of = [&](int i) {
-      return __ldcg(ml_at + (2 * r + (i == 0 ? 1 : 0)) * workers + c0 + i);
-    };
-    const bool in = d < p.D;
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float m = -INFINITY, l = 0.0f;
-    if (n <= LJ_FEW) {
-      float2 ml[LJ_FEW];
-      float4 u[LJ_FEW];
+    i0 += AHEAD;
+    if (i0 >= x.n) break;
 #pragma unroll
-      for (int i = 0; i < LJ_FEW; ++i) {
-        ml[i] = make_float2(-INFINITY, 0.0f);
-        if (i < n) {
-          ml[i] = ml_of(i);
-          if (in) u[i] = __ldcg(part(i));
-        }
-        m = fmaxf(m, ml[i].x);
-      }
-      const float b = m == -INFINITY ? 0.0f : m;
-      float x[LJ_FEW];
+    for (int e = 0; e < AHEAD; ++e)
+      if (i0 + e < x.n && in) u[e] = x.out(i0 + e, d);
+  }
+  put_row(p, row, d, v, m, l);
+}
+// Rows of more parts.
+template <int MQ>
+__device__ __forceinline__ void join_long_row(const AttnParams &p, const RowParts<MQ> &x, int row,
+                                           int d, int lane) {
+  constexpr int AHEAD = 4;
+  const bool in = d < p.D;
+  float m = -INFINITY;
+  for (int i = lane; i < x.n; i += 32) m = fmaxf(m, x.ml(i).x);
 #pragma unroll
-      for (int i = 0; i < LJ_FEW; ++i) {
-        const float f = ex2(ml[i].x - b);
-        x[i] = __fmul_rn(f, ml[i].y);
-        if (i < n && in) v = plus(v, scaled(f, u[i]));
-      }
-      l = __fadd_rn(__fadd_rn(x[0], x[2]), __fadd_rn(x[1], x[3]));
-    } else {
-      for (int i = lane; i < n; i += 32) m = fmaxf(m, ml_of(i).x);
-#pragma unroll
-      for (int e = 16; e > 0; e >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, e));
-      const float b = m == -INFINITY ? 0.0f : m;
-      const int per = (n + LJ_SHARES - 1) / LJ_SHARES;
-      const int lo = WIDE ? min(warp * per, n) : 0, hi = WIDE ? min(lo + per, n) : n;
-      int stop = lo + per;  // the end of a share
-      float4 w = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      for (int i0 = 0; i0 < n; i0 += 32) {
-        float f = 0.0f;
-        if (i0 + lane < n) {
-          const float2 ml = ml_of(i0 + lane);
-          f = ex2(ml.x - b);
-          l = __fmaf_rn(f, ml.y, l);
-        }
-        const int from = max(lo, i0), to = min(hi, i0 + 32);
-        for (int i = from; i < to; i += AHEAD) {
-          float4 u[AHEAD];
-#pragma unroll
-          for (int e = 0; e < AHEAD; ++e)
-            if (i + e < to && in)
-              u[e] = __ldcg(part(i + e));
-#pragma unroll
-          for (int e = 0; e < AHEAD; ++e) {
-            const float g = __shfl_sync(0xffffffffu, f, (i + e - i0) & 31);
-            if (i + e < to && i + e == stop) {
-              stop += per;
-              v = plus(v, w);
-              w = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            }
-            if (i + e < to && in) w = fused(g, u[e], w);
-          }
-        }
-      }
-#pragma unroll
-      for (int e = 16; e > 0; e >>= 1) l = __fadd_rn(l, __shfl_xor_sync(0xffffffffu, l, e));
-      v = plus(v, w);
+  for (int e = 16; e > 0; e >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, e));
+  const float base = m == -INFINITY ? 0.0f : m;
+  const int per = (x.n + LJ_SHARES - 1) / LJ_SHARES;
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f), w = v;
+  float l = 0.0f;
+  int stop = per;
+  for (int i0 = 0; i0 < x.n; i0 += 32) {
+    float f = 0.0f;
+    if (i0 + lane < x.n) {
+      const float2 ml = x.ml(i0 + lane);
+      f = ex2(ml.x - base);
+      l = __fmaf_rn(f, ml.y, l);
     }
-    if (WIDE && n > LJ_FEW) {  // (the CTA has one row)
-      sums[warp][lane] = v;
-      __syncthreads();
-      if (warp == 0) {
+    const int to = min(x.n, i0 + 32);
+    for (int i = i0; i < to; i += AHEAD) {
+      float4 u[AHEAD];
 #pragma unroll
-        for (int i = 1; i < LJ_SHARES; ++i)
-          if (i * ((n + LJ_SHARES - 1) / LJ_SHARES) < n) v = plus(v, sums[i][lane]);
+      for (int e = 0; e < AHEAD; ++e)
+        if (i + e < to && in) u[e] = x.out(i + e, d);
+#pragma unroll
+      for (int e = 0; e < AHEAD; ++e) {
+        const float g = __shfl_sync(0xffffffffu, f, (i + e - i0) & 31);
+        if (i + e < to && i + e == stop) {
+          stop += per;
+          v = plus(v, w);
+          w = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+        if (i + e < to && in) w = fused(g, u[e], w);
       }
-      __syncthreads();
-    }
-    if (n > 1 && (!WIDE || warp == 0)) {
-      const int t = row / H, h = row - t * H;
-      const float inv = l == 0.0f ? 0.0f : v_scale / l;
-      uint2 u = make_uint2(0u, 0u);  // a row that saw nothing
-      if (l != 0.0f) {
-        u.x = pack2<false>(v.x * inv, v.y * inv);
-        u.y = pack2<false>(v.z * inv, v.w * inv);
-      }
-      if (in)
-        *reinterpret_cast<uint2 *>(p.out + t * p.out_stride + static_cast<long long>(h) * p.D +
-                                   d) = u;
-      if (d == 0 && p.lse) p.lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * LN2;
     }
   }
+#pragma unroll
+  for (int e = 16; e > 0; e >>= 1) l = __fadd_rn(l, __shfl_xor_sync(0xffffffffu, l, e));
+  put_row(p, row, d, plus(v, w), m, l);
+}
+
+template <int MQ>
+__global__ void __launch_bounds__(256, 4)
+    latent_join_kernel(const __grid_constant__ AttnParams p, const int2 *rows, const float2 *ml,
+                       const float *partials, int workers) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, cuts = (p.D + 127) >> 7, units = p.T * p.Hq * cuts;
+  for (int unit = blockIdx.x * 8 + (threadIdx.x >> 5); unit < units; unit += gridDim.x * 8) {
+    const int row = unit / cuts, d = (unit - row * cuts) * 128 + 4 * lane;
+    const RowParts<MQ> x(rows, row, ml, partials, workers);
+    if (x.n < 2) continue;
+    if (x.n <= LJ_SHARES) join_row<MQ>(p, x, row, d, lane);
+    else join_long_row<MQ>(p, x, row, d, lane);
+  }
+}
+
+// A CTA a row's 128 elements, a thread a part's maximum and sum (there are fewer SMs than threads).
+template <int MQ>
+__global__ void __launch_bounds__(32 * LJ_SHARES)
+    latent_join_few_kernel(const __grid_constant__ AttnParams p, const int2 *rows,
+                           const float2 *ml, const float *partials, int workers) {
+  constexpr int AHEAD = 12;
+  __shared__ float4 sums[LJ_SHARES][32];
+  __shared__ float tops[LJ_SHARES], factor[32 * LJ_SHARES], part_l[32 * LJ_SHARES];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, d = blockIdx.y * 128 + 4 * lane;
+  const bool in = d < p.D;
+  const RowParts<MQ> x(rows, blockIdx.x, ml, partials, workers);
+  if (x.n < 2) return;
+  const int per = (x.n + LJ_SHARES - 1) / LJ_SHARES, lo = min(warp * per, x.n);
+  const int hi = min(lo + per, x.n);
+  float4 u[AHEAD];
+#pragma unroll
+  for (int e = 0; e < AHEAD; ++e)
+    if (lo + e < hi && in) u[e] = x.out(lo + e, d);
+  const float2 one = tid < x.n ? x.ml(tid) : make_float2(-INFINITY, 0.0f);
+  float m = one.x;
+#pragma unroll
+  for (int e = 16; e > 0; e >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, e));
+  if (lane == 0) tops[warp] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < LJ_SHARES; ++i) m = fmaxf(m, tops[i]);
+  const float f = ex2(one.x - (m == -INFINITY ? 0.0f : m));
+  factor[tid] = f;
+  part_l[tid] = one.y;
+  __syncthreads();
+  float4 w = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int i0 = lo;;) {
+#pragma unroll
+    for (int e = 0; e < AHEAD; ++e)
+      if (i0 + e < hi && in) w = fused(factor[i0 + e], u[e], w);
+    i0 += AHEAD;
+    if (i0 >= hi) break;
+#pragma unroll
+    for (int e = 0; e < AHEAD; ++e)
+      if (i0 + e < hi && in) u[e] = x.out(i0 + e, d);
+  }
+  sums[warp][lane] = w;
+  __syncthreads();
+  if (warp > 0) return;
+  float l = 0.0f;
+  for (int i = lane; i < x.n; i += 32) l = __fmaf_rn(factor[i], part_l[i], l);
+#pragma unroll
+  for (int e = 16; e > 0; e >>= 1) l = __fadd_rn(l, __shfl_xor_sync(0xffffffffu, l, e));
+  float4 v = sums[0][lane];
+#pragma unroll
+  for (int i = 1; i < LJ_SHARES; ++i)
+    if (i * per < x.n) v = plus(v, sums[i][lane]);
+  put_row(p, blockIdx.x, d, v, m, l);
 }
 
 template <int MQ>
 cudaError_t launch_join(const AttnParams &p, const LatentLaunch &a, cudaStream_t s) {
-  const long long units = static_cast<long long>(p.T) * p.Hq * ((p.D + 127) / 128);
-  // few rows: a CTA of 16 warps each, two an SM
-  const bool wide = units <= 2ll * a.num_sms;
-  const long long ctas = wide ? units : (units + 7) / 8, most = 4ll * a.num_sms;
-  return launch_pdl(wide ? latent_join_kernel<MQ, true> : latent_join_kernel<MQ, false>,
-                    dim3(static_cast<unsigned>(ctas < most ? ctas : most)),
-                    dim3(wide ? 512 : 256), 0, s, p, static_cast<const int2 *>(a.rows),
+  const int all = p.T * p.Hq, cuts = (p.D + 127) / 128, most = 4 * a.num_sms;
+  const bool few = all * cuts <= 2 * a.num_sms && a.num_sms <= 32 * LJ_SHARES;
+  const int ctas = (all * cuts + 7) / 8;
+  return launch_pdl(few ? latent_join_few_kernel<MQ> : latent_join_kernel<MQ>,
+                    few ? dim3(all, cuts) : dim3(ctas < most ? ctas : most),
+                    dim3(few ? 32 * LJ_SHARES : 256), 0, s, p, static_cast<const int2 *>(a.rows),
                     static_cast<const float2 *>(a.ml), static_cast<const float *>(a.partials),
                     a.num_sms);
 }
