@@ -51,9 +51,10 @@
 namespace ssd {
 namespace {
 
-// Stages ahead of their copy at which boxes are requested into L2: the ring holds two stages, and
-// the one that is on its way (74 KB an SM) is too little for HBM's latency under load.
-constexpr int LD_AHEAD = 2;
+// Stages ahead at which boxes are requested into L2, behind the copy of a stage: the ring holds two
+// stages, and the one that is on its way (74 KB an SM) is too little for HBM's latency under
+// load (64 sequences to 16384 tokens: 137 us without, 125 with one stage, 126 with two, 142 three).
+constexpr int LD_AHEAD = 1;
 // Units that an item is charged (its q and outputs), and the smallest share.
 constexpr int LD_ITEM_COST = 4, LD_LEAST = 1;
 
@@ -371,13 +372,6 @@ __global__ void __launch_bounds__((LdCfg<MQ, E4M3>::THREADS), 1)
           for (int b = 0; b < 8; ++b)
             if (blocks >> b & 1) bits |= 255ull << (8 * b);
           if (left < TOK) bits &= (1ull << max(left, 0)) - 1;
-          // the boxes LD_AHEAD stages on, toward L2
-          const int far = i + LD_AHEAD;
-          if (lane >> 3 == (far & 3)) {
-            const int pg = far < 4 ? page : next_page;
-            if (pg >= 0 && pg < p.c.num_pages) tma_prefetch_4d(&map, 0, far < 4 ? off : next_off, 0, pg);
-          }
-          __syncwarp();
           // a quarter of the stage as soon as the last product that reads it is done
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
@@ -401,6 +395,13 @@ __global__ void __launch_bounds__((LdCfg<MQ, E4M3>::THREADS), 1)
             }
           }
           if (!go) break;
+          // the boxes LD_AHEAD stages on, toward L2
+          const int far = i + LD_AHEAD;
+          if (lane >> 3 == (far & 3)) {
+            const int pg = far < 4 ? page : next_page;
+            if (pg >= 0 && pg < p.c.num_pages) tma_prefetch_4d(&map, 0, far < 4 ? off : next_off, 0, pg);
+          }
+          __syncwarp();
         }
         page = next_page;
         off = next_off;
@@ -536,7 +537,7 @@ __global__ void __launch_bounds__((LdCfg<MQ, E4M3>::THREADS), 1)
           const uint32_t exist = __ballot_sync(0xffffffffu, here >= 0);
           const long long after = place(t + 2);
           if (after >= 0 && (lane & 3) == 0) prefetch_l2_bulk(bytes + after, width);
-          if (k >= ST) wait(&empty[4 * st + 3], k / ST - 1);
+          if (k >= ST) wait(&empty[4 * st + hw / 2], k / ST - 1);  // this warp's quarter
           uint8_t *d = ring + st * C::STAGE + hw * group_bytes + r * 128;
 #pragma unroll
           for (int i = 0; i < LATENT_MAX_W / 64; ++i) {
@@ -576,7 +577,7 @@ __global__ void __launch_bounds__((LdCfg<MQ, E4M3>::THREADS), 1)
               at = pg * p.c.page_stride + (j - i * p.c.page_size) * p.c.token_stride;
           }
           const uint32_t exist = __ballot_sync(0xffffffffu, at >= 0) & 0xffffu;
-          if (k >= ST) wait(&empty[4 * st + 3], k / ST - 1);
+          if (k >= ST) wait(&empty[4 * st + hw], k / ST - 1);  // this warp's quarter
 #pragma unroll 1
           for (int x0 = 0; x0 < 16; x0 += 4) {
             uint4 v[4][3];
