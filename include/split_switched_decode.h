@@ -595,7 +595,7 @@ DEC_API dec_status attn_decode(const dec_bf16 *q, int64_t q_stride, const void *
  * NULL: c is taken as it is. The rotation is rope_append's, over the first `rot` of the P
  * elements; the same rotation of q_rope [T,H,P] goes to q_out. A slot below 0 or not below
  * num_pages * page_size is not written; two rows with the same slot leave a mix of the two
- * there. Sums, norm and rotation are fp32.
+ * there. Sums, norm and rotation are fp32. token_stride is R + P at least.
  *
  * c [T,R], k_rope [T,P], q_rope and q_out [T,H,P], rows_opt [T,R+P] with the given row (and
  * head) strides in elements, multiples of 8, pointers 16-byte aligned: the parts of one

@@ -66,6 +66,7 @@ dec_status latent_append(const dec_bf16 *c, int64_t c_stride, const dec_bf16 *we
   if (st != DEC_OK) return st;
   if (rot < 0 || rot > P || rot % 2 || (rot > 0 && !inv_freq) || (P > 0 && !k_rope))
     return DEC_ERR_INVALID_ARG;
+  if (page_size > 1 && token_stride < R + P) return DEC_ERR_INVALID_ARG;  // tokens that overlap
   if (P == 0) H = 0;
   if (H > 0 && (!q_rope || !q_out)) return DEC_ERR_INVALID_ARG;
   if (weight && !(eps >= 0.0f)) return DEC_ERR_INVALID_ARG;

@@ -429,12 +429,6 @@ __global__ void __launch_bounds__((LdCfg<MQ, E4M3>::THREADS), 1)
       __syncwarp();
       ++seg;
     }
-    if (p.q_start) {  // rows behind the last sequence: no parts
-      const long long first = static_cast<long long>(min(max(p.q_start[p.S], 0), p.T)) * H;
-      const long long all = static_cast<long long>(p.T) * H;
-      for (long long i = first + blockIdx.x * 32 + lane; i < all; i += gridDim.x * 32)
-        pl.rows[i] = make_int2(0, 0);
-    }
   } else if (warp >= 12) {
     // ================================================================ rows of q, stages by hand
     const int hw = warp - 12;

@@ -27,6 +27,13 @@ __device__ __forceinline__ float4 plus(float4 u, float4 v) {
                      __fadd_rn(u.w, v.w));
 }
 
+// Rows of no sequence, before the first and behind the last, have no entry.
+__device__ __forceinline__ int2 rows_in_use(const AttnParams &p) {
+  if (!p.q_start) return make_int2(0, p.S * p.Hq);
+  return make_int2(min(max(p.q_start[0], 0), p.T) * p.Hq,
+                   min(max(p.q_start[p.S], 0), p.T) * p.Hq);
+}
+
 // The parts of a row.
 template <int MQ>
 struct RowParts {
@@ -147,11 +154,12 @@ __global__ void __launch_bounds__(256, 4)
                        const float *partials, int workers) {
   griddep_wait();
   griddep_launch_dependents();
+  const int2 used = rows_in_use(p);
   const int lane = threadIdx.x & 31, cuts = (p.D + 127) >> 7, units = p.T * p.Hq * cuts;
   for (int unit = blockIdx.x * 8 + (threadIdx.x >> 5); unit < units; unit += gridDim.x * 8) {
     const int row = unit / cuts, d = (unit - row * cuts) * 128 + 4 * lane;
     const RowParts<MQ> x(rows, row, ml, partials, workers);
-    if (x.n < 2) continue;
+    if (x.n < 2 || row < used.x || row >= used.y) continue;
     if (x.n <= LJ_SHARES) join_row<MQ>(p, x, row, d, lane);
     else join_long_row<MQ>(p, x, row, d, lane);
   }
@@ -169,8 +177,10 @@ __global__ void __launch_bounds__(32 * LJ_SHARES)
   griddep_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, d = blockIdx.y * 128 + 4 * lane;
   const bool in = d < p.D;
+  const int2 used = rows_in_use(p);
   const RowParts<MQ> x(rows, blockIdx.x, ml, partials, workers);
-  if (x.n < 2) return;
+  if (x.n < 2 || static_cast<int>(blockIdx.x) < used.x || static_cast<int>(blockIdx.x) >= used.y)
+    return;
   const int per = (x.n + LJ_SHARES - 1) / LJ_SHARES, lo = min(warp * per, x.n);
   const int hi = min(lo + per, x.n);
   float4 u[AHEAD];

@@ -449,6 +449,77 @@ def test_decode_strided_rows(env):
     assert bool((out[:, 4096:] == 0).all())
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("H", [8, 64])
+def test_decode_rows_of_no_sequence_and_a_used_workspace(env, H, e4m3):
+    """Rows before the first sequence and behind the last stay, sequences without rows are passed over,
+    and nothing is expected of what the workspace holds."""
+    torch, ssd, dev = env
+    lens = [0] * 45 + [700] + [90] * 4
+    rows = [0] * 45 + [2] + [1, 0, 3, 0]
+    d = _Decode(env, lens, rows, H, e4m3=e4m3)
+    d.ws.fill_(255)
+    d.run()
+    d.check()
+    q, starts = torch.empty_like(d.q[:d.T + 1]), d.q_start + 1
+    q[0], q[1:] = 1.0, d.q[:d.T]
+    out = torch.full((d.T + 1, H, 512), 5.0, device=dev).to(torch.bfloat16)
+    lse = torch.full((d.T + 1, H), 5.0, device=dev)
+    d.ws.random_(0, 256)
+    ssd.latent_decode(q, d.cache, d.table, d.seq_len, out, d.ws, d.scale, q_start=starts, lse=lse,
+                      cache_scale=d.c_scale)
+    assert torch.equal(out[1:], d.out[:d.T]) and torch.equal(lse[1:], d.lse[:d.T])
+    assert bool((out[0] == 5.0).all()) and bool((lse[0] == 5.0).all())
+
+
+def test_decode_two_graphs_share_a_workspace(env):
+    torch, ssd, dev = env
+    a, b = (_Decode(env, lens, [1] * 3, 16) for lens in ([5000, 3, 800], [64, 9000, 200]))
+    ws = a.ws if a.ws.numel() >= b.ws.numel() else b.ws
+    a.ws = b.ws = ws
+    want = []
+    for d in (a, b):
+        d.run()
+        want.append((d.out.clone(), d.lse.clone()))
+    graphs = []
+    for d in (a, b):
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            d.run()
+        graphs.append(g)
+    for _ in range(3):
+        for d, g, (out, lse) in zip((a, b), graphs, want):
+            d.out.fill_(5.0)
+            d.lse.fill_(5.0)
+            g.replay()
+            assert torch.equal(d.out, out) and torch.equal(d.lse, lse)
+
+
+def test_decode_pages_far_apart(env):
+    """Pages whose elements lie past 2^31."""
+    torch, ssd, dev = env
+    store = torch.zeros((5, 1 << 29), dtype=torch.bfloat16, device=dev)
+    cache = store[:, :16 * 576].unflatten(1, (16, 576))
+    g = _gen(torch, dev, 9)
+    cache.copy_(_randn(torch, dev, g, 5, 16, 576))
+    table = _i32(torch, [4, 0, 3], dev).view(1, 3)
+    q = _randn(torch, dev, g, 1, 16, 576)
+    ws = ssd.workspace(ssd.latent_decode_workspace_bytes(1, 1, 16, 512, 64), dev)
+    outs = []
+    for c in (cache, cache.contiguous()):
+        out = torch.empty((1, 16, 512), dtype=torch.bfloat16, device=dev)
+        ssd.latent_decode(q, c, table, _i32(torch, [45], dev), out, ws, 0.06)
+        outs.append(out)
+    assert torch.equal(*outs)
+    # and the write
+    c = _randn(torch, dev, g, 2, 512)
+    r = _randn(torch, dev, g, 2, 64)
+    ssd.latent_append(c, r, _i32(torch, [1, 2], dev), _i32(torch, [4 * 16 + 3, 16], dev), None, cache)
+    assert torch.equal(cache[4, 3], torch.cat([c[0], r[0]])) and torch.equal(cache[1, 0],
+                                                                             torch.cat([c[1], r[1]]))
+
+
 def test_decode_wait_that_runs_out(env):
     """A wait that nothing ends gives a status, and the context goes on."""
     torch, ssd, dev = env
