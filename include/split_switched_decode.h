@@ -679,6 +679,20 @@ DEC_API dec_status latent_prompt(const dec_bf16 *q, int64_t q_stride, const dec_
                                  dec_bf16 *out, int64_t out_stride, float *lse_opt,
                                  dec_stream_t s);
 
+/*
+ * The four calls with their arguments in order in slots of eight bytes (pointers and integers as
+ * int64, numbers as double), for bindings that pay for every argument: a ctypes call of 32
+ * arguments takes 4 us more than one of two. Integers beyond an int's range are refused like
+ * the largest int. The slots are read before the call returns.
+ */
+typedef enum {
+    DEC_LATENT_APPEND = 0,
+    DEC_LATENT_PROJECT = 1,
+    DEC_LATENT_DECODE = 2,
+    DEC_LATENT_PROMPT = 3
+} dec_latent_entry;
+DEC_API dec_status dec_latent_call(int which, const int64_t *slots);
+
 /* ------------------------------------------------------------ read stream ----- */
 
 /*

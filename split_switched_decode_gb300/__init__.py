@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 from . import build as _build
 
@@ -46,7 +47,7 @@ EXPORTS = [
     "dec_debug_attn_timeout",
     "kv_plan", "rope_frequencies", "rope_append", "attn_decode_workspace_bytes", "attn_decode",
     "latent_append", "latent_project", "latent_decode_workspace_bytes", "latent_decode",
-    "latent_prompt",
+    "latent_prompt", "dec_latent_call",
 ]
 
 KV_BF16 = 0
@@ -135,6 +136,7 @@ def _load():
                               P, P, S, P]),
         "latent_prompt": (I, [P, L, P, L, L, P, L, P, L, L, P, P, I, I, I, I, I, I, I, F, P, L,
                               P, P]),
+        "dec_latent_call": (I, [I, ctypes.c_char_p]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -575,33 +577,49 @@ def attn_decode(q, k_cache, v_cache, block_table, seq_len, out, ws, q_start=None
 
 # ---------------------------------------------------------- latent attention ----
 
-def _part(t, name, dims):
+# Arguments go over in slots of eight bytes: ctypes converts each argument of a plain call in 0.1
+# to 0.2 us, and these calls have up to 32.
+_APPEND = struct.Struct("<2qqdqqqqq3qd6q6q7q")
+_PROJECT = struct.Struct("<12q")
+_DECODE = struct.Struct("<18qd7q")
+_PROMPT = struct.Struct("<19qd4q")
+
+
+def _part(t, name, dims, device):
     """(pointer, shape, strides) of a bf16 tensor of `dims` dimensions, the last contiguous, on
-    the current device."""
-    if t.dtype is not _BF16 or not t.is_cuda or t.dim() != dims:
+    `device`."""
+    if t.dtype is not _BF16 or not t.is_cuda:
         raise TypeError(f"{name} must be a bfloat16 CUDA tensor of {dims} dimensions")
-    if t.get_device() != _current_device():
-        raise ValueError(f"{name} is not on the current device")
-    stride = t.stride()
-    if stride[-1] != 1:
+    shape, stride = t.shape, t.stride()
+    if len(shape) != dims:
+        raise TypeError(f"{name} must be a bfloat16 CUDA tensor of {dims} dimensions")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on another device than the first tensor")
+    if stride[-1] != 1 and shape[-1] != 1:
         raise TypeError(f"the last dimension of {name} must be contiguous")
-    return t.data_ptr(), t.shape, stride
+    return t.data_ptr(), shape, stride
 
 
-def _latent_cache(t):
+def _latent_cache(t, device):
     """(type, pages, page size, width, page stride, token stride) of a [pages, page size, R + P]
     cache."""
     kind = t.dtype
     if (kind is not _BF16 and kind is not _F8) or not t.is_cuda or t.dim() != 3:
         raise TypeError("cache must be a bfloat16 or float8_e4m3fn CUDA tensor "
                         "[pages, page size, R + P]")
-    if t.get_device() != _current_device():
-        raise ValueError("cache is not on the current device")
+    if t.get_device() != device:
+        raise ValueError("cache is on another device than the first tensor")
     stride = t.stride()
     if stride[2] != 1:
         raise TypeError("the last dimension of the cache must be contiguous")
     pages, page, width = t.shape
     return (KV_BF16 if kind is _BF16 else KV_E4M3), pages, page, width, stride[0], stride[1]
+
+
+def _launch_stream(device, stream):
+    if device != _current_device():
+        raise ValueError("the tensors are not on the current device")
+    return _current_stream(device) if stream is None else stream.cuda_stream
 
 
 def latent_append(c, k_rope, positions, slots, inv_freq, cache, weight=None, eps=1e-6,
@@ -613,39 +631,41 @@ def latent_append(c, k_rope, positions, slots, inv_freq, cache, weight=None, eps
     (which may be q_rope). The first 2 * len(inv_freq) elements are rotated (inv_freq None:
     none); k_rope None: a cache of R elements."""
     lib = _attention_lib()
-    kind, pages, page, width, page_stride, token_stride = _latent_cache(cache)
-    cp, (T, R), cs = _part(c, "c", 2)
+    dev = cache.get_device()
+    kind, pages, page, width, page_stride, token_stride = _latent_cache(cache, dev)
+    cp, (T, R), cs = _part(c, "c", 2, dev)
     P = width - R
-    kp, ks, qp, qs, op, os_, rp, rs, H = None, 0, None, (0, 0), None, (0, 0), None, 0, 0
+    kp = ks = qp = q0 = q1 = op = o0 = o1 = rp = rs = wp = H = rot = fp = 0
     if k_rope is not None:
-        kp, shape, st = _part(k_rope, "k_rope", 2)
-        ks = st[0]
-        if tuple(shape) != (T, P):
+        kp, (Tk, Pk), (ks, _) = _part(k_rope, "k_rope", 2, dev)
+        if Tk != T or Pk != P:
             raise ValueError("latent_append: k_rope must be [T, width of the cache - R]")
     elif P:
         raise ValueError("latent_append: the cache is wider than c, and k_rope is missing")
     if q_rope is not None:
-        qp, shape, qs = _part(q_rope, "q_rope", 3)
-        op, shape2, os_ = _part(q_out, "q_out", 3)
-        H = shape[1]
-        if tuple(shape) != (T, H, P) or tuple(shape2) != (T, H, P):
+        qp, (Tq, H, Pq), (q0, q1, _) = _part(q_rope, "q_rope", 3, dev)
+        op, (To, Ho, Po), (o0, o1, _) = _part(q_out, "q_out", 3, dev)
+        if Tq != T or To != T or Ho != H or Pq != P or Po != P:
             raise ValueError("latent_append: q_rope and q_out must be [T, H, P]")
     if rows is not None:
-        rp, shape, st = _part(rows, "rows", 2)
-        rs = st[0]
-        if tuple(shape) != (T, width):
+        rp, (Tr, Wr), (rs, _) = _part(rows, "rows", 2, dev)
+        if Tr != T or Wr != width:
             raise ValueError("latent_append: rows must be [T, width of the cache]")
-    if positions.numel() != T or slots.numel() != T or \
-            (weight is not None and tuple(weight.shape) != (R,)):
-        raise ValueError("latent_append: sizes do not agree")
-    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    status = lib.latent_append(
-        cp, cs[0], None if weight is None else _part(weight, "weight", 1)[0], eps, kp, ks, qp,
-        qs[0], qs[1], _int32(positions, "positions"), _int32(slots, "slots"),
-        _scales(inv_freq, "inv_freq", rot // 2), magnitude, T, H, R, P, rot,
-        1 if interleaved else 0, op, os_[0], os_[1], rp, rs, cache.data_ptr(), kind,
-        _scales(cache_scale, "cache_scale", 1), pages, page, page_stride, token_stride,
-        _current_stream(_current_device()) if stream is None else stream.cuda_stream)
+    if weight is not None:
+        wp, (Rw,), _ = _part(weight, "weight", 1, dev)
+        if Rw != R:
+            raise ValueError("latent_append: weight must be [R]")
+    if positions.numel() != T or slots.numel() != T:
+        raise ValueError("latent_append: positions and slots must be [T]")
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        fp = _scales(inv_freq, "inv_freq", rot // 2)
+    status = lib.dec_latent_call(0, _APPEND.pack(
+        cp, cs[0], wp, eps, kp, ks, qp, q0, q1, _int32(positions, "positions"),
+        _int32(slots, "slots"), fp, magnitude, T, H, R, P, rot, 1 if interleaved else 0, op, o0, o1,
+        rp, rs, cache.data_ptr(), kind,
+        0 if cache_scale is None else _scales(cache_scale, "cache_scale", 1), pages, page,
+        page_stride, token_stride, _launch_stream(dev, stream)))
     if status:
         raise DecError(status, "latent_append")
 
@@ -654,17 +674,17 @@ def latent_project(x, W, y, stream=None):
     """y[t, h] = W[h] x[t, h] for x [T,H,K], W [H,N,K] (contiguous) and y [T,H,N]; x and y may be
     parts of wider rows or heads, or [H,T,...] tensors transposed."""
     lib = _attention_lib()
-    xp, (T, H, K), xs = _part(x, "x", 3)
-    wp, wshape, _ = _part(W, "W", 3)
-    yp, yshape, ys = _part(y, "y", 3)
-    N = wshape[1]
-    if tuple(wshape) != (H, N, K) or tuple(yshape) != (T, H, N):
+    dev = x.get_device()
+    xp, (T, H, K), xs = _part(x, "x", 3, dev)
+    wp, (Hw, N, Kw), _ = _part(W, "W", 3, dev)
+    yp, (Ty, Hy, Ny), ys = _part(y, "y", 3, dev)
+    if Hw != H or Kw != K or Ty != T or Hy != H or Ny != N:
         raise ValueError("latent_project: sizes do not agree")
     if not W.is_contiguous():
         raise TypeError("W must be contiguous")
-    status = lib.latent_project(
+    status = lib.dec_latent_call(1, _PROJECT.pack(
         xp, xs[0], xs[1], wp, yp, ys[0], ys[1], T, H, K, N,
-        _current_stream(_current_device()) if stream is None else stream.cuda_stream)
+        _launch_stream(dev, stream)))
     if status:
         raise DecError(status, "latent_project")
 
@@ -679,9 +699,10 @@ def latent_decode(q, cache, block_table, seq_len, out, ws, scale, q_start=None, 
     [T,H,R] (and lse [T,H]); rows, lengths, pages and window as attn_decode. `scale` has no
     default: it belongs to the expanded heads, 1/sqrt of their elements."""
     lib = _attention_lib()
-    kind, pages, page, width, page_stride, token_stride = _latent_cache(cache)
-    qp, (T, H, Wq), qs = _part(q, "q", 3)
-    op, (To, Ho, R), os_ = _part(out, "out", 3)
+    dev = cache.get_device()
+    kind, pages, page, width, page_stride, token_stride = _latent_cache(cache, dev)
+    qp, (T, H, Wq), qs = _part(q, "q", 3, dev)
+    op, (To, Ho, R), os_ = _part(out, "out", 3, dev)
     table = _int32(block_table, "block_table")
     if block_table.dim() != 2:
         raise TypeError("block_table must have two dimensions")
@@ -693,12 +714,13 @@ def latent_decode(q, cache, block_table, seq_len, out, ws, scale, q_start=None, 
         raise TypeError("latent_decode: heads must be contiguous within a row")
     if not ws.is_cuda or not ws.is_contiguous():
         raise TypeError("ws must be a contiguous CUDA tensor")
-    status = lib.latent_decode(
-        qp, qs[0], cache.data_ptr(), kind, _scales(cache_scale, "cache_scale", 1), pages, page,
+    status = lib.dec_latent_call(2, _DECODE.pack(
+        qp, qs[0], cache.data_ptr(), kind,
+        0 if cache_scale is None else _scales(cache_scale, "cache_scale", 1), pages, page,
         page_stride, token_stride, table, max_pages, _int32(seq_len, "seq_len"),
-        None if q_start is None else _int32(q_start, "q_start"), S, T, H, R, width - R, scale,
-        window, op, os_[0], _scales(lse, "lse", T * H), ws.data_ptr(), ws.nbytes,
-        _current_stream(_current_device()) if stream is None else stream.cuda_stream)
+        0 if q_start is None else _int32(q_start, "q_start"), S, T, H, R, width - R,
+        scale, window, op, os_[0], 0 if lse is None else _scales(lse, "lse", T * H), ws.data_ptr(),
+        ws.nbytes, _launch_stream(dev, stream)))
     if status:
         raise DecError(status, "latent_decode")
 
@@ -710,30 +732,31 @@ def latent_prompt(q, k_nope, k_rope, v, q_start, out, scale, k_start=None, lse=N
     q_start[s+1]-1 and the keys k_start[s] .. k_start[s+1]-1 (None: the same), the last of
     which are its rows'."""
     lib = _attention_lib()
-    qp, (T, H, D), qs = _part(q, "q", 3)
-    kp, (Tk, Hk, N), ks = _part(k_nope, "k_nope", 3)
-    vp, (Tv, Hv, V), vs = _part(v, "v", 3)
-    op, (To, Ho, Vo), os_ = _part(out, "out", 3)
+    dev = q.get_device()
+    qp, (T, H, D), qs = _part(q, "q", 3, dev)
+    kp, (Tk, Hk, N), ks = _part(k_nope, "k_nope", 3, dev)
+    vp, (Tv, Hv, V), vs = _part(v, "v", 3, dev)
+    op, (To, Ho, Vo), os_ = _part(out, "out", 3, dev)
     P = D - N
-    rp, rs = None, 0
+    rp = rs = 0
     if k_rope is not None:
-        rp, shape, st = _part(k_rope, "k_rope", 2)
-        rs = st[0]
-        if tuple(shape) != (Tk, P):
+        rp, (Tr, Pr), (rs, _) = _part(k_rope, "k_rope", 2, dev)
+        if Tr != Tk or Pr != P:
             raise ValueError("latent_prompt: k_rope must be [Tk, P]")
     elif P:
         raise ValueError("latent_prompt: q is wider than k_nope, and k_rope is missing")
-    if (Tv, Hv, Hk, To, Ho, Vo) != (Tk, H, H, T, H, V):
+    if Tv != Tk or Hv != H or Hk != H or To != T or Ho != H or Vo != V:
         raise ValueError("latent_prompt: sizes do not agree")
     S = q_start.numel() - 1
     if k_start is not None and k_start.numel() != S + 1:
         raise ValueError("latent_prompt: q_start and k_start do not agree")
     if H > 1 and (qs[1] != D or os_[1] != V):
         raise TypeError("latent_prompt: heads of q and out must be contiguous within a row")
-    status = lib.latent_prompt(
+    status = lib.dec_latent_call(3, _PROMPT.pack(
         qp, qs[0], kp, ks[0], ks[1], rp, rs, vp, vs[0], vs[1], _int32(q_start, "q_start"),
-        None if k_start is None else _int32(k_start, "k_start"), S, T, Tk, H, N, P, V, scale, op,
-        os_[0], _scales(lse, "lse", T * H),
-        _current_stream(_current_device()) if stream is None else stream.cuda_stream)
+        0 if k_start is None else _int32(k_start, "k_start"), S, T,
+        Tk, H, N, P, V, scale, op, os_[0],
+        0 if lse is None else _scales(lse, "lse", T * H),
+        _launch_stream(dev, stream)))
     if status:
         raise DecError(status, "latent_prompt")

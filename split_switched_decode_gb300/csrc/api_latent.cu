@@ -1,5 +1,7 @@
 // api_latent.cu -- host side of the latent attention entry points of
 // include/split_switched_decode.h: latent_append, latent_project, latent_decode, latent_prompt.
+#include <cstring>
+
 #include "../../include/split_switched_decode.h"
 #include "common.cuh"
 #include "latent.h"
@@ -252,6 +254,45 @@ dec_status latent_prompt(const dec_bf16 *q, int64_t q_stride, const dec_bf16 *k_
   return status_of(launch_latent_prompt(p, q, q_stride, k_nope, k_stride, k_head, k_rope, r_stride,
                                         v, v_stride, v_head, sms,
                                         reinterpret_cast<cudaStream_t>(s)));
+}
+
+dec_status dec_latent_call(int which, const int64_t *a) {
+  if (!a) return DEC_ERR_INVALID_ARG;
+  auto f = [&](int i) {
+    double d;
+    static_assert(sizeof(d) == sizeof(*a), "a slot");
+    memcpy(&d, a + i, sizeof(d));
+    return static_cast<float>(d);
+  };
+  // beyond an int: the ends, which every check refuses
+  auto n = [&](int i) {
+    return static_cast<int>(a[i] > INT32_MAX ? INT32_MAX : (a[i] < INT32_MIN ? INT32_MIN : a[i]));
+  };
+  auto at = [&](int i) { return reinterpret_cast<void *>(a[i]); };
+  auto stream = [&](int i) { return reinterpret_cast<dec_stream_t>(a[i]); };
+  auto rows = [&](int i) { return static_cast<dec_bf16 *>(at(i)); };
+  auto ints = [&](int i) { return static_cast<const int32_t *>(at(i)); };
+  auto floats = [&](int i) { return static_cast<float *>(at(i)); };
+  switch (which) {
+    case DEC_LATENT_APPEND:
+      return latent_append(rows(0), a[1], rows(2), f(3), rows(4), a[5], rows(6), a[7], a[8], ints(9),
+                           ints(10), floats(11), f(12), n(13), n(14), n(15), n(16), n(17), n(18),
+                           rows(19), a[20], a[21], rows(22), a[23], at(24), n(25), floats(26), n(27),
+                           n(28), a[29], a[30], stream(31));
+    case DEC_LATENT_PROJECT:
+      return latent_project(rows(0), a[1], a[2], rows(3), rows(4), a[5], a[6], n(7), n(8), n(9),
+                            n(10), stream(11));
+    case DEC_LATENT_DECODE:
+      return latent_decode(rows(0), a[1], at(2), n(3), floats(4), n(5), n(6), a[7], a[8], ints(9),
+                           n(10), ints(11), ints(12), n(13), n(14), n(15), n(16), n(17), f(18), n(19),
+                           rows(20), a[21], floats(22), at(23), static_cast<size_t>(a[24]), stream(25));
+    case DEC_LATENT_PROMPT:
+      return latent_prompt(rows(0), a[1], rows(2), a[3], a[4], rows(5), a[6], rows(7), a[8], a[9],
+                           ints(10), ints(11), n(12), n(13), n(14), n(15), n(16), n(17), n(18), f(19),
+                           rows(20), a[21], floats(22), stream(23));
+    default:
+      return DEC_ERR_INVALID_ARG;
+  }
 }
 
 }  // extern "C"

@@ -122,6 +122,46 @@ def test_prompt_refusals(ssd):
     ])
 
 
+def test_calls_in_slots_are_the_calls(ssd):
+    """Arguments in slots reach the same checks: each refusal above that concerns one argument."""
+    import struct
+    lib = ssd.lib()
+    call = lib.dec_latent_call
+    assert call(4, b"\0" * 512) == ssd.DEC_ERR_INVALID_ARG and call(-1, b"\0" * 512) == ssd.DEC_ERR_INVALID_ARG
+    assert call(0, None) == ssd.DEC_ERR_INVALID_ARG
+    good = [0x10000, 576, 0x10000, 1e-6, 0x10000, 576, 0x10000, 512, 64, 0x10000, 0x10000, 0x10000, 1.0, 4, 8,
+            512, 64, 64, 0, 0x20000, 512, 64, 0x10000, 576, 0x10000, 0, 0, 3, 16, 16 * 576, 576, 0]
+    form = "<" + "".join("d" if isinstance(x, float) else "q" for x in good)
+    bad = [(0, 0, 1), (0, 0x10002, 3), (1, 504, 1), (3, -1.0, 1), (5, 56, 1), (8, 56, 1), (11, 0, 1),
+           (13, 0, 1), (13, 1 << 40, 2), (14, 1 << 33, 2), (15, 500, 2), (16, 32, 2), (17, 24, 2), (18, 2, 1),
+           (20, 516, 3), (22, 0x10002, 3), (25, 5, 1), (28, 0, 1), (30, 580, 3)]
+    status = {1: ssd.DEC_ERR_INVALID_ARG, 2: ssd.DEC_ERR_UNSUPPORTED_SHAPE, 3: ssd.DEC_ERR_MISALIGNED}
+    for i, value, want in bad:
+        args = list(good)
+        args[i] = value
+        assert call(0, struct.pack(form, *args)) == status[want], (i, value)
+    good = [0x10000, 1024, 128, 0x10000, 0x20000, 4096, 512, 4, 8, 128, 512, 0]
+    for i, value, want in [(0, 0, 1), (2, 120, 1), (3, 0x10004, 3), (6, 516, 3), (7, 0, 1), (9, 132, 2),
+                           (10, 516, 2), (9, (1 << 32) + 128, 2)]:
+        args = list(good)
+        args[i] = value
+        assert call(1, struct.pack("<12q", *args)) == status[want], (i, value)
+    good = [0x10000, 4608, 0x10000, 0, 0, 3, 16, 9216, 576, 0x10000, 4, 0x10000, 0x10000, 2, 4, 8, 512, 64, 0.1, 0,
+            0x20000, 4096, 0, 0x10000, 0, 0]
+    for i, value, want in [(2, 0, 1), (3, 7, 1), (8, 580, 3), (10, 0, 1), (12, 0, 1), (13, 8193, 2), (16, 520, 2),
+                           (19, -1, 1), (20, 0x10000, 1), (21, 4088, 1), (22, 0x10002, 3), (23, 0, 1)]:
+        args = list(good)
+        args[i] = value
+        assert call(2, struct.pack("<18qd7q", *args)) == status[want], (i, value)
+    good = [0x10000, 1536, 0x10000, 2048, 256, 0x10000, 64, 0x10000, 2048, 256, 0x10000, 0x10000, 2, 300, 400, 8, 128,
+            64, 128, 0.1, 0x20000, 1024, 0, 0]
+    for i, value, want in [(5, 0, 1), (6, 56, 1), (9, 260, 3), (11, 0, 1), (14, 0, 1), (16, 96, 2), (18, 256, 2),
+                           (20, 0x10000, 1), (21, 1016, 1), (22, 0x10002, 3)]:
+        args = list(good)
+        args[i] = value
+        assert call(3, struct.pack("<19qd4q", *args)) == status[want], (i, value)
+
+
 def test_binding_wants_cuda_tensors(ssd):
     torch = pytest.importorskip("torch")
     x = torch.zeros((2, 3, 64), dtype=torch.bfloat16)
