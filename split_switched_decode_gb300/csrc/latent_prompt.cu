@@ -194,16 +194,16 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
   if (warp == 8) {
     // ================================================================ boxes
     bool go = true;
-    if (elect_one()) {
-      for (int g = 0; g < 2; ++g) {
-        if ((g ? nt1 : nt0) == 0) continue;
+    auto queries = [&](int g) {
+      if ((g ? nt1 : nt0) > 0 && elect_one()) {
         mbar_arrive_expect_tx(&qfull[g], KN * PR_SLAB);
         for (int i = 0; i < KN; ++i)
           tma_load_3d(smem_u32(pr_smem + (g * PR_MAX_Q + i) * PR_SLAB), &qmap, &qfull[g], i * 64, h,
                       b.q0 + b.row0 + 128 * g);
       }
-    }
-    __syncwarp();
+      __syncwarp();
+    };
+    queries(0);
     for (int i = 0, j = 0; go && j < nt; ++j) {
       const int tok = b.k0 + j * 128;
 #pragma unroll 1
@@ -225,6 +225,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
           else tma_load_3d(to, &vmap, bar, (x - KN) * 64, h, tok);
         }
         __syncwarp();
+        if (i == KN - 1) queries(1);  // behind the first keys, with which the first rows begin
       }
     }
   } else if (warp == 9) {
@@ -340,7 +341,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + g * 128 + lanes, o_at = tmem + 256 + g * 128 + lanes;
     const int mine = g ? nt1 : nt0, row = b.row0 + 128 * g + r, pos = shift + row;
-    const float zf = p.scale * LOG2E;
+    // (a scale of zero as one that no score shows: keys not seen stay at -infinity)
+    const float zf = p.scale == 0.0f ? 1e-30f : p.scale * LOG2E;
     const bool least = zf < 0.0f;
     float m = -INFINITY, l = 0.0f;
     float z[2][32];
@@ -433,10 +435,6 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                           make_float2(-base, -base));
           y.x = ex2(y.x);
           y.y = ex2(y.y);
-          if (!whole) {
-            if (32 * c + 2 * i > to) y.x = 0.0f;
-            if (32 * c + 2 * i + 1 > to) y.y = 0.0f;
-          }
           sum[i & 1] = add2(sum[i & 1], y);
           u[i] = pack2<false>(y.x, y.y);
         }
