@@ -116,6 +116,18 @@ __device__ __forceinline__ bool find_block(const LatentPromptParams &p, int blk,
   return true;
 }
 
+// Of three numbers in one instruction; NaN as in fmaxf.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float d;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 template <int KN, int VN>  // slabs of a key tile, of a value tile
 __global__ void __launch_bounds__(PR_THREADS, 1)
     latent_prompt_kernel(const __grid_constant__ CUtensorMap qmap,
@@ -305,17 +317,27 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
       // first let them run ahead, and the products never saw v_ready's phase.)
       wait(&v_full[j % PR_TB], j / PR_TB);
       if (partial(0, j) || partial(1, j)) {
-        // 64 tokens a warp, four rows of eight chunks a step
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          uint32_t seen = 0;
+        // 64 tokens a warp, four rows of eight chunks a step. An exponent of all ones is the only
+        // one that carries into the sign's place: nothing but a look where all are finite.
+        uint32_t carry = 0;
 #pragma unroll
+        for (int i = 0; i < VN; ++i) {
+          const uint8_t *from = ring + (j * STEP + KN + i) % PR_SLOTS * PR_SLAB + w * (64 * 128);
+#pragma unroll 8
+          for (int x = 0; x < 16; ++x) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(from + x * 512 + lane * 16);
+            carry |= ((u.x & 0x7f807f80u) + 0x00800080u) | ((u.y & 0x7f807f80u) + 0x00800080u) |
+                     ((u.z & 0x7f807f80u) + 0x00800080u) | ((u.w & 0x7f807f80u) + 0x00800080u);
+          }
+        }
+        uint32_t seen[2] = {0, 0};
+        if (__any_sync(0xffffffffu, carry & 0x80008000u)) {
+#pragma unroll 1
           for (int i = 0; i < VN; ++i) {
-            uint8_t *slab = ring + (j * STEP + KN + i) % PR_SLOTS * PR_SLAB;
-#pragma unroll 4
-            for (int x = 0; x < 8; ++x) {
-              const int tok = w * 64 + half * 32 + x * 4 + (lane >> 3);
-              uint4 *at = reinterpret_cast<uint4 *>(slab + tok * 128 + ((lane & 7) << 4));
+            uint8_t *slab = ring + (j * STEP + KN + i) % PR_SLOTS * PR_SLAB + w * (64 * 128);
+#pragma unroll 1
+            for (int x = 0; x < 16; ++x) {
+              uint4 *at = reinterpret_cast<uint4 *>(slab + x * 512 + lane * 16);
               const uint4 u = *at;
               constexpr uint32_t INF2 = 0x7f807f80u;
               const uint4 no = make_uint4(__vcmpeq2(u.x & INF2, INF2), __vcmpeq2(u.y & INF2, INF2),
@@ -323,14 +345,16 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
               const bool any = (no.x | no.y | no.z | no.w) != 0;
               if (any) *at = make_uint4(u.x & ~no.x, u.y & ~no.y, u.z & ~no.z, u.w & ~no.w);
               const uint32_t vote = __ballot_sync(0xffffffffu, any);
-#pragma unroll
               for (int r = 0; r < 4; ++r)
-                if (vote >> (8 * r) & 255u) seen |= 1u << (x * 4 + r);
+                if (vote >> (8 * r) & 255u) seen[x >> 3] |= 1u << ((x & 7) * 4 + r);
             }
           }
-          if (lane == 0) bad[j % PR_TB][2 * w + half] = seen;
+          fence_proxy_async_smem();
         }
-        fence_proxy_async_smem();
+        if (lane == 0) {
+          bad[j % PR_TB][2 * w] = seen[0];
+          bad[j % PR_TB][2 * w + 1] = seen[1];
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&v_ready[j % PR_TB]);
@@ -370,10 +394,12 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
         float best[4] = {z[0][0], z[0][1], z[0][2], z[0][3]};
         if (least) {
 #pragma unroll
-          for (int i = 4; i < 64; ++i) best[i & 3] = fminf(best[i & 3], z[i >> 5][i & 31]);
+          for (int i = 4; i < 64; i += 2)
+            best[i >> 1 & 3] = min3(best[i >> 1 & 3], z[i >> 5][i & 31], z[i >> 5][(i & 31) + 1]);
         } else {
 #pragma unroll
-          for (int i = 4; i < 64; ++i) best[i & 3] = fmaxf(best[i & 3], z[i >> 5][i & 31]);
+          for (int i = 4; i < 64; i += 2)
+            best[i >> 1 & 3] = max3(best[i >> 1 & 3], z[i >> 5][i & 31], z[i >> 5][(i & 31) + 1]);
         }
         const float mx = least ? fminf(fminf(best[0], best[1]), fminf(best[2], best[3]))
                                : fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3]));
