@@ -2,8 +2,8 @@
 // out = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i over a row's parts, in their order.
 //
 // Reads what the parts hold (fp32, in L2 since just before) and writes the row: latencies bound
-// it. A warp has 128 elements of a row, in few registers, so that 40 warps an SM wait at once:
-// where the parts are, then maxima, sums and the first parts' elements together, then the others.
+// it, then instructions. A warp has a row, so that what is the same for its elements is done once:
+// where the parts are, then maxima, sums and the first two parts together, then two at a time.
 // While rows are few, 16 warps share the parts of 128 elements of a row. Sums are those of a
 // sixteenth of the parts each, added in order, either way: the bits of a row depend on its
 // parts alone.
@@ -73,14 +73,19 @@ __device__ __forceinline__ void put_row(const AttnParams &p, int row, int d, flo
 
 // Rows of up to 16 parts: a part a share.
 template <int MQ>
-__device__ __forceinline__ void join_row(const AttnParams &p, const RowParts<MQ> &x, int row, int d,
+__device__ __forceinline__ void join_row(const AttnParams &p, const RowParts<MQ> &x, int row,
                                          int lane) {
-  constexpr int AHEAD = 4;
-  const bool in = d < p.D;
-  float4 u[AHEAD], v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  constexpr int CUTS = LATENT_MAX_R / 128, AHEAD = 2;
+  const int d = 4 * lane;
+  float4 u[AHEAD][CUTS], v[CUTS];
+  auto load = [&](int i0) {
 #pragma unroll
-  for (int e = 0; e < AHEAD; ++e)
-    if (e < x.n && in) u[e] = x.out(e, d);
+    for (int e = 0; e < AHEAD; ++e)
+#pragma unroll
+      for (int c = 0; c < CUTS; ++c)
+        if (i0 + e < x.n && d + 128 * c < p.D) u[e][c] = x.out(i0 + e, d + 128 * c);
+  };
+  load(0);
   const float2 one = lane < x.n ? x.ml(lane) : make_float2(-INFINITY, 0.0f);
   float m = one.x;
 #pragma unroll
@@ -89,19 +94,34 @@ __device__ __forceinline__ void join_row(const AttnParams &p, const RowParts<MQ>
   float l = __fmul_rn(f, one.y);
 #pragma unroll
   for (int e = 16; e > 0; e >>= 1) l = __fadd_rn(l, __shfl_xor_sync(0xffffffffu, l, e));
+#pragma unroll
+  for (int c = 0; c < CUTS; ++c) v[c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   for (int i0 = 0;;) {
 #pragma unroll
     for (int e = 0; e < AHEAD; ++e) {
       const float g = __shfl_sync(0xffffffffu, f, (i0 + e) & 31);
-      if (i0 + e < x.n && in) v = plus(v, scaled(g, u[e]));
+#pragma unroll
+      for (int c = 0; c < CUTS; ++c)
+        if (i0 + e < x.n && d + 128 * c < p.D) v[c] = plus(v[c], scaled(g, u[e][c]));
     }
     i0 += AHEAD;
     if (i0 >= x.n) break;
-#pragma unroll
-    for (int e = 0; e < AHEAD; ++e)
-      if (i0 + e < x.n && in) u[e] = x.out(i0 + e, d);
+    load(i0);
   }
-  put_row(p, row, d, v, m, l);
+  const int t = row / p.Hq, h = row - t * p.Hq;
+  const float inv = l == 0.0f ? 0.0f : (p.c.v_scale ? p.c.v_scale[0] : 1.0f) / l;
+  uint16_t *out = p.out + t * p.out_stride + static_cast<long long>(h) * p.D;
+#pragma unroll
+  for (int c = 0; c < CUTS; ++c)
+    if (d + 128 * c < p.D) {
+      uint2 y = make_uint2(0u, 0u);  // a row that saw nothing
+      if (l != 0.0f) {
+        y.x = pack2<false>(v[c].x * inv, v[c].y * inv);
+        y.y = pack2<false>(v[c].z * inv, v[c].w * inv);
+      }
+      *reinterpret_cast<uint2 *>(out + d + 128 * c) = y;
+    }
+  if (lane == 0 && p.lse) p.lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * LN2;
 }
 // Rows of more parts.
 template <int MQ>
@@ -149,19 +169,19 @@ __device__ __forceinline__ void join_long_row(const AttnParams &p, const RowPart
 }
 
 template <int MQ>
-__global__ void __launch_bounds__(256, 4)
+__global__ void __launch_bounds__(256, 3)
     latent_join_kernel(const __grid_constant__ AttnParams p, const int2 *rows, const float2 *ml,
                        const float *partials, int workers) {
   griddep_wait();
   griddep_launch_dependents();
   const int2 used = rows_in_use(p);
-  const int lane = threadIdx.x & 31, cuts = (p.D + 127) >> 7, units = p.T * p.Hq * cuts;
-  for (int unit = blockIdx.x * 8 + (threadIdx.x >> 5); unit < units; unit += gridDim.x * 8) {
-    const int row = unit / cuts, d = (unit - row * cuts) * 128 + 4 * lane;
+  const int lane = threadIdx.x & 31, all = p.T * p.Hq;
+  for (int row = blockIdx.x * 8 + (threadIdx.x >> 5); row < all; row += gridDim.x * 8) {
     const RowParts<MQ> x(rows, row, ml, partials, workers);
     if (x.n < 2 || row < used.x || row >= used.y) continue;
-    if (x.n <= LJ_SHARES) join_row<MQ>(p, x, row, d, lane);
-    else join_long_row<MQ>(p, x, row, d, lane);
+    if (x.n <= LJ_SHARES) join_row<MQ>(p, x, row, lane);
+    else
+      for (int d = 0; d < p.D; d += 128) join_long_row<MQ>(p, x, row, d + 4 * lane, lane);
   }
 }
 
@@ -226,9 +246,9 @@ __global__ void __launch_bounds__(32 * LJ_SHARES)
 
 template <int MQ>
 cudaError_t launch_join(const AttnParams &p, const LatentLaunch &a, cudaStream_t s) {
-  const int all = p.T * p.Hq, cuts = (p.D + 127) / 128, most = 4 * a.num_sms;
+  const int all = p.T * p.Hq, cuts = (p.D + 127) / 128, most = 3 * a.num_sms;
   const bool few = all * cuts <= 2 * a.num_sms && a.num_sms <= 32 * LJ_SHARES;
-  const int ctas = (all * cuts + 7) / 8;
+  const int ctas = (all + 7) / 8;
   return launch_pdl(few ? latent_join_few_kernel<MQ> : latent_join_kernel<MQ>,
                     few ? dim3(all, cuts) : dim3(ctas < most ? ctas : most),
                     dim3(few ? 32 * LJ_SHARES : 256), 0, s, p, static_cast<const int2 *>(a.rows),
