@@ -668,8 +668,9 @@ DEC_API dec_status latent_decode(const dec_bf16 *q, int64_t q_stride, const void
  * S 1..8192, T and Tk 1..2^20, H 1..1024. Rows of no sequence are not written; rows that see
  * no key give 0 and -infinity. What is not finite at a key that a row does not see does not
  * reach it; a value that is not finite makes that element of the rows that see it infinite or
- * NaN. Scores, maxima and sums are fp32, the weights round to bf16 for the product with v.
- * Deterministic. No workspace.
+ * NaN. Scores, maxima and sums are fp32, the weights round to bf16 for the product with v; weights
+ * are at most 2^16 on the way (in latent_decode 2^8), so that sums of values beyond 2^110 may pass
+ * fp32's range. Deterministic. No workspace.
  */
 DEC_API dec_status latent_prompt(const dec_bf16 *q, int64_t q_stride, const dec_bf16 *k_nope,
                                  int64_t k_stride, int64_t k_head, const dec_bf16 *k_rope,
@@ -682,8 +683,8 @@ DEC_API dec_status latent_prompt(const dec_bf16 *q, int64_t q_stride, const dec_
 /*
  * The four calls with their arguments in order in slots of eight bytes (pointers and integers as
  * int64, numbers as double), for bindings that pay for every argument: a ctypes call of 32
- * arguments takes 4 us more than one of two. Integers beyond an int's range are refused like
- * the largest int. The slots are read before the call returns.
+ * arguments takes 4 us more than one of two. Integers beyond an int's range count as the end of it
+ * that they passed. The slots are read before the call returns.
  */
 typedef enum {
     DEC_LATENT_APPEND = 0,

@@ -264,7 +264,7 @@ dec_status dec_latent_call(int which, const int64_t *a) {
     memcpy(&d, a + i, sizeof(d));
     return static_cast<float>(d);
   };
-  // beyond an int: the ends, which every check refuses
+  // beyond an int: its ends
   auto n = [&](int i) {
     return static_cast<int>(a[i] > INT32_MAX ? INT32_MAX : (a[i] < INT32_MIN ? INT32_MIN : a[i]));
   };

@@ -812,3 +812,140 @@ def test_layer_prompt_then_tokens(env, e4m3):
 
 def test_layer_many_heads(env):
     _layer(env, [33, 130], 5, H=128)
+
+
+# ------------------------------------------------- batches and calls at the edges ----
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("count", [32, 33, 400])
+def test_decode_many_sequences(env, count, e4m3):
+    lens = [(37 * i) % 150 for i in range(count)]
+    rows = [(i * 5) % 3 for i in range(count)]
+    lens[count // 2], rows[count // 2] = 5000, 2
+    for H, page in ((8, 16), (64, 13)):
+        d = _Decode(env, lens, rows, H, page=page, e4m3=e4m3)
+        d.run()
+        d.check()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_decode_as_many_sequences_as_there_can_be(env, e4m3):
+    torch, ssd, dev = env
+    S, H, R, W, page = 8192, 4, 64, 128, 16
+    g = _gen(torch, dev, 77)
+    cache = _cache_of(torch, dev, g, (S, page, W), e4m3, 0.013)
+    c_scale = torch.full((1,), 0.013, device=dev) if e4m3 else None
+    table = torch.randperm(S, generator=g, device=dev).to(torch.int32).view(S, 1)
+    lens = torch.randint(0, page + 1, (S,), generator=g, device=dev, dtype=torch.int32)
+    q = _randn(torch, dev, g, S, H, W)
+    out = torch.empty((S, H, R), dtype=torch.bfloat16, device=dev)
+    ws = ssd.workspace(ssd.latent_decode_workspace_bytes(S, S, H, R, W - R), dev)
+    ssd.latent_decode(q, cache, table, lens, out, ws, 0.1, cache_scale=c_scale)
+    torch.cuda.synchronize()
+    keys = _values(torch, cache)[table[:, 0].long()] * (c_scale.double() if e4m3 else 1.0)
+    seen = torch.arange(page, device=dev)[None, None] < lens[:, None, None]
+    z = (0.1 * q.double() @ keys.transpose(1, 2)).masked_fill(~seen, float("-inf"))
+    reach = (0.1 * q.double().abs() @ keys.abs().transpose(1, 2)).masked_fill(~seen, 0).amax(-1)
+    w = z.softmax(-1).nan_to_num(0.0)
+    want, size = w @ keys[..., :R], w @ keys[..., :R].abs()
+    score = (W + 16) * 2.0 ** -24 * reach + 2.0 ** -18  # as in _Decode.check
+    _within(out, want, U * want.abs() + (U + 2 * score[..., None]) * size + 1e-30, "out")
+
+
+@pytest.mark.parametrize("page", [1 << 16, (1 << 16) - 3])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_decode_far_tokens_of_a_window(env, e4m3, page):
+    """Token numbers up to the last that an int32 length allows, all pages of a sequence in one place."""
+    torch, ssd, dev = env
+    import latent_ref
+    H, R, W, n, window = 8, 128, 192, 0x7ffffe25, 100
+    g = _gen(torch, dev, 78)
+    cache = _cache_of(torch, dev, g, (1, page, W), e4m3, 0.013)
+    c_scale = torch.full((1,), 0.013, device=dev) if e4m3 else None
+    table = torch.zeros((1, (1 << 31) // page + 1), dtype=torch.int32, device=dev)
+    q = _randn(torch, dev, g, 2, H, W)
+    out = torch.empty((2, H, R), dtype=torch.bfloat16, device=dev)
+    lse = torch.empty((2, H), device=dev)
+    ws = ssd.workspace(ssd.latent_decode_workspace_bytes(1, 2, H, R, W - R), dev)
+    ssd.latent_decode(q, cache, table, _i32(torch, [n], dev), out, ws, 0.06, window=window, lse=lse,
+                      q_start=_i32(torch, [0, 2], dev), cache_scale=c_scale)
+    torch.cuda.synchronize()
+    at = torch.arange(n - window - 1, n, device=dev) % page
+    keys = _values(torch, cache[0])[at] * (c_scale.double() if e4m3 else 1.0)
+    pos = torch.arange(2, device=dev) + window - 1
+    want, want_lse, size, reach = latent_ref.attend(q.double(), keys[None], keys[None, :, :R], pos, 0.06,
+                                                    window)
+    score = (W + 16) * 2.0 ** -24 * reach + 2.0 ** -18  # as in _Decode.check
+    _within(out, want, U * want.abs() + (U + 2 * score[..., None]) * size + 1e-30, "out")
+    _within(lse, want_lse, score + 2.0 ** -22 * want_lse.abs(), "lse")
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.06])
+def test_scales_of_zero_and_below(env, scale):
+    for e4m3 in (False, True):
+        d = _Decode(env, [1, 70, 600, 0], [1, 2, 3, 1], 16, e4m3=e4m3, scale=scale)
+        d.run()
+        d.check()
+    p = _Prompt(env, [300, 20], [300, 220], 3, scale=scale)
+    p.run()
+    p.check()
+
+
+def test_prompt_scale_of_zero_with_large_scores(env):
+    """Equal weights, whatever the scores are (about 1e30 here)."""
+    torch, ssd, dev = env
+    p = _Prompt(env, [200], [200], 2, scale=0.0)
+    p.q.mul_(1e14)
+    p.k.mul_(1e14)
+    p.run()
+    torch.cuda.synchronize()
+    n = torch.arange(1, 201, device=dev).double()[:, None]
+    v = p.v[:200].double()
+    mean, size = v.cumsum(0) / n[..., None], v.abs().cumsum(0) / n[..., None]
+    _within(p.out[:200], mean, U * mean.abs() + (U + 2.0 ** -17) * size, "out")
+    _within(p.lse[:200], n.log().expand(200, 2), 2.0 ** -18 + 2.0 ** -22 * n.log(), "lse")
+
+
+def test_calls_at_once_on_two_streams(env):
+    torch, ssd, dev = env
+    a = _Decode(env, [9000, 40, 3000], [2, 1, 4], 64)
+    b = _Decode(env, [5000, 300], [1, 3], 16, e4m3=True)
+    p = _Prompt(env, [700, 3], [900, 3], 8)
+    each = (a, b, p)
+    for x in each:
+        x.run()
+    torch.cuda.synchronize()
+    want = [(x.out.clone(), x.lse.clone()) for x in each]
+    streams = [torch.cuda.Stream() for _ in each]
+    for _ in range(20):
+        for x in each:
+            x.out.fill_(5.0)
+            x.lse.fill_(5.0)
+        for x, s in zip(each, streams):
+            s.wait_stream(torch.cuda.current_stream())
+            x.run(stream=s)
+        for s in streams:
+            torch.cuda.current_stream().wait_stream(s)
+        for x, (out, lse) in zip(each, want):
+            assert torch.equal(x.out, out) and torch.equal(x.lse, lse)
+    assert ssd.dec_sync_status() == ssd.DEC_OK
+
+
+def test_prompt_replayed_with_other_lengths(env):
+    """One captured graph serves every division of its rows and keys."""
+    torch, ssd, dev = env
+    p = _Prompt(env, [300, 20, 100], [300, 220, 100], 4)
+    p.run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        p.run()
+    for rows, keys in (([300, 20, 100], [300, 220, 100]), ([0, 400, 20], [10, 500, 110]),
+                       ([1, 1, 418], [200, 1, 419]), ([0, 0, 0], [5, 5, 5])):
+        p.rows, p.keys = rows, keys
+        p.q_start.copy_(_i32(torch, _starts(rows), dev))
+        p.k_start.copy_(_i32(torch, _starts(keys), dev))
+        p.out.fill_(5.0)
+        p.lse.fill_(5.0)
+        graph.replay()
+        p.check()
