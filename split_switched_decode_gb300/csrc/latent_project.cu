@@ -4,11 +4,13 @@
 // Few rows: every weight is used once a row, so reading the weights bounds it; many rows: each
 // element of x and y is read or written once (K N / (K + N) operations a byte, 102 for 128 and
 // 512, below what the tensor cores need), so the copy rate bounds that too. Rows are the M of
-// the products at any count: BM = 64 rows x BN = 64 columns a tile while they fill one tile,
+// the products at any count: BM = 64 rows x BN = 64 columns a tile while the rows fill one tile,
 // so that a decode step's products come to several tiles an SM (64 heads of 128 x 512: 512
-// tiles of 16 KB), and 128 x 256 above, which read x and W from L2 0.5 + 1 times for each
-// byte of y. Tiles go around the CTAs that stay; loads of the next tile and the stores of
-// the last overlap the products through a ring of k-blocks of 64 and two accumulators.
+// tiles of 16 KB), 128 x 64 while the widest tiles would leave SMs idle, and 128 x 256 above, which
+// read x and W from L2 0.5 + 1 times for each byte of y (launch_latent_project has what each
+// measured; 4096 rows of 64 heads, 128 to 512, 60.6 us, 5.7 TB/s). Tiles go around the CTAs that
+// stay; loads of the next tile and the stores of the last overlap the products through a ring of
+// k-blocks of 64 and two accumulators.
 //
 // Warps: 4 write tiles out (TMEM, bf16, shared memory, one TMA box of their rows each 64
 // columns; boxes leave out what lies past the tensor), one brings boxes, one issues products.
@@ -233,6 +235,12 @@ cudaError_t launch_latent_project(const uint16_t *x, long long x_stride, long lo
   // strides of dimensions of one are never used, but have to be valid
   if (H == 1) x_head = K, y_head = N;
   if (T == 1) x_stride = x_head * H, y_stride = y_head * H;
+  // us, with inputs that take turns from memory, tiles of 64 x 64 / 128 x 64 / 128 x 256 (heads x
+  // K to N):
+  //      1 row,  64 x 128 to 512    4.9 /  5.9 /  5.5      64 rows, 64 x 512 to 128    6.2 /  6.4 /  7.8
+  //    128 rows, 16 x 128 to 512    4.1 /  4.2 /  5.7     128 rows, 64 x 512 to 128    8.5 /  7.1 /  8.6
+  //    512 rows, 16 x 128 to 512    6.0 /  5.6 /  6.3     512 rows, 64 x 512 to 128   21.1 / 15.1 / 14.1
+  //    512 rows, 64 x 128 to 512   13.9 / 12.2 / 13.2    4096 rows, 64 x 128 to 512   83.6 / 74.7 / 60.6
   const long long wide = static_cast<long long>(H) * ((T + 127) / 128) * ((N + 255) / 256);
   auto launch = T <= 64 ? launch_shape<64, 64>
                         : (wide < num_sms ? launch_shape<128, 64> : launch_shape<128, 256>);
