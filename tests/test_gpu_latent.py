@@ -672,7 +672,7 @@ def test_prompt_not_finite_where_not_seen(env):
     """NaN in keys and values of later tokens and of other sequences does not reach a row; a value
     that is seen makes its element what the sum makes it."""
     torch, ssd, dev = env
-    for at in (150, 40, 299, 128, 255):
+    for at in (150, 40, 299, 128, 255, 100, 70, 200):
         p = _Prompt(env, [300, 90], [300, 90], 2)
         p.run()
         clean = p.out.clone()
