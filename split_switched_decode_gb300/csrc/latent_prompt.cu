@@ -41,7 +41,7 @@
 //
 // Measured: 4096 tokens, 64 heads of 128 + 64 and 128 elements 257 us, 1337 TFLOP/s of the pairs
 // seen (235 us without any softmax: products, loads, starts and ends of blocks); 777 tokens, 16
-// heads 17.5 us.
+// heads 18.3 us.
 #include <float.h>
 
 #include "attn_tc.cuh"
@@ -52,13 +52,21 @@ namespace ssd {
 namespace {
 
 constexpr int PR_THREADS = 384;  // 8 softmax warps, boxes, products, 2 that look at values
-constexpr int PR_SLOTS = 8, PR_SLAB = 128 * 128, PR_ROWS = 256;
+constexpr int PR_SLAB = 128 * 128;
+constexpr int PR_MAX_Q = 3;  // slabs of q and k
 // Barriers of tiles, taken in turn: as many as there are tiles in the ring (two slabs each at least),
 // so that the last use of one is over when it is armed again.
 constexpr int PR_TB = 4;
-constexpr int PR_MAX_Q = 3;  // slabs of q and k
 constexpr float PR_LATE = 16.0f;  // growth in the second half that moves the maximum
-constexpr size_t PR_SMEM = (2 * PR_MAX_Q + PR_SLOTS) * static_cast<size_t>(PR_SLAB);
+
+template <bool SPLIT>
+struct PrCfg {
+  static constexpr int ROWS = SPLIT ? 128 : 256;  // of a block
+  static constexpr int QS = SPLIT ? 1 : 2;        // tiles of q
+  // Slabs of the ring, or of two rings of two tiles each.
+  static constexpr int SLOTS = SPLIT ? 10 : 8;
+  static constexpr size_t SMEM = (QS * PR_MAX_Q + SLOTS) * static_cast<size_t>(PR_SLAB);
+};
 
 struct PromptBlock {
   int q0, n, k0, len, row0;  // the sequence's rows and keys, the block's first row
@@ -73,13 +81,14 @@ __device__ __forceinline__ int2 clamped_range(const int32_t *start, int s, int m
   return make_int2(a, max(b - a, 0));
 }
 // The blk-th block of rows of all sequences; false: there are fewer.
+template <int ROWS>
 __device__ __forceinline__ bool find_block(const LatentPromptParams &p, int blk,
                                            PromptSearch &f, PromptBlock &b) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.S + PR_THREADS - 1) / PR_THREADS;
   const int lo = min(tid * per, p.S), hi = min(lo + per, p.S);
   auto blocks = [&](int s) {
-    return (clamped_range(p.q_start, s, p.T).y + PR_ROWS - 1) / PR_ROWS;
+    return (clamped_range(p.q_start, s, p.T).y + ROWS - 1) / ROWS;
   };
   int mine = 0;
   for (int s = lo; s < hi; ++s) mine += blocks(s);
@@ -116,7 +125,7 @@ __device__ __forceinline__ bool find_block(const LatentPromptParams &p, int blk,
   b.n = q.y;
   b.k0 = k.x;
   b.len = k.y;
-  b.row0 = f.block * PR_ROWS;
+  b.row0 = f.block * ROWS;
   return true;
 }
 
@@ -132,7 +141,7 @@ __device__ __forceinline__ float min3(float a, float b, float c) {
   return d;
 }
 
-template <int KN, int VN>  // slabs of a key tile, of a value tile
+template <int KN, int VN, bool SPLIT>  // slabs of a key tile, of a value tile
 __global__ void __launch_bounds__(PR_THREADS, 1)
     latent_prompt_kernel(const __grid_constant__ CUtensorMap qmap,
                          const __grid_constant__ CUtensorMap kmap,
@@ -140,7 +149,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                          const __grid_constant__ CUtensorMap vmap,
                          const __grid_constant__ LatentPromptParams p, const uint16_t *values,
                          const long long v_stride, const long long v_head) {
-  extern __shared__ __align__(1024) uint8_t pr_smem[];  // Q0, Q1, the ring
+  using C = PrCfg<SPLIT>;
+  extern __shared__ __align__(1024) uint8_t pr_smem[];  // q, the ring
   __shared__ PromptSearch search;
   __shared__ __align__(8) uint64_t k_full[PR_TB], k_empty[PR_TB], v_full[PR_TB], v_empty[PR_TB];
   __shared__ __align__(8) uint64_t v_ready[PR_TB], qfull[2], s_full[2], p_half[2], p_full[2], h_done[2];
@@ -148,6 +158,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
   __shared__ uint32_t bad[PR_TB][4];  // tokens with values that are not finite
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
+  __shared__ float2 half_ml[SPLIT ? 2 : 1][SPLIT ? 128 : 1];  // a group's maximum and sum of a row
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     abort_flag = 0;
@@ -176,7 +187,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
   griddep_wait();
   const int h = blockIdx.x % p.H;
   PromptBlock b;
-  if (!find_block(p, blockIdx.x / p.H, search, b)) return;
+  if (!find_block<C::ROWS>(p, blockIdx.x / p.H, search, b)) return;
   if (warp == 9) {
     tmem_alloc(&tmem_slot, 512);
     tmem_relinquish();
@@ -190,21 +201,31 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
   constexpr int STEP = KN + VN;
   // position of row i is shift + i; tiles of 128 keys that some row of a group sees
   const int shift = b.len - b.n;
-  auto rows_of = [&](int g) { return min(128, b.n - b.row0 - 128 * g); };
+  auto first_of = [&](int g) { return b.row0 + (SPLIT ? 0 : 128 * g); };  // a group's first row
+  auto rows_of = [&](int g) { return min(128, b.n - first_of(g)); };
   auto tiles_of = [&](int g) {
     const int rows = rows_of(g);
-    return rows > 0 ? (max(shift + b.row0 + 128 * g + rows, 0) + 127) >> 7 : 0;
+    return rows > 0 ? (max(shift + first_of(g) + rows, 0) + 127) >> 7 : 0;
   };
-  const int nt0 = tiles_of(0), nt1 = tiles_of(1), nt = max(nt0, nt1);
+  // A group's tiles, and the CTA's; a group's i-th.
+  const int both = tiles_of(0);
+  const int nt0 = SPLIT ? (both + 1) >> 1 : both, nt1 = SPLIT ? both >> 1 : tiles_of(1);
+  const int nt = SPLIT ? both : max(nt0, nt1);
+  auto tile = [&](int g, int i) { return SPLIT ? 2 * i + g : i; };
   // whether some row of the group does not see the whole tile
   auto partial = [&](int g, int j) {
-    return j < (g ? nt1 : nt0) && j * 128 + 127 > shift + b.row0 + 128 * g;
+    return (SPLIT || j < (g ? nt1 : nt0)) && j * 128 + 127 > shift + first_of(g);
   };
   auto wait = [&](uint64_t *bar, int phase) {
     return mbar_wait_bounded(bar, phase & 1, p.status, &abort_flag, p.wait_limit_ns);
   };
-  uint8_t *const ring = pr_smem + 2 * PR_MAX_Q * PR_SLAB;
-  int issued = 0;
+  uint8_t *const ring = pr_smem + C::QS * PR_MAX_Q * PR_SLAB;
+  // the slot of slab x of tile j: keys, then values
+  auto slot_of = [&](int j, int x) {
+    if (SPLIT) return x < KN ? (j & 1) * KN + x : 2 * KN + (j & 1) * VN + x - KN;
+    return static_cast<int>(static_cast<uint32_t>(j * STEP + x) % C::SLOTS);
+  };
+  int k_issued = 0, v_issued = 0;  // tiles that were begun
 
   if (warp == 8) {
     // ================================================================ boxes
@@ -218,29 +239,56 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
       }
       __syncwarp();
     };
-    queries(0);
-    for (int i = 0, j = 0; go && j < nt; ++j) {
+    auto box = [&](int j, int x, uint32_t to) {  // slab x of tile j
       const int tok = b.k0 + j * 128;
-#pragma unroll 1
-      for (int x = 0; x < STEP; ++x, ++i) {
-        if (i >= PR_SLOTS) {  // what held the slot: a slab of tile j2's keys or values
-          const int j2 = (i - PR_SLOTS) / STEP, x2 = i - PR_SLOTS - j2 * STEP;
-          uint64_t *const bar = x2 < KN ? &k_empty[j2 % PR_TB] : &v_empty[j2 % PR_TB];
-          go = __all_sync(0xffffffffu, wait(bar, j2 / PR_TB));
-          if (!go) break;
+      uint64_t *const bar = x < KN ? &k_full[j % PR_TB] : &v_full[j % PR_TB];
+      if (x == 0) mbar_arrive_expect_tx(bar, KN * PR_SLAB);
+      if (x == KN) mbar_arrive_expect_tx(bar, VN * PR_SLAB);
+      if (x * 64 < p.N) tma_load_3d(to, &kmap, bar, x * 64, h, tok);
+      else if (x < KN) tma_load_3d(to, &rmap, bar, x * 64 - p.N, 0, tok);
+      else tma_load_3d(to, &vmap, bar, (x - KN) * 64, h, tok);
+    };
+    queries(0);
+    if constexpr (SPLIT) {
+      auto part = [&](int j, int from, int end) {  // keys or values of tile j
+        if (!go || j >= nt) return;
+        if (j >= 2) {
+          uint64_t *const bar = from < KN ? &k_empty[(j - 2) % PR_TB] : &v_empty[(j - 2) % PR_TB];
+          go = __all_sync(0xffffffffu, wait(bar, (j - 2) / PR_TB));
+          if (!go) return;
         }
-        issued = i + 1;
-        if (elect_one()) {
-          const uint32_t to = smem_u32(ring + i % PR_SLOTS * PR_SLAB);
-          uint64_t *const bar = x < KN ? &k_full[j % PR_TB] : &v_full[j % PR_TB];
-          if (x == 0) mbar_arrive_expect_tx(bar, KN * PR_SLAB);
-          if (x == KN) mbar_arrive_expect_tx(bar, VN * PR_SLAB);
-          if (x * 64 < p.N) tma_load_3d(to, &kmap, bar, x * 64, h, tok);
-          else if (x < KN) tma_load_3d(to, &rmap, bar, x * 64 - p.N, 0, tok);
-          else tma_load_3d(to, &vmap, bar, (x - KN) * 64, h, tok);
-        }
+        (from < KN ? k_issued : v_issued) = j + 1;
+        if (elect_one())
+          for (int x = from; x < end; ++x) box(j, x, smem_u32(ring + slot_of(j, x) * PR_SLAB));
         __syncwarp();
-        if (i == KN - 1) queries(1);  // behind the first keys, with which the first rows begin
+      };
+      // in the order in which slots become free: keys leave a tile before its values do
+      part(0, 0, KN);
+      part(0, KN, STEP);
+      part(1, 0, KN);
+      part(1, KN, STEP);
+      part(2, 0, KN);
+      part(3, 0, KN);
+#pragma unroll 1
+      for (int j = 2; go && j < nt; ++j) {
+        part(j, KN, STEP);
+        part(j + 2, 0, KN);
+      }
+    } else {
+      for (int i = 0, j = 0; go && j < nt; ++j) {
+#pragma unroll 1
+        for (int x = 0; x < STEP; ++x, ++i) {
+          if (i >= C::SLOTS) {  // what held the slot: a slab of tile j2's keys or values
+            const int j2 = (i - C::SLOTS) / STEP, x2 = i - C::SLOTS - j2 * STEP;
+            uint64_t *const bar = x2 < KN ? &k_empty[j2 % PR_TB] : &v_empty[j2 % PR_TB];
+            go = __all_sync(0xffffffffu, wait(bar, j2 / PR_TB));
+            if (!go) break;
+          }
+          (x < KN ? k_issued : v_issued) = j + 1;
+          if (elect_one()) box(j, x, smem_u32(ring + i % C::SLOTS * PR_SLAB));
+          __syncwarp();
+          if (i == KN - 1) queries(1);  // behind the first keys, with which the first rows begin
+        }
       }
     }
   } else if (warp == 9) {
@@ -250,32 +298,35 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
       const uint32_t id_o64 = idesc_bf16(64) | (1u << 16);
       const uint64_t ring_k = sw128_desc(smem_u32(ring));
       const uint64_t ring_v = sw128_mn_desc(smem_u32(ring), PR_SLAB);
-      auto scores = [&](int g, int j, bool last) {
-        const uint64_t q = sw128_desc(smem_u32(pr_smem) + g * PR_MAX_Q * PR_SLAB);
-        if (g == 0 || j >= nt0) wait(&k_full[j % PR_TB], j / PR_TB);
+      // `last`: no other rows need the tile
+      auto scores = [&](int g, int n, bool last) {
+        const int j = tile(g, n);
+        const uint64_t q = sw128_desc(smem_u32(pr_smem) + (SPLIT ? 0 : g * PR_MAX_Q * PR_SLAB));
+        if (SPLIT || g == 0 || j >= nt0) wait(&k_full[j % PR_TB], j / PR_TB);
         tc_fence_after();
 #pragma unroll
         for (int i = 0; i < KN; ++i) {
           const uint64_t a = q + i * (PR_SLAB >> 4);
-          const uint64_t k = ring_k + static_cast<uint32_t>((j * STEP + i) % PR_SLOTS) * (PR_SLAB >> 4);
+          const uint64_t k = ring_k + static_cast<uint32_t>(slot_of(j, i)) * (PR_SLAB >> 4);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             tc_mma(tmem + g * 128, a + 2 * kk, k + 2 * kk, id_s, i > 0 || kk > 0 ? 1u : 0u);
         }
         tc_commit(&s_full[g]);
-        if (last) tc_commit(&k_empty[j % PR_TB]);
+        if (SPLIT || last) tc_commit(&k_empty[j % PR_TB]);
       };
-      auto outputs = [&](int g, int j, bool last) {
-        const uint32_t slot = static_cast<uint32_t>(j * STEP + KN) % PR_SLOTS;
+      auto outputs = [&](int g, int n, bool last) {
+        const int j = tile(g, n);
+        const uint32_t slot = slot_of(j, KN);
         const uint64_t v = ring_v + slot * (PR_SLAB >> 4);
-        const bool split = VN == 2 && slot == PR_SLOTS - 1;  // the second slab is slot 0
+        const bool split = !SPLIT && VN == 2 && slot == C::SLOTS - 1;  // the second slab is slot 0
         const uint32_t o = tmem + 256 + g * 128, w = tmem + g * 128;
-        if (g == 0 || j >= nt0) wait(&v_ready[j % PR_TB], j / PR_TB);
+        if (SPLIT || g == 0 || j >= nt0) wait(&v_ready[j % PR_TB], j / PR_TB);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          wait(half ? &p_full[g] : &p_half[g], j);
+          wait(half ? &p_full[g] : &p_half[g], n);
           tc_fence_after();
-          const uint32_t acc = half || j > 0 ? 1u : 0u;
+          const uint32_t acc = half || n > 0 ? 1u : 0u;
           if (!split) {
 #pragma unroll
             for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
@@ -290,19 +341,19 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
           }
           if (half == 0) tc_commit(&h_done[g]);
         }
-        if (last) tc_commit(&v_empty[j % PR_TB]);
-        if (j + 1 == (g ? nt1 : nt0)) tc_commit(&o_full[g]);
+        if (SPLIT || last) tc_commit(&v_empty[j % PR_TB]);
+        if (n + 1 == (g ? nt1 : nt0)) tc_commit(&o_full[g]);
       };
       if (nt0 > 0) {
         wait(&qfull[0], 0);
         scores(0, 0, nt1 == 0);
       }
       if (nt1 > 0) {
-        wait(&qfull[1], 0);
+        if (!SPLIT) wait(&qfull[1], 0);
         scores(1, 0, true);
       }
 #pragma unroll 1
-      for (int j = 0; j < nt; ++j) {
+      for (int j = 0; j < (SPLIT ? nt0 : nt); ++j) {
         if (j < nt0) outputs(0, j, j >= nt1);
         if (j + 1 < nt0) scores(0, j + 1, j + 1 >= nt1);
         if (j < nt1) outputs(1, j, true);
@@ -324,7 +375,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
         uint32_t carry = 0;
 #pragma unroll
         for (int i = 0; i < VN; ++i) {
-          const uint8_t *from = ring + (j * STEP + KN + i) % PR_SLOTS * PR_SLAB + w * (64 * 128);
+          const uint8_t *from = ring + slot_of(j, KN + i) * PR_SLAB + w * (64 * 128);
 #pragma unroll 8
           for (int x = 0; x < 16; ++x) {
             const uint4 u = *reinterpret_cast<const uint4 *>(from + x * 512 + lane * 16);
@@ -336,7 +387,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
         if (__any_sync(0xffffffffu, carry & 0x80008000u)) {
 #pragma unroll 1
           for (int i = 0; i < VN; ++i) {
-            uint8_t *slab = ring + (j * STEP + KN + i) % PR_SLOTS * PR_SLAB + w * (64 * 128);
+            uint8_t *slab = ring + slot_of(j, KN + i) * PR_SLAB + w * (64 * 128);
 #pragma unroll 1
             for (int x = 0; x < 16; ++x) {
               uint4 *at = reinterpret_cast<uint4 *>(slab + x * 512 + lane * 16);
@@ -366,15 +417,16 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
     const int g = warp >> 2, r = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + g * 128 + lanes, o_at = tmem + 256 + g * 128 + lanes;
-    const int mine = g ? nt1 : nt0, row = b.row0 + 128 * g + r, pos = shift + row;
+    const int mine = g ? nt1 : nt0, row = first_of(g) + r, pos = shift + row;
     // (a scale of zero as one that no score shows: keys not seen stay at -infinity)
     const float zf = p.scale == 0.0f ? FLT_MIN : p.scale * LOG2E;
     const bool least = zf < 0.0f;
     float m = -INFINITY, l = 0.0f;
     float z[2][32];
     float2 sum[2];
-    for (int j = 0; j < mine; ++j) {
-      wait(&s_full[g], j);
+    for (int n = 0; n < mine; ++n) {
+      const int j = tile(g, n);
+      wait(&s_full[g], n);
       tc_fence_after();
       const bool whole = !partial(g, j);
       const int to = pos - j * 128;  // the last key seen, in the tile
@@ -431,7 +483,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
       tmem_ld32(s_at + 32, z[1]);
       tmem_wait_ld();
       float mx = largest(0);
-      if (j == 0) m = mx;
+      if (n == 0) m = mx;
       else if (__any_sync(0xffffffffu, mx - m >= TC_LAZY)) move(mx, TC_LAZY);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
@@ -439,7 +491,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
           tmem_wait_ld();
           mx = largest(1);
           if (__any_sync(0xffffffffu, mx - m >= PR_LATE)) {
-            wait(&h_done[g], j);
+            wait(&h_done[g], n);
             tc_fence_after();
             move(mx, PR_LATE);
           }
@@ -470,7 +522,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
       if (taken) {
         // values that were taken out: added where they are seen (a weight of zero is taken as
         // the smallest number), between the two products
-        wait(&h_done[g], j);
+        wait(&h_done[g], n);
         tc_fence_after();
 #pragma unroll 1
         for (int d = 0; d < p.V; d += 16) {
@@ -500,20 +552,43 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
       tc_fence_before();
       mbar_arrive(&p_full[g]);
     }
-    if (mine > 0) wait(&o_full[g], 0);
+    // what the row's two groups (or its one) hold, as factors of the outputs in tensor memory
+    float f0 = 1.0f, f1 = 0.0f;
+    if constexpr (SPLIT) {
+      half_ml[g][r] = make_float2(m, l);
+      named_bar_sync(1, 256);
+      const float2 x = half_ml[0][r], y = half_ml[1][r];
+      m = fmaxf(x.x, y.x);
+      const float base = m == -INFINITY ? 0.0f : m;
+      f0 = ex2(x.x - base);
+      f1 = ex2(y.x - base);
+      l = f0 * x.y + f1 * y.y;
+      if (nt0 > 0) wait(&o_full[0], 0);
+      if (nt1 > 0) wait(&o_full[1], 0);
+    } else if (mine > 0) {
+      wait(&o_full[g], 0);
+    }
     tc_fence_after();
     const bool stored = r < rows_of(g);
-    if (stored && p.lse)
+    if (stored && p.lse && (!SPLIT || g == 0))
       p.lse[static_cast<long long>(b.q0 + row) * p.H + h] =
           l == 0.0f ? -INFINITY : (m + log2f(l)) * LN2;
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     uint16_t *out = p.out + (b.q0 + row) * p.out_stride + static_cast<long long>(h) * p.V;
+    // (of one tile of rows each group writes every other 32 elements)
 #pragma unroll 1
-    for (int d = 0; d < p.V; d += 32) {
+    for (int d = SPLIT ? 32 * g : 0; d < p.V; d += SPLIT ? 64 : 32) {
       float o[32];
-      if (mine > 0) {
-        tmem_ld32(o_at + d, o);
+      if (SPLIT ? nt0 > 0 : mine > 0) {
+        tmem_ld32((SPLIT ? tmem + 256 + lanes : o_at) + d, o);
         tmem_wait_ld();
+      }
+      if (SPLIT && nt1 > 0) {
+        float o1[32];
+        tmem_ld32(tmem + 384 + lanes + d, o1);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = f0 * o[e] + f1 * o1[e];
       }
       if (!stored) continue;
 #pragma unroll
@@ -539,20 +614,42 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
       mbar_wait_drain(&drained, 0, 10000000ull);
     }
     if (warp == 8) {
-      for (int g = 0; g < 2; ++g)
+      for (int g = 0; g < C::QS; ++g)
         if ((g ? nt1 : nt0) > 0) mbar_wait_drain(&qfull[g], 0, 10000000ull);
       // (a tile of which only some slabs were requested never completes: short waits)
-      const int last = (issued - 1) / STEP;
-      for (int j = last; issued > 0 && j >= 0 && j > last - PR_TB; --j) {
+      for (int j = k_issued - 1; j >= 0 && j >= k_issued - PR_TB; --j)
         mbar_wait_drain(&k_full[j % PR_TB], (j / PR_TB) & 1, 5000000ull);
-        if (issued > j * STEP + KN) mbar_wait_drain(&v_full[j % PR_TB], (j / PR_TB) & 1, 5000000ull);
-      }
+      for (int j = v_issued - 1; j >= 0 && j >= v_issued - PR_TB; --j)
+        mbar_wait_drain(&v_full[j % PR_TB], (j / PR_TB) & 1, 5000000ull);
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
   }
   if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+template <bool SPLIT>
+cudaError_t launch_widths(const LatentPromptParams &p, cudaStream_t s, const CUtensorMap &qm,
+                          const CUtensorMap &km, const CUtensorMap &rm, const CUtensorMap &vm,
+                          const uint16_t *v, long long v_stride, long long v_head) {
+  using C = PrCfg<SPLIT>;
+  void (*kernel)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, LatentPromptParams,
+                 const uint16_t *, long long, long long) = nullptr;
+  switch ((p.N + p.P) / 64 * 2 + p.V / 64 - 1) {
+    case 2: kernel = latent_prompt_kernel<1, 1, SPLIT>; break;
+    case 3: kernel = latent_prompt_kernel<1, 2, SPLIT>; break;
+    case 4: kernel = latent_prompt_kernel<2, 1, SPLIT>; break;
+    case 5: kernel = latent_prompt_kernel<2, 2, SPLIT>; break;
+    case 6: kernel = latent_prompt_kernel<3, 1, SPLIT>; break;
+    default: kernel = latent_prompt_kernel<3, 2, SPLIT>; break;
+  }
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(C::SMEM));
+  if (e != cudaSuccess) return e;
+  const long long blocks = p.T / C::ROWS + static_cast<long long>(p.S);
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks * p.H)), dim3(PR_THREADS), C::SMEM, s,
+                    qm, km, rm, vm, p, v, v_stride, v_head);
 }
 
 }  // namespace
@@ -562,7 +659,6 @@ cudaError_t launch_latent_prompt(const LatentPromptParams &p, const uint16_t *q,
                                  long long k_head, const uint16_t *k_rope, long long r_stride,
                                  const uint16_t *v, long long v_stride, long long v_head,
                                  int num_sms, cudaStream_t s) {
-  (void)num_sms;
   CUtensorMap qm, km, rm = {}, vm;
   const int D = p.N + p.P;
   // strides of dimensions of one are never used, but have to be valid
@@ -578,23 +674,10 @@ cudaError_t launch_latent_prompt(const LatentPromptParams &p, const uint16_t *q,
       (p.P > 0 && !host_map(&rm, k_rope, 2, 3, rd, rs, box, true)) ||
       !host_map(&vm, v, 2, 3, vd, vs, box, true))
     return cudaErrorInvalidValue;
-  void (*kernel)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, LatentPromptParams,
-                 const uint16_t *, long long, long long) = nullptr;
-  switch (D / 64 * 2 + p.V / 64 - 1) {
-    case 2: kernel = latent_prompt_kernel<1, 1>; break;
-    case 3: kernel = latent_prompt_kernel<1, 2>; break;
-    case 4: kernel = latent_prompt_kernel<2, 1>; break;
-    case 5: kernel = latent_prompt_kernel<2, 2>; break;
-    case 6: kernel = latent_prompt_kernel<3, 1>; break;
-    default: kernel = latent_prompt_kernel<3, 2>; break;
-  }
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(PR_SMEM));
-  if (e != cudaSuccess) return e;
   // as many blocks of rows as there can be: a part of one a sequence
-  const long long blocks = p.T / PR_ROWS + p.S;
-  return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks * p.H)), dim3(PR_THREADS), PR_SMEM, s,
-                    qm, km, rm, vm, p, v, v_stride, v_head);
+  const long long blocks = (p.T / PrCfg<false>::ROWS + static_cast<long long>(p.S)) * p.H;
+  auto launch = blocks < num_sms ? launch_widths<true> : launch_widths<false>;
+  return launch(p, s, qm, km, rm, vm, v, v_stride, v_head);
 }
 
 }  // namespace ssd

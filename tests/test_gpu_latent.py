@@ -602,12 +602,24 @@ def test_prompt(env, rows, keys):
         p.check()
 
 
-@pytest.mark.parametrize("N,P,V", [(64, 64, 64), (64, 0, 64), (128, 0, 128), (128, 64, 64), (64, 64, 128)])
+@pytest.mark.parametrize("rows,keys", [
+    ([1], [500]), ([129], [129]), ([255, 256, 257], [255, 256, 257]), ([777], [777]), ([130, 3], [400, 1000]),
+    ([60, 200], [10, 150]), ([40, 7], [0, 0]), ([513], [1200]),
+])
+def test_prompt_many_heads(env, rows, keys):
+    p = _Prompt(env, rows, keys, 160)
+    p.run()
+    p.check()
+
+
+@pytest.mark.parametrize("N,P,V", [(64, 64, 64), (64, 0, 64), (128, 0, 128), (128, 64, 64), (64, 64, 128),
+                                   (64, 0, 128)])
 def test_prompt_widths(env, N, P, V):
     for joint in (True, False):
-        p = _Prompt(env, [300, 20], [300, 220], 3, N, P, V, joint=joint)
-        p.run()
-        p.check()
+        for H, rows, keys in ((3, [300, 20], [300, 220]), (1, [30], [1900]), (80, [300, 20], [300, 220])):
+            p = _Prompt(env, rows, keys, H, N, P, V, joint=joint)
+            p.run()
+            p.check()
 
 
 def test_prompt_many_sequences(env):
@@ -617,10 +629,11 @@ def test_prompt_many_sequences(env):
     p.check()
 
 
-def test_prompt_many_calls(env):
-    """The same bits and no wait that runs out over a thousand blocks of rows, 300 times."""
+@pytest.mark.parametrize("rows,H", [([4096], 64), ([777], 16), ([1000], 3)])
+def test_prompt_many_calls(env, rows, H):
+    """The same bits and no wait that runs out over up to a thousand blocks of rows, 300 times."""
     torch, ssd, dev = env
-    p = _Prompt(env, [4096], [4096], 64, extra=0)
+    p = _Prompt(env, rows, rows, H, extra=0)
     p.run()
     first = p.out.clone()
     for _ in range(300):
@@ -638,9 +651,11 @@ def test_prompt_keys_by_default(env):
     assert torch.equal(out, p.out)
 
 
-def test_prompt_growing_scores(env):
+# (a CTA takes 128 rows where there are few, 256 rows with many heads)
+@pytest.mark.parametrize("H", [2, 160])
+def test_prompt_growing_scores(env, H):
     torch, ssd, dev = env
-    p = _Prompt(env, [600], [600], 2)
+    p = _Prompt(env, [600], [600], H)
     ramp = torch.linspace(0, 2, p.Tk + 1, device=dev)[:, None, None]
     p.k.copy_((p.k.float() * 0.1 + ramp).to(torch.bfloat16))
     p.q.copy_((p.q.float() * 0.1 + 0.5).to(torch.bfloat16))
@@ -650,11 +665,12 @@ def test_prompt_growing_scores(env):
         p.check()
 
 
-def test_prompt_scores_that_jump(env):
+@pytest.mark.parametrize("H", [2, 160])
+def test_prompt_scores_that_jump(env, H):
     """Scores that grow by far more than what moves the maximum at once, within a tile's halves and from
     tile to tile, for some rows only."""
     torch, ssd, dev = env
-    p = _Prompt(env, [700], [700], 2)
+    p = _Prompt(env, [700], [700], H)
     for j, size in ((3, 1.0), (70, 8.0), (100, 20.0), (127, 30.0), (200, 45.0), (330, 60.0), (331, 61.0),
                     (500, 90.0), (640, 130.0)):
         p.k[j] = 0
@@ -668,19 +684,20 @@ def test_prompt_scores_that_jump(env):
         p.check()
 
 
-def test_prompt_not_finite_where_not_seen(env):
+@pytest.mark.parametrize("H", [2, 160])
+def test_prompt_not_finite_where_not_seen(env, H):
     """NaN in keys and values of later tokens and of other sequences does not reach a row; a value
     that is seen makes its element what the sum makes it."""
     torch, ssd, dev = env
     for at in (150, 40, 299, 128, 255, 100, 70, 200):
-        p = _Prompt(env, [300, 90], [300, 90], 2)
+        p = _Prompt(env, [300, 90], [300, 90], H)
         p.run()
         clean = p.out.clone()
         p.k[300:] = math.nan
         p.v[300:] = math.nan
         p.run()
         assert torch.equal(p.out[:300], clean[:300])
-        p = _Prompt(env, [300, 90], [300, 90], 2)
+        p = _Prompt(env, [300, 90], [300, 90], H)
         p.v[at, 1, 17] = math.inf
         p.v[at, 1, 18] = math.nan
         p.run()
@@ -694,7 +711,7 @@ def test_prompt_not_finite_where_not_seen(env):
         # rows that see it hold its weight in the sum all the same: the others' elements stay
         assert bool((got.float() - want.float()).abs().max() <= 2.0 ** -7 * want.float().abs().max())
         assert torch.equal(got[:at], want[:at]) and torch.equal(got[300:], want[300:])
-        p = _Prompt(env, [300, 90], [300, 90], 2)
+        p = _Prompt(env, [300, 90], [300, 90], H)
         p.k[at, 0, 3] = math.nan
         p.run()
         assert bool(p.out[at:300, 0].isnan().all()) and torch.equal(p.out[:at], clean[:at])
