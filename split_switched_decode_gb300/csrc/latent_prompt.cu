@@ -251,16 +251,16 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
     queries(0);
     if constexpr (SPLIT) {
       auto part = [&](int j, int from, int end) {  // keys or values of tile j
-        if (!go || j >= nt) return;
-        if (j >= 2) {
+        if (go && j >= 2 && j < nt) {
           uint64_t *const bar = from < KN ? &k_empty[(j - 2) % PR_TB] : &v_empty[(j - 2) % PR_TB];
           go = __all_sync(0xffffffffu, wait(bar, (j - 2) / PR_TB));
-          if (!go) return;
         }
-        (from < KN ? k_issued : v_issued) = j + 1;
-        if (elect_one())
-          for (int x = from; x < end; ++x) box(j, x, smem_u32(ring + slot_of(j, x) * PR_SLAB));
-        __syncwarp();
+        if (go && j < nt) {
+          (from < KN ? k_issued : v_issued) = j + 1;
+          if (elect_one())
+            for (int x = from; x < end; ++x) box(j, x, smem_u32(ring + slot_of(j, x) * PR_SLAB));
+          __syncwarp();
+        }
       };
       // in the order in which slots become free: keys leave a tile before its values do
       part(0, 0, KN);
