@@ -587,17 +587,27 @@ _PROMPT = struct.Struct("<19qd4q")
 
 def _part(t, name, dims, device):
     """(pointer, shape, strides) of a bf16 tensor of `dims` dimensions, the last contiguous, on
-    `device`."""
-    if t.dtype is not _BF16 or not t.is_cuda:
-        raise TypeError(f"{name} must be a bfloat16 CUDA tensor of {dims} dimensions")
+    `device` (of the first tensor; negative: that is not a CUDA tensor)."""
     shape, stride = t.shape, t.stride()
-    if len(shape) != dims:
+    if t.dtype is not _BF16 or len(shape) != dims or device < 0 or t.get_device() != device:
+        if t.is_cuda and t.dtype is _BF16 and len(shape) == dims and device >= 0:
+            raise ValueError(f"{name} is on another device than the first tensor")
         raise TypeError(f"{name} must be a bfloat16 CUDA tensor of {dims} dimensions")
-    if t.get_device() != device:
-        raise ValueError(f"{name} is on another device than the first tensor")
     if stride[-1] != 1 and shape[-1] != 1:
         raise TypeError(f"the last dimension of {name} must be contiguous")
     return t.data_ptr(), shape, stride
+
+
+def _plain(t, name, kind, count, device):
+    """Pointer of a contiguous tensor of `kind` with `count` elements on `device`."""
+    if t.dtype is not kind or t.get_device() != device or not t.is_contiguous():
+        if t.is_cuda and t.dtype is kind and t.is_contiguous():
+            raise ValueError(f"{name} is on another device than the first tensor")
+        raise TypeError(f"{name} must be a contiguous {'int32' if kind is _I32 else 'float32'} "
+                        "CUDA tensor")
+    if t.numel() != count:
+        raise ValueError(f"{name} must have {count} elements")
+    return t.data_ptr()
 
 
 def _latent_cache(t, device):
@@ -655,16 +665,14 @@ def latent_append(c, k_rope, positions, slots, inv_freq, cache, weight=None, eps
         wp, (Rw,), _ = _part(weight, "weight", 1, dev)
         if Rw != R:
             raise ValueError("latent_append: weight must be [R]")
-    if positions.numel() != T or slots.numel() != T:
-        raise ValueError("latent_append: positions and slots must be [T]")
     if inv_freq is not None:
-        rot = 2 * inv_freq.numel()
-        fp = _scales(inv_freq, "inv_freq", rot // 2)
+        n = inv_freq.numel()
+        rot, fp = 2 * n, _plain(inv_freq, "inv_freq", _F32, n, dev)
     status = lib.dec_latent_call(0, _APPEND.pack(
-        cp, cs[0], wp, eps, kp, ks, qp, q0, q1, _int32(positions, "positions"),
-        _int32(slots, "slots"), fp, magnitude, T, H, R, P, rot, 1 if interleaved else 0, op, o0, o1,
+        cp, cs[0], wp, eps, kp, ks, qp, q0, q1, _plain(positions, "positions", _I32, T, dev),
+        _plain(slots, "slots", _I32, T, dev), fp, magnitude, T, H, R, P, rot, 1 if interleaved else 0, op, o0, o1,
         rp, rs, cache.data_ptr(), kind,
-        0 if cache_scale is None else _scales(cache_scale, "cache_scale", 1), pages, page,
+        0 if cache_scale is None else _plain(cache_scale, "cache_scale", _F32, 1, dev), pages, page,
         page_stride, token_stride, _launch_stream(dev, stream)))
     if status:
         raise DecError(status, "latent_append")
@@ -703,23 +711,22 @@ def latent_decode(q, cache, block_table, seq_len, out, ws, scale, q_start=None, 
     kind, pages, page, width, page_stride, token_stride = _latent_cache(cache, dev)
     qp, (T, H, Wq), qs = _part(q, "q", 3, dev)
     op, (To, Ho, R), os_ = _part(out, "out", 3, dev)
-    table = _int32(block_table, "block_table")
     if block_table.dim() != 2:
         raise TypeError("block_table must have two dimensions")
     S, max_pages = block_table.shape
-    if Wq != width or R > width or To != T or Ho != H or seq_len.numel() != S or \
-            (q_start is not None and q_start.numel() != S + 1):
+    table = _plain(block_table, "block_table", _I32, S * max_pages, dev)
+    if Wq != width or R > width or To != T or Ho != H:
         raise ValueError("latent_decode: sizes do not agree")
     if H > 1 and (qs[1] != width or os_[1] != R):
         raise TypeError("latent_decode: heads must be contiguous within a row")
-    if not ws.is_cuda or not ws.is_contiguous():
-        raise TypeError("ws must be a contiguous CUDA tensor")
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise TypeError("ws must be a contiguous CUDA tensor on the cache's device")
     status = lib.dec_latent_call(2, _DECODE.pack(
         qp, qs[0], cache.data_ptr(), kind,
-        0 if cache_scale is None else _scales(cache_scale, "cache_scale", 1), pages, page,
-        page_stride, token_stride, table, max_pages, _int32(seq_len, "seq_len"),
-        0 if q_start is None else _int32(q_start, "q_start"), S, T, H, R, width - R,
-        scale, window, op, os_[0], 0 if lse is None else _scales(lse, "lse", T * H), ws.data_ptr(),
+        0 if cache_scale is None else _plain(cache_scale, "cache_scale", _F32, 1, dev), pages, page,
+        page_stride, token_stride, table, max_pages, _plain(seq_len, "seq_len", _I32, S, dev),
+        0 if q_start is None else _plain(q_start, "q_start", _I32, S + 1, dev), S, T, H, R, width - R,
+        scale, window, op, os_[0], 0 if lse is None else _plain(lse, "lse", _F32, T * H, dev), ws.data_ptr(),
         ws.nbytes, _launch_stream(dev, stream)))
     if status:
         raise DecError(status, "latent_decode")
@@ -748,15 +755,13 @@ def latent_prompt(q, k_nope, k_rope, v, q_start, out, scale, k_start=None, lse=N
     if Tv != Tk or Hv != H or Hk != H or To != T or Ho != H or Vo != V:
         raise ValueError("latent_prompt: sizes do not agree")
     S = q_start.numel() - 1
-    if k_start is not None and k_start.numel() != S + 1:
-        raise ValueError("latent_prompt: q_start and k_start do not agree")
     if H > 1 and (qs[1] != D or os_[1] != V):
         raise TypeError("latent_prompt: heads of q and out must be contiguous within a row")
     status = lib.dec_latent_call(3, _PROMPT.pack(
-        qp, qs[0], kp, ks[0], ks[1], rp, rs, vp, vs[0], vs[1], _int32(q_start, "q_start"),
-        0 if k_start is None else _int32(k_start, "k_start"), S, T,
+        qp, qs[0], kp, ks[0], ks[1], rp, rs, vp, vs[0], vs[1], _plain(q_start, "q_start", _I32, S + 1, dev),
+        0 if k_start is None else _plain(k_start, "k_start", _I32, S + 1, dev), S, T,
         Tk, H, N, P, V, scale, op, os_[0],
-        0 if lse is None else _scales(lse, "lse", T * H),
+        0 if lse is None else _plain(lse, "lse", _F32, T * H, dev),
         _launch_stream(dev, stream)))
     if status:
         raise DecError(status, "latent_prompt")
