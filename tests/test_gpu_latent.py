@@ -966,3 +966,46 @@ def test_prompt_replayed_with_other_lengths(env):
         p.lse.fill_(5.0)
         graph.replay()
         p.check()
+
+
+def test_binding_refuses_what_is_elsewhere_or_of_another_size(env):
+    torch, ssd, dev = env
+    d = _Decode(env, [100, 30], [1, 1], 8)
+    q, out = d.q[:2], d.out[:2]
+    good = dict(table=d.table, lens=d.seq_len, q_start=d.q_start, lse=d.lse[:2], ws=d.ws)
+
+    def run(**kw):
+        a = dict(good, **kw)
+        ssd.latent_decode(q, d.cache, a["table"], a["lens"], out, a["ws"], 0.06, q_start=a["q_start"],
+                          lse=a["lse"])
+
+    run()
+    for name in good:
+        with pytest.raises(TypeError):
+            run(**{name: good[name].cpu()})
+    for name in ("lens", "q_start", "lse"):
+        with pytest.raises(ValueError):
+            run(**{name: good[name][:1]})
+    for name in ("table", "lens", "q_start"):
+        with pytest.raises(TypeError):
+            run(**{name: good[name].long()})
+    c, r = _randn(torch, dev, _gen(torch, dev, 5), 2, 576).split([512, 64], 1)
+    at = _i32(torch, [0, 1], dev)
+    freq = torch.ones(32, device=dev)
+    ssd.latent_append(c, r, at, at, freq, d.cache)
+    for args in ((at.cpu(), at, freq), (at, at.cpu(), freq), (at, at, freq.cpu()), (at, at, freq.double())):
+        with pytest.raises(TypeError):
+            ssd.latent_append(c, r, *args, d.cache)
+    with pytest.raises(ValueError):
+        ssd.latent_append(c, r, at[:1], at, freq, d.cache)
+    with pytest.raises(TypeError):
+        ssd.latent_append(c.cpu(), r, at, at, freq, d.cache)
+    p = _Prompt(env, [30], [30], 2)
+    p.run()
+    for name in ("q_start", "k_start", "lse", "r", "v"):
+        was = getattr(p, name)
+        setattr(p, name, was.cpu())
+        with pytest.raises(TypeError):
+            p.run()
+        setattr(p, name, was)
+    assert ssd.dec_sync_status() == ssd.DEC_OK
