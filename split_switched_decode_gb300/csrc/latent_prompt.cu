@@ -39,9 +39,19 @@
 // Blocks of rows are handed out by the grid's order, the last of a sequence (with the most
 // keys) first, heads next to each other.
 //
-// Measured: 4096 tokens, 64 heads of 128 + 64 and 128 elements 257 us, 1337 TFLOP/s of the pairs
-// seen (235 us without any softmax: products, loads, starts and ends of blocks); 777 tokens, 16
-// heads 18.3 us.
+// While there are fewer blocks of 256 rows than SMs, a CTA takes 128 (SPLIT): the two groups have
+// the same rows, one the even tiles of keys and the other the odd ones, each with its own maximum,
+// sum and outputs, which join at the end from tensor memory, where every warp reaches its lanes of
+// both. A row's way through its keys is half as long. Each tile of keys then serves 128 rows
+// instead of 256, so copies bound it sooner: keys and values have rings of two tiles of their own,
+// as keys leave a tile long before its values do (with one ring 8192 tokens of two heads took 95 us
+// instead of 57). us, 128 / 256 rows a CTA: 777 tokens, 16 heads 12.5 / 17.4; 2048, 16 28.3 / 37.3;
+// 512, 32 11.2 / 14.3; 8192, 2 55 / 111; 128 rows behind 4096 tokens, 16 heads 33 / 54; with more
+// blocks than SMs 4096, 64 393 (with one ring) / 260.
+//
+// Measured: 4096 tokens, 64 heads of 128 + 64 and 128 elements 257 to 268 us, 1337 to 1280 TFLOP/s of
+// the pairs seen, at the GPU's power limit (241 us without loads of keys and values past the first
+// two tiles); 777 tokens, 16 heads 12.5 us.
 #include <float.h>
 
 #include "attn_tc.cuh"
@@ -344,20 +354,34 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
         if (SPLIT || last) tc_commit(&v_empty[j % PR_TB]);
         if (n + 1 == (g ? nt1 : nt0)) tc_commit(&o_full[g]);
       };
-      if (nt0 > 0) {
-        wait(&qfull[0], 0);
-        scores(0, 0, nt1 == 0);
-      }
-      if (nt1 > 0) {
-        if (!SPLIT) wait(&qfull[1], 0);
-        scores(1, 0, true);
-      }
+      if constexpr (SPLIT) {
+        // S0 S1, then PV0 S0 PV1 S1 of every step, in one copy of either: jumping back over two
+        // copies takes 400 clocks (2048 tokens, 16 heads 29.8 us, 28.3 with one). Where blocks of 256
+        // rows fill the SMs, power bounds them, and one copy gains nothing (4096 tokens, 64 heads:
+        // 264 us against 261).
 #pragma unroll 1
-      for (int j = 0; j < (SPLIT ? nt0 : nt); ++j) {
-        if (j < nt0) outputs(0, j, j >= nt1);
-        if (j + 1 < nt0) scores(0, j + 1, j + 1 >= nt1);
-        if (j < nt1) outputs(1, j, true);
-        if (j + 1 < nt1) scores(1, j + 1, true);
+        for (int i = -2; i < 2 * nt0; ++i) {
+          const int g = i & 1, n = i >> 1, mine = g ? nt1 : nt0;
+          if (n >= 0 && n < mine) outputs(g, n, true);
+          if (i == -2 && nt0 > 0) wait(&qfull[0], 0);
+          if (n + 1 < mine) scores(g, n + 1, true);
+        }
+      } else {
+        if (nt0 > 0) {
+          wait(&qfull[0], 0);
+          scores(0, 0, nt1 == 0);
+        }
+        if (nt1 > 0) {
+          wait(&qfull[1], 0);
+          scores(1, 0, true);
+        }
+#pragma unroll 1
+        for (int j = 0; j < nt; ++j) {
+          if (j < nt0) outputs(0, j, j >= nt1);
+          if (j + 1 < nt0) scores(0, j + 1, j + 1 >= nt1);
+          if (j < nt1) outputs(1, j, true);
+          if (j + 1 < nt1) scores(1, j + 1, true);
+        }
       }
     }
     __syncwarp();
@@ -676,6 +700,7 @@ cudaError_t launch_latent_prompt(const LatentPromptParams &p, const uint16_t *q,
     return cudaErrorInvalidValue;
   // as many blocks of rows as there can be: a part of one a sequence
   const long long blocks = (p.T / PrCfg<false>::ROWS + static_cast<long long>(p.S)) * p.H;
+  // (both sides are at the top)
   auto launch = blocks < num_sms ? launch_widths<true> : launch_widths<false>;
   return launch(p, s, qm, km, rm, vm, v, v_stride, v_head);
 }
