@@ -64,11 +64,16 @@ __device__ __forceinline__ void put_cache8(const LatentAppendParams &p, long lon
 // rotary part apart, so that every thread owns what it overwrites and q_out may be q_rope.
 // Read once and written once: the copy rate bounds it, the launch's latency when rows are few;
 // then a row's heads are cut over gridDim.y, whose first CTA has the latent row. A thread requests
-// AHEAD units at a time, the first before the CTA meets. 8192 rows of 64 heads with rows kept 31.8 us
-// (163 MB, 5.1 TB/s; 37.2 with one unit at a time), one row 1.8 us.
-template <bool E4M3, bool INTER>
-__global__ void __launch_bounds__(LA_THREADS) latent_append_kernel(const LatentAppendParams p) {
-  constexpr int AHEAD = INTER ? 4 : 2;
+// AHEAD units at a time, the first before the CTA meets. With many rows (MANY) CTAs on an SM hide
+// more than units ahead do: 14 or 12 of them with half of the units; with few, registers for units
+// are better. us, MANY / not (64 heads, interleaved bf16, half pairs bf16, half pairs e4m3): 8192
+// rows 29.3 / 31.8, 32.0 / 33.1, 32.8 / 36.2 (16 heads 15.6 / 18.3, 16.9 / 18.7, 18.5 / 22.6); 2048 rows
+// 9.3 / 9.6, 10.8 / 10.3, 11.5 / 10.8; 512 rows 3.8 / 3.4, 4.0 / 3.7, 4.4 / 4.0. 8192 rows of 64 heads with
+// rows kept are 163 MB: 5.5 TB/s.
+template <bool E4M3, bool INTER, bool MANY>
+__global__ void __launch_bounds__(LA_THREADS, MANY ? (INTER ? 14 : 12) : 0)
+    latent_append_kernel(const LatentAppendParams p) {
+  constexpr int AHEAD = (INTER ? 4 : 2) / (MANY ? 2 : 1);
   __shared__ float2 cs[LATENT_MAX_W / 2];
   __shared__ float sums[LA_THREADS / 32];
   griddep_wait();
@@ -178,9 +183,16 @@ cudaError_t launch_latent_append(const LatentAppendParams &p, bool e4m3, bool in
   const int turning = interleaved ? p.rot / 8 : p.rot / 16;
   const int units = p.H * (turning + (p.P - p.rot) / 8);
   const int cuts = p.T < 2 * num_sms && units > 0 ? 1 + (units + LA_THREADS - 1) / LA_THREADS : 1;
+  const bool many = p.T >= 16 * num_sms;
   void (*kernel)(const LatentAppendParams);
-  if (interleaved) kernel = e4m3 ? latent_append_kernel<true, true> : latent_append_kernel<false, true>;
-  else kernel = e4m3 ? latent_append_kernel<true, false> : latent_append_kernel<false, false>;
+  if (many && interleaved)
+    kernel = e4m3 ? latent_append_kernel<true, true, true> : latent_append_kernel<false, true, true>;
+  else if (many)
+    kernel = e4m3 ? latent_append_kernel<true, false, true> : latent_append_kernel<false, false, true>;
+  else if (interleaved)
+    kernel = e4m3 ? latent_append_kernel<true, true, false> : latent_append_kernel<false, true, false>;
+  else
+    kernel = e4m3 ? latent_append_kernel<true, false, false> : latent_append_kernel<false, false, false>;
   return launch_pdl(kernel, dim3(p.T, cuts), dim3(LA_THREADS), 0, s, p);
 }
 

@@ -121,6 +121,7 @@ def _append(env, T, H, R, P, rot, interleaved, e4m3, page, rows, norm=True, seed
 @pytest.mark.parametrize("T,H,R,P,rot,page", [
     (1, 64, 512, 64, 64, 16), (1, 1, 64, 64, 32, 1), (3, 16, 512, 64, 64, 7), (37, 128, 256, 64, 48, 16),
     (303, 5, 448, 128, 128, 64), (304, 8, 512, 64, 16, 16), (700, 16, 192, 64, 0, 48),
+    (2432, 3, 192, 128, 64, 16), (3001, 20, 512, 64, 64, 48),  # (with many rows: another form)
 ])
 def test_append(env, T, H, R, P, rot, page, interleaved, e4m3):
     _append(env, T, H, R, P, rot, interleaved, e4m3, page, rows=T % 2 == 1, pad=16 * (T % 3))
