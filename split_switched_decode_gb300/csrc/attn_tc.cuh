@@ -706,16 +706,17 @@ __global__ void __launch_bounds__((TcCfg<DP, MQ, E4M3>::THREADS), 1)
                 // seen, in this copy? (a weight of zero does not tell: one far below the row's
                 // maximum is zero too, and is taken as the smallest number)
                 const int at = i - first_tok;
-                if (at < 0 || at >= TS || at < lo - j0 - first_tok || at > hi - j0 - first_tok ||
-                    !(valid >> i & 1))
-                  continue;
-                if (pr == 0.0f) pr = FLT_MIN;
+                if (at >= 0 && at < TS && at >= lo - j0 - first_tok && at <= hi - j0 - first_tok &&
+                    (valid >> i & 1)) {
+                  if (pr == 0.0f) pr = FLT_MIN;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                  const uint16_t y = *reinterpret_cast<const uint16_t *>(
-                      v + swz<RB, TOK>(i, (d + e) >> 3) + ((d + e) & 7) * 2);
-                  if ((y & INF2) == (INF2 & 0xffffu)) o[e] += pr * to_f32<E4M3>(y);
+                  for (int e = 0; e < 16; ++e) {
+                    const uint16_t y = *reinterpret_cast<const uint16_t *>(
+                        v + swz<RB, TOK>(i, (d + e) >> 3) + ((d + e) & 7) * 2);
+                    if ((y & INF2) == (INF2 & 0xffffu)) o[e] += pr * to_f32<E4M3>(y);
+                  }
                 }
+                __syncwarp();  // what reads and writes tensor memory next wants the warp in one place
               }
 #pragma unroll
               for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(o[e]);
@@ -816,6 +817,7 @@ __global__ void __launch_bounds__((TcCfg<DP, MQ, E4M3>::THREADS), 1)
               for (int e = 0; e < CHUNK; e += 4)
                 *join_at(grp, gt, (d + e) >> 2) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
             }
+            __syncwarp();  // (as above)
           }
         }
         tc_fence_before();  // the next segment's products overwrite the columns

@@ -902,6 +902,7 @@ __global__ void __launch_bounds__((LdCfg<MQ, E4M3>::THREADS), 1)
             for (int e = 0; e < CH; ++e)
               if (r0 + e < n_rows) slot[(r0 + e) * DP + dim] = o[e];
           }
+          __syncwarp();  // the next read of tensor memory wants the warp in one place
         }
       }
       tc_fence_before();  // the next segment's products overwrite the columns

@@ -556,16 +556,19 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
           tmem_wait_ld();
 #pragma unroll 1
           for (int t = 0; t < 128; ++t) {
-            if (!(words[t >> 5] >> (t & 31) & 1) || j * 128 + t >= b.len) continue;
-            const uint32_t two = tmem_ld1(s_at + t / 2);
-            tmem_wait_ld();
-            float w = bf16_to_f32(static_cast<uint16_t>(t & 1 ? two >> 16 : two & 0xffffu));
-            if (t > to) continue;
-            if (w == 0.0f) w = FLT_MIN;
-            const uint16_t *v = values + (b.k0 + j * 128 + t) * v_stride + h * v_head + d;
+            if ((words[t >> 5] >> (t & 31) & 1) && j * 128 + t < b.len) {
+              const uint32_t two = tmem_ld1(s_at + t / 2);
+              tmem_wait_ld();
+              if (t <= to) {  // rows differ here
+                float w = bf16_to_f32(static_cast<uint16_t>(t & 1 ? two >> 16 : two & 0xffffu));
+                if (w == 0.0f) w = FLT_MIN;
+                const uint16_t *v = values + (b.k0 + j * 128 + t) * v_stride + h * v_head + d;
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if ((v[e] & 0x7f80u) == 0x7f80u) o[e] += w * bf16_to_f32(v[e]);
+                for (int e = 0; e < 16; ++e)
+                  if ((v[e] & 0x7f80u) == 0x7f80u) o[e] += w * bf16_to_f32(v[e]);
+              }
+            }
+            __syncwarp();  // what reads and writes tensor memory next wants the warp in one place
           }
 #pragma unroll
           for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(o[e]);
@@ -614,16 +617,18 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = f0 * o[e] + f1 * o1[e];
       }
-      if (!stored) continue;
+      if (stored) {
 #pragma unroll
-      for (int e = 0; e < 32; e += 8) {
-        float y[8];
+        for (int e = 0; e < 32; e += 8) {
+          float y[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = l == 0.0f ? 0.0f : o[e + i] * inv;
-        *reinterpret_cast<uint4 *>(out + d + e) =
-            make_uint4(pack2<false>(y[0], y[1]), pack2<false>(y[2], y[3]),
-                       pack2<false>(y[4], y[5]), pack2<false>(y[6], y[7]));
+          for (int i = 0; i < 8; ++i) y[i] = l == 0.0f ? 0.0f : o[e + i] * inv;
+          *reinterpret_cast<uint4 *>(out + d + e) =
+              make_uint4(pack2<false>(y[0], y[1]), pack2<false>(y[2], y[3]),
+                         pack2<false>(y[4], y[5]), pack2<false>(y[6], y[7]));
+        }
       }
+      __syncwarp();  // (as above)
     }
   }
   tc_fence_before();

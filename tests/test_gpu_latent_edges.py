@@ -1,0 +1,41 @@
+"""GPU tests of latent attention where rows of a warp differ. Tolerances as in test_gpu_latent.py."""
+import math
+
+import pytest
+
+from test_gpu_latent import _Prompt, env  # noqa: F401 (a fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("V", [64, 128])
+@pytest.mark.parametrize("H", [2, 160])  # (128 and 256 rows a CTA)
+def test_prompt_values_not_finite_in_many_tokens(env, H, V):  # noqa: F811
+    """Several values that are not finite in a tile, some rows of a warp that see them and some
+    that do not, warps of which only some rows exist: rows that see one have it, the others keep
+    their bits."""
+    torch, ssd, dev = env
+    p = _Prompt(env, [300, 77, 1], [300, 90, 40], H, V=V)
+    p.run()
+    assert ssd.dec_sync_status() == ssd.DEC_OK
+    p.check()
+    clean = p.out.clone()
+    at = [(5, 3, math.inf), (40, 9, -math.inf), (41, 10, math.nan), (131, 17, math.inf), (290, 60, math.inf),
+          (299, 61, math.nan), (300 + 20, 30, math.inf), (300 + 89, 31, -math.inf), (390 + 39, 5, math.inf)]
+    for j, e, value in at:
+        p.v[j, 1, e] = value
+    p.out.fill_(5.0)
+    p.run()
+    assert ssd.dec_sync_status() == ssd.DEC_OK
+    want = clean.clone()
+    # token j of the keys belongs to row j - 300 - 13 + 300 of the second sequence, the last to the third's
+    for j, e, value in at:
+        rows = slice(j, 300) if j < 300 else (slice(max(300, j - 13), 377) if j < 390 else slice(377, 378))
+        got = p.out[rows, 1, e]
+        assert bool(got.isnan().all() if math.isnan(value) else (got == value).all()), (j, e)
+        want[rows, 1, e] = got
+    first = min(j for j, _, _ in at)
+    assert torch.equal(p.out[:first], want[:first]) and torch.equal(p.out[:, 0], clean[:, 0])
+    fine = want.isfinite()
+    assert torch.equal(fine, p.out.isfinite())
+    assert bool((p.out.float() - want.float())[fine].abs().max() <= 2.0 ** -7 * want.float()[fine].abs().max())
