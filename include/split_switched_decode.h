@@ -24,10 +24,11 @@
  *    completed call leaves it ready for the next of its kind (a call whose kernels timed
  *    out, see Errors, does not: zero-fill it again), and one workspace must not be used
  *    by two calls that can run at the same time. Of its kind: the same entry point
- *    with the same sizes, or attn_decode with any sizes and cache type that the
- *    workspace is large enough for. Between calls of different kinds zero-fill it, or
- *    give each its own: counters that have to be zero stand where another kind has
- *    its partial sums, and nothing detects the difference.
+ *    with the same sizes, or attn_decode, or latent_decode, with any sizes and cache
+ *    type that the workspace is large enough for. Between calls of different kinds
+ *    zero-fill it, or give each its own: counters that have to be zero stand where
+ *    another kind has its partial sums, and nothing detects the difference.
+ *    (latent_decode alone expects nothing of what its workspace holds.)
  *  - Alignment. X, W, Wcat, Wgu, Wd and every workspace must be 16-byte aligned; K and
  *    every other reduction length must be a multiple of 8 (rows are then 16-byte
  *    multiples). Other pointers need their natural alignment.
@@ -640,6 +641,9 @@ DEC_API dec_status latent_project(const dec_bf16 *x, int64_t x_stride, int64_t x
  * not reach that row; a row that sees an element that is not finite becomes NaN, as its score
  * is not finite (short of a score of -infinity: that token then weighs nothing, or makes the
  * element NaN). Rounding of the weights and, for e4m3 caches, of q as attn_decode.
+ *
+ * ws: latent_decode_workspace_bytes(S, T, H, R, P) are enough for every call with at most S
+ * sequences, T rows and H heads, of any lengths and cache type.
  */
 DEC_API size_t latent_decode_workspace_bytes(int S, int T, int H, int R, int P);
 DEC_API dec_status latent_decode(const dec_bf16 *q, int64_t q_stride, const void *cache,

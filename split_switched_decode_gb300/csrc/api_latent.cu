@@ -151,7 +151,9 @@ size_t latent_decode_workspace_bytes(int S, int T, int H, int R, int P) {
     return 0;
   cudaError_t ce;
   const int sms = host_num_sms(&ce);
-  return sms > 0 ? latent_workspace_bytes(S, T, H, sms) : 0;
+  // the rows of an item grow with those of an average sequence: one sequence that has them all
+  // takes the most, and what is enough for it is enough for every smaller call
+  return sms > 0 ? latent_workspace_bytes(1, T, H, sms) : 0;
 }
 
 dec_status latent_decode(const dec_bf16 *q, int64_t q_stride, const void *cache, int kv_type,

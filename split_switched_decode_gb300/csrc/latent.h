@@ -54,7 +54,7 @@ struct LatentLaunch {
   uint64_t wait_limit_ns;
   bool hold;  // self-test: waits that run out
 };
-size_t latent_workspace_bytes(int S, int T, int H, int num_sms);
+size_t latent_workspace_bytes(int S, int T, int H, int num_sms);  // of one call
 cudaError_t launch_latent_decode(const AttnParams &p, int width, bool e4m3, void *ws, int num_sms,
                                  unsigned *status, uint64_t wait_limit_ns, bool hold,
                                  cudaStream_t s);

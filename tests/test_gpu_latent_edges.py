@@ -3,7 +3,7 @@ import math
 
 import pytest
 
-from test_gpu_latent import _Prompt, env  # noqa: F401 (a fixture)
+from test_gpu_latent import _Decode, _Prompt, env  # noqa: F401 (a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -39,3 +39,24 @@ def test_prompt_values_not_finite_in_many_tokens(env, H, V):  # noqa: F811
     fine = want.isfinite()
     assert torch.equal(fine, p.out.isfinite())
     assert bool((p.out.float() - want.float())[fine].abs().max() <= 2.0 ** -7 * want.float()[fine].abs().max())
+
+
+def test_decode_workspace_of_the_largest_call_serves_smaller_ones(env):  # noqa: F811
+    """Sized once for a batch of single tokens, then used by fewer sequences with more rows each."""
+    torch, ssd, dev = env
+    size = lambda S, T, H: ssd.latent_decode_workspace_bytes(S, T, H, 512, 64)
+    for most in ((64, 64, 16), (300, 300, 3), (5, 40, 128), (8192, 8192, 4)):
+        for part in ((1, 1), (1, 2), (2, 1), (8, 3), (64, 64), (1, 4)):
+            S, T = max(1, most[0] // part[0]), max(1, most[1] // part[1])
+            for H in {most[2], max(1, most[2] // 2), 1}:
+                assert size(S, T, H) <= size(*most), (most, S, T, H)
+    ws = ssd.workspace(size(64, 64, 16), dev)
+    for lens, rows, H in (([500] * 64, [1] * 64, 16), ([9000], [8], 16), ([3000, 20], [3, 20], 16),
+                          ([9000], [64], 5), ([70] * 3, [21] * 3, 16)):
+        for e4m3 in (False, True):
+            d = _Decode(env, lens, rows, H, e4m3=e4m3)
+            d.q, d.out, d.lse = d.q[:d.T], d.out[:d.T], d.lse[:d.T]
+            d.ws = ws
+            d.run()
+            assert ssd.dec_sync_status() == ssd.DEC_OK
+            d.check()
