@@ -142,7 +142,8 @@ dec_status latent_project(const dec_bf16 *x, int64_t x_stride, int64_t x_head, c
   uint64_t limit = 0;
   unsigned *status = host_wait_status(&limit);
   return status_of(launch_latent_project(x, x_stride, x_head, W, y, y_stride, y_head, T, H, K, N,
-                                         sms, status, limit, reinterpret_cast<cudaStream_t>(s)));
+                                         sms, status, limit, host_attn_hold(),
+                                         reinterpret_cast<cudaStream_t>(s)));
 }
 
 size_t latent_decode_workspace_bytes(int S, int T, int H, int R, int P) {
@@ -253,6 +254,7 @@ dec_status latent_prompt(const dec_bf16 *q, int64_t q_stride, const dec_bf16 *k_
   p.out_stride = out_stride;
   p.lse = lse_opt;
   p.status = host_wait_status(&p.wait_limit_ns);
+  p.hold = host_attn_hold();
   return status_of(launch_latent_prompt(p, q, q_stride, k_nope, k_stride, k_head, k_rope, r_stride,
                                         v, v_stride, v_head, sms,
                                         reinterpret_cast<cudaStream_t>(s)));

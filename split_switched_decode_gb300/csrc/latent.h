@@ -35,11 +35,13 @@ struct LatentProjectParams {
   long long items;  // H * tb * nb
   unsigned *status;
   uint64_t wait_limit_ns;
+  bool hold;  // self-test: waits that run out
 };
 cudaError_t launch_latent_project(const uint16_t *x, long long x_stride, long long x_head,
                                   const uint16_t *w, uint16_t *y, long long y_stride,
                                   long long y_head, int T, int H, int K, int N, int num_sms,
-                                  unsigned *status, uint64_t wait_limit_ns, cudaStream_t s);
+                                  unsigned *status, uint64_t wait_limit_ns, bool hold,
+                                  cudaStream_t s);
 
 // ---------------------------------------------------------- latent_decode.cu --
 // AttnParams with one kv head of D = R elements, the first of a row of R + P in the cache.
@@ -75,6 +77,7 @@ struct LatentPromptParams {
   float *lse;  // or nullptr
   unsigned *status;
   uint64_t wait_limit_ns;
+  bool hold;  // self-test: waits that run out
 };
 cudaError_t launch_latent_prompt(const LatentPromptParams &p, const uint16_t *q,
                                  long long q_stride, const uint16_t *k, long long k_stride,

@@ -1,5 +1,6 @@
 """GPU tests of latent attention where rows of a warp differ. Tolerances as in test_gpu_latent.py."""
 import math
+import time
 
 import pytest
 
@@ -60,3 +61,56 @@ def test_decode_workspace_of_the_largest_call_serves_smaller_ones(env):  # noqa:
             d.run()
             assert ssd.dec_sync_status() == ssd.DEC_OK
             d.check()
+
+
+# ----------------------------------------------------------- waits that run out ----
+
+def _held(env, run, outputs):  # noqa: F811
+    """Runs with the warps that read the products waiting for what never comes, under a limit of a
+    millisecond: that is told, soon, and the next call gives what the first one gave."""
+    torch, ssd, dev = env
+    run()
+    assert ssd.dec_sync_status() == ssd.DEC_OK
+    want = [x.clone() for x in outputs]
+    ssd.dec_set_wait_limit_ns(1_000_000)
+    ssd.dec_debug_attn_timeout(True)
+    try:
+        began = time.monotonic()
+        run()
+        assert ssd.dec_sync_status() == ssd.DEC_ERR_TIMEOUT
+        took = time.monotonic() - began
+    finally:
+        ssd.dec_debug_attn_timeout(False)
+        ssd.dec_set_wait_limit_ns(2_000_000_000)
+    for x in outputs:
+        x.fill_(5.0)
+    run()
+    assert ssd.dec_sync_status() == ssd.DEC_OK
+    for x, y in zip(outputs, want):
+        assert torch.equal(x, y)
+    return took
+
+
+# Each CTA meets the limit and then waits for its copies and products: 1 ms, and at most 10 ms for
+# products, 20 for queries, 40 for tiles that were requested in part, whatever the lengths.
+@pytest.mark.parametrize("rows,keys,H", [
+    ([1], [1], 1), ([777], [777], 16), ([300, 0, 5], [300, 40, 700], 3), ([128], [60000], 2),
+    ([300, 77], [300, 90], 160), ([256], [60000], 160),
+])
+def test_prompt_wait_that_runs_out(env, rows, keys, H):  # noqa: F811
+    p = _Prompt(env, rows, keys, H, extra=0)
+    took = _held(env, p.run, (p.out, p.lse))
+    blocks = sum(-(-n // 128) for n in rows) * H
+    assert took < 0.5 + 0.071 * -(-blocks // 152)
+
+
+@pytest.mark.parametrize("T,H,K,N", [(1, 1, 8, 8), (1, 64, 128, 512), (65, 4, 128, 512), (128, 2, 64, 64),
+                                     (4096, 64, 128, 512), (20000, 16, 512, 128)])
+def test_project_wait_that_runs_out(env, T, H, K, N):  # noqa: F811
+    """Few tiles, several a CTA, and thousands."""
+    torch, ssd, dev = env
+    g = torch.Generator(device=dev).manual_seed(T)
+    x, w = (torch.randn(s, generator=g, device=dev).to(torch.bfloat16) for s in ((T, H, K), (H, N, K)))
+    y = torch.empty((T, H, N), dtype=torch.bfloat16, device=dev)
+    took = _held(env, lambda: ssd.latent_project(x, w, y), (y,))
+    assert took < 0.5
