@@ -114,3 +114,23 @@ def test_project_wait_that_runs_out(env, T, H, K, N):  # noqa: F811
     y = torch.empty((T, H, N), dtype=torch.bfloat16, device=dev)
     took = _held(env, lambda: ssd.latent_project(x, w, y), (y,))
     assert took < 0.5
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("H", [16, 64])
+def test_decode_wait_that_runs_out_over_a_long_sequence(env, H, e4m3):  # noqa: F811
+    """33 million tokens (four pages again and again) are more than 3000 stages a CTA; what is left of
+    them after the time-out takes a few microseconds each, not a hundred."""
+    torch, ssd, dev = env
+    page, times = 4096, 2048
+    g = torch.Generator(device=dev).manual_seed(H)
+    kind = torch.float8_e4m3fn if e4m3 else torch.bfloat16
+    cache = torch.randn((4, page, 576), generator=g, device=dev).to(kind)
+    table = (torch.arange(4 * times, dtype=torch.int32, device=dev).view(1, -1) % 4).contiguous()
+    lens = torch.tensor([4 * page * times], dtype=torch.int32, device=dev)
+    q = torch.randn((1, H, 576), generator=g, device=dev).to(torch.bfloat16)
+    out = torch.empty((1, H, 512), dtype=torch.bfloat16, device=dev)
+    lse = torch.empty((1, H), device=dev)
+    ws = ssd.workspace(ssd.latent_decode_workspace_bytes(1, 1, H, 512, 64), dev)
+    took = _held(env, lambda: ssd.latent_decode(q, cache, table, lens, out, ws, 0.05, lse=lse), (out, lse))
+    assert took < 0.1
