@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(LP_THREADS)
                           const __grid_constant__ CUtensorMap ymap, const LatentProjectParams p) {
   using C = LpCfg<BM, BN>;
   extern __shared__ __align__(1024) uint8_t lp_smem[];  // outputs, then the ring
-  __shared__ __align__(8) uint64_t full[C::MAX_ST], empty[C::MAX_ST], done[2], freed[2], drained, hold;
+  __shared__ __align__(8) uint64_t full[C::MAX_ST], empty[C::MAX_ST], done[2], freed[2], drained;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   uint8_t *const ring = lp_smem + C::OUT;
@@ -51,11 +51,10 @@ __global__ void __launch_bounds__(LP_THREADS)
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&done[i], 1);
+      mbar_init(&done[i], p.hold ? 2 : 1);  // self-test: one arrival too many is waited for
       mbar_init(&freed[i], 4);
     }
     mbar_init(&drained, 1);
-    mbar_init(&hold, 1);
     fence_mbar_init();
     prefetch_tensormap(&xmap);
     prefetch_tensormap(&wmap);
@@ -75,10 +74,6 @@ __global__ void __launch_bounds__(LP_THREADS)
   auto wait = [&](uint64_t *bar, int phase) {
     return mbar_wait_bounded(bar, phase & 1, p.status, &abort_flag, p.wait_limit_ns);
   };
-  // of a whole warp; the tiles that are left are not walked through after a wait that ran out
-  auto all_wait = [&](uint64_t *bar, int phase) {
-    return __all_sync(0xffffffffu, wait(bar, phase));
-  };
   // item: head, row tile, column tile (the fastest, so that neighbours share rows of x)
   auto place = [&](long long item, int &h, int &t0, int &n0) {
     const int i = static_cast<int>(item / p.nb);
@@ -95,7 +90,7 @@ __global__ void __launch_bounds__(LP_THREADS)
       place(item, h, t0, n0);
       for (int b = 0; b < p.kb; ++b, ++k) {
         const int st = k % ST;
-        if (k >= ST) go = all_wait(&empty[st], k / ST - 1);
+        if (k >= ST) go = __all_sync(0xffffffffu, wait(&empty[st], k / ST - 1));
         if (!go) break;
         issued = k + 1;
         if (elect_one()) {
@@ -110,14 +105,12 @@ __global__ void __launch_bounds__(LP_THREADS)
   } else if (warp == 5) {
     const uint32_t id = (idesc_bf16(BN) & ~(31u << 24)) | static_cast<uint32_t>(BM >> 4) << 24;
     int k = 0, i = 0;
-    bool go = true;
-    for (long long item = blockIdx.x; go && item < p.items; item += gridDim.x, ++i) {
+    for (long long item = blockIdx.x; item < p.items; item += gridDim.x, ++i) {
       const int buf = i & 1;
-      if (i >= 2 && !all_wait(&freed[buf], (i >> 1) - 1)) break;
+      if (i >= 2) wait(&freed[buf], (i >> 1) - 1);
       for (int b = 0; b < p.kb; ++b, ++k) {
         const int st = k % ST;
-        go = all_wait(&full[st], k / ST);
-        if (!go) break;
+        wait(&full[st], k / ST);
         tc_fence_after();
         if (elect_one()) {
           const uint32_t at = smem_u32(ring + st * C::STAGE);
@@ -136,7 +129,6 @@ __global__ void __launch_bounds__(LP_THREADS)
     uint8_t *const out = lp_smem + warp * (C::ROWS * BN * 2);
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
     int i = 0;
-    if (p.hold) wait(&hold, 0);  // self-test: nobody arrives
     for (long long item = blockIdx.x; item < p.items; item += gridDim.x, ++i) {
       int h, t0, n0;
       place(item, h, t0, n0);
@@ -145,7 +137,7 @@ __global__ void __launch_bounds__(LP_THREADS)
         if (lane == 0) bulk_wait_read();  // the last tile's boxes
         __syncwarp();
       }
-      if (!all_wait(&done[buf], i >> 1)) break;
+      wait(&done[buf], i >> 1);
       tc_fence_after();
 #pragma unroll
       for (int c0 = 0; c0 < BN; c0 += 32) {

@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
   __shared__ PromptSearch search;
   __shared__ __align__(8) uint64_t k_full[PR_TB], k_empty[PR_TB], v_full[PR_TB], v_empty[PR_TB];
   __shared__ __align__(8) uint64_t v_ready[PR_TB], qfull[2], s_full[2], p_half[2], p_full[2], h_done[2];
-  __shared__ __align__(8) uint64_t o_full[2], drained, hold;
+  __shared__ __align__(8) uint64_t o_full[2], drained;
   __shared__ uint32_t bad[PR_TB][4];  // tokens with values that are not finite
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
@@ -181,14 +181,13 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
     }
     for (int g = 0; g < 2; ++g) {
       mbar_init(&qfull[g], 1);
-      mbar_init(&s_full[g], 1);
+      mbar_init(&s_full[g], p.hold ? 2 : 1);  // self-test: one arrival too many is waited for
       mbar_init(&p_half[g], 128);
       mbar_init(&p_full[g], 128);
       mbar_init(&h_done[g], 1);
       mbar_init(&o_full[g], 1);
     }
     mbar_init(&drained, 1);
-    mbar_init(&hold, 1);
     fence_mbar_init();
     prefetch_tensormap(&qmap);
     prefetch_tensormap(&kmap);
@@ -230,10 +229,6 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
   auto wait = [&](uint64_t *bar, int phase) {
     return mbar_wait_bounded(bar, phase & 1, p.status, &abort_flag, p.wait_limit_ns);
   };
-  // of a whole warp; the tiles that are left are not walked through after a wait that ran out
-  auto all_wait = [&](uint64_t *bar, int phase) {
-    return __all_sync(0xffffffffu, wait(bar, phase));
-  };
   uint8_t *const ring = pr_smem + C::QS * PR_MAX_Q * PR_SLAB;
   // the slot of slab x of tile j: keys, then values
   auto slot_of = [&](int j, int x) {
@@ -268,7 +263,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
       auto part = [&](int j, int from, int end) {  // keys or values of tile j
         if (go && j >= 2 && j < nt) {
           uint64_t *const bar = from < KN ? &k_empty[(j - 2) % PR_TB] : &v_empty[(j - 2) % PR_TB];
-          go = all_wait(bar, (j - 2) / PR_TB);
+          go = __all_sync(0xffffffffu, wait(bar, (j - 2) / PR_TB));
         }
         if (go && j < nt) {
           (from < KN ? k_issued : v_issued) = j + 1;
@@ -296,7 +291,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
           if (i >= C::SLOTS) {  // what held the slot: a slab of tile j2's keys or values
             const int j2 = (i - C::SLOTS) / STEP, x2 = i - C::SLOTS - j2 * STEP;
             uint64_t *const bar = x2 < KN ? &k_empty[j2 % PR_TB] : &v_empty[j2 % PR_TB];
-            go = all_wait(bar, j2 / PR_TB);
+            go = __all_sync(0xffffffffu, wait(bar, j2 / PR_TB));
             if (!go) break;
           }
           (x < KN ? k_issued : v_issued) = j + 1;
@@ -313,11 +308,11 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
       const uint32_t id_o64 = idesc_bf16(64) | (1u << 16);
       const uint64_t ring_k = sw128_desc(smem_u32(ring));
       const uint64_t ring_v = sw128_mn_desc(smem_u32(ring), PR_SLAB);
-      // `last`: no other rows need the tile; false: a wait ran out
+      // `last`: no other rows need the tile
       auto scores = [&](int g, int n, bool last) {
         const int j = tile(g, n);
         const uint64_t q = sw128_desc(smem_u32(pr_smem) + (SPLIT ? 0 : g * PR_MAX_Q * PR_SLAB));
-        if ((SPLIT || g == 0 || j >= nt0) && !wait(&k_full[j % PR_TB], j / PR_TB)) return false;
+        if (SPLIT || g == 0 || j >= nt0) wait(&k_full[j % PR_TB], j / PR_TB);
         tc_fence_after();
 #pragma unroll
         for (int i = 0; i < KN; ++i) {
@@ -329,7 +324,6 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
         }
         tc_commit(&s_full[g]);
         if (SPLIT || last) tc_commit(&k_empty[j % PR_TB]);
-        return true;
       };
       auto outputs = [&](int g, int n, bool last) {
         const int j = tile(g, n);
@@ -337,10 +331,10 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
         const uint64_t v = ring_v + slot * (PR_SLAB >> 4);
         const bool split = !SPLIT && VN == 2 && slot == C::SLOTS - 1;  // the second slab is slot 0
         const uint32_t o = tmem + 256 + g * 128, w = tmem + g * 128;
-        if ((SPLIT || g == 0 || j >= nt0) && !wait(&v_ready[j % PR_TB], j / PR_TB)) return false;
+        if (SPLIT || g == 0 || j >= nt0) wait(&v_ready[j % PR_TB], j / PR_TB);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          if (!wait(half ? &p_full[g] : &p_half[g], n)) return false;
+          wait(half ? &p_full[g] : &p_half[g], n);
           tc_fence_after();
           const uint32_t acc = half || n > 0 ? 1u : 0u;
           if (!split) {
@@ -359,7 +353,6 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
         }
         if (SPLIT || last) tc_commit(&v_empty[j % PR_TB]);
         if (n + 1 == (g ? nt1 : nt0)) tc_commit(&o_full[g]);
-        return true;
       };
       if constexpr (SPLIT) {
         // S0 S1, then PV0 S0 PV1 S1 of every step, in one copy of either: jumping back over two
@@ -369,20 +362,25 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
 #pragma unroll 1
         for (int i = -2; i < 2 * nt0; ++i) {
           const int g = i & 1, n = i >> 1, mine = g ? nt1 : nt0;
-          if (n >= 0 && n < mine && !outputs(g, n, true)) break;
-          if (i == -2 && nt0 > 0 && !wait(&qfull[0], 0)) break;
-          if (n + 1 < mine && !scores(g, n + 1, true)) break;
+          if (n >= 0 && n < mine) outputs(g, n, true);
+          if (i == -2 && nt0 > 0) wait(&qfull[0], 0);
+          if (n + 1 < mine) scores(g, n + 1, true);
         }
       } else {
-        bool go = true;
-        if (nt0 > 0) go = wait(&qfull[0], 0) && scores(0, 0, nt1 == 0);
-        if (go && nt1 > 0) go = wait(&qfull[1], 0) && scores(1, 0, true);
+        if (nt0 > 0) {
+          wait(&qfull[0], 0);
+          scores(0, 0, nt1 == 0);
+        }
+        if (nt1 > 0) {
+          wait(&qfull[1], 0);
+          scores(1, 0, true);
+        }
 #pragma unroll 1
-        for (int j = 0; go && j < nt; ++j) {
-          if (j < nt0 && !outputs(0, j, j >= nt1)) break;
-          if (j + 1 < nt0 && !scores(0, j + 1, j + 1 >= nt1)) break;
-          if (j < nt1 && !outputs(1, j, true)) break;
-          if (j + 1 < nt1 && !scores(1, j + 1, true)) break;
+        for (int j = 0; j < nt; ++j) {
+          if (j < nt0) outputs(0, j, j >= nt1);
+          if (j + 1 < nt0) scores(0, j + 1, j + 1 >= nt1);
+          if (j < nt1) outputs(1, j, true);
+          if (j + 1 < nt1) scores(1, j + 1, true);
         }
       }
     }
@@ -394,7 +392,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
       // Every tile in turn: a wait tells only neighbouring phases apart. (These warps once waited
       // for slots in which keys stood before, without waiting for the keys; values that landed
       // first let them run ahead, and the products never saw v_ready's phase.)
-      if (!all_wait(&v_full[j % PR_TB], j / PR_TB)) break;
+      wait(&v_full[j % PR_TB], j / PR_TB);
       if (partial(0, j) || partial(1, j)) {
         // 64 tokens a warp, four rows of eight chunks a step. An exponent of all ones is the only
         // one that carries into the sign's place: nothing but a look where all are finite.
@@ -450,10 +448,9 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
     float m = -INFINITY, l = 0.0f;
     float z[2][32];
     float2 sum[2];
-    if (p.hold) wait(&hold, 0);  // self-test: nobody arrives
     for (int n = 0; n < mine; ++n) {
       const int j = tile(g, n);
-      if (!all_wait(&s_full[g], n)) break;
+      wait(&s_full[g], n);
       tc_fence_after();
       const bool whole = !partial(g, j);
       const int to = pos - j * 128;  // the last key seen, in the tile
