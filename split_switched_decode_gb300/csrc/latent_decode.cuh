@@ -337,6 +337,13 @@ __global__ void __launch_bounds__((LdCfg<MQ, E4M3>::THREADS), 1)
   auto wait = [&](uint64_t *bar, int phase) {
     return mbar_wait_bounded(bar, phase & 1, pl.status, &abort_flag, pl.wait_limit_ns);
   };
+  // For what comes once a segment: the limit times the waits of all `stages` so far (four a
+  // stage, each with the limit to itself), as a segment may well take longer than the limit.
+  auto wait_stages = [&](uint64_t *bar, int phase, int stages) {
+    const uint64_t one = pl.wait_limit_ns;
+    const uint64_t limit = one >> 34 == 0 ? one * (4ull * stages + 4) : one;  // below 2^64
+    return mbar_wait_bounded(bar, phase & 1, pl.status, &abort_flag, limit);
+  };
   // As many barriers in turn as there are S: who waits for stage i knows that i - NS is done.
   auto wait_pv = [&](int i) { wait(&pv_done[i % NS], i / NS); };
   int issued = 0, q_issued = 0;  // boxes: stages, items' q that were begun
@@ -417,11 +424,13 @@ __global__ void __launch_bounds__((LdCfg<MQ, E4M3>::THREADS), 1)
   } else if (warp == 11) {
     // ================================================================ boxes of q
     // Rows past the item's, of other sequences, fill columns that nobody reads.
-    int seg = 0;
+    int seg = 0, stages = 0;
     bool go = pl.q_boxes;
     while (go && c.next(p, H)) {
       const int qb = seg % QB;
-      if (seg >= QB) go = __all_sync(0xffffffffu, wait(&qempty[qb], seg / QB - 1));
+      if (seg >= QB)
+        go = __all_sync(0xffffffffu, wait_stages(&qempty[qb], seg / QB - 1, stages));
+      stages += c.t1 - c.t0;
       if (!go) break;
       q_issued = seg + 1;
       if (elect_one()) {
@@ -439,7 +448,7 @@ __global__ void __launch_bounds__((LdCfg<MQ, E4M3>::THREADS), 1)
     const int hw = warp - 12;
     const bool q_by_hand = !pl.q_boxes;
     const int chunks = width >> 3;  // 16-byte chunks of a row: at most 72
-    int k = 0, seg = 0;
+    int k = 0, seg = 0, stages = 0;
     while ((!boxes || q_by_hand) && c.next(p, H)) {
       // q: a warp a row, four rows at a time
       const int qb = seg % QB;
@@ -463,7 +472,7 @@ __global__ void __launch_bounds__((LdCfg<MQ, E4M3>::THREADS), 1)
           }
         }
         if (!waited) {
-          wait(&qempty[qb], seg / QB - 1);
+          wait_stages(&qempty[qb], seg / QB - 1, stages);
           waited = true;
         }
 #pragma unroll
@@ -505,6 +514,7 @@ __global__ void __launch_bounds__((LdCfg<MQ, E4M3>::THREADS), 1)
         if (lane == 0) mbar_arrive(&qfull[qb]);
       }
       ++seg;
+      stages += c.t1 - c.t0;
       if (boxes) continue;
       const int32_t *table = p.block_table + static_cast<long long>(c.s) * p.max_pages;
       if constexpr (E4M3) {

@@ -4,7 +4,7 @@ import time
 
 import pytest
 
-from test_gpu_latent import _Decode, _Prompt, env  # noqa: F401 (a fixture)
+from test_gpu_latent import U, _Decode, _Prompt, _within, env  # noqa: F401 (a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -134,3 +134,45 @@ def test_decode_wait_that_runs_out_over_a_long_sequence(env, H, e4m3):  # noqa: 
     ws = ssd.workspace(ssd.latent_decode_workspace_bytes(1, 1, H, 512, 64), dev)
     took = _held(env, lambda: ssd.latent_decode(q, cache, table, lens, out, ws, 0.05, lse=lse), (out, lse))
     assert took < 0.15
+
+
+@pytest.mark.parametrize("strided", [False, True])  # rows of q in boxes, or copied
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("H", [16, 64])
+def test_decode_segments_longer_than_the_wait_limit(env, H, e4m3, strided):  # noqa: F811
+    """Every stage comes in time, so nothing runs out, however long a CTA is at one sequence before it
+    turns to the next: 11 million tokens, 100 and 22 million (four pages again and again) take
+    milliseconds under a limit of one. Repeated tokens change the sum of the weights, not the mean.
+
+    Tolerance: that of the other cases, and for each of a CTA's 3500 stages 2^-23 for each of the
+    four sums of products that an output adds up, 2^-24 for that of its weights."""
+    torch, ssd, dev = env
+    import latent_ref
+    page, R, W, scale = 4096, 512, 576, 0.05
+    n, times = 4 * page, (683, 0, 1365)
+    g = torch.Generator(device=dev).manual_seed(H)
+    kind = torch.float8_e4m3fn if e4m3 else torch.bfloat16
+    cache = torch.randn((4, page, W), generator=g, device=dev).to(kind)
+    table = torch.arange(4 * max(times), dtype=torch.int32, device=dev).expand(3, -1) % 4
+    lens = torch.tensor([n * times[0], 100, n * times[2]], dtype=torch.int32, device=dev)
+    q = torch.randn((3, H * W + (64 if strided else 0)), generator=g, device=dev).to(torch.bfloat16)
+    q = q[:, :H * W].unflatten(1, (H, W))
+    out = torch.empty((3, H, R), dtype=torch.bfloat16, device=dev)
+    lse = torch.empty((3, H), device=dev)
+    ws = ssd.workspace(ssd.latent_decode_workspace_bytes(3, 3, H, R, W - R), dev)
+    ssd.dec_set_wait_limit_ns(1_000_000)
+    try:
+        ssd.latent_decode(q, cache, table.contiguous(), lens, out, ws, scale, lse=lse)
+        assert ssd.dec_sync_status() == ssd.DEC_OK
+    finally:
+        ssd.dec_set_wait_limit_ns(2_000_000_000)
+    keys = cache.float().double().view(1, n, W)
+    extra = 3500 * (4 * 2.0 ** -23 + 2.0 ** -24)
+    for s in range(3):
+        k = keys if times[s] else keys[:, :100]
+        at = torch.full((1,), k.shape[1] - 1, device=dev)
+        want, wl, size, reach = latent_ref.attend(q[s:s + 1].double(), k, k[..., :R], at, scale)
+        score = (W + 16) * 2.0 ** -24 * reach + 2.0 ** -18  # as in _Decode.check
+        _within(out[s:s + 1], want, U * want.abs() + (U + 2 * score[..., None] + extra) * size, "out")
+        wl = wl + math.log(max(times[s], 1))
+        _within(lse[s:s + 1], wl, score + 2.0 ** -22 * wl.abs() + 3500 * 2.0 ** -24, "lse")
