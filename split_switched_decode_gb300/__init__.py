@@ -653,6 +653,8 @@ def latent_append(c, k_rope, positions, slots, inv_freq, cache, weight=None, eps
     elif P:
         raise ValueError("latent_append: the cache is wider than c, and k_rope is missing")
     if q_rope is not None:
+        if q_out is None:
+            raise ValueError("latent_append: q_rope without q_out")
         qp, (Tq, H, Pq), (q0, q1, _) = _part(q_rope, "q_rope", 3, dev)
         op, (To, Ho, Po), (o0, o1, _) = _part(q_out, "q_out", 3, dev)
         if Tq != T or To != T or Ho != H or Pq != P or Po != P:

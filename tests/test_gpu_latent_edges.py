@@ -397,3 +397,14 @@ def test_append_and_project_of_very_many_rows(env):  # noqa: F811
     want = torch.einsum("thk,hnk->thn", x[-200:].double(), w.double())
     size = torch.einsum("thk,hnk->thn", x[-200:].double().abs(), w.double().abs())
     _within(y[-200:], want, U * want.abs() + (K + 2) * 2.0 ** -24 * size, "y")
+
+
+def test_append_wants_a_place_for_the_queries(env):  # noqa: F811
+    torch, ssd, dev = env
+    c, r = torch.zeros((2, 576), dtype=torch.bfloat16, device=dev).split([512, 64], 1)
+    cache = torch.ones((1, 8, 576), dtype=torch.bfloat16, device=dev)
+    at = torch.arange(2, dtype=torch.int32, device=dev)
+    q = torch.zeros((2, 4, 64), dtype=torch.bfloat16, device=dev)
+    with pytest.raises(ValueError, match="q_out"):
+        ssd.latent_append(c, r, at, at, torch.ones(32, device=dev), cache, q_rope=q)
+    assert bool((cache == 1).all())
