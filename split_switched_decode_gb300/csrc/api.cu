@@ -13,7 +13,6 @@
 #include "common.cuh"
 #include "internal.h"
 #include "latent.h"
-#include "latent.h"
 
 using namespace ssd;
 
@@ -189,19 +188,18 @@ bool host_cache_map(CUtensorMap *m, const PagedCache &c, const void *base, bool 
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool host_map(CUtensorMap *m, const void *base, int es, int rank, const long long *dims,
-              const long long *strides, const int *box, bool swizzled) {
+bool host_map(CUtensorMap *m, const void *base, int rank, const long long *dims,
+              const long long *strides, const int *box) {
   if (!encoder_ready()) return false;
-  cuuint64_t d[5], st[4];
-  cuuint32_t b[5], one[5] = {1, 1, 1, 1, 1};
+  cuuint64_t d[4], st[3];
+  cuuint32_t b[4], one[4] = {1, 1, 1, 1};
   for (int i = 0; i < rank; ++i) {
     d[i] = static_cast<cuuint64_t>(dims[i]);
     b[i] = static_cast<cuuint32_t>(box[i]);
-    if (i + 1 < rank) st[i] = static_cast<cuuint64_t>(strides[i]) * es;
+    if (i + 1 < rank) st[i] = static_cast<cuuint64_t>(strides[i]) * 2;
   }
-  return g_encode(m, es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                  rank, const_cast<void *>(base), d, st, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), d, st, b, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

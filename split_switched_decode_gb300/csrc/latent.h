@@ -85,9 +85,9 @@ cudaError_t launch_latent_prompt(const LatentPromptParams &p, const uint16_t *q,
                                  const uint16_t *v, long long v_stride, long long v_head,
                                  int num_sms, cudaStream_t s);
 
-// api.cu: a tensor map of up to five dimensions (strides in elements, of dimensions 1 on) with
-// boxes, swizzled in 128 bytes or not at all; false where the encoder refuses.
-bool host_map(CUtensorMap *m, const void *base, int es, int rank, const long long *dims,
-              const long long *strides, const int *box, bool swizzled);
+// api.cu: a tensor map of bf16 elements in up to four dimensions (strides in elements, of dimensions
+// 1 on) with boxes swizzled in 128 bytes; false where the encoder refuses.
+bool host_map(CUtensorMap *m, const void *base, int rank, const long long *dims,
+              const long long *strides, const int *box);
 
 }  // namespace ssd

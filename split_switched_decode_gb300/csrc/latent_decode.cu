@@ -46,7 +46,7 @@ cudaError_t launch_latent_decode(const AttnParams &params, int width, bool e4m3,
     const long long dims[4] = {64, p.c.page_size, width / 64, p.c.num_pages};
     const long long strides[3] = {p.c.token_stride, 64, p.c.page_stride};
     const int box[4] = {64, 8, width / 64, 1};
-    if (host_map(&a.map, p.c.k, 2, 4, dims, strides, box, true)) p.box = 8;
+    if (host_map(&a.map, p.c.k, 4, dims, strides, box)) p.box = 8;
   }
   // rows of q without gaps between tokens: boxes of an item's rows (for e4m3 caches they are
   // converted on the way)
@@ -54,7 +54,7 @@ cudaError_t launch_latent_decode(const AttnParams &params, int width, bool e4m3,
     const long long dims[2] = {width, static_cast<long long>(p.T) * p.Hq};
     const long long strides[1] = {width};
     const int box[2] = {64, rows};
-    a.q_boxes = host_map(&a.qmap, p.q, 2, 2, dims, strides, box, true);
+    a.q_boxes = host_map(&a.qmap, p.q, 2, dims, strides, box);
   }
   const cudaError_t e = e4m3 ? launch_latent_e4m3(p, width, rows, a, s)
                              : launch_latent<false>(p, width, rows, a, s);

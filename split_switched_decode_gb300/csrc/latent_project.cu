@@ -202,8 +202,8 @@ cudaError_t launch_shape(LatentProjectParams p, const uint16_t *x, long long x_s
   const long long wd[3] = {p.K, p.N, p.H}, wst[2] = {p.K, static_cast<long long>(p.N) * p.K};
   const long long yd[3] = {p.N, p.H, p.T}, ys[2] = {y_head, y_stride};
   const int xb[3] = {64, 1, BM}, wb[3] = {64, BN, 1}, yb[3] = {64, 1, C::ROWS};
-  if (!host_map(&xm, x, 2, 3, xd, xs, xb, true) || !host_map(&wm, w, 2, 3, wd, wst, wb, true) ||
-      !host_map(&ym, y, 2, 3, yd, ys, yb, true))
+  if (!host_map(&xm, x, 3, xd, xs, xb) || !host_map(&wm, w, 3, wd, wst, wb) ||
+      !host_map(&ym, y, 3, yd, ys, yb))
     return cudaErrorInvalidValue;
   auto kernel = latent_project_kernel<BM, BN>;
   const size_t smem = C::OUT + static_cast<size_t>(p.stages) * C::STAGE;

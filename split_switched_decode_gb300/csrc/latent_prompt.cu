@@ -699,9 +699,9 @@ cudaError_t launch_latent_prompt(const LatentPromptParams &p, const uint16_t *q,
   const long long rd[3] = {p.P, 1, p.Tk}, rs[2] = {p.P, r_stride};
   const long long vd[3] = {p.V, p.H, p.Tk}, vs[2] = {v_head, v_stride};
   const int box[3] = {64, 1, 128};
-  if (!host_map(&qm, q, 2, 3, qd, qs, box, true) || !host_map(&km, k, 2, 3, kd, ks, box, true) ||
-      (p.P > 0 && !host_map(&rm, k_rope, 2, 3, rd, rs, box, true)) ||
-      !host_map(&vm, v, 2, 3, vd, vs, box, true))
+  if (!host_map(&qm, q, 3, qd, qs, box) || !host_map(&km, k, 3, kd, ks, box) ||
+      (p.P > 0 && !host_map(&rm, k_rope, 3, rd, rs, box)) ||
+      !host_map(&vm, v, 3, vd, vs, box))
     return cudaErrorInvalidValue;
   // as many blocks of rows as there can be: a part of one a sequence
   const long long blocks = (p.T / PrCfg<false>::ROWS + static_cast<long long>(p.S)) * p.H;
