@@ -674,8 +674,8 @@ DEC_API dec_status latent_decode(const dec_bf16 *q, int64_t q_stride, const void
  * no key give 0 and -infinity. What is not finite at a key that a row does not see does not
  * reach it; a value that is not finite makes that element of the rows that see it infinite or
  * NaN. Scores, maxima and sums are fp32, the weights round to bf16 for the product with v; weights
- * are at most 2^16 on the way (in latent_decode 2^8), so that sums of values beyond 2^110 may pass
- * fp32's range. Deterministic. No workspace.
+ * are at most 2^16 on the way (in latent_decode 2^8 on a bf16 cache and 2^15 on an e4m3 one), so
+ * that sums of values beyond 2^110 may pass fp32's range. Deterministic. No workspace.
  */
 DEC_API dec_status latent_prompt(const dec_bf16 *q, int64_t q_stride, const dec_bf16 *k_nope,
                                  int64_t k_stride, int64_t k_head, const dec_bf16 *k_rope,

@@ -672,10 +672,10 @@ def latent_append(c, k_rope, positions, slots, inv_freq, cache, weight=None, eps
         rot, fp = 2 * n, _plain(inv_freq, "inv_freq", _F32, n, dev)
     status = lib.dec_latent_call(0, _APPEND.pack(
         cp, cs[0], wp, eps, kp, ks, qp, q0, q1, _plain(positions, "positions", _I32, T, dev),
-        _plain(slots, "slots", _I32, T, dev), fp, magnitude, T, H, R, P, rot, 1 if interleaved else 0, op, o0, o1,
-        rp, rs, cache.data_ptr(), kind,
-        0 if cache_scale is None else _plain(cache_scale, "cache_scale", _F32, 1, dev), pages, page,
-        page_stride, token_stride, _launch_stream(dev, stream)))
+        _plain(slots, "slots", _I32, T, dev), fp, magnitude, T, H, R, P, rot,
+        1 if interleaved else 0, op, o0, o1, rp, rs, cache.data_ptr(), kind,
+        0 if cache_scale is None else _plain(cache_scale, "cache_scale", _F32, 1, dev), pages,
+        page, page_stride, token_stride, _launch_stream(dev, stream)))
     if status:
         raise DecError(status, "latent_append")
 
@@ -725,11 +725,13 @@ def latent_decode(q, cache, block_table, seq_len, out, ws, scale, q_start=None, 
         raise TypeError("ws must be a contiguous CUDA tensor on the cache's device")
     status = lib.dec_latent_call(2, _DECODE.pack(
         qp, qs[0], cache.data_ptr(), kind,
-        0 if cache_scale is None else _plain(cache_scale, "cache_scale", _F32, 1, dev), pages, page,
-        page_stride, token_stride, table, max_pages, _plain(seq_len, "seq_len", _I32, S, dev),
-        0 if q_start is None else _plain(q_start, "q_start", _I32, S + 1, dev), S, T, H, R, width - R,
-        scale, window, op, os_[0], 0 if lse is None else _plain(lse, "lse", _F32, T * H, dev), ws.data_ptr(),
-        ws.nbytes, _launch_stream(dev, stream)))
+        0 if cache_scale is None else _plain(cache_scale, "cache_scale", _F32, 1, dev), pages,
+        page, page_stride, token_stride, table, max_pages,
+        _plain(seq_len, "seq_len", _I32, S, dev),
+        0 if q_start is None else _plain(q_start, "q_start", _I32, S + 1, dev), S, T, H, R,
+        width - R, scale, window, op, os_[0],
+        0 if lse is None else _plain(lse, "lse", _F32, T * H, dev), ws.data_ptr(), ws.nbytes,
+        _launch_stream(dev, stream)))
     if status:
         raise DecError(status, "latent_decode")
 
@@ -760,10 +762,10 @@ def latent_prompt(q, k_nope, k_rope, v, q_start, out, scale, k_start=None, lse=N
     if H > 1 and (qs[1] != D or os_[1] != V):
         raise TypeError("latent_prompt: heads of q and out must be contiguous within a row")
     status = lib.dec_latent_call(3, _PROMPT.pack(
-        qp, qs[0], kp, ks[0], ks[1], rp, rs, vp, vs[0], vs[1], _plain(q_start, "q_start", _I32, S + 1, dev),
-        0 if k_start is None else _plain(k_start, "k_start", _I32, S + 1, dev), S, T,
-        Tk, H, N, P, V, scale, op, os_[0],
-        0 if lse is None else _plain(lse, "lse", _F32, T * H, dev),
+        qp, qs[0], kp, ks[0], ks[1], rp, rs, vp, vs[0], vs[1],
+        _plain(q_start, "q_start", _I32, S + 1, dev),
+        0 if k_start is None else _plain(k_start, "k_start", _I32, S + 1, dev), S, T, Tk, H, N, P,
+        V, scale, op, os_[0], 0 if lse is None else _plain(lse, "lse", _F32, T * H, dev),
         _launch_stream(dev, stream)))
     if status:
         raise DecError(status, "latent_prompt")

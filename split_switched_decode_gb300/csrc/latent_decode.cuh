@@ -21,8 +21,9 @@
 // of each warp's quarter (M = 64), and a thread reads four elements of each 16 x 8 block (two
 // tokens, two rows). Two groups of four warps have half of the rows each and share nothing; a
 // thread holds the running maximum and its tokens' part of the sum of MQ / 8 rows. The maximum
-// is moved only when a row's has grown by 8 or more (weights then stay below 2^8, and their
-// rounding to bf16, relative 2^-8, is not enlarged): the common stage needs one vote over the
+// is moved only when a row's has grown by 8 or more (weights then stay below 2^8 in bf16, and
+// below 2^15 in f16, where they refer to less than the maximum; their rounding, relative 2^-8 or
+// 2^-11, is not enlarged): the common stage needs one vote over the
 // group and no exchange of maxima. Sums are fp32, of the weights before rounding, added over
 // lanes and warps at the segment's end.
 //

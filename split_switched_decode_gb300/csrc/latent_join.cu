@@ -245,6 +245,15 @@ __global__ void __launch_bounds__(32 * LJ_SHARES)
   put_row(p, blockIdx.x, d, v, m, l);
 }
 
+// The kernel for few rows while its CTAs fit two to an SM. us of latent_decode with it / with the other
+// (CTAs; sequences of tokens each x heads):
+//   64 CTAs,  1 x 777 x 16        9.2 / 13.2     256,  4 x 20000 x 16     27.5 /  55.3
+//   256,      1 x 131072 x 64    43.2 / 145.6    512,  8 x 100 x 16       14.9 /   9.4
+//   512,      8 x 777 x 16       15.7 / 16.2     512,  1 x 131072 x 128   62.9 / 115.7
+//   1024,    16 x 100 x 16       20.6 /  9.6    1024, 16 x 20000 x 16     76.3 /  72.0
+//   4096,    64 to 8192 x 16    102.0 / 63.2    1024,  one of 40000 and 15 of 100 x 16  21.9 / 91.8
+// Beyond two an SM short sequences decide for the other kernel; a row of more than 16 parts then waits
+// for one warp (all lengths are on the device).
 template <int MQ>
 cudaError_t launch_join(const AttnParams &p, const LatentLaunch &a, cudaStream_t s) {
   const int all = p.T * p.Hq, cuts = (p.D + 127) / 128, most = 3 * a.num_sms;

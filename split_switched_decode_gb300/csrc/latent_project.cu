@@ -243,6 +243,7 @@ cudaError_t launch_latent_project(const uint16_t *x, long long x_stride, long lo
   //    128 rows, 16 x 128 to 512    4.1 /  4.2 /  5.7     128 rows, 64 x 512 to 128    8.5 /  7.1 /  8.6
   //    512 rows, 16 x 128 to 512    6.0 /  5.6 /  6.3     512 rows, 64 x 512 to 128   21.1 / 15.1 / 14.1
   //    512 rows, 64 x 128 to 512   13.9 / 12.2 / 13.2    4096 rows, 64 x 128 to 512   83.6 / 74.7 / 60.6
+  // (512 rows of 64 heads into the latent space are on the slower side of the rule.)
   const long long wide = static_cast<long long>(H) * ((T + 127) / 128) * ((N + 255) / 256);
   auto launch = T <= 64 ? launch_shape<64, 64>
                         : (wide < num_sms ? launch_shape<128, 64> : launch_shape<128, 256>);

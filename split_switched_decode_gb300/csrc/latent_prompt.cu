@@ -49,9 +49,10 @@
 // 512, 32 11.2 / 14.3; 8192, 2 55 / 111; 128 rows behind 4096 tokens, 16 heads 33 / 54; with more
 // blocks than SMs 4096, 64 393 (with one ring) / 260.
 //
-// Measured: 4096 tokens, 64 heads of 128 + 64 and 128 elements 257 to 268 us, 1337 to 1280 TFLOP/s of
-// the pairs seen, at the GPU's power limit (241 us without loads of keys and values past the first
-// two tiles); 777 tokens, 16 heads 12.5 us.
+// Measured: 4096 tokens, 64 heads of 128 + 64 and 128 elements 257 to 263 us at the highest clock, 1337
+// to 1308 TFLOP/s of the pairs seen (241 us without loads of keys and values past the first two
+// tiles), 276 after seconds of load, when the power limit has lowered the clock by some 6 %; 777
+// tokens, 16 heads 12.3 us.
 #include <float.h>
 
 #include "attn_tc.cuh"
@@ -357,8 +358,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
       if constexpr (SPLIT) {
         // S0 S1, then PV0 S0 PV1 S1 of every step, in one copy of either: jumping back over two
         // copies takes 400 clocks (2048 tokens, 16 heads 29.8 us, 28.3 with one). Where blocks of 256
-        // rows fill the SMs, power bounds them, and one copy gains nothing (4096 tokens, 64 heads:
-        // 264 us against 261).
+        // rows fill the SMs one copy gains nothing (4096 tokens, 64 heads: 264 us against 261).
 #pragma unroll 1
         for (int i = -2; i < 2 * nt0; ++i) {
           const int g = i & 1, n = i >> 1, mine = g ? nt1 : nt0;
